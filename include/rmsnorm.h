@@ -224,6 +224,64 @@ int rmsnorm_vjp_ws(const void *x, const void *w, const void *g, float eps,
                    void *stream);
 
 /*
+ * The norms before and after a block, fused with the block's gate and residual
+ * scale.  Per row of D elements, with w'_ = weight_bias + w_ and gate row
+ * i * gate_rows / rows for row i:
+ *     r_y = 1 / sqrt(mean(y^2) + eps),  p = y * r_y * w'_post   (norm after)
+ *     h   = residual + scale * gate * p                         (new_residual)
+ *     r_h = 1 / sqrt(mean(h^2) + eps),  out = h * r_h * w'_pre  (norm before)
+ *   y            [rows, D] dtype, the block's output (attention or MLP).
+ *   residual     [rows, D] dtype, the residual stream before the block.
+ *   w_post       [D] dtype, weight of the norm after the block, or NULL: no
+ *                such norm (p = y, r_y = 1).
+ *   w_pre        [D] dtype, weight of the next block's norm.
+ *   gate         [gate_rows, D] dtype with row stride ld_gate, or NULL (1).
+ *                gate_rows divides rows: gate row j multiplies the rows / gate_rows
+ *                consecutive rows from j * rows / gate_rows on (gate_rows = 1: one
+ *                learned gate; a row per sequence; gate_rows = rows: one per row).
+ *   scale        finite scalar, the residual scale of the block.
+ *   out, new_residual  [rows, D] dtype; new_residual receives round(h), h is
+ *                normalised unrounded.
+ *   rstd         [2, rows] fp32, receives r_y and r_h for rmsnorm_block_vjp; or NULL.
+ * Row strides in elements (>= D; ignored when rows == 1).  Numerics, aliasing
+ * (out and new_residual may be y or residual) and errors as for rmsnorm_fwd;
+ * gate, weights and rstd may not overlap an output.
+ */
+int rmsnorm_block_fwd(const void *y, int64_t ld_y, const void *residual, int64_t ld_residual,
+                      const void *w_post, const void *w_pre, const void *gate, int64_t ld_gate,
+                      int64_t gate_rows, float scale, float eps, float weight_bias, void *out,
+                      int64_t ld_out, void *new_residual, int64_t ld_new_residual, float *rstd,
+                      int64_t rows, int64_t D, int dtype, void *stream);
+
+/*
+ * VJP of rmsnorm_block_fwd at (y, h), h being the new_residual it wrote:
+ *     c = r_h^2 * mean(g_out * w'_pre * h)
+ *     g_h = r_h * (g_out * w'_pre - h * c) + g_residual
+ *     m = scale * gate * w'_post,  e = r_y^2 * mean(m * g_h * y)
+ *     g_y = r_y * (m * g_h - y * e)           (no w_post: g_y = m * g_h)
+ *     gw_pre = sum of g_out * h * r_h;  gw_post = sum of scale * gate * g_h * y * r_y
+ *     g_gate = sum over each gate row's rows of scale * g_h * p
+ *   g_out, g_residual  [rows, D] dtype, the gradients of out and of new_residual
+ *                (g_residual may be NULL: none).
+ *   rstd         what the forward wrote for these rows, or NULL: recomputed from
+ *                y and h.
+ *   g_y, g_h     [rows, D] dtype, the gradients of y and of residual, each
+ *                rounded once (g_y from the unrounded g_h).
+ *   gw_post, gw_pre  [D] fp32; gw_post NULL exactly when w_post is.
+ *   g_gate       [gate_rows, D] fp32, dense; NULL exactly when gate is.
+ * gw_post, gw_pre and g_gate are overwritten (rows == 0: zeros) and bit-identical
+ * from run to run, as gw of rmsnorm_vjp; their scratch (three fp32 rows a CTA)
+ * comes from the library's pool.  g_y and g_h may each be one of the row inputs.
+ */
+int rmsnorm_block_vjp(const void *y, int64_t ld_y, const void *h, int64_t ld_h, const void *w_post,
+                      const void *w_pre, const void *gate, int64_t ld_gate, int64_t gate_rows,
+                      float scale, const void *g_out, int64_t ld_g_out, const void *g_residual,
+                      int64_t ld_g_residual, const float *rstd, float eps, float weight_bias,
+                      void *g_y, int64_t ld_g_y, void *g_h, int64_t ld_g_h, float *gw_post,
+                      float *gw_pre, float *g_gate, int64_t rows, int64_t D, int dtype,
+                      void *stream);
+
+/*
  * Gated activation of the decode loop.  Source: "Fused residual-add RMSNorm
  * and fused RoPE + KV-append decode kernels", Background, third bullet (a
  * fused silu(x[:d]) * x[d:2d] gate with 16-byte vectorised loads).

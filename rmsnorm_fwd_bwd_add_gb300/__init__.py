@@ -14,7 +14,9 @@ include/rmsnorm.h (librmsnorm_gb300.so), with these thin Python bindings:
   rmsnorm_fwd_ex, rmsnorm_vjp_ex -- the same on rows a stride apart, with the
                   forward's per-row scale (rstd) written and reused.
   fp16, bf16 and fp32 tensors.
-  fused_add_rmsnorm, rms_norm -- torch.autograd wrappers.
+  rmsnorm_block_fwd, rmsnorm_block_vjp -- the norms before and after a block
+                  fused with the block's gate and residual scale.
+  fused_add_rmsnorm, rms_norm, block_norm -- torch.autograd wrappers.
   rmsnorm_gated_silu -- the decode loop's gated activation silu(x[:d]) * x[d:].
   rmsnorm_rope_kv_append -- rotary embedding of q and k with the KV-cache append.
 
@@ -22,6 +24,8 @@ PyTorch supplies device memory and streams only.
 """
 from .api import (  # noqa: F401
     BoundCall,
+    rmsnorm_block_fwd,
+    rmsnorm_block_vjp,
     rmsnorm_debug_claim_counters,
     rmsnorm_debug_fail_allocs,
     rmsnorm_debug_inject,
@@ -42,7 +46,7 @@ from .api import (  # noqa: F401
     rmsnorm_vjp_ws,
 )
 from ._native import DEVSTATUS_BAD_INDEX, DEVSTATUS_WAIT_TIMEOUT, MAX_D, RmsnormError  # noqa: F401
-from .autograd import fused_add_rmsnorm, rms_norm  # noqa: F401
+from .autograd import block_norm, fused_add_rmsnorm, rms_norm  # noqa: F401
 
 __all__ = [
     "rmsnorm_fwd",
@@ -53,10 +57,13 @@ __all__ = [
     "rmsnorm_fused_vjp",
     "rmsnorm_fwd_ex",
     "rmsnorm_vjp_ex",
+    "rmsnorm_block_fwd",
+    "rmsnorm_block_vjp",
     "rmsnorm_gated_silu",
     "rmsnorm_rope_kv_append",
     "fused_add_rmsnorm",
     "rms_norm",
+    "block_norm",
     "rmsnorm_vjp_ws",
     "rmsnorm_vjp_noalloc",
     "rmsnorm_vjp_workspace_size",

@@ -19,6 +19,8 @@ EXPORTS = (
     "rmsnorm_fused_vjp",
     "rmsnorm_fwd_ex",
     "rmsnorm_vjp_ex",
+    "rmsnorm_block_fwd",
+    "rmsnorm_block_vjp",
     "rmsnorm_gated_silu",
     "rmsnorm_rope_kv_append",
     "rmsnorm_vjp_workspace_size",
@@ -80,6 +82,13 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.rmsnorm_vjp_ex.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _f, _f, _vp, _i64,
                                    _vp, _i64, _i64, _i, _vp]
     lib.rmsnorm_vjp_ex.restype = _i
+    lib.rmsnorm_block_fwd.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _f, _f, _f,
+                                      _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i, _vp]
+    lib.rmsnorm_block_fwd.restype = _i
+    lib.rmsnorm_block_vjp.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _f, _vp, _i64,
+                                      _vp, _i64, _vp, _f, _f, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                      _i64, _i64, _i, _vp]
+    lib.rmsnorm_block_vjp.restype = _i
     lib.rmsnorm_gated_silu.argtypes = [_vp, _vp, _i64, _i64, _i, _vp]
     lib.rmsnorm_gated_silu.restype = _i
     lib.rmsnorm_rope_kv_append.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _f,

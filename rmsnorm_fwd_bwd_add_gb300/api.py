@@ -505,6 +505,131 @@ def rmsnorm_vjp_ex(x: torch.Tensor, w: torch.Tensor, g: torch.Tensor, eps: float
     return gx, gw
 
 
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """An output allocated for use on `stream` (the current one when None):
+    memory of that stream's pool, so that no earlier work on another stream can
+    still be using it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _row_output(name, t, ref, stream):
+    """(t or a new dense tensor like ref, its row stride)."""
+    if t is None:
+        t = _new(ref.shape, ref.dtype, ref.device, stream)
+    return t, _check_rows_like(name, t, ref)
+
+
+def _fp32_output(name, t, shape, device, stream):
+    if t is None:
+        return _new(shape, torch.float32, device, stream)
+    if (t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or t.device != device
+            or not t.is_contiguous()):
+        raise ValueError("%s must be a contiguous float32 tensor of shape %s on %s" % (
+            name, tuple(shape), device))
+    return t
+
+
+def _check_gate(gate: Optional[torch.Tensor], x: torch.Tensor, rows: int, D: int) -> Tuple[int, int]:
+    """(gate rows, row stride) of a [..., D] gate whose rows divide x's rows."""
+    if gate is None:
+        return 0, 0
+    if gate.dtype != x.dtype or gate.device != x.device:
+        raise ValueError("gate must be %s on %s" % (x.dtype, x.device))
+    if gate.dim() < 1 or gate.shape[-1] != D:
+        raise ValueError("gate must be [..., %d], got %s" % (D, tuple(gate.shape)))
+    G, _, ld = _rows_ld("gate", gate)
+    if G < 1 or rows % G:
+        raise ValueError("the gate's %d rows must divide the %d rows" % (G, rows))
+    return G, ld
+
+
+def _check_block(x, w_post, w_pre, gate, rows, D):
+    _check_w(w_pre, x, D)
+    if w_post is not None:
+        _check_w(w_post, x, D)
+    return _check_gate(gate, x, rows, D)
+
+
+def _check_rstd2(rstd: torch.Tensor, rows: int, device: torch.device) -> None:
+    if (rstd.dtype != torch.float32 or rstd.dim() < 1 or rstd.shape[0] != 2 or rstd.numel() != 2 * rows
+            or rstd.device != device or not rstd.is_contiguous()):
+        raise ValueError("rstd must be a contiguous float32 tensor [2, rows] of %d rows on %s" % (
+            rows, device))
+
+
+def rmsnorm_block_fwd(y: torch.Tensor, residual: torch.Tensor, w_post: Optional[torch.Tensor],
+                      w_pre: torch.Tensor, eps: float, weight_bias: float = 0.0,
+                      gate: Optional[torch.Tensor] = None, scale: float = 1.0, *,
+                      out: Optional[torch.Tensor] = None,
+                      new_residual: Optional[torch.Tensor] = None, rstd=None, stream=None):
+    """The norms before and after a block with its gate and residual scale:
+    h = residual + scale * gate * norm(y; w_post), out = norm(h; w_pre).
+    w_post None: no norm after the block.  gate: None, [D] or [..., D] with a
+    number of rows that divides y's, each for as many consecutive rows of y.
+    Rows may lie a stride apart.  rstd: None (not written), True (allocated
+    here) or a [2, rows] float32 tensor that receives both norms' scales.
+    Returns (out, new_residual, rstd); pass out=y or new_residual=residual to
+    update in place."""
+    rows, D, ld_y = _rows_ld("y", y)
+    code = _dtype_code(y)
+    ld_r = _check_rows_like("residual", residual, y)
+    G, ld_gate = _check_block(y, w_post, w_pre, gate, rows, D)
+    out, ld_o = _row_output("out", out, y, stream)
+    new_residual, ld_n = _row_output("new_residual", new_residual, y, stream)
+    if rstd is True:
+        rstd = _new((2, *y.shape[:-1]), torch.float32, y.device, stream)
+    if rstd is not None:
+        _check_rstd2(rstd, rows, y.device)
+    st = _call(y.get_device(), stream, _fn("rmsnorm_block_fwd"), _ptr(y), ld_y, _ptr(residual), ld_r,
+               _ptr(w_post), _ptr(w_pre), _ptr(gate), ld_gate, G, scale, eps, weight_bias, _ptr(out),
+               ld_o, _ptr(new_residual), ld_n, _ptr(rstd), rows, D, code)
+    _native.check("rmsnorm_block_fwd", st)
+    return out, new_residual, rstd
+
+
+def rmsnorm_block_vjp(y: torch.Tensor, h: torch.Tensor, w_post: Optional[torch.Tensor],
+                      w_pre: torch.Tensor, g_out: torch.Tensor, eps: float, weight_bias: float = 0.0,
+                      gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                      g_residual: Optional[torch.Tensor] = None, *,
+                      rstd: Optional[torch.Tensor] = None, g_y: Optional[torch.Tensor] = None,
+                      g_h: Optional[torch.Tensor] = None, gw_post: Optional[torch.Tensor] = None,
+                      gw_pre: Optional[torch.Tensor] = None, g_gate: Optional[torch.Tensor] = None,
+                      stream=None):
+    """VJP of rmsnorm_block_fwd at (y, h), h its new_residual, from the
+    gradients of out and (optionally) of new_residual, with the forward's rstd
+    or without.  Returns (g_y, g_h, gw_post, gw_pre, g_gate): g_h is the
+    gradient of residual, the weights' and the gate's gradients are float32
+    (None without a post-norm, without a gate)."""
+    rows, D, ld_y = _rows_ld("y", y)
+    code = _dtype_code(y)
+    ld_h = _check_rows_like("h", h, y)
+    ld_g = _check_rows_like("g_out", g_out, y)
+    ld_gr = D if g_residual is None else _check_rows_like("g_residual", g_residual, y)
+    G, ld_gate = _check_block(y, w_post, w_pre, gate, rows, D)
+    if rstd is not None:
+        _check_rstd2(rstd, rows, y.device)
+    g_y, ld_gy = _row_output("g_y", g_y, y, stream)
+    g_h, ld_gh = _row_output("g_h", g_h, y, stream)
+    gw_pre = _fp32_output("gw_pre", gw_pre, (D,), y.device, stream)
+    if w_post is not None:
+        gw_post = _fp32_output("gw_post", gw_post, (D,), y.device, stream)
+    elif gw_post is not None:
+        raise ValueError("gw_post given without w_post")
+    if gate is not None:
+        g_gate = _fp32_output("g_gate", g_gate, gate.shape, y.device, stream)
+    elif g_gate is not None:
+        raise ValueError("g_gate given without a gate")
+    st = _call(y.get_device(), stream, _fn("rmsnorm_block_vjp"), _ptr(y), ld_y, _ptr(h), ld_h,
+               _ptr(w_post), _ptr(w_pre), _ptr(gate), ld_gate, G, scale, _ptr(g_out), ld_g,
+               _ptr(g_residual), ld_gr, _ptr(rstd), eps, weight_bias, _ptr(g_y), ld_gy, _ptr(g_h),
+               ld_gh, _ptr(gw_post), _ptr(gw_pre), _ptr(g_gate), rows, D, code)
+    _native.check("rmsnorm_block_vjp", st)
+    return g_y, g_h, gw_post, gw_pre, g_gate
+
+
 def rmsnorm_vjp_workspace_size(rows: int, D: int, dtype: torch.dtype) -> int:
     """Bytes of scratch rmsnorm_vjp_ws needs on the current device."""
     return int(_native.lib().rmsnorm_vjp_workspace_size(rows, D, _DTYPES[dtype]))

@@ -6,6 +6,9 @@ fused_add_rmsnorm(x, residual, w, eps, weight_bias) -> (out, new_residual)
     one gradient for x and residual (they enter as a sum) and gw.
 rms_norm(x, w, eps, weight_bias) -> out
     forward: rmsnorm_fwd_ex without a residual; backward: rmsnorm_vjp_ex.
+block_norm(y, residual, w_post, w_pre, eps, weight_bias, gate, scale) -> (out, new_residual)
+    forward: rmsnorm_block_fwd with both scales saved; backward:
+    rmsnorm_block_vjp on y and the saved new_residual.
 Inputs whose rows sit a stride apart (slices of wider buffers) are used in
 place; fp16, bf16 and fp32.
 
@@ -21,8 +24,10 @@ rms_norm through autograd).
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
-from .api import rmsnorm_fwd_ex, rmsnorm_vjp_ex, rows_layout_ok
+from .api import (rmsnorm_block_fwd, rmsnorm_block_vjp, rmsnorm_fwd_ex, rmsnorm_vjp_ex,
+                  rows_layout_ok)
 
 
 def _rows(t):
@@ -77,6 +82,40 @@ class RMSNormFunction(torch.autograd.Function):
                 gw32.to(w.dtype) if ctx.needs_input_grad[1] else None, None, None)
 
 
+class BlockNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, residual, w_post, w_pre, eps: float, weight_bias: float, gate, scale: float):
+        ctx.set_materialize_grads(False)
+        y = _rows(y)
+        gate_rows = None if gate is None else _rows(gate)
+        out, new_res, rstd = rmsnorm_block_fwd(
+            y, _rows(residual), None if w_post is None else w_post.contiguous(), w_pre.contiguous(),
+            eps, weight_bias, gate_rows, scale, rstd=True)
+        ctx.save_for_backward(y, new_res, w_post, w_pre, gate, rstd)
+        ctx.eps = eps
+        ctx.weight_bias = weight_bias
+        ctx.scale = scale
+        return out, new_res
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_out, g_res):
+        if g_out is None and g_res is None:
+            return (None,) * 8
+        y, new_res, w_post, w_pre, gate, rstd = ctx.saved_tensors
+        if g_out is None:  # only new_residual was used
+            g_out = torch.zeros_like(new_res)
+        g_y, g_h, gw_post, gw_pre, g_gate = rmsnorm_block_vjp(
+            y, new_res, None if w_post is None else w_post.contiguous(), w_pre.contiguous(),
+            _rows(g_out), ctx.eps, ctx.weight_bias, None if gate is None else _rows(gate), ctx.scale,
+            None if g_res is None else _rows(g_res), rstd=rstd)
+        need = ctx.needs_input_grad
+        return (g_y if need[0] else None, g_h if need[1] else None,
+                gw_post.to(w_post.dtype) if need[2] else None,
+                gw_pre.to(w_pre.dtype) if need[3] else None, None, None,
+                g_gate.to(gate.dtype) if need[6] else None, None)
+
+
 def fused_add_rmsnorm(x, residual, w, eps: float, weight_bias: float = 0.0):
     """(out, new_residual) with h = x + residual and
     out = h * rsqrt(mean(h^2) + eps) * (weight_bias + w); differentiable."""
@@ -86,3 +125,12 @@ def fused_add_rmsnorm(x, residual, w, eps: float, weight_bias: float = 0.0):
 def rms_norm(x, w, eps: float, weight_bias: float = 0.0):
     """x * rsqrt(mean(x^2) + eps) * (weight_bias + w); differentiable."""
     return RMSNormFunction.apply(x, w, eps, weight_bias)
+
+
+def block_norm(y, residual, w_post, w_pre, eps: float, weight_bias: float = 0.0, gate=None,
+               scale: float = 1.0):
+    """(out, new_residual) with h = residual + scale * gate * norm(y; w_post) and
+    out = norm(h; w_pre): the norms after a block and before the next one, with
+    the block's gate and residual scale; differentiable in y, residual, both
+    weights and the gate (scale is a constant)."""
+    return BlockNormFunction.apply(y, residual, w_post, w_pre, eps, weight_bias, gate, scale)

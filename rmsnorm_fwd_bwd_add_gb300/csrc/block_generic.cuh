@@ -1,0 +1,254 @@
+// block_generic.cuh -- the norm pair around a block for any row length and
+// alignment, and the second stage of its weight and gate gradients.
+//
+// One CTA per row at a time, one element per thread and step; a row is read
+// from global memory once per pass (forward: sum of y^2, sum of h^2, outputs).
+// It takes the rows the tiers that hold a row on chip cannot.
+#pragma once
+
+#include "block.h"
+#include "common.cuh"
+
+namespace rmsn {
+
+constexpr int BLOCK_GENERIC_NT = 512;
+
+// Sum of v over the CTA, the same in every thread: warp butterfly, then the
+// warp totals in warp order.  `red` holds a float a warp; the CTA passes two
+// barriers.
+template <int NT>
+__device__ __forceinline__ float cta_sum(float v, float *red) {
+    v = group_sum<32>(v);
+    __syncthreads();  // the previous sum has been read
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) t += red[w];
+    return t;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(BLOCK_GENERIC_NT) block_fwd_generic_kernel(const BlockArgs a) {
+    constexpr int NT = BLOCK_GENERIC_NT;
+    __shared__ float red[NT / 32];
+    const int tid = threadIdx.x, D = a.D;
+    const float wb = a.weight_bias, inv_D = 1.0f / (float)D;
+    const T *w1 = static_cast<const T *>(a.w_pre), *w2 = static_cast<const T *>(a.w_post);
+    griddep_wait();
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T *y = static_cast<const T *>(a.y) + row * a.ld_y;
+        const T *res = static_cast<const T *>(a.res) + row * a.ld_res;
+        const T *gate = a.gate ? static_cast<const T *>(a.gate) + row / a.rows_per_gate * a.ld_gate : nullptr;
+        T *out = static_cast<T *>(a.out0) + row * a.ld_out0;
+        T *nres = static_cast<T *>(a.out1) + row * a.ld_out1;
+        float r_y = 1.f;
+        if (w2) {
+            float s = 0.f;
+            for (int c = tid; c < D; c += NT) {
+                const float v = Cvt<T>::load1(y + c);
+                s = fmaf(v, v, s);
+            }
+            r_y = rsqrtf(cta_sum<NT>(s, red) * inv_D + a.eps);
+        }
+        auto joined = [&](int c) -> float {
+            float m = a.scale;
+            if (gate) m *= Cvt<T>::load1(gate + c);
+            if (w2) m *= wb + Cvt<T>::load1(w2 + c);
+            return fmaf(m * r_y, Cvt<T>::load1(y + c), Cvt<T>::load1(res + c));
+        };
+        float s = 0.f;
+        for (int c = tid; c < D; c += NT) {
+            const float h = joined(c);
+            s = fmaf(h, h, s);
+        }
+        const float r_h = rsqrtf(cta_sum<NT>(s, red) * inv_D + a.eps);
+        for (int c = tid; c < D; c += NT) {
+            const float h = joined(c);
+            Cvt<T>::store1(nres + c, h);
+            Cvt<T>::store1(out + c, h * r_h * (wb + Cvt<T>::load1(w1 + c)));
+        }
+        if (a.rstd && tid == 0) {
+            a.rstd[row] = r_y;
+            a.rstd[a.rows + row] = r_h;
+        }
+    }
+    griddep_launch_dependents();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(BLOCK_GENERIC_NT) block_vjp_generic_kernel(const BlockArgs a) {
+    constexpr int NT = BLOCK_GENERIC_NT;
+    __shared__ float red[NT / 32];
+    const int tid = threadIdx.x, D = a.D;
+    const float wb = a.weight_bias, inv_D = 1.0f / (float)D;
+    const T *w1 = static_cast<const T *>(a.w_pre), *w2 = static_cast<const T *>(a.w_post);
+    const int64_t cta = blockIdx.x, grid = gridDim.x;
+    const int64_t r0 = first_row(cta, grid, a.rows), r1 = first_row(cta + 1, grid, a.rows);
+    const bool per_row = a.gate && a.rows_per_gate == 1;
+    griddep_wait();
+    float *pre = a.part_pre + cta * D;
+    for (int64_t row = r0; row < r1; ++row) {
+        const int64_t gr = row / a.rows_per_gate;
+        const T *y = static_cast<const T *>(a.y) + row * a.ld_y;
+        const T *hp = static_cast<const T *>(a.res) + row * a.ld_res;
+        const T *g = static_cast<const T *>(a.g) + row * a.ld_g;
+        const T *gres = a.g_res ? static_cast<const T *>(a.g_res) + row * a.ld_g_res : nullptr;
+        const T *gate = a.gate ? static_cast<const T *>(a.gate) + gr * a.ld_gate : nullptr;
+        T *gy = static_cast<T *>(a.out0) + row * a.ld_out0;
+        T *gh = static_cast<T *>(a.out1) + row * a.ld_out1;
+        float r_y = 1.f, r_h;
+        if (a.rstd) {
+            if (w2) r_y = a.rstd[row];
+            r_h = a.rstd[a.rows + row];
+        } else {
+            float sy = 0.f, sh = 0.f;
+            for (int c = tid; c < D; c += NT) {
+                const float v = Cvt<T>::load1(y + c), u = Cvt<T>::load1(hp + c);
+                sy = fmaf(v, v, sy);
+                sh = fmaf(u, u, sh);
+            }
+            if (w2) r_y = rsqrtf(cta_sum<NT>(sy, red) * inv_D + a.eps);
+            r_h = rsqrtf(cta_sum<NT>(sh, red) * inv_D + a.eps);
+        }
+        float s = 0.f;
+        for (int c = tid; c < D; c += NT)
+            s = fmaf(Cvt<T>::load1(g + c) * (wb + Cvt<T>::load1(w1 + c)), Cvt<T>::load1(hp + c), s);
+        const float cc = (r_h * r_h) * (cta_sum<NT>(s, red) * inv_D);
+        auto grad_h = [&](int c) -> float {
+            float v = r_h * (Cvt<T>::load1(g + c) * (wb + Cvt<T>::load1(w1 + c)) - Cvt<T>::load1(hp + c) * cc);
+            if (gres) v += Cvt<T>::load1(gres + c);
+            return v;
+        };
+        auto mult = [&](int c) -> float {
+            float m = a.scale;
+            if (gate) m *= Cvt<T>::load1(gate + c);
+            if (w2) m *= wb + Cvt<T>::load1(w2 + c);
+            return m;
+        };
+        float ee = 0.f;
+        if (w2) {
+            s = 0.f;
+            for (int c = tid; c < D; c += NT) s = fmaf(mult(c) * grad_h(c), Cvt<T>::load1(y + c), s);
+            ee = (r_y * r_y) * (cta_sum<NT>(s, red) * inv_D);
+        }
+        // this gate row's sum: whole here (its own row of g_gate), or a part
+        const bool whole = a.g_gate && gr * a.rows_per_gate >= r0 && (gr + 1) * a.rows_per_gate <= r1;
+        float *mid = per_row ? a.part_mid + 2 * cta * D
+                     : whole ? a.g_gate + gr * D
+                             : a.part_mid + mid_slot(cta, gr, grid, a.rows, a.rows_per_gate) * D;
+        const bool first = per_row ? row == r0 : row == r0 || row % a.rows_per_gate == 0;
+        for (int c = tid; c < D; c += NT) {
+            const float v = grad_h(c), yv = Cvt<T>::load1(y + c), m = mult(c);
+            const float p = Cvt<T>::load1(g + c) * Cvt<T>::load1(hp + c) * r_h;
+            pre[c] = row == r0 ? p : pre[c] + p;
+            float q = a.scale * v * yv * r_y;
+            if (per_row) {
+                a.g_gate[gr * D + c] = w2 ? q * (wb + Cvt<T>::load1(w2 + c)) : q;
+                q *= Cvt<T>::load1(gate + c);
+            }
+            mid[c] = first ? q : mid[c] + q;
+            Cvt<T>::store1(gh + c, v);
+            Cvt<T>::store1(gy + c, r_y * (m * v - yv * ee));
+        }
+    }
+    griddep_launch_dependents();
+}
+
+// Second stage: a CTA covers 32 columns with BR_WARPS warps.
+//   gw_pre = the CTAs' partial rows, each warp a contiguous run of them, the
+//   warps' sums added in warp order.
+//   A of each gate row: with fewer gate rows than warps, BR_WARPS / G warps
+//   share a gate row's parts; with more, warp k takes the gate rows k, k +
+//   BR_WARPS, ...  A part is a row of part_mid, or the whole sum that one CTA
+//   left in g_gate, which becomes w2 * A in place.  Gate rows of one row each
+//   come finished from the first stage, which also weighted its sums.
+// The order of every sum depends on (rows, G, grid) alone.
+constexpr int BR_WARPS = 32;
+constexpr int BR_BATCH = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const BlockArgs a, int grid) {
+    __shared__ float sums[2][BR_WARPS][33];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int D = a.D;
+    const int64_t col = (int64_t)blockIdx.x * 32 + lane;
+    const bool in = col < D;
+    const T *w2 = static_cast<const T *>(a.w_post);
+    const T *gate = static_cast<const T *>(a.gate);
+    // rows first, first + step, ... (n of them) of a [*, D] array, in that order
+    auto add_rows = [&](const float *base, int64_t first, int64_t step, int64_t n) -> float {
+        float s = 0.f;
+        for (int64_t b = 0; b < n; b += BR_BATCH) {
+            float v[BR_BATCH];
+#pragma unroll
+            for (int i = 0; i < BR_BATCH; ++i)
+                v[i] = b + i < n ? base[(first + (b + i) * step) * D + col] : 0.f;
+#pragma unroll
+            for (int i = 0; i < BR_BATCH; ++i) s += v[i];
+        }
+        return s;
+    };
+    const int per = (grid + BR_WARPS - 1) / BR_WARPS;
+    const int p0 = min(grid, warp * per), p1 = min(grid, p0 + per);
+    float pre = 0.f, post = 0.f;
+    if (in) pre = add_rows(a.part_pre, p0, 1, p1 - p0);
+    const float w2c = in && w2 ? a.weight_bias + Cvt<T>::load1(w2 + col) : 1.f;
+    const int64_t rpg = a.rows_per_gate, G = a.rows / rpg;
+    const bool need_mid = w2 || gate, per_row = gate && rpg == 1;
+    const int team = G >= BR_WARPS ? 1 : BR_WARPS / (int)G;  // warps a gate row
+    if (need_mid && per_row) {
+        if (in) post = add_rows(a.part_mid, 2 * p0, 2, p1 - p0);
+    } else if (need_mid) {
+        float A = 0.f;
+        for (int64_t gr = warp / team; gr < G; gr += BR_WARPS / team) {
+            const int64_t c0 = cta_of_row(gr * rpg, grid, a.rows);
+            const int64_t c1 = cta_of_row((gr + 1) * rpg - 1, grid, a.rows);
+            if (!in) continue;
+            if (c0 == c1 && a.g_gate) {
+                A = warp % team == 0 ? a.g_gate[gr * D + col] : 0.f;
+            } else {
+                // parts: CTA c0's, then c0 + 1 ... c1 (each its first gate row)
+                const int64_t n = c1 - c0 + 1, share = (n + team - 1) / team;
+                const int64_t i0 = min(n, (int64_t)(warp % team) * share), i1 = min(n, i0 + share);
+                A = 0.f;
+                if (i0 == 0 && i1 > 0)
+                    A = a.part_mid[mid_slot(c0, gr, grid, a.rows, rpg) * D + col];
+                const int64_t j = max(i0, (int64_t)1);
+                if (j < i1) A += add_rows(a.part_mid, 2 * (c0 + j), 2, i1 - j);
+            }
+            if (team == 1) {
+                if (gate) a.g_gate[gr * D + col] = A * w2c;
+                post = fmaf(gate ? Cvt<T>::load1(gate + gr * a.ld_gate + col) : 1.f, A, post);
+            }
+        }
+        if (team > 1) post = A;  // this warp's part of its gate row's A
+    }
+    sums[0][warp][lane] = pre;
+    sums[1][warp][lane] = post;
+    __syncthreads();
+    if (warp == 0 && in) {
+        float t = sums[0][0][lane];
+#pragma unroll
+        for (int k = 1; k < BR_WARPS; ++k) t += sums[0][k][lane];
+        a.gw_pre[col] = t;
+    }
+    if (warp == 1 && in && need_mid) {
+        float t = 0.f;
+        if (per_row || team == 1) {
+            for (int k = 0; k < BR_WARPS; ++k) t += sums[1][k][lane];
+        } else {
+            for (int gr = 0; gr < (int)G; ++gr) {
+                float A = 0.f;
+                for (int k = 0; k < team; ++k) A += sums[1][gr * team + k][lane];
+                if (gate) a.g_gate[gr * (int64_t)D + col] = A * w2c;
+                t = fmaf(gate ? Cvt<T>::load1(gate + gr * a.ld_gate + col) : 1.f, A, t);
+            }
+        }
+        if (w2) a.gw_post[col] = t;
+    }
+}
+
+}  // namespace rmsn
