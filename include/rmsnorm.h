@@ -86,8 +86,8 @@ extern "C" {
 typedef enum {
     RMSNORM_F16 = 0,  /* IEEE binary16 */
     RMSNORM_BF16 = 1, /* bfloat16 */
-    RMSNORM_F32 = 2   /* IEEE binary32 (norm entry points only; the gate and
-                         the rotary embedding take fp16 or bf16) */
+    RMSNORM_F32 = 2   /* IEEE binary32 (rmsnorm_gated_silu and
+                         rmsnorm_rope_kv_append take fp16 or bf16 only) */
 } rmsnorm_dtype_t;
 
 typedef enum {
@@ -108,8 +108,9 @@ typedef enum {
 
 /* Bits of the device status word. */
 #define RMSNORM_DEVSTATUS_WAIT_TIMEOUT 1u
-#define RMSNORM_DEVSTATUS_BAD_INDEX 2u /* rmsnorm_rope_kv_append: a position or
-                                          slot out of range (that token skipped) */
+#define RMSNORM_DEVSTATUS_BAD_INDEX 2u /* the rotary and cache entry points: a position,
+                                          slot, length or block id out of range
+                                          (what it names is skipped) */
 
 /*
  * Fused residual-add RMSNorm forward.
@@ -328,6 +329,125 @@ int rmsnorm_rope_kv_append(const void *q, const void *k, const void *v,
                            int64_t max_pos, float rope_base, int interleaved, int64_t T,
                            int64_t Hq, int64_t Hkv, int64_t Dh, int64_t num_slots, int dtype,
                            void *stream);
+
+/*
+ * Rotary positions for every head layout, forward and backward.  The first
+ * rot_dim elements of each head are pairs (a, b) that become
+ *     attn_scale * (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq[i]
+ * for pair i; the rest are copied.  inverse = 1 negates t: the VJP (the
+ * gradient of q from that of q_out), with the same attn_scale.
+ *   q, q_out     [B, S, Hq, Dh] dtype; k, k_out [B, S, Hkv, Dh] dtype (Hq or Hkv
+ *                may be 0, its pointers then NULL).  The last dimension is
+ *                contiguous; *_strides are host arrays of the batch, token and
+ *                head strides in elements, so views of one fused projection
+ *                and heads-first layouts are taken as they are.  q_out may be q
+ *                and k_out k (same strides); outputs may not overlap anything else,
+ *                nor themselves.
+ *   positions    [B * S] int64, device memory.
+ *   inv_freq     [rot_dim / 2] double, HOST memory, read during the call: radians
+ *                per position of each pair, as rmsnorm_rope_frequencies gives
+ *                them (or any finite ones of up to 10^6).
+ *   interleaved  0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1).
+ * fp16, bf16 or fp32; arithmetic in fp32, angles to about 1e-8 turns up to
+ * positions of 10^7, each output rounded once.  rot_dim even, at most Dh; Dh at most 1024.
+ * Strides and pointers in multiples of 16 bytes, with rot_dim and Dh in whole
+ * vectors, take the vectorised kernel.  A negative position is detected on the
+ * device: that token is skipped and RMSNORM_DEVSTATUS_BAD_INDEX is set.
+ */
+int rmsnorm_rope(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                 const int64_t *positions, void *q_out, const int64_t *q_out_strides, void *k_out,
+                 const int64_t *k_out_strides, const double *inv_freq, float attn_scale,
+                 int interleaved, int inverse, int64_t B, int64_t S, int64_t Hq, int64_t Hkv,
+                 int64_t Dh, int64_t rot_dim, int dtype, void *stream);
+
+/*
+ * rmsnorm_rope_kv_append with the layouts and frequencies of rmsnorm_rope: q, k
+ * and v [T, H, Dh] with host arrays of their token and head strides, caches
+ * [num_slots, Hkv, Dh] with slot and head strides, part of the head rotated.
+ * Token t's rotated k and its v go to row slots[t] (negative: not written; the
+ * slots of one call are distinct, else that row holds parts of either token).
+ * Negative positions and slots >= num_slots are skipped and set
+ * RMSNORM_DEVSTATUS_BAD_INDEX, as there.
+ */
+int rmsnorm_rope_kv_append_ex(const void *q, const int64_t *q_strides, const void *k,
+                              const int64_t *k_strides, const void *v, const int64_t *v_strides,
+                              const int64_t *positions, const int64_t *slots, void *q_out,
+                              const int64_t *q_out_strides, void *k_cache,
+                              const int64_t *k_cache_strides, void *v_cache,
+                              const int64_t *v_cache_strides, const double *inv_freq,
+                              float attn_scale, int interleaved, int64_t T, int64_t Hq, int64_t Hkv,
+                              int64_t Dh, int64_t rot_dim, int64_t num_slots, int dtype,
+                              void *stream);
+
+/* How rmsnorm_rope_frequencies stretches the frequencies f_i = base^(-2i / rot_dim)
+ * of a model trained on trained_length positions by `factor`. */
+typedef enum {
+    RMSNORM_ROPE_PLAIN = 0,  /* f_i */
+    RMSNORM_ROPE_LINEAR = 1, /* f_i / factor (interpolated positions) */
+    RMSNORM_ROPE_NTK = 2,    /* base grown to base * factor^(rot_dim / (rot_dim - 2)) */
+    RMSNORM_ROPE_YARN = 3,   /* a ramp over the pair index from f_i, at the pair that turns
+                                `high` times over trained_length, to f_i / factor, at the one
+                                that turns `low` times; attn_scale 0.1 ln(factor) + 1 */
+    RMSNORM_ROPE_LLAMA3 = 4  /* a ramp over the turns themselves: f_i at `high` turns or more,
+                                f_i / factor at `low` or fewer */
+} rmsnorm_rope_scaling_t;
+
+/*
+ * Host only: the frequencies of a rotary embedding, [rot_dim / 2] doubles, and the
+ * factor on cosine and sine.  factor, trained_length, low and high are read by
+ * the scalings that name them.
+ */
+int rmsnorm_rope_frequencies(int scaling, int64_t rot_dim, double base, double factor,
+                             double trained_length, double low, double high, double *inv_freq,
+                             float *attn_scale);
+
+/*
+ * Block tables and slot maps of a paged KV cache, on the GPU.  The pool has
+ * num_blocks blocks of block_size slots; free_blocks [num_blocks] int32 is a
+ * stack whose first *free_count entries are the free block ids.  Request b
+ * holds lens[b] tokens in the blocks block_table[b * ld_table + i], i <
+ * ceil(lens[b] / block_size); entries past those have no meaning.  All arrays
+ * are device memory.
+ *
+ * rmsnorm_kv_release pushes the blocks of every request with finished[b] != 0
+ * onto the stack, in request and table order, and sets its length to 0:
+ * lens_out [B] and free_count_out [1] receive the new state (they may be lens
+ * and free_count); the table is not changed.
+ */
+int rmsnorm_kv_release(const int32_t *lens, const uint8_t *finished, const int32_t *block_table,
+                       int64_t ld_table, int64_t table_width, int64_t block_size,
+                       int32_t *free_blocks, const int32_t *free_count, int64_t num_blocks,
+                       int32_t *lens_out, int32_t *free_count_out, int64_t B, void *stream);
+
+/*
+ * rmsnorm_kv_plan makes room for new_lens[b] more tokens of each request and maps
+ * them: the step's tokens are packed in request order, request b's from
+ * starts[b] on.
+ *   block_table  [B, table_width] int32, row stride ld_table; receives the ids
+ *                of the blocks taken (popped off the stack in request and table
+ *                order; the stack itself is not written).
+ *   free_blocks, free_count, free_count_out  the pool, or all NULL: no blocks
+ *                are taken, the table already has them.
+ *   lens_out     [B] int32, lens + new_lens of granted requests (may be lens).
+ *   granted      [B] uint8, 1 if the request got its room.  It does not when its blocks
+ *                would pass table_width, its tokens T, or the blocks that it
+ *                and the requests before it need the stack; it keeps its
+ *                length then, and its tokens get slot -1.
+ *   starts       [B + 1] int64, the first token of each request and their total.
+ *   positions, slots  [T] int64, requests [T] int32: token t's position in its
+ *                request, its cache slot (block * block_size + offset) and its
+ *                request; 0, -1 and -1 for the tokens from the total on (a step
+ *                captured in a graph is padded to T).
+ * Lengths below 0 and block ids outside the pool set
+ * RMSNORM_DEVSTATUS_BAD_INDEX; such a request is not granted, such an id gives
+ * slot -1.  B at most 2^31 - 2, T at most 2^31 - 1.
+ */
+int rmsnorm_kv_plan(const int32_t *lens, const int32_t *new_lens, int32_t *block_table,
+                    int64_t ld_table, int64_t table_width, int64_t block_size,
+                    const int32_t *free_blocks, const int32_t *free_count, int64_t num_blocks,
+                    int32_t *lens_out, int32_t *free_count_out, int64_t *starts, int64_t *positions,
+                    int64_t *slots, int32_t *requests, uint8_t *granted, int64_t B, int64_t T,
+                    void *stream);
 
 /* Size of the fixed device array behind rmsnorm_vjp_noalloc: 16 MiB. */
 #define RMSNORM_VJP_NOALLOC_MAX_BYTES ((size_t)16 << 20)

@@ -19,11 +19,18 @@ include/rmsnorm.h (librmsnorm_gb300.so), with these thin Python bindings:
   fused_add_rmsnorm, rms_norm, block_norm -- torch.autograd wrappers.
   rmsnorm_gated_silu -- the decode loop's gated activation silu(x[:d]) * x[d:].
   rmsnorm_rope_kv_append -- rotary embedding of q and k with the KV-cache append.
+  rope_frequencies, rmsnorm_rope, rmsnorm_rope_kv_append_ex, rope -- rotary
+                  positions over part of the head, stretched for long contexts,
+                  on strided heads: forward, VJP (rope: torch.autograd) and the
+                  append.
+  rmsnorm_kv_plan, rmsnorm_kv_release -- block tables and slot maps of a paged
+                  cache from the requests' lengths.
 
 PyTorch supplies device memory and streams only.
 """
 from .api import (  # noqa: F401
     BoundCall,
+    KvPlan,
     rmsnorm_block_fwd,
     rmsnorm_block_vjp,
     rmsnorm_debug_claim_counters,
@@ -36,7 +43,11 @@ from .api import (  # noqa: F401
     rmsnorm_fwd_bind,
     rmsnorm_fwd_ex,
     rmsnorm_gated_silu,
+    rmsnorm_kv_plan,
+    rmsnorm_kv_release,
+    rmsnorm_rope,
     rmsnorm_rope_kv_append,
+    rmsnorm_rope_kv_append_ex,
     rmsnorm_status_string,
     rmsnorm_vjp,
     rmsnorm_vjp_bind,
@@ -44,9 +55,10 @@ from .api import (  # noqa: F401
     rmsnorm_vjp_noalloc,
     rmsnorm_vjp_workspace_size,
     rmsnorm_vjp_ws,
+    rope_frequencies,
 )
 from ._native import DEVSTATUS_BAD_INDEX, DEVSTATUS_WAIT_TIMEOUT, MAX_D, RmsnormError  # noqa: F401
-from .autograd import block_norm, fused_add_rmsnorm, rms_norm  # noqa: F401
+from .autograd import block_norm, fused_add_rmsnorm, rms_norm, rope  # noqa: F401
 
 __all__ = [
     "rmsnorm_fwd",
@@ -61,6 +73,13 @@ __all__ = [
     "rmsnorm_block_vjp",
     "rmsnorm_gated_silu",
     "rmsnorm_rope_kv_append",
+    "rope_frequencies",
+    "rmsnorm_rope",
+    "rmsnorm_rope_kv_append_ex",
+    "rmsnorm_kv_plan",
+    "rmsnorm_kv_release",
+    "KvPlan",
+    "rope",
     "fused_add_rmsnorm",
     "rms_norm",
     "block_norm",

@@ -23,6 +23,11 @@ EXPORTS = (
     "rmsnorm_block_vjp",
     "rmsnorm_gated_silu",
     "rmsnorm_rope_kv_append",
+    "rmsnorm_rope",
+    "rmsnorm_rope_kv_append_ex",
+    "rmsnorm_rope_frequencies",
+    "rmsnorm_kv_release",
+    "rmsnorm_kv_plan",
     "rmsnorm_vjp_workspace_size",
     "rmsnorm_vjp_ws",
     "rmsnorm_vjp_noalloc",
@@ -45,11 +50,13 @@ STATUS = {
 }
 DEVSTATUS_WAIT_TIMEOUT = 1
 DEVSTATUS_BAD_INDEX = 2
+ROPE_SCALING = {None: 0, "linear": 1, "ntk": 2, "yarn": 3, "llama3": 4}
 MAX_D = 1 << 24
 VJP_NOALLOC_MAX_BYTES = 16 << 20
 
 _vp = ctypes.c_void_p
 _f = ctypes.c_float
+_d = ctypes.c_double
 _i64 = ctypes.c_int64
 _i = ctypes.c_int
 
@@ -94,6 +101,22 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.rmsnorm_rope_kv_append.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _f,
                                            _i, _i64, _i64, _i64, _i64, _i64, _i, _vp]
     lib.rmsnorm_rope_kv_append.restype = _i
+    lib.rmsnorm_rope.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f, _i, _i, _i64,
+                                 _i64, _i64, _i64, _i64, _i64, _i, _vp]
+    lib.rmsnorm_rope.restype = _i
+    lib.rmsnorm_rope_kv_append_ex.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                              _vp, _vp, _vp, _vp, _f, _i, _i64, _i64, _i64, _i64,
+                                              _i64, _i64, _i, _vp]
+    lib.rmsnorm_rope_kv_append_ex.restype = _i
+    lib.rmsnorm_rope_frequencies.argtypes = [_i, _i64, _d, _d, _d, _d, _d, _vp,
+                                             ctypes.POINTER(ctypes.c_float)]
+    lib.rmsnorm_rope_frequencies.restype = _i
+    lib.rmsnorm_kv_release.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64,
+                                       _vp]
+    lib.rmsnorm_kv_release.restype = _i
+    lib.rmsnorm_kv_plan.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp,
+                                    _vp, _vp, _vp, _i64, _i64, _vp]
+    lib.rmsnorm_kv_plan.restype = _i
     lib.rmsnorm_vjp_workspace_size.argtypes = [_i64, _i64, _i]
     lib.rmsnorm_vjp_workspace_size.restype = ctypes.c_size_t
     lib.rmsnorm_vjp_ws.argtypes = [_vp, _vp, _vp, _f, _f, _vp, _vp, _i64, _i64, _i, _vp,

@@ -12,7 +12,7 @@ dimensions are flattened into rows.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -430,6 +430,266 @@ def rmsnorm_rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
             Dh, k_cache.shape[0], code, _stream(q.device, stream))
     _native.check("rmsnorm_rope_kv_append", st)
     return q_out
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, *,
+                     factor: float = 1.0, trained_length: float = 0.0,
+                     low: float = 1.0, high: Optional[float] = None) -> Tuple[torch.Tensor, float]:
+    """(inv_freq, attn_scale) of a rotary embedding over rot_dim elements:
+    radians a position of each pair ([rot_dim / 2] float64, host memory) and the
+    factor on cosine and sine.  scaling stretches it by `factor`: None,
+    "linear", "ntk", "yarn" (high defaults to 32 turns) or "llama3" (high
+    defaults to 4), the last two for a model trained on trained_length
+    positions."""
+    if scaling not in _native.ROPE_SCALING:
+        raise ValueError("scaling must be one of %s" % (tuple(_native.ROPE_SCALING),))
+    if rot_dim <= 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and positive")
+    inv = torch.empty(rot_dim // 2, dtype=torch.float64)
+    attn = ctypes.c_float(1.0)
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
+    st = _fn("rmsnorm_rope_frequencies")(_native.ROPE_SCALING[scaling], rot_dim, base, factor,
+                                         trained_length, low, high, inv.data_ptr(), ctypes.byref(attn))
+    _native.check("rmsnorm_rope_frequencies", st)
+    return inv, float(attn.value)
+
+
+def _inv_freq(inv_freq: torch.Tensor, Dh: int) -> int:
+    """rot_dim of a checked inv_freq."""
+    if (inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.device.type != "cpu"
+            or not inv_freq.is_contiguous()):
+        raise ValueError("inv_freq must be a contiguous [rot_dim / 2] float64 CPU tensor")
+    rot = 2 * inv_freq.shape[0]
+    if rot < 2 or rot > Dh:
+        raise ValueError("inv_freq has %d pairs, a head of %d elements at most %d" % (rot // 2, Dh, Dh // 2))
+    return rot
+
+
+_I64x3 = ctypes.c_int64 * 3
+_I64x2 = ctypes.c_int64 * 2
+
+
+def _head_strides(name: str, t: torch.Tensor):
+    """Batch, token and head strides of a [(B,) S, H, Dh] tensor, for the C call."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("%s: the elements of a head must be contiguous" % name)
+    st = t.stride()
+    return _I64x3(st[0] if t.dim() == 4 else 0, st[-3], st[-2])
+
+
+def _check_heads(name: str, t: torch.Tensor, ref: torch.Tensor, H: Optional[int] = None) -> None:
+    if t.dtype != ref.dtype or t.device != ref.device:
+        raise ValueError("%s must be %s on %s" % (name, ref.dtype, ref.device))
+    want = (*ref.shape[:-2], ref.shape[-2] if H is None else H, ref.shape[-1])
+    if tuple(t.shape) != want:
+        raise ValueError("%s must have shape %s, got %s" % (name, want, tuple(t.shape)))
+
+
+def _check_tokens(name: str, t: torch.Tensor, shape, ref: torch.Tensor) -> None:
+    if (t.dtype != torch.int64 or tuple(t.shape) != tuple(shape) or t.device != ref.device
+            or not t.is_contiguous()):
+        raise ValueError("%s must be a contiguous %s int64 tensor on %s" % (name, tuple(shape), ref.device))
+
+
+def rmsnorm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
+                 inv_freq: torch.Tensor, *, attn_scale: float = 1.0, interleaved: bool = False,
+                 inverse: bool = False, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, stream=None):
+    """Rotates the first 2 * len(inv_freq) elements of each head of q and k (k
+    may be None) by their tokens' positions; inverse=True is the VJP.  q: [S,
+    Hq, Dh] or [B, S, Hq, Dh] with any strides but a contiguous last dimension
+    (views of a fused projection, transposed heads), k with Hkv heads;
+    positions: int64 of q's leading shape; inv_freq, attn_scale as
+    rope_frequencies returns them.  Pass q_out=q, k_out=k for in place; new
+    outputs are allocated dense.  Returns (q_out, k_out)."""
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [S, Hq, Dh] or [B, S, Hq, Dh]")
+    if not q.is_cuda:
+        raise ValueError("tensors must be CUDA tensors (there is no CPU path)")
+    code = _dtype_code(q)
+    lead, Hq, Dh = q.shape[:-2], q.shape[-2], q.shape[-1]
+    rot = _inv_freq(inv_freq, Dh)
+    _check_tokens("positions", positions, lead, q)
+    Hkv = 0
+    if k is not None:
+        if k.dim() != q.dim():
+            raise ValueError("k must have q's leading dimensions")
+        Hkv = k.shape[-2]
+        _check_heads("k", k, q, Hkv)
+    elif k_out is not None:
+        raise ValueError("k_out given without k")
+    if q_out is None:
+        q_out = _new(q.shape, q.dtype, q.device, stream)
+    _check_heads("q_out", q_out, q)
+    if k is not None:
+        if k_out is None:
+            k_out = _new(k.shape, k.dtype, k.device, stream)
+        _check_heads("k_out", k_out, k)
+    st = _call(q.get_device(), stream, _fn("rmsnorm_rope"), _ptr(q), _head_strides("q", q), _ptr(k),
+               None if k is None else _head_strides("k", k), _ptr(positions), _ptr(q_out),
+               _head_strides("q_out", q_out), _ptr(k_out),
+               None if k is None else _head_strides("k_out", k_out), inv_freq.data_ptr(), attn_scale,
+               1 if interleaved else 0, 1 if inverse else 0, lead[0] if len(lead) == 2 else 1, lead[-1],
+               Hq, Hkv, Dh, rot, code)
+    _native.check("rmsnorm_rope", st)
+    return q_out, k_out
+
+
+def _strides2(name: str, t: torch.Tensor):
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("%s: the elements of a head must be contiguous" % name)
+    return _I64x2(t.stride(0), t.stride(1))
+
+
+def rmsnorm_rope_kv_append_ex(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                              positions: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+                              v_cache: torch.Tensor, inv_freq: torch.Tensor, *,
+                              attn_scale: float = 1.0, interleaved: bool = False,
+                              q_out: Optional[torch.Tensor] = None, stream=None):
+    """rmsnorm_rope_kv_append with rmsnorm_rope's layouts and frequencies: q, k, v
+    [T, H, Dh] and the caches [num_slots, Hkv, Dh] with any token, slot and head
+    strides, the first 2 * len(inv_freq) elements of each head rotated; fp32
+    too.  Returns q_out."""
+    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("q must be [T, Hq, Dh] and k, v [T, Hkv, Dh]")
+    if not q.is_cuda:
+        raise ValueError("tensors must be CUDA tensors (there is no CPU path)")
+    code = _dtype_code(q)
+    T, Hq, Dh = q.shape
+    Hkv = k.shape[1]
+    rot = _inv_freq(inv_freq, Dh)
+    _check_heads("k", k, q, Hkv)
+    _check_heads("v", v, q, Hkv)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if (t.dtype != q.dtype or t.device != q.device or t.dim() != 3 or t.shape[1:] != (Hkv, Dh)
+                or t.shape[0] != k_cache.shape[0]):
+            raise ValueError("the caches must be [num_slots, %d, %d] %s on %s" % (Hkv, Dh, q.dtype, q.device))
+    _check_tokens("positions", positions, (T,), q)
+    _check_tokens("slots", slots, (T,), q)
+    if q_out is None:
+        q_out = _new(q.shape, q.dtype, q.device, stream)
+    _check_heads("q_out", q_out, q)
+    st = _call(q.get_device(), stream, _fn("rmsnorm_rope_kv_append_ex"), _ptr(q), _strides2("q", q), _ptr(k),
+               _strides2("k", k), _ptr(v), _strides2("v", v), _ptr(positions), _ptr(slots), _ptr(q_out),
+               _strides2("q_out", q_out), _ptr(k_cache), _strides2("k_cache", k_cache), _ptr(v_cache),
+               _strides2("v_cache", v_cache), inv_freq.data_ptr(), attn_scale, 1 if interleaved else 0, T,
+               Hq, Hkv, Dh, rot, k_cache.shape[0], code)
+    _native.check("rmsnorm_rope_kv_append_ex", st)
+    return q_out
+
+
+class KvPlan(NamedTuple):
+    """What rmsnorm_kv_plan writes: positions, slots [T] int64 and requests [T]
+    int32 of the tokens, starts [B + 1] int64, granted [B] bool, and the state
+    after the step."""
+    positions: torch.Tensor
+    slots: torch.Tensor
+    requests: torch.Tensor
+    starts: torch.Tensor
+    granted: torch.Tensor
+    lens: torch.Tensor
+    free_count: Optional[torch.Tensor]
+
+
+def _ints(name: str, t: torch.Tensor, shape, dtype, device) -> None:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s %s tensor on %s" % (name, tuple(shape), dtype, device))
+
+
+def _int_output(name: str, t, shape, dtype, device, stream) -> torch.Tensor:
+    if t is None:
+        return _new(shape, dtype, device, stream)
+    _ints(name, t, shape, dtype, device)
+    return t
+
+
+def _kv_state(lens, block_table, free_blocks, free_count):
+    """(B, device, table width, table row stride, number of blocks) of checked state."""
+    if not lens.is_cuda:
+        raise ValueError("tensors must be CUDA tensors (there is no CPU path)")
+    B, dev = lens.shape[0] if lens.dim() == 1 else -1, lens.device
+    _ints("lens", lens, (B,), torch.int32, dev)
+    if (block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B
+            or block_table.device != dev or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+        raise ValueError("block_table must be a [%d, width] int32 tensor on %s with contiguous rows" % (B, dev))
+    W = block_table.shape[1]
+    ld = block_table.stride(0) if B > 1 else W
+    if ld < W:
+        raise ValueError("block_table: rows overlap")
+    if (free_blocks is None) != (free_count is None):
+        raise ValueError("free_blocks and free_count go together")
+    N = 0
+    if free_blocks is not None:
+        if free_blocks.dim() != 1:
+            raise ValueError("free_blocks must be [num_blocks]")
+        N = free_blocks.shape[0]
+        _ints("free_blocks", free_blocks, (N,), torch.int32, dev)
+        _ints("free_count", free_count, (1,), torch.int32, dev)
+    return B, dev, W, ld, N
+
+
+def rmsnorm_kv_release(lens: torch.Tensor, finished: torch.Tensor, block_table: torch.Tensor,
+                       block_size: int, free_blocks: torch.Tensor, free_count: torch.Tensor, *,
+                       lens_out: Optional[torch.Tensor] = None,
+                       free_count_out: Optional[torch.Tensor] = None, stream=None):
+    """Gives the blocks of finished requests back: pushes them onto the stack
+    free_blocks ([num_blocks] int32, the first free_count[0] entries free) and
+    sets their lengths to 0, in place unless lens_out and free_count_out are
+    given.  lens: [B] int32; finished: [B] bool; block_table: [B, width] int32.
+    Returns (lens, free_count)."""
+    if free_blocks is None or free_count is None:
+        raise ValueError("rmsnorm_kv_release needs free_blocks and free_count")
+    B, dev, W, ld, N = _kv_state(lens, block_table, free_blocks, free_count)
+    _ints("finished", finished, (B,), torch.bool, dev)
+    lens_out = lens if lens_out is None else lens_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    _ints("lens_out", lens_out, (B,), torch.int32, dev)
+    _ints("free_count_out", free_count_out, (1,), torch.int32, dev)
+    st = _call(lens.get_device(), stream, _fn("rmsnorm_kv_release"), _ptr(lens), _ptr(finished),
+               _ptr(block_table), ld, W, block_size, _ptr(free_blocks), _ptr(free_count), N, _ptr(lens_out),
+               _ptr(free_count_out), B)
+    _native.check("rmsnorm_kv_release", st)
+    return lens_out, free_count_out
+
+
+def rmsnorm_kv_plan(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+                    block_size: int, num_tokens: int, *, free_blocks: Optional[torch.Tensor] = None,
+                    free_count: Optional[torch.Tensor] = None, lens_out: Optional[torch.Tensor] = None,
+                    free_count_out: Optional[torch.Tensor] = None,
+                    positions: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                    requests: Optional[torch.Tensor] = None, starts: Optional[torch.Tensor] = None,
+                    granted: Optional[torch.Tensor] = None, stream=None) -> KvPlan:
+    """Makes room for new_lens[b] tokens of each request and maps the step's
+    tokens (packed in request order, padded to num_tokens) to their positions,
+    cache slots and requests, as rmsnorm_rope_kv_append takes them.  Blocks come
+    off the stack free_blocks / free_count into block_table; without a pool the
+    table must have them already.  lens and free_count are updated in place
+    unless lens_out and free_count_out are given; a request without room is not
+    granted and its tokens get slot -1.  Returns a KvPlan."""
+    B, dev, W, ld, N = _kv_state(lens, block_table, free_blocks, free_count)
+    _ints("new_lens", new_lens, (B,), torch.int32, dev)
+    T = num_tokens
+    if T < 0:
+        raise ValueError("num_tokens must not be negative")
+    lens_out = lens if lens_out is None else lens_out
+    _ints("lens_out", lens_out, (B,), torch.int32, dev)
+    if free_count is not None:
+        free_count_out = free_count if free_count_out is None else free_count_out
+        _ints("free_count_out", free_count_out, (1,), torch.int32, dev)
+    elif free_count_out is not None:
+        raise ValueError("free_count_out given without a pool")
+    positions = _int_output("positions", positions, (T,), torch.int64, dev, stream)
+    slots = _int_output("slots", slots, (T,), torch.int64, dev, stream)
+    requests = _int_output("requests", requests, (T,), torch.int32, dev, stream)
+    starts = _int_output("starts", starts, (B + 1,), torch.int64, dev, stream)
+    granted = _int_output("granted", granted, (B,), torch.bool, dev, stream)
+    st = _call(lens.get_device(), stream, _fn("rmsnorm_kv_plan"), _ptr(lens), _ptr(new_lens),
+               _ptr(block_table), ld, W, block_size, _ptr(free_blocks), _ptr(free_count), N, _ptr(lens_out),
+               _ptr(free_count_out), _ptr(starts), _ptr(positions), _ptr(slots), _ptr(requests),
+               _ptr(granted), B, T)
+    _native.check("rmsnorm_kv_plan", st)
+    return KvPlan(positions, slots, requests, starts, granted, lens_out, free_count_out)
 
 
 def _check_rstd(rstd: torch.Tensor, rows: int, device: torch.device) -> None:

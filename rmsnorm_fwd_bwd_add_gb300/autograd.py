@@ -9,6 +9,8 @@ rms_norm(x, w, eps, weight_bias) -> out
 block_norm(y, residual, w_post, w_pre, eps, weight_bias, gate, scale) -> (out, new_residual)
     forward: rmsnorm_block_fwd with both scales saved; backward:
     rmsnorm_block_vjp on y and the saved new_residual.
+rope(q, k, positions, inv_freq, attn_scale, interleaved) -> (q_out, k_out)
+    forward: rmsnorm_rope; backward: the same rotation inverted.
 Inputs whose rows sit a stride apart (slices of wider buffers) are used in
 place; fp16, bf16 and fp32.
 
@@ -26,8 +28,8 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from .api import (rmsnorm_block_fwd, rmsnorm_block_vjp, rmsnorm_fwd_ex, rmsnorm_vjp_ex,
-                  rows_layout_ok)
+from .api import (rmsnorm_block_fwd, rmsnorm_block_vjp, rmsnorm_fwd_ex, rmsnorm_rope,
+                  rmsnorm_vjp_ex, rows_layout_ok)
 
 
 def _rows(t):
@@ -82,6 +84,36 @@ class RMSNormFunction(torch.autograd.Function):
                 gw32.to(w.dtype) if ctx.needs_input_grad[1] else None, None, None)
 
 
+def _heads(t):
+    """t itself when its heads' elements are contiguous, else a dense copy."""
+    return t if t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
+
+
+class RopeFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, attn_scale: float, interleaved: bool):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.attn_scale = attn_scale
+        ctx.interleaved = interleaved
+        return rmsnorm_rope(_heads(q), None if k is None else _heads(k), positions, inv_freq,
+                            attn_scale=attn_scale, interleaved=interleaved)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_q, g_k):
+        positions, inv_freq = ctx.saved_tensors
+        both = [g for g in (g_q, g_k) if g is not None]
+        turned = (None, None)
+        if both:  # a gradient that is missing takes no part
+            turned = rmsnorm_rope(_heads(both[0]), _heads(both[1]) if len(both) == 2 else None, positions,
+                                  inv_freq, attn_scale=ctx.attn_scale, interleaved=ctx.interleaved,
+                                  inverse=True)
+        got = iter(turned)
+        return (next(got) if g_q is not None else None, next(got) if g_k is not None else None,
+                None, None, None, None)
+
+
 class BlockNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, residual, w_post, w_pre, eps: float, weight_bias: float, gate, scale: float):
@@ -134,3 +166,9 @@ def block_norm(y, residual, w_post, w_pre, eps: float, weight_bias: float = 0.0,
     the block's gate and residual scale; differentiable in y, residual, both
     weights and the gate (scale is a constant)."""
     return BlockNormFunction.apply(y, residual, w_post, w_pre, eps, weight_bias, gate, scale)
+
+
+def rope(q, k, positions, inv_freq, attn_scale: float = 1.0, interleaved: bool = False):
+    """(q_out, k_out): q and k (which may be None) rotated to their positions, as
+    rmsnorm_rope; differentiable in q and k."""
+    return RopeFunction.apply(q, k, positions, inv_freq, attn_scale, interleaved)
