@@ -1,13 +1,13 @@
 // block.cu -- rmsnorm_block_fwd and rmsnorm_block_vjp: the norms before and
 // after a block fused with its gate and residual scale (argument checks and
-// the choice of kernel; the kernels are in block_generic.cuh).
+// the choice of kernel; the kernels are in block.cuh and block_generic.cuh).
 #include "rmsnorm.h"
 
 #include <algorithm>
 #include <cmath>
 
 #include "block.h"
-#include "block_generic.cuh"
+#include "common.cuh"
 #include "checks.h"
 #include "launch_util.h"
 
@@ -24,18 +24,62 @@ namespace {
 
 using namespace rmsn;
 
-template <typename T>
-cudaError_t launch_fwd(const BlockArgs &a, int sm, cudaStream_t s) {
-    const int grid = (int)std::min<int64_t>(a.rows, (int64_t)sm * 4);
-    return launch_pdl(block_fwd_generic_kernel<T>, dim3(grid), dim3(BLOCK_GENERIC_NT), 0, s, a);
+constexpr size_t SMEM_PER_SM = 227 * 1024;
+
+// Picks tier, unit and grid.  `unit` divides every address and stride (16 at
+// most); `tensors` row tensors are read.
+BlockPlan make_plan(int64_t rows, int64_t D, int es, int unit, int tensors, bool vjp, int sm) {
+    BlockPlan p{};
+    const int64_t row = D * es;
+    p.ub = unit % 16 == 0 && row % 16 == 0 ? 16 : unit % 4 == 0 && row % 4 == 0 ? 4 : 2;
+    const int per_thread = es == 2 && p.ub >= 4 ? 16 : 8;  // block_elems of block.cuh
+    const int64_t threads = ((D + per_thread - 1) / per_thread + 31) / 32 * 32;
+    if (threads > 1024) {
+        p.kind = BLOCK_GENERIC;
+        // the VJP keeps three fp32 rows of scratch a CTA: two CTAs an SM, fewer
+        // where they would take more than 256 MB
+        const int64_t fit = vjp ? std::max<int64_t>(8, ((int64_t)256 << 20) / (12 * D)) : 4 * sm;
+        p.grid = (int)std::min<int64_t>(rows, std::min<int64_t>((vjp ? 2 : 4) * (int64_t)sm, fit));
+        return p;
+    }
+    p.threads = (int)threads;
+    // threads an SM holds of the instance these take (block_launch.cuh)
+    const int resident = threads > 512 ? 1024 : 512;
+    const int per_sm = resident / (int)threads;
+    if (threads == 32) {
+        p.kind = BLOCK_WARP;
+        int warps = 8;  // rows side by side; fewer when the SMs would idle
+        while (warps > 1 && rows < (int64_t)warps * sm) warps /= 2;
+        p.threads = 32 * warps;
+        p.smem = vjp ? (size_t)warps * row / es * 4 : 0;
+        p.grid = (int)std::min<int64_t>((rows + warps - 1) / warps, (int64_t)sm * (512 / p.threads));
+    } else if (rows <= (int64_t)sm * per_sm) {
+        p.kind = BLOCK_DIRECT;
+        p.grid = (int)rows;
+    } else {
+        p.kind = BLOCK_STAGED;
+        p.grid = sm * per_sm;
+        p.stage_bytes = (uint32_t)((row + (p.ub == 16 ? 0 : 15) + 15) / 16 * 16);
+        // an SM's shared memory, less 1 KB a CTA for the system and 2 KB for the rest
+        const size_t room = (SMEM_PER_SM + 1024) / per_sm - 3 * 1024;
+        p.stages = (int)std::min<size_t>(8, room / ((size_t)tensors * p.stage_bytes));
+        p.smem = 128 + (size_t)p.stages * tensors * p.stage_bytes;
+    }
+    if (vjp && p.kind != BLOCK_DIRECT)  // scratch traffic small beside the rows'
+        p.grid = (int)std::min<int64_t>(p.grid, std::max<int64_t>(sm, rows / 48));
+    return p;
 }
 
-template <typename T>
-cudaError_t launch_vjp(const BlockArgs &a, int grid, cudaStream_t s) {
-    cudaError_t e = launch_pdl(block_vjp_generic_kernel<T>, dim3(grid), dim3(BLOCK_GENERIC_NT), 0, s, a);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(block_reduce_kernel<T>, dim3((unsigned)((a.D + 31) / 32)), dim3(32 * BR_WARPS), 0,
-                      s, a, grid);
+// The largest power of two up to 16 that divides the address and row stride.
+int unit_of(const Mat &m, int64_t rows, int es) {
+    if (!m.p) return 16;
+    const uintptr_t bits = (uintptr_t)m.p | (rows > 1 ? (uintptr_t)(m.ld * es) : 0) | 16u;
+    return (int)(bits & (~bits + 1));
+}
+
+template <typename T> struct Tag { using type = T; };
+template <typename F> auto by_type(int dtype, F f) {
+    return dtype == RMSNORM_F16 ? f(Tag<__half>{}) : dtype == RMSNORM_BF16 ? f(Tag<__nv_bfloat16>{}) : f(Tag<float>{});
 }
 
 // What both directions check about the weights, the gate and the scale.
@@ -117,9 +161,14 @@ extern "C" int rmsnorm_block_fwd(const void *y, int64_t ld_y, const void *residu
     a.rows = rows; a.D = (int)D;
     a.eps = eps; a.weight_bias = weight_bias; a.scale = scale;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == RMSNORM_F16    ? launch_fwd<__half>(a, sm, s)
-                          : dtype == RMSNORM_BF16 ? launch_fwd<__nv_bfloat16>(a, sm, s)
-                                                  : launch_fwd<float>(a, sm, s);
+    int unit = 16;
+    for (const Mat *m : {&my, &mr, &mo, &mn}) unit = std::min(unit, unit_of(*m, rows, es));
+    unit = std::min({unit, unit_of(mg, gate_rows, es), unit_of(Mat{w_pre, 0}, 1, es), unit_of(Mat{w_post, 0}, 1, es)});
+    const bool per_row = gate && gate_rows == rows;
+    const BlockPlan p = make_plan(rows, D, es, unit, per_row ? 3 : 2, false, sm);
+    a.stages = p.stages;
+    a.stage_bytes = p.stage_bytes;
+    const cudaError_t e = by_type(dtype, [&](auto t) { return launch_block_fwd<typename decltype(t)::type>(p, a, s); });
     return e == cudaSuccess ? RMSNORM_OK : record_cuda_error(e);
 }
 
@@ -204,18 +253,21 @@ extern "C" int rmsnorm_block_vjp(const void *y, int64_t ld_y, const void *h, int
     a.gw_post = gw_post; a.gw_pre = gw_pre; a.g_gate = g_gate;
     a.rows = rows; a.D = (int)D;
     a.eps = eps; a.weight_bias = weight_bias; a.scale = scale;
-    // three fp32 rows of scratch a CTA: two CTAs an SM, fewer where the rows
-    // are so long that they would take more than 256 MB
-    const int64_t fit = ((int64_t)256 << 20) / (12 * D);
-    const int grid = (int)std::min<int64_t>(rows, std::max<int64_t>(8, std::min<int64_t>(2 * sm, fit)));
+    int unit = 16;
+    for (const Mat &x : m) unit = std::min(unit, unit_of(x, rows, es));
+    unit = std::min({unit, unit_of(mgate, gate_rows, es), unit_of(Mat{w_pre, 0}, 1, es),
+                     unit_of(Mat{w_post, 0}, 1, es), unit_of(Mat{g_gate, 0}, 1, 4)});
+    const bool per_row = gate && gate_rows == rows;
+    const BlockPlan p = make_plan(rows, D, es, unit, 3 + (g_residual != nullptr) + per_row, true, sm);
+    a.stages = p.stages;
+    a.stage_bytes = p.stage_bytes;
+    const int grid = p.grid;
     void *ws = nullptr;
     st = scratch_alloc((size_t)grid * D * 12, s, &ws);
     if (st != RMSNORM_OK) return st;
     a.part_pre = static_cast<float *>(ws);
     a.part_mid = a.part_pre + (size_t)grid * D;
-    cudaError_t e = dtype == RMSNORM_F16    ? launch_vjp<__half>(a, grid, s)
-                    : dtype == RMSNORM_BF16 ? launch_vjp<__nv_bfloat16>(a, grid, s)
-                                            : launch_vjp<float>(a, grid, s);
+    const cudaError_t e = by_type(dtype, [&](auto t) { return launch_block_vjp<typename decltype(t)::type>(p, a, s); });
     st = e == cudaSuccess ? RMSNORM_OK : record_cuda_error(e);
     const int freed = scratch_free(ws, s);
     return st != RMSNORM_OK ? st : freed;

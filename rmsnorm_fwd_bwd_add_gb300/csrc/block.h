@@ -67,4 +67,18 @@ __host__ __device__ inline int64_t mid_slot(int64_t c, int64_t gr, int64_t grid,
     return 2 * c + (gr != first_row(c, grid, rows) / rows_per_gate ? 1 : 0);
 }
 
+// How a call runs: BLOCK_GENERIC for rows that do not fit on chip, else the
+// tier of block.cuh with units of `ub` bytes.
+enum : int { BLOCK_STAGED = 0, BLOCK_DIRECT = 1, BLOCK_WARP = 2, BLOCK_GENERIC = 3 };
+
+struct BlockPlan {
+    int kind, ub, threads, grid, stages;
+    uint32_t stage_bytes;
+    size_t smem;
+};
+
+// Launchers of one element type each (block_fwd_<type>.cu, block_vjp_<type>.cu).
+template <typename T> cudaError_t launch_block_fwd(const BlockPlan &p, const BlockArgs &a, cudaStream_t s);
+template <typename T> cudaError_t launch_block_vjp(const BlockPlan &p, const BlockArgs &a, cudaStream_t s);
+
 }  // namespace rmsn

@@ -1,0 +1,63 @@
+// block_launch.cuh -- picks the instance of a block kernel for a plan.
+#pragma once
+
+#include "block.cuh"
+#include "block_generic.cuh"
+#include "launch_util.h"
+
+namespace rmsn {
+
+template <bool VJP, typename T, int UB, int MAXT, int MINB, int KIND, bool GROW>
+cudaError_t launch_block_inst(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
+    static std::atomic<uint64_t> smem_mask{0};
+    void (*kern)(BlockArgs);
+    if constexpr (VJP) kern = block_vjp_kernel<T, UB, MAXT, MINB, KIND, GROW>;
+    else kern = block_fwd_kernel<T, UB, MAXT, MINB, KIND, GROW>;
+    if (p.smem > 0) {
+        const cudaError_t e = allow_max_dynamic_smem((const void *)kern, smem_mask);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(kern, dim3(p.grid), dim3(p.threads), p.smem, s, a);
+}
+
+template <bool VJP, typename T, int UB, bool GROW>
+cudaError_t launch_block_kind(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
+    if (p.kind == BLOCK_WARP) return launch_block_inst<VJP, T, UB, 256, 2, BLOCK_WARP, GROW>(p, a, s);
+    if (p.kind == BLOCK_DIRECT) {
+        if (p.threads <= 512) return launch_block_inst<VJP, T, UB, 512, 1, BLOCK_DIRECT, GROW>(p, a, s);
+        return launch_block_inst<VJP, T, UB, 1024, 1, BLOCK_DIRECT, GROW>(p, a, s);
+    }
+    if (p.threads <= 256) return launch_block_inst<VJP, T, UB, 256, 2, BLOCK_STAGED, GROW>(p, a, s);
+    if (p.threads <= 512) return launch_block_inst<VJP, T, UB, 512, 1, BLOCK_STAGED, GROW>(p, a, s);
+    return launch_block_inst<VJP, T, UB, 1024, 1, BLOCK_STAGED, GROW>(p, a, s);
+}
+
+template <bool VJP, typename T, int UB>
+cudaError_t launch_block_unit(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
+    return a.gate && a.rows_per_gate == 1 ? launch_block_kind<VJP, T, UB, true>(p, a, s)
+                                          : launch_block_kind<VJP, T, UB, false>(p, a, s);
+}
+
+template <bool VJP, typename T>
+cudaError_t launch_block(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
+    if (p.kind == BLOCK_GENERIC) {
+        if constexpr (VJP)
+            return launch_pdl(block_vjp_generic_kernel<T>, dim3(p.grid), dim3(BLOCK_GENERIC_NT), 0, s, a);
+        else
+            return launch_pdl(block_fwd_generic_kernel<T>, dim3(p.grid), dim3(BLOCK_GENERIC_NT), 0, s, a);
+    }
+    if (p.ub == 16) return launch_block_unit<VJP, T, 16>(p, a, s);
+    if constexpr (sizeof(T) == 2)
+        if (p.ub == 2) return launch_block_unit<VJP, T, 2>(p, a, s);
+    return launch_block_unit<VJP, T, 4>(p, a, s);
+}
+
+template <typename T>
+cudaError_t launch_block_vjp_both(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
+    const cudaError_t e = launch_block<true, T>(p, a, s);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(block_reduce_kernel<T>, dim3((unsigned)((a.D + 31) / 32)), dim3(32 * BR_WARPS), 0, s, a,
+                      p.grid);
+}
+
+}  // namespace rmsn

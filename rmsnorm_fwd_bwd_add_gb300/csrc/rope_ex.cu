@@ -28,6 +28,7 @@
 #include "checks.h"
 #include "common.cuh"
 #include "launch_util.h"
+#include "units.cuh"
 
 namespace rmsn {
 int current_sm_count(int *sm);
@@ -61,36 +62,6 @@ struct RopeExArgs {
     unsigned int *status;
 };
 
-// Vectors of VB bytes (16, or one element) and what one lane does with them.
-template <int VB> struct Raw;
-template <> struct Raw<16> { using type = uint4; };
-template <> struct Raw<4> { using type = uint32_t; };
-template <> struct Raw<2> { using type = uint16_t; };
-
-template <typename T, int VB>
-__device__ __forceinline__ void unpack_raw(const typename Raw<VB>::type &v, float (&f)[VB / sizeof(T)]) {
-    if constexpr (VB == 16) {
-        unpack_vec<T>(v, f);
-    } else {
-        T x;
-        memcpy(&x, &v, sizeof(T));
-        f[0] = Cvt<T>::load1(&x);
-    }
-}
-
-template <typename T, int VB>
-__device__ __forceinline__ typename Raw<VB>::type pack_raw(const float (&f)[VB / sizeof(T)]) {
-    if constexpr (VB == 16) {
-        return pack_vec<T>(f);
-    } else {
-        T x;
-        Cvt<T>::store1(&x, f[0]);
-        typename Raw<VB>::type v;
-        memcpy(&v, &x, sizeof(T));
-        return v;
-    }
-}
-
 // (cos, sin) of p times a frequency in turns.
 template <bool PRECISE>
 __device__ __forceinline__ float2 cos_sin(int64_t p, float2 f) {
@@ -115,7 +86,7 @@ __device__ __forceinline__ float2 cos_sin(int64_t p, float2 f) {
 template <typename T, int VB, bool INTERLEAVED>
 __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __grid_constant__ RopeExArgs a,
                                                                        int wpt) {
-    using V = typename Raw<VB>::type;
+    using V = typename RawUnit<VB>::type;
     constexpr int VE = VB / (int)sizeof(T);
     constexpr bool PAIRED = INTERLEAVED && VE > 1;  // both halves of a pair in one vector
     constexpr int PPU = PAIRED ? VE / 2 : VE;       // pairs a unit
@@ -181,7 +152,7 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
                     if (h < heads) {
                         T *dp = dst_of(h);
                         float fa[VE], fb[VE], ga[VE], gb[VE];
-                        unpack_raw<T, VB>(xa[j], fa);
+                        unpack_unit<T, VB>(xa[j], fa);
                         if constexpr (PAIRED) {
 #pragma unroll
                             for (int m = 0; m < PPU; ++m) {
@@ -189,15 +160,15 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
                                 ga[2 * m + 1] = fa[2 * m + 1] * cs[m].x + fa[2 * m] * cs[m].y;
                             }
                         } else {
-                            unpack_raw<T, VB>(xb[j], fb);
+                            unpack_unit<T, VB>(xb[j], fb);
 #pragma unroll
                             for (int m = 0; m < PPU; ++m) {
                                 ga[m] = fa[m] * cs[m].x - fb[m] * cs[m].y;
                                 gb[m] = fb[m] * cs[m].x + fa[m] * cs[m].y;
                             }
-                            *reinterpret_cast<V *>(dp + ib) = pack_raw<T, VB>(gb);
+                            *reinterpret_cast<V *>(dp + ib) = pack_unit<T, VB>(gb);
                         }
-                        *reinterpret_cast<V *>(dp + ia) = pack_raw<T, VB>(ga);
+                        *reinterpret_cast<V *>(dp + ia) = pack_unit<T, VB>(ga);
                     }
                 }
             }
