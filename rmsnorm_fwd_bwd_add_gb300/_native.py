@@ -7,10 +7,12 @@ library has not been built, every entry point raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
-from .build import LIB_PATH
+from .build import LIB_PATH, binding_path
 
 # Names exported by the library, in header order.
 EXPORTS = (
@@ -153,6 +155,32 @@ def lib() -> ctypes.CDLL:
                         "(nvcc, sm_103a); there is no CPU fallback" % LIB_PATH)
                 _lib = _bind(ctypes.CDLL(LIB_PATH))
     return _lib
+
+
+_BOUND = ("rmsnorm_block_fwd", "rmsnorm_block_vjp", "rmsnorm_rope", "rmsnorm_rope_kv_append_ex",
+          "rmsnorm_kv_release", "rmsnorm_kv_plan")
+_binding = None
+
+
+def binding():
+    """The native marshalling module (csrc/binding.cpp), bound to the library.
+    Raises if it was never built."""
+    global _binding
+    if _binding is None:
+        c = lib()
+        with _lock:
+            if _binding is None:
+                path = binding_path()
+                if not os.path.exists(path):
+                    raise RuntimeError(
+                        "%s is missing: build it with `python -m rmsnorm_fwd_bwd_add_gb300.build`" % path)
+                loader = importlib.machinery.ExtensionFileLoader("_binding", path)
+                mod = importlib.util.module_from_spec(
+                    importlib.util.spec_from_loader("_binding", loader))
+                loader.exec_module(mod)
+                mod.bind(check, {n: ctypes.cast(getattr(c, n), ctypes.c_void_p).value for n in _BOUND})
+                _binding = mod
+    return _binding
 
 
 def check(fn: str, status: int) -> None:

@@ -1,7 +1,8 @@
 """Python front end of the C ABI: same names, argument marshalling only.
 
 Every function checks dtype, device, contiguity and shape, then passes raw
-pointers and the current CUDA stream to librmsnorm_gb300.so.  All arithmetic
+pointers and the current CUDA stream to librmsnorm_gb300.so (the calls with the
+most tensors through csrc/binding.cpp, which does so natively).  All arithmetic
 runs in the library's CUDA kernels; nothing here computes.
 
 Tensors: x, residual, g are [..., D] fp16, bf16 or fp32 CUDA tensors,
@@ -455,43 +456,6 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str]
     return inv, float(attn.value)
 
 
-def _inv_freq(inv_freq: torch.Tensor, Dh: int) -> int:
-    """rot_dim of a checked inv_freq."""
-    if (inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.device.type != "cpu"
-            or not inv_freq.is_contiguous()):
-        raise ValueError("inv_freq must be a contiguous [rot_dim / 2] float64 CPU tensor")
-    rot = 2 * inv_freq.shape[0]
-    if rot < 2 or rot > Dh:
-        raise ValueError("inv_freq has %d pairs, a head of %d elements at most %d" % (rot // 2, Dh, Dh // 2))
-    return rot
-
-
-_I64x3 = ctypes.c_int64 * 3
-_I64x2 = ctypes.c_int64 * 2
-
-
-def _head_strides(name: str, t: torch.Tensor):
-    """Batch, token and head strides of a [(B,) S, H, Dh] tensor, for the C call."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError("%s: the elements of a head must be contiguous" % name)
-    st = t.stride()
-    return _I64x3(st[0] if t.dim() == 4 else 0, st[-3], st[-2])
-
-
-def _check_heads(name: str, t: torch.Tensor, ref: torch.Tensor, H: Optional[int] = None) -> None:
-    if t.dtype != ref.dtype or t.device != ref.device:
-        raise ValueError("%s must be %s on %s" % (name, ref.dtype, ref.device))
-    want = (*ref.shape[:-2], ref.shape[-2] if H is None else H, ref.shape[-1])
-    if tuple(t.shape) != want:
-        raise ValueError("%s must have shape %s, got %s" % (name, want, tuple(t.shape)))
-
-
-def _check_tokens(name: str, t: torch.Tensor, shape, ref: torch.Tensor) -> None:
-    if (t.dtype != torch.int64 or tuple(t.shape) != tuple(shape) or t.device != ref.device
-            or not t.is_contiguous()):
-        raise ValueError("%s must be a contiguous %s int64 tensor on %s" % (name, tuple(shape), ref.device))
-
-
 def rmsnorm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
                  inv_freq: torch.Tensor, *, attn_scale: float = 1.0, interleaved: bool = False,
                  inverse: bool = False, q_out: Optional[torch.Tensor] = None,
@@ -503,43 +467,7 @@ def rmsnorm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Te
     positions: int64 of q's leading shape; inv_freq, attn_scale as
     rope_frequencies returns them.  Pass q_out=q, k_out=k for in place; new
     outputs are allocated dense.  Returns (q_out, k_out)."""
-    if q.dim() not in (3, 4):
-        raise ValueError("q must be [S, Hq, Dh] or [B, S, Hq, Dh]")
-    if not q.is_cuda:
-        raise ValueError("tensors must be CUDA tensors (there is no CPU path)")
-    code = _dtype_code(q)
-    lead, Hq, Dh = q.shape[:-2], q.shape[-2], q.shape[-1]
-    rot = _inv_freq(inv_freq, Dh)
-    _check_tokens("positions", positions, lead, q)
-    Hkv = 0
-    if k is not None:
-        if k.dim() != q.dim():
-            raise ValueError("k must have q's leading dimensions")
-        Hkv = k.shape[-2]
-        _check_heads("k", k, q, Hkv)
-    elif k_out is not None:
-        raise ValueError("k_out given without k")
-    if q_out is None:
-        q_out = _new(q.shape, q.dtype, q.device, stream)
-    _check_heads("q_out", q_out, q)
-    if k is not None:
-        if k_out is None:
-            k_out = _new(k.shape, k.dtype, k.device, stream)
-        _check_heads("k_out", k_out, k)
-    st = _call(q.get_device(), stream, _fn("rmsnorm_rope"), _ptr(q), _head_strides("q", q), _ptr(k),
-               None if k is None else _head_strides("k", k), _ptr(positions), _ptr(q_out),
-               _head_strides("q_out", q_out), _ptr(k_out),
-               None if k is None else _head_strides("k_out", k_out), inv_freq.data_ptr(), attn_scale,
-               1 if interleaved else 0, 1 if inverse else 0, lead[0] if len(lead) == 2 else 1, lead[-1],
-               Hq, Hkv, Dh, rot, code)
-    _native.check("rmsnorm_rope", st)
-    return q_out, k_out
-
-
-def _strides2(name: str, t: torch.Tensor):
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError("%s: the elements of a head must be contiguous" % name)
-    return _I64x2(t.stride(0), t.stride(1))
+    return _run("rope", stream, q, k, positions, inv_freq, attn_scale, interleaved, inverse, q_out, k_out)
 
 
 def rmsnorm_rope_kv_append_ex(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -551,32 +479,8 @@ def rmsnorm_rope_kv_append_ex(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     [T, H, Dh] and the caches [num_slots, Hkv, Dh] with any token, slot and head
     strides, the first 2 * len(inv_freq) elements of each head rotated; fp32
     too.  Returns q_out."""
-    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape:
-        raise ValueError("q must be [T, Hq, Dh] and k, v [T, Hkv, Dh]")
-    if not q.is_cuda:
-        raise ValueError("tensors must be CUDA tensors (there is no CPU path)")
-    code = _dtype_code(q)
-    T, Hq, Dh = q.shape
-    Hkv = k.shape[1]
-    rot = _inv_freq(inv_freq, Dh)
-    _check_heads("k", k, q, Hkv)
-    _check_heads("v", v, q, Hkv)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if (t.dtype != q.dtype or t.device != q.device or t.dim() != 3 or t.shape[1:] != (Hkv, Dh)
-                or t.shape[0] != k_cache.shape[0]):
-            raise ValueError("the caches must be [num_slots, %d, %d] %s on %s" % (Hkv, Dh, q.dtype, q.device))
-    _check_tokens("positions", positions, (T,), q)
-    _check_tokens("slots", slots, (T,), q)
-    if q_out is None:
-        q_out = _new(q.shape, q.dtype, q.device, stream)
-    _check_heads("q_out", q_out, q)
-    st = _call(q.get_device(), stream, _fn("rmsnorm_rope_kv_append_ex"), _ptr(q), _strides2("q", q), _ptr(k),
-               _strides2("k", k), _ptr(v), _strides2("v", v), _ptr(positions), _ptr(slots), _ptr(q_out),
-               _strides2("q_out", q_out), _ptr(k_cache), _strides2("k_cache", k_cache), _ptr(v_cache),
-               _strides2("v_cache", v_cache), inv_freq.data_ptr(), attn_scale, 1 if interleaved else 0, T,
-               Hq, Hkv, Dh, rot, k_cache.shape[0], code)
-    _native.check("rmsnorm_rope_kv_append_ex", st)
-    return q_out
+    return _run("rope_append", stream, q, k, v, positions, slots, k_cache, v_cache, inv_freq, attn_scale,
+                interleaved, q_out)
 
 
 class KvPlan(NamedTuple):
@@ -592,43 +496,6 @@ class KvPlan(NamedTuple):
     free_count: Optional[torch.Tensor]
 
 
-def _ints(name: str, t: torch.Tensor, shape, dtype, device) -> None:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s %s tensor on %s" % (name, tuple(shape), dtype, device))
-
-
-def _int_output(name: str, t, shape, dtype, device, stream) -> torch.Tensor:
-    if t is None:
-        return _new(shape, dtype, device, stream)
-    _ints(name, t, shape, dtype, device)
-    return t
-
-
-def _kv_state(lens, block_table, free_blocks, free_count):
-    """(B, device, table width, table row stride, number of blocks) of checked state."""
-    if not lens.is_cuda:
-        raise ValueError("tensors must be CUDA tensors (there is no CPU path)")
-    B, dev = lens.shape[0] if lens.dim() == 1 else -1, lens.device
-    _ints("lens", lens, (B,), torch.int32, dev)
-    if (block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B
-            or block_table.device != dev or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
-        raise ValueError("block_table must be a [%d, width] int32 tensor on %s with contiguous rows" % (B, dev))
-    W = block_table.shape[1]
-    ld = block_table.stride(0) if B > 1 else W
-    if ld < W:
-        raise ValueError("block_table: rows overlap")
-    if (free_blocks is None) != (free_count is None):
-        raise ValueError("free_blocks and free_count go together")
-    N = 0
-    if free_blocks is not None:
-        if free_blocks.dim() != 1:
-            raise ValueError("free_blocks must be [num_blocks]")
-        N = free_blocks.shape[0]
-        _ints("free_blocks", free_blocks, (N,), torch.int32, dev)
-        _ints("free_count", free_count, (1,), torch.int32, dev)
-    return B, dev, W, ld, N
-
-
 def rmsnorm_kv_release(lens: torch.Tensor, finished: torch.Tensor, block_table: torch.Tensor,
                        block_size: int, free_blocks: torch.Tensor, free_count: torch.Tensor, *,
                        lens_out: Optional[torch.Tensor] = None,
@@ -638,19 +505,8 @@ def rmsnorm_kv_release(lens: torch.Tensor, finished: torch.Tensor, block_table: 
     sets their lengths to 0, in place unless lens_out and free_count_out are
     given.  lens: [B] int32; finished: [B] bool; block_table: [B, width] int32.
     Returns (lens, free_count)."""
-    if free_blocks is None or free_count is None:
-        raise ValueError("rmsnorm_kv_release needs free_blocks and free_count")
-    B, dev, W, ld, N = _kv_state(lens, block_table, free_blocks, free_count)
-    _ints("finished", finished, (B,), torch.bool, dev)
-    lens_out = lens if lens_out is None else lens_out
-    free_count_out = free_count if free_count_out is None else free_count_out
-    _ints("lens_out", lens_out, (B,), torch.int32, dev)
-    _ints("free_count_out", free_count_out, (1,), torch.int32, dev)
-    st = _call(lens.get_device(), stream, _fn("rmsnorm_kv_release"), _ptr(lens), _ptr(finished),
-               _ptr(block_table), ld, W, block_size, _ptr(free_blocks), _ptr(free_count), N, _ptr(lens_out),
-               _ptr(free_count_out), B)
-    _native.check("rmsnorm_kv_release", st)
-    return lens_out, free_count_out
+    return _run("kv_release", stream, lens, finished, block_table, block_size, free_blocks, free_count,
+                lens_out, free_count_out)
 
 
 def rmsnorm_kv_plan(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
@@ -667,29 +523,8 @@ def rmsnorm_kv_plan(lens: torch.Tensor, new_lens: torch.Tensor, block_table: tor
     table must have them already.  lens and free_count are updated in place
     unless lens_out and free_count_out are given; a request without room is not
     granted and its tokens get slot -1.  Returns a KvPlan."""
-    B, dev, W, ld, N = _kv_state(lens, block_table, free_blocks, free_count)
-    _ints("new_lens", new_lens, (B,), torch.int32, dev)
-    T = num_tokens
-    if T < 0:
-        raise ValueError("num_tokens must not be negative")
-    lens_out = lens if lens_out is None else lens_out
-    _ints("lens_out", lens_out, (B,), torch.int32, dev)
-    if free_count is not None:
-        free_count_out = free_count if free_count_out is None else free_count_out
-        _ints("free_count_out", free_count_out, (1,), torch.int32, dev)
-    elif free_count_out is not None:
-        raise ValueError("free_count_out given without a pool")
-    positions = _int_output("positions", positions, (T,), torch.int64, dev, stream)
-    slots = _int_output("slots", slots, (T,), torch.int64, dev, stream)
-    requests = _int_output("requests", requests, (T,), torch.int32, dev, stream)
-    starts = _int_output("starts", starts, (B + 1,), torch.int64, dev, stream)
-    granted = _int_output("granted", granted, (B,), torch.bool, dev, stream)
-    st = _call(lens.get_device(), stream, _fn("rmsnorm_kv_plan"), _ptr(lens), _ptr(new_lens),
-               _ptr(block_table), ld, W, block_size, _ptr(free_blocks), _ptr(free_count), N, _ptr(lens_out),
-               _ptr(free_count_out), _ptr(starts), _ptr(positions), _ptr(slots), _ptr(requests),
-               _ptr(granted), B, T)
-    _native.check("rmsnorm_kv_plan", st)
-    return KvPlan(positions, slots, requests, starts, granted, lens_out, free_count_out)
+    return KvPlan(*_run("kv_plan", stream, lens, new_lens, block_table, block_size, num_tokens, free_blocks,
+                        free_count, lens_out, free_count_out, positions, slots, requests, starts, granted))
 
 
 def _check_rstd(rstd: torch.Tensor, rows: int, device: torch.device) -> None:
@@ -765,59 +600,21 @@ def rmsnorm_vjp_ex(x: torch.Tensor, w: torch.Tensor, g: torch.Tensor, eps: float
     return gx, gw
 
 
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """An output allocated for use on `stream` (the current one when None):
-    memory of that stream's pool, so that no earlier work on another stream can
-    still be using it."""
+_native_fns = {}
+
+
+def _run(name: str, stream, *args):
+    """The binding's `name` on the current stream, or on `stream`: what it
+    allocates then comes from that stream's memory."""
+    f = _native_fns.get(name)
+    if f is None:
+        f = _native_fns[name] = getattr(_native.binding(), name)
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return f(*args)
+    if args[0].get_device() != stream.device_index:
+        raise ValueError("the stream is on cuda:%d, the tensors on %s" % (stream.device_index, args[0].device))
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _row_output(name, t, ref, stream):
-    """(t or a new dense tensor like ref, its row stride)."""
-    if t is None:
-        t = _new(ref.shape, ref.dtype, ref.device, stream)
-    return t, _check_rows_like(name, t, ref)
-
-
-def _fp32_output(name, t, shape, device, stream):
-    if t is None:
-        return _new(shape, torch.float32, device, stream)
-    if (t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or t.device != device
-            or not t.is_contiguous()):
-        raise ValueError("%s must be a contiguous float32 tensor of shape %s on %s" % (
-            name, tuple(shape), device))
-    return t
-
-
-def _check_gate(gate: Optional[torch.Tensor], x: torch.Tensor, rows: int, D: int) -> Tuple[int, int]:
-    """(gate rows, row stride) of a [..., D] gate whose rows divide x's rows."""
-    if gate is None:
-        return 0, 0
-    if gate.dtype != x.dtype or gate.device != x.device:
-        raise ValueError("gate must be %s on %s" % (x.dtype, x.device))
-    if gate.dim() < 1 or gate.shape[-1] != D:
-        raise ValueError("gate must be [..., %d], got %s" % (D, tuple(gate.shape)))
-    G, _, ld = _rows_ld("gate", gate)
-    if G < 1 or rows % G:
-        raise ValueError("the gate's %d rows must divide the %d rows" % (G, rows))
-    return G, ld
-
-
-def _check_block(x, w_post, w_pre, gate, rows, D):
-    _check_w(w_pre, x, D)
-    if w_post is not None:
-        _check_w(w_post, x, D)
-    return _check_gate(gate, x, rows, D)
-
-
-def _check_rstd2(rstd: torch.Tensor, rows: int, device: torch.device) -> None:
-    if (rstd.dtype != torch.float32 or rstd.dim() < 1 or rstd.shape[0] != 2 or rstd.numel() != 2 * rows
-            or rstd.device != device or not rstd.is_contiguous()):
-        raise ValueError("rstd must be a contiguous float32 tensor [2, rows] of %d rows on %s" % (
-            rows, device))
+        return f(*args)
 
 
 def rmsnorm_block_fwd(y: torch.Tensor, residual: torch.Tensor, w_post: Optional[torch.Tensor],
@@ -833,21 +630,8 @@ def rmsnorm_block_fwd(y: torch.Tensor, residual: torch.Tensor, w_post: Optional[
     here) or a [2, rows] float32 tensor that receives both norms' scales.
     Returns (out, new_residual, rstd); pass out=y or new_residual=residual to
     update in place."""
-    rows, D, ld_y = _rows_ld("y", y)
-    code = _dtype_code(y)
-    ld_r = _check_rows_like("residual", residual, y)
-    G, ld_gate = _check_block(y, w_post, w_pre, gate, rows, D)
-    out, ld_o = _row_output("out", out, y, stream)
-    new_residual, ld_n = _row_output("new_residual", new_residual, y, stream)
-    if rstd is True:
-        rstd = _new((2, *y.shape[:-1]), torch.float32, y.device, stream)
-    if rstd is not None:
-        _check_rstd2(rstd, rows, y.device)
-    st = _call(y.get_device(), stream, _fn("rmsnorm_block_fwd"), _ptr(y), ld_y, _ptr(residual), ld_r,
-               _ptr(w_post), _ptr(w_pre), _ptr(gate), ld_gate, G, scale, eps, weight_bias, _ptr(out),
-               ld_o, _ptr(new_residual), ld_n, _ptr(rstd), rows, D, code)
-    _native.check("rmsnorm_block_fwd", st)
-    return out, new_residual, rstd
+    return _run("block_fwd", stream, y, residual, w_post, w_pre, eps, weight_bias, gate, scale, out,
+                new_residual, rstd)
 
 
 def rmsnorm_block_vjp(y: torch.Tensor, h: torch.Tensor, w_post: Optional[torch.Tensor],
@@ -863,31 +647,8 @@ def rmsnorm_block_vjp(y: torch.Tensor, h: torch.Tensor, w_post: Optional[torch.T
     or without.  Returns (g_y, g_h, gw_post, gw_pre, g_gate): g_h is the
     gradient of residual, the weights' and the gate's gradients are float32
     (None without a post-norm, without a gate)."""
-    rows, D, ld_y = _rows_ld("y", y)
-    code = _dtype_code(y)
-    ld_h = _check_rows_like("h", h, y)
-    ld_g = _check_rows_like("g_out", g_out, y)
-    ld_gr = D if g_residual is None else _check_rows_like("g_residual", g_residual, y)
-    G, ld_gate = _check_block(y, w_post, w_pre, gate, rows, D)
-    if rstd is not None:
-        _check_rstd2(rstd, rows, y.device)
-    g_y, ld_gy = _row_output("g_y", g_y, y, stream)
-    g_h, ld_gh = _row_output("g_h", g_h, y, stream)
-    gw_pre = _fp32_output("gw_pre", gw_pre, (D,), y.device, stream)
-    if w_post is not None:
-        gw_post = _fp32_output("gw_post", gw_post, (D,), y.device, stream)
-    elif gw_post is not None:
-        raise ValueError("gw_post given without w_post")
-    if gate is not None:
-        g_gate = _fp32_output("g_gate", g_gate, gate.shape, y.device, stream)
-    elif g_gate is not None:
-        raise ValueError("g_gate given without a gate")
-    st = _call(y.get_device(), stream, _fn("rmsnorm_block_vjp"), _ptr(y), ld_y, _ptr(h), ld_h,
-               _ptr(w_post), _ptr(w_pre), _ptr(gate), ld_gate, G, scale, _ptr(g_out), ld_g,
-               _ptr(g_residual), ld_gr, _ptr(rstd), eps, weight_bias, _ptr(g_y), ld_gy, _ptr(g_h),
-               ld_gh, _ptr(gw_post), _ptr(gw_pre), _ptr(g_gate), rows, D, code)
-    _native.check("rmsnorm_block_vjp", st)
-    return g_y, g_h, gw_post, gw_pre, g_gate
+    return _run("block_vjp", stream, y, h, w_post, w_pre, g_out, eps, weight_bias, gate, scale,
+                g_residual, rstd, g_y, g_h, gw_post, gw_pre, g_gate)
 
 
 def rmsnorm_vjp_workspace_size(rows: int, D: int, dtype: torch.dtype) -> int:

@@ -1,4 +1,6 @@
-"""Builds librmsnorm_gb300.so in-tree from csrc/*.cu with nvcc for sm_103a.
+"""Builds librmsnorm_gb300.so in-tree from csrc/*.cu with nvcc for sm_103a, and
+_binding.*.so, the native argument marshalling of api.py, from csrc/binding.cpp
+with g++ against the installed torch (its version is part of the file's name).
 
 Each translation unit compiles in its own nvcc process (in parallel), then
 nvcc links them into one shared library with the CUDA runtime linked
@@ -16,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_DIR = os.path.dirname(PKG_DIR)
@@ -28,6 +31,13 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
               "-I" + INCLUDE, "-I" + CSRC]
+
+
+def binding_path() -> str:
+    """The binding built for this torch and Python."""
+    import torch
+    return os.path.join(PKG_DIR, "_binding.%s.torch%s.so" % (
+        sys.implementation.cache_tag, torch.__version__.replace("+", "_")))
 
 
 def _nvcc() -> str:
@@ -66,14 +76,44 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _binding_stale(path: str) -> bool:
+    src = os.path.join(CSRC, "binding.cpp")
+    return not os.path.exists(path) or os.path.getmtime(src) > os.path.getmtime(path)
+
+
+def _compile_binding(path: str) -> None:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")]
+    tmp = path + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(),
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp]
+    cmd += ["-isystem" + i for i in inc]
+    cmd += ["-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on binding.cpp:\n%s\n%s" % (r.stdout, r.stderr))
+    os.replace(tmp, path)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link the library if needed; returns its path."""
-    if not force and not _stale(LIB_PATH):
+    """Compile and link the library and the binding if needed; returns the
+    library's path."""
+    binding = binding_path()
+    lib_stale, binding_stale = force or _stale(LIB_PATH), force or _binding_stale(binding)
+    if not lib_stale and not binding_stale:
         return LIB_PATH
     os.makedirs(OBJ_DIR, exist_ok=True)
-    srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    srcs = _sources() if lib_stale else []
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        bound = ex.submit(_compile_binding, binding) if binding_stale else None
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        if bound is not None:
+            bound.result()
+    if not lib_stale:
+        return LIB_PATH
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
     cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
