@@ -26,13 +26,20 @@ using namespace rmsn;
 
 constexpr size_t SMEM_PER_SM = 227 * 1024;
 
+// Threads an SM holds of the instance that CTAs of `threads` take (the register
+// caps of block_launch.cuh).
+int block_resident(int threads, bool vjp) {
+    if (!vjp && ((threads > 256 && threads <= 320) || (threads > 512 && threads <= 640))) return 640;
+    return threads > 512 ? 1024 : 512;
+}
+
 // Picks tier, unit and grid.  `unit` divides every address and stride (16 at
 // most); `tensors` row tensors are read.
 BlockPlan make_plan(int64_t rows, int64_t D, int es, int unit, int tensors, bool vjp, int sm) {
     BlockPlan p{};
     const int64_t row = D * es;
     p.ub = unit % 16 == 0 && row % 16 == 0 ? 16 : unit % 4 == 0 && row % 4 == 0 ? 4 : 2;
-    const int per_thread = es == 2 && p.ub >= 4 ? 16 : 8;  // block_elems of block.cuh
+    const int per_thread = 32 / es;  // elements: block_units of block.cuh
     const int64_t threads = ((D + per_thread - 1) / per_thread + 31) / 32 * 32;
     if (threads > 1024) {
         p.kind = BLOCK_GENERIC;
@@ -43,27 +50,29 @@ BlockPlan make_plan(int64_t rows, int64_t D, int es, int unit, int tensors, bool
         return p;
     }
     p.threads = (int)threads;
+    const size_t table = (size_t)(D * 4 + 127) / 128 * 128;  // w1 (block_table_bytes)
     // threads an SM holds of the instance these take (block_launch.cuh)
-    const int resident = threads > 512 ? 1024 : 512;
+    const int resident = block_resident((int)threads, vjp);
     const int per_sm = resident / (int)threads;
     if (threads == 32) {
         p.kind = BLOCK_WARP;
         int warps = 8;  // rows side by side; fewer when the SMs would idle
         while (warps > 1 && rows < (int64_t)warps * sm) warps /= 2;
         p.threads = 32 * warps;
-        p.smem = vjp ? (size_t)warps * row / es * 4 : 0;
+        p.smem = 128 + table + (vjp ? (size_t)warps * ((D + 3) / 4 * 16) : 0);
         p.grid = (int)std::min<int64_t>((rows + warps - 1) / warps, (int64_t)sm * (512 / p.threads));
     } else if (rows <= (int64_t)sm * per_sm) {
         p.kind = BLOCK_DIRECT;
         p.grid = (int)rows;
+        p.smem = 128 + table;
     } else {
         p.kind = BLOCK_STAGED;
         p.grid = sm * per_sm;
         p.stage_bytes = (uint32_t)((row + (p.ub == 16 ? 0 : 15) + 15) / 16 * 16);
         // an SM's shared memory, less 1 KB a CTA for the system and 2 KB for the rest
-        const size_t room = (SMEM_PER_SM + 1024) / per_sm - 3 * 1024;
+        const size_t room = (SMEM_PER_SM + 1024) / per_sm - 3 * 1024 - table;
         p.stages = (int)std::min<size_t>(8, room / ((size_t)tensors * p.stage_bytes));
-        p.smem = 128 + (size_t)p.stages * tensors * p.stage_bytes;
+        p.smem = 128 + table + (size_t)p.stages * tensors * p.stage_bytes;
     }
     if (vjp && p.kind != BLOCK_DIRECT)  // scratch traffic small beside the rows'
         p.grid = (int)std::min<int64_t>(p.grid, std::max<int64_t>(sm, rows / 48));

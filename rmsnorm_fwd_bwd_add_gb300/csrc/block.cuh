@@ -1,8 +1,14 @@
 // block.cuh -- the norm pair around a block for rows that fit on chip.
 //
 // HBM-bound: the forward moves four row tensors, the VJP up to six, each once.
-// A row's elements sit in registers, UNITS units a thread, from the one read to
-// the outputs; both norms' sums cross the CTA through one barrier each.
+// A row's elements sit in registers, 32 bytes of each tensor a thread, from the
+// one read to the outputs, and all of a row's sums cross the CTA through one
+// barrier, although the second norm's depends on the first's:
+//   forward: with v = m y, m = scale * gate * w2, sum h^2 = sum res^2 + 2 r_y sum
+//     res v + r_y^2 sum v^2.  Where the block nearly undoes the stream (the
+//     result is below an eighth of its terms) it is summed again from h itself.
+//   VJP: sum m g_h y = r_h (sum u g w1 - c sum u h) + sum u g_res, u = m y: the
+//     same terms as its own sum has, so no digits are lost.
 //
 //   BLOCK_STAGED  one row a CTA at a time out of a shared-memory ring that thread
 //                 0 fills with 1-D bulk copies `stages` rows ahead, so that the
@@ -14,45 +20,187 @@
 //                 CTAs fit at once, where a ring has nothing to run ahead of.
 //   BLOCK_WARP    one row a warp (short rows): no barriers; several rows a CTA.
 //
-// Per-thread state: w1 = weight_bias + w_pre and m = scale * gate * (weight_bias
-// + w_post) of its columns in fp32 (m is rebuilt when the CTA's rows pass to
+// w1 = weight_bias + w_pre sits in shared memory in fp32 (in registers the VJP
+// spilled), m = scale * gate * (weight_bias + w_post) of a thread's columns in
+// its registers (m is rebuilt when the CTA's rows pass to
 // another gate row; with a gate row per row, the gate streams with the row and
 // m holds the rest), the VJP's two accumulators of its columns.
 #pragma once
+
+#include <type_traits>
 
 #include "block.h"
 #include "units.cuh"
 
 namespace rmsn {
 
-// Elements a thread owns: 32 bytes of a row in 16-byte or 4-byte units of 16-bit
-// types; 8 elements otherwise.
-template <typename T, int UB> __host__ __device__ constexpr int block_units() {
-    return sizeof(T) == 2 && UB >= 4 ? 16 / unit_elems<T, UB>() : 8 / unit_elems<T, UB>();
-}
-template <typename T, int UB> __host__ __device__ constexpr int block_elems() {
-    return block_units<T, UB>() * unit_elems<T, UB>();
-}
+// A thread owns 32 bytes of a row as SLOTS slots of P float2 pairs, the operands of
+// packed fp32x2 arithmetic.  A slot is one unit, or, for one-element units, two
+// of them a CTA's width apart (its second may lie past the row: it reads 0 and
+// is not written).  `raw` keeps a slot's elements packed.
+template <typename T, int UB> struct Slot {
+    static constexpr int E = unit_elems<T, UB>();
+    static constexpr int P = E > 1 ? E / 2 : 1;
+    static constexpr int COUNT = 32 / (int)sizeof(T) / (2 * P);
+    using Unit = typename RawUnit<UB>::type;
+    struct Two { uint32_t a, b; };  // two fp32 units
+    using Raw = typename std::conditional<(E > 1), Unit,
+                                          typename std::conditional<sizeof(T) == 4, Two, uint32_t>::type>::type;
+
+    // First unit of slot j of thread t among NT; whether the slot has any.
+    static __device__ __forceinline__ int unit(int j, int t, int NT) { return t + (E > 1 ? j : 2 * j) * NT; }
+
+    static __device__ __forceinline__ Raw load(const void *row, int u, int NT, int NU) {
+        const Unit *p = static_cast<const Unit *>(row);
+        if constexpr (E > 1) {
+            return p[u];
+        } else if constexpr (sizeof(T) == 4) {
+            return Two{p[u], u + NT < NU ? p[u + NT] : 0u};
+        } else {
+            return (uint32_t)p[u] | (u + NT < NU ? (uint32_t)p[u + NT] << 16 : 0u);
+        }
+    }
+    static __device__ __forceinline__ void unpack(const Raw &v, float2 (&f)[P]) {
+        if constexpr (E > 2) {
+            unpack_vec<T>(v, f);
+        } else if constexpr (sizeof(T) == 4) {
+            f[0] = make_float2(__uint_as_float(v.a), __uint_as_float(v.b));
+        } else {
+            f[0] = Cvt<T>::unpack2(v);
+        }
+    }
+    static __device__ __forceinline__ void load_pairs(const void *row, int u, int NT, int NU, float2 (&f)[P]) {
+        unpack(load(row, u, NT, NU), f);
+    }
+    static __device__ __forceinline__ void store(void *row, int u, int NT, int NU, const float2 (&f)[P]) {
+        Unit *p = static_cast<Unit *>(row);
+        if constexpr (E > 2) {
+            p[u] = pack_vec<T>(f);
+        } else if constexpr (E == 2) {
+            p[u] = Cvt<T>::pack2(f[0].x, f[0].y);
+        } else if constexpr (sizeof(T) == 4) {
+            p[u] = __float_as_uint(f[0].x);
+            if (u + NT < NU) p[u + NT] = __float_as_uint(f[0].y);
+        } else {
+            const uint32_t v = Cvt<T>::pack2(f[0].x, f[0].y);
+            p[u] = (uint16_t)v;
+            if (u + NT < NU) p[u + NT] = (uint16_t)(v >> 16);
+        }
+    }
+    // The slot's elements as floats at their columns of an fp32 row (16-byte
+    // aligned where a unit has four elements or more).
+    static __device__ __forceinline__ void store_floats(float *row, int u, int NT, int NU, const float2 (&f)[P], float k) {
+        if constexpr (E >= 4) {
+#pragma unroll
+            for (int i = 0; i < E / 4; ++i)
+                reinterpret_cast<float4 *>(row + (size_t)u * E)[i] =
+                    make_float4(f[2 * i].x * k, f[2 * i].y * k, f[2 * i + 1].x * k, f[2 * i + 1].y * k);
+        } else if constexpr (E == 2) {
+            row[2 * u] = f[0].x * k;
+            row[2 * u + 1] = f[0].y * k;
+        } else {
+            row[u] = f[0].x * k;
+            if (u + NT < NU) row[u + NT] = f[0].y * k;
+        }
+    }
+    // A per-column table in shared memory, laid out so that a warp's lanes read
+    // consecutive 16- or 8-byte words: [pairs of pairs][units] (E >= 4), [units].
+    static __device__ __forceinline__ void put(float *tab, int u, int NT, int NU, const float2 (&f)[P]) {
+        if constexpr (E >= 4) {
+#pragma unroll
+            for (int i = 0; i < E / 4; ++i)
+                reinterpret_cast<float4 *>(tab)[i * NU + u] = make_float4(f[2 * i].x, f[2 * i].y, f[2 * i + 1].x, f[2 * i + 1].y);
+        } else if constexpr (E == 2) {
+            reinterpret_cast<float2 *>(tab)[u] = f[0];
+        } else {
+            tab[u] = f[0].x;
+            if (u + NT < NU) tab[u + NT] = f[0].y;
+        }
+    }
+    static __device__ __forceinline__ void get(const float *tab, int u, int NT, int NU, float2 (&f)[P]) {
+        if constexpr (E >= 4) {
+#pragma unroll
+            for (int i = 0; i < E / 4; ++i) {
+                const float4 v = reinterpret_cast<const float4 *>(tab)[i * NU + u];
+                f[2 * i] = make_float2(v.x, v.y);
+                f[2 * i + 1] = make_float2(v.z, v.w);
+            }
+        } else if constexpr (E == 2) {
+            f[0] = reinterpret_cast<const float2 *>(tab)[u];
+        } else {
+            f[0] = make_float2(tab[u], u + NT < NU ? tab[u + NT] : 0.f);
+        }
+    }
+};
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 constexpr int BLOCK_MAX_STAGES = 8;
-constexpr int BLOCK_HEADER = 128;  // the ring's mbarriers, ahead of its data
+// Shared memory: the ring's mbarriers, the table w1, then the ring (or the VJP's
+// sums over warps, BLOCK_WARP).
+constexpr int BLOCK_HEADER = 128;
+__host__ __device__ constexpr uint32_t block_table_bytes(int D) { return ((uint32_t)D * 4u + 127u) & ~127u; }
+
+// Sums of four (N <= 4) or eight (N <= 8) values over a warp at once.  The first
+// steps halve the number of values a lane carries instead of summing each over
+// all lanes: 2 + 1 + 1 + 1 + 1 shuffles for four values where one butterfly each
+// takes 20.  Lane l ends with the sum of value l % K over the warp, the same bits
+// in every lane that has it.
+template <int K>
+__device__ __forceinline__ float spread_sums(float (&v)[K]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = K / 2; h > 0; h /= 2) {  // lanes with bit h keep the upper h values
+        const bool up = lane & h;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            const float give = up ? v[i] : v[i + h], keep = up ? v[i + h] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, h);
+        }
+    }
+    float t = v[0];
+#pragma unroll
+    for (int off = K; off < 32; off *= 2) t += __shfl_xor_sync(0xffffffffu, t, off);
+    return t;
+}
+
+template <int N> __host__ __device__ constexpr int spread_of() { return N <= 1 ? 1 : N <= 4 ? 4 : 8; }
+
+// Sums of N values over a warp, the same in every lane.
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&v)[N]) {
+    constexpr int K = spread_of<N>();
+    float x[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) x[i] = i < N ? v[i < N ? i : 0] : 0.f;
+    const float t = spread_sums<K>(x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, t, i);
+}
 
 // Sums of N values over the CTA's `nw` warps (at most MAXW), the same in every
-// thread; `red` holds N floats a warp.  Returns false if any thread passed !ok.
+// thread; `red` holds eight floats a warp.  Returns false if any thread passed
+// !ok.
 template <int N, int MAXW>
-__device__ __forceinline__ bool cta_sums(float (&v)[N], float (*red)[4], int nw, bool ok) {
-    constexpr int WP = MAXW <= 4 ? 4 : MAXW <= 8 ? 8 : MAXW <= 16 ? 16 : 32;
+__device__ __forceinline__ bool cta_sums(float (&v)[N], float (*red)[8], int nw, bool ok) {
+    constexpr int K = spread_of<N>(), ROWS = 32 / K;  // warps a step covers
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float x[K];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = group_sum<32>(v[i]);
-    if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) red[warp][i] = v[i];
-    }
+    for (int i = 0; i < K; ++i) x[i] = i < N ? v[i < N ? i : 0] : 0.f;
+    const float t = spread_sums<K>(x);
+    if (lane < K) red[warp][lane] = t;
     const bool bad = __syncthreads_or(!ok);
-    const int w = lane & (WP - 1);
+    float s = 0.f;  // value lane % K of warps lane / K, lane / K + ROWS, ...
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = group_sum<WP>(w < nw ? red[w][i] : 0.f);
+    for (int w0 = 0; w0 < MAXW; w0 += ROWS) {
+        const int w = w0 + lane / K;
+        if (w < nw) s += red[w][lane % K];
+    }
+#pragma unroll
+    for (int off = K; off < 32; off *= 2) s += __shfl_xor_sync(0xffffffffu, s, off);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, s, i);
     return !bad;
 }
 
@@ -90,13 +238,25 @@ __device__ __forceinline__ void ring_issue(const BlockRing &ring, const BlockArg
         }
 }
 
+// Hides from the compiler that a register's value is unchanged, so that units
+// kept across a barrier stay packed and are unpacked again behind it (bf16: 8
+// registers a tensor instead of 16).
+__device__ __forceinline__ void keep_packed(uint4 &v) {
+    asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w));
+}
+__device__ __forceinline__ void keep_packed(uint32_t &v) { asm volatile("" : "+r"(v)); }
+template <typename V> __device__ __forceinline__ void keep_packed(V &v) {
+    asm volatile("" : "+r"(v.a), "+r"(v.b));
+}
+
 // Forward -----------------------------------------------------------------
 template <typename T, int UB, int MAXT, int MINB, int KIND, bool GROW>
 __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_constant__ BlockArgs a) {
-    using Raw = typename RawUnit<UB>::type;
-    constexpr int E = unit_elems<T, UB>(), V = block_units<T, UB>(), MAXW = MAXT / 32;
+    using SL = Slot<T, UB>;
+    using Raw = typename SL::Raw;
+    constexpr int E = SL::E, V = SL::COUNT, P = SL::P, MAXW = MAXT / 32;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float s_red[2][KIND == BLOCK_WARP ? 1 : MAXW][4];
+    __shared__ float s_red[2][KIND == BLOCK_WARP ? 1 : MAXW][8];
     const int NT = KIND == BLOCK_WARP ? 32 : (int)blockDim.x;
     const int t0 = KIND == BLOCK_WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
     const int R = KIND == BLOCK_WARP ? (int)(blockDim.x >> 5) : 1;
@@ -108,7 +268,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
 
     const void *src[5] = {a.y, a.res, per_row ? a.gate : nullptr, nullptr, nullptr};
     const int64_t ld[5] = {a.ld_y, a.ld_res, a.ld_gate, 0, 0};
-    BlockRing ring{reinterpret_cast<uint64_t *>(smem), smem + BLOCK_HEADER, a.stages, a.stage_bytes, per_row ? 3 : 2};
+    BlockRing ring{reinterpret_cast<uint64_t *>(smem), smem + BLOCK_HEADER + block_table_bytes(a.D), a.stages, a.stage_bytes, per_row ? 3 : 2};
     uint64_t policy = 0;
     if constexpr (KIND == BLOCK_STAGED) {
         policy = l2_evict_first_policy();
@@ -124,35 +284,39 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
             for (int s = 0; s < ring.S && r0 + s < r1; ++s) ring_issue<T>(ring, a, src, ld, r0 + s, s, policy);
     }
 
-    // w1, and m without the gate
-    float w1[V][E], m[V][E];
-    auto load_unit = [&](const void *base, int u, float (&f)[E]) {
-        unpack_unit<T, UB>(static_cast<const Raw *>(base)[u], f);
+    // w1 in shared memory, m without the gate in registers
+    float *w1 = reinterpret_cast<float *>(smem + BLOCK_HEADER);
+    float2 m[V][P];
+    auto load_unit = [&](const void *base, int u, float2 (&f)[P]) {
+        SL::load_pairs(base, u, NT, NU, f);
     };
     auto load_m = [&](const T *gate_row) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int u = t0 + j * NT;
+            const int u = SL::unit(j, t0, NT);
             if (u < NU) {
-                float f[E], q[E];
+                float2 f[P], q[P];
                 if (post) load_unit(a.w_post, u, f);
                 if (gate_row) load_unit(gate_row, u, q);
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    m[j][e] = (post ? a.weight_bias + f[e] : 1.f) * (gate_row ? a.scale * q[e] : a.scale);
+                for (int p = 0; p < P; ++p)
+                    m[j][p] = f2mul(post ? f2add(both(a.weight_bias), f[p]) : both(1.f),
+                                    gate_row ? f2mul(both(a.scale), q[p]) : both(a.scale));
             }
         }
     };
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int u = t0 + j * NT;
+        const int u = SL::unit(j, t0, NT);
         if (u < NU) {
-            float f[E];
+            float2 f[P];
             load_unit(a.w_pre, u, f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) w1[j][e] = a.weight_bias + f[e];
+            for (int p = 0; p < P; ++p) f[p] = f2add(both(a.weight_bias), f[p]);
+            if (KIND != BLOCK_WARP || threadIdx.x < 32) SL::put(w1, u, NT, NU, f);
         }
     }
+    if (KIND == BLOCK_WARP) __syncthreads();  // otherwise a thread reads what it wrote
     if (!a.gate || per_row) load_m(nullptr);
 
     int64_t group_end = a.gate && !per_row ? r0 : INT64_MAX;  // first row past the gate row held in m
@@ -175,40 +339,51 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
             if (per_row) pg = reinterpret_cast<const T *>(st + 2 * ring.stage_bytes + ((uintptr_t)pg & 15u));
             ok = mbar_wait_bounded(&ring.full[s], ph, a.wait_budget);
         }
-        Raw vy[V], vr[V];
-        float v[V][E];  // m * y, the added term before r_y
-        float sum[1] = {0.f};
+        Raw vy[V], vr[V], vg[GROW ? V : 1];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int u = t0 + j * NT;
+            const int u = SL::unit(j, t0, NT);
             if (u < NU) {
-                vy[j] = reinterpret_cast<const Raw *>(py)[u];
-                vr[j] = reinterpret_cast<const Raw *>(pr)[u];
+                vy[j] = SL::load(py, u, NT, NU);
+                vr[j] = SL::load(pr, u, NT, NU);
+                if constexpr (GROW) vg[j] = SL::load(pg, u, NT, NU);
             }
         }
+        // v = m y of unit j, the added term before r_y
+        auto added = [&](int j, const float2 (&y)[P], float2 (&v)[P]) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) v[p] = f2mul(m[j][p], y[p]);
+            if constexpr (GROW) {
+                float2 q[P];
+                SL::unpack(vg[j], q);
+#pragma unroll
+                for (int p = 0; p < P; ++p) v[p] = f2mul(v[p], q[p]);
+            }
+        };
+        float2 s2[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};  // y^2, res^2, res v, v^2
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int u = t0 + j * NT;
-            if (u < NU) {
-                float f[E];
-                unpack_unit<T, UB>(vy[j], f);
+            if (SL::unit(j, t0, NT) < NU) {
+                float2 y[P], r[P], v[P];
+                SL::unpack(vy[j], y);
+                SL::unpack(vr[j], r);
+                added(j, y, v);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    sum[0] = fmaf(f[e], f[e], sum[0]);
-                    v[j][e] = m[j][e] * f[e];
-                }
-                if constexpr (GROW) {
-                    float q[E];
-                    load_unit(pg, u, q);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) v[j][e] *= q[e];
+                for (int p = 0; p < P; ++p) {
+                    s2[0] = f2fma(y[p], y[p], s2[0]);
+                    s2[1] = f2fma(r[p], r[p], s2[1]);
+                    s2[2] = f2fma(r[p], v[p], s2[2]);
+                    s2[3] = f2fma(v[p], v[p], s2[3]);
                 }
             }
         }
+        float sum[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = s2[i].x + s2[i].y;
         if constexpr (KIND == BLOCK_WARP) {
-            sum[0] = group_sum<32>(sum[0]);
+            warp_sums<4>(sum);
         } else {
-            ok = cta_sums<1, MAXW>(sum, s_red[0], nw, ok);
+            ok = cta_sums<4, MAXW>(sum, s_red[row & 1], nw, ok);
         }
         if constexpr (KIND == BLOCK_STAGED) {
             if (!ok) {  // leave once this CTA's copies have landed
@@ -225,38 +400,60 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
             // every thread has its units of this stage in registers
             if (threadIdx.x == 0 && row + ring.S < r1) ring_issue<T>(ring, a, src, ld, row + ring.S, s, policy);
         }
-        const float r_y = post ? rsqrtf(sum[0] * inv_D + a.eps) : 1.f;
-        sum[0] = 0.f;
+        if constexpr (MAXT * MINB > 512) {  // 96 registers or fewer
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int u = t0 + j * NT;
-            if (u < NU) {
-                float f[E];
-                unpack_unit<T, UB>(vr[j], f);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    v[j][e] = fmaf(v[j][e], r_y, f[e]);  // h
-                    sum[0] = fmaf(v[j][e], v[j][e], sum[0]);
-                }
+            for (int j = 0; j < V; ++j) {
+                keep_packed(vy[j]);
+                keep_packed(vr[j]);
             }
         }
-        if constexpr (KIND == BLOCK_WARP) {
-            sum[0] = group_sum<32>(sum[0]);
-        } else {
-            cta_sums<1, MAXW>(sum, s_red[1], nw, true);
+        const float r_y = post ? rsqrtf(sum[0] * inv_D + a.eps) : 1.f;
+        const float tail = r_y * r_y * sum[3];
+        float ss = fmaf(2.f * r_y, sum[2], sum[1] + tail);
+        // h of unit j
+        auto joined = [&](int j, float2 (&h)[P]) {
+            float2 y[P], r[P], v[P];
+            SL::unpack(vy[j], y);
+            SL::unpack(vr[j], r);
+            added(j, y, v);
+#pragma unroll
+            for (int p = 0; p < P; ++p) h[p] = f2fma(v[p], both(r_y), r[p]);
+        };
+        if (!(ss * 8.f >= sum[1] + tail)) {  // the same in every thread of the row
+            float2 t2 = both(0.f);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (SL::unit(j, t0, NT) < NU) {
+                    float2 h[P];
+                    joined(j, h);
+#pragma unroll
+                    for (int p = 0; p < P; ++p) t2 = f2fma(h[p], h[p], t2);
+                }
+            }
+            float one[1] = {t2.x + t2.y};
+            if constexpr (KIND == BLOCK_WARP) {
+                one[0] = group_sum<32>(one[0]);
+            } else {
+                __syncthreads();  // this row's sums have been read
+                cta_sums<1, MAXW>(one, s_red[row & 1], nw, true);
+            }
+            ss = one[0];
         }
-        const float r_h = rsqrtf(sum[0] * inv_D + a.eps);
-        Raw *out = reinterpret_cast<Raw *>(static_cast<T *>(a.out0) + row * a.ld_out0);
-        Raw *nres = reinterpret_cast<Raw *>(static_cast<T *>(a.out1) + row * a.ld_out1);
+        const float r_h = rsqrtf(ss * inv_D + a.eps);
+        T *out = static_cast<T *>(a.out0) + row * a.ld_out0;
+        T *nres = static_cast<T *>(a.out1) + row * a.ld_out1;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int u = t0 + j * NT;
+            const int u = SL::unit(j, t0, NT);
             if (u < NU) {
-                nres[u] = pack_unit<T, UB>(v[j]);
-                float o[E];
+                float2 h[P];
+                joined(j, h);
+                SL::store(nres, u, NT, NU, h);
+                float2 w[P];
+                SL::get(w1, u, NT, NU, w);
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = v[j][e] * r_h * w1[j][e];
-                out[u] = pack_unit<T, UB>(o);
+                for (int p = 0; p < P; ++p) h[p] = f2mul(f2mul(h[p], both(r_h)), w[p]);
+                SL::store(out, u, NT, NU, h);
             }
         }
         if (a.rstd && t0 == 0) {
@@ -274,37 +471,13 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
 }
 
 // VJP -----------------------------------------------------------------------
-// Hides from the compiler that a register's value is unchanged, so that units
-// kept across a barrier stay packed and are unpacked again behind it (bf16: 8
-// registers a tensor instead of 16; without it the VJP spills 208 bytes).
-__device__ __forceinline__ void keep_packed(uint4 &v) {
-    asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w));
-}
-__device__ __forceinline__ void keep_packed(uint32_t &) {}
-__device__ __forceinline__ void keep_packed(uint16_t &) {}
-
-// E consecutive floats; a unit's floats start on a 16-byte boundary when E >= 4.
-template <int E>
-__device__ __forceinline__ void store_floats(float *p, const float (&f)[E]) {
-    if constexpr (E >= 4) {
-#pragma unroll
-        for (int i = 0; i < E / 4; ++i)
-            reinterpret_cast<float4 *>(p)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) p[e] = f[e];
-    }
-}
-
 template <typename T, int UB, int MAXT, int MINB, int KIND, bool GROW>
 __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_constant__ BlockArgs a) {
-    using Raw = typename RawUnit<UB>::type;
-    constexpr int E = unit_elems<T, UB>(), V = block_units<T, UB>(), MAXW = MAXT / 32;
-    // 16-byte units stay in registers; smaller ones take a register each and are
-    // read from the stage (or L1) again instead.
-    constexpr bool HOLD = UB == 16;
+    using SL = Slot<T, UB>;
+    using Raw = typename SL::Raw;
+    constexpr int E = SL::E, V = SL::COUNT, P = SL::P, MAXW = MAXT / 32;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float s_red[2][KIND == BLOCK_WARP ? 1 : MAXW][4];
+    __shared__ float s_red[2][KIND == BLOCK_WARP ? 1 : MAXW][8];
     const int NT = KIND == BLOCK_WARP ? 32 : (int)blockDim.x;
     const int t0 = KIND == BLOCK_WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
     const int R = KIND == BLOCK_WARP ? (int)(blockDim.x >> 5) : 1;
@@ -319,7 +492,8 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
 
     const void *src[5] = {a.y, a.res, a.g, a.g_res, per_row ? a.gate : nullptr};
     const int64_t ld[5] = {a.ld_y, a.ld_res, a.ld_g, a.ld_g_res, a.ld_gate};
-    BlockRing ring{reinterpret_cast<uint64_t *>(smem), smem + BLOCK_HEADER, a.stages, a.stage_bytes, 3 + more + per_row};
+    BlockRing ring{reinterpret_cast<uint64_t *>(smem), smem + BLOCK_HEADER + block_table_bytes(a.D), a.stages, a.stage_bytes,
+                   3 + more + per_row};
     uint64_t policy = 0;
     if constexpr (KIND == BLOCK_STAGED) {
         policy = l2_evict_first_policy();
@@ -335,64 +509,70 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
             for (int s = 0; s < ring.S && r0 + s < r1; ++s) ring_issue<T>(ring, a, src, ld, r0 + s, s, policy);
     }
 
-    float w1[V][E], m[V][E], acc_pre[V][E], acc_mid[V][E];
-    auto load_unit = [&](const void *base, int u, float (&f)[E]) {
-        unpack_unit<T, UB>(static_cast<const Raw *>(base)[u], f);
+    float *w1 = reinterpret_cast<float *>(smem + BLOCK_HEADER);
+    float2 m[V][P], acc_pre[V][P], acc_mid[V][P];
+    auto load_unit = [&](const void *base, int u, float2 (&f)[P]) {
+        SL::load_pairs(base, u, NT, NU, f);
     };
     auto load_m = [&](const T *gate_row) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int u = t0 + j * NT;
+            const int u = SL::unit(j, t0, NT);
             if (u < NU) {
-                float f[E], q[E];
+                float2 f[P], q[P];
                 if (post) load_unit(a.w_post, u, f);
                 if (gate_row) load_unit(gate_row, u, q);
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    m[j][e] = (post ? a.weight_bias + f[e] : 1.f) * (gate_row ? a.scale * q[e] : a.scale);
+                for (int p = 0; p < P; ++p)
+                    m[j][p] = f2mul(post ? f2add(both(a.weight_bias), f[p]) : both(1.f),
+                                    gate_row ? f2mul(both(a.scale), q[p]) : both(a.scale));
             }
         }
     };
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int u = t0 + j * NT;
-        float f[E];
-        if (u < NU) load_unit(a.w_pre, u, f);
+        const int u = SL::unit(j, t0, NT);
+        if (u < NU) {
+            float2 f[P];
+            load_unit(a.w_pre, u, f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            w1[j][e] = u < NU ? a.weight_bias + f[e] : 0.f;
-            acc_pre[j][e] = acc_mid[j][e] = 0.f;
+            for (int p = 0; p < P; ++p) f[p] = f2add(both(a.weight_bias), f[p]);
+            if (KIND != BLOCK_WARP || threadIdx.x < 32) SL::put(w1, u, NT, NU, f);
         }
+#pragma unroll
+        for (int p = 0; p < P; ++p) acc_pre[j][p] = acc_mid[j][p] = both(0.f);
     }
+    if (KIND == BLOCK_WARP) __syncthreads();  // otherwise a thread reads what it wrote
     if (!a.gate || per_row) load_m(nullptr);
 
-    // Adds the warps' accumulators (BLOCK_WARP) in warp order and writes the row.
-    auto flush = [&](float (&acc)[V][E], float *dst) {
+    // Writes k times the accumulators to the row dst (BLOCK_WARP: the warps' added
+    // in warp order) and clears them.
+    auto flush = [&](float2 (&acc)[V][P], float *dst, float k) {
         if constexpr (KIND == BLOCK_WARP) {
-            float *buf = reinterpret_cast<float *>(smem);  // [R][D]
+            float *buf = reinterpret_cast<float *>(smem + BLOCK_HEADER + block_table_bytes(D));  // [R][D]
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const int u = t0 + j * NT;
-                if (u < NU) store_floats<E>(buf + (size_t)ry * D + u * E, acc[j]);
+                const int u = SL::unit(j, t0, NT);
+                if (u < NU) SL::store_floats(buf + (size_t)ry * ((D + 3) & ~3), u, NT, NU, acc[j], k);
             }
             __syncthreads();
             for (int c = threadIdx.x; c < D; c += blockDim.x) {
                 float t = buf[c];
-                for (int k = 1; k < R; ++k) t += buf[(size_t)k * D + c];
+                for (int w = 1; w < R; ++w) t += buf[(size_t)w * ((D + 3) & ~3) + c];
                 dst[c] = t;
             }
             __syncthreads();  // buf may be written again
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const int u = t0 + j * NT;
-                if (u < NU) store_floats<E>(dst + (size_t)u * E, acc[j]);
+                const int u = SL::unit(j, t0, NT);
+                if (u < NU) SL::store_floats(dst, u, NT, NU, acc[j], k);
             }
         }
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[j][e] = 0.f;
+            for (int p = 0; p < P; ++p) acc[j][p] = both(0.f);
     };
 
     int s = 0;
@@ -432,57 +612,68 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
             auto fetch = [&](const T *p, Raw *v) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const int u = t0 + j * NT;
-                    if (u < NU) v[j] = reinterpret_cast<const Raw *>(p)[u];
+                    const int u = SL::unit(j, t0, NT);
+                    if (u < NU) v[j] = SL::load(p, u, NT, NU);
                 }
             };
-            if constexpr (HOLD) {
-                fetch(py, vy);
-                fetch(phh, vh);
-                fetch(pgo, vg);
-                if (more) fetch(pgr, vr);
-                if constexpr (GROW) fetch(pga, va);
-            }
-            auto repack = [&]() {
-                if constexpr (HOLD && sizeof(T) == 2) {
+            fetch(py, vy);
+            fetch(phh, vh);
+            fetch(pgo, vg);
+            if (more) fetch(pgr, vr);
+            if constexpr (GROW) fetch(pga, va);
+            // m of unit j with the row's own gate
+            auto mult = [&](int j, float2 (&mm)[P]) {
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        keep_packed(vy[j]);
-                        keep_packed(vh[j]);
-                        keep_packed(vg[j]);
-                    }
+                for (int p = 0; p < P; ++p) mm[p] = m[j][p];
+                if constexpr (GROW) {
+                    float2 q[P];
+                    SL::unpack(va[j], q);
+#pragma unroll
+                    for (int p = 0; p < P; ++p) mm[p] = f2mul(mm[p], q[p]);
                 }
             };
-            // unit j of a row, from the registers or from where it was staged
-            auto get = [&](const T *p, const Raw *v, int j, float (&f)[E]) {
-                if constexpr (HOLD) unpack_unit<T, UB>(v[j], f);
-                else unpack_unit<T, UB>(reinterpret_cast<const Raw *>(p)[t0 + j * NT], f);
-            };
-            float sum[3] = {0.f, 0.f, 0.f};  // g w1 h, h^2, y^2
+            // a h, u a, u h, u g_res (a = g w1, u = m y), h^2, y^2
+            float2 s2[6] = {both(0.f), both(0.f), both(0.f), both(0.f), both(0.f), both(0.f)};
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                if (t0 + j * NT < NU) {
-                    float fh[E], fg[E];
-                    get(phh, vh, j, fh);
-                    get(pgo, vg, j, fg);
+                if (SL::unit(j, t0, NT) < NU) {
+                    float2 y[P], h[P], x[P], u[P], w[P];
+                    SL::unpack(vy[j], y);
+                    SL::unpack(vh[j], h);
+                    SL::unpack(vg[j], x);
+                    mult(j, u);
+                    SL::get(w1, SL::unit(j, t0, NT), NT, NU, w);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) sum[0] = fmaf(fg[e] * w1[j][e], fh[e], sum[0]);
+                    for (int p = 0; p < P; ++p) {
+                        x[p] = f2mul(x[p], w[p]);
+                        u[p] = f2mul(u[p], y[p]);
+                        s2[0] = f2fma(x[p], h[p], s2[0]);
+                        s2[1] = f2fma(u[p], x[p], s2[1]);
+                        s2[2] = f2fma(u[p], h[p], s2[2]);
+                    }
+                    if (more) {
+                        SL::unpack(vr[j], x);
+#pragma unroll
+                        for (int p = 0; p < P; ++p) s2[3] = f2fma(u[p], x[p], s2[3]);
+                    }
                     if (!saved) {
-                        float fy[E];
-                        get(py, vy, j, fy);
 #pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            sum[1] = fmaf(fh[e], fh[e], sum[1]);
-                            sum[2] = fmaf(fy[e], fy[e], sum[2]);
+                        for (int p = 0; p < P; ++p) {
+                            s2[4] = f2fma(h[p], h[p], s2[4]);
+                            s2[5] = f2fma(y[p], y[p], s2[5]);
                         }
                     }
                 }
             }
-            if constexpr (KIND == BLOCK_WARP) {
+            float sum[6];
 #pragma unroll
-                for (int i = 0; i < 3; ++i) sum[i] = group_sum<32>(sum[i]);
+            for (int i = 0; i < 6; ++i) sum[i] = s2[i].x + s2[i].y;
+            if constexpr (KIND == BLOCK_WARP) {
+                if (saved) warp_sums<4>(reinterpret_cast<float (&)[4]>(sum));
+                else warp_sums<6>(sum);
             } else {
-                ok = cta_sums<3, MAXW>(sum, s_red[0], nw, ok);
+                ok = saved ? cta_sums<4, MAXW>(reinterpret_cast<float (&)[4]>(sum), s_red[row & 1], nw, ok)
+                           : cta_sums<6, MAXW>(sum, s_red[row & 1], nw, ok);
             }
             if constexpr (KIND == BLOCK_STAGED) {
                 if (!ok) {
@@ -497,101 +688,70 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                     }
                     return;
                 }
-                if (HOLD && threadIdx.x == 0 && row + ring.S < r1)
-                    ring_issue<T>(ring, a, src, ld, row + ring.S, s, policy);
+                // every thread has its slots of this stage in registers
+                if (threadIdx.x == 0 && row + ring.S < r1) ring_issue<T>(ring, a, src, ld, row + ring.S, s, policy);
             }
-            repack();
-            if (!saved) {
-                r_h = rsqrtf(sum[1] * inv_D + a.eps);
-                if (post) r_y = rsqrtf(sum[2] * inv_D + a.eps);
-            }
-            const float cc = (r_h * r_h) * (sum[0] * inv_D);
-            // g_h of unit j
-            auto grad_h = [&](int j, const float (&fh)[E], const float (&fg)[E], float (&o)[E]) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = r_h * (fg[e] * w1[j][e] - fh[e] * cc);
-                if (more) {
-                    float fr[E];
-                    get(pgr, vr, j, fr);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) o[e] += fr[e];
-                }
-            };
-            auto mult = [&](int j, float (&mm)[E]) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) mm[e] = m[j][e];
-                if constexpr (GROW) {
-                    float q[E];
-                    get(pga, va, j, q);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) mm[e] *= q[e];
-                }
-            };
-            sum[0] = 0.f;
-            if (post) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    if (t0 + j * NT < NU) {
-                        float fh[E], fg[E], fy[E], o[E], mm[E];
-                        get(phh, vh, j, fh);
-                        get(pgo, vg, j, fg);
-                        get(py, vy, j, fy);
-                        grad_h(j, fh, fg, o);
-                        mult(j, mm);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) sum[0] = fmaf(mm[e] * o[e], fy[e], sum[0]);
-                    }
-                }
-                float one[1] = {sum[0]};
-                if constexpr (KIND == BLOCK_WARP) one[0] = group_sum<32>(one[0]);
-                else cta_sums<1, MAXW>(one, s_red[1], nw, true);
-                sum[0] = one[0];
-            }
-            repack();
-            const float ee = (r_y * r_y) * (sum[0] * inv_D);
-            Raw *gy = reinterpret_cast<Raw *>(static_cast<T *>(a.out0) + row * a.ld_out0);
-            Raw *gh = reinterpret_cast<Raw *>(static_cast<T *>(a.out1) + row * a.ld_out1);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const int u = t0 + j * NT;
+                keep_packed(vy[j]);
+                keep_packed(vh[j]);
+                keep_packed(vg[j]);
+                keep_packed(vr[j]);
+            }
+            if (!saved) {
+                r_h = rsqrtf(sum[4] * inv_D + a.eps);
+                if (post) r_y = rsqrtf(sum[5] * inv_D + a.eps);
+            }
+            const float cc = (r_h * r_h) * (sum[0] * inv_D);
+            const float dot = fmaf(r_h, sum[1] - cc * sum[2], sum[3]);  // sum of m g_h y
+            const float ee = post ? (r_y * r_y) * (dot * inv_D) : 0.f;
+            T *gy = static_cast<T *>(a.out0) + row * a.ld_out0;
+            T *gh = static_cast<T *>(a.out1) + row * a.ld_out1;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int u = SL::unit(j, t0, NT);
                 if (u < NU) {
-                    float fh[E], fg[E], fy[E], o[E], mm[E], q[E];
-                    get(phh, vh, j, fh);
-                    get(pgo, vg, j, fg);
-                    get(py, vy, j, fy);
-                    grad_h(j, fh, fg, o);
+                    float2 h[P], x[P], o[P], w[P];
+                    SL::get(w1, u, NT, NU, w);
+                    SL::unpack(vh[j], h);
+                    SL::unpack(vg[j], x);
+#pragma unroll
+                    for (int p = 0; p < P; ++p) {
+                        acc_pre[j][p] = f2fma(x[p], f2mul(h[p], both(r_h)), acc_pre[j][p]);
+                        o[p] = f2mul(f2fma(h[p], both(-cc), f2mul(x[p], w[p])), both(r_h));
+                    }
+                    if (more) {
+                        SL::unpack(vr[j], x);
+#pragma unroll
+                        for (int p = 0; p < P; ++p) o[p] = f2add(o[p], x[p]);
+                    }
+                    SL::store(gh, u, NT, NU, o);  // g_h
+                    float2 y[P], mm[P];
+                    SL::unpack(vy[j], y);
                     mult(j, mm);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        acc_pre[j][e] = fmaf(fg[e], fh[e] * r_h, acc_pre[j][e]);
-                        q[e] = o[e] * (fy[e] * r_y);  // g_h y r_y
-                    }
+                    for (int p = 0; p < P; ++p) h[p] = f2mul(o[p], f2mul(y[p], both(r_y)));  // g_h y r_y
                     if constexpr (GROW) {  // this row is its gate row: finished here, and gw_post's term weighted
-                        float ga[E], w2[E];
-                        get(pga, va, j, ga);
+                        float2 w2[P];
+                        SL::unpack(va[j], x);
                         if (post) load_unit(a.w_post, u, w2);
 #pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            acc_mid[j][e] = fmaf(q[e], a.scale * ga[e], acc_mid[j][e]);
-                            w2[e] = q[e] * a.scale * (post ? a.weight_bias + w2[e] : 1.f);
+                        for (int p = 0; p < P; ++p) {
+                            acc_mid[j][p] = f2fma(h[p], x[p], acc_mid[j][p]);
+                            w2[p] = f2mul(h[p], post ? f2add(both(a.weight_bias), w2[p]) : both(1.f));
                         }
-                        store_floats<E>(a.g_gate + row * D + (size_t)u * E, w2);
+                        SL::store_floats(a.g_gate + row * D, u, NT, NU, w2, a.scale);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < E; ++e) acc_mid[j][e] = fmaf(q[e], a.scale, acc_mid[j][e]);
+                        for (int p = 0; p < P; ++p) acc_mid[j][p] = f2add(h[p], acc_mid[j][p]);
                     }
-                    gh[u] = pack_unit<T, UB>(o);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) o[e] = r_y * (mm[e] * o[e] - fy[e] * ee);
-                    gy[u] = pack_unit<T, UB>(o);
+                    for (int p = 0; p < P; ++p)
+                        o[p] = f2mul(f2fma(y[p], both(-ee), f2mul(mm[p], o[p])), both(r_y));
+                    SL::store(gy, u, NT, NU, o);
                 }
             }
             if constexpr (KIND == BLOCK_STAGED) {
-                if constexpr (!HOLD) {  // the stage is read until here
-                    __syncthreads();
-                    if (threadIdx.x == 0 && row + ring.S < r1)
-                        ring_issue<T>(ring, a, src, ld, row + ring.S, s, policy);
-                }
                 if (++s == ring.S) {
                     s = 0;
                     ph ^= 1u;
@@ -600,13 +760,15 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
         }
         if (a.gate || post) {
             const bool whole = a.g_gate && !per_row && gr * a.rows_per_gate >= r0 && g_end <= r1;
-            flush(acc_mid, per_row ? a.part_mid + 2 * cta * D
-                           : whole ? a.g_gate + gr * D
-                                   : a.part_mid + mid_slot(cta, gr, grid, a.rows, a.rows_per_gate) * D);
+            flush(acc_mid,
+                  per_row ? a.part_mid + 2 * cta * D
+                  : whole ? a.g_gate + gr * D
+                          : a.part_mid + mid_slot(cta, gr, grid, a.rows, a.rows_per_gate) * D,
+                  a.scale);
         }
         seg = end;
     }
-    flush(acc_pre, a.part_pre + cta * D);
+    flush(acc_pre, a.part_pre + cta * D, 1.f);
     griddep_launch_dependents();
 }
 

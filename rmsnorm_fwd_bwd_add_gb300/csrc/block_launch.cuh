@@ -27,8 +27,15 @@ cudaError_t launch_block_kind(const BlockPlan &p, const BlockArgs &a, cudaStream
         if (p.threads <= 512) return launch_block_inst<VJP, T, UB, 512, 1, BLOCK_DIRECT, GROW>(p, a, s);
         return launch_block_inst<VJP, T, UB, 1024, 1, BLOCK_DIRECT, GROW>(p, a, s);
     }
+    // Threads an SM holds (block_resident): 512 with 128 registers each; the
+    // forward also fits 96, so its CTAs of 257-320 threads sit two an SM and
+    // those of 513-640 one.
     if (p.threads <= 256) return launch_block_inst<VJP, T, UB, 256, 2, BLOCK_STAGED, GROW>(p, a, s);
+    if constexpr (!VJP)
+        if (p.threads <= 320) return launch_block_inst<VJP, T, UB, 320, 2, BLOCK_STAGED, GROW>(p, a, s);
     if (p.threads <= 512) return launch_block_inst<VJP, T, UB, 512, 1, BLOCK_STAGED, GROW>(p, a, s);
+    if constexpr (!VJP)
+        if (p.threads <= 640) return launch_block_inst<VJP, T, UB, 640, 1, BLOCK_STAGED, GROW>(p, a, s);
     return launch_block_inst<VJP, T, UB, 1024, 1, BLOCK_STAGED, GROW>(p, a, s);
 }
 

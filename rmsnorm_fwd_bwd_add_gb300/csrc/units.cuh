@@ -17,10 +17,6 @@ template <typename T, int UB>
 __device__ __forceinline__ void unpack_unit(const typename RawUnit<UB>::type &v, float (&f)[unit_elems<T, UB>()]) {
     if constexpr (UB == 16) {
         unpack_vec<T>(v, f);
-    } else if constexpr (UB == 4 && sizeof(T) == 2) {
-        const float2 p = Cvt<T>::unpack2(v);
-        f[0] = p.x;
-        f[1] = p.y;
     } else {
         T x;
         memcpy(&x, &v, sizeof(T));
@@ -32,8 +28,6 @@ template <typename T, int UB>
 __device__ __forceinline__ typename RawUnit<UB>::type pack_unit(const float (&f)[unit_elems<T, UB>()]) {
     if constexpr (UB == 16) {
         return pack_vec<T>(f);
-    } else if constexpr (UB == 4 && sizeof(T) == 2) {
-        return Cvt<T>::pack2(f[0], f[1]);
     } else {
         T x;
         Cvt<T>::store1(&x, f[0]);
