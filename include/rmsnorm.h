@@ -283,6 +283,23 @@ int rmsnorm_block_vjp(const void *y, int64_t ld_y, const void *h, int64_t ld_h, 
                       void *stream);
 
 /*
+ * rmsnorm_block_vjp with caller-owned scratch, as rmsnorm_vjp_ws: `workspace` is a
+ * device buffer of at least rmsnorm_block_vjp_workspace_size(rows, D, dtype)
+ * bytes (for the current device), 256-byte aligned, apart from every operand
+ * and used by no other work while the call runs.  Its contents do not matter.
+ */
+int rmsnorm_block_vjp_ws(const void *y, int64_t ld_y, const void *h, int64_t ld_h,
+                         const void *w_post, const void *w_pre, const void *gate, int64_t ld_gate,
+                         int64_t gate_rows, float scale, const void *g_out, int64_t ld_g_out,
+                         const void *g_residual, int64_t ld_g_residual, const float *rstd, float eps,
+                         float weight_bias, void *g_y, int64_t ld_g_y, void *g_h, int64_t ld_g_h,
+                         float *gw_post, float *gw_pre, float *g_gate, int64_t rows, int64_t D,
+                         int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of that scratch (0 for rows == 0 and for invalid arguments). */
+size_t rmsnorm_block_vjp_workspace_size(int64_t rows, int64_t D, int dtype);
+
+/*
  * Gated activation of the decode loop.  Source: "Fused residual-add RMSNorm
  * and fused RoPE + KV-append decode kernels", Background, third bullet (a
  * fused silu(x[:d]) * x[d:2d] gate with 16-byte vectorised loads).

@@ -23,6 +23,8 @@ EXPORTS = (
     "rmsnorm_vjp_ex",
     "rmsnorm_block_fwd",
     "rmsnorm_block_vjp",
+    "rmsnorm_block_vjp_ws",
+    "rmsnorm_block_vjp_workspace_size",
     "rmsnorm_gated_silu",
     "rmsnorm_rope_kv_append",
     "rmsnorm_rope",
@@ -98,6 +100,10 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
                                       _vp, _i64, _vp, _f, _f, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
                                       _i64, _i64, _i, _vp]
     lib.rmsnorm_block_vjp.restype = _i
+    lib.rmsnorm_block_vjp_ws.argtypes = lib.rmsnorm_block_vjp.argtypes[:-1] + [_vp, ctypes.c_size_t, _vp]
+    lib.rmsnorm_block_vjp_ws.restype = _i
+    lib.rmsnorm_block_vjp_workspace_size.argtypes = [_i64, _i64, _i]
+    lib.rmsnorm_block_vjp_workspace_size.restype = ctypes.c_size_t
     lib.rmsnorm_gated_silu.argtypes = [_vp, _vp, _i64, _i64, _i, _vp]
     lib.rmsnorm_gated_silu.restype = _i
     lib.rmsnorm_rope_kv_append.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _f,
@@ -157,7 +163,7 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-_BOUND = ("rmsnorm_block_fwd", "rmsnorm_block_vjp", "rmsnorm_rope", "rmsnorm_rope_kv_append_ex",
+_BOUND = ("rmsnorm_block_fwd", "rmsnorm_block_vjp_ws", "rmsnorm_block_vjp_workspace_size", "rmsnorm_rope", "rmsnorm_rope_kv_append_ex",
           "rmsnorm_kv_release", "rmsnorm_kv_plan")
 _binding = None
 

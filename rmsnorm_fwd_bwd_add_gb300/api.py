@@ -646,7 +646,7 @@ def rmsnorm_block_vjp(y: torch.Tensor, h: torch.Tensor, w_post: Optional[torch.T
     gradients of out and (optionally) of new_residual, with the forward's rstd
     or without.  Returns (g_y, g_h, gw_post, gw_pre, g_gate): g_h is the
     gradient of residual, the weights' and the gate's gradients are float32
-    (None without a post-norm, without a gate)."""
+    (None without a post-norm, without a gate).  The scratch is torch's."""
     return _run("block_vjp", stream, y, h, w_post, w_pre, g_out, eps, weight_bias, gate, scale,
                 g_residual, rstd, g_y, g_h, gw_post, gw_pre, g_gate)
 

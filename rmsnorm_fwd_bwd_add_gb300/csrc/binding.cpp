@@ -66,7 +66,8 @@ using BlockFwd = int (*)(const void *, int64_t, const void *, int64_t, const voi
 using BlockVjp = int (*)(const void *, int64_t, const void *, int64_t, const void *, const void *, const void *,
                          int64_t, int64_t, float, const void *, int64_t, const void *, int64_t, const float *, float,
                          float, void *, int64_t, void *, int64_t, float *, float *, float *, int64_t, int64_t, int,
-                         void *);
+                         void *, size_t, void *);
+using BlockVjpSize = size_t (*)(int64_t, int64_t, int);
 using Rope = int (*)(const void *, const int64_t *, const void *, const int64_t *, const int64_t *, void *,
                      const int64_t *, void *, const int64_t *, const double *, float, int, int, int64_t, int64_t,
                      int64_t, int64_t, int64_t, int64_t, int, void *);
@@ -80,7 +81,8 @@ using KvPlan = int (*)(const int32_t *, const int32_t *, int32_t *, int64_t, int
                        const int32_t *, int64_t, int32_t *, int32_t *, int64_t *, int64_t *, int64_t *, int32_t *,
                        uint8_t *, int64_t, int64_t, void *);
 BlockFwd c_block_fwd;
-BlockVjp c_block_vjp;
+BlockVjp c_block_vjp_ws;
+BlockVjpSize c_block_vjp_size;
 Rope c_rope;
 RopeAppend c_rope_append;
 KvRelease c_kv_release;
@@ -335,12 +337,15 @@ PyObject *block_vjp(PyObject *, PyObject *const *argv, Py_ssize_t n) {
         if (gate)
             g_gate = given_or_empty("g_gate", a.optional(15, "g_gate"), at::kFloat, gate->sizes(), y.device());
         auto f32 = [](const std::optional<Tensor> &t) { return t ? static_cast<float *>(ptr(&*t)) : nullptr; };
+        const int64_t bytes = (int64_t)c_block_vjp_size(r.rows, r.D, code);
+        const Tensor ws = empty({bytes}, at::kByte, y.device());
         check_status("rmsnorm_block_vjp",
-                     c_block_vjp(ptr(&y), r.ld, ptr(&h), ld_h, ptr(w_post), ptr(&w_pre), ptr(gate), g.ld, g.G,
+                     c_block_vjp_ws(ptr(&y), r.ld, ptr(&h), ld_h, ptr(w_post), ptr(&w_pre), ptr(gate), g.ld, g.G,
                                  (float)a.number(8), ptr(&g_out), ld_g, ptr(g_res), ld_gr,
                                  static_cast<const float *>(ptr(rstd)), (float)a.number(5), (float)a.number(6),
                                  ptr(&g_y.first), g_y.second, ptr(&g_h.first), g_h.second, f32(gw_post),
-                                 static_cast<float *>(ptr(&gw_pre)), f32(g_gate), r.rows, r.D, code, on.stream));
+                                 static_cast<float *>(ptr(&gw_pre)), f32(g_gate), r.rows, r.D, code, ptr(&ws), (size_t)bytes,
+                                 on.stream));
         return tuple_of(wrap(g_y.first), wrap(g_h.first), wrap_or_none(gw_post), wrap(gw_pre), wrap_or_none(g_gate));
     });
 }
@@ -545,7 +550,8 @@ PyObject *kv_plan(PyObject *, PyObject *const *argv, Py_ssize_t n) {
 PyObject *bind(PyObject *, PyObject *const *argv, Py_ssize_t n) {
     return guarded(n, 2, [&]() -> PyObject * {
         const struct { const char *name; void *slot; } table[] = {
-            {"rmsnorm_block_fwd", &c_block_fwd}, {"rmsnorm_block_vjp", &c_block_vjp}, {"rmsnorm_rope", &c_rope},
+            {"rmsnorm_block_fwd", &c_block_fwd}, {"rmsnorm_block_vjp_ws", &c_block_vjp_ws},
+            {"rmsnorm_block_vjp_workspace_size", &c_block_vjp_size}, {"rmsnorm_rope", &c_rope},
             {"rmsnorm_rope_kv_append_ex", &c_rope_append}, {"rmsnorm_kv_release", &c_kv_release},
             {"rmsnorm_kv_plan", &c_kv_plan}};
         for (const auto &e : table) {

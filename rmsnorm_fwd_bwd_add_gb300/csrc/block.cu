@@ -59,12 +59,11 @@ BlockPlan make_plan(int64_t rows, int64_t D, int es, int unit, int tensors, bool
         int warps = 8;  // rows side by side; fewer when the SMs would idle
         while (warps > 1 && rows < (int64_t)warps * sm) warps /= 2;
         p.threads = 32 * warps;
-        p.smem = 128 + table + (vjp ? (size_t)warps * ((D + 3) / 4 * 16) : 0);
+        p.smem = vjp ? (size_t)warps * ((D + 3) / 4 * 16) : 0;
         p.grid = (int)std::min<int64_t>((rows + warps - 1) / warps, (int64_t)sm * (512 / p.threads));
     } else if (rows <= (int64_t)sm * per_sm) {
         p.kind = BLOCK_DIRECT;
         p.grid = (int)rows;
-        p.smem = 128 + table;
     } else {
         p.kind = BLOCK_STAGED;
         p.grid = sm * per_sm;
@@ -75,7 +74,7 @@ BlockPlan make_plan(int64_t rows, int64_t D, int es, int unit, int tensors, bool
         p.smem = 128 + table + (size_t)p.stages * tensors * p.stage_bytes;
     }
     if (vjp && p.kind != BLOCK_DIRECT)  // scratch traffic small beside the rows'
-        p.grid = (int)std::min<int64_t>(p.grid, std::max<int64_t>(sm, rows / 48));
+        p.grid = (int)std::min<int64_t>(p.grid, std::max<int64_t>(sm, rows / 12));
     return p;
 }
 
@@ -181,14 +180,17 @@ extern "C" int rmsnorm_block_fwd(const void *y, int64_t ld_y, const void *residu
     return e == cudaSuccess ? RMSNORM_OK : record_cuda_error(e);
 }
 
-extern "C" int rmsnorm_block_vjp(const void *y, int64_t ld_y, const void *h, int64_t ld_h,
-                                 const void *w_post, const void *w_pre, const void *gate,
-                                 int64_t ld_gate, int64_t gate_rows, float scale, const void *g_out,
-                                 int64_t ld_g_out, const void *g_residual, int64_t ld_g_residual,
-                                 const float *rstd, float eps, float weight_bias, void *g_y,
-                                 int64_t ld_g_y, void *g_h, int64_t ld_g_h, float *gw_post,
-                                 float *gw_pre, float *g_gate, int64_t rows, int64_t D, int dtype,
-                                 void *stream) {
+namespace {
+
+size_t scratch_bytes(int grid, int64_t D) { return ((size_t)grid * (size_t)D * 12 + 255) & ~(size_t)255; }
+
+// The VJP with its scratch in `workspace`, or, with `pooled`, from the library's pool.
+int block_vjp(const void *y, int64_t ld_y, const void *h, int64_t ld_h, const void *w_post,
+              const void *w_pre, const void *gate, int64_t ld_gate, int64_t gate_rows, float scale,
+              const void *g_out, int64_t ld_g_out, const void *g_residual, int64_t ld_g_residual,
+              const float *rstd, float eps, float weight_bias, void *g_y, int64_t ld_g_y, void *g_h,
+              int64_t ld_g_h, float *gw_post, float *gw_pre, float *g_gate, int64_t rows, int64_t D,
+              int dtype, bool pooled, void *workspace, size_t workspace_bytes, void *stream) {
     int st = check_block(w_post, w_pre, gate, ld_gate, gate_rows, scale, eps, weight_bias, rows, D, dtype);
     if (st != RMSNORM_OK) return st;
     if (!gw_pre || (gw_post != nullptr) != (w_post != nullptr) || (g_gate != nullptr) != (gate != nullptr))
@@ -270,14 +272,53 @@ extern "C" int rmsnorm_block_vjp(const void *y, int64_t ld_y, const void *h, int
     const BlockPlan p = make_plan(rows, D, es, unit, 3 + (g_residual != nullptr) + per_row, true, sm);
     a.stages = p.stages;
     a.stage_bytes = p.stage_bytes;
-    const int grid = p.grid;
-    void *ws = nullptr;
-    st = scratch_alloc((size_t)grid * D * 12, s, &ws);
-    if (st != RMSNORM_OK) return st;
+    const size_t need = scratch_bytes(p.grid, D);
+    void *ws = workspace;
+    if (pooled) {
+        st = scratch_alloc(need, s, &ws);
+        if (st != RMSNORM_OK) return st;
+    } else {
+        if (!ws || workspace_bytes < need || ((uintptr_t)ws & 255u)) return RMSNORM_ERR_INVALID_ARG;
+        for (const Mat &x : m)
+            if (x.p && mat_hits(x, rows, D, es, ws, need)) return RMSNORM_ERR_INVALID_ARG;
+        for (const auto &o : outs)
+            if (overlaps(o.p, o.n, ws, need)) return RMSNORM_ERR_INVALID_ARG;
+        if (overlaps(ws, need, w_post, nw) || overlaps(ws, need, w_pre, nw) || overlaps(ws, need, rstd, nr) ||
+            overlaps(ws, need, gate, ngate))
+            return RMSNORM_ERR_INVALID_ARG;
+    }
     a.part_pre = static_cast<float *>(ws);
-    a.part_mid = a.part_pre + (size_t)grid * D;
+    a.part_mid = a.part_pre + (size_t)p.grid * D;
     const cudaError_t e = by_type(dtype, [&](auto t) { return launch_block_vjp<typename decltype(t)::type>(p, a, s); });
     st = e == cudaSuccess ? RMSNORM_OK : record_cuda_error(e);
-    const int freed = scratch_free(ws, s);
+    const int freed = pooled ? scratch_free(ws, s) : RMSNORM_OK;
     return st != RMSNORM_OK ? st : freed;
+}
+
+}  // namespace
+
+#define BLOCK_VJP_PARAMS                                                                                    \
+    const void *y, int64_t ld_y, const void *h, int64_t ld_h, const void *w_post, const void *w_pre,        \
+        const void *gate, int64_t ld_gate, int64_t gate_rows, float scale, const void *g_out,               \
+        int64_t ld_g_out, const void *g_residual, int64_t ld_g_residual, const float *rstd, float eps,      \
+        float weight_bias, void *g_y, int64_t ld_g_y, void *g_h, int64_t ld_g_h, float *gw_post,            \
+        float *gw_pre, float *g_gate, int64_t rows, int64_t D, int dtype
+#define BLOCK_VJP_ARGS                                                                                      \
+    y, ld_y, h, ld_h, w_post, w_pre, gate, ld_gate, gate_rows, scale, g_out, ld_g_out, g_residual,          \
+        ld_g_residual, rstd, eps, weight_bias, g_y, ld_g_y, g_h, ld_g_h, gw_post, gw_pre, g_gate, rows, D,  \
+        dtype
+
+extern "C" int rmsnorm_block_vjp(BLOCK_VJP_PARAMS, void *stream) {
+    return block_vjp(BLOCK_VJP_ARGS, true, nullptr, 0, stream);
+}
+
+extern "C" int rmsnorm_block_vjp_ws(BLOCK_VJP_PARAMS, void *workspace, size_t workspace_bytes, void *stream) {
+    return block_vjp(BLOCK_VJP_ARGS, false, workspace, workspace_bytes, stream);
+}
+
+extern "C" size_t rmsnorm_block_vjp_workspace_size(int64_t rows, int64_t D, int dtype) {
+    int sm = 0;
+    if (check_common(rows, D, dtype, 0.f, 0.f) != RMSNORM_OK || rows == 0 || current_sm_count(&sm) != RMSNORM_OK)
+        return 0;
+    return scratch_bytes(make_plan(rows, D, esize_of(dtype), 16, 3, true, sm).grid, D);
 }

@@ -21,7 +21,7 @@
 //   BLOCK_WARP    one row a warp (short rows): no barriers; several rows a CTA.
 //
 // w1 = weight_bias + w_pre sits in shared memory in fp32 (in registers the VJP
-// spilled), m = scale * gate * (weight_bias + w_post) of a thread's columns in
+// spilled), or packed in registers where a thread sees few rows; m = scale * gate * (weight_bias + w_post) of a thread's columns in
 // its registers (m is rebuilt when the CTA's rows pass to
 // another gate row; with a gate row per row, the gate streams with the row and
 // m holds the rest), the VJP's two accumulators of its columns.
@@ -136,8 +136,7 @@ template <typename T, int UB> struct Slot {
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 constexpr int BLOCK_MAX_STAGES = 8;
-// Shared memory: the ring's mbarriers, the table w1, then the ring (or the VJP's
-// sums over warps, BLOCK_WARP).
+// Shared memory of BLOCK_STAGED: the ring's mbarriers, the table w1, the ring.
 constexpr int BLOCK_HEADER = 128;
 __host__ __device__ constexpr uint32_t block_table_bytes(int D) { return ((uint32_t)D * 4u + 127u) & ~127u; }
 
@@ -284,9 +283,30 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
             for (int s = 0; s < ring.S && r0 + s < r1; ++s) ring_issue<T>(ring, a, src, ld, r0 + s, s, policy);
     }
 
-    // w1 in shared memory, m without the gate in registers
-    float *w1 = reinterpret_cast<float *>(smem + BLOCK_HEADER);
-    float2 m[V][P];
+    // A row's slots; the first row's loads go ahead of the weights' where no ring does.
+    const int64_t row0 = r0 + (KIND == BLOCK_WARP ? (int)(threadIdx.x >> 5) : 0);
+    Raw vy[V], vr[V], vg[GROW ? V : 1];
+    auto fetch = [&](const T *py, const T *pr, const T *pg) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int u = SL::unit(j, t0, NT);
+            if (u < NU) {
+                vy[j] = SL::load(py, u, NT, NU);
+                vr[j] = SL::load(pr, u, NT, NU);
+                if constexpr (GROW) vg[j] = SL::load(pg, u, NT, NU);
+            }
+        }
+    };
+    auto fetch_global = [&](int64_t row) {
+        fetch(static_cast<const T *>(a.y) + row * a.ld_y, static_cast<const T *>(a.res) + row * a.ld_res,
+              per_row ? static_cast<const T *>(a.gate) + row * a.ld_gate : nullptr);
+    };
+    if constexpr (KIND != BLOCK_STAGED)
+        if (row0 < r1) fetch_global(row0);
+
+    float *table = reinterpret_cast<float *>(smem + BLOCK_HEADER);
+    Raw vw[KIND == BLOCK_STAGED ? 1 : V];
+    float2 m[V][P];  // without the gate if it has a row for each row
     auto load_unit = [&](const void *base, int u, float2 (&f)[P]) {
         SL::load_pairs(base, u, NT, NU, f);
     };
@@ -309,45 +329,52 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
     for (int j = 0; j < V; ++j) {
         const int u = SL::unit(j, t0, NT);
         if (u < NU) {
-            float2 f[P];
-            load_unit(a.w_pre, u, f);
+            const Raw w = SL::load(a.w_pre, u, NT, NU);
+            if constexpr (KIND == BLOCK_STAGED) {  // a thread reads only what it wrote itself
+                float2 f[P];
+                SL::unpack(w, f);
 #pragma unroll
-            for (int p = 0; p < P; ++p) f[p] = f2add(both(a.weight_bias), f[p]);
-            if (KIND != BLOCK_WARP || threadIdx.x < 32) SL::put(w1, u, NT, NU, f);
+                for (int p = 0; p < P; ++p) f[p] = f2add(both(a.weight_bias), f[p]);
+                SL::put(table, u, NT, NU, f);
+            } else {
+                vw[j] = w;
+            }
         }
     }
-    if (KIND == BLOCK_WARP) __syncthreads();  // otherwise a thread reads what it wrote
     if (!a.gate || per_row) load_m(nullptr);
+    // w1 of slot j, first unit u
+    auto w1_of = [&](int j, int u, float2 (&w)[P]) {
+        if constexpr (KIND == BLOCK_STAGED) {
+            SL::get(table, u, NT, NU, w);
+        } else {
+            SL::unpack(vw[j], w);
+#pragma unroll
+            for (int p = 0; p < P; ++p) w[p] = f2add(both(a.weight_bias), w[p]);
+        }
+    };
 
     int64_t group_end = a.gate && !per_row ? r0 : INT64_MAX;  // first row past the gate row held in m
     int s = 0;
     uint32_t ph = 0;
-    for (int64_t row = r0 + (KIND == BLOCK_WARP ? (int)(threadIdx.x >> 5) : 0); row < r1; row += R) {
+    for (int64_t row = row0; row < r1; row += R) {
         if (row >= group_end) {
             const int64_t gr = row / a.rows_per_gate;
             group_end = (gr + 1) * a.rows_per_gate;
             load_m(static_cast<const T *>(a.gate) + gr * a.ld_gate);
         }
-        const T *py = static_cast<const T *>(a.y) + row * a.ld_y;
-        const T *pr = static_cast<const T *>(a.res) + row * a.ld_res;
-        const T *pg = per_row ? static_cast<const T *>(a.gate) + row * a.ld_gate : nullptr;
         bool ok = true;
-        if constexpr (KIND == BLOCK_STAGED) {  // the same rows in the stage
+        if constexpr (KIND == BLOCK_STAGED) {
             const unsigned char *st = ring.data + (size_t)s * ring.tensors * ring.stage_bytes;
-            py = reinterpret_cast<const T *>(st + ((uintptr_t)py & 15u));
-            pr = reinterpret_cast<const T *>(st + ring.stage_bytes + ((uintptr_t)pr & 15u));
-            if (per_row) pg = reinterpret_cast<const T *>(st + 2 * ring.stage_bytes + ((uintptr_t)pg & 15u));
+            auto staged = [&](const void *base, int64_t ld) {
+                const uintptr_t p = (uintptr_t)(static_cast<const T *>(base) + row * ld);
+                const T *q = reinterpret_cast<const T *>(st + (p & 15u));
+                st += ring.stage_bytes;
+                return q;
+            };
+            const T *py = staged(a.y, a.ld_y), *pr = staged(a.res, a.ld_res);
+            const T *pg = per_row ? staged(a.gate, a.ld_gate) : nullptr;
             ok = mbar_wait_bounded(&ring.full[s], ph, a.wait_budget);
-        }
-        Raw vy[V], vr[V], vg[GROW ? V : 1];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int u = SL::unit(j, t0, NT);
-            if (u < NU) {
-                vy[j] = SL::load(py, u, NT, NU);
-                vr[j] = SL::load(pr, u, NT, NU);
-                if constexpr (GROW) vg[j] = SL::load(pg, u, NT, NU);
-            }
+            fetch(py, pr, pg);
         }
         // v = m y of unit j, the added term before r_y
         auto added = [&](int j, const float2 (&y)[P], float2 (&v)[P]) {
@@ -450,7 +477,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
                 joined(j, h);
                 SL::store(nres, u, NT, NU, h);
                 float2 w[P];
-                SL::get(w1, u, NT, NU, w);
+                w1_of(j, u, w);
 #pragma unroll
                 for (int p = 0; p < P; ++p) h[p] = f2mul(f2mul(h[p], both(r_h)), w[p]);
                 SL::store(out, u, NT, NU, h);
@@ -465,13 +492,16 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
                 s = 0;
                 ph ^= 1u;
             }
+        } else if constexpr (KIND == BLOCK_WARP) {
+            if (row + R < r1) fetch_global(row + R);
         }
     }
     griddep_launch_dependents();
 }
 
 // VJP -----------------------------------------------------------------------
-template <typename T, int UB, int MAXT, int MINB, int KIND, bool GROW>
+// FULL: a norm after the block, g_res and saved scales are all there.
+template <typename T, int UB, int MAXT, int MINB, int KIND, bool GROW, bool FULL>
 __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_constant__ BlockArgs a) {
     using SL = Slot<T, UB>;
     using Raw = typename SL::Raw;
@@ -485,8 +515,8 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
     const int D = a.D, NU = D / E, nw = (int)(blockDim.x >> 5);
     const float inv_D = 1.0f / (float)D;
     constexpr bool per_row = GROW;  // a gate row for each row
-    const bool post = a.w_post != nullptr, more = a.g_res != nullptr;
-    const bool saved = a.rstd != nullptr;
+    const bool post = FULL || a.w_post != nullptr, more = FULL || a.g_res != nullptr;
+    const bool saved = FULL || a.rstd != nullptr;
     const int64_t cta = blockIdx.x, grid = gridDim.x;
     const int64_t r0 = first_row(cta, grid, a.rows), r1 = first_row(cta + 1, grid, a.rows);
 
@@ -509,7 +539,39 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
             for (int s = 0; s < ring.S && r0 + s < r1; ++s) ring_issue<T>(ring, a, src, ld, r0 + s, s, policy);
     }
 
-    float *w1 = reinterpret_cast<float *>(smem + BLOCK_HEADER);
+    // A row's slots; the first row's loads go ahead of the weights' where no ring does.
+    Raw vy[V], vh[V], vg[V], vr[V], va[GROW ? V : 1];
+    auto fetch = [&](const T *py, const T *ph, const T *pg, const T *pr, const T *pa) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int u = SL::unit(j, t0, NT);
+            if (u < NU) {
+                vy[j] = SL::load(py, u, NT, NU);
+                vh[j] = SL::load(ph, u, NT, NU);
+                vg[j] = SL::load(pg, u, NT, NU);
+                if (more) vr[j] = SL::load(pr, u, NT, NU);
+                if constexpr (GROW) va[j] = SL::load(pa, u, NT, NU);
+            }
+        }
+    };
+    auto fetch_global = [&](int64_t row) {
+        fetch(static_cast<const T *>(a.y) + row * a.ld_y, static_cast<const T *>(a.res) + row * a.ld_res,
+              static_cast<const T *>(a.g) + row * a.ld_g,
+              more ? static_cast<const T *>(a.g_res) + row * a.ld_g_res : nullptr,
+              per_row ? static_cast<const T *>(a.gate) + row * a.ld_gate : nullptr);
+    };
+    // The row this thread takes after `row` (rows of one gate row are dealt out to
+    // the warps from its first on), or r1.
+    auto next_row = [&](int64_t row, int64_t seg_end) -> int64_t {
+        if (row + R < seg_end) return row + R;
+        return min(r1, seg_end + ry);  // (not taken if the next gate row is shorter)
+    };
+    if constexpr (KIND != BLOCK_STAGED)
+        if (r0 + ry < r1) fetch_global(r0 + ry);
+    int64_t fetched = r0 + ry;  // the row in the slots
+
+    float *table = reinterpret_cast<float *>(smem + BLOCK_HEADER);
+    Raw vw[KIND == BLOCK_STAGED ? 1 : V];
     float2 m[V][P], acc_pre[V][P], acc_mid[V][P];
     auto load_unit = [&](const void *base, int u, float2 (&f)[P]) {
         SL::load_pairs(base, u, NT, NU, f);
@@ -533,23 +595,37 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
     for (int j = 0; j < V; ++j) {
         const int u = SL::unit(j, t0, NT);
         if (u < NU) {
-            float2 f[P];
-            load_unit(a.w_pre, u, f);
+            const Raw w = SL::load(a.w_pre, u, NT, NU);
+            if constexpr (KIND == BLOCK_STAGED) {  // a thread reads only what it wrote itself
+                float2 f[P];
+                SL::unpack(w, f);
 #pragma unroll
-            for (int p = 0; p < P; ++p) f[p] = f2add(both(a.weight_bias), f[p]);
-            if (KIND != BLOCK_WARP || threadIdx.x < 32) SL::put(w1, u, NT, NU, f);
+                for (int p = 0; p < P; ++p) f[p] = f2add(both(a.weight_bias), f[p]);
+                SL::put(table, u, NT, NU, f);
+            } else {
+                vw[j] = w;
+            }
         }
 #pragma unroll
         for (int p = 0; p < P; ++p) acc_pre[j][p] = acc_mid[j][p] = both(0.f);
     }
-    if (KIND == BLOCK_WARP) __syncthreads();  // otherwise a thread reads what it wrote
     if (!a.gate || per_row) load_m(nullptr);
+    // w1 of slot j, first unit u
+    auto w1_of = [&](int j, int u, float2 (&w)[P]) {
+        if constexpr (KIND == BLOCK_STAGED) {
+            SL::get(table, u, NT, NU, w);
+        } else {
+            SL::unpack(vw[j], w);
+#pragma unroll
+            for (int p = 0; p < P; ++p) w[p] = f2add(both(a.weight_bias), w[p]);
+        }
+    };
 
     // Writes k times the accumulators to the row dst (BLOCK_WARP: the warps' added
     // in warp order) and clears them.
     auto flush = [&](float2 (&acc)[V][P], float *dst, float k) {
         if constexpr (KIND == BLOCK_WARP) {
-            float *buf = reinterpret_cast<float *>(smem + BLOCK_HEADER + block_table_bytes(D));  // [R][D]
+            float *buf = reinterpret_cast<float *>(smem);  // [R][D]
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int u = SL::unit(j, t0, NT);
@@ -588,39 +664,23 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                 if (post) r_y = __ldg(a.rstd + row);
                 r_h = __ldg(a.rstd + a.rows + row);
             }
-            const T *py = static_cast<const T *>(a.y) + row * a.ld_y;
-            const T *phh = static_cast<const T *>(a.res) + row * a.ld_res;
-            const T *pgo = static_cast<const T *>(a.g) + row * a.ld_g;
-            const T *pgr = more ? static_cast<const T *>(a.g_res) + row * a.ld_g_res : nullptr;
-            const T *pga = per_row ? static_cast<const T *>(a.gate) + row * a.ld_gate : nullptr;
             bool ok = true;
             if constexpr (KIND == BLOCK_STAGED) {
                 const unsigned char *st = ring.data + (size_t)s * ring.tensors * ring.stage_bytes;
-                auto staged = [&](const T *p) {
-                    const T *q = reinterpret_cast<const T *>(st + ((uintptr_t)p & 15u));
+                auto staged = [&](const void *base, int64_t ld) {
+                    const uintptr_t p = (uintptr_t)(static_cast<const T *>(base) + row * ld);
+                    const T *q = reinterpret_cast<const T *>(st + (p & 15u));
                     st += ring.stage_bytes;
                     return q;
                 };
-                py = staged(py);
-                phh = staged(phh);
-                pgo = staged(pgo);
-                if (more) pgr = staged(pgr);
-                if (per_row) pga = staged(pga);
+                const T *py = staged(a.y, a.ld_y), *phh = staged(a.res, a.ld_res), *pgo = staged(a.g, a.ld_g);
+                const T *pgr = more ? staged(a.g_res, a.ld_g_res) : nullptr;
+                const T *pga = per_row ? staged(a.gate, a.ld_gate) : nullptr;
                 ok = mbar_wait_bounded(&ring.full[s], ph, a.wait_budget);
+                fetch(py, phh, pgo, pgr, pga);
+            } else if (row != fetched) {
+                fetch_global(row);
             }
-            Raw vy[V], vh[V], vg[V], vr[V], va[GROW ? V : 1];
-            auto fetch = [&](const T *p, Raw *v) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const int u = SL::unit(j, t0, NT);
-                    if (u < NU) v[j] = SL::load(p, u, NT, NU);
-                }
-            };
-            fetch(py, vy);
-            fetch(phh, vh);
-            fetch(pgo, vg);
-            if (more) fetch(pgr, vr);
-            if constexpr (GROW) fetch(pga, va);
             // m of unit j with the row's own gate
             auto mult = [&](int j, float2 (&mm)[P]) {
 #pragma unroll
@@ -642,7 +702,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                     SL::unpack(vh[j], h);
                     SL::unpack(vg[j], x);
                     mult(j, u);
-                    SL::get(w1, SL::unit(j, t0, NT), NT, NU, w);
+                    w1_of(j, SL::unit(j, t0, NT), w);
 #pragma unroll
                     for (int p = 0; p < P; ++p) {
                         x[p] = f2mul(x[p], w[p]);
@@ -712,7 +772,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                 const int u = SL::unit(j, t0, NT);
                 if (u < NU) {
                     float2 h[P], x[P], o[P], w[P];
-                    SL::get(w1, u, NT, NU, w);
+                    w1_of(j, u, w);
                     SL::unpack(vh[j], h);
                     SL::unpack(vg[j], x);
 #pragma unroll
@@ -756,6 +816,9 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                     s = 0;
                     ph ^= 1u;
                 }
+            } else if constexpr (KIND == BLOCK_WARP) {
+                fetched = next_row(row, end);
+                if (fetched < r1) fetch_global(fetched);
             }
         }
         if (a.gate || post) {

@@ -163,69 +163,94 @@ __global__ void __launch_bounds__(BLOCK_GENERIC_NT) block_vjp_generic_kernel(con
 //   BR_WARPS, ...  A part is a row of part_mid, or the whole sum that one CTA
 //   left in g_gate, which becomes w2 * A in place.  Gate rows of one row each
 //   come finished from the first stage, which also weighted its sums.
-// The order of every sum depends on (rows, G, grid) alone.
+// The order of every sum depends on (rows, G, grid) alone.  Latency-bound: a
+// warp's first loads of both sums are in flight together, and the row
+// arithmetic is 32-bit (I) where the row count allows (64-bit divisions made
+// the whole stage 14 us at 16384 x 4096 in 8 gate rows).
 constexpr int BR_WARPS = 32;
-constexpr int BR_BATCH = 8;
+constexpr int BR_BATCH = 16;
 
-template <typename T>
+template <typename I>
+__device__ __forceinline__ I row_of_cta(I c, I q, I r) { return c * q + (c < r ? c : r); }
+
+template <typename T, typename I>
 __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const BlockArgs a, int grid) {
     __shared__ float sums[2][BR_WARPS][33];
-    griddep_wait();
-    griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int D = a.D;
     const int64_t col = (int64_t)blockIdx.x * 32 + lane;
     const bool in = col < D;
     const T *w2 = static_cast<const T *>(a.w_post);
     const T *gate = static_cast<const T *>(a.gate);
-    // rows first, first + step, ... (n of them) of a [*, D] array, in that order
-    auto add_rows = [&](const float *base, int64_t first, int64_t step, int64_t n) -> float {
-        float s = 0.f;
-        for (int64_t b = 0; b < n; b += BR_BATCH) {
+    const I rows = (I)a.rows, rpg = (I)a.rows_per_gate, G = rows / rpg;
+    const I q = rows / (I)grid, r = rows % (I)grid;  // as first_row and cta_of_row split them
+    const bool need_mid = w2 || gate, per_row = gate && rpg == 1;
+    const int team = G >= BR_WARPS ? 1 : BR_WARPS / (int)G;  // warps a gate row
+    const int per = (grid + BR_WARPS - 1) / BR_WARPS;
+    const int p0 = min(grid, warp * per), p1 = min(grid, p0 + per);
+    // CTAs c0 .. c1 have gate row gr's rows; the warps of a team take equal runs of them
+    auto ctas_of = [&](I gr, I &c0, I &c1) {
+        auto cta_of = [&](I i) { return i < r * (q + 1) ? i / (q + 1) : r + (i - r * (q + 1)) / q; };
+        c0 = cta_of(gr * rpg);
+        c1 = cta_of(gr * rpg + (rpg - 1));
+    };
+    // c0's part of gr is its second one unless gr is also its first gate row
+    auto slot_of = [&](I c0, I gr) { return 2 * c0 + (row_of_cta<I>(c0, q, r) / rpg != gr ? 1 : 0); };
+    // rows first, first + step, ... (n of them) of a [*, D] array, added in that order
+    auto load_rows = [&](const float *base, int64_t first, int step, int n, float (&v)[BR_BATCH]) {
+#pragma unroll
+        for (int i = 0; i < BR_BATCH; ++i) v[i] = in && i < n ? base[(first + (int64_t)i * step) * D + col] : 0.f;
+    };
+    auto add_all = [](const float (&v)[BR_BATCH], float s) {
+#pragma unroll
+        for (int i = 0; i < BR_BATCH; ++i) s += v[i];
+        return s;
+    };
+    auto add_rows = [&](const float *base, int64_t first, int step, int n, float s) {
+        for (int b = 0; b < n; b += BR_BATCH) {
             float v[BR_BATCH];
-#pragma unroll
-            for (int i = 0; i < BR_BATCH; ++i)
-                v[i] = b + i < n ? base[(first + (b + i) * step) * D + col] : 0.f;
-#pragma unroll
-            for (int i = 0; i < BR_BATCH; ++i) s += v[i];
+            load_rows(base, first + (int64_t)b * step, step, n - b, v);
+            s = add_all(v, s);
         }
         return s;
     };
-    const int per = (grid + BR_WARPS - 1) / BR_WARPS;
-    const int p0 = min(grid, warp * per), p1 = min(grid, p0 + per);
-    float pre = 0.f, post = 0.f;
-    if (in) pre = add_rows(a.part_pre, p0, 1, p1 - p0);
+    griddep_wait();
+    griddep_launch_dependents();
+    float head[BR_BATCH];  // the first of this warp's rows of part_pre
+    load_rows(a.part_pre, p0, 1, p1 - p0, head);
     const float w2c = in && w2 ? a.weight_bias + Cvt<T>::load1(w2 + col) : 1.f;
-    const int64_t rpg = a.rows_per_gate, G = a.rows / rpg;
-    const bool need_mid = w2 || gate, per_row = gate && rpg == 1;
-    const int team = G >= BR_WARPS ? 1 : BR_WARPS / (int)G;  // warps a gate row
+    float post = 0.f;
     if (need_mid && per_row) {
-        if (in) post = add_rows(a.part_mid, 2 * p0, 2, p1 - p0);
+        post = add_rows(a.part_mid, 2 * (int64_t)p0, 2, p1 - p0, 0.f);
     } else if (need_mid) {
-        float A = 0.f;
-        for (int64_t gr = warp / team; gr < G; gr += BR_WARPS / team) {
-            const int64_t c0 = cta_of_row(gr * rpg, grid, a.rows);
-            const int64_t c1 = cta_of_row((gr + 1) * rpg - 1, grid, a.rows);
-            if (!in) continue;
+        const int mate = warp % team;
+        for (I gr = warp / team; gr < G; gr += BR_WARPS / team) {
+            I c0, c1;
+            ctas_of(gr, c0, c1);
+            float A = 0.f;
+            const float gt = in && gate && team == 1 ? Cvt<T>::load1(gate + (int64_t)gr * a.ld_gate + col) : 1.f;
             if (c0 == c1 && a.g_gate) {
-                A = warp % team == 0 ? a.g_gate[gr * D + col] : 0.f;
+                if (mate == 0 && in) A = a.g_gate[(int64_t)gr * D + col];
             } else {
                 // parts: CTA c0's, then c0 + 1 ... c1 (each its first gate row)
-                const int64_t n = c1 - c0 + 1, share = (n + team - 1) / team;
-                const int64_t i0 = min(n, (int64_t)(warp % team) * share), i1 = min(n, i0 + share);
-                A = 0.f;
-                if (i0 == 0 && i1 > 0)
-                    A = a.part_mid[mid_slot(c0, gr, grid, a.rows, rpg) * D + col];
-                const int64_t j = max(i0, (int64_t)1);
-                if (j < i1) A += add_rows(a.part_mid, 2 * (c0 + j), 2, i1 - j);
+                const int n = (int)(c1 - c0) + 1, share = (n + team - 1) / team;
+                int i0 = min(n, mate * share);
+                const int i1 = min(n, i0 + share);
+                if (i0 == 0 && i1 > 0) {
+                    if (in) A = a.part_mid[(int64_t)slot_of(c0, gr) * D + col];
+                    i0 = 1;
+                }
+                A = add_rows(a.part_mid, 2 * ((int64_t)c0 + i0), 2, i1 - i0, A);
             }
-            if (team == 1) {
-                if (gate) a.g_gate[gr * D + col] = A * w2c;
-                post = fmaf(gate ? Cvt<T>::load1(gate + gr * a.ld_gate + col) : 1.f, A, post);
+            if (team == 1 && in) {
+                if (gate) a.g_gate[(int64_t)gr * D + col] = A * w2c;
+                post = fmaf(gt, A, post);
             }
+            if (team > 1) post = A;  // this warp's part of its gate row's A
         }
-        if (team > 1) post = A;  // this warp's part of its gate row's A
     }
+    float pre = add_all(head, 0.f);
+    pre = add_rows(a.part_pre, (int64_t)p0 + BR_BATCH, 1, p1 - p0 - BR_BATCH, pre);
     sums[0][warp][lane] = pre;
     sums[1][warp][lane] = post;
     __syncthreads();
@@ -238,13 +263,15 @@ __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const Block
     if (warp == 1 && in && need_mid) {
         float t = 0.f;
         if (per_row || team == 1) {
+#pragma unroll
             for (int k = 0; k < BR_WARPS; ++k) t += sums[1][k][lane];
         } else {
             for (int gr = 0; gr < (int)G; ++gr) {
+                const float gt = gate ? Cvt<T>::load1(gate + gr * a.ld_gate + col) : 1.f;
                 float A = 0.f;
                 for (int k = 0; k < team; ++k) A += sums[1][gr * team + k][lane];
                 if (gate) a.g_gate[gr * (int64_t)D + col] = A * w2c;
-                t = fmaf(gate ? Cvt<T>::load1(gate + gr * a.ld_gate + col) : 1.f, A, t);
+                t = fmaf(gt, A, t);
             }
         }
         if (w2) a.gw_post[col] = t;

@@ -7,11 +7,11 @@
 
 namespace rmsn {
 
-template <bool VJP, typename T, int UB, int MAXT, int MINB, int KIND, bool GROW>
+template <bool VJP, typename T, int UB, int MAXT, int MINB, int KIND, bool GROW, bool FULL = false>
 cudaError_t launch_block_inst(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> smem_mask{0};
     void (*kern)(BlockArgs);
-    if constexpr (VJP) kern = block_vjp_kernel<T, UB, MAXT, MINB, KIND, GROW>;
+    if constexpr (VJP) kern = block_vjp_kernel<T, UB, MAXT, MINB, KIND, GROW, FULL>;
     else kern = block_fwd_kernel<T, UB, MAXT, MINB, KIND, GROW>;
     if (p.smem > 0) {
         const cudaError_t e = allow_max_dynamic_smem((const void *)kern, smem_mask);
@@ -27,6 +27,13 @@ cudaError_t launch_block_kind(const BlockPlan &p, const BlockArgs &a, cudaStream
         if (p.threads <= 512) return launch_block_inst<VJP, T, UB, 512, 1, BLOCK_DIRECT, GROW>(p, a, s);
         return launch_block_inst<VJP, T, UB, 1024, 1, BLOCK_DIRECT, GROW>(p, a, s);
     }
+    // The training backward with all its operands, without their run-time tests:
+    // 15 % fewer instructions (16384 x 4096 bf16: 139 -> 129 us).
+    if constexpr (VJP && UB == 16 && !GROW)
+        if (a.w_post && a.g_res && a.rstd) {
+            if (p.threads <= 256) return launch_block_inst<VJP, T, UB, 256, 2, BLOCK_STAGED, GROW, true>(p, a, s);
+            if (p.threads <= 512) return launch_block_inst<VJP, T, UB, 512, 1, BLOCK_STAGED, GROW, true>(p, a, s);
+        }
     // Threads an SM holds (block_resident): 512 with 128 registers each; the
     // forward also fits 96, so its CTAs of 257-320 threads sit two an SM and
     // those of 513-640 one.
@@ -63,8 +70,9 @@ template <typename T>
 cudaError_t launch_block_vjp_both(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
     const cudaError_t e = launch_block<true, T>(p, a, s);
     if (e != cudaSuccess) return e;
-    return launch_pdl(block_reduce_kernel<T>, dim3((unsigned)((a.D + 31) / 32)), dim3(32 * BR_WARPS), 0, s, a,
-                      p.grid);
+    const dim3 grid((unsigned)((a.D + 31) / 32)), block(32 * BR_WARPS);
+    return a.rows <= INT32_MAX ? launch_pdl(block_reduce_kernel<T, uint32_t>, grid, block, 0, s, a, p.grid)
+                               : launch_pdl(block_reduce_kernel<T, int64_t>, grid, block, 0, s, a, p.grid);
 }
 
 }  // namespace rmsn

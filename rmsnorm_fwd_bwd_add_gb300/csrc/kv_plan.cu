@@ -5,11 +5,14 @@
 // slot and request, as rmsnorm_rope_kv_append takes them.
 //
 // Both are a scan over the requests followed by copies, a few kilobytes in
-// all: bound by latency.  One CTA scans (a request a thread, tiles of KV_NT
-// requests with a carry) and moves the blocks, a warp per request that has any;
-// the tokens are written by a second kernel over all SMs, or by the same CTA
-// when they are few.  Everything is in request order: the results are the same
-// on every run.
+// all: bound by latency, that is by the number of dependent trips to memory.  One
+// CTA scans (KV_PER requests a thread), lists the requests that move blocks, and
+// moves all their blocks together, KV_BATCH loads in flight a thread, whatever
+// request they belong to (a warp per request took 41 us to give back 80 requests
+// of 128 blocks each among 4000, and 32 us to hand out 1400 single blocks).  The
+// tokens are written by a second kernel over all SMs, or by the same CTA, from
+// shared memory, when they are few.  Everything is in request order: the
+// results are the same on every run.
 //
 // Lengths and block ids are device data and are checked there: a negative
 // length, a stack that runs over or an id outside the pool sets
@@ -34,8 +37,12 @@ namespace {
 using namespace rmsn;
 
 constexpr int KV_NT = 1024;
+constexpr int KV_PER = 4;                      // consecutive requests a thread scans
+constexpr int KV_TILE = KV_NT * KV_PER;        // requests a pass of the CTA
+constexpr int KV_BATCH = 4;                    // block ids a thread keeps in flight
 constexpr int KV_TOKEN_NT = 256;
-constexpr int KV_FUSED_TOKENS = 4096;
+constexpr int KV_TOKENS = 4 * KV_TOKEN_NT;     // tokens a CTA of the second kernel writes
+constexpr int KV_FUSED_TOKENS = 4096;          // the scanning CTA writes up to so many itself
 constexpr unsigned int BAD_INDEX = RMSNORM_DEVSTATUS_BAD_INDEX;
 
 struct KvArgs {
@@ -77,6 +84,97 @@ __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *sums, int64_t *t
     return v + (warp ? before : 0);
 }
 
+// Inclusive sums of KV_PER values a thread over the CTA, in order; returns the
+// CTA's sum.
+__device__ __forceinline__ int64_t cta_scan_per(int64_t (&v)[KV_PER], int64_t *sums) {
+#pragma unroll
+    for (int i = 1; i < KV_PER; ++i) v[i] += v[i - 1];
+    const int64_t own = v[KV_PER - 1];
+    int64_t total;
+    const int64_t before = cta_scan(own, sums, &total) - own;
+#pragma unroll
+    for (int i = 0; i < KV_PER; ++i) v[i] += before;
+    return total;
+}
+
+// The requests of a tile that move blocks, in order.  A scanned word carries
+// both a request's place in the list (its top bits) and its first block's place
+// among all of them.
+constexpr int KV_COUNT_SHIFT = 48;  // a tile moves fewer than 2^12 * 2^31 < 2^48 blocks
+struct Moves {
+    int64_t first[KV_TILE];  // place of an entry's first block among the tile's
+    int32_t from[KV_TILE];   // index of its first block in its table row
+    uint16_t req[KV_TILE];   // its request within the tile
+};
+
+struct PlanShared {
+    int64_t sums[KV_NT / 32];
+    union {
+        Moves moves;
+        struct {               // for the tokens, once the blocks are moved
+            int64_t starts[KV_TILE + 1];
+            int32_t base[KV_TILE];  // length before the step, or -1 - length if not granted
+        } map;
+    };
+};
+
+// Entries n[k] blocks long, from[k] on in request row b's table row, join the list;
+// returns the tile's blocks, and *entries their requests.  The list may be read
+// once the CTA has passed a barrier.
+__device__ __forceinline__ int64_t list_moves(const int64_t (&n)[KV_PER], const int32_t (&from)[KV_PER], Moves &mv,
+                                              int64_t *sums, int *entries) {
+    int64_t v[KV_PER];
+#pragma unroll
+    for (int k = 0; k < KV_PER; ++k) v[k] = n[k] + (n[k] > 0 ? (int64_t)1 << KV_COUNT_SHIFT : 0);
+    const int64_t total = cta_scan_per(v, sums);
+    const int64_t mask = ((int64_t)1 << KV_COUNT_SHIFT) - 1;
+#pragma unroll
+    for (int k = 0; k < KV_PER; ++k)
+        if (n[k] > 0) {
+            const int at = (int)(v[k] >> KV_COUNT_SHIFT) - 1;
+            mv.first[at] = (v[k] & mask) - n[k];
+            mv.from[at] = from[k];
+            mv.req[at] = (uint16_t)(threadIdx.x * KV_PER + k);
+        }
+    *entries = (int)(total >> KV_COUNT_SHIFT);
+    return total & mask;
+}
+
+// The last i < n with a[i] <= x (a ascending, a[0] <= x).
+template <typename A> __device__ __forceinline__ int last_at_most(const A *a, int n, A x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// Moves the tile's `total` blocks: f(row pointer at the block, its place) loads,
+// g(row pointer, place, id) stores, KV_BATCH of the first ahead of the second.
+template <typename F, typename G>
+__device__ __forceinline__ void move_blocks(const KvArgs &a, const Moves &mv, int entries, int64_t total, int64_t b0,
+                                            F load, G store) {
+    for (int64_t e0 = threadIdx.x; e0 < total; e0 += KV_NT * KV_BATCH) {
+        int32_t *at[KV_BATCH];
+        int32_t id[KV_BATCH];
+#pragma unroll
+        for (int i = 0; i < KV_BATCH; ++i) {
+            const int64_t e = e0 + i * KV_NT;
+            if (e < total) {
+                const int k = last_at_most(mv.first, entries, e);
+                at[i] = a.table + (b0 + mv.req[k]) * a.ld_table + mv.from[k] + (e - mv.first[k]);
+                id[i] = load(at[i], e);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < KV_BATCH; ++i) {
+            const int64_t e = e0 + i * KV_NT;
+            if (e < total) store(at[i], e, id[i]);
+        }
+    }
+}
+
 // The free count, clamped to what the stack holds.
 __device__ __forceinline__ int64_t stack_top(const KvArgs &a) {
     const int64_t n = *a.free_count;
@@ -84,141 +182,241 @@ __device__ __forceinline__ int64_t stack_top(const KvArgs &a) {
     return min(max(n, (int64_t)0), a.num_blocks);
 }
 
+// ceil(len / block) for 0 <= len < 2^32 and block >= 1
+__device__ __forceinline__ int64_t blocks_of(int64_t len, const KvArgs &a) {
+    return (int64_t)(((uint32_t)len + (uint64_t)a.block - 1) / (uint32_t)a.block);
+}
+
 __global__ void __launch_bounds__(KV_NT) kv_release_kernel(const KvArgs a) {
-    __shared__ int64_t sums[KV_NT / 32];
+    extern __shared__ __align__(16) unsigned char smem[];
+    PlanShared &sh = *reinterpret_cast<PlanShared *>(smem);
     griddep_wait();
-    const int lane = threadIdx.x & 31;
     const int64_t top = stack_top(a);
     int64_t pushed = 0;
-    for (int64_t b0 = 0; b0 < a.B; b0 += KV_NT) {
-        const int64_t b = b0 + threadIdx.x;
-        const int64_t len = b < a.B ? a.lens[b] : 0;
-        const bool done = b < a.B && a.finished[b];
-        int64_t n = done && len > 0 ? (len + a.block - 1) / a.block : 0;
-        if (len < 0 || n > a.width) {  // such a request gives nothing back
-            atomicOr(a.status, BAD_INDEX);
-            n = 0;
+    for (int64_t b0 = 0; b0 < a.B; b0 += KV_TILE) {
+        int32_t len[KV_PER];
+        bool done[KV_PER];
+        const int64_t b = b0 + threadIdx.x * KV_PER;
+#pragma unroll
+        for (int k = 0; k < KV_PER; ++k) {
+            len[k] = b + k < a.B ? a.lens[b + k] : 0;
+            done[k] = b + k < a.B && a.finished[b + k];
         }
-        int64_t total;
-        const int64_t first = top + pushed + cta_scan(n, sums, &total) - n;
-        pushed += total;
-        for (unsigned todo = __ballot_sync(0xffffffffu, n > 0); todo; todo &= todo - 1) {
-            const int j = __ffs(todo) - 1;
-            const int64_t nj = __shfl_sync(0xffffffffu, n, j), at = __shfl_sync(0xffffffffu, first, j);
-            const int32_t *row = a.table + (b - lane + j) * a.ld_table;
-            for (int64_t i = lane; i < nj; i += 32) {
-                const int32_t id = row[i];
-                if (id < 0 || id >= a.num_blocks || at + i >= a.num_blocks) atomicOr(a.status, BAD_INDEX);
-                if (at + i < a.num_blocks) a.free_blocks[at + i] = id;
+        int64_t n[KV_PER];
+        const int32_t from[KV_PER] = {};
+#pragma unroll
+        for (int k = 0; k < KV_PER; ++k) {
+            n[k] = done[k] && len[k] > 0 ? blocks_of(len[k], a) : 0;
+            if (len[k] < 0 || n[k] > a.width) {  // such a request gives nothing back
+                atomicOr(a.status, BAD_INDEX);
+                n[k] = 0;
             }
+            if (b + k < a.B) a.lens_out[b + k] = done[k] ? 0 : len[k];
         }
-        if (b < a.B) a.lens_out[b] = done ? 0 : (int32_t)len;
+        int entries;
+        const int64_t total = list_moves(n, from, sh.moves, sh.sums, &entries);
+        __syncthreads();
+        const int64_t base = top + pushed;
+        move_blocks(a, sh.moves, entries, total, b0, [](const int32_t *p, int64_t) { return *p; },
+                    [&](const int32_t *, int64_t e, int32_t id) {
+                        const int64_t at = base + e;
+                        if (id < 0 || id >= a.num_blocks || at >= a.num_blocks) atomicOr(a.status, BAD_INDEX);
+                        if (at < a.num_blocks) a.free_blocks[at] = id;
+                    });
+        pushed += total;
+        __syncthreads();  // the list may be written again
     }
     __syncthreads();  // every thread has read the count it may overwrite
     if (threadIdx.x == 0) *a.free_count_out = (int32_t)min(top + pushed, a.num_blocks);
     griddep_launch_dependents();
 }
 
-// Position, slot and request of token t.
-__device__ __forceinline__ void write_token(const KvArgs &a, int64_t t, int64_t total) {
-    int64_t pos = 0, slot = -1;
-    int32_t req = -1;
-    if (t < total) {
-        int64_t lo = 0, hi = a.B;  // the last request whose first token is at or before t
-        while (hi - lo > 1) {
-            const int64_t mid = (lo + hi) >> 1;
-            if (a.starts[mid] <= t) lo = mid; else hi = mid;
-        }
-        const int64_t s0 = a.starts[lo], s1 = a.starts[lo + 1];
-        const bool ok = a.granted[lo] != 0;
-        req = (int32_t)lo;
-        pos = (int64_t)a.lens_out[lo] - (ok ? s1 - s0 : 0) + (t - s0);
-        if (ok) {
-            const int64_t blk = pos / a.block;
-            const int32_t id = a.table[lo * a.ld_table + blk];
-            if (id < 0 || (a.free_count && id >= a.num_blocks)) atomicOr(a.status, BAD_INDEX);
-            else slot = (int64_t)id * a.block + (pos - blk * a.block);
-        } else {
-            pos = max(pos, (int64_t)0);
-        }
+// Position, slot and request of token t, which is request `req`'s token number
+// `off`; `base` is its length before the step, or -1 - length if not granted.
+__device__ __forceinline__ void write_token(const KvArgs &a, int64_t t, int64_t req, int64_t off, int32_t base) {
+    int64_t slot = -1;
+    const bool ok = base >= 0;
+    const int64_t pos = (ok ? (int64_t)base : -1 - (int64_t)base) + off;
+    if (ok) {
+        const int64_t blk = (int64_t)((uint64_t)pos / (uint32_t)a.block);
+        const int32_t id = a.table[req * a.ld_table + blk];
+        if (id < 0 || (a.free_count && id >= a.num_blocks)) atomicOr(a.status, BAD_INDEX);
+        else slot = (int64_t)id * a.block + (pos - blk * a.block);
     }
     a.positions[t] = pos;
     a.slots[t] = slot;
-    a.requests[t] = req;
+    a.requests[t] = (int32_t)req;
 }
 
-// The scan over the requests; with `tokens`, the same CTA writes the tokens.
+__device__ __forceinline__ void write_padding(const KvArgs &a, int64_t t) {
+    a.positions[t] = 0;
+    a.slots[t] = -1;
+    a.requests[t] = -1;
+}
+
+// The scan over the requests; with `tokens` (one tile), the same CTA writes the
+// tokens.
 __global__ void __launch_bounds__(KV_NT) kv_plan_kernel(const KvArgs a, bool tokens) {
-    __shared__ int64_t sums[KV_NT / 32];
+    extern __shared__ __align__(16) unsigned char smem[];
+    PlanShared &sh = *reinterpret_cast<PlanShared *>(smem);
     griddep_wait();
-    const int lane = threadIdx.x & 31;
     const bool pool = a.free_count != nullptr;
     const int64_t top = pool ? stack_top(a) : 0;
     int64_t total_new = 0, total_need = 0, popped = 0;
-    for (int64_t b0 = 0; b0 < a.B; b0 += KV_NT) {
-        const int64_t b = b0 + threadIdx.x;
-        int64_t len = 0, add = 0;
-        bool valid = b < a.B;
-        if (valid) {
-            len = a.lens[b];
-            add = a.new_lens[b];
-            if (len < 0 || add < 0) {
+    int64_t start[KV_PER];
+    int32_t base[KV_PER];  // for the tokens of the last tile
+    for (int64_t b0 = 0; b0 < a.B; b0 += KV_TILE) {
+        const int64_t b = b0 + threadIdx.x * KV_PER;
+        int32_t len[KV_PER], add[KV_PER];
+        bool valid[KV_PER];
+#pragma unroll
+        for (int k = 0; k < KV_PER; ++k) {
+            valid[k] = b + k < a.B;
+            len[k] = valid[k] ? a.lens[b + k] : 0;
+            add[k] = valid[k] ? a.new_lens[b + k] : 0;
+        }
+        int64_t end[KV_PER], need[KV_PER], cum[KV_PER];
+        int32_t have[KV_PER];
+#pragma unroll
+        for (int k = 0; k < KV_PER; ++k) {
+            if (len[k] < 0 || add[k] < 0) {
                 atomicOr(a.status, BAD_INDEX);
-                valid = false;
-                add = 0;
+                valid[k] = false;
+                add[k] = 0;
+            }
+            end[k] = add[k];
+        }
+        const int64_t tile_new = cta_scan_per(end, sh.sums);
+        bool ok[KV_PER];
+#pragma unroll
+        for (int k = 0; k < KV_PER; ++k) {
+            end[k] += total_new;
+            const int64_t sum = (int64_t)len[k] + add[k];
+            const int64_t h = valid[k] ? blocks_of(len[k], a) : 0, want = valid[k] ? blocks_of(sum, a) : 0;
+            ok[k] = valid[k] && want <= a.width && end[k] <= a.T && sum <= INT_MAX;
+            need[k] = cum[k] = ok[k] && pool ? want - h : 0;
+            have[k] = (int32_t)min(h, (int64_t)INT_MAX);
+        }
+        const int64_t tile_need = cta_scan_per(cum, sh.sums);
+        int64_t take[KV_PER];
+#pragma unroll
+        for (int k = 0; k < KV_PER; ++k) {
+            cum[k] += total_need;
+            ok[k] = ok[k] && (need[k] == 0 || cum[k] <= top);
+            take[k] = ok[k] ? need[k] : 0;
+            start[k] = end[k] - add[k];
+            base[k] = ok[k] ? len[k] : -1 - max(len[k], 0);
+            if (b + k < a.B) {
+                a.starts[b + k] = start[k];
+                a.granted[b + k] = ok[k] ? 1 : 0;
+                a.lens_out[b + k] = ok[k] ? len[k] + add[k] : len[k];
             }
         }
-        int64_t tile_new, tile_need;
-        const int64_t end = total_new + cta_scan(add, sums, &tile_new);
-        const int64_t have = valid ? (len + a.block - 1) / a.block : 0;
-        const int64_t want = valid ? (len + add + a.block - 1) / a.block : 0;
-        const bool fits = valid && want <= a.width && end <= a.T && len + add <= INT_MAX;
-        const int64_t need = fits && pool ? want - have : 0;
-        const int64_t cum = total_need + cta_scan(need, sums, &tile_need);
-        const bool ok = fits && (need == 0 || cum <= top);
         total_new += tile_new;
         total_need += tile_need;
-        const int64_t take = ok ? need : 0;
-        if (take) popped = max(popped, cum);
-        for (unsigned todo = __ballot_sync(0xffffffffu, take > 0); todo; todo &= todo - 1) {
-            const int j = __ffs(todo) - 1;
-            const int64_t n = __shfl_sync(0xffffffffu, take, j);
-            const int64_t from = top - 1 - (__shfl_sync(0xffffffffu, cum, j) - n);
-            int32_t *row = a.table + (b - lane + j) * a.ld_table + __shfl_sync(0xffffffffu, have, j);
-            for (int64_t i = lane; i < n; i += 32) {
-                const int32_t id = a.free_blocks[from - i];
-                if (id < 0 || id >= a.num_blocks) atomicOr(a.status, BAD_INDEX);
-                row[i] = id;
-            }
-        }
-        if (b < a.B) {
-            a.starts[b] = end - add;
-            a.granted[b] = ok ? 1 : 0;
-            a.lens_out[b] = (int32_t)(ok ? len + add : len);
-        }
+        // Requests that take blocks are granted in order, so the tile's blocks are
+        // the next ones off the stack.
+        int entries;
+        const int64_t total = list_moves(take, have, sh.moves, sh.sums, &entries);
+        __syncthreads();
+        const int64_t from = top - 1 - popped;
+        move_blocks(a, sh.moves, entries, total, b0, [&](const int32_t *, int64_t e) { return a.free_blocks[from - e]; },
+                    [&](int32_t *p, int64_t, int32_t id) {
+                        if (id < 0 || id >= a.num_blocks) atomicOr(a.status, BAD_INDEX);
+                        *p = id;
+                    });
+        popped += total;
+        __syncthreads();  // the list may be written again
     }
-    // blocks taken: the furthest any granted request reached
-    for (int off = 16; off > 0; off >>= 1) popped = max(popped, __shfl_xor_sync(0xffffffffu, popped, off));
-    __syncthreads();
-    if (lane == 0) sums[threadIdx.x >> 5] = popped;
-    __syncthreads();
+    __syncthreads();  // every thread has read the count it may overwrite
     if (threadIdx.x == 0) {
-        for (int w = 1; w < KV_NT / 32; ++w) popped = max(popped, sums[w]);
         a.starts[a.B] = total_new;
         if (pool) *a.free_count_out = (int32_t)(top - popped);
     }
     griddep_launch_dependents();
     if (tokens) {
-        __syncthreads();  // this CTA's own writes above
-        for (int64_t t = threadIdx.x; t < a.T; t += KV_NT) write_token(a, t, total_new);
+        const int n = (int)a.B;
+#pragma unroll
+        for (int k = 0; k < KV_PER; ++k) {
+            const int b = threadIdx.x * KV_PER + k;
+            if (b < n) {
+                sh.map.starts[b] = start[k];
+                sh.map.base[b] = base[k];
+            }
+        }
+        __syncthreads();  // with the table entries written above
+        for (int64_t t = threadIdx.x; t < a.T; t += KV_NT) {
+            if (t < total_new) {
+                const int req = last_at_most(sh.map.starts, n, t);
+                write_token(a, t, req, t - sh.map.starts[req], sh.map.base[req]);
+            } else {
+                write_padding(a, t);
+            }
+        }
     }
 }
 
+// The last request whose first token is at or before t, by a whole warp: 32
+// probes a step.
+__device__ __forceinline__ int64_t request_of(const KvArgs &a, int64_t t) {
+    const int lane = threadIdx.x & 31;
+    int64_t lo = 0, n = a.B;  // in [lo, lo + n)
+    while (n > 1) {
+        const int64_t step = (n + 31) / 32;
+        const int64_t at = lo + lane * step;
+        const bool below = lane * step < n && a.starts[at] <= t;
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));  // lane 0 always is
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    return lo;
+}
+
+// A CTA writes KV_TOKENS consecutive tokens.  Two warps find its first and last
+// requests; their starts go to shared memory, where every token finds its own.
 __global__ void __launch_bounds__(KV_TOKEN_NT) kv_tokens_kernel(const KvArgs a) {
+    constexpr int CAP = 2048;  // requests a CTA's tokens usually span fewer of
+    __shared__ int64_t s_starts[CAP + 1];
+    __shared__ int32_t s_base[CAP];
+    __shared__ int64_t s_range[2];
     griddep_wait();
     const int64_t total = a.starts[a.B];
-    for (int64_t t = (int64_t)blockIdx.x * KV_TOKEN_NT + threadIdx.x; t < a.T; t += (int64_t)gridDim.x * KV_TOKEN_NT)
-        write_token(a, t, total);
+    const int warp = threadIdx.x >> 5;
+    for (int64_t t0 = (int64_t)blockIdx.x * KV_TOKENS; t0 < a.T; t0 += (int64_t)gridDim.x * KV_TOKENS) {
+        const int64_t t1 = min(min(t0 + KV_TOKENS, a.T), total);  // its live tokens end
+        if (warp < 2 && t0 < t1) {
+            const int64_t r = request_of(a, warp == 0 ? t0 : t1 - 1);
+            if ((threadIdx.x & 31) == 0) s_range[warp] = r;
+        }
+        __syncthreads();
+        const int64_t lo = t0 < t1 ? s_range[0] : 0, n = t0 < t1 ? s_range[1] - lo + 1 : 0;
+        const bool fits = n <= CAP;
+        auto base_of = [&](int64_t req, int64_t s0, int64_t s1) -> int32_t {
+            const int32_t len = a.lens_out[req];
+            return a.granted[req] ? (int32_t)(len - (s1 - s0)) : -1 - max(len, 0);
+        };
+        if (fits) {
+            for (int i = threadIdx.x; i < n; i += KV_TOKEN_NT) {
+                const int64_t s0 = a.starts[lo + i], s1 = a.starts[lo + i + 1];
+                s_starts[i] = s0;
+                s_base[i] = base_of(lo + i, s0, s1);
+            }
+        }
+        __syncthreads();
+        for (int64_t t = t0 + threadIdx.x; t < min(t0 + KV_TOKENS, a.T); t += KV_TOKEN_NT) {
+            if (t >= total) {
+                write_padding(a, t);
+            } else if (fits) {
+                const int i = last_at_most(s_starts, (int)n, t);
+                write_token(a, t, lo + i, t - s_starts[i], s_base[i]);
+            } else {
+                const int64_t req = lo + last_at_most(a.starts + lo, (int)n, t);
+                const int64_t s0 = a.starts[req];
+                write_token(a, t, req, t - s0, base_of(req, s0, a.starts[req + 1]));
+            }
+        }
+        __syncthreads();  // the starts are written again
+    }
     griddep_launch_dependents();
 }
 
@@ -284,8 +482,10 @@ extern "C" int rmsnorm_kv_release(const int32_t *lens, const uint8_t *finished, 
     a.free_blocks = free_blocks; a.free_count = free_count; a.num_blocks = num_blocks;
     a.lens_out = lens_out; a.free_count_out = free_count_out;
     a.B = B;
-    const cudaError_t e = launch_pdl(kv_release_kernel, dim3(1), dim3(KV_NT), 0,
-                                     static_cast<cudaStream_t>(stream), a);
+    static std::atomic<uint64_t> smem_mask{0};
+    cudaError_t e = allow_max_dynamic_smem((const void *)kv_release_kernel, smem_mask);
+    if (e == cudaSuccess)
+        e = launch_pdl(kv_release_kernel, dim3(1), dim3(KV_NT), sizeof(PlanShared), static_cast<cudaStream_t>(stream), a);
     return e == cudaSuccess ? RMSNORM_OK : record_cuda_error(e);
 }
 
@@ -330,11 +530,13 @@ extern "C" int rmsnorm_kv_plan(const int32_t *lens, const int32_t *new_lens, int
     a.lens_out = lens_out; a.free_count_out = free_count_out;
     a.starts = starts; a.positions = positions; a.slots = slots; a.requests = requests; a.granted = granted;
     a.B = B; a.T = T;
-    const bool fused = T <= KV_FUSED_TOKENS;
+    const bool fused = T <= KV_FUSED_TOKENS && B <= KV_TILE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_pdl(kv_plan_kernel, dim3(1), dim3(KV_NT), 0, s, a, fused);
+    static std::atomic<uint64_t> smem_mask{0};
+    cudaError_t e = allow_max_dynamic_smem((const void *)kv_plan_kernel, smem_mask);
+    if (e == cudaSuccess) e = launch_pdl(kv_plan_kernel, dim3(1), dim3(KV_NT), sizeof(PlanShared), s, a, fused);
     if (e == cudaSuccess && !fused) {
-        const int grid = (int)std::min<int64_t>((T + KV_TOKEN_NT - 1) / KV_TOKEN_NT, (int64_t)sm * 8);
+        const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((T + KV_TOKENS - 1) / KV_TOKENS, (int64_t)sm * 8));
         e = launch_pdl(kv_tokens_kernel, dim3(grid), dim3(KV_TOKEN_NT), 0, s, a);
     }
     return e == cudaSuccess ? RMSNORM_OK : record_cuda_error(e);

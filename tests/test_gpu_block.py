@@ -353,8 +353,33 @@ def test_block_refusals():
     g32 = torch.zeros(64, device=DEV)
     with pytest.raises(rn.RmsnormError):
         rn.rmsnorm_block_vjp(y, y, w, w, y, EPS, gw_post=g32, gw_pre=g32)
+
+
+def test_block_vjp_scratch():
+    """The C entry points with pooled and with the caller's scratch give the same
+    bits; a failed allocation and a bad workspace leave the outputs alone."""
+    lib, rows, D = rn._native.lib(), 300, 512
+    p = _problem(rows, D, torch.bfloat16, 3, True, 0.0)
+    want = rn.rmsnorm_block_vjp(p["y"], p["h"], p["w_post"], p["w_pre"], p["g"], EPS, 0.0, p["gate"], 0.5, p["g_res"])
+
+    def call(fn, *tail):
+        out = [torch.full_like(t, 5.0) for t in want]
+        st = fn(p["y"].data_ptr(), D, p["h"].data_ptr(), D, p["w_post"].data_ptr(), p["w_pre"].data_ptr(),
+                p["gate"].data_ptr(), D, 3, 0.5, p["g"].data_ptr(), D, p["g_res"].data_ptr(), D, None, EPS, 0.0,
+                out[0].data_ptr(), D, out[1].data_ptr(), D, out[2].data_ptr(), out[3].data_ptr(), out[4].data_ptr(),
+                rows, D, 1, *tail, torch.cuda.current_stream().cuda_stream)
+        return st, out
+    n = lib.rmsnorm_block_vjp_workspace_size(rows, D, 1)
+    ws = torch.full((n + 512,), 255, dtype=torch.uint8, device=DEV)
+    at = ws.data_ptr() + (-ws.data_ptr()) % 256
+    for st, out in (call(lib.rmsnorm_block_vjp), call(lib.rmsnorm_block_vjp_ws, at, n)):
+        assert st == 0
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
+    assert (ws[at - ws.data_ptr() + n:] == 255).all()
     rn.rmsnorm_debug_fail_allocs(1)
-    gy = torch.full_like(y, 5.0)
-    with pytest.raises(rn.RmsnormError) as e:
-        rn.rmsnorm_block_vjp(y, y, w, w, y, EPS, g_y=gy)
-    assert e.value.status == 4 and (gy == 5).all()
+    for st, out in (call(lib.rmsnorm_block_vjp), call(lib.rmsnorm_block_vjp_ws, at, n - 1),
+                    call(lib.rmsnorm_block_vjp_ws, None, n), call(lib.rmsnorm_block_vjp_ws, at + 16, n),
+                    call(lib.rmsnorm_block_vjp_ws, p["y"].data_ptr(), rows * D * 2 + n)):
+        assert st in (1, 4) and all((t == 5).all() for t in out)
+    assert lib.rmsnorm_block_vjp_workspace_size(0, D, 1) == 0 == lib.rmsnorm_block_vjp_workspace_size(4, 0, 1)
