@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
     const float inv_D = 1.0f / (float)a.D;
     constexpr bool per_row = GROW;  // a gate row for each row
     const bool post = a.w_post != nullptr;
-    const int64_t r0 = first_row(blockIdx.x, gridDim.x, a.rows), r1 = first_row(blockIdx.x + 1, gridDim.x, a.rows);
+    const RowDeal deal = fwd_rows(a, blockIdx.x, gridDim.x);
 
     const void *src[5] = {a.y, a.res, per_row ? a.gate : nullptr, nullptr, nullptr};
     const int64_t ld[5] = {a.ld_y, a.ld_res, a.ld_gate, 0, 0};
@@ -280,11 +280,11 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
     griddep_wait();
     if constexpr (KIND == BLOCK_STAGED) {
         if (threadIdx.x == 0)
-            for (int s = 0; s < ring.S && r0 + s < r1; ++s) ring_issue<T>(ring, a, src, ld, r0 + s, s, policy);
+            for (int s = 0; s < ring.S && s < deal.n; ++s) ring_issue<T>(ring, a, src, ld, deal.row(s), s, policy);
     }
 
     // A row's slots; the first row's loads go ahead of the weights' where no ring does.
-    const int64_t row0 = r0 + (KIND == BLOCK_WARP ? (int)(threadIdx.x >> 5) : 0);
+    const int ry = KIND == BLOCK_WARP ? (int)(threadIdx.x >> 5) : 0;
     Raw vy[V], vr[V], vg[GROW ? V : 1];
     auto fetch = [&](const T *py, const T *pr, const T *pg) {
 #pragma unroll
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
               per_row ? static_cast<const T *>(a.gate) + row * a.ld_gate : nullptr);
     };
     if constexpr (KIND != BLOCK_STAGED)
-        if (row0 < r1) fetch_global(row0);
+        if (ry < deal.n) fetch_global(deal.row(ry));
 
     float *table = reinterpret_cast<float *>(smem + BLOCK_HEADER);
     Raw vw[KIND == BLOCK_STAGED ? 1 : V];
@@ -353,12 +353,13 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
         }
     };
 
-    int64_t group_end = a.gate && !per_row ? r0 : INT64_MAX;  // first row past the gate row held in m
+    int64_t group_end = a.gate && !per_row ? 0 : INT64_MAX;  // first row past the gate row held in m
     int s = 0;
     uint32_t ph = 0;
-    for (int64_t row = row0; row < r1; row += R) {
+    for (int64_t i = ry; i < deal.n; i += R) {
+        const int64_t row = deal.row(i);
         if (row >= group_end) {
-            const int64_t gr = row / a.rows_per_gate;
+            const int64_t gr = gate_row(row, a.rows_per_gate);
             group_end = (gr + 1) * a.rows_per_gate;
             load_m(static_cast<const T *>(a.gate) + gr * a.ld_gate);
         }
@@ -410,22 +411,21 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
         if constexpr (KIND == BLOCK_WARP) {
             warp_sums<4>(sum);
         } else {
-            ok = cta_sums<4, MAXW>(sum, s_red[row & 1], nw, ok);
+            ok = cta_sums<4, MAXW>(sum, s_red[i & 1], nw, ok);
         }
         if constexpr (KIND == BLOCK_STAGED) {
             if (!ok) {  // leave once this CTA's copies have landed
                 if (threadIdx.x == 0) {
                     atomicOr(a.status, DEVSTATUS_WAIT_TIMEOUT);
-                    for (int64_t k = row; k < r1 && k < row + ring.S; ++k) {
-                        const int64_t i = k - r0;
-                        if (k != a.drop_row)
-                            mbar_wait_bounded(&ring.full[i % ring.S], (uint32_t)((i / ring.S) & 1), DEFAULT_WAIT_BUDGET);
-                    }
+                    for (int64_t k = i; k < deal.n && k < i + ring.S; ++k)
+                        if (deal.row(k) != a.drop_row)
+                            mbar_wait_bounded(&ring.full[k % ring.S], (uint32_t)((k / ring.S) & 1), DEFAULT_WAIT_BUDGET);
                 }
                 return;
             }
             // every thread has its units of this stage in registers
-            if (threadIdx.x == 0 && row + ring.S < r1) ring_issue<T>(ring, a, src, ld, row + ring.S, s, policy);
+            if (threadIdx.x == 0 && i + ring.S < deal.n)
+                ring_issue<T>(ring, a, src, ld, deal.row(i + ring.S), s, policy);
         }
         if constexpr (MAXT * MINB > 512) {  // 96 registers or fewer
 #pragma unroll
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
                 one[0] = group_sum<32>(one[0]);
             } else {
                 __syncthreads();  // this row's sums have been read
-                cta_sums<1, MAXW>(one, s_red[row & 1], nw, true);
+                cta_sums<1, MAXW>(one, s_red[i & 1], nw, true);
             }
             ss = one[0];
         }
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
                 ph ^= 1u;
             }
         } else if constexpr (KIND == BLOCK_WARP) {
-            if (row + R < r1) fetch_global(row + R);
+            if (i + R < deal.n) fetch_global(deal.row(i + R));
         }
     }
     griddep_launch_dependents();
@@ -517,8 +517,8 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
     constexpr bool per_row = GROW;  // a gate row for each row
     const bool post = FULL || a.w_post != nullptr, more = FULL || a.g_res != nullptr;
     const bool saved = FULL || a.rstd != nullptr;
-    const int64_t cta = blockIdx.x, grid = gridDim.x;
-    const int64_t r0 = first_row(cta, grid, a.rows), r1 = first_row(cta + 1, grid, a.rows);
+    const int64_t cta = blockIdx.x;
+    const RowDeal deal = vjp_rows(a, cta);
 
     const void *src[5] = {a.y, a.res, a.g, a.g_res, per_row ? a.gate : nullptr};
     const int64_t ld[5] = {a.ld_y, a.ld_res, a.ld_g, a.ld_g_res, a.ld_gate};
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
     griddep_wait();
     if constexpr (KIND == BLOCK_STAGED) {
         if (threadIdx.x == 0)
-            for (int s = 0; s < ring.S && r0 + s < r1; ++s) ring_issue<T>(ring, a, src, ld, r0 + s, s, policy);
+            for (int s = 0; s < ring.S && s < deal.n; ++s) ring_issue<T>(ring, a, src, ld, deal.row(s), s, policy);
     }
 
     // A row's slots; the first row's loads go ahead of the weights' where no ring does.
@@ -560,15 +560,9 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
               more ? static_cast<const T *>(a.g_res) + row * a.ld_g_res : nullptr,
               per_row ? static_cast<const T *>(a.gate) + row * a.ld_gate : nullptr);
     };
-    // The row this thread takes after `row` (rows of one gate row are dealt out to
-    // the warps from its first on), or r1.
-    auto next_row = [&](int64_t row, int64_t seg_end) -> int64_t {
-        if (row + R < seg_end) return row + R;
-        return min(r1, seg_end + ry);  // (not taken if the next gate row is shorter)
-    };
     if constexpr (KIND != BLOCK_STAGED)
-        if (r0 + ry < r1) fetch_global(r0 + ry);
-    int64_t fetched = r0 + ry;  // the row in the slots
+        if (ry < deal.n) fetch_global(deal.row(ry));
+    int64_t fetched = ry;  // the row in the slots
 
     float *table = reinterpret_cast<float *>(smem + BLOCK_HEADER);
     Raw vw[KIND == BLOCK_STAGED ? 1 : V];
@@ -624,7 +618,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
     // Writes k times the accumulators to the row dst (BLOCK_WARP: the warps' added
     // in warp order) and clears them.
     auto flush = [&](float2 (&acc)[V][P], float *dst, float k) {
-        if constexpr (KIND == BLOCK_WARP) {
+        if (KIND == BLOCK_WARP && R > 1) {
             float *buf = reinterpret_cast<float *>(smem);  // [R][D]
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -653,12 +647,12 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
 
     int s = 0;
     uint32_t ph = 0;
-    for (int64_t seg = r0; seg < r1;) {  // rows of one gate row
-        const int64_t gr = per_row ? 0 : seg / a.rows_per_gate;
-        const int64_t g_end = per_row ? a.rows : (gr + 1) * a.rows_per_gate;
-        const int64_t end = min(r1, g_end);
+    for (int64_t seg = 0; seg < deal.n;) {  // rows of one gate row: deal.row(seg), ..., deal.row(end - 1)
+        const int64_t gr = per_row ? 0 : gate_row(deal.row(seg), a.rows_per_gate);
+        const int64_t end = per_row || a.team ? deal.n : min(deal.n, (gr + 1) * a.rows_per_gate - deal.lo);
         if (a.gate && !per_row) load_m(static_cast<const T *>(a.gate) + gr * a.ld_gate);
-        for (int64_t row = seg + ry; row < end; row += R) {
+        for (int64_t i = seg + ry; i < end; i += R) {
+            const int64_t row = deal.row(i);
             float r_y = 1.f, r_h = 0.f;
             if (saved) {
                 if (post) r_y = __ldg(a.rstd + row);
@@ -678,7 +672,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                 const T *pga = per_row ? staged(a.gate, a.ld_gate) : nullptr;
                 ok = mbar_wait_bounded(&ring.full[s], ph, a.wait_budget);
                 fetch(py, phh, pgo, pgr, pga);
-            } else if (row != fetched) {
+            } else if (i != fetched) {
                 fetch_global(row);
             }
             // m of unit j with the row's own gate
@@ -732,24 +726,23 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                 if (saved) warp_sums<4>(reinterpret_cast<float (&)[4]>(sum));
                 else warp_sums<6>(sum);
             } else {
-                ok = saved ? cta_sums<4, MAXW>(reinterpret_cast<float (&)[4]>(sum), s_red[row & 1], nw, ok)
-                           : cta_sums<6, MAXW>(sum, s_red[row & 1], nw, ok);
+                ok = saved ? cta_sums<4, MAXW>(reinterpret_cast<float (&)[4]>(sum), s_red[i & 1], nw, ok)
+                           : cta_sums<6, MAXW>(sum, s_red[i & 1], nw, ok);
             }
             if constexpr (KIND == BLOCK_STAGED) {
                 if (!ok) {
                     if (threadIdx.x == 0) {
                         atomicOr(a.status, DEVSTATUS_WAIT_TIMEOUT);
-                        for (int64_t k = row; k < r1 && k < row + ring.S; ++k) {
-                            const int64_t i = k - r0;
-                            if (k != a.drop_row)
-                                mbar_wait_bounded(&ring.full[i % ring.S], (uint32_t)((i / ring.S) & 1),
+                        for (int64_t k = i; k < deal.n && k < i + ring.S; ++k)
+                            if (deal.row(k) != a.drop_row)
+                                mbar_wait_bounded(&ring.full[k % ring.S], (uint32_t)((k / ring.S) & 1),
                                                   DEFAULT_WAIT_BUDGET);
-                        }
                     }
                     return;
                 }
                 // every thread has its slots of this stage in registers
-                if (threadIdx.x == 0 && row + ring.S < r1) ring_issue<T>(ring, a, src, ld, row + ring.S, s, policy);
+                if (threadIdx.x == 0 && i + ring.S < deal.n)
+                    ring_issue<T>(ring, a, src, ld, deal.row(i + ring.S), s, policy);
             }
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -817,16 +810,17 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                     ph ^= 1u;
                 }
             } else if constexpr (KIND == BLOCK_WARP) {
-                fetched = next_row(row, end);
-                if (fetched < r1) fetch_global(fetched);
+                // the next gate row's rows are dealt out to the warps from its first on
+                fetched = i + R < end ? i + R : end + ry;
+                if (fetched < deal.n) fetch_global(deal.row(fetched));
             }
         }
         if (a.gate || post) {
-            const bool whole = a.g_gate && !per_row && gr * a.rows_per_gate >= r0 && g_end <= r1;
+            const bool whole = a.g_gate && !per_row && end - seg == a.rows_per_gate;
             flush(acc_mid,
                   per_row ? a.part_mid + 2 * cta * D
                   : whole ? a.g_gate + gr * D
-                          : a.part_mid + mid_slot(cta, gr, grid, a.rows, a.rows_per_gate) * D,
+                          : a.part_mid + mid_slot(cta, seg == 0) * D,
                   a.scale);
         }
         seg = end;

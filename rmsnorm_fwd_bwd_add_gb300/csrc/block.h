@@ -39,40 +39,81 @@ struct BlockArgs {
     int64_t drop_row;              // test hook: this row's copy is never issued
     int64_t rows;
     int64_t rows_per_gate;         // rows / G (rows without a gate)
+    int chunk_shift;               // rows are dealt out 2^chunk_shift at a time
+    int team;                      // rows are dealt out (VJP: a gate row's to CTAs of their own)
+    int64_t rows_per_team;         // VJP: rows_per_gate, or all rows where the gate has one for each
+    int64_t split_q, split_r;      // team: CTAs / gate rows, else rows / CTAs, and the remainder
     float eps, weight_bias, scale;
     int D;
     int stages;
     uint32_t stage_bytes;          // of one tensor's row in the ring
 };
 
-// CTA c takes the consecutive rows [first_row(c), first_row(c + 1)), so a gate
-// row's rows meet as few CTAs as they can and the sums over rows have a fixed
-// order.
-__host__ __device__ inline int64_t first_row(int64_t c, int64_t grid, int64_t rows) {
-    const int64_t q = rows / grid, r = rows % grid;
-    return c * q + (c < r ? c : r);
-}
+// Part c of n things split into equal consecutive runs, the first n % parts of them
+// one longer: q = n / parts and r = n % parts, divided once on the host.
+__host__ __device__ inline int64_t split_first(int64_t c, int64_t q, int64_t r) { return c * q + (c < r ? c : r); }
 
-// The CTA that takes row i.
-__host__ __device__ inline int64_t cta_of_row(int64_t i, int64_t grid, int64_t rows) {
-    const int64_t q = rows / grid, r = rows % grid;
+// The part that has thing i.
+template <typename I> __host__ __device__ inline I split_part(I i, I q, I r) {
     return i < r * (q + 1) ? i / (q + 1) : r + (i - r * (q + 1)) / q;
 }
 
-// Where CTA c leaves its part of gate row gr's sum A when it has not got all
-// of that gate row's rows: at most its first and its last gate row are such, so
-// two rows of part_mid a CTA hold them whatever the number of gate rows.
-__host__ __device__ inline int64_t mid_slot(int64_t c, int64_t gr, int64_t grid, int64_t rows,
-                                            int64_t rows_per_gate) {
-    return 2 * c + (gr != first_row(c, grid, rows) / rows_per_gate ? 1 : 0);
+// row / rows_per_gate; 64-bit division costs a hundred instructions.
+__host__ __device__ inline int64_t gate_row(int64_t row, int64_t rows_per_gate) {
+    return (uint64_t)(row | rows_per_gate) >> 32 ? row / rows_per_gate : (uint32_t)row / (uint32_t)rows_per_gate;
 }
+
+// The rows of one CTA, in order.  They are dealt out to `size` CTAs in chunks of
+// 2^shift: this one, `rank`, has rows lo + (k * size + rank) * 2^shift + j of [lo,
+// hi).
+struct RowDeal {
+    int64_t lo, hi, n;  // n: how many rows
+    int64_t rank, size;
+    int shift;
+    __host__ __device__ RowDeal(int64_t lo_, int64_t hi_, int64_t rank_, int64_t size_, int shift_)
+        : lo(lo_), hi(hi_), rank(rank_), size(size_), shift(shift_) {
+        const int64_t cycle = size << shift, full = gate_row(hi - lo, cycle);
+        int64_t rest = (hi - lo) - full * cycle - (rank << shift);
+        rest = rest < 0 ? 0 : rest < ((int64_t)1 << shift) ? rest : (int64_t)1 << shift;
+        n = (full << shift) + rest;
+    }
+    __host__ __device__ int64_t row(int64_t i) const {
+        return lo + ((((i >> shift) * size + rank) << shift) | (i & (((int64_t)1 << shift) - 1)));
+    }
+};
+
+// The forward's rows of CTA c.  team: dealt out to all CTAs; otherwise a run each.
+__host__ __device__ inline RowDeal fwd_rows(const BlockArgs &a, int64_t c, int64_t grid) {
+    if (a.team) return RowDeal(0, a.rows, c, grid, a.chunk_shift);
+    return RowDeal(split_first(c, a.split_q, a.split_r), split_first(c + 1, a.split_q, a.split_r), 0, 1, 0);
+}
+
+// The VJP's rows of CTA c.  team: the CTAs are split among the gate rows, and each
+// gate row's rows dealt out to its CTAs (one gate row a CTA).  Otherwise CTA c has
+// one run of rows, which may meet several gate rows.
+__host__ __device__ inline RowDeal vjp_rows(const BlockArgs &a, int64_t c) {
+    if (!a.team) {
+        const int64_t r0 = split_first(c, a.split_q, a.split_r);
+        return RowDeal(r0, split_first(c + 1, a.split_q, a.split_r), 0, 1, 0);
+    }
+    const int64_t q = a.split_q, r = a.split_r;
+    const int64_t gr = (uint64_t)(c | q) >> 31 ? split_part<int64_t>(c, q, r)
+                                                : (int64_t)split_part<uint32_t>((uint32_t)c, (uint32_t)q, (uint32_t)r);
+    const int64_t c0 = split_first(gr, q, r);
+    return RowDeal(gr * a.rows_per_team, (gr + 1) * a.rows_per_team, c - c0, split_first(gr + 1, q, r) - c0, a.chunk_shift);
+}
+
+// Where CTA c leaves its part of a gate row's sum A when it has not got all of
+// that gate row's rows: at most its first and its last gate row are such, so two
+// rows of part_mid a CTA hold them whatever the number of gate rows.
+__host__ __device__ inline int64_t mid_slot(int64_t c, bool first) { return 2 * c + (first ? 0 : 1); }
 
 // How a call runs: BLOCK_GENERIC for rows that do not fit on chip, else the
 // tier of block.cuh with units of `ub` bytes.
 enum : int { BLOCK_STAGED = 0, BLOCK_DIRECT = 1, BLOCK_WARP = 2, BLOCK_GENERIC = 3 };
 
 struct BlockPlan {
-    int kind, ub, threads, grid, stages;
+    int kind, ub, threads, grid, stages, chunk_shift, team;
     uint32_t stage_bytes;
     size_t smem;
 };

@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(BLOCK_GENERIC_NT) block_fwd_generic_kernel(con
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *y = static_cast<const T *>(a.y) + row * a.ld_y;
         const T *res = static_cast<const T *>(a.res) + row * a.ld_res;
-        const T *gate = a.gate ? static_cast<const T *>(a.gate) + row / a.rows_per_gate * a.ld_gate : nullptr;
+        const T *gate = a.gate ? static_cast<const T *>(a.gate) + gate_row(row, a.rows_per_gate) * a.ld_gate : nullptr;
         T *out = static_cast<T *>(a.out0) + row * a.ld_out0;
         T *nres = static_cast<T *>(a.out1) + row * a.ld_out1;
         float r_y = 1.f;
@@ -83,13 +83,13 @@ __global__ void __launch_bounds__(BLOCK_GENERIC_NT) block_vjp_generic_kernel(con
     const int tid = threadIdx.x, D = a.D;
     const float wb = a.weight_bias, inv_D = 1.0f / (float)D;
     const T *w1 = static_cast<const T *>(a.w_pre), *w2 = static_cast<const T *>(a.w_post);
-    const int64_t cta = blockIdx.x, grid = gridDim.x;
-    const int64_t r0 = first_row(cta, grid, a.rows), r1 = first_row(cta + 1, grid, a.rows);
+    const int64_t cta = blockIdx.x;
+    const int64_t r0 = split_first(cta, a.split_q, a.split_r), r1 = split_first(cta + 1, a.split_q, a.split_r);
     const bool per_row = a.gate && a.rows_per_gate == 1;
     griddep_wait();
     float *pre = a.part_pre + cta * D;
     for (int64_t row = r0; row < r1; ++row) {
-        const int64_t gr = row / a.rows_per_gate;
+        const int64_t gr = gate_row(row, a.rows_per_gate);
         const T *y = static_cast<const T *>(a.y) + row * a.ld_y;
         const T *hp = static_cast<const T *>(a.res) + row * a.ld_res;
         const T *g = static_cast<const T *>(a.g) + row * a.ld_g;
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(BLOCK_GENERIC_NT) block_vjp_generic_kernel(con
         const bool whole = a.g_gate && gr * a.rows_per_gate >= r0 && (gr + 1) * a.rows_per_gate <= r1;
         float *mid = per_row ? a.part_mid + 2 * cta * D
                      : whole ? a.g_gate + gr * D
-                             : a.part_mid + mid_slot(cta, gr, grid, a.rows, a.rows_per_gate) * D;
+                             : a.part_mid + mid_slot(cta, gr == gate_row(r0, a.rows_per_gate)) * D;
         const bool first = per_row ? row == r0 : row == r0 || row % a.rows_per_gate == 0;
         for (int c = tid; c < D; c += NT) {
             const float v = grad_h(c), yv = Cvt<T>::load1(y + c), m = mult(c);
@@ -163,15 +163,12 @@ __global__ void __launch_bounds__(BLOCK_GENERIC_NT) block_vjp_generic_kernel(con
 //   BR_WARPS, ...  A part is a row of part_mid, or the whole sum that one CTA
 //   left in g_gate, which becomes w2 * A in place.  Gate rows of one row each
 //   come finished from the first stage, which also weighted its sums.
-// The order of every sum depends on (rows, G, grid) alone.  Latency-bound: a
+// The order of every sum depends on how the rows are dealt out alone.  Latency-bound: a
 // warp's first loads of both sums are in flight together, and the row
 // arithmetic is 32-bit (I) where the row count allows (64-bit divisions made
 // the whole stage 14 us at 16384 x 4096 in 8 gate rows).
 constexpr int BR_WARPS = 32;
 constexpr int BR_BATCH = 16;
-
-template <typename I>
-__device__ __forceinline__ I row_of_cta(I c, I q, I r) { return c * q + (c < r ? c : r); }
 
 template <typename T, typename I>
 __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const BlockArgs a, int grid) {
@@ -183,19 +180,26 @@ __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const Block
     const T *w2 = static_cast<const T *>(a.w_post);
     const T *gate = static_cast<const T *>(a.gate);
     const I rows = (I)a.rows, rpg = (I)a.rows_per_gate, G = rows / rpg;
-    const I q = rows / (I)grid, r = rows % (I)grid;  // as first_row and cta_of_row split them
+    const I q = (I)a.split_q, r = (I)a.split_r;
     const bool need_mid = w2 || gate, per_row = gate && rpg == 1;
     const int team = G >= BR_WARPS ? 1 : BR_WARPS / (int)G;  // warps a gate row
     const int per = (grid + BR_WARPS - 1) / BR_WARPS;
     const int p0 = min(grid, warp * per), p1 = min(grid, p0 + per);
-    // CTAs c0 .. c1 have gate row gr's rows; the warps of a team take equal runs of them
+    // CTAs c0 .. c1 have gate row gr's rows (as vjp_rows deals them out); the warps
+    // of a team take equal runs of them
     auto ctas_of = [&](I gr, I &c0, I &c1) {
-        auto cta_of = [&](I i) { return i < r * (q + 1) ? i / (q + 1) : r + (i - r * (q + 1)) / q; };
-        c0 = cta_of(gr * rpg);
-        c1 = cta_of(gr * rpg + (rpg - 1));
+        if (a.team) {
+            c0 = (I)split_first(gr, q, r);
+            c1 = (I)split_first((int64_t)gr + 1, q, r) - 1;
+        } else {
+            c0 = split_part<I>(gr * rpg, q, r);
+            c1 = split_part<I>(gr * rpg + (rpg - 1), q, r);
+        }
     };
-    // c0's part of gr is its second one unless gr is also its first gate row
-    auto slot_of = [&](I c0, I gr) { return 2 * c0 + (row_of_cta<I>(c0, q, r) / rpg != gr ? 1 : 0); };
+    // c0's part of gr is its second one unless gr is its first gate row
+    auto slot_of = [&](I c0, I gr) {
+        return mid_slot(c0, a.team || (I)split_first(c0, q, r) / rpg == gr);
+    };
     // rows first, first + step, ... (n of them) of a [*, D] array, added in that order
     auto load_rows = [&](const float *base, int64_t first, int step, int n, float (&v)[BR_BATCH]) {
 #pragma unroll
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const Block
                 int i0 = min(n, mate * share);
                 const int i1 = min(n, i0 + share);
                 if (i0 == 0 && i1 > 0) {
-                    if (in) A = a.part_mid[(int64_t)slot_of(c0, gr) * D + col];
+                    if (in) A = a.part_mid[slot_of(c0, gr) * D + col];
                     i0 = 1;
                 }
                 A = add_rows(a.part_mid, 2 * ((int64_t)c0 + i0), 2, i1 - i0, A);

@@ -68,32 +68,36 @@ int main() {
     srand(1);
     for (int it = 0; it < 20000; ++it) {
         const int64_t G = 1 + rand() % 40, rpg = 1 + rand() % 50, rows = G * rpg;
-        const int64_t grid = 1 + rand() % (rows < 60 ? rows : 60);
+        const int64_t grid = 1 + rand() % (rows < 60 ? rows : 60), q = rows / grid, r = rows % grid;
         std::vector<int> written(2 * grid, -1);
-        if (first_row(0, grid, rows) != 0 || first_row(grid, grid, rows) != rows) return 1;
+        if (first_row(0, q, r) != 0 || first_row(grid, q, r) != rows) return 1;
+        // the second stage's own arithmetic: the CTA that takes row i
+        auto cta_of = [&](int64_t i) { return i < r * (q + 1) ? i / (q + 1) : r + (i - r * (q + 1)) / q; };
         for (int64_t c = 0; c < grid; ++c) {
-            const int64_t r0 = first_row(c, grid, rows), r1 = first_row(c + 1, grid, rows);
+            const int64_t r0 = first_row(c, q, r), r1 = first_row(c + 1, q, r);
             if (r1 <= r0) return 2;
             for (int64_t i = r0; i < r1; ++i) {
-                if (cta_of_row(i, grid, rows) != c) return 3;
+                if (cta_of(i) != c || gate_row(i, rpg) != i / rpg) return 3;
                 const int64_t gr = i / rpg;
                 if (gr * rpg >= r0 && (gr + 1) * rpg <= r1) continue;  // whole
-                const int64_t s = mid_slot(c, gr, grid, rows, rpg);
+                const int64_t s = mid_slot(c, gr, q, r, rpg);
                 if (s < 0 || s >= 2 * grid || (written[s] != -1 && written[s] != gr)) return 4;
                 written[s] = (int)gr;
             }
         }
         for (int64_t gr = 0; gr < G; ++gr) {  // the second stage finds every part
-            const int64_t c0 = cta_of_row(gr * rpg, grid, rows), c1 = cta_of_row((gr + 1) * rpg - 1, grid, rows);
+            const int64_t c0 = cta_of(gr * rpg), c1 = cta_of((gr + 1) * rpg - 1);
             if (c0 == c1) continue;
-            if (written[mid_slot(c0, gr, grid, rows, rpg)] != gr) return 5;
+            if (written[mid_slot(c0, gr, q, r, rpg)] != gr) return 5;
             for (int64_t c = c0 + 1; c <= c1; ++c) {
                 if (written[2 * c] != gr) return 6;
                 written[2 * c] = -1;
             }
-            written[mid_slot(c0, gr, grid, rows, rpg)] = -1;
+            written[mid_slot(c0, gr, q, r, rpg)] = -1;
         }
         for (int w : written) if (w != -1) return 7;  // and no part is left over
+        const int64_t big = ((int64_t)1 << 40) + rand(), per = 1 + rand();
+        if (gate_row(big, per) != big / per) return 8;
     }
     return 0;
 }
