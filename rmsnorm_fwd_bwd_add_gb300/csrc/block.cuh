@@ -356,8 +356,8 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
     int64_t group_end = a.gate && !per_row ? 0 : INT64_MAX;  // first row past the gate row held in m
     int s = 0;
     uint32_t ph = 0;
-    for (int64_t i = ry; i < deal.n; i += R) {
-        const int64_t row = deal.row(i);
+    for (int64_t ri = ry; ri < deal.n; ri += R) {
+        const int64_t row = deal.row(ri);
         if (row >= group_end) {
             const int64_t gr = gate_row(row, a.rows_per_gate);
             group_end = (gr + 1) * a.rows_per_gate;
@@ -411,21 +411,21 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
         if constexpr (KIND == BLOCK_WARP) {
             warp_sums<4>(sum);
         } else {
-            ok = cta_sums<4, MAXW>(sum, s_red[i & 1], nw, ok);
+            ok = cta_sums<4, MAXW>(sum, s_red[ri & 1], nw, ok);
         }
         if constexpr (KIND == BLOCK_STAGED) {
             if (!ok) {  // leave once this CTA's copies have landed
                 if (threadIdx.x == 0) {
                     atomicOr(a.status, DEVSTATUS_WAIT_TIMEOUT);
-                    for (int64_t k = i; k < deal.n && k < i + ring.S; ++k)
+                    for (int64_t k = ri; k < deal.n && k < ri + ring.S; ++k)
                         if (deal.row(k) != a.drop_row)
                             mbar_wait_bounded(&ring.full[k % ring.S], (uint32_t)((k / ring.S) & 1), DEFAULT_WAIT_BUDGET);
                 }
                 return;
             }
             // every thread has its units of this stage in registers
-            if (threadIdx.x == 0 && i + ring.S < deal.n)
-                ring_issue<T>(ring, a, src, ld, deal.row(i + ring.S), s, policy);
+            if (threadIdx.x == 0 && ri + ring.S < deal.n)
+                ring_issue<T>(ring, a, src, ld, deal.row(ri + ring.S), s, policy);
         }
         if constexpr (MAXT * MINB > 512) {  // 96 registers or fewer
 #pragma unroll
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
                 one[0] = group_sum<32>(one[0]);
             } else {
                 __syncthreads();  // this row's sums have been read
-                cta_sums<1, MAXW>(one, s_red[i & 1], nw, true);
+                cta_sums<1, MAXW>(one, s_red[ri & 1], nw, true);
             }
             ss = one[0];
         }
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
                 ph ^= 1u;
             }
         } else if constexpr (KIND == BLOCK_WARP) {
-            if (i + R < deal.n) fetch_global(deal.row(i + R));
+            if (ri + R < deal.n) fetch_global(deal.row(ri + R));
         }
     }
     griddep_launch_dependents();
@@ -651,8 +651,8 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
         const int64_t gr = per_row ? 0 : gate_row(deal.row(seg), a.rows_per_gate);
         const int64_t end = per_row || a.team ? deal.n : min(deal.n, (gr + 1) * a.rows_per_gate - deal.lo);
         if (a.gate && !per_row) load_m(static_cast<const T *>(a.gate) + gr * a.ld_gate);
-        for (int64_t i = seg + ry; i < end; i += R) {
-            const int64_t row = deal.row(i);
+        for (int64_t ri = seg + ry; ri < end; ri += R) {
+            const int64_t row = deal.row(ri);
             float r_y = 1.f, r_h = 0.f;
             if (saved) {
                 if (post) r_y = __ldg(a.rstd + row);
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                 const T *pga = per_row ? staged(a.gate, a.ld_gate) : nullptr;
                 ok = mbar_wait_bounded(&ring.full[s], ph, a.wait_budget);
                 fetch(py, phh, pgo, pgr, pga);
-            } else if (i != fetched) {
+            } else if (ri != fetched) {
                 fetch_global(row);
             }
             // m of unit j with the row's own gate
@@ -726,14 +726,14 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                 if (saved) warp_sums<4>(reinterpret_cast<float (&)[4]>(sum));
                 else warp_sums<6>(sum);
             } else {
-                ok = saved ? cta_sums<4, MAXW>(reinterpret_cast<float (&)[4]>(sum), s_red[i & 1], nw, ok)
-                           : cta_sums<6, MAXW>(sum, s_red[i & 1], nw, ok);
+                ok = saved ? cta_sums<4, MAXW>(reinterpret_cast<float (&)[4]>(sum), s_red[ri & 1], nw, ok)
+                           : cta_sums<6, MAXW>(sum, s_red[ri & 1], nw, ok);
             }
             if constexpr (KIND == BLOCK_STAGED) {
                 if (!ok) {
                     if (threadIdx.x == 0) {
                         atomicOr(a.status, DEVSTATUS_WAIT_TIMEOUT);
-                        for (int64_t k = i; k < deal.n && k < i + ring.S; ++k)
+                        for (int64_t k = ri; k < deal.n && k < ri + ring.S; ++k)
                             if (deal.row(k) != a.drop_row)
                                 mbar_wait_bounded(&ring.full[k % ring.S], (uint32_t)((k / ring.S) & 1),
                                                   DEFAULT_WAIT_BUDGET);
@@ -741,8 +741,8 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                     return;
                 }
                 // every thread has its slots of this stage in registers
-                if (threadIdx.x == 0 && i + ring.S < deal.n)
-                    ring_issue<T>(ring, a, src, ld, deal.row(i + ring.S), s, policy);
+                if (threadIdx.x == 0 && ri + ring.S < deal.n)
+                    ring_issue<T>(ring, a, src, ld, deal.row(ri + ring.S), s, policy);
             }
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                 }
             } else if constexpr (KIND == BLOCK_WARP) {
                 // the next gate row's rows are dealt out to the warps from its first on
-                fetched = i + R < end ? i + R : end + ry;
+                fetched = ri + R < end ? ri + R : end + ry;
                 if (fetched < deal.n) fetch_global(deal.row(fetched));
             }
         }

@@ -43,7 +43,6 @@ using namespace rmsn;
 constexpr int RX_NT = 256;
 constexpr int RX_CTAS_PER_SM = 2;
 constexpr int RX_MAX_DH = 1024;
-constexpr int RX_HEADS = 4;  // heads whose loads a lane keeps in flight
 constexpr unsigned int BAD_INDEX = RMSNORM_DEVSTATUS_BAD_INDEX;
 
 // One tensor [B, S, H, Dh]: strides in elements, Dh contiguous.
@@ -80,9 +79,60 @@ __device__ __forceinline__ float2 cos_sin(int64_t p, float2 f) {
     return cs;
 }
 
-// Interleaved layout: a unit is one vector (VE / 2 pairs); element kernels (VE =
-// 1) take the pair as two vectors one apart.  Half layout: two vectors rot / 2
-// apart (VE pairs).
+// A head as `lanes` work units, each VE elements from `a` on and, where a unit has two
+// vectors, VE more from `b` on: first its rotation units, then the copied rest.
+//   interleaved, VE > 1: a rotation unit is one vector (VE / 2 pairs), a copied one too;
+//   else: a rotation unit is two vectors whose elements are partners (half layout:
+//   rot / 2 apart; one-element vectors: neighbours), a copied unit two vectors half
+//   the copied part apart (the second may be past it).
+template <int VE, bool PAIRED, bool INTERLEAVED> struct HeadMap {
+    int rot_units, lanes, rest, tail, tail_units;
+    __device__ __forceinline__ HeadMap(int Dh, int rot, bool copies) {
+        rot_units = PAIRED ? rot / VE : rot / 2 / VE;
+        rest = rot;
+        tail = copies ? (Dh - rot) / VE : 0;  // vectors
+        tail_units = PAIRED ? tail : (tail + 1) / 2;
+        lanes = rot_units + tail_units;
+    }
+    __device__ __forceinline__ void at(int l, int &a, int &b, bool &two) const {
+        if (l < rot_units) {
+            a = PAIRED ? l * VE : INTERLEAVED ? 2 * l : l * VE;
+            b = INTERLEAVED ? a + 1 : a + rest / 2;
+            two = !PAIRED;
+        } else {
+            const int c = l - rot_units;
+            a = rest + c * VE;
+            b = a + tail_units * VE;
+            two = !PAIRED && c + tail_units < tail;
+        }
+    }
+};
+
+// float2 number m of a 16-byte vector.
+template <typename T> __device__ __forceinline__ float2 get_pair(const uint4 &v, int m) {
+    if constexpr (sizeof(T) == 2) return Cvt<T>::unpack2(m == 0 ? v.x : m == 1 ? v.y : m == 2 ? v.z : v.w);
+    else return m == 0 ? make_float2(__uint_as_float(v.x), __uint_as_float(v.y))
+                       : make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+template <typename T> __device__ __forceinline__ void put_pair(uint4 &v, int m, float2 f) {
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t w = Cvt<T>::pack2(f.x, f.y);
+        if (m == 0) v.x = w;
+        else if (m == 1) v.y = w;
+        else if (m == 2) v.z = w;
+        else v.w = w;
+    } else if (m == 0) {
+        v.x = __float_as_uint(f.x);
+        v.y = __float_as_uint(f.y);
+    } else {
+        v.z = __float_as_uint(f.x);
+        v.w = __float_as_uint(f.y);
+    }
+}
+
+// Heads whose loads a lane keeps in flight: eight vectors.
+template <bool PAIRED> __host__ __device__ constexpr int heads_in_flight() { return PAIRED ? 8 : 4; }
+
 template <typename T, int VB, bool INTERLEAVED>
 __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __grid_constant__ RopeExArgs a,
                                                                        int wpt) {
@@ -90,118 +140,132 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
     constexpr int VE = VB / (int)sizeof(T);
     constexpr bool PAIRED = INTERLEAVED && VE > 1;  // both halves of a pair in one vector
     constexpr int PPU = PAIRED ? VE / 2 : VE;       // pairs a unit
+    constexpr int PP = PAIRED || VE == 1 ? PPU : PPU / 2;  // float2 of cosines a unit
     constexpr bool PRECISE = sizeof(T) == 4;
+    constexpr int HB = heads_in_flight<PAIRED>();
     __shared__ float2 s_turns[RX_MAX_DH / 2];
     const int half = a.rot / 2;
     for (int i = threadIdx.x; i < half; i += RX_NT) s_turns[i] = a.turns[i];
     __syncthreads();
     griddep_wait();
 
+    // A warp covers `hpi` heads a step, a lane one unit of each head it meets: the
+    // heads of q, then of k, then of v, which has as many units, all copied.
     const int lane = threadIdx.x & 31;
-    const int units = half / PPU;
-    const int hpi = units >= 32 ? 1 : 32 / units;  // heads a warp covers a step
-    const int hs = units >= 32 ? 0 : lane / units;
-    const int H = a.Hq + a.Hkv;
+    const HeadMap<VE, PAIRED, INTERLEAVED> map(a.Dh, a.rot, true);
+    const HeadMap<VE, PAIRED, INTERLEAVED> v_map(a.Dh, 0, true);
+    const bool q_moves = a.q_out.p != a.q.p, k_moves = a.k_out.p != a.k.p;  // in place: nothing to copy
+    const int hpi = map.lanes >= 32 ? 1 : 32 / map.lanes;
+    const int hs = map.lanes >= 32 ? 0 : lane / map.lanes;
+    const int n_qk = a.Hq + a.Hkv, n_all = n_qk + (a.slots ? a.Hkv : 0);
     const int64_t n_items = a.T * wpt, n_warps = (int64_t)gridDim.x * (RX_NT / 32);
-    for (int64_t w = ((int64_t)blockIdx.x * RX_NT + threadIdx.x) >> 5; w < n_items; w += n_warps) {
-        const int64_t t = w / wpt;
-        const int part = (int)(w - t * wpt);
+    const int wshift = 31 - __clz(wpt);  // wpt is a power of two
+    int64_t w = ((int64_t)blockIdx.x * RX_NT + threadIdx.x) >> 5;
+    int64_t p_next = 0, slot_next = 0;  // of the item ahead, loaded one item early
+    auto look_ahead = [&](int64_t item) {
+        if (item < n_items) {
+            p_next = a.positions[item >> wshift];
+            if (a.slots) slot_next = a.slots[item >> wshift];
+        }
+    };
+    look_ahead(w);
+    for (; w < n_items; w += n_warps) {
+        const int64_t t = w >> wshift, p = p_next, slot = slot_next;
+        const int part = (int)(w & (wpt - 1));
+        look_ahead(w + n_warps);
         const int64_t b = a.S == a.T ? 0 : t / a.S, s = t - b * a.S;
-        const int64_t p = a.positions[t];
-        const int64_t slot = a.slots ? a.slots[t] : 0;
         const bool pos_ok = p >= 0, slot_ok = slot < a.num_slots;
         if ((!pos_ok || !slot_ok) && lane == 0 && part == 0) atomicOr(a.status, BAD_INDEX);
         if (!pos_ok) continue;
-        const bool kv = slot_ok && slot >= 0;
-        const int heads = kv ? H : a.Hq;  // q's, then k's
+        const int heads = slot_ok && slot >= 0 ? n_all : a.Hq;
+        // head h of its tensor is `stride` times h from its base
         const T *q = static_cast<const T *>(a.q.p) + b * a.q.sb + s * a.q.st;
-        const T *k = static_cast<const T *>(a.k.p) + b * a.k.sb + s * a.k.st;
+        const T *k = static_cast<const T *>(a.k.p) + b * a.k.sb + s * a.k.st - a.Hq * a.k.sh;
+        const T *v = static_cast<const T *>(a.v.p) + b * a.v.sb + s * a.v.st - n_qk * a.v.sh;
         T *qo = static_cast<T *>(const_cast<void *>(a.q_out.p)) + b * a.q_out.sb + s * a.q_out.st;
         T *ko = static_cast<T *>(const_cast<void *>(a.k_out.p)) +
-                (a.slots ? slot * a.k_out.st : b * a.k_out.sb + s * a.k_out.st);
-        auto src_of = [&](int h) -> const T * { return h < a.Hq ? q + h * a.q.sh : k + (h - a.Hq) * a.k.sh; };
-        auto dst_of = [&](int h) -> T * { return h < a.Hq ? qo + h * a.q_out.sh : ko + (h - a.Hq) * a.k_out.sh; };
-
-        for (int u0 = 0; u0 < units; u0 += 32) {
-            const int u = units >= 32 ? u0 + lane : lane - hs * units;
-            if (u >= units || hs >= hpi) continue;
-            float2 cs[PPU];
+                (a.slots ? slot * a.k_out.st : b * a.k_out.sb + s * a.k_out.st) - a.Hq * a.k_out.sh;
+        T *vo = static_cast<T *>(const_cast<void *>(a.v_out.p)) + slot * a.v_out.st - n_qk * a.v_out.sh;
+        float2 cs[PP], sn[PP];  // cosines and sines of the unit's pairs
+        for (int u0 = 0; u0 < map.lanes; u0 += 32) {
+            const int l = map.lanes >= 32 ? u0 + lane : lane - hs * map.lanes;
+            if (l >= map.lanes || hs >= hpi) continue;
+            int ia, ib, va, vb;
+            bool two, v_two;
+            map.at(l, ia, ib, two);
+            v_map.at(l, va, vb, v_two);
+            const bool turn = l < map.rot_units;
+            if (turn) {
 #pragma unroll
-            for (int m = 0; m < PPU; ++m) {
-                cs[m] = cos_sin<PRECISE>(p, s_turns[u * PPU + m]);
-                cs[m].x *= a.scale;
-                cs[m].y *= a.scale * a.sign;
+                for (int m = 0; m < PPU; ++m) {
+                    const float2 x = cos_sin<PRECISE>(p, s_turns[l * PPU + m]);
+                    const float cm = x.x * a.scale, sm = x.y * (a.scale * a.sign);
+                    if constexpr (PAIRED || VE == 1) {
+                        cs[m].x = cm;
+                        sn[m].x = sm;
+                    } else if (m & 1) {
+                        cs[m / 2].y = cm;
+                        sn[m / 2].y = sm;
+                    } else {
+                        cs[m / 2].x = cm;
+                        sn[m / 2].x = sm;
+                    }
+                }
             }
-            const int ia = PAIRED ? u * VE : INTERLEAVED ? 2 * u : u * VE;  // first element
-            const int ib = INTERLEAVED ? ia + 1 : ia + half;                // its partner (not PAIRED)
             const int step = wpt * hpi;
-            for (int h0 = part * hpi + hs; h0 < heads; h0 += RX_HEADS * step) {
-                V xa[RX_HEADS], xb[RX_HEADS];
+            // HB heads' loads ahead of their stores (heads never share an address, so
+            // in place too)
+            for (int h0 = part * hpi + hs; h0 < heads; h0 += HB * step) {
+                V xa[HB], xb[HB];
 #pragma unroll
-                for (int j = 0; j < RX_HEADS; ++j) {
+                for (int j = 0; j < HB; ++j) {
                     const int h = h0 + j * step;
-                    if (h < heads) {
-                        const T *sp = src_of(h);
-                        xa[j] = *reinterpret_cast<const V *>(sp + ia);
-                        if constexpr (!PAIRED) xb[j] = *reinterpret_cast<const V *>(sp + ib);
+                    if (h < heads && (turn || h >= n_qk || (h < a.Hq ? q_moves : k_moves))) {
+                        const T *src = h < a.Hq ? q + h * a.q.sh : h < n_qk ? k + h * a.k.sh : v + h * a.v.sh;
+                        xa[j] = *reinterpret_cast<const V *>(src + (h < n_qk ? ia : va));
+                        if constexpr (!PAIRED)
+                            if (h < n_qk ? two : v_two) xb[j] = *reinterpret_cast<const V *>(src + (h < n_qk ? ib : vb));
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < RX_HEADS; ++j) {
+                for (int j = 0; j < HB; ++j) {
                     const int h = h0 + j * step;
-                    if (h < heads) {
-                        T *dp = dst_of(h);
-                        float fa[VE], fb[VE], ga[VE], gb[VE];
-                        unpack_unit<T, VB>(xa[j], fa);
-                        if constexpr (PAIRED) {
+                    if (h < heads && (turn || h >= n_qk || (h < a.Hq ? q_moves : k_moves))) {
+                        if (turn && h < n_qk) {
+                            // word by word, so that no vector is unpacked whole
+                            constexpr int W = sizeof(T) == 2 ? 4 : 2;  // float2 a vector
+                            if constexpr (PAIRED) {                    // (a, b): one pair a float2
 #pragma unroll
-                            for (int m = 0; m < PPU; ++m) {
-                                ga[2 * m] = fa[2 * m] * cs[m].x - fa[2 * m + 1] * cs[m].y;
-                                ga[2 * m + 1] = fa[2 * m + 1] * cs[m].x + fa[2 * m] * cs[m].y;
-                            }
-                        } else {
-                            unpack_unit<T, VB>(xb[j], fb);
+                                for (int m = 0; m < W; ++m) {
+                                    const float2 f = get_pair<T>(xa[j], m);
+                                    put_pair<T>(xa[j], m, make_float2(fmaf(-f.y, sn[m].x, f.x * cs[m].x),
+                                                                      fmaf(f.x, sn[m].x, f.y * cs[m].x)));
+                                }
+                            } else if constexpr (VE > 1) {  // two pairs: first elements in xa, second ones in xb
 #pragma unroll
-                            for (int m = 0; m < PPU; ++m) {
-                                ga[m] = fa[m] * cs[m].x - fb[m] * cs[m].y;
-                                gb[m] = fb[m] * cs[m].x + fa[m] * cs[m].y;
+                                for (int m = 0; m < W; ++m) {
+                                    const float2 f = get_pair<T>(xa[j], m), g = get_pair<T>(xb[j], m);
+                                    const float2 fc = f2mul(f, cs[m]);
+                                    put_pair<T>(xa[j], m, make_float2(fmaf(-g.x, sn[m].x, fc.x), fmaf(-g.y, sn[m].y, fc.y)));
+                                    put_pair<T>(xb[j], m, f2fma(f, sn[m], f2mul(g, cs[m])));
+                                }
+                            } else {
+                                float f[1], g[1], o[1], r[1];
+                                unpack_unit<T, VB>(xa[j], f);
+                                unpack_unit<T, VB>(xb[j], g);
+                                o[0] = f[0] * cs[0].x - g[0] * sn[0].x;
+                                r[0] = g[0] * cs[0].x + f[0] * sn[0].x;
+                                xa[j] = pack_unit<T, VB>(o);
+                                xb[j] = pack_unit<T, VB>(r);
                             }
-                            *reinterpret_cast<V *>(dp + ib) = pack_unit<T, VB>(gb);
                         }
-                        *reinterpret_cast<V *>(dp + ia) = pack_unit<T, VB>(ga);
+                        T *dst = h < a.Hq ? qo + h * a.q_out.sh : h < n_qk ? ko + h * a.k_out.sh : vo + h * a.v_out.sh;
+                        *reinterpret_cast<V *>(dst + (h < n_qk ? ia : va)) = xa[j];
+                        if constexpr (!PAIRED)
+                            if (h < n_qk ? two : v_two) *reinterpret_cast<V *>(dst + (h < n_qk ? ib : vb)) = xb[j];
                     }
                 }
             }
-        }
-        // Vectors [c0, c1) of heads [h_lo, h_hi) copied unchanged.
-        auto copy_heads = [&](auto from, auto to, int h_lo, int h_hi, int c0, int c1) {
-            const int nv = c1 - c0;
-            if (nv <= 0) return;
-            const int chp = nv >= 32 ? 1 : 32 / nv;
-            const int ch = nv >= 32 ? 0 : lane / nv;
-            if (ch >= chp) return;
-            for (int c = nv >= 32 ? lane : lane - ch * nv; c < nv; c += 32) {
-                const int off = (c0 + c) * VE, step = wpt * chp;
-                for (int h0 = h_lo + part * chp + ch; h0 < h_hi; h0 += RX_HEADS * step) {
-                    V x[RX_HEADS];
-#pragma unroll
-                    for (int j = 0; j < RX_HEADS; ++j)
-                        if (h0 + j * step < h_hi) x[j] = *reinterpret_cast<const V *>(from(h0 + j * step) + off);
-#pragma unroll
-                    for (int j = 0; j < RX_HEADS; ++j)
-                        if (h0 + j * step < h_hi) *reinterpret_cast<V *>(to(h0 + j * step) + off) = x[j];
-                }
-            }
-        };
-        if (a.rot < a.Dh) {
-            const bool q_moves = a.q_out.p != a.q.p, k_moves = a.k_out.p != a.k.p;
-            copy_heads(src_of, dst_of, q_moves ? 0 : a.Hq, k_moves ? heads : a.Hq, a.rot / VE, a.Dh / VE);
-        }
-        if (a.slots && kv) {
-            const T *v = static_cast<const T *>(a.v.p) + b * a.v.sb + s * a.v.st;
-            T *vo = static_cast<T *>(const_cast<void *>(a.v_out.p)) + slot * a.v_out.st;
-            copy_heads([&](int h) { return v + h * a.v.sh; }, [&](int h) { return vo + h * a.v_out.sh; }, 0,
-                       a.Hkv, 0, a.Dh / VE);
         }
     }
     griddep_launch_dependents();
@@ -215,9 +279,25 @@ cudaError_t launch_layout(const RopeExArgs &a, bool interleaved, int grid, int w
 
 template <typename T>
 cudaError_t launch_type(const RopeExArgs &a, bool interleaved, bool vec, int sm, cudaStream_t s) {
-    // warps a token: a few tokens are spread over up to eight warps each
+    // Warps a token.  Each of them computes the token's angles again, about half a
+    // trip to memory, and makes a trip for every few heads; all warps go through
+    // equal rounds of tokens' parts.
     const int64_t resident = (int64_t)sm * RX_CTAS_PER_SM, warps = resident * (RX_NT / 32);
-    const int wpt = (int)std::max<int64_t>(1, std::min<int64_t>(8, warps / a.T));
+    const int ve = vec ? 16 / (int)sizeof(T) : 1;
+    const bool paired = interleaved && ve > 1;
+    const int lanes = paired ? a.Dh / ve : (a.Dh / ve + 1) / 2, hpi = std::max(1, 32 / lanes);
+    const int per_trip = hpi * (paired ? heads_in_flight<true>() : heads_in_flight<false>());
+    const int heads = a.Hq + a.Hkv * (a.slots ? 2 : 1);
+    int wpt = 1;
+    int64_t best = INT64_MAX;
+    for (int k = 1; k <= 8; k *= 2) {
+        const int64_t rounds = (a.T * k + warps - 1) / warps, trips = (heads + per_trip * k - 1) / (per_trip * k);
+        const int64_t cost = rounds * (1 + 2 * trips * ((lanes + 31) / 32));
+        if (cost < best) {
+            best = cost;
+            wpt = k;
+        }
+    }
     const int grid = (int)std::min<int64_t>((a.T * wpt + RX_NT / 32 - 1) / (RX_NT / 32), resident);
     return vec ? launch_layout<T, 16>(a, interleaved, grid, wpt, s)
                : launch_layout<T, (int)sizeof(T)>(a, interleaved, grid, wpt, s);
