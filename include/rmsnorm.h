@@ -366,7 +366,8 @@ int rmsnorm_rope_kv_append(const void *q, const void *k, const void *v,
  *                them (or any finite ones of up to 10^6).
  *   interleaved  0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1).
  * fp16, bf16 or fp32; arithmetic in fp32, angles to about 1e-8 turns up to
- * positions of 10^7, each output rounded once.  rot_dim even, at most Dh; Dh at most 1024.
+ * positions of 10^7, each output rounded once.  rot_dim even, at most Dh; Dh at
+ * most 1024; head strides below 4 GB.
  * Strides and pointers in multiples of 16 bytes, with rot_dim and Dh in whole
  * vectors, take the vectorised kernel.  A negative position is detected on the
  * device: that token is skipped and RMSNORM_DEVSTATUS_BAD_INDEX is set.

@@ -45,10 +45,12 @@ constexpr int RX_CTAS_PER_SM = 2;
 constexpr int RX_MAX_DH = 1024;
 constexpr unsigned int BAD_INDEX = RMSNORM_DEVSTATUS_BAD_INDEX;
 
-// One tensor [B, S, H, Dh]: strides in elements, Dh contiguous.
+// One tensor [B, S, H, Dh]: strides in elements, Dh contiguous; and the head stride
+// in bytes, below 2^32, so that a head's address is one multiply-add.
 struct Heads {
     const void *p;
     int64_t sb, st, sh;
+    uint32_t head_bytes;
 };
 
 struct RopeExArgs {
@@ -79,40 +81,43 @@ __device__ __forceinline__ float2 cos_sin(int64_t p, float2 f) {
     return cs;
 }
 
-// A head as `lanes` work units, each VE elements from `a` on and, where a unit has two
-// vectors, VE more from `b` on: first its rotation units, then the copied rest.
-//   interleaved, VE > 1: a rotation unit is one vector (VE / 2 pairs), a copied one too;
-//   else: a rotation unit is two vectors whose elements are partners (half layout:
-//   rot / 2 apart; one-element vectors: neighbours), a copied unit two vectors half
-//   the copied part apart (the second may be past it).
+// A head as `lanes` work units of two vectors, VE elements from `a` on and VE from `b`
+// on (`two`: the second is there): first its rotation units, then the copied rest.
+//   half layout (and one-element vectors): the two vectors' elements are partners.
+//   interleaved, VE > 1: partners sit side by side in each of the two, which are half
+//   the rotated part apart, as the copied ones are half the copied part apart.
 template <int VE, bool PAIRED, bool INTERLEAVED> struct HeadMap {
-    int rot_units, lanes, rest, tail, tail_units;
-    __device__ __forceinline__ HeadMap(int Dh, int rot, bool copies) {
-        rot_units = PAIRED ? rot / VE : rot / 2 / VE;
-        rest = rot;
-        tail = copies ? (Dh - rot) / VE : 0;  // vectors
-        tail_units = PAIRED ? tail : (tail + 1) / 2;
+    int rot_units, lanes, rot, tail, tail_units;
+    __host__ __device__ __forceinline__ HeadMap(int Dh, int rot_) {
+        rot = rot_;
+        rot_units = PAIRED ? (rot / VE + 1) / 2 : rot / 2 / VE;
+        tail = (Dh - rot) / VE;  // vectors
+        tail_units = (tail + 1) / 2;
         lanes = rot_units + tail_units;
     }
     __device__ __forceinline__ void at(int l, int &a, int &b, bool &two) const {
         if (l < rot_units) {
-            a = PAIRED ? l * VE : INTERLEAVED ? 2 * l : l * VE;
-            b = INTERLEAVED ? a + 1 : a + rest / 2;
-            two = !PAIRED;
+            a = !PAIRED && INTERLEAVED ? 2 * l : l * VE;
+            b = PAIRED ? a + rot_units * VE : INTERLEAVED ? a + 1 : a + rot / 2;
+            two = !PAIRED || b < rot;
         } else {
             const int c = l - rot_units;
-            a = rest + c * VE;
+            a = rot + c * VE;
             b = a + tail_units * VE;
-            two = !PAIRED && c + tail_units < tail;
+            two = c + tail_units < tail;
         }
     }
 };
 
-// float2 number m of a 16-byte vector.
+// float2 number m of a vector.
 template <typename T> __device__ __forceinline__ float2 get_pair(const uint4 &v, int m) {
     if constexpr (sizeof(T) == 2) return Cvt<T>::unpack2(m == 0 ? v.x : m == 1 ? v.y : m == 2 ? v.z : v.w);
     else return m == 0 ? make_float2(__uint_as_float(v.x), __uint_as_float(v.y))
                        : make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+template <typename T> __device__ __forceinline__ float2 get_pair(uint32_t v, int) { return Cvt<T>::unpack2(v); }
+template <typename T> __device__ __forceinline__ void put_pair(uint32_t &v, int, float2 f) {
+    v = Cvt<T>::pack2(f.x, f.y);
 }
 template <typename T> __device__ __forceinline__ void put_pair(uint4 &v, int m, float2 f) {
     if constexpr (sizeof(T) == 2) {
@@ -130,19 +135,21 @@ template <typename T> __device__ __forceinline__ void put_pair(uint4 &v, int m, 
     }
 }
 
-// Heads whose loads a lane keeps in flight: eight vectors.
-template <bool PAIRED> __host__ __device__ constexpr int heads_in_flight() { return PAIRED ? 8 : 4; }
+// Heads whose loads a lane keeps in flight, two vectors each: with smaller vectors,
+// more of them.
+template <int VB> __host__ __device__ constexpr int heads_in_flight() { return VB == 16 ? 4 : 8; }
 
-template <typename T, int VB, bool INTERLEAVED>
+// wpt: warps a token; cw: units of a head a warp takes at a time.
+// APPEND: k and v go to cache rows.
+template <typename T, int VB, bool INTERLEAVED, bool APPEND>
 __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __grid_constant__ RopeExArgs a,
-                                                                       int wpt) {
+                                                                       int wpt, int cw) {
     using V = typename RawUnit<VB>::type;
     constexpr int VE = VB / (int)sizeof(T);
     constexpr bool PAIRED = INTERLEAVED && VE > 1;  // both halves of a pair in one vector
-    constexpr int PPU = PAIRED ? VE / 2 : VE;       // pairs a unit
-    constexpr int PP = PAIRED || VE == 1 ? PPU : PPU / 2;  // float2 of cosines a unit
+    constexpr int PP = VE;  // pairs a unit: float2 of cosines and of sines hold PP of them
     constexpr bool PRECISE = sizeof(T) == 4;
-    constexpr int HB = heads_in_flight<PAIRED>();
+    constexpr int HB = heads_in_flight<VB>();
     __shared__ float2 s_turns[RX_MAX_DH / 2];
     const int half = a.rot / 2;
     for (int i = threadIdx.x; i < half; i += RX_NT) s_turns[i] = a.turns[i];
@@ -150,14 +157,13 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
     griddep_wait();
 
     // A warp covers `hpi` heads a step, a lane one unit of each head it meets: the
-    // heads of q, then of k, then of v, which has as many units, all copied.
+    // heads of q, then of k, then of v, which has no more units, all copied.
     const int lane = threadIdx.x & 31;
-    const HeadMap<VE, PAIRED, INTERLEAVED> map(a.Dh, a.rot, true);
-    const HeadMap<VE, PAIRED, INTERLEAVED> v_map(a.Dh, 0, true);
+    const HeadMap<VE, PAIRED, INTERLEAVED> map(a.Dh, a.rot);
+    const HeadMap<VE, PAIRED, INTERLEAVED> v_map(a.Dh, 0);
     const bool q_moves = a.q_out.p != a.q.p, k_moves = a.k_out.p != a.k.p;  // in place: nothing to copy
-    const int hpi = map.lanes >= 32 ? 1 : 32 / map.lanes;
-    const int hs = map.lanes >= 32 ? 0 : lane / map.lanes;
-    const int n_qk = a.Hq + a.Hkv, n_all = n_qk + (a.slots ? a.Hkv : 0);
+    const int hpi = 32 / cw, hs = lane / cw, lu = lane - hs * cw;
+    const int n_qk = a.Hq + a.Hkv, n_all = n_qk + (APPEND ? a.Hkv : 0);
     const int64_t n_items = a.T * wpt, n_warps = (int64_t)gridDim.x * (RX_NT / 32);
     const int wshift = 31 - __clz(wpt);  // wpt is a power of two
     int64_t w = ((int64_t)blockIdx.x * RX_NT + threadIdx.x) >> 5;
@@ -165,7 +171,7 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
     auto look_ahead = [&](int64_t item) {
         if (item < n_items) {
             p_next = a.positions[item >> wshift];
-            if (a.slots) slot_next = a.slots[item >> wshift];
+            if constexpr (APPEND) slot_next = a.slots[item >> wshift];
         }
     };
     look_ahead(w);
@@ -174,36 +180,47 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
         const int part = (int)(w & (wpt - 1));
         look_ahead(w + n_warps);
         const int64_t b = a.S == a.T ? 0 : t / a.S, s = t - b * a.S;
-        const bool pos_ok = p >= 0, slot_ok = slot < a.num_slots;
+        const bool pos_ok = p >= 0, slot_ok = !APPEND || slot < a.num_slots;
         if ((!pos_ok || !slot_ok) && lane == 0 && part == 0) atomicOr(a.status, BAD_INDEX);
         if (!pos_ok) continue;
-        const int heads = slot_ok && slot >= 0 ? n_all : a.Hq;
-        // head h of its tensor is `stride` times h from its base
-        const T *q = static_cast<const T *>(a.q.p) + b * a.q.sb + s * a.q.st;
-        const T *k = static_cast<const T *>(a.k.p) + b * a.k.sb + s * a.k.st - a.Hq * a.k.sh;
-        const T *v = static_cast<const T *>(a.v.p) + b * a.v.sb + s * a.v.st - n_qk * a.v.sh;
-        T *qo = static_cast<T *>(const_cast<void *>(a.q_out.p)) + b * a.q_out.sb + s * a.q_out.st;
-        T *ko = static_cast<T *>(const_cast<void *>(a.k_out.p)) +
-                (a.slots ? slot * a.k_out.st : b * a.k_out.sb + s * a.k_out.st) - a.Hq * a.k_out.sh;
-        T *vo = static_cast<T *>(const_cast<void *>(a.v_out.p)) + slot * a.v_out.st - n_qk * a.v_out.sh;
-        float2 cs[PP], sn[PP];  // cosines and sines of the unit's pairs
-        for (int u0 = 0; u0 < map.lanes; u0 += 32) {
-            const int l = map.lanes >= 32 ? u0 + lane : lane - hs * map.lanes;
+        const int heads = !APPEND || (slot_ok && slot >= 0) ? n_all : a.Hq;
+        // where heads 0 would be, counted through the list: q's, k's, v's
+        auto place = [&](const Heads &x, int64_t row, bool batched, int before) {
+            return (unsigned char *)x.p + ((batched ? b * x.sb + s * x.st : row * x.st) * (int64_t)sizeof(T) -
+                                           (int64_t)before * x.head_bytes);
+        };
+        const unsigned char *q = place(a.q, 0, true, 0), *k = place(a.k, 0, true, a.Hq);
+        const unsigned char *v = APPEND ? place(a.v, 0, true, n_qk) : nullptr;
+        unsigned char *qo = place(a.q_out, 0, true, 0), *ko = place(a.k_out, slot, !APPEND, a.Hq);
+        unsigned char *vo = APPEND ? place(a.v_out, slot, false, n_qk) : nullptr;
+        auto head = [&](int h, const unsigned char *x0, const Heads &x, const unsigned char *y0, const Heads &y,
+                        const unsigned char *z0, const Heads &z) {
+            const unsigned char *base = h < a.Hq ? x0 : y0;
+            uint32_t sh = h < a.Hq ? x.head_bytes : y.head_bytes;
+            if (APPEND && h >= n_qk) {
+                base = z0;
+                sh = z.head_bytes;
+            }
+            return base + (uint64_t)(uint32_t)h * sh;
+        };
+        constexpr int PF = (PP + 1) / 2;
+        float2 cs[PF], sn[PF];  // cosines and sines of the unit's pairs
+        for (int u0 = 0; u0 < map.lanes; u0 += cw) {
+            const int l = u0 + lu;
             if (l >= map.lanes || hs >= hpi) continue;
             int ia, ib, va, vb;
             bool two, v_two;
             map.at(l, ia, ib, two);
             v_map.at(l, va, vb, v_two);
-            const bool turn = l < map.rot_units;
+            const bool turn = l < map.rot_units, copies_v = l < v_map.lanes;
             if (turn) {
 #pragma unroll
-                for (int m = 0; m < PPU; ++m) {
-                    const float2 x = cos_sin<PRECISE>(p, s_turns[l * PPU + m]);
+                for (int m = 0; m < PP; ++m) {
+                    // pairs of the first vector, then (PAIRED) of the second
+                    const int pair = !PAIRED ? l * PP + m : m < PP / 2 ? ia / 2 + m : min(ib / 2 + m - PP / 2, half - 1);
+                    const float2 x = cos_sin<PRECISE>(p, s_turns[pair]);
                     const float cm = x.x * a.scale, sm = x.y * (a.scale * a.sign);
-                    if constexpr (PAIRED || VE == 1) {
-                        cs[m].x = cm;
-                        sn[m].x = sm;
-                    } else if (m & 1) {
+                    if (m & 1) {
                         cs[m / 2].y = cm;
                         sn[m / 2].y = sm;
                     } else {
@@ -217,30 +234,39 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
             // in place too)
             for (int h0 = part * hpi + hs; h0 < heads; h0 += HB * step) {
                 V xa[HB], xb[HB];
+                auto wanted = [&](int h) {
+                    if (APPEND && h >= n_qk) return h < heads && (!PAIRED || copies_v);
+                    return h < heads && (turn || (h < a.Hq ? q_moves : k_moves));
+                };
 #pragma unroll
                 for (int j = 0; j < HB; ++j) {
                     const int h = h0 + j * step;
-                    if (h < heads && (turn || h >= n_qk || (h < a.Hq ? q_moves : k_moves))) {
-                        const T *src = h < a.Hq ? q + h * a.q.sh : h < n_qk ? k + h * a.k.sh : v + h * a.v.sh;
-                        xa[j] = *reinterpret_cast<const V *>(src + (h < n_qk ? ia : va));
-                        if constexpr (!PAIRED)
-                            if (h < n_qk ? two : v_two) xb[j] = *reinterpret_cast<const V *>(src + (h < n_qk ? ib : vb));
+                    if (wanted(h)) {
+                        const bool qk = !APPEND || h < n_qk;
+                        const T *src = reinterpret_cast<const T *>(head(h, q, a.q, k, a.k, v, a.v));
+                        xa[j] = *reinterpret_cast<const V *>(src + (qk ? ia : va));
+                        if (qk ? two : v_two) xb[j] = *reinterpret_cast<const V *>(src + (qk ? ib : vb));
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < HB; ++j) {
                     const int h = h0 + j * step;
-                    if (h < heads && (turn || h >= n_qk || (h < a.Hq ? q_moves : k_moves))) {
-                        if (turn && h < n_qk) {
+                    if (wanted(h)) {
+                        if (turn && (!APPEND || h < n_qk)) {
                             // word by word, so that no vector is unpacked whole
-                            constexpr int W = sizeof(T) == 2 ? 4 : 2;  // float2 a vector
+                            constexpr int W = VB / 2 / (int)sizeof(T);  // float2 a vector
                             if constexpr (PAIRED) {                    // (a, b): one pair a float2
+                                auto pairs = [&](V &x, int from) {
 #pragma unroll
-                                for (int m = 0; m < W; ++m) {
-                                    const float2 f = get_pair<T>(xa[j], m);
-                                    put_pair<T>(xa[j], m, make_float2(fmaf(-f.y, sn[m].x, f.x * cs[m].x),
-                                                                      fmaf(f.x, sn[m].x, f.y * cs[m].x)));
-                                }
+                                    for (int m = 0; m < W; ++m) {
+                                        const float c = (from + m) & 1 ? cs[(from + m) / 2].y : cs[(from + m) / 2].x;
+                                        const float s1 = (from + m) & 1 ? sn[(from + m) / 2].y : sn[(from + m) / 2].x;
+                                        const float2 f = get_pair<T>(x, m);
+                                        put_pair<T>(x, m, make_float2(fmaf(-f.y, s1, f.x * c), fmaf(f.x, s1, f.y * c)));
+                                    }
+                                };
+                                pairs(xa[j], 0);
+                                if (two) pairs(xb[j], W);
                             } else if constexpr (VE > 1) {  // two pairs: first elements in xa, second ones in xb
 #pragma unroll
                                 for (int m = 0; m < W; ++m) {
@@ -259,10 +285,10 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
                                 xb[j] = pack_unit<T, VB>(r);
                             }
                         }
-                        T *dst = h < a.Hq ? qo + h * a.q_out.sh : h < n_qk ? ko + h * a.k_out.sh : vo + h * a.v_out.sh;
-                        *reinterpret_cast<V *>(dst + (h < n_qk ? ia : va)) = xa[j];
-                        if constexpr (!PAIRED)
-                            if (h < n_qk ? two : v_two) *reinterpret_cast<V *>(dst + (h < n_qk ? ib : vb)) = xb[j];
+                        const bool qk = !APPEND || h < n_qk;
+                        T *dst = reinterpret_cast<T *>(const_cast<unsigned char *>(head(h, qo, a.q_out, ko, a.k_out, vo, a.v_out)));
+                        *reinterpret_cast<V *>(dst + (qk ? ia : va)) = xa[j];
+                        if (qk ? two : v_two) *reinterpret_cast<V *>(dst + (qk ? ib : vb)) = xb[j];
                     }
                 }
             }
@@ -271,36 +297,43 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
     griddep_launch_dependents();
 }
 
-template <typename T, int VB>
-cudaError_t launch_layout(const RopeExArgs &a, bool interleaved, int grid, int wpt, cudaStream_t s) {
-    return interleaved ? launch_pdl(rope_ex_kernel<T, VB, true>, dim3(grid), dim3(RX_NT), 0, s, a, wpt)
-                       : launch_pdl(rope_ex_kernel<T, VB, false>, dim3(grid), dim3(RX_NT), 0, s, a, wpt);
-}
-
-template <typename T>
-cudaError_t launch_type(const RopeExArgs &a, bool interleaved, bool vec, int sm, cudaStream_t s) {
-    // Warps a token.  Each of them computes the token's angles again, about half a
-    // trip to memory, and makes a trip for every few heads; all warps go through
-    // equal rounds of tokens' parts.
+template <typename T, int VB, bool INTERLEAVED>
+cudaError_t launch_layout(const RopeExArgs &a, int sm, cudaStream_t s) {
+    // Warps a token (k) and units a step (c).  Each warp computes its units' angles,
+    // about half a trip to memory, and makes a trip for every few heads; all warps go
+    // through equal rounds of tokens' parts.
     const int64_t resident = (int64_t)sm * RX_CTAS_PER_SM, warps = resident * (RX_NT / 32);
-    const int ve = vec ? 16 / (int)sizeof(T) : 1;
-    const bool paired = interleaved && ve > 1;
-    const int lanes = paired ? a.Dh / ve : (a.Dh / ve + 1) / 2, hpi = std::max(1, 32 / lanes);
-    const int per_trip = hpi * (paired ? heads_in_flight<true>() : heads_in_flight<false>());
+    constexpr int VE = VB / (int)sizeof(T);
+    const int lanes = HeadMap<VE, (INTERLEAVED && VE > 1), INTERLEAVED>(a.Dh, a.rot).lanes;
     const int heads = a.Hq + a.Hkv * (a.slots ? 2 : 1);
-    int wpt = 1;
+    int wpt = 1, cw = 1;
     int64_t best = INT64_MAX;
-    for (int k = 1; k <= 8; k *= 2) {
-        const int64_t rounds = (a.T * k + warps - 1) / warps, trips = (heads + per_trip * k - 1) / (per_trip * k);
-        const int64_t cost = rounds * (1 + 2 * trips * ((lanes + 31) / 32));
-        if (cost < best) {
-            best = cost;
-            wpt = k;
+    for (int steps = (lanes + 31) / 32; steps <= 12; ++steps) {
+        const int c = (lanes + steps - 1) / steps;  // a head in `steps` equal steps
+        for (int k = 1; k <= 8; k *= 2) {
+            const int per_trip = (32 / c) * heads_in_flight<VB>() * k;
+            const int64_t rounds = (a.T * k + warps - 1) / warps, trips = (heads + per_trip - 1) / per_trip;
+            const int64_t cost = rounds * (1 + (1 + 2 * trips) * steps);
+            if (cost < best) {
+                best = cost;
+                wpt = k;
+                cw = c;
+            }
         }
+        if (c == 1) break;
     }
     const int grid = (int)std::min<int64_t>((a.T * wpt + RX_NT / 32 - 1) / (RX_NT / 32), resident);
-    return vec ? launch_layout<T, 16>(a, interleaved, grid, wpt, s)
-               : launch_layout<T, (int)sizeof(T)>(a, interleaved, grid, wpt, s);
+    return launch_pdl(a.slots ? rope_ex_kernel<T, VB, INTERLEAVED, true> : rope_ex_kernel<T, VB, INTERLEAVED, false>,
+                      dim3(grid), dim3(RX_NT), 0, s, a, wpt, cw);
+}
+
+// unit: bytes that divide every address, stride and length.
+template <typename T>
+cudaError_t launch_type(const RopeExArgs &a, bool interleaved, int unit, int sm, cudaStream_t s) {
+    if (unit == 16) return interleaved ? launch_layout<T, 16, true>(a, sm, s) : launch_layout<T, 16, false>(a, sm, s);
+    if constexpr (sizeof(T) == 2)
+        if (unit < 4) return interleaved ? launch_layout<T, 2, true>(a, sm, s) : launch_layout<T, 2, false>(a, sm, s);
+    return interleaved ? launch_layout<T, 4, true>(a, sm, s) : launch_layout<T, 4, false>(a, sm, s);
 }
 
 // A [B, S, H, Dh] operand: whether its strides are usable, the bytes it spans,
@@ -321,6 +354,7 @@ int span_of(const Heads &h, int64_t B, int64_t S, int64_t H, int64_t Dh, int es,
     *out = Span{0, 0, Mat{nullptr, 0}, 0};
     if (!h.p || B * S == 0 || H == 0) return RMSNORM_OK;
     if (!elem_aligned(h.p, es) || h.sb < 0 || h.st < 0 || h.sh < 0) return RMSNORM_ERR_INVALID_ARG;
+    if (H > 1 && h.sh > (int64_t)UINT32_MAX / es) return RMSNORM_ERR_UNSUPPORTED;
     int64_t last = Dh - 1;
     if (!safe_mul_add(B, h.sb, &last) || !safe_mul_add(S, h.st, &last) || !safe_mul_add(H, h.sh, &last))
         return RMSNORM_ERR_UNSUPPORTED;
@@ -366,14 +400,17 @@ bool same_place(const Heads &a, const Heads &b, int64_t B, int64_t S, int64_t H)
     return a.p == b.p && (B <= 1 || a.sb == b.sb) && (S <= 1 || a.st == b.st) && (H <= 1 || a.sh == b.sh);
 }
 
-bool vec_ok(const Heads &h, int64_t B, int64_t S, int64_t H, int es) {
-    return !h.p || (aligned16(h.p) && (B <= 1 || h.sb * es % 16 == 0) && (S <= 1 || h.st * es % 16 == 0) &&
-                    (H <= 1 || h.sh * es % 16 == 0));
+// The bits of every address and stride in bytes.
+uintptr_t byte_bits(const Heads &h, int64_t B, int64_t S, int64_t H, int es) {
+    if (!h.p) return 0;
+    return (uintptr_t)h.p | (uintptr_t)((B > 1 ? h.sb : 0) * es) | (uintptr_t)((S > 1 ? h.st : 0) * es) |
+           (uintptr_t)((H > 1 ? h.sh : 0) * es);
 }
 
-Heads heads(const void *p, const int64_t *st, int n) {
+Heads heads(const void *p, const int64_t *st, int n, int es) {
     // n = 3: batch, token, head; n = 2: token, head
-    return p && st ? Heads{p, n == 3 ? st[0] : 0, st[n - 2], st[n - 1]} : Heads{nullptr, 0, 0, 0};
+    return p && st ? Heads{p, n == 3 ? st[0] : 0, st[n - 2], st[n - 1], (uint32_t)(st[n - 1] * es)}
+                   : Heads{nullptr, 0, 0, 0, 0};
 }
 
 // Checks, plans and launches; slots null: k_out has k's tokens.
@@ -429,14 +466,17 @@ int rope_run(const Heads &q, const Heads &k, const Heads &v, const int64_t *posi
     a.scale = attn_scale;
     a.sign = inverse ? -1.f : 1.f;
     a.status = status;
-    const int ve = 16 / es;
-    const bool vec = (interleaved ? rot : rot / 2) % ve == 0 && Dh % ve == 0 && vec_ok(q, B, S, Hq, es) &&
-                     vec_ok(q_out, B, S, Hq, es) && vec_ok(k, B, S, Hkv, es) && vec_ok(v, B, S, Hkv, es) &&
-                     vec_ok(k_out, cb, cs, Hkv, es) && vec_ok(v_out, cb, cs, Hkv, es);
+    // the widest vectors that divide all of it, the rotated part's halves (half
+    // layout) or whole (interleaved) and the head
+    const uintptr_t bits = byte_bits(q, B, S, Hq, es) | byte_bits(q_out, B, S, Hq, es) |
+                           byte_bits(k, B, S, Hkv, es) | byte_bits(v, B, S, Hkv, es) |
+                           byte_bits(k_out, cb, cs, Hkv, es) | byte_bits(v_out, cb, cs, Hkv, es) |
+                           (uintptr_t)((interleaved ? rot : rot / 2) * es) | (uintptr_t)(Dh * es);
+    const int unit = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == RMSNORM_F16    ? launch_type<__half>(a, interleaved, vec, sm, s)
-                          : dtype == RMSNORM_BF16 ? launch_type<__nv_bfloat16>(a, interleaved, vec, sm, s)
-                                                  : launch_type<float>(a, interleaved, vec, sm, s);
+    const cudaError_t e = dtype == RMSNORM_F16    ? launch_type<__half>(a, interleaved, unit, sm, s)
+                          : dtype == RMSNORM_BF16 ? launch_type<__nv_bfloat16>(a, interleaved, unit, sm, s)
+                                                  : launch_type<float>(a, interleaved, unit, sm, s);
     return e == cudaSuccess ? RMSNORM_OK : record_cuda_error(e);
 }
 
@@ -467,10 +507,11 @@ extern "C" int rmsnorm_rope(const void *q, const int64_t *q_strides, const void 
     if (!positions || (Hq > 0 && (!q || !q_out || !q_strides || !q_out_strides)) ||
         (Hkv > 0 && (!k || !k_out || !k_strides || !k_out_strides)))
         return RMSNORM_ERR_INVALID_ARG;
-    const Heads none{nullptr, 0, 0, 0};
-    return rope_run(Hq ? heads(q, q_strides, 3) : none, Hkv ? heads(k, k_strides, 3) : none, none, positions,
-                    nullptr, Hq ? heads(q_out, q_out_strides, 3) : none,
-                    Hkv ? heads(k_out, k_out_strides, 3) : none, none, inv_freq, attn_scale, interleaved,
+    const Heads none{nullptr, 0, 0, 0, 0};
+    const int es = esize_of(dtype);
+    return rope_run(Hq ? heads(q, q_strides, 3, es) : none, Hkv ? heads(k, k_strides, 3, es) : none, none, positions,
+                    nullptr, Hq ? heads(q_out, q_out_strides, 3, es) : none,
+                    Hkv ? heads(k_out, k_out_strides, 3, es) : none, none, inv_freq, attn_scale, interleaved,
                     inverse, B, S, Hq, Hkv, Dh, rot_dim, 0, dtype, stream);
 }
 
@@ -491,11 +532,12 @@ extern "C" int rmsnorm_rope_kv_append_ex(const void *q, const int64_t *q_strides
         (Hkv > 0 && (!k || !v || !k_strides || !v_strides || !k_cache_strides || !v_cache_strides ||
                      (num_slots > 0 && (!k_cache || !v_cache)))))
         return RMSNORM_ERR_INVALID_ARG;
-    const Heads none{nullptr, 0, 0, 0};
-    return rope_run(Hq ? heads(q, q_strides, 2) : none, Hkv ? heads(k, k_strides, 2) : none,
-                    Hkv ? heads(v, v_strides, 2) : none, positions, slots,
-                    Hq ? heads(q_out, q_out_strides, 2) : none, Hkv ? heads(k_cache, k_cache_strides, 2) : none,
-                    Hkv ? heads(v_cache, v_cache_strides, 2) : none, inv_freq, attn_scale, interleaved, 0, 1, T,
+    const Heads none{nullptr, 0, 0, 0, 0};
+    const int es = esize_of(dtype);
+    return rope_run(Hq ? heads(q, q_strides, 2, es) : none, Hkv ? heads(k, k_strides, 2, es) : none,
+                    Hkv ? heads(v, v_strides, 2, es) : none, positions, slots,
+                    Hq ? heads(q_out, q_out_strides, 2, es) : none, Hkv ? heads(k_cache, k_cache_strides, 2, es) : none,
+                    Hkv ? heads(v_cache, v_cache_strides, 2, es) : none, inv_freq, attn_scale, interleaved, 0, 1, T,
                     Hq, Hkv, Dh, rot_dim, num_slots, dtype, stream);
 }
 
