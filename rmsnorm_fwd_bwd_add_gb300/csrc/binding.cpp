@@ -10,7 +10,8 @@
 // module links against torch alone.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -194,13 +195,16 @@ void exactly(const char *name, const Tensor &t, at::ScalarType type, c10::IntArr
              dtype_str(type), dev.str().c_str());
 }
 
-Tensor empty(c10::IntArrayRef shape, at::ScalarType type, const c10::Device &dev) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+// A new tensor on the current device (OnDevice), from torch's allocator for the
+// current stream, without the operator dispatch of at::empty.
+Tensor empty(c10::IntArrayRef shape, at::ScalarType type) {
+    return at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(),
+                                     c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt);
 }
 
 Tensor given_or_empty(const char *name, const Tensor *t, at::ScalarType type, c10::IntArrayRef shape,
                       const c10::Device &dev) {
-    if (!t) return empty(shape, type, dev);
+    if (!t) return empty(shape, type);
     exactly(name, *t, type, shape, dev);
     return *t;
 }
@@ -275,7 +279,7 @@ void check_rstd(const Tensor &rstd, int64_t rows, const c10::Device &dev) {
 
 // A row output: the given tensor, or a dense new one like ref.
 std::pair<Tensor, int64_t> row_output(const char *name, const Tensor *t, const Tensor &ref, int64_t D) {
-    if (!t) return {empty(ref.sizes(), ref.scalar_type(), ref.device()), D};
+    if (!t) return {empty(ref.sizes(), ref.scalar_type()), D};
     return {*t, rows_like(name, *t, ref)};
 }
 
@@ -297,7 +301,7 @@ PyObject *block_fwd(PyObject *, PyObject *const *argv, Py_ssize_t n) {
         if (argv[10] == Py_True) {
             c10::SmallVector<int64_t, 6> shape{2};
             shape.append(y.sizes().begin(), y.sizes().end() - 1);
-            rstd = empty(shape, at::kFloat, y.device());
+            rstd = empty(shape, at::kFloat);
         } else if (argv[10] != Py_None) {
             rstd = a.tensor(10, "rstd");
             check_rstd(*rstd, r.rows, y.device());
@@ -338,7 +342,7 @@ PyObject *block_vjp(PyObject *, PyObject *const *argv, Py_ssize_t n) {
             g_gate = given_or_empty("g_gate", a.optional(15, "g_gate"), at::kFloat, gate->sizes(), y.device());
         auto f32 = [](const std::optional<Tensor> &t) { return t ? static_cast<float *>(ptr(&*t)) : nullptr; };
         const int64_t bytes = (int64_t)c_block_vjp_size(r.rows, r.D, code);
-        const Tensor ws = empty({bytes}, at::kByte, y.device());
+        const Tensor ws = empty({bytes}, at::kByte);
         check_status("rmsnorm_block_vjp",
                      c_block_vjp_ws(ptr(&y), r.ld, ptr(&h), ld_h, ptr(w_post), ptr(&w_pre), ptr(gate), g.ld, g.G,
                                  (float)a.number(8), ptr(&g_out), ld_g, ptr(g_res), ld_gr,
@@ -386,7 +390,7 @@ void heads_like(const char *name, const Tensor &t, const Tensor &ref, int64_t H)
 }
 
 Tensor heads_output(const char *name, const Tensor *t, const Tensor &ref) {
-    if (!t) return empty(ref.sizes(), ref.scalar_type(), ref.device());
+    if (!t) return empty(ref.sizes(), ref.scalar_type());
     heads_like(name, *t, ref, ref.size(-2));
     return *t;
 }

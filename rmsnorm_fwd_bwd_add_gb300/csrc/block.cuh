@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
         __syncthreads();
     }
     griddep_wait();
+    griddep_launch_dependents();
     if constexpr (KIND == BLOCK_STAGED) {
         if (threadIdx.x == 0)
             for (int s = 0; s < ring.S && s < deal.n; ++s) ring_issue<T>(ring, a, src, ld, deal.row(s), s, policy);
@@ -496,7 +497,6 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
             if (ri + R < deal.n) fetch_global(deal.row(ri + R));
         }
     }
-    griddep_launch_dependents();
 }
 
 // VJP -----------------------------------------------------------------------
@@ -534,6 +534,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
         __syncthreads();
     }
     griddep_wait();
+    griddep_launch_dependents();
     if constexpr (KIND == BLOCK_STAGED) {
         if (threadIdx.x == 0)
             for (int s = 0; s < ring.S && s < deal.n; ++s) ring_issue<T>(ring, a, src, ld, deal.row(s), s, policy);
@@ -826,7 +827,6 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
         seg = end;
     }
     flush(acc_pre, a.part_pre + cta * D, 1.f);
-    griddep_launch_dependents();
 }
 
 }  // namespace rmsn

@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(BLOCK_GENERIC_NT) block_fwd_generic_kernel(con
     const float wb = a.weight_bias, inv_D = 1.0f / (float)D;
     const T *w1 = static_cast<const T *>(a.w_pre), *w2 = static_cast<const T *>(a.w_post);
     griddep_wait();
+    griddep_launch_dependents();
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *y = static_cast<const T *>(a.y) + row * a.ld_y;
         const T *res = static_cast<const T *>(a.res) + row * a.ld_res;
@@ -73,7 +74,6 @@ __global__ void __launch_bounds__(BLOCK_GENERIC_NT) block_fwd_generic_kernel(con
             a.rstd[a.rows + row] = r_h;
         }
     }
-    griddep_launch_dependents();
 }
 
 template <typename T>
@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(BLOCK_GENERIC_NT) block_vjp_generic_kernel(con
     const int64_t r0 = split_first(cta, a.split_q, a.split_r), r1 = split_first(cta + 1, a.split_q, a.split_r);
     const bool per_row = a.gate && a.rows_per_gate == 1;
     griddep_wait();
+    griddep_launch_dependents();
     float *pre = a.part_pre + cta * D;
     for (int64_t row = r0; row < r1; ++row) {
         const int64_t gr = gate_row(row, a.rows_per_gate);
@@ -152,7 +153,6 @@ __global__ void __launch_bounds__(BLOCK_GENERIC_NT) block_vjp_generic_kernel(con
             Cvt<T>::store1(gy + c, r_y * (m * v - yv * ee));
         }
     }
-    griddep_launch_dependents();
 }
 
 // Second stage: a CTA covers 32 columns with BR_WARPS warps.

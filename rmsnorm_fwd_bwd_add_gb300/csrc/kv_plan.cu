@@ -61,40 +61,46 @@ struct KvArgs {
     unsigned int *status;
 };
 
-// Inclusive sum of v over the CTA's threads in thread order; *total is the
-// CTA's sum.  `sums` holds an int64 a warp; the CTA passes two barriers.
-__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *sums, int64_t *total) {
+// Inclusive sums over the CTA of N sequences of KV_PER values a thread, in order;
+// total[n] is the sum of all.  `sums` holds N int64 a warp; the CTA passes two
+// barriers, whatever N.
+template <int N>
+__device__ __forceinline__ void cta_scan(int64_t (&v)[N][KV_PER], int64_t (*sums)[2], int64_t (&total)[N]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t own[N], run[N];
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, v, off);
-        if (lane >= off) v += u;
+    for (int n = 0; n < N; ++n) {
+#pragma unroll
+        for (int k = 1; k < KV_PER; ++k) v[n][k] += v[n][k - 1];
+        own[n] = run[n] = v[n][KV_PER - 1];
     }
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, run[n], off);
+            if (lane >= off) run[n] += u;
+        }
     __syncthreads();  // the previous scan's sums have been read
-    if (lane == 31) sums[warp] = v;
-    __syncthreads();
-    int64_t w = lane < KV_NT / 32 ? sums[lane] : 0;
+    if (lane == 31) {
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, w, off);
-        if (lane >= off) w += u;
+        for (int n = 0; n < N; ++n) sums[warp][n] = run[n];
     }
-    *total = __shfl_sync(0xffffffffu, w, 31);
-    const int64_t before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
-    return v + (warp ? before : 0);
-}
-
-// Inclusive sums of KV_PER values a thread over the CTA, in order; returns the
-// CTA's sum.
-__device__ __forceinline__ int64_t cta_scan_per(int64_t (&v)[KV_PER], int64_t *sums) {
+    __syncthreads();
 #pragma unroll
-    for (int i = 1; i < KV_PER; ++i) v[i] += v[i - 1];
-    const int64_t own = v[KV_PER - 1];
-    int64_t total;
-    const int64_t before = cta_scan(own, sums, &total) - own;
+    for (int n = 0; n < N; ++n) {
+        int64_t w = sums[lane][n];  // KV_NT / 32 == 32 warps
 #pragma unroll
-    for (int i = 0; i < KV_PER; ++i) v[i] += before;
-    return total;
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, w, off);
+            if (lane >= off) w += u;
+        }
+        total[n] = __shfl_sync(0xffffffffu, w, 31);
+        const int64_t warps_before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+        const int64_t before = run[n] - own[n] + (warp ? warps_before : 0);
+#pragma unroll
+        for (int k = 0; k < KV_PER; ++k) v[n][k] += before;
+    }
 }
 
 // The requests of a tile that move blocks, in order.  A scanned word carries
@@ -108,7 +114,8 @@ struct Moves {
 };
 
 struct PlanShared {
-    int64_t sums[KV_NT / 32];
+    int64_t sums[KV_NT / 32][2];
+    unsigned long long last;
     union {
         Moves moves;
         struct {               // for the tokens, once the blocks are moved
@@ -118,26 +125,18 @@ struct PlanShared {
     };
 };
 
-// Entries n[k] blocks long, from[k] on in request row b's table row, join the list;
-// returns the tile's blocks, and *entries their requests.  The list may be read
-// once the CTA has passed a barrier.
-__device__ __forceinline__ int64_t list_moves(const int64_t (&n)[KV_PER], const int32_t (&from)[KV_PER], Moves &mv,
-                                              int64_t *sums, int *entries) {
-    int64_t v[KV_PER];
-#pragma unroll
-    for (int k = 0; k < KV_PER; ++k) v[k] = n[k] + (n[k] > 0 ? (int64_t)1 << KV_COUNT_SHIFT : 0);
-    const int64_t total = cta_scan_per(v, sums);
-    const int64_t mask = ((int64_t)1 << KV_COUNT_SHIFT) - 1;
-#pragma unroll
-    for (int k = 0; k < KV_PER; ++k)
-        if (n[k] > 0) {
-            const int at = (int)(v[k] >> KV_COUNT_SHIFT) - 1;
-            mv.first[at] = (v[k] & mask) - n[k];
-            mv.from[at] = from[k];
-            mv.req[at] = (uint16_t)(threadIdx.x * KV_PER + k);
-        }
-    *entries = (int)(total >> KV_COUNT_SHIFT);
-    return total & mask;
+constexpr int64_t KV_BLOCKS = ((int64_t)1 << KV_COUNT_SHIFT) - 1;
+
+__device__ __forceinline__ int64_t move_word(int64_t n) { return n + (n > 0 ? (int64_t)1 << KV_COUNT_SHIFT : 0); }
+
+// Request k of this thread, whose inclusive sum of words is v, moves n blocks from
+// block `from` of its row on.  The list may be read once the CTA has passed a
+// barrier.
+__device__ __forceinline__ void list_move(Moves &mv, int64_t v, int64_t n, int32_t from, int k) {
+    const int at = (int)(v >> KV_COUNT_SHIFT) - 1;
+    mv.first[at] = (v & KV_BLOCKS) - n;
+    mv.from[at] = from;
+    mv.req[at] = (uint16_t)(threadIdx.x * KV_PER + k);
 }
 
 // The last i < n with a[i] <= x (a ascending, a[0] <= x).
@@ -175,9 +174,8 @@ __device__ __forceinline__ void move_blocks(const KvArgs &a, const Moves &mv, in
     }
 }
 
-// The free count, clamped to what the stack holds.
-__device__ __forceinline__ int64_t stack_top(const KvArgs &a) {
-    const int64_t n = *a.free_count;
+// The free count as loaded, clamped to what the stack holds.
+__device__ __forceinline__ int64_t stack_top(const KvArgs &a, int64_t n) {
     if ((n < 0 || n > a.num_blocks) && threadIdx.x == 0) atomicOr(a.status, BAD_INDEX);
     return min(max(n, (int64_t)0), a.num_blocks);
 }
@@ -191,7 +189,8 @@ __global__ void __launch_bounds__(KV_NT) kv_release_kernel(const KvArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     PlanShared &sh = *reinterpret_cast<PlanShared *>(smem);
     griddep_wait();
-    const int64_t top = stack_top(a);
+    griddep_launch_dependents();
+    const int32_t count = *a.free_count;  // in flight with the first requests' loads
     int64_t pushed = 0;
     for (int64_t b0 = 0; b0 < a.B; b0 += KV_TILE) {
         int32_t len[KV_PER];
@@ -202,8 +201,7 @@ __global__ void __launch_bounds__(KV_NT) kv_release_kernel(const KvArgs a) {
             len[k] = b + k < a.B ? a.lens[b + k] : 0;
             done[k] = b + k < a.B && a.finished[b + k];
         }
-        int64_t n[KV_PER];
-        const int32_t from[KV_PER] = {};
+        int64_t n[KV_PER], v[1][KV_PER], sum[1];
 #pragma unroll
         for (int k = 0; k < KV_PER; ++k) {
             n[k] = done[k] && len[k] > 0 ? blocks_of(len[k], a) : 0;
@@ -212,11 +210,15 @@ __global__ void __launch_bounds__(KV_NT) kv_release_kernel(const KvArgs a) {
                 n[k] = 0;
             }
             if (b + k < a.B) a.lens_out[b + k] = done[k] ? 0 : len[k];
+            v[0][k] = move_word(n[k]);
         }
-        int entries;
-        const int64_t total = list_moves(n, from, sh.moves, sh.sums, &entries);
+        cta_scan<1>(v, sh.sums, sum);
+#pragma unroll
+        for (int k = 0; k < KV_PER; ++k)
+            if (n[k] > 0) list_move(sh.moves, v[0][k], n[k], 0, k);
         __syncthreads();
-        const int64_t base = top + pushed;
+        const int entries = (int)(sum[0] >> KV_COUNT_SHIFT);
+        const int64_t total = sum[0] & KV_BLOCKS, base = stack_top(a, count) + pushed;
         move_blocks(a, sh.moves, entries, total, b0, [](const int32_t *p, int64_t) { return *p; },
                     [&](const int32_t *, int64_t e, int32_t id) {
                         const int64_t at = base + e;
@@ -227,8 +229,7 @@ __global__ void __launch_bounds__(KV_NT) kv_release_kernel(const KvArgs a) {
         __syncthreads();  // the list may be written again
     }
     __syncthreads();  // every thread has read the count it may overwrite
-    if (threadIdx.x == 0) *a.free_count_out = (int32_t)min(top + pushed, a.num_blocks);
-    griddep_launch_dependents();
+    if (threadIdx.x == 0) *a.free_count_out = (int32_t)min(stack_top(a, count) + pushed, a.num_blocks);
 }
 
 // Position, slot and request of token t, which is request `req`'s token number
@@ -260,9 +261,10 @@ __global__ void __launch_bounds__(KV_NT) kv_plan_kernel(const KvArgs a, bool tok
     extern __shared__ __align__(16) unsigned char smem[];
     PlanShared &sh = *reinterpret_cast<PlanShared *>(smem);
     griddep_wait();
+    griddep_launch_dependents();
     const bool pool = a.free_count != nullptr;
-    const int64_t top = pool ? stack_top(a) : 0;
-    int64_t total_new = 0, total_need = 0, popped = 0;
+    const int32_t count = pool ? *a.free_count : 0;  // in flight with the first requests' loads
+    int64_t total_new = 0, total_need = 0, popped = 0;  // so far: tokens, blocks asked for, blocks taken
     int64_t start[KV_PER];
     int32_t base[KV_PER];  // for the tokens of the last tile
     for (int64_t b0 = 0; b0 < a.B; b0 += KV_TILE) {
@@ -275,8 +277,9 @@ __global__ void __launch_bounds__(KV_NT) kv_plan_kernel(const KvArgs a, bool tok
             len[k] = valid[k] ? a.lens[b + k] : 0;
             add[k] = valid[k] ? a.new_lens[b + k] : 0;
         }
-        int64_t end[KV_PER], need[KV_PER], cum[KV_PER];
+        int64_t need[KV_PER], v[2][KV_PER], sum[2];  // v: tokens, words of blocks
         int32_t have[KV_PER];
+        bool fits[KV_PER];
 #pragma unroll
         for (int k = 0; k < KV_PER; ++k) {
             if (len[k] < 0 || add[k] < 0) {
@@ -284,40 +287,60 @@ __global__ void __launch_bounds__(KV_NT) kv_plan_kernel(const KvArgs a, bool tok
                 valid[k] = false;
                 add[k] = 0;
             }
-            end[k] = add[k];
-        }
-        const int64_t tile_new = cta_scan_per(end, sh.sums);
-        bool ok[KV_PER];
-#pragma unroll
-        for (int k = 0; k < KV_PER; ++k) {
-            end[k] += total_new;
-            const int64_t sum = (int64_t)len[k] + add[k];
-            const int64_t h = valid[k] ? blocks_of(len[k], a) : 0, want = valid[k] ? blocks_of(sum, a) : 0;
-            ok[k] = valid[k] && want <= a.width && end[k] <= a.T && sum <= INT_MAX;
-            need[k] = cum[k] = ok[k] && pool ? want - h : 0;
+            const int64_t all = (int64_t)len[k] + add[k];
+            const int64_t h = valid[k] ? blocks_of(len[k], a) : 0, want = valid[k] ? blocks_of(all, a) : 0;
+            fits[k] = valid[k] && want <= a.width && all <= INT_MAX;
+            need[k] = fits[k] && pool ? want - h : 0;
             have[k] = (int32_t)min(h, (int64_t)INT_MAX);
+            v[0][k] = add[k];
+            v[1][k] = move_word(need[k]);
         }
-        const int64_t tile_need = cta_scan_per(cum, sh.sums);
-        int64_t take[KV_PER];
+        cta_scan<2>(v, sh.sums, sum);
+        if (total_new + sum[0] > a.T) {  // the last requests' tokens do not fit: their blocks do not count
+            int64_t again[1][KV_PER], sum1[1];
+#pragma unroll
+            for (int k = 0; k < KV_PER; ++k) {
+                fits[k] = fits[k] && total_new + v[0][k] <= a.T;
+                need[k] = fits[k] ? need[k] : 0;
+                again[0][k] = move_word(need[k]);
+            }
+            cta_scan<1>(again, sh.sums, sum1);
+#pragma unroll
+            for (int k = 0; k < KV_PER; ++k) v[1][k] = again[0][k];
+            sum[1] = sum1[0];
+        }
+        // Requests that need blocks are granted in order until the stack runs out, so
+        // the tile's blocks are the next ones off the stack, and the list's entries
+        // the first so many.
+        const int64_t top = pool ? stack_top(a, count) : 0;
+        int64_t granted_word = 0;
 #pragma unroll
         for (int k = 0; k < KV_PER; ++k) {
-            cum[k] += total_need;
-            ok[k] = ok[k] && (need[k] == 0 || cum[k] <= top);
-            take[k] = ok[k] ? need[k] : 0;
-            start[k] = end[k] - add[k];
-            base[k] = ok[k] ? len[k] : -1 - max(len[k], 0);
+            const bool ok = fits[k] && (need[k] == 0 || total_need + (v[1][k] & KV_BLOCKS) <= top);
+            start[k] = total_new + v[0][k] - add[k];
+            base[k] = ok ? len[k] : -1 - max(len[k], 0);
+            if (ok && need[k] > 0) {
+                list_move(sh.moves, v[1][k], need[k], have[k], k);
+                granted_word = v[1][k];
+            }
             if (b + k < a.B) {
                 a.starts[b + k] = start[k];
-                a.granted[b + k] = ok[k] ? 1 : 0;
-                a.lens_out[b + k] = ok[k] ? len[k] + add[k] : len[k];
+                a.granted[b + k] = ok ? 1 : 0;
+                a.lens_out[b + k] = ok ? len[k] + add[k] : len[k];
             }
         }
-        total_new += tile_new;
-        total_need += tile_need;
-        // Requests that take blocks are granted in order, so the tile's blocks are
-        // the next ones off the stack.
-        int entries;
-        const int64_t total = list_moves(take, have, sh.moves, sh.sums, &entries);
+        total_new += sum[0];
+        int64_t moved = sum[1];
+        if (total_need + (moved & KV_BLOCKS) > top) {  // not all of them were: the last one's word
+            if (threadIdx.x == 0) sh.last = 0;
+            __syncthreads();
+            if (granted_word) atomicMax(&sh.last, (unsigned long long)granted_word);
+            __syncthreads();
+            moved = (int64_t)sh.last;
+        }
+        total_need += sum[1] & KV_BLOCKS;
+        const int entries = (int)(moved >> KV_COUNT_SHIFT);
+        const int64_t total = moved & KV_BLOCKS;
         __syncthreads();
         const int64_t from = top - 1 - popped;
         move_blocks(a, sh.moves, entries, total, b0, [&](const int32_t *, int64_t e) { return a.free_blocks[from - e]; },
@@ -331,9 +354,8 @@ __global__ void __launch_bounds__(KV_NT) kv_plan_kernel(const KvArgs a, bool tok
     __syncthreads();  // every thread has read the count it may overwrite
     if (threadIdx.x == 0) {
         a.starts[a.B] = total_new;
-        if (pool) *a.free_count_out = (int32_t)(top - popped);
+        if (pool) *a.free_count_out = (int32_t)(stack_top(a, count) - popped);
     }
-    griddep_launch_dependents();
     if (tokens) {
         const int n = (int)a.B;
 #pragma unroll
@@ -380,6 +402,7 @@ __global__ void __launch_bounds__(KV_TOKEN_NT) kv_tokens_kernel(const KvArgs a) 
     __shared__ int32_t s_base[CAP];
     __shared__ int64_t s_range[2];
     griddep_wait();
+    griddep_launch_dependents();
     const int64_t total = a.starts[a.B];
     const int warp = threadIdx.x >> 5;
     for (int64_t t0 = (int64_t)blockIdx.x * KV_TOKENS; t0 < a.T; t0 += (int64_t)gridDim.x * KV_TOKENS) {
@@ -417,7 +440,6 @@ __global__ void __launch_bounds__(KV_TOKEN_NT) kv_tokens_kernel(const KvArgs a) 
         }
         __syncthreads();  // the starts are written again
     }
-    griddep_launch_dependents();
 }
 
 struct Buf {

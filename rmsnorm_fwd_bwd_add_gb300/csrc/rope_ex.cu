@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
     for (int i = threadIdx.x; i < half; i += RX_NT) s_turns[i] = a.turns[i];
     __syncthreads();
     griddep_wait();
+    griddep_launch_dependents();
 
     // A warp covers `hpi` heads a step, a lane one unit of each head it meets: the
     // heads of q, then of k, then of v, which has no more units, all copied.
@@ -294,7 +295,6 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
             }
         }
     }
-    griddep_launch_dependents();
 }
 
 template <typename T, int VB, bool INTERLEAVED>
