@@ -41,7 +41,7 @@ constexpr int KV_PER = 4;                      // consecutive requests a thread 
 constexpr int KV_TILE = KV_NT * KV_PER;        // requests a pass of the CTA
 constexpr int KV_BATCH = 4;                    // block ids a thread keeps in flight
 constexpr int KV_TOKEN_NT = 256;
-constexpr int KV_TOKENS = 4 * KV_TOKEN_NT;     // tokens a CTA of the second kernel writes
+constexpr int KV_TOKENS = 2 * KV_TOKEN_NT;     // tokens a CTA of the second kernel writes
 constexpr int KV_FUSED_TOKENS = 4096;          // the scanning CTA writes up to so many itself
 constexpr unsigned int BAD_INDEX = RMSNORM_DEVSTATUS_BAD_INDEX;
 
@@ -108,7 +108,7 @@ __device__ __forceinline__ void cta_scan(int64_t (&v)[N][KV_PER], int64_t (*sums
 // among all of them.
 constexpr int KV_COUNT_SHIFT = 48;  // a tile moves fewer than 2^12 * 2^31 < 2^48 blocks
 struct Moves {
-    int64_t first[KV_TILE];  // place of an entry's first block among the tile's
+    uint32_t first[KV_TILE]; // place of an entry's first block among the tile's (saturated)
     int32_t from[KV_TILE];   // index of its first block in its table row
     uint16_t req[KV_TILE];   // its request within the tile
 };
@@ -134,7 +134,7 @@ __device__ __forceinline__ int64_t move_word(int64_t n) { return n + (n > 0 ? (i
 // barrier.
 __device__ __forceinline__ void list_move(Moves &mv, int64_t v, int64_t n, int32_t from, int k) {
     const int at = (int)(v >> KV_COUNT_SHIFT) - 1;
-    mv.first[at] = (v & KV_BLOCKS) - n;
+    mv.first[at] = (uint32_t)min((v & KV_BLOCKS) - n, (int64_t)UINT32_MAX);
     mv.from[at] = from;
     mv.req[at] = (uint16_t)(threadIdx.x * KV_PER + k);
 }
@@ -149,26 +149,27 @@ template <typename A> __device__ __forceinline__ int last_at_most(const A *a, in
     return lo;
 }
 
-// Moves the tile's `total` blocks: f(row pointer at the block, its place) loads,
-// g(row pointer, place, id) stores, KV_BATCH of the first ahead of the second.
+// Moves the tile's `total` (below 2^31) blocks: load(row pointer at the block, its
+// place), then store(row pointer, place, id), KV_BATCH of the first ahead of the
+// second.
 template <typename F, typename G>
-__device__ __forceinline__ void move_blocks(const KvArgs &a, const Moves &mv, int entries, int64_t total, int64_t b0,
+__device__ __forceinline__ void move_blocks(const KvArgs &a, const Moves &mv, int entries, uint32_t total, int64_t b0,
                                             F load, G store) {
-    for (int64_t e0 = threadIdx.x; e0 < total; e0 += KV_NT * KV_BATCH) {
+    for (uint32_t e0 = threadIdx.x; e0 < total; e0 += KV_NT * KV_BATCH) {
         int32_t *at[KV_BATCH];
         int32_t id[KV_BATCH];
 #pragma unroll
         for (int i = 0; i < KV_BATCH; ++i) {
-            const int64_t e = e0 + i * KV_NT;
+            const uint32_t e = e0 + i * KV_NT;
             if (e < total) {
                 const int k = last_at_most(mv.first, entries, e);
-                at[i] = a.table + (b0 + mv.req[k]) * a.ld_table + mv.from[k] + (e - mv.first[k]);
+                at[i] = a.table + (b0 + mv.req[k]) * a.ld_table + (mv.from[k] + (int64_t)(e - mv.first[k]));
                 id[i] = load(at[i], e);
             }
         }
 #pragma unroll
         for (int i = 0; i < KV_BATCH; ++i) {
-            const int64_t e = e0 + i * KV_NT;
+            const uint32_t e = e0 + i * KV_NT;
             if (e < total) store(at[i], e, id[i]);
         }
     }
@@ -180,9 +181,10 @@ __device__ __forceinline__ int64_t stack_top(const KvArgs &a, int64_t n) {
     return min(max(n, (int64_t)0), a.num_blocks);
 }
 
-// ceil(len / block) for 0 <= len < 2^32 and block >= 1
-__device__ __forceinline__ int64_t blocks_of(int64_t len, const KvArgs &a) {
-    return (int64_t)(((uint32_t)len + (uint64_t)a.block - 1) / (uint32_t)a.block);
+// ceil(len / block), both below 2^31 (in 32 bits: the 64-bit divisions of the scan
+// alone were a third of its instructions)
+__device__ __forceinline__ int64_t blocks_of(uint32_t len, const KvArgs &a) {
+    return (len + (uint32_t)a.block - 1u) / (uint32_t)a.block;
 }
 
 __global__ void __launch_bounds__(KV_NT) kv_release_kernel(const KvArgs a) {
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(KV_NT) kv_release_kernel(const KvArgs a) {
         int64_t n[KV_PER], v[1][KV_PER], sum[1];
 #pragma unroll
         for (int k = 0; k < KV_PER; ++k) {
-            n[k] = done[k] && len[k] > 0 ? blocks_of(len[k], a) : 0;
+            n[k] = done[k] && len[k] > 0 ? blocks_of((uint32_t)len[k], a) : 0;
             if (len[k] < 0 || n[k] > a.width) {  // such a request gives nothing back
                 atomicOr(a.status, BAD_INDEX);
                 n[k] = 0;
@@ -219,11 +221,13 @@ __global__ void __launch_bounds__(KV_NT) kv_release_kernel(const KvArgs a) {
         __syncthreads();
         const int entries = (int)(sum[0] >> KV_COUNT_SHIFT);
         const int64_t total = sum[0] & KV_BLOCKS, base = stack_top(a, count) + pushed;
-        move_blocks(a, sh.moves, entries, total, b0, [](const int32_t *p, int64_t) { return *p; },
-                    [&](const int32_t *, int64_t e, int32_t id) {
-                        const int64_t at = base + e;
-                        if (id < 0 || id >= a.num_blocks || at >= a.num_blocks) atomicOr(a.status, BAD_INDEX);
-                        if (at < a.num_blocks) a.free_blocks[at] = id;
+        // what the stack has no room for is not pushed
+        const int64_t room = max((int64_t)0, a.num_blocks - base);
+        if (total > room && threadIdx.x == 0) atomicOr(a.status, BAD_INDEX);
+        move_blocks(a, sh.moves, entries, (uint32_t)min(total, room), b0, [](const int32_t *p, uint32_t) { return *p; },
+                    [&](const int32_t *, uint32_t e, int32_t id) {
+                        if (id < 0 || id >= a.num_blocks) atomicOr(a.status, BAD_INDEX);
+                        a.free_blocks[base + e] = id;
                     });
         pushed += total;
         __syncthreads();  // the list may be written again
@@ -238,11 +242,11 @@ __device__ __forceinline__ void write_token(const KvArgs &a, int64_t t, int64_t 
     int64_t slot = -1;
     const bool ok = base >= 0;
     const int64_t pos = (ok ? (int64_t)base : -1 - (int64_t)base) + off;
-    if (ok) {
-        const int64_t blk = (int64_t)((uint64_t)pos / (uint32_t)a.block);
+    if (ok) {  // pos < 2^31
+        const uint32_t blk = (uint32_t)pos / (uint32_t)a.block;
         const int32_t id = a.table[req * a.ld_table + blk];
         if (id < 0 || (a.free_count && id >= a.num_blocks)) atomicOr(a.status, BAD_INDEX);
-        else slot = (int64_t)id * a.block + (pos - blk * a.block);
+        else slot = (int64_t)id * a.block + ((uint32_t)pos - blk * (uint32_t)a.block);
     }
     a.positions[t] = pos;
     a.slots[t] = slot;
@@ -288,8 +292,10 @@ __global__ void __launch_bounds__(KV_NT) kv_plan_kernel(const KvArgs a, bool tok
                 add[k] = 0;
             }
             const int64_t all = (int64_t)len[k] + add[k];
-            const int64_t h = valid[k] ? blocks_of(len[k], a) : 0, want = valid[k] ? blocks_of(all, a) : 0;
-            fits[k] = valid[k] && want <= a.width && all <= INT_MAX;
+            valid[k] = valid[k] && all <= INT_MAX;
+            const int64_t h = valid[k] ? blocks_of((uint32_t)len[k], a) : 0;
+            const int64_t want = valid[k] ? blocks_of((uint32_t)all, a) : 0;
+            fits[k] = valid[k] && want <= a.width;
             need[k] = fits[k] && pool ? want - h : 0;
             have[k] = (int32_t)min(h, (int64_t)INT_MAX);
             v[0][k] = add[k];
@@ -343,8 +349,9 @@ __global__ void __launch_bounds__(KV_NT) kv_plan_kernel(const KvArgs a, bool tok
         const int64_t total = moved & KV_BLOCKS;
         __syncthreads();
         const int64_t from = top - 1 - popped;
-        move_blocks(a, sh.moves, entries, total, b0, [&](const int32_t *, int64_t e) { return a.free_blocks[from - e]; },
-                    [&](int32_t *p, int64_t, int32_t id) {
+        move_blocks(a, sh.moves, entries, (uint32_t)total, b0,
+                    [&](const int32_t *, uint32_t e) { return a.free_blocks[from - e]; },
+                    [&](int32_t *p, uint32_t, int32_t id) {
                         if (id < 0 || id >= a.num_blocks) atomicOr(a.status, BAD_INDEX);
                         *p = id;
                     });
