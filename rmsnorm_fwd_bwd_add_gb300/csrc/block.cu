@@ -40,7 +40,14 @@ BlockPlan make_plan(int64_t rows, int64_t D, int es, int unit, int tensors, bool
     const int64_t row = D * es;
     p.ub = unit % 16 == 0 && row % 16 == 0 ? 16 : unit % 4 == 0 && row % 4 == 0 ? 4 : 2;
     const int per_thread = 32 / es;  // elements: block_units of block.cuh
-    const int64_t threads = ((D + per_thread - 1) / per_thread + 31) / 32 * 32;
+    int64_t threads = ((D + per_thread - 1) / per_thread + 31) / 32 * 32;
+    // VJP rows of 257-320 threads leave an SM one CTA of 9 or 10 warps; with half as
+    // much a thread it is 17 to 20 (16384 rows of bf16: D = 5120 232 -> 218 us, 4097
+    // 470 -> 365).
+    if (vjp && threads > 256 && threads <= 320 && rows > sm) {
+        p.half = 1;
+        threads = ((D + per_thread / 2 - 1) / (per_thread / 2) + 31) / 32 * 32;
+    }
     auto generic_plan = [&] {
         BlockPlan g{};
         g.kind = BLOCK_GENERIC;
@@ -55,7 +62,7 @@ BlockPlan make_plan(int64_t rows, int64_t D, int es, int unit, int tensors, bool
     const size_t tables = (size_t)(D * 4 + 127) / 128 * 128;  // w1 (block_table_bytes)
     // threads an SM holds of the instance these take (block_launch.cuh)
     const int resident = block_resident((int)threads, vjp);
-    int per_sm = resident / (int)threads;
+    int per_sm = p.half ? 1 : resident / (int)threads;
     if (threads == 32) {
         p.kind = BLOCK_WARP;
         int warps = 8;  // rows side by side; fewer when the SMs would idle
@@ -206,7 +213,10 @@ extern "C" int rmsnorm_block_fwd(const void *y, int64_t ld_y, const void *residu
 
 namespace {
 
-size_t scratch_bytes(int grid, int64_t D) { return ((size_t)grid * (size_t)D * 12 + 255) & ~(size_t)255; }
+// Three fp32 rows a CTA, and the second stage's slices.
+size_t scratch_bytes(int grid, int64_t D) {
+    return (((size_t)grid * 3 + BLOCK_MAX_SLICES) * (size_t)D * 4 + 255) & ~(size_t)255;
+}
 
 // The VJP with its scratch in `workspace`, or, with `pooled`, from the library's pool.
 int block_vjp(const void *y, int64_t ld_y, const void *h, int64_t ld_h, const void *w_post,
@@ -319,6 +329,7 @@ int block_vjp(const void *y, int64_t ld_y, const void *h, int64_t ld_h, const vo
     }
     a.part_pre = static_cast<float *>(ws);
     a.part_mid = a.part_pre + (size_t)p.grid * D;
+    a.part_post = a.part_mid + 2 * (size_t)p.grid * D;
     const cudaError_t e = by_type(dtype, [&](auto t) { return launch_block_vjp<typename decltype(t)::type>(p, a, s); });
     st = e == cudaSuccess ? RMSNORM_OK : record_cuda_error(e);
     const int freed = pooled ? scratch_free(ws, s) : RMSNORM_OK;

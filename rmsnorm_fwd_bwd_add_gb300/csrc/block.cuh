@@ -500,12 +500,13 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
 }
 
 // VJP -----------------------------------------------------------------------
-// FULL: a norm after the block, g_res and saved scales are all there.
-template <typename T, int UB, int MAXT, int MINB, int KIND, bool GROW, bool FULL>
+// FULL: a norm after the block, g_res and saved scales are all there.  HALF: 16 bytes
+// of a row a thread instead of 32.
+template <typename T, int UB, int MAXT, int MINB, int KIND, bool GROW, bool FULL, bool HALF>
 __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_constant__ BlockArgs a) {
     using SL = Slot<T, UB>;
     using Raw = typename SL::Raw;
-    constexpr int E = SL::E, V = SL::COUNT, P = SL::P, MAXW = MAXT / 32;
+    constexpr int E = SL::E, V = HALF ? SL::COUNT / 2 : SL::COUNT, P = SL::P, MAXW = MAXT / 32;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float s_red[2][KIND == BLOCK_WARP ? 1 : MAXW][8];
     const int NT = KIND == BLOCK_WARP ? 32 : (int)blockDim.x;

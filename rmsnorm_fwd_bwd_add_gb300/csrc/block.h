@@ -34,6 +34,7 @@ struct BlockArgs {
     float *gw_post, *gw_pre;       // VJP: [D]
     float *part_pre;               // VJP: [grid, D] sums of g h r_h
     float *part_mid;               // VJP: [2 * grid, D] sums A of gate rows split over CTAs
+    float *part_post;              // VJP: [BLOCK_MAX_SLICES, D] sums of gw_post over runs of gate rows
     unsigned int *status;
     long long wait_budget;
     int64_t drop_row;              // test hook: this row's copy is never issued
@@ -108,12 +109,20 @@ __host__ __device__ inline RowDeal vjp_rows(const BlockArgs &a, int64_t c) {
 // rows of part_mid a CTA hold them whatever the number of gate rows.
 __host__ __device__ inline int64_t mid_slot(int64_t c, bool first) { return 2 * c + (first ? 0 : 1); }
 
+// The second stage splits many gate rows into so many runs, a CTA each per 32
+// columns: 5461 gate rows of 3 rows on 32 warps took 170 us of dependent trips to
+// memory (D = 1000).
+constexpr int BLOCK_MAX_SLICES = 32;
+inline int block_slices(int64_t gate_rows) {
+    return gate_rows < 128 ? 1 : gate_rows >= 64 * BLOCK_MAX_SLICES ? BLOCK_MAX_SLICES : (int)(gate_rows / 64);
+}
+
 // How a call runs: BLOCK_GENERIC for rows that do not fit on chip, else the
 // tier of block.cuh with units of `ub` bytes.
 enum : int { BLOCK_STAGED = 0, BLOCK_DIRECT = 1, BLOCK_WARP = 2, BLOCK_GENERIC = 3 };
 
 struct BlockPlan {
-    int kind, ub, threads, grid, stages, chunk_shift, team;
+    int kind, ub, threads, grid, stages, chunk_shift, team, half;
     uint32_t stage_bytes;
     size_t smem;
 };

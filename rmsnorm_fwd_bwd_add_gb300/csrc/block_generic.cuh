@@ -163,6 +163,8 @@ __global__ void __launch_bounds__(BLOCK_GENERIC_NT) block_vjp_generic_kernel(con
 //   BR_WARPS, ...  A part is a row of part_mid, or the whole sum that one CTA
 //   left in g_gate, which becomes w2 * A in place.  Gate rows of one row each
 //   come finished from the first stage, which also weighted its sums.
+// With many gate rows the grid has slices in y, each with a run of them, whose
+// sums of gw_post the library's column sum then adds.
 // The order of every sum depends on how the rows are dealt out alone.  Latency-bound: a
 // warp's first loads of both sums are in flight together, and the row
 // arithmetic is 32-bit (I) where the row count allows (64-bit divisions made
@@ -220,15 +222,17 @@ __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const Block
     };
     griddep_wait();
     griddep_launch_dependents();
-    float head[BR_BATCH];  // the first of this warp's rows of part_pre
-    load_rows(a.part_pre, p0, 1, p1 - p0, head);
+    const bool pre_here = blockIdx.y == 0;  // the slices share out the gate rows alone
+    float head[BR_BATCH];                   // the first of this warp's rows of part_pre
+    load_rows(a.part_pre, p0, 1, pre_here ? p1 - p0 : 0, head);
     const float w2c = in && w2 ? a.weight_bias + Cvt<T>::load1(w2 + col) : 1.f;
     float post = 0.f;
     if (need_mid && per_row) {
         post = add_rows(a.part_mid, 2 * (int64_t)p0, 2, p1 - p0, 0.f);
     } else if (need_mid) {
         const int mate = warp % team;
-        for (I gr = warp / team; gr < G; gr += BR_WARPS / team) {
+        const I g0 = (I)((uint64_t)G * blockIdx.y / gridDim.y), g1 = (I)((uint64_t)G * (blockIdx.y + 1) / gridDim.y);
+        for (I gr = g0 + warp / team; gr < g1; gr += BR_WARPS / team) {
             I c0, c1;
             ctas_of(gr, c0, c1);
             float A = 0.f;
@@ -254,11 +258,11 @@ __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const Block
         }
     }
     float pre = add_all(head, 0.f);
-    pre = add_rows(a.part_pre, (int64_t)p0 + BR_BATCH, 1, p1 - p0 - BR_BATCH, pre);
+    if (pre_here) pre = add_rows(a.part_pre, (int64_t)p0 + BR_BATCH, 1, p1 - p0 - BR_BATCH, pre);
     sums[0][warp][lane] = pre;
     sums[1][warp][lane] = post;
     __syncthreads();
-    if (warp == 0 && in) {
+    if (warp == 0 && in && pre_here) {
         float t = sums[0][0][lane];
 #pragma unroll
         for (int k = 1; k < BR_WARPS; ++k) t += sums[0][k][lane];
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const Block
                 t = fmaf(gt, A, t);
             }
         }
-        if (w2) a.gw_post[col] = t;
+        if (w2) (gridDim.y == 1 ? a.gw_post : a.part_post + (size_t)blockIdx.y * D)[col] = t;
     }
 }
 

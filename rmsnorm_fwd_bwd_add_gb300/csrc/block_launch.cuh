@@ -7,11 +7,13 @@
 
 namespace rmsn {
 
-template <bool VJP, typename T, int UB, int MAXT, int MINB, int KIND, bool GROW, bool FULL = false>
+cudaError_t launch_gw_reduce(const float *partials, float *gw, int P, int D, cudaStream_t stream);
+
+template <bool VJP, typename T, int UB, int MAXT, int MINB, int KIND, bool GROW, bool FULL = false, bool HALF = false>
 cudaError_t launch_block_inst(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> smem_mask{0};
     void (*kern)(BlockArgs);
-    if constexpr (VJP) kern = block_vjp_kernel<T, UB, MAXT, MINB, KIND, GROW, FULL>;
+    if constexpr (VJP) kern = block_vjp_kernel<T, UB, MAXT, MINB, KIND, GROW, FULL, HALF>;
     else kern = block_fwd_kernel<T, UB, MAXT, MINB, KIND, GROW>;
     if (p.smem > 0) {
         const cudaError_t e = allow_max_dynamic_smem((const void *)kern, smem_mask);
@@ -27,6 +29,13 @@ cudaError_t launch_block_kind(const BlockPlan &p, const BlockArgs &a, cudaStream
         if (p.threads <= 512) return launch_block_inst<VJP, T, UB, 512, 1, BLOCK_DIRECT, GROW>(p, a, s);
         return launch_block_inst<VJP, T, UB, 1024, 1, BLOCK_DIRECT, GROW>(p, a, s);
     }
+    if constexpr (VJP)
+        if (p.half) {  // at most 96 registers
+            if constexpr (UB == 16 && !GROW)
+                if (a.w_post && a.g_res && a.rstd)
+                    return launch_block_inst<VJP, T, UB, 640, 1, BLOCK_STAGED, GROW, true, true>(p, a, s);
+            return launch_block_inst<VJP, T, UB, 640, 1, BLOCK_STAGED, GROW, false, true>(p, a, s);
+        }
     // The training backward with all its operands, without their run-time tests:
     // 15 % fewer instructions (16384 x 4096 bf16: 139 -> 129 us).
     if constexpr (VJP && UB == 16 && !GROW)
@@ -68,11 +77,15 @@ cudaError_t launch_block(const BlockPlan &p, const BlockArgs &a, cudaStream_t s)
 
 template <typename T>
 cudaError_t launch_block_vjp_both(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
-    const cudaError_t e = launch_block<true, T>(p, a, s);
+    cudaError_t e = launch_block<true, T>(p, a, s);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((a.D + 31) / 32)), block(32 * BR_WARPS);
-    return a.rows <= INT32_MAX ? launch_pdl(block_reduce_kernel<T, uint32_t>, grid, block, 0, s, a, p.grid)
-                               : launch_pdl(block_reduce_kernel<T, int64_t>, grid, block, 0, s, a, p.grid);
+    const int64_t G = a.rows / a.rows_per_gate;
+    const int slices = block_slices(a.team || a.rows_per_gate == 1 ? 1 : G);
+    const dim3 grid((unsigned)((a.D + 31) / 32), slices), block(32 * BR_WARPS);
+    e = a.rows <= INT32_MAX ? launch_pdl(block_reduce_kernel<T, uint32_t>, grid, block, 0, s, a, p.grid)
+                            : launch_pdl(block_reduce_kernel<T, int64_t>, grid, block, 0, s, a, p.grid);
+    if (e != cudaSuccess || slices == 1 || !a.w_post) return e;
+    return launch_gw_reduce(a.part_post, a.gw_post, slices, a.D, s);
 }
 
 }  // namespace rmsn
