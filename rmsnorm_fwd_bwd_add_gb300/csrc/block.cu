@@ -89,8 +89,15 @@ BlockPlan make_plan(int64_t rows, int64_t D, int es, int unit, int tensors, bool
         p.smem = 128 + tables + (size_t)p.stages * set;
         if (p.stages < 1) return generic_plan();
     }
-    if (vjp && p.kind != BLOCK_DIRECT)  // scratch traffic small beside the rows'
+    if (vjp && p.kind == BLOCK_WARP)  // scratch traffic small beside the rows'
         p.grid = (int)std::min<int64_t>(p.grid, std::max<int64_t>(sm, rows / 12));
+    if (vjp && p.kind == BLOCK_STAGED) {
+        // A CTA's partial rows are 24 bytes a column, written and read in L2, a row 12
+        // from and to memory: fewer rows a CTA the fewer its threads, whose waits
+        // other CTAs must fill.
+        const int64_t least = std::max<int64_t>(2, threads / 32);
+        p.grid = (int)std::min<int64_t>(p.grid, std::max<int64_t>(sm, rows / least));
+    }
     // Rows of 8 KB or more are dealt out to the CTAs in turn, so that all of them work
     // on neighbouring memory: one row at a time in the VJP, 32 KB of them in the
     // forward while each CTA gets eight such chunks (16384 rows of bf16, D = 8192:

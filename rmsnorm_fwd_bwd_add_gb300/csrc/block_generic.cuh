@@ -202,33 +202,39 @@ __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const Block
     auto slot_of = [&](I c0, I gr) {
         return mid_slot(c0, a.team || (I)split_first(c0, q, r) / rpg == gr);
     };
-    // rows first, first + step, ... (n of them) of a [*, D] array, added in that order
-    auto load_rows = [&](const float *base, int64_t first, int step, int n, float (&v)[BR_BATCH]) {
+    // Up to BR_BATCH of n rows of a [*, D] array, `step` rows apart from p on, at this column.
+    auto load_rows = [&](const float *p, int64_t step, int n, float (&v)[BR_BATCH]) {
 #pragma unroll
-        for (int i = 0; i < BR_BATCH; ++i) v[i] = in && i < n ? base[(first + (int64_t)i * step) * D + col] : 0.f;
-    };
-    auto add_all = [](const float (&v)[BR_BATCH], float s) {
-#pragma unroll
-        for (int i = 0; i < BR_BATCH; ++i) s += v[i];
-        return s;
-    };
-    auto add_rows = [&](const float *base, int64_t first, int step, int n, float s) {
-        for (int b = 0; b < n; b += BR_BATCH) {
-            float v[BR_BATCH];
-            load_rows(base, first + (int64_t)b * step, step, n - b, v);
-            s = add_all(v, s);
+        for (int i = 0; i < BR_BATCH; ++i) {
+            v[i] = i < n ? *p : 0.f;
+            p += step;
         }
-        return s;
+    };
+    // s plus n rows from p on in order, the first of them in v already
+    auto add_rows = [&](const float *p, int64_t step, int n, float (&v)[BR_BATCH], float s) {
+        while (true) {
+#pragma unroll
+            for (int i = 0; i < BR_BATCH; ++i) s += v[i];
+            n -= BR_BATCH;
+            if (n <= 0) return s;
+            p += BR_BATCH * step;
+            load_rows(p, step, n, v);
+        }
     };
     griddep_wait();
     griddep_launch_dependents();
     const bool pre_here = blockIdx.y == 0;  // the slices share out the gate rows alone
-    float head[BR_BATCH];                   // the first of this warp's rows of part_pre
-    load_rows(a.part_pre, p0, 1, pre_here ? p1 - p0 : 0, head);
+    const int pre_n = in && pre_here ? p1 - p0 : 0;
+    const float *pre_p = a.part_pre + (int64_t)p0 * D + col;
+    float head[BR_BATCH];
+    load_rows(pre_p, D, pre_n, head);  // in flight while the gate rows are found
     const float w2c = in && w2 ? a.weight_bias + Cvt<T>::load1(w2 + col) : 1.f;
-    float post = 0.f;
+    float post = 0.f, gt = 1.f;
     if (need_mid && per_row) {
-        post = add_rows(a.part_mid, 2 * (int64_t)p0, 2, p1 - p0, 0.f);
+        const float *p = a.part_mid + 2 * (int64_t)p0 * D + col;
+        float v[BR_BATCH];
+        load_rows(p, 2 * (int64_t)D, in ? p1 - p0 : 0, v);
+        post = add_rows(p, 2 * (int64_t)D, in ? p1 - p0 : 0, v, 0.f);
     } else if (need_mid) {
         const int mate = warp % team;
         const I g0 = (I)((uint64_t)G * blockIdx.y / gridDim.y), g1 = (I)((uint64_t)G * (blockIdx.y + 1) / gridDim.y);
@@ -236,7 +242,7 @@ __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const Block
             I c0, c1;
             ctas_of(gr, c0, c1);
             float A = 0.f;
-            const float gt = in && gate && team == 1 ? Cvt<T>::load1(gate + (int64_t)gr * a.ld_gate + col) : 1.f;
+            if (in && gate && mate == 0) gt = Cvt<T>::load1(gate + (int64_t)gr * a.ld_gate + col);
             if (c0 == c1 && a.g_gate) {
                 if (mate == 0 && in) A = a.g_gate[(int64_t)gr * D + col];
             } else {
@@ -244,11 +250,17 @@ __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const Block
                 const int n = (int)(c1 - c0) + 1, share = (n + team - 1) / team;
                 int i0 = min(n, mate * share);
                 const int i1 = min(n, i0 + share);
+                const float *first = nullptr;
                 if (i0 == 0 && i1 > 0) {
-                    if (in) A = a.part_mid[slot_of(c0, gr) * D + col];
+                    first = a.part_mid + slot_of(c0, gr) * D + col;
                     i0 = 1;
                 }
-                A = add_rows(a.part_mid, 2 * ((int64_t)c0 + i0), 2, i1 - i0, A);
+                const int more = in ? i1 - i0 : 0;
+                const float *p = a.part_mid + 2 * ((int64_t)c0 + i0) * D + col;
+                float v[BR_BATCH];
+                load_rows(p, 2 * (int64_t)D, more, v);
+                if (first && in) A = *first;
+                A = add_rows(p, 2 * (int64_t)D, more, v, A);
             }
             if (team == 1 && in) {
                 if (gate) a.g_gate[(int64_t)gr * D + col] = A * w2c;
@@ -257,9 +269,7 @@ __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const Block
             if (team > 1) post = A;  // this warp's part of its gate row's A
         }
     }
-    float pre = add_all(head, 0.f);
-    if (pre_here) pre = add_rows(a.part_pre, (int64_t)p0 + BR_BATCH, 1, p1 - p0 - BR_BATCH, pre);
-    sums[0][warp][lane] = pre;
+    sums[0][warp][lane] = add_rows(pre_p, D, pre_n, head, 0.f);
     sums[1][warp][lane] = post;
     __syncthreads();
     if (warp == 0 && in && pre_here) {
@@ -268,21 +278,22 @@ __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const Block
         for (int k = 1; k < BR_WARPS; ++k) t += sums[0][k][lane];
         a.gw_pre[col] = t;
     }
-    if (warp == 1 && in && need_mid) {
-        float t = 0.f;
-        if (per_row || team == 1) {
-#pragma unroll
-            for (int k = 0; k < BR_WARPS; ++k) t += sums[1][k][lane];
-        } else {
-            for (int gr = 0; gr < (int)G; ++gr) {
-                const float gt = gate ? Cvt<T>::load1(gate + gr * a.ld_gate + col) : 1.f;
-                float A = 0.f;
-                for (int k = 0; k < team; ++k) A += sums[1][gr * team + k][lane];
-                if (gate) a.g_gate[gr * (int64_t)D + col] = A * w2c;
-                t = fmaf(gt, A, t);
-            }
+    if (!need_mid) return;
+    const int places = per_row || team == 1 ? BR_WARPS : (int)G;  // what gw_post adds up
+    if (places == (int)G && team > 1) {  // each team's first warp joins its gate row's parts
+        float A = 0.f;
+        if (warp % team == 0 && warp / team < (int)G) {
+            for (int k = 0; k < team; ++k) A += sums[1][warp + k][lane];
+            if (gate && in) a.g_gate[(int64_t)(warp / team) * D + col] = A * w2c;
         }
-        if (w2) (gridDim.y == 1 ? a.gw_post : a.part_post + (size_t)blockIdx.y * D)[col] = t;
+        __syncthreads();
+        if (warp % team == 0 && warp / team < (int)G) sums[1][warp / team][lane] = gt * A;
+        __syncthreads();
+    }
+    if (warp == 1 && in && w2) {
+        float t = 0.f;
+        for (int k = 0; k < places; ++k) t += sums[1][k][lane];
+        (gridDim.y == 1 ? a.gw_post : a.part_post + (size_t)blockIdx.y * D)[col] = t;
     }
 }
 
