@@ -7,6 +7,7 @@
 #include <cmath>
 
 #include "block.h"
+#include "block_plan.h"
 #include "common.cuh"
 #include "checks.h"
 #include "launch_util.h"
@@ -23,94 +24,6 @@ int scratch_free(void *p, cudaStream_t s);
 namespace {
 
 using namespace rmsn;
-
-constexpr size_t SMEM_PER_SM = 227 * 1024;
-
-// Threads an SM holds of the instance that CTAs of `threads` take (the register
-// caps of block_launch.cuh).
-int block_resident(int threads, bool vjp) {
-    if (!vjp && ((threads > 256 && threads <= 320) || (threads > 512 && threads <= 640))) return 640;
-    return threads > 512 ? 1024 : 512;
-}
-
-// Picks tier, unit and grid.  `unit` divides every address and stride (16 at
-// most); `tensors` row tensors are read.
-BlockPlan make_plan(int64_t rows, int64_t D, int es, int unit, int tensors, bool vjp, int64_t gates, int sm) {
-    BlockPlan p{};
-    const int64_t row = D * es;
-    p.ub = unit % 16 == 0 && row % 16 == 0 ? 16 : unit % 4 == 0 && row % 4 == 0 ? 4 : 2;
-    const int per_thread = 32 / es;  // elements: block_units of block.cuh
-    int64_t threads = ((D + per_thread - 1) / per_thread + 31) / 32 * 32;
-    // VJP rows of 257-320 threads leave an SM one CTA of 9 or 10 warps; with half as
-    // much a thread it is 17 to 20 (16384 rows of bf16: D = 5120 232 -> 218 us, 4097
-    // 470 -> 365).
-    if (vjp && threads > 256 && threads <= 320 && rows > sm) {
-        p.half = 1;
-        threads = ((D + per_thread / 2 - 1) / (per_thread / 2) + 31) / 32 * 32;
-    }
-    auto generic_plan = [&] {
-        BlockPlan g{};
-        g.kind = BLOCK_GENERIC;
-        // the VJP keeps three fp32 rows of scratch a CTA: two CTAs an SM, fewer
-        // where they would take more than 256 MB
-        const int64_t fit = vjp ? std::max<int64_t>(8, ((int64_t)256 << 20) / (12 * D)) : 4 * sm;
-        g.grid = (int)std::min<int64_t>(rows, std::min<int64_t>((vjp ? 2 : 4) * (int64_t)sm, fit));
-        return g;
-    };
-    if (threads > 1024) return generic_plan();
-    p.threads = (int)threads;
-    const size_t tables = (size_t)(D * 4 + 127) / 128 * 128;  // w1 (block_table_bytes)
-    // threads an SM holds of the instance these take (block_launch.cuh)
-    const int resident = block_resident((int)threads, vjp);
-    int per_sm = p.half ? 1 : resident / (int)threads;
-    if (threads == 32) {
-        p.kind = BLOCK_WARP;
-        int warps = 8;  // rows side by side; fewer when the SMs would idle
-        while (warps > 1 && rows < (int64_t)warps * sm) warps /= 2;
-        p.threads = 32 * warps;
-        p.smem = vjp ? (size_t)warps * ((D + 3) / 4 * 16) : 0;
-        p.grid = (int)std::min<int64_t>((rows + warps - 1) / warps, (int64_t)sm * (512 / p.threads));
-    } else if (rows <= (int64_t)sm * per_sm) {
-        p.kind = BLOCK_DIRECT;
-        p.grid = (int)rows;
-    } else {
-        p.kind = BLOCK_STAGED;
-        p.stage_bytes = (uint32_t)((row + (p.ub == 16 ? 0 : 15) + 15) / 16 * 16);
-        // an SM's shared memory, less 1 KB a CTA for the system and 2 KB for the
-        // rest; fewer CTAs where it would leave them no second stage
-        const size_t set = (size_t)tensors * p.stage_bytes;
-        auto stages_of = [&](int ctas) {
-            const size_t share = (SMEM_PER_SM + 1024) / ctas, used = 3 * 1024 + tables;
-            return share > used ? (int)std::min<size_t>(8, (share - used) / set) : 0;
-        };
-        while (per_sm > 1 && stages_of(per_sm) < 2) --per_sm;
-        p.stages = stages_of(per_sm);
-        p.grid = (int)std::min<int64_t>(rows, (int64_t)sm * per_sm);
-        p.smem = 128 + tables + (size_t)p.stages * set;
-        if (p.stages < 1) return generic_plan();
-    }
-    if (vjp && p.kind == BLOCK_WARP)  // scratch traffic small beside the rows'
-        p.grid = (int)std::min<int64_t>(p.grid, std::max<int64_t>(sm, rows / 12));
-    if (vjp && p.kind == BLOCK_STAGED) {
-        // A CTA's partial rows are 24 bytes a column, written and read in L2, a row 12
-        // from and to memory: fewer rows a CTA the fewer its threads, whose waits
-        // other CTAs must fill.
-        const int64_t least = std::max<int64_t>(2, threads / 32);
-        p.grid = (int)std::min<int64_t>(p.grid, std::max<int64_t>(sm, rows / least));
-    }
-    // Rows of 8 KB or more are dealt out to the CTAs in turn, so that all of them work
-    // on neighbouring memory: one row at a time in the VJP, 32 KB of them in the
-    // forward while each CTA gets eight such chunks (16384 rows of bf16, D = 8192:
-    // 183 us in one run a CTA, 169 dealt out singly, 166 in twos; 4096: 96, 91, and
-    // 87 in fours; VJP 4096: 135.0 and 132.8).  Shorter rows lose by it (D = 1024:
-    // 25 us in runs, 29 dealt out).  With a gate, its rows' CTAs must come out even
-    // enough.
-    p.team = p.kind != BLOCK_DIRECT && row >= 8192 && !(vjp && gates * 8 > p.grid);
-    while (p.team && !vjp && (row << (p.chunk_shift + 1)) <= 32768 &&
-           ((int64_t)p.grid << (p.chunk_shift + 1)) * 8 <= rows)
-        ++p.chunk_shift;
-    return p;
-}
 
 // The largest power of two up to 16 that divides the address and row stride.
 int unit_of(const Mat &m, int64_t rows, int es) {
@@ -207,7 +120,7 @@ extern "C" int rmsnorm_block_fwd(const void *y, int64_t ld_y, const void *residu
     for (const Mat *m : {&my, &mr, &mo, &mn}) unit = std::min(unit, unit_of(*m, rows, es));
     unit = std::min({unit, unit_of(mg, gate_rows, es), unit_of(Mat{w_pre, 0}, 1, es), unit_of(Mat{w_post, 0}, 1, es)});
     const bool per_row = gate && gate_rows == rows;
-    const BlockPlan p = make_plan(rows, D, es, unit, per_row ? 3 : 2, false, 1, sm);
+    const BlockPlan p = make_block_plan(rows, D, es, unit, per_row ? 3 : 2, false, 1, sm);
     a.stages = p.stages;
     a.stage_bytes = p.stage_bytes;
     a.chunk_shift = p.chunk_shift;
@@ -311,7 +224,7 @@ int block_vjp(const void *y, int64_t ld_y, const void *h, int64_t ld_h, const vo
                      unit_of(Mat{w_post, 0}, 1, es), unit_of(Mat{g_gate, 0}, 1, 4)});
     const bool per_row = gate && gate_rows == rows;
     const int64_t gates = gate && !per_row ? gate_rows : 1;  // gate rows with sums of their own
-    const BlockPlan p = make_plan(rows, D, es, unit, 3 + (g_residual != nullptr) + per_row, true, gates, sm);
+    const BlockPlan p = make_block_plan(rows, D, es, unit, 3 + (g_residual != nullptr) + per_row, true, gates, sm);
     a.stages = p.stages;
     a.stage_bytes = p.stage_bytes;
     a.chunk_shift = p.chunk_shift;
@@ -368,5 +281,5 @@ extern "C" size_t rmsnorm_block_vjp_workspace_size(int64_t rows, int64_t D, int 
     int sm = 0;
     if (check_common(rows, D, dtype, 0.f, 0.f) != RMSNORM_OK || rows == 0 || current_sm_count(&sm) != RMSNORM_OK)
         return 0;
-    return scratch_bytes(make_plan(rows, D, esize_of(dtype), 16, 3, true, 1, sm).grid, D);
+    return scratch_bytes(make_block_plan(rows, D, esize_of(dtype), 16, 3, true, 1, sm).grid, D);
 }

@@ -6,9 +6,12 @@
 // barrier, although the second norm's depends on the first's:
 //   forward: with v = m y, m = scale * gate * w2, sum h^2 = sum res^2 + 2 r_y sum
 //     res v + r_y^2 sum v^2.  Where the block nearly undoes the stream (the
-//     result is below an eighth of its terms) it is summed again from h itself.
+//     result is below an eighth of its terms), or v^2 is out of fp32's range, it is
+//     summed again from h itself.
 //   VJP: sum m g_h y = r_h (sum u g w1 - c sum u h) + sum u g_res, u = m y: the
-//     same terms as its own sum has, so no digits are lost.
+//     same terms as its own sum has, so no digits are lost.  u g w1 and u h must
+//     stay in fp32's range (a second way through, as in the forward, cost the
+//     instances without FULL 150 to 500 bytes of spills a thread).
 //
 //   BLOCK_STAGED  one row a CTA at a time out of a shared-memory ring that thread
 //                 0 fills with 1-D bulk copies `stages` rows ahead, so that the
@@ -21,12 +24,13 @@
 //   BLOCK_WARP    one row a warp (short rows): no barriers; several rows a CTA.
 //
 // w1 = weight_bias + w_pre sits in shared memory in fp32 (in registers the VJP
-// spilled), or packed in registers where a thread sees few rows; m = scale * gate * (weight_bias + w_post) of a thread's columns in
-// its registers (m is rebuilt when the CTA's rows pass to
-// another gate row; with a gate row per row, the gate streams with the row and
-// m holds the rest), the VJP's two accumulators of its columns.
+// spilled), or packed in registers where a thread sees few rows.  In registers,
+// for a thread's columns: m = scale * gate * (weight_bias + w_post), rebuilt when
+// the CTA's rows pass to another gate row (with a gate row per row, the gate
+// streams with the row and m holds the rest), and the VJP's two accumulators.
 #pragma once
 
+#include <cfloat>
 #include <type_traits>
 
 #include "block.h"
@@ -68,9 +72,6 @@ template <typename T, int UB> struct Slot {
         } else {
             f[0] = Cvt<T>::unpack2(v);
         }
-    }
-    static __device__ __forceinline__ void load_pairs(const void *row, int u, int NT, int NU, float2 (&f)[P]) {
-        unpack(load(row, u, NT, NU), f);
     }
     static __device__ __forceinline__ void store(void *row, int u, int NT, int NU, const float2 (&f)[P]) {
         Unit *p = static_cast<Unit *>(row);
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
     Raw vw[KIND == BLOCK_STAGED ? 1 : V];
     float2 m[V][P];  // without the gate if it has a row for each row
     auto load_unit = [&](const void *base, int u, float2 (&f)[P]) {
-        SL::load_pairs(base, u, NT, NU, f);
+        SL::unpack(SL::load(base, u, NT, NU), f);
     };
     auto load_m = [&](const T *gate_row) {
 #pragma unroll
@@ -447,7 +448,11 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
 #pragma unroll
             for (int p = 0; p < P; ++p) h[p] = f2fma(v[p], both(r_y), r[p]);
         };
-        if (!(ss * 8.f >= sum[1] + tail)) {  // the same in every thread of the row
+        // Also where v^2 left fp32's range on either side (below: the 2^-126 that a sum
+        // of subnormals may be off by shows in the result).  The same in every thread
+        // of the row.
+        const float terms = sum[1] + tail;
+        if (!(ss * 8.f >= terms && terms <= FLT_MAX) || r_y * r_y * 0x1p-100f > terms + (float)a.D * a.eps) {
             float2 t2 = both(0.f);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -570,7 +575,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
     Raw vw[KIND == BLOCK_STAGED ? 1 : V];
     float2 m[V][P], acc_pre[V][P], acc_mid[V][P];
     auto load_unit = [&](const void *base, int u, float2 (&f)[P]) {
-        SL::load_pairs(base, u, NT, NU, f);
+        SL::unpack(SL::load(base, u, NT, NU), f);
     };
     auto load_m = [&](const T *gate_row) {
 #pragma unroll

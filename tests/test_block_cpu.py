@@ -62,52 +62,154 @@ SPLIT = r"""
 #include <cstdio>
 #include <cstdlib>
 #include <vector>
-#include "block.h"
+#include "block_plan.h"
 using namespace rmsn;
+
+// Every row is one CTA's, and the second stage finds every part of every gate row.
+int check(const BlockArgs &a, int64_t grid, int64_t G) {
+    const int64_t rpg = a.rows_per_gate, q = a.split_q, r = a.split_r;
+    std::vector<int> seen(a.rows, 0), written(2 * grid, -1);
+    for (int64_t c = 0; c < grid; ++c) {
+        const RowDeal d = vjp_rows(a, c);
+        if (d.n < 1) return 1;
+        for (int64_t seg = 0; seg < d.n;) {
+            const int64_t gr = gate_row(d.row(seg), rpg);
+            int64_t end = seg;
+            for (; end < d.n && gate_row(d.row(end), rpg) == gr; ++end) ++seen[d.row(end)];
+            if (end - seg != rpg) {
+                const int64_t s = mid_slot(c, seg == 0);
+                if (s < 0 || s >= 2 * grid || written[s] != -1) return 2;
+                written[s] = (int)gr;
+            }
+            seg = end;
+        }
+        if (a.team && gate_row(d.row(0), rpg) != gate_row(d.row(d.n - 1), rpg)) return 3;
+    }
+    for (int n : seen) if (n != 1) return 4;
+    for (int64_t gr = 0; gr < G; ++gr) {
+        int64_t c0, c1;
+        if (a.team) {
+            c0 = split_first(gr, q, r);
+            c1 = split_first(gr + 1, q, r) - 1;
+        } else {
+            c0 = split_part<int64_t>(gr * rpg, q, r);
+            c1 = split_part<int64_t>(gr * rpg + rpg - 1, q, r);
+        }
+        if (c0 == c1) continue;
+        for (int64_t c = c0; c <= c1; ++c) {
+            const int64_t s = mid_slot(c, c > c0 || a.team || split_first(c0, q, r) / rpg == gr);
+            if (written[s] != gr) return 5;
+            written[s] = -1;
+        }
+    }
+    for (int w : written) if (w != -1) return 6;  // and no part is left over
+    return 0;
+}
+
 int main() {
     srand(1);
     for (int it = 0; it < 20000; ++it) {
-        const int64_t G = 1 + rand() % 40, rpg = 1 + rand() % 50, rows = G * rpg;
-        const int64_t grid = 1 + rand() % (rows < 60 ? rows : 60), q = rows / grid, r = rows % grid;
-        std::vector<int> written(2 * grid, -1);
-        if (first_row(0, q, r) != 0 || first_row(grid, q, r) != rows) return 1;
-        // the second stage's own arithmetic: the CTA that takes row i
-        auto cta_of = [&](int64_t i) { return i < r * (q + 1) ? i / (q + 1) : r + (i - r * (q + 1)) / q; };
+        BlockArgs a{};
+        const int64_t G = 1 + rand() % 40;
+        a.rows_per_gate = 1 + rand() % 50;
+        a.rows = G * a.rows_per_gate;
+        const int64_t grid = 1 + rand() % (a.rows < 60 ? a.rows : 60);
+        a.team = grid >= 8 * G && rand() % 2;
+        a.rows_per_team = a.rows / G;
+        a.split_q = a.team ? grid / G : a.rows / grid;
+        a.split_r = a.team ? grid % G : a.rows % grid;
+        if (split_first(0, a.split_q, a.split_r) != 0) return 10;
+        if (const int e = check(a, grid, G)) return 20 + e;
+        // the forward's deal, in chunks
+        a.team = rand() % 2;
+        a.chunk_shift = rand() % 4;
+        a.split_q = a.rows / grid;
+        a.split_r = a.rows % grid;
+        std::vector<int> seen(a.rows, 0);
         for (int64_t c = 0; c < grid; ++c) {
-            const int64_t r0 = first_row(c, q, r), r1 = first_row(c + 1, q, r);
-            if (r1 <= r0) return 2;
-            for (int64_t i = r0; i < r1; ++i) {
-                if (cta_of(i) != c || gate_row(i, rpg) != i / rpg) return 3;
-                const int64_t gr = i / rpg;
-                if (gr * rpg >= r0 && (gr + 1) * rpg <= r1) continue;  // whole
-                const int64_t s = mid_slot(c, gr, q, r, rpg);
-                if (s < 0 || s >= 2 * grid || (written[s] != -1 && written[s] != gr)) return 4;
-                written[s] = (int)gr;
+            const RowDeal d = fwd_rows(a, c, grid);
+            for (int64_t i = 0; i < d.n; ++i) {
+                if (d.row(i) < 0 || d.row(i) >= a.rows) return 30;
+                ++seen[d.row(i)];
             }
         }
-        for (int64_t gr = 0; gr < G; ++gr) {  // the second stage finds every part
-            const int64_t c0 = cta_of(gr * rpg), c1 = cta_of((gr + 1) * rpg - 1);
-            if (c0 == c1) continue;
-            if (written[mid_slot(c0, gr, q, r, rpg)] != gr) return 5;
-            for (int64_t c = c0 + 1; c <= c1; ++c) {
-                if (written[2 * c] != gr) return 6;
-                written[2 * c] = -1;
-            }
-            written[mid_slot(c0, gr, q, r, rpg)] = -1;
-        }
-        for (int w : written) if (w != -1) return 7;  // and no part is left over
+        for (int n : seen) if (n != 1) return 31;
         const int64_t big = ((int64_t)1 << 40) + rand(), per = 1 + rand();
-        if (gate_row(big, per) != big / per) return 8;
+        if (gate_row(big, per) != big / per) return 32;
     }
     return 0;
 }
 """
 
+PLAN = r"""
+#include <cstdio>
+#include "block_plan.h"
+using namespace rmsn;
+int main() {
+    const int sms[] = {1, 2, 132, 152};
+    for (int64_t D = 1; D <= 40000; D += D < 1100 ? 1 : D < 9000 ? 7 : 61)
+        for (int64_t rows : {1, 2, 7, 151, 300, 305, 1217, 5000, 16384, 1000000})
+            for (int es : {2, 4})
+                for (int vjp = 0; vjp < 2; ++vjp)
+                    for (int sm : sms) {
+                        const int asked = make_block_plan(rows, D, es, 16, 3, true, 1, sm).grid;
+                        for (int tensors = vjp ? 3 : 2; tensors <= (vjp ? 5 : 3); ++tensors)
+                            for (int unit : {16, 8, 4, 2})
+                                for (int64_t gates : {(int64_t)1, (int64_t)5, rows}) {
+                                    if (unit < es) continue;
+                                    const BlockPlan p = make_block_plan(rows, D, es, unit, tensors, vjp, gates, sm);
+                                    const char *why = nullptr;
+                                    if (p.grid < 1 || p.grid > rows) why = "grid";
+                                    if (vjp && p.grid > asked) why = "more scratch than the size asked beforehand";
+                                    if (p.kind != BLOCK_GENERIC) {
+                                        const int64_t lanes = p.kind == BLOCK_WARP ? 32 : p.threads;
+                                        const int per = p.half ? 16 : 32;
+                                        if (p.threads < 32 || p.threads > 1024 || p.threads % 32) why = "threads";
+                                        if (lanes * per < D * es) why = "a row does not fit its threads";
+                                        if (D * es % p.ub || (p.ub != 16 && p.ub != 4 && p.ub != 2)) why = "unit";
+                                        if (p.half && (!vjp || p.kind != BLOCK_STAGED)) why = "half";
+                                        if (p.half && p.threads > 640) why = "half's threads";
+                                    }
+                                    if (p.kind == BLOCK_STAGED) {
+                                        if (p.stages < 1 || p.stages > 8) why = "stages";
+                                        if (p.smem > 227 * 1024) why = "shared memory";
+                                        if (p.stage_bytes % 16 || p.stage_bytes < D * es + (p.ub == 16 ? 0 : 15)) why = "stage";
+                                        if (8 * p.stages > 128) why = "barriers";
+                                    }
+                                    if (p.kind == BLOCK_WARP && vjp &&
+                                        p.smem != (size_t)p.threads / 32 * ((D + 3) / 4 * 16)) why = "warps' rows";
+                                    if (p.kind == BLOCK_DIRECT && p.grid != rows) why = "direct";
+                                    if (p.team && vjp && gates * 8 > p.grid) why = "team";
+                                    if (p.kind == BLOCK_GENERIC && p.team) why = "generic team";
+                                    if (p.chunk_shift && ((int64_t)p.grid << p.chunk_shift) > rows) why = "chunk";
+                                    if (why) {
+                                        printf("%s: rows %ld D %ld es %d vjp %d unit %d tensors %d gates %ld sm %d: kind %d grid %d "
+                                               "threads %d stages %d\n", why, (long)rows, (long)D, es, vjp, unit, tensors,
+                                               (long)gates, sm, p.kind, p.grid, p.threads, p.stages);
+                                        return 1;
+                                    }
+                                }
+                    }
+    return 0;
+}
+"""
+
+
+def _run(tmp_path, name, text):
+    src, exe = tmp_path / (name + ".cu"), tmp_path / name
+    src.write_text(text)
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    subprocess.run([nvcc, "-std=c++17", "-O2", "-I" + os.path.join(ROOT, "rmsnorm_fwd_bwd_add_gb300", "csrc"), "-o",
+                    str(exe), str(src)], check=True, capture_output=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, (r.returncode, r.stdout)
+
 
 def test_row_split_and_partial_slots(tmp_path):
-    src, exe = tmp_path / "split.cu", tmp_path / "split"
-    src.write_text(SPLIT)
-    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
-    subprocess.run([nvcc, "-std=c++17", "-I" + os.path.join(ROOT, "rmsnorm_fwd_bwd_add_gb300", "csrc"), "-o",
-                    str(exe), str(src)], check=True, capture_output=True)
-    assert subprocess.run([str(exe)]).returncode == 0
+    _run(tmp_path, "split", SPLIT)
+
+
+def test_plans_stay_within_the_chip_and_the_workspace(tmp_path):
+    """Every plan fits its threads, ring and shared memory, and the VJP's never has
+    more CTAs than the workspace query counted on."""
+    _run(tmp_path, "plan", PLAN)

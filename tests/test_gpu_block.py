@@ -383,3 +383,81 @@ def test_block_vjp_scratch():
                     call(lib.rmsnorm_block_vjp_ws, p["y"].data_ptr(), rows * D * 2 + n)):
         assert st in (1, 4) and all((t == 5).all() for t in out)
     assert lib.rmsnorm_block_vjp_workspace_size(0, D, 1) == 0 == lib.rmsnorm_block_vjp_workspace_size(4, 0, 1)
+
+
+@pytest.mark.parametrize("rows,D,groups,pad,off", [(400, 5120, 0, 0, 0), (400, 5120, 400, 0, 0), (333, 5000, 3, 4, 0),
+                                                   (305, 5120, 5, 0, 1), (400, 10240, 4, 0, 0), (310, 10250, 310, 0, 0)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_block_wide_ctas(rows, D, groups, pad, off, dt):
+    """Rows whose CTAs are just past half or all of an SM's threads."""
+    for saved in (False, True):
+        p = _problem(rows, D, DT[dt], groups, True, 0.0, pad, off, seed=11 + saved)
+        _check_fwd(p, 0.9)
+        _check_vjp(p, 0.9, saved=saved)
+
+
+@pytest.mark.parametrize("D", [384, 4096, 4099, 20000])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("y_std,gate_std,res_std", [(1e12, 1e12, 1e12), (1e-15, 1e-10, 1e-10), (1e-15, 1e-10, 0.0)])
+def test_block_fwd_terms_past_fp32(D, dt, y_std, gate_std, res_std):
+    """Rows whose norms are in fp32's range while the square of gate * y is not: it
+    overflows, or (with no epsilon to hide it) vanishes."""
+    g = torch.Generator().manual_seed(D)
+    rows = 330
+    y, res = (_rand(g, rows, D, DT[dt], std=s) for s in (y_std, res_std))
+    gate = _rand(g, 1, D, DT[dt], std=gate_std)
+    w_post, w_pre = (_rand(g, 1, D, DT[dt], std=0.2, mean=1.0)[0] for _ in range(2))
+    out, h, _ = rn.rmsnorm_block_fwd(y, res, w_post, w_pre, 0.0, 0.0, gate)
+    want_out, want_h, _, t_out, t_h, _ = ref.fwd(y, res, w_post, w_pre, 0.0, 0.0, gate, 1.0)
+    ref.check("new_residual", h, want_h, t_h)
+    ref.check("out", out, want_out, t_out)
+
+
+def test_block_wait_timeout_is_reported_and_context_survives():
+    """A row whose copies are never issued: the wait ends, the status says so, and
+    the next calls are right."""
+    p = _problem(2000, 4096, torch.bfloat16, 4, True, 0.0, seed=3)
+    rn.rmsnorm_device_status(clear=True)
+    for backward in (False, True):
+        rn.rmsnorm_debug_inject(drop_tile=1501, budget_cycles=2_000_000)
+        try:
+            if backward:
+                rn.rmsnorm_block_vjp(p["y"], p["h"], p["w_post"], p["w_pre"], p["g"], EPS, 0.0, p["gate"], 1.0, p["g_res"])
+            else:
+                rn.rmsnorm_block_fwd(p["y"], p["res"], p["w_post"], p["w_pre"], EPS, 0.0, p["gate"])
+            bits = rn.rmsnorm_device_status(clear=True)
+        finally:
+            rn.rmsnorm_debug_inject(-1, 0)
+        assert bits & rn.DEVSTATUS_WAIT_TIMEOUT
+        _check_fwd(p, 1.0)
+        _check_vjp(p, 1.0)
+        assert rn.rmsnorm_device_status(clear=True) == 0
+
+
+def test_block_calls_of_two_threads():
+    """Two host threads, each with its own stream and problem, at once."""
+    import threading
+    problems = [_problem(3000, 4096, torch.bfloat16, 5, True, 0.0, seed=21), _problem(2000, 1024, torch.float16, 200, True, 0.0, seed=22)]
+
+    def both(p):
+        return rn.rmsnorm_block_fwd(p["y"], p["res"], p["w_post"], p["w_pre"], EPS, 0.0, p["gate"], rstd=True) + \
+            rn.rmsnorm_block_vjp(p["y"], p["h"], p["w_post"], p["w_pre"], p["g"], EPS, 0.0, p["gate"], 1.0, p["g_res"])
+
+    want = [both(p) for p in problems]
+    torch.cuda.synchronize()
+    same = [True, True]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(30):
+                got = both(problems[i])
+                same[i] = same[i] and all(torch.equal(a, b) for a, b in zip(got, want[i]))
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert same == [True, True]

@@ -271,3 +271,29 @@ def test_python_refusals():
         rn.rmsnorm_kv_plan(lens, lens.clone(), table, 0, 4)
     with pytest.raises(rn.RmsnormError):  # new_lens is the output too
         rn.rmsnorm_kv_plan(lens, lens, table, 16, 4)
+
+
+@pytest.mark.parametrize("B,every,T", [(9001, 1, 12000), (9001, 1, 3000), (13000, 2500, 40), (13000, 2500, 9000),
+                                       (4097, 4096, 8)])
+def test_more_requests_than_a_pass(B, every, T):
+    """Several passes of the scan, with tokens in all requests, or in one of
+    `every`, whose neighbours lie further apart than the tokens' table holds."""
+    W, bs, blocks = 3, 4, 2 * B
+    m = Model(B, W, bs, blocks, B)
+    rng = random.Random(every)
+    lens, table = i32([0] * B), torch.full((B, W), -1, dtype=torch.int32, device=DEV)
+    free, count = i32(m.stack), i32([blocks])
+    for step in range(4):
+        done = [rng.random() < 0.4 for _ in range(B)]
+        rn.rmsnorm_kv_release(lens, torch.tensor(done, device=DEV), table, bs, free, count)
+        m.release(done)
+        assert lens.tolist() == m.lens and free[:len(m.stack)].tolist() == m.stack
+        new = [rng.choice([0, 1, 1, 6]) if b % every == 0 else 0 for b in range(B)]
+        got = rn.rmsnorm_kv_plan(lens, i32(new), table, bs, T, free_blocks=free, free_count=count)
+        want = m.plan(new, T)
+        assert got.starts.tolist() == want["starts"]
+        assert got.granted.tolist() == want["granted"]
+        assert got.positions.tolist() == want["pos"]
+        assert got.slots.tolist() == want["slots"]
+        assert got.requests.tolist() == want["req"]
+        assert lens.tolist() == m.lens and count.item() == len(m.stack)
