@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 
 #include "block.h"
 #include "block_plan.h"
@@ -30,6 +31,30 @@ int unit_of(const Mat &m, int64_t rows, int es) {
     if (!m.p) return 16;
     const uintptr_t bits = (uintptr_t)m.p | (rows > 1 ? (uintptr_t)(m.ld * es) : 0) | 16u;
     return (int)(bits & (~bits + 1));
+}
+
+// Whether the tensors' rows all stand alike to 16-byte boundaries: how many rows on
+// they stand like the first again, or 0.
+int classes_of(std::initializer_list<const Mat *> tensors, int64_t rows, int es) {
+    int start = -1, step = 0;
+    for (const Mat *m : tensors) {
+        if (!m->p) continue;
+        const int b = (int)((uintptr_t)m->p & 15u), d = rows > 1 ? (int)((uint64_t)(m->ld * es) & 15u) : 0;
+        if (start >= 0 && (b != start || d != step)) return 0;
+        start = b;
+        step = d;
+    }
+    int classes = 1;
+    while (step * classes % 16) classes *= 2;
+    return classes;
+}
+
+// The runs of rows within a team.
+void set_runs(BlockArgs *a, const BlockPlan &p, int64_t rows, int64_t size) {
+    a->run = p.run;
+    if (!p.run) return;
+    a->run_q = rows / (size / p.run);
+    a->run_r = rows % (size / p.run);
 }
 
 template <typename T> struct Tag { using type = T; };
@@ -120,13 +145,15 @@ extern "C" int rmsnorm_block_fwd(const void *y, int64_t ld_y, const void *residu
     for (const Mat *m : {&my, &mr, &mo, &mn}) unit = std::min(unit, unit_of(*m, rows, es));
     unit = std::min({unit, unit_of(mg, gate_rows, es), unit_of(Mat{w_pre, 0}, 1, es), unit_of(Mat{w_post, 0}, 1, es)});
     const bool per_row = gate && gate_rows == rows;
-    const BlockPlan p = make_block_plan(rows, D, es, unit, per_row ? 3 : 2, false, 1, sm);
+    const int classes = classes_of({&my, &mr, &mo, &mn, per_row ? &mg : &my}, rows, es);
+    const BlockPlan p = make_block_plan(rows, D, es, unit, per_row ? 3 : 2, false, 1, sm, classes);
     a.stages = p.stages;
     a.stage_bytes = p.stage_bytes;
     a.chunk_shift = p.chunk_shift;
     a.team = p.team;
     a.split_q = rows / p.grid;
     a.split_r = rows % p.grid;
+    set_runs(&a, p, rows, p.grid);
     const cudaError_t e = by_type(dtype, [&](auto t) { return launch_block_fwd<typename decltype(t)::type>(p, a, s); });
     return e == cudaSuccess ? RMSNORM_OK : record_cuda_error(e);
 }
@@ -224,7 +251,9 @@ int block_vjp(const void *y, int64_t ld_y, const void *h, int64_t ld_h, const vo
                      unit_of(Mat{w_post, 0}, 1, es), unit_of(Mat{g_gate, 0}, 1, 4)});
     const bool per_row = gate && gate_rows == rows;
     const int64_t gates = gate && !per_row ? gate_rows : 1;  // gate rows with sums of their own
-    const BlockPlan p = make_block_plan(rows, D, es, unit, 3 + (g_residual != nullptr) + per_row, true, gates, sm);
+    const int classes = classes_of({&m[0], &m[1], &m[2], &m[3], &m[4], &m[5], per_row ? &mgate : &m[0]}, rows, es);
+    const BlockPlan p = make_block_plan(rows, D, es, unit, 3 + (g_residual != nullptr) + per_row, true, gates, sm,
+                                        classes);
     a.stages = p.stages;
     a.stage_bytes = p.stage_bytes;
     a.chunk_shift = p.chunk_shift;
@@ -232,6 +261,7 @@ int block_vjp(const void *y, int64_t ld_y, const void *h, int64_t ld_h, const vo
     a.rows_per_team = rows / gates;
     a.split_q = p.team ? p.grid / gates : rows / p.grid;
     a.split_r = p.team ? p.grid % gates : rows % p.grid;
+    set_runs(&a, p, a.rows_per_team, p.grid / gates);
     const size_t need = scratch_bytes(p.grid, D);
     void *ws = workspace;
     if (pooled) {
@@ -281,5 +311,8 @@ extern "C" size_t rmsnorm_block_vjp_workspace_size(int64_t rows, int64_t D, int 
     int sm = 0;
     if (check_common(rows, D, dtype, 0.f, 0.f) != RMSNORM_OK || rows == 0 || current_sm_count(&sm) != RMSNORM_OK)
         return 0;
-    return scratch_bytes(make_block_plan(rows, D, esize_of(dtype), 16, 3, true, 1, sm).grid, D);
+    // rows on 16-byte boundaries, or off them and alike: no other plan has more CTAs
+    const int es = esize_of(dtype);
+    return scratch_bytes(std::max(make_block_plan(rows, D, es, 16, 3, true, 1, sm, 0).grid,
+                                  make_block_plan(rows, D, es, es, 3, true, 1, sm, 1).grid), D);
 }

@@ -104,6 +104,19 @@ template <typename T, int UB> struct Slot {
             if (u + NT < NU) row[u + NT] = f[0].y * k;
         }
     }
+    // The same for a slot whose columns start at `c`, on no boundary (16-byte units).
+    static __device__ __forceinline__ Raw load_columns(const T *p, int c) {
+        T t[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) t[e] = p[c + e];
+        Raw v;
+        memcpy(&v, t, sizeof(v));
+        return v;
+    }
+    static __device__ __forceinline__ void store_floats_at(float *row, int c, const float2 (&f)[P], float k) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) row[c + e] = (e & 1 ? f[e / 2].y : f[e / 2].x) * k;
+    }
     // A per-column table in shared memory, laid out so that a warp's lanes read
     // consecutive 16- or 8-byte words: [pairs of pairs][units] (E >= 4), [units].
     static __device__ __forceinline__ void put(float *tab, int u, int NT, int NU, const float2 (&f)[P]) {
@@ -139,7 +152,7 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 constexpr int BLOCK_MAX_STAGES = 8;
 // Shared memory of BLOCK_STAGED: the ring's mbarriers, the table w1, the ring.
 constexpr int BLOCK_HEADER = 128;
-__host__ __device__ constexpr uint32_t block_table_bytes(int D) { return ((uint32_t)D * 4u + 127u) & ~127u; }
+
 
 // Sums of four (N <= 4) or eight (N <= 8) values over a warp at once.  The first
 // steps halve the number of values a lane carries instead of summing each over
@@ -250,7 +263,7 @@ template <typename V> __device__ __forceinline__ void keep_packed(V &v) {
 }
 
 // Forward -----------------------------------------------------------------
-template <typename T, int UB, int MAXT, int MINB, int KIND, bool GROW>
+template <typename T, int UB, int MAXT, int MINB, int KIND, bool GROW, bool SHIFT>
 __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_constant__ BlockArgs a) {
     using SL = Slot<T, UB>;
     using Raw = typename SL::Raw;
@@ -260,15 +273,21 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
     const int NT = KIND == BLOCK_WARP ? 32 : (int)blockDim.x;
     const int t0 = KIND == BLOCK_WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
     const int R = KIND == BLOCK_WARP ? (int)(blockDim.x >> 5) : 1;
-    const int NU = a.D / E, nw = (int)(blockDim.x >> 5);
-    const float inv_D = 1.0f / (float)a.D;
+    const int D = a.D, nw = (int)(blockDim.x >> 5);
+    const float inv_D = 1.0f / (float)D;
     constexpr bool per_row = GROW;  // a gate row for each row
     const bool post = a.w_post != nullptr;
     const RowDeal deal = fwd_rows(a, blockIdx.x, gridDim.x);
+    // SHIFT: `hd` columns before a row's first 16-byte boundary, the same for all of
+    // this CTA's rows; thread t0 also has column cx, one of those or of the rest behind
+    // the last unit.
+    const int hd = SHIFT ? (int)(-((uintptr_t)(static_cast<const T *>(a.y) + deal.row(0) * a.ld_y)) & 15u) / (int)sizeof(T) : 0;
+    const int NU = SHIFT ? min((D - hd) / E, V * NT) : D / E;
+    const int cx = !SHIFT || t0 >= D - NU * E ? -1 : t0 < hd ? t0 : NU * E + t0;
 
     const void *src[5] = {a.y, a.res, per_row ? a.gate : nullptr, nullptr, nullptr};
     const int64_t ld[5] = {a.ld_y, a.ld_res, a.ld_gate, 0, 0};
-    BlockRing ring{reinterpret_cast<uint64_t *>(smem), smem + BLOCK_HEADER + block_table_bytes(a.D), a.stages, a.stage_bytes, per_row ? 3 : 2};
+    BlockRing ring{reinterpret_cast<uint64_t *>(smem), smem + BLOCK_HEADER + block_table_bytes(D), a.stages, a.stage_bytes, per_row ? 3 : 2};
     uint64_t policy = 0;
     if constexpr (KIND == BLOCK_STAGED) {
         policy = l2_evict_first_policy();
@@ -288,6 +307,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
     // A row's slots; the first row's loads go ahead of the weights' where no ring does.
     const int ry = KIND == BLOCK_WARP ? (int)(threadIdx.x >> 5) : 0;
     Raw vy[V], vr[V], vg[GROW ? V : 1];
+    float xy = 0.f, xr = 0.f, xg = 1.f;  // of column cx
     auto fetch = [&](const T *py, const T *pr, const T *pg) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -298,10 +318,16 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
                 if constexpr (GROW) vg[j] = SL::load(pg, u, NT, NU);
             }
         }
+        if constexpr (SHIFT)
+            if (cx >= 0) {
+                xy = Cvt<T>::load1(py + (cx - hd));
+                xr = Cvt<T>::load1(pr + (cx - hd));
+                if constexpr (GROW) xg = Cvt<T>::load1(pg + (cx - hd));
+            }
     };
     auto fetch_global = [&](int64_t row) {
-        fetch(static_cast<const T *>(a.y) + row * a.ld_y, static_cast<const T *>(a.res) + row * a.ld_res,
-              per_row ? static_cast<const T *>(a.gate) + row * a.ld_gate : nullptr);
+        fetch(static_cast<const T *>(a.y) + row * a.ld_y + hd, static_cast<const T *>(a.res) + row * a.ld_res + hd,
+              per_row ? static_cast<const T *>(a.gate) + row * a.ld_gate + hd : nullptr);
     };
     if constexpr (KIND != BLOCK_STAGED)
         if (ry < deal.n) fetch_global(deal.row(ry));
@@ -309,9 +335,12 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
     float *table = reinterpret_cast<float *>(smem + BLOCK_HEADER);
     Raw vw[KIND == BLOCK_STAGED ? 1 : V];
     float2 m[V][P];  // without the gate if it has a row for each row
-    auto load_unit = [&](const void *base, int u, float2 (&f)[P]) {
-        SL::unpack(SL::load(base, u, NT, NU), f);
+    float xm = 0.f, xw = 0.f;  // m and w1 of column cx
+    auto load_raw = [&](const void *base, int u) {  // of a row of weights or a gate row
+        if constexpr (SHIFT) return SL::load_columns(static_cast<const T *>(base), hd + u * E);
+        else return SL::load(base, u, NT, NU);
     };
+    auto load_unit = [&](const void *base, int u, float2 (&f)[P]) { SL::unpack(load_raw(base, u), f); };
     auto load_m = [&](const T *gate_row) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -326,12 +355,18 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
                                     gate_row ? f2mul(both(a.scale), q[p]) : both(a.scale));
             }
         }
+        if constexpr (SHIFT)
+            if (cx >= 0)
+                xm = (post ? a.weight_bias + Cvt<T>::load1(static_cast<const T *>(a.w_post) + cx) : 1.f) *
+                     (gate_row ? a.scale * Cvt<T>::load1(gate_row + cx) : a.scale);
     };
+    if constexpr (SHIFT)
+        if (cx >= 0) xw = a.weight_bias + Cvt<T>::load1(static_cast<const T *>(a.w_pre) + cx);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int u = SL::unit(j, t0, NT);
         if (u < NU) {
-            const Raw w = SL::load(a.w_pre, u, NT, NU);
+            const Raw w = load_raw(a.w_pre, u);
             if constexpr (KIND == BLOCK_STAGED) {  // a thread reads only what it wrote itself
                 float2 f[P];
                 SL::unpack(w, f);
@@ -355,6 +390,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
         }
     };
 
+
     int64_t group_end = a.gate && !per_row ? 0 : INT64_MAX;  // first row past the gate row held in m
     int s = 0;
     uint32_t ph = 0;
@@ -370,7 +406,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
             const unsigned char *st = ring.data + (size_t)s * ring.tensors * ring.stage_bytes;
             auto staged = [&](const void *base, int64_t ld) {
                 const uintptr_t p = (uintptr_t)(static_cast<const T *>(base) + row * ld);
-                const T *q = reinterpret_cast<const T *>(st + (p & 15u));
+                const T *q = reinterpret_cast<const T *>(st + (p & 15u)) + hd;
                 st += ring.stage_bytes;
                 return q;
             };
@@ -407,6 +443,14 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
                 }
             }
         }
+        const float xv = SHIFT ? xm * xy * (GROW ? xg : 1.f) : 0.f;  // v of column cx
+        if constexpr (SHIFT)
+            if (cx >= 0) {
+                s2[0].x = fmaf(xy, xy, s2[0].x);
+                s2[1].x = fmaf(xr, xr, s2[1].x);
+                s2[2].x = fmaf(xr, xv, s2[2].x);
+                s2[3].x = fmaf(xv, xv, s2[3].x);
+            }
         float sum[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] = s2[i].x + s2[i].y;
@@ -463,6 +507,11 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
                     for (int p = 0; p < P; ++p) t2 = f2fma(h[p], h[p], t2);
                 }
             }
+            if constexpr (SHIFT)
+                if (cx >= 0) {
+                    const float h = fmaf(xv, r_y, xr);
+                    t2.x = fmaf(h, h, t2.x);
+                }
             float one[1] = {t2.x + t2.y};
             if constexpr (KIND == BLOCK_WARP) {
                 one[0] = group_sum<32>(one[0]);
@@ -481,14 +530,20 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
             if (u < NU) {
                 float2 h[P];
                 joined(j, h);
-                SL::store(nres, u, NT, NU, h);
                 float2 w[P];
                 w1_of(j, u, w);
 #pragma unroll
-                for (int p = 0; p < P; ++p) h[p] = f2mul(f2mul(h[p], both(r_h)), w[p]);
-                SL::store(out, u, NT, NU, h);
+                for (int p = 0; p < P; ++p) w[p] = f2mul(f2mul(h[p], both(r_h)), w[p]);
+                SL::store(nres + hd, u, NT, NU, h);
+                SL::store(out + hd, u, NT, NU, w);
             }
         }
+        if constexpr (SHIFT)
+            if (cx >= 0) {
+                const float h = fmaf(xv, r_y, xr);
+                Cvt<T>::store1(nres + cx, h);
+                Cvt<T>::store1(out + cx, h * r_h * xw);
+            }
         if (a.rstd && t0 == 0) {
             a.rstd[row] = r_y;
             a.rstd[a.rows + row] = r_h;
@@ -507,7 +562,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
 // VJP -----------------------------------------------------------------------
 // FULL: a norm after the block, g_res and saved scales are all there.  HALF: 16 bytes
 // of a row a thread instead of 32.
-template <typename T, int UB, int MAXT, int MINB, int KIND, bool GROW, bool FULL, bool HALF>
+template <typename T, int UB, int MAXT, int MINB, int KIND, bool GROW, bool SHIFT, bool FULL, bool HALF>
 __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_constant__ BlockArgs a) {
     using SL = Slot<T, UB>;
     using Raw = typename SL::Raw;
@@ -518,17 +573,23 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
     const int t0 = KIND == BLOCK_WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
     const int R = KIND == BLOCK_WARP ? (int)(blockDim.x >> 5) : 1;
     const int ry = KIND == BLOCK_WARP ? (int)(threadIdx.x >> 5) : 0;
-    const int D = a.D, NU = D / E, nw = (int)(blockDim.x >> 5);
+    const int D = a.D, nw = (int)(blockDim.x >> 5);
     const float inv_D = 1.0f / (float)D;
     constexpr bool per_row = GROW;  // a gate row for each row
     const bool post = FULL || a.w_post != nullptr, more = FULL || a.g_res != nullptr;
     const bool saved = FULL || a.rstd != nullptr;
     const int64_t cta = blockIdx.x;
     const RowDeal deal = vjp_rows(a, cta);
+    // SHIFT: `hd` columns before a row's first 16-byte boundary, the same for all of
+    // this CTA's rows; thread t0 also has column cx, one of those or of the rest behind
+    // the last unit.
+    const int hd = SHIFT ? (int)(-((uintptr_t)(static_cast<const T *>(a.y) + deal.row(0) * a.ld_y)) & 15u) / (int)sizeof(T) : 0;
+    const int NU = SHIFT ? min((D - hd) / E, V * NT) : D / E;
+    const int cx = !SHIFT || t0 >= D - NU * E ? -1 : t0 < hd ? t0 : NU * E + t0;
 
     const void *src[5] = {a.y, a.res, a.g, a.g_res, per_row ? a.gate : nullptr};
     const int64_t ld[5] = {a.ld_y, a.ld_res, a.ld_g, a.ld_g_res, a.ld_gate};
-    BlockRing ring{reinterpret_cast<uint64_t *>(smem), smem + BLOCK_HEADER + block_table_bytes(a.D), a.stages, a.stage_bytes,
+    BlockRing ring{reinterpret_cast<uint64_t *>(smem), smem + BLOCK_HEADER + block_table_bytes(D), a.stages, a.stage_bytes,
                    3 + more + per_row};
     uint64_t policy = 0;
     if constexpr (KIND == BLOCK_STAGED) {
@@ -548,6 +609,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
 
     // A row's slots; the first row's loads go ahead of the weights' where no ring does.
     Raw vy[V], vh[V], vg[V], vr[V], va[GROW ? V : 1];
+    float xy = 0.f, xh = 0.f, xg = 0.f, xr = 0.f, xa = 1.f;  // of column cx
     auto fetch = [&](const T *py, const T *ph, const T *pg, const T *pr, const T *pa) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -560,12 +622,20 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                 if constexpr (GROW) va[j] = SL::load(pa, u, NT, NU);
             }
         }
+        if constexpr (SHIFT)
+            if (cx >= 0) {
+                xy = Cvt<T>::load1(py + (cx - hd));
+                xh = Cvt<T>::load1(ph + (cx - hd));
+                xg = Cvt<T>::load1(pg + (cx - hd));
+                if (more) xr = Cvt<T>::load1(pr + (cx - hd));
+                if constexpr (GROW) xa = Cvt<T>::load1(pa + (cx - hd));
+            }
     };
     auto fetch_global = [&](int64_t row) {
-        fetch(static_cast<const T *>(a.y) + row * a.ld_y, static_cast<const T *>(a.res) + row * a.ld_res,
-              static_cast<const T *>(a.g) + row * a.ld_g,
-              more ? static_cast<const T *>(a.g_res) + row * a.ld_g_res : nullptr,
-              per_row ? static_cast<const T *>(a.gate) + row * a.ld_gate : nullptr);
+        fetch(static_cast<const T *>(a.y) + row * a.ld_y + hd, static_cast<const T *>(a.res) + row * a.ld_res + hd,
+              static_cast<const T *>(a.g) + row * a.ld_g + hd,
+              more ? static_cast<const T *>(a.g_res) + row * a.ld_g_res + hd : nullptr,
+              per_row ? static_cast<const T *>(a.gate) + row * a.ld_gate + hd : nullptr);
     };
     if constexpr (KIND != BLOCK_STAGED)
         if (ry < deal.n) fetch_global(deal.row(ry));
@@ -574,9 +644,12 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
     float *table = reinterpret_cast<float *>(smem + BLOCK_HEADER);
     Raw vw[KIND == BLOCK_STAGED ? 1 : V];
     float2 m[V][P], acc_pre[V][P], acc_mid[V][P];
-    auto load_unit = [&](const void *base, int u, float2 (&f)[P]) {
-        SL::unpack(SL::load(base, u, NT, NU), f);
+    float xm = 0.f, xw = 0.f, x_pre = 0.f, x_mid = 0.f;  // of column cx
+    auto load_raw = [&](const void *base, int u) {  // of a row of weights or a gate row
+        if constexpr (SHIFT) return SL::load_columns(static_cast<const T *>(base), hd + u * E);
+        else return SL::load(base, u, NT, NU);
     };
+    auto load_unit = [&](const void *base, int u, float2 (&f)[P]) { SL::unpack(load_raw(base, u), f); };
     auto load_m = [&](const T *gate_row) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -591,12 +664,18 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                                     gate_row ? f2mul(both(a.scale), q[p]) : both(a.scale));
             }
         }
+        if constexpr (SHIFT)
+            if (cx >= 0)
+                xm = (post ? a.weight_bias + Cvt<T>::load1(static_cast<const T *>(a.w_post) + cx) : 1.f) *
+                     (gate_row ? a.scale * Cvt<T>::load1(gate_row + cx) : a.scale);
     };
+    if constexpr (SHIFT)
+        if (cx >= 0) xw = a.weight_bias + Cvt<T>::load1(static_cast<const T *>(a.w_pre) + cx);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int u = SL::unit(j, t0, NT);
         if (u < NU) {
-            const Raw w = SL::load(a.w_pre, u, NT, NU);
+            const Raw w = load_raw(a.w_pre, u);
             if constexpr (KIND == BLOCK_STAGED) {  // a thread reads only what it wrote itself
                 float2 f[P];
                 SL::unpack(w, f);
@@ -622,9 +701,13 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
         }
     };
 
+    auto store_floats = [&](float *row, int u, const float2 (&f)[P], float k) {
+        if constexpr (SHIFT) SL::store_floats_at(row, hd + u * E, f, k);
+        else SL::store_floats(row, u, NT, NU, f, k);
+    };
     // Writes k times the accumulators to the row dst (BLOCK_WARP: the warps' added
     // in warp order) and clears them.
-    auto flush = [&](float2 (&acc)[V][P], float *dst, float k) {
+    auto flush = [&](float2 (&acc)[V][P], float &extra, float *dst, float k) {
         if (KIND == BLOCK_WARP && R > 1) {
             float *buf = reinterpret_cast<float *>(smem);  // [R][D]
 #pragma unroll
@@ -643,8 +726,11 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int u = SL::unit(j, t0, NT);
-                if (u < NU) SL::store_floats(dst, u, NT, NU, acc[j], k);
+                if (u < NU) store_floats(dst, u, acc[j], k);
             }
+            if constexpr (SHIFT)
+                if (cx >= 0) dst[cx] = extra * k;
+            extra = 0.f;
         }
 #pragma unroll
         for (int j = 0; j < V; ++j)
@@ -670,7 +756,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                 const unsigned char *st = ring.data + (size_t)s * ring.tensors * ring.stage_bytes;
                 auto staged = [&](const void *base, int64_t ld) {
                     const uintptr_t p = (uintptr_t)(static_cast<const T *>(base) + row * ld);
-                    const T *q = reinterpret_cast<const T *>(st + (p & 15u));
+                    const T *q = reinterpret_cast<const T *>(st + (p & 15u)) + hd;
                     st += ring.stage_bytes;
                     return q;
                 };
@@ -726,6 +812,18 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                     }
                 }
             }
+            if constexpr (SHIFT)
+                if (cx >= 0) {
+                    const float x = xg * xw, u = xm * (GROW ? xa : 1.f) * xy;
+                    s2[0].x = fmaf(x, xh, s2[0].x);
+                    s2[1].x = fmaf(u, x, s2[1].x);
+                    s2[2].x = fmaf(u, xh, s2[2].x);
+                    s2[3].x = fmaf(u, xr, s2[3].x);
+                    if (!saved) {
+                        s2[4].x = fmaf(xh, xh, s2[4].x);
+                        s2[5].x = fmaf(xy, xy, s2[5].x);
+                    }
+                }
             float sum[6];
 #pragma unroll
             for (int i = 0; i < 6; ++i) sum[i] = s2[i].x + s2[i].y;
@@ -771,26 +869,26 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
             for (int j = 0; j < V; ++j) {
                 const int u = SL::unit(j, t0, NT);
                 if (u < NU) {
-                    float2 h[P], x[P], o[P], w[P];
+                    float2 h[P], x[P], z[P], w[P];
                     w1_of(j, u, w);
                     SL::unpack(vh[j], h);
                     SL::unpack(vg[j], x);
 #pragma unroll
                     for (int p = 0; p < P; ++p) {
                         acc_pre[j][p] = f2fma(x[p], f2mul(h[p], both(r_h)), acc_pre[j][p]);
-                        o[p] = f2mul(f2fma(h[p], both(-cc), f2mul(x[p], w[p])), both(r_h));
+                        z[p] = f2mul(f2fma(h[p], both(-cc), f2mul(x[p], w[p])), both(r_h));
                     }
                     if (more) {
                         SL::unpack(vr[j], x);
 #pragma unroll
-                        for (int p = 0; p < P; ++p) o[p] = f2add(o[p], x[p]);
+                        for (int p = 0; p < P; ++p) z[p] = f2add(z[p], x[p]);
                     }
-                    SL::store(gh, u, NT, NU, o);  // g_h
+                    SL::store(gh + hd, u, NT, NU, z);  // g_h
                     float2 y[P], mm[P];
                     SL::unpack(vy[j], y);
                     mult(j, mm);
 #pragma unroll
-                    for (int p = 0; p < P; ++p) h[p] = f2mul(o[p], f2mul(y[p], both(r_y)));  // g_h y r_y
+                    for (int p = 0; p < P; ++p) h[p] = f2mul(z[p], f2mul(y[p], both(r_y)));  // g_h y r_y
                     if constexpr (GROW) {  // this row is its gate row: finished here, and gw_post's term weighted
                         float2 w2[P];
                         SL::unpack(va[j], x);
@@ -800,17 +898,31 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                             acc_mid[j][p] = f2fma(h[p], x[p], acc_mid[j][p]);
                             w2[p] = f2mul(h[p], post ? f2add(both(a.weight_bias), w2[p]) : both(1.f));
                         }
-                        SL::store_floats(a.g_gate + row * D, u, NT, NU, w2, a.scale);
+                        store_floats(a.g_gate + row * D, u, w2, a.scale);
                     } else {
 #pragma unroll
                         for (int p = 0; p < P; ++p) acc_mid[j][p] = f2add(h[p], acc_mid[j][p]);
                     }
 #pragma unroll
                     for (int p = 0; p < P; ++p)
-                        o[p] = f2mul(f2fma(y[p], both(-ee), f2mul(mm[p], o[p])), both(r_y));
-                    SL::store(gy, u, NT, NU, o);
+                        z[p] = f2mul(f2fma(y[p], both(-ee), f2mul(mm[p], z[p])), both(r_y));
+                    SL::store(gy + hd, u, NT, NU, z);
                 }
             }
+            if constexpr (SHIFT)
+                if (cx >= 0) {
+                    x_pre = fmaf(xg, xh * r_h, x_pre);
+                    const float z = r_h * fmaf(xh, -cc, xg * xw) + xr, q = z * (xy * r_y);
+                    Cvt<T>::store1(gh + cx, z);
+                    if constexpr (GROW) {
+                        x_mid = fmaf(q, xa, x_mid);
+                        const float w2 = post ? a.weight_bias + Cvt<T>::load1(static_cast<const T *>(a.w_post) + cx) : 1.f;
+                        a.g_gate[row * D + cx] = q * w2 * a.scale;
+                    } else {
+                        x_mid += q;
+                    }
+                    Cvt<T>::store1(gy + cx, r_y * fmaf(xy, -ee, xm * (GROW ? xa : 1.f) * z));
+                }
             if constexpr (KIND == BLOCK_STAGED) {
                 if (++s == ring.S) {
                     s = 0;
@@ -824,7 +936,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
         }
         if (a.gate || post) {
             const bool whole = a.g_gate && !per_row && end - seg == a.rows_per_gate;
-            flush(acc_mid,
+            flush(acc_mid, x_mid,
                   per_row ? a.part_mid + 2 * cta * D
                   : whole ? a.g_gate + gr * D
                           : a.part_mid + mid_slot(cta, seg == 0) * D,
@@ -832,7 +944,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
         }
         seg = end;
     }
-    flush(acc_pre, a.part_pre + cta * D, 1.f);
+    flush(acc_pre, x_pre, a.part_pre + cta * D, 1.f);
 }
 
 }  // namespace rmsn

@@ -44,6 +44,8 @@ struct BlockArgs {
     int team;                      // rows are dealt out (VJP: a gate row's to CTAs of their own)
     int64_t rows_per_team;         // VJP: rows_per_gate, or all rows where the gate has one for each
     int64_t split_q, split_r;      // team: CTAs / gate rows, else rows / CTAs, and the remainder
+    int run;                       // team: CTAs that share a run of rows (0: all of them)
+    int64_t run_q, run_r;          // a team's rows / its runs, and the remainder
     float eps, weight_bias, scale;
     int D;
     int stages;
@@ -83,9 +85,18 @@ struct RowDeal {
     }
 };
 
+// Rows [lo, hi) of CTA `rank` of `size`: dealt out to all of them, or, with a.run, one
+// of that many runs' to a.run CTAs each.
+__host__ __device__ inline RowDeal team_rows(const BlockArgs &a, int64_t lo, int64_t hi, int64_t rank, int64_t size) {
+    if (!a.run) return RowDeal(lo, hi, rank, size, a.chunk_shift);
+    const int64_t g = (int64_t)((uint32_t)rank / (uint32_t)a.run);  // there are fewer than 2^31 CTAs
+    return RowDeal(lo + split_first(g, a.run_q, a.run_r), lo + split_first(g + 1, a.run_q, a.run_r), rank - g * a.run,
+                   a.run, 0);
+}
+
 // The forward's rows of CTA c.  team: dealt out to all CTAs; otherwise a run each.
 __host__ __device__ inline RowDeal fwd_rows(const BlockArgs &a, int64_t c, int64_t grid) {
-    if (a.team) return RowDeal(0, a.rows, c, grid, a.chunk_shift);
+    if (a.team) return team_rows(a, 0, a.rows, c, grid);
     return RowDeal(split_first(c, a.split_q, a.split_r), split_first(c + 1, a.split_q, a.split_r), 0, 1, 0);
 }
 
@@ -101,7 +112,7 @@ __host__ __device__ inline RowDeal vjp_rows(const BlockArgs &a, int64_t c) {
     const int64_t gr = (uint64_t)(c | q) >> 31 ? split_part<int64_t>(c, q, r)
                                                 : (int64_t)split_part<uint32_t>((uint32_t)c, (uint32_t)q, (uint32_t)r);
     const int64_t c0 = split_first(gr, q, r);
-    return RowDeal(gr * a.rows_per_team, (gr + 1) * a.rows_per_team, c - c0, split_first(gr + 1, q, r) - c0, a.chunk_shift);
+    return team_rows(a, gr * a.rows_per_team, (gr + 1) * a.rows_per_team, c - c0, split_first(gr + 1, q, r) - c0);
 }
 
 // Where CTA c leaves its part of a gate row's sum A when it has not got all of
@@ -117,12 +128,15 @@ inline int block_slices(int64_t gate_rows) {
     return gate_rows < 128 ? 1 : gate_rows >= 64 * BLOCK_MAX_SLICES ? BLOCK_MAX_SLICES : (int)(gate_rows / 64);
 }
 
+// Bytes of the table w1 in shared memory.
+__host__ __device__ constexpr uint32_t block_table_bytes(int64_t D) { return ((uint32_t)D * 4u + 127u) & ~127u; }
+
 // How a call runs: BLOCK_GENERIC for rows that do not fit on chip, else the
 // tier of block.cuh with units of `ub` bytes.
 enum : int { BLOCK_STAGED = 0, BLOCK_DIRECT = 1, BLOCK_WARP = 2, BLOCK_GENERIC = 3 };
 
 struct BlockPlan {
-    int kind, ub, threads, grid, stages, chunk_shift, team, half;
+    int kind, ub, threads, grid, stages, chunk_shift, team, half, shift, run;
     uint32_t stage_bytes;
     size_t smem;
 };

@@ -9,12 +9,12 @@ namespace rmsn {
 
 cudaError_t launch_gw_reduce(const float *partials, float *gw, int P, int D, cudaStream_t stream);
 
-template <bool VJP, typename T, int UB, int MAXT, int MINB, int KIND, bool GROW, bool FULL = false, bool HALF = false>
+template <bool VJP, typename T, int UB, int MAXT, int MINB, int KIND, bool GROW, bool SHIFT, bool FULL = false, bool HALF = false>
 cudaError_t launch_block_inst(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> smem_mask{0};
     void (*kern)(BlockArgs);
-    if constexpr (VJP) kern = block_vjp_kernel<T, UB, MAXT, MINB, KIND, GROW, FULL, HALF>;
-    else kern = block_fwd_kernel<T, UB, MAXT, MINB, KIND, GROW>;
+    if constexpr (VJP) kern = block_vjp_kernel<T, UB, MAXT, MINB, KIND, GROW, SHIFT, FULL, HALF>;
+    else kern = block_fwd_kernel<T, UB, MAXT, MINB, KIND, GROW, SHIFT>;
     if (p.smem > 0) {
         const cudaError_t e = allow_max_dynamic_smem((const void *)kern, smem_mask);
         if (e != cudaSuccess) return e;
@@ -22,43 +22,44 @@ cudaError_t launch_block_inst(const BlockPlan &p, const BlockArgs &a, cudaStream
     return launch_pdl(kern, dim3(p.grid), dim3(p.threads), p.smem, s, a);
 }
 
-template <bool VJP, typename T, int UB, bool GROW>
+template <bool VJP, typename T, int UB, bool GROW, bool SHIFT>
 cudaError_t launch_block_kind(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
-    if (p.kind == BLOCK_WARP) return launch_block_inst<VJP, T, UB, 256, 2, BLOCK_WARP, GROW>(p, a, s);
+    if constexpr (!SHIFT)
+        if (p.kind == BLOCK_WARP) return launch_block_inst<VJP, T, UB, 256, 2, BLOCK_WARP, GROW, false>(p, a, s);
     if (p.kind == BLOCK_DIRECT) {
-        if (p.threads <= 512) return launch_block_inst<VJP, T, UB, 512, 1, BLOCK_DIRECT, GROW>(p, a, s);
-        return launch_block_inst<VJP, T, UB, 1024, 1, BLOCK_DIRECT, GROW>(p, a, s);
+        if (p.threads <= 512) return launch_block_inst<VJP, T, UB, 512, 1, BLOCK_DIRECT, GROW, SHIFT>(p, a, s);
+        return launch_block_inst<VJP, T, UB, 1024, 1, BLOCK_DIRECT, GROW, SHIFT>(p, a, s);
     }
     if constexpr (VJP)
         if (p.half) {  // at most 96 registers
             if constexpr (UB == 16 && !GROW)
                 if (a.w_post && a.g_res && a.rstd)
-                    return launch_block_inst<VJP, T, UB, 640, 1, BLOCK_STAGED, GROW, true, true>(p, a, s);
-            return launch_block_inst<VJP, T, UB, 640, 1, BLOCK_STAGED, GROW, false, true>(p, a, s);
+                    return launch_block_inst<VJP, T, UB, 640, 1, BLOCK_STAGED, GROW, SHIFT, true, true>(p, a, s);
+            return launch_block_inst<VJP, T, UB, 640, 1, BLOCK_STAGED, GROW, SHIFT, false, true>(p, a, s);
         }
     // The training backward with all its operands, without their run-time tests:
     // 15 % fewer instructions (16384 x 4096 bf16: 139 -> 129 us).
     if constexpr (VJP && UB == 16 && !GROW)
         if (a.w_post && a.g_res && a.rstd) {
-            if (p.threads <= 256) return launch_block_inst<VJP, T, UB, 256, 2, BLOCK_STAGED, GROW, true>(p, a, s);
-            if (p.threads <= 512) return launch_block_inst<VJP, T, UB, 512, 1, BLOCK_STAGED, GROW, true>(p, a, s);
+            if (p.threads <= 256) return launch_block_inst<VJP, T, UB, 256, 2, BLOCK_STAGED, GROW, SHIFT, true>(p, a, s);
+            if (p.threads <= 512) return launch_block_inst<VJP, T, UB, 512, 1, BLOCK_STAGED, GROW, SHIFT, true>(p, a, s);
         }
     // Threads an SM holds (block_resident): 512 with 128 registers each; the
     // forward also fits 96, so its CTAs of 257-320 threads sit two an SM and
     // those of 513-640 one.
-    if (p.threads <= 256) return launch_block_inst<VJP, T, UB, 256, 2, BLOCK_STAGED, GROW>(p, a, s);
+    if (p.threads <= 256) return launch_block_inst<VJP, T, UB, 256, 2, BLOCK_STAGED, GROW, SHIFT>(p, a, s);
     if constexpr (!VJP)
-        if (p.threads <= 320) return launch_block_inst<VJP, T, UB, 320, 2, BLOCK_STAGED, GROW>(p, a, s);
-    if (p.threads <= 512) return launch_block_inst<VJP, T, UB, 512, 1, BLOCK_STAGED, GROW>(p, a, s);
+        if (p.threads <= 320) return launch_block_inst<VJP, T, UB, 320, 2, BLOCK_STAGED, GROW, SHIFT>(p, a, s);
+    if (p.threads <= 512) return launch_block_inst<VJP, T, UB, 512, 1, BLOCK_STAGED, GROW, SHIFT>(p, a, s);
     if constexpr (!VJP)
-        if (p.threads <= 640) return launch_block_inst<VJP, T, UB, 640, 1, BLOCK_STAGED, GROW>(p, a, s);
-    return launch_block_inst<VJP, T, UB, 1024, 1, BLOCK_STAGED, GROW>(p, a, s);
+        if (p.threads <= 640) return launch_block_inst<VJP, T, UB, 640, 1, BLOCK_STAGED, GROW, SHIFT>(p, a, s);
+    return launch_block_inst<VJP, T, UB, 1024, 1, BLOCK_STAGED, GROW, SHIFT>(p, a, s);
 }
 
-template <bool VJP, typename T, int UB>
+template <bool VJP, typename T, int UB, bool SHIFT = false>
 cudaError_t launch_block_unit(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
-    return a.gate && a.rows_per_gate == 1 ? launch_block_kind<VJP, T, UB, true>(p, a, s)
-                                          : launch_block_kind<VJP, T, UB, false>(p, a, s);
+    return a.gate && a.rows_per_gate == 1 ? launch_block_kind<VJP, T, UB, true, SHIFT>(p, a, s)
+                                          : launch_block_kind<VJP, T, UB, false, SHIFT>(p, a, s);
 }
 
 template <bool VJP, typename T>
@@ -69,6 +70,7 @@ cudaError_t launch_block(const BlockPlan &p, const BlockArgs &a, cudaStream_t s)
         else
             return launch_pdl(block_fwd_generic_kernel<T>, dim3(p.grid), dim3(BLOCK_GENERIC_NT), 0, s, a);
     }
+    if (p.shift) return launch_block_unit<VJP, T, 16, true>(p, a, s);
     if (p.ub == 16) return launch_block_unit<VJP, T, 16>(p, a, s);
     if constexpr (sizeof(T) == 2)
         if (p.ub == 2) return launch_block_unit<VJP, T, 2>(p, a, s);

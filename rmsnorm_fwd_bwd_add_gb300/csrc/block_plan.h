@@ -22,19 +22,33 @@ inline int block_resident(int threads, bool vjp) {
 }
 
 // Picks tier, unit and grid.  `unit` divides every address and stride (16 at
-// most); `tensors` row tensors are read.
-inline BlockPlan make_block_plan(int64_t rows, int64_t D, int es, int unit, int tensors, bool vjp, int64_t gates, int sm) {
+// most); `tensors` row tensors are read.  `classes`: 0, or all row tensors stand
+// alike to 16-byte boundaries, a row `classes` rows on (1, 2, 4 or 8) like this one.
+inline BlockPlan make_block_plan(int64_t rows, int64_t D, int es, int unit, int tensors, bool vjp, int64_t gates, int sm,
+                                 int classes) {
     BlockPlan p{};
     const int64_t row = D * es;
     p.ub = unit % 16 == 0 && row % 16 == 0 ? 16 : unit % 4 == 0 && row % 4 == 0 ? 4 : 2;
-    const int per_thread = 32 / es;  // elements: block_units of block.cuh
+    const int per_thread = 32 / es;  // elements
     int64_t threads = ((D + per_thread - 1) / per_thread + 31) / 32 * 32;
+    // Rows off 16-byte boundaries whose tensors stand alike: in the 16-byte units of
+    // memory, the elements before the first and behind the last one a thread each (5000
+    // rows of bf16, D = 4097: 49.6 us in 2-byte units, 28.7 so; VJP of 16384: 365 and
+    // 159).  A CTA's rows all have to stand the same way: they are dealt out to a
+    // multiple of `classes` CTAs.  Up to four units that would take a warp of their own
+    // go the same way (D = 4104: VJP 206 us with it).
+    int64_t units = row / 16;
+    const bool few = units % 64 >= 1 && units % 64 <= 4;
+    if (few) units -= units % 64;
+    p.shift = classes > 0 && units > 64 && (p.ub < 16 || few);  // more than a warp's
+    const int64_t width = p.shift ? units * (16 / es) : D;  // columns in units
+    if (p.shift) threads = ((width + per_thread - 1) / per_thread + 31) / 32 * 32;
     // VJP rows of 257-320 threads leave an SM one CTA of 9 or 10 warps; with half as
     // much a thread it is 17 to 20 (16384 rows of bf16: D = 5120 232 -> 218 us, 4097
     // 470 -> 365).
     if (vjp && threads > 256 && threads <= 320 && rows > sm) {
         p.half = 1;
-        threads = ((D + per_thread / 2 - 1) / (per_thread / 2) + 31) / 32 * 32;
+        threads = ((width + per_thread / 2 - 1) / (per_thread / 2) + 31) / 32 * 32;
     }
     auto generic_plan = [&] {
         BlockPlan g{};
@@ -45,9 +59,11 @@ inline BlockPlan make_block_plan(int64_t rows, int64_t D, int es, int unit, int 
         g.grid = (int)std::min<int64_t>(rows, std::min<int64_t>((vjp ? 2 : 4) * (int64_t)sm, fit));
         return g;
     };
-    if (threads > 1024) return generic_plan();
+    auto unshifted = [&] { return make_block_plan(rows, D, es, unit, tensors, vjp, gates, sm, 0); };
+    p.ub = p.shift ? 16 : p.ub;
+    if (threads > 1024) return p.shift ? unshifted() : generic_plan();
     p.threads = (int)threads;
-    const size_t tables = (size_t)(D * 4 + 127) / 128 * 128;  // w1 (block_table_bytes)
+    const size_t tables = block_table_bytes(D);
     // threads an SM holds of the instance these take (block_launch.cuh)
     const int resident = block_resident((int)threads, vjp);
     int per_sm = p.half ? 1 : resident / (int)threads;
@@ -63,7 +79,7 @@ inline BlockPlan make_block_plan(int64_t rows, int64_t D, int es, int unit, int 
         p.grid = (int)rows;
     } else {
         p.kind = BLOCK_STAGED;
-        p.stage_bytes = (uint32_t)((row + (p.ub == 16 ? 0 : 15) + 15) / 16 * 16);
+        p.stage_bytes = (uint32_t)((row + (unit % 16 == 0 && row % 16 == 0 ? 0 : 15) + 15) / 16 * 16);
         // an SM's shared memory, less 1 KB a CTA for the system and 2 KB for the
         // rest; fewer CTAs where it would leave them no second stage
         const size_t set = (size_t)tensors * p.stage_bytes;
@@ -75,7 +91,7 @@ inline BlockPlan make_block_plan(int64_t rows, int64_t D, int es, int unit, int 
         p.stages = stages_of(per_sm);
         p.grid = (int)std::min<int64_t>(rows, (int64_t)sm * per_sm);
         p.smem = 128 + tables + (size_t)p.stages * set;
-        if (p.stages < 1) return generic_plan();
+        if (p.stages < 1) return p.shift ? unshifted() : generic_plan();
     }
     if (vjp && p.kind == BLOCK_WARP)  // scratch traffic small beside the rows'
         p.grid = (int)std::min<int64_t>(p.grid, std::max<int64_t>(sm, rows / 12));
@@ -85,6 +101,14 @@ inline BlockPlan make_block_plan(int64_t rows, int64_t D, int es, int unit, int 
         // other CTAs must fill.
         const int64_t least = std::max<int64_t>(2, threads / 32);
         p.grid = (int)std::min<int64_t>(p.grid, std::max<int64_t>(sm, rows / least));
+    }
+    if (p.shift && classes > 1 && p.kind == BLOCK_STAGED) {
+        const int64_t teams = vjp ? gates : 1, size = p.grid / teams / classes * classes;  // CTAs of a team
+        if (size == 0) return unshifted();
+        p.grid = (int)(size * teams);
+        p.team = 1;
+        p.run = row < 8192 ? classes : 0;
+        return p;
     }
     // Rows of 8 KB or more are dealt out to the CTAs in turn, so that all of them work
     // on neighbouring memory: one row at a time in the VJP, 32 KB of them in the

@@ -119,17 +119,27 @@ int main() {
         a.split_q = a.team ? grid / G : a.rows / grid;
         a.split_r = a.team ? grid % G : a.rows % grid;
         if (split_first(0, a.split_q, a.split_r) != 0) return 10;
+        auto runs = [&](int64_t rows, int64_t size) {  // rows of a team in runs of a.run CTAs
+            a.run = 0;
+            for (int k = 8; k > 1 && !a.run; k /= 2)
+                if (size % k == 0 && rand() % 2) a.run = k;
+            if (a.run) a.run_q = rows / (size / a.run), a.run_r = rows % (size / a.run);
+        };
+        if (a.team && grid % G == 0) runs(a.rows_per_team, grid / G);
         if (const int e = check(a, grid, G)) return 20 + e;
         // the forward's deal, in chunks
         a.team = rand() % 2;
         a.chunk_shift = rand() % 4;
         a.split_q = a.rows / grid;
         a.split_r = a.rows % grid;
+        a.run = 0;
+        if (a.team) runs(a.rows, grid);
         std::vector<int> seen(a.rows, 0);
         for (int64_t c = 0; c < grid; ++c) {
             const RowDeal d = fwd_rows(a, c, grid);
             for (int64_t i = 0; i < d.n; ++i) {
                 if (d.row(i) < 0 || d.row(i) >= a.rows) return 30;
+                if (a.run && (d.row(i) - d.row(0)) % a.run) return 33;  // alike rows only
                 ++seen[d.row(i)];
             }
         }
@@ -145,6 +155,7 @@ PLAN = r"""
 #include <cstdio>
 #include "block_plan.h"
 using namespace rmsn;
+int64_t lanes_units(const BlockPlan &p) { return (int64_t)p.threads * (p.half ? 1 : 2); }
 int main() {
     const int sms[] = {1, 2, 132, 152};
     for (int64_t D = 1; D <= 40000; D += D < 1100 ? 1 : D < 9000 ? 7 : 61)
@@ -152,12 +163,15 @@ int main() {
             for (int es : {2, 4})
                 for (int vjp = 0; vjp < 2; ++vjp)
                     for (int sm : sms) {
-                        const int asked = make_block_plan(rows, D, es, 16, 3, true, 1, sm).grid;
+                        const int asked = std::max(make_block_plan(rows, D, es, 16, 3, true, 1, sm, 0).grid,
+                                                   make_block_plan(rows, D, es, es, 3, true, 1, sm, 1).grid);
                         for (int tensors = vjp ? 3 : 2; tensors <= (vjp ? 5 : 3); ++tensors)
-                            for (int unit : {16, 8, 4, 2})
+                            for (int how = 0; how < 12; ++how)
                                 for (int64_t gates : {(int64_t)1, (int64_t)5, rows}) {
-                                    if (unit < es) continue;
-                                    const BlockPlan p = make_block_plan(rows, D, es, unit, tensors, vjp, gates, sm);
+                                    const int unit = 16 >> how / 3, classes = how % 3 == 0 ? 0 : how % 3 == 1 ? 1 : 8;
+                                    if (unit < es || rows % gates) continue;
+                                    const BlockPlan p =
+                                        make_block_plan(rows, D, es, unit, tensors, vjp, gates, sm, classes);
                                     const char *why = nullptr;
                                     if (p.grid < 1 || p.grid > rows) why = "grid";
                                     if (vjp && p.grid > asked) why = "more scratch than the size asked beforehand";
@@ -165,27 +179,41 @@ int main() {
                                         const int64_t lanes = p.kind == BLOCK_WARP ? 32 : p.threads;
                                         const int per = p.half ? 16 : 32;
                                         if (p.threads < 32 || p.threads > 1024 || p.threads % 32) why = "threads";
-                                        if (lanes * per < D * es) why = "a row does not fit its threads";
-                                        if (D * es % p.ub || (p.ub != 16 && p.ub != 4 && p.ub != 2)) why = "unit";
+                                        const int64_t width = p.shift ? D * es / 16 * 16 - 64 : D * es;
+                                        if (lanes * per < width) why = "a row does not fit its threads";
+                                        if ((D * es % p.ub && !p.shift) || (p.ub != 16 && p.ub != 4 && p.ub != 2)) why = "unit";
                                         if (p.half && (!vjp || p.kind != BLOCK_STAGED)) why = "half";
                                         if (p.half && p.threads > 640) why = "half's threads";
                                     }
                                     if (p.kind == BLOCK_STAGED) {
                                         if (p.stages < 1 || p.stages > 8) why = "stages";
+                                        if (p.smem < 128 + (size_t)D * 4 +
+                                                     (size_t)p.stages * tensors * p.stage_bytes) why = "ring";
                                         if (p.smem > 227 * 1024) why = "shared memory";
-                                        if (p.stage_bytes % 16 || p.stage_bytes < D * es + (p.ub == 16 ? 0 : 15)) why = "stage";
+                                        if (p.stage_bytes % 16 || p.stage_bytes < D * es + (unit == 16 && D * es % 16 == 0 ? 0 : 15)) why = "stage";
                                         if (8 * p.stages > 128) why = "barriers";
                                     }
                                     if (p.kind == BLOCK_WARP && vjp &&
                                         p.smem != (size_t)p.threads / 32 * ((D + 3) / 4 * 16)) why = "warps' rows";
+                                    if (p.kind != BLOCK_GENERIC && p.kind != BLOCK_WARP && p.shift &&
+                                        D - std::min(D * es / 16 - 1, lanes_units(p)) * (16 / es) > p.threads)
+                                        why = "threads for the ends";
+                                    if (p.shift) {
+                                        const int64_t teams = vjp ? gates : 1;
+                                        if (p.ub != 16 || classes == 0 || p.kind == BLOCK_WARP || p.kind == BLOCK_GENERIC)
+                                            why = "shift";
+                                        if (p.kind == BLOCK_STAGED && classes > 1 && (!p.team || p.chunk_shift || p.grid % teams ||
+                                                                       p.grid / teams % classes || p.grid / teams > rows / teams ||
+                                                                       (p.run && p.run != classes)))
+                                            why = "shift's teams";
+                                    } else if (p.team && vjp && gates * 8 > p.grid) why = "team";
                                     if (p.kind == BLOCK_DIRECT && p.grid != rows) why = "direct";
-                                    if (p.team && vjp && gates * 8 > p.grid) why = "team";
                                     if (p.kind == BLOCK_GENERIC && p.team) why = "generic team";
                                     if (p.chunk_shift && ((int64_t)p.grid << p.chunk_shift) > rows) why = "chunk";
                                     if (why) {
-                                        printf("%s: rows %ld D %ld es %d vjp %d unit %d tensors %d gates %ld sm %d: kind %d grid %d "
+                                        printf("%s: rows %ld D %ld es %d vjp %d unit %d tensors %d gates %ld sm %d classes %d: kind %d grid %d "
                                                "threads %d stages %d\n", why, (long)rows, (long)D, es, vjp, unit, tensors,
-                                               (long)gates, sm, p.kind, p.grid, p.threads, p.stages);
+                                               (long)gates, sm, classes, p.kind, p.grid, p.threads, p.stages);
                                         return 1;
                                     }
                                 }

@@ -396,6 +396,53 @@ def test_block_wide_ctas(rows, D, groups, pad, off, dt):
         _check_vjp(p, 0.9, saved=saved)
 
 
+@pytest.mark.parametrize("rows,D,groups,pad,off", [
+    (1300, 1000, 0, 1, 0), (1300, 1025, 5, 0, 3), (2600, 515, 1, 0, 0), (700, 2049, 700, 0, 5), (650, 4098, 10, 0, 2),
+    (320, 4104, 2, 0, 0), (320, 4130, 320, 0, 0), (3, 4097, 3, 0, 7), (1, 2050, 0, 0, 1), (330, 8191, 3, 0, 0),
+    (310, 10241, 1, 0, 0), (400, 5127, 2, 0, 0), (2500, 1028, 4, 4, 1), (307, 16383, 1, 0, 0), (340, 4090, 0, 6, 1)])
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_block_rows_off_boundaries(rows, D, groups, pad, off, dt):
+    """Rows that all stand alike to 16-byte boundaries, at every distance from one, in
+    one or several kinds; and with one tensor standing differently."""
+    for i, (post, wb) in enumerate([(True, 0.0), (True, 1.0), (False, 0.0)]):
+        p = _problem(rows, D, DT[dt], groups, post, wb, pad, off, seed=31 + i, gate_pad=pad)
+        _check_fwd(p, 0.8)
+        a = _check_vjp(p, 0.8, g_res=i != 1, saved=i != 1)
+        p["y"] = _rand(torch.Generator().manual_seed(i), rows, D, DT[dt], pad + 1, off)
+        _check_fwd(p, 0.8)
+        _check_vjp(p, 0.8, g_res=i != 1, saved=i != 1)
+        del a
+
+
+def test_block_rows_off_boundaries_leave_their_neighbours_alone():
+    """Cut units at a row's ends: what lies between and around the rows stays, whatever
+    stands there."""
+    rows, D, ld, off = 640, 2043, 2051, 5
+    p = _problem(rows, D, torch.bfloat16, 4, True, 0.0, 8, off, seed=41)
+
+    def put(t, fill):
+        buf = torch.full((off + rows * ld + 16,), fill, dtype=t.dtype, device=DEV)
+        v = buf[off:off + rows * ld].view(rows, ld)[:, :D]
+        v.copy_(t)
+        return buf, v
+
+    def both(fill):  # the inputs in buffers of `fill`: the same path, so the same bits
+        q = {k: put(p[k], fill)[1] for k in ("y", "res", "h", "g", "g_res")}
+        outs = [put(torch.zeros_like(p["y"]), 7.0) for _ in range(4)]
+        rn.rmsnorm_block_fwd(q["y"], q["res"], p["w_post"], p["w_pre"], EPS, 0.0, p["gate"], out=outs[0][1], new_residual=outs[1][1])
+        got = rn.rmsnorm_block_vjp(q["y"], q["h"], p["w_post"], p["w_pre"], q["g"], EPS, 0.0, p["gate"], 1.0, q["g_res"],
+                                   g_y=outs[2][1], g_h=outs[3][1])
+        return outs, [o[1] for o in outs] + list(got[2:])
+
+    keep = torch.ones(off + rows * ld + 16, dtype=torch.bool)
+    keep[off:off + rows * ld].view(rows, ld)[:, :D] = False
+    (outs, got), (_, want) = both(float("nan")), both(0.0)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    for buf, _ in outs:
+        assert (buf.cpu()[keep] == 7.0).all()
+
+
 @pytest.mark.parametrize("D", [384, 4096, 4099, 20000])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("y_std,gate_std,res_std", [(1e12, 1e12, 1e12), (1e-15, 1e-10, 1e-10), (1e-15, 1e-10, 0.0)])
