@@ -271,8 +271,11 @@ int rmsnorm_block_fwd(const void *y, int64_t ld_y, const void *residual, int64_t
  *   gw_post, gw_pre  [D] fp32; gw_post NULL exactly when w_post is.
  *   g_gate       [gate_rows, D] fp32, dense; NULL exactly when gate is.
  * gw_post, gw_pre and g_gate are overwritten (rows == 0: zeros) and bit-identical
- * from run to run, as gw of rmsnorm_vjp; their scratch (three fp32 rows a CTA)
- * comes from the library's pool.  g_y and g_h may each be one of the row inputs.
+ * from run to run, as gw of rmsnorm_vjp; their scratch (three fp32 rows a CTA and
+ * 32 more) comes from the library's pool.  g_y and g_h may each be one of the row
+ * inputs.  With w_post, the products of m = scale * gate * (weight_bias + w_post),
+ * y and h or g_out are summed in fp32 before the scales are applied, and have to stay
+ * in its range.
  */
 int rmsnorm_block_vjp(const void *y, int64_t ld_y, const void *h, int64_t ld_h, const void *w_post,
                       const void *w_pre, const void *gate, int64_t ld_gate, int64_t gate_rows,
@@ -366,7 +369,7 @@ int rmsnorm_rope_kv_append(const void *q, const void *k, const void *v,
  *                them (or any finite ones of up to 10^6).
  *   interleaved  0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1).
  * fp16, bf16 or fp32; arithmetic in fp32, angles to about 1e-8 turns up to
- * positions of 10^7, each output rounded once.  rot_dim even, at most Dh; Dh at
+ * positions of 10^7 at one radian a position, each output rounded once.  rot_dim even, at most Dh; Dh at
  * most 1024; head strides below 4 GB.
  * Strides and pointers in multiples of 16 bytes, with rot_dim and Dh in whole
  * vectors, take the vectorised kernel.  A negative position is detected on the
@@ -425,7 +428,7 @@ int rmsnorm_rope_frequencies(int scaling, int64_t rot_dim, double base, double f
  * stack whose first *free_count entries are the free block ids.  Request b
  * holds lens[b] tokens in the blocks block_table[b * ld_table + i], i <
  * ceil(lens[b] / block_size); entries past those have no meaning.  All arrays
- * are device memory.
+ * are device memory, and the calls on one pool are ordered on one stream.
  *
  * rmsnorm_kv_release pushes the blocks of every request with finished[b] != 0
  * onto the stack, in request and table order, and sets its length to 0:

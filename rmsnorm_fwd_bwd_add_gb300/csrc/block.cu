@@ -262,9 +262,11 @@ int block_vjp(const void *y, int64_t ld_y, const void *h, int64_t ld_h, const vo
     a.split_q = p.team ? p.grid / gates : rows / p.grid;
     a.split_r = p.team ? p.grid % gates : rows % p.grid;
     set_runs(&a, p, a.rows_per_team, p.grid / gates);
-    const size_t need = scratch_bytes(p.grid, D);
+    const size_t need = scratch_bytes(p.cluster ? 1 : p.grid, D);
     void *ws = workspace;
-    if (pooled) {
+    if (pooled && p.cluster) {
+        ws = nullptr;  // nothing leaves the cluster
+    } else if (pooled) {
         st = scratch_alloc(need, s, &ws);
         if (st != RMSNORM_OK) return st;
     } else {
@@ -277,12 +279,15 @@ int block_vjp(const void *y, int64_t ld_y, const void *h, int64_t ld_h, const vo
             overlaps(ws, need, gate, ngate))
             return RMSNORM_ERR_INVALID_ARG;
     }
-    a.part_pre = static_cast<float *>(ws);
-    a.part_mid = a.part_pre + (size_t)p.grid * D;
-    a.part_post = a.part_mid + 2 * (size_t)p.grid * D;
+    a.cluster = p.cluster;
+    if (ws) {
+        a.part_pre = static_cast<float *>(ws);
+        a.part_mid = a.part_pre + (size_t)p.grid * D;
+        a.part_post = a.part_mid + 2 * (size_t)p.grid * D;
+    }
     const cudaError_t e = by_type(dtype, [&](auto t) { return launch_block_vjp<typename decltype(t)::type>(p, a, s); });
     st = e == cudaSuccess ? RMSNORM_OK : record_cuda_error(e);
-    const int freed = pooled ? scratch_free(ws, s) : RMSNORM_OK;
+    const int freed = pooled && ws ? scratch_free(ws, s) : RMSNORM_OK;
     return st != RMSNORM_OK ? st : freed;
 }
 
@@ -311,8 +316,9 @@ extern "C" size_t rmsnorm_block_vjp_workspace_size(int64_t rows, int64_t D, int 
     int sm = 0;
     if (check_common(rows, D, dtype, 0.f, 0.f) != RMSNORM_OK || rows == 0 || current_sm_count(&sm) != RMSNORM_OK)
         return 0;
-    // rows on 16-byte boundaries, or off them and alike: no other plan has more CTAs
+    // rows on 16-byte boundaries, or off them and alike, with a gate that keeps them out
+    // of one cluster: no other plan has more CTAs
     const int es = esize_of(dtype);
-    return scratch_bytes(std::max(make_block_plan(rows, D, es, 16, 3, true, 1, sm, 0).grid,
-                                  make_block_plan(rows, D, es, es, 3, true, 1, sm, 1).grid), D);
+    return scratch_bytes(std::max(make_block_plan(rows, D, es, 16, 3, true, 2, sm, 0).grid,
+                                  make_block_plan(rows, D, es, es, 3, true, 2, sm, 1).grid), D);
 }

@@ -217,6 +217,14 @@ __device__ __forceinline__ bool cta_sums(float (&v)[N], float (*red)[8], int nw,
     return !bad;
 }
 
+// A float of the cluster's CTA `rank`, at the place that `p` is in this one's
+// shared memory.
+__device__ __forceinline__ float load_remote(const float *p, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(dsmem_addr(p, rank)) : "memory");
+    return v;
+}
+
 // The ring of one CTA: rows r0, r0 + 1, ... of N tensors.
 struct BlockRing {
     uint64_t *full;
@@ -713,12 +721,12 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int u = SL::unit(j, t0, NT);
-                if (u < NU) SL::store_floats(buf + (size_t)ry * ((D + 3) & ~3), u, NT, NU, acc[j], k);
+                if (u < NU) SL::store_floats(buf + (size_t)ry * (block_sum_bytes(D) / 4), u, NT, NU, acc[j], k);
             }
             __syncthreads();
             for (int c = threadIdx.x; c < D; c += blockDim.x) {
                 float t = buf[c];
-                for (int w = 1; w < R; ++w) t += buf[(size_t)w * ((D + 3) & ~3) + c];
+                for (int w = 1; w < R; ++w) t += buf[(size_t)w * (block_sum_bytes(D) / 4) + c];
                 dst[c] = t;
             }
             __syncthreads();  // buf may be written again
@@ -736,6 +744,12 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
         for (int j = 0; j < V; ++j)
 #pragma unroll
             for (int p = 0; p < P; ++p) acc[j][p] = both(0.f);
+    };
+
+    // a.cluster: this CTA's sums, of gw_pre and of A, behind the warps' rows
+    auto sums_of = [&](int i) {
+        const size_t row = block_sum_bytes(D) / 4;
+        return reinterpret_cast<float *>(smem) + (KIND == BLOCK_WARP ? R + i : i) * row;
     };
 
     int s = 0;
@@ -934,7 +948,9 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                 if (fetched < deal.n) fetch_global(deal.row(fetched));
             }
         }
-        if (a.gate || post) {
+        if (KIND != BLOCK_STAGED && a.cluster) {
+            if (a.gate || post) flush(acc_mid, x_mid, sums_of(1), a.scale);  // the only segment
+        } else if (a.gate || post) {
             const bool whole = a.g_gate && !per_row && end - seg == a.rows_per_gate;
             flush(acc_mid, x_mid,
                   per_row ? a.part_mid + 2 * cta * D
@@ -944,6 +960,45 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
         }
         seg = end;
     }
+    if constexpr (KIND != BLOCK_STAGED)
+        if (a.cluster) {
+            // The second stage, here: each CTA takes columns and adds up all CTAs' sums of
+            // them in the CTAs' order, gate row by gate row (several only with a row a CTA).
+            flush(acc_pre, x_pre, sums_of(0), 1.f);
+            cluster_sync_all();
+            const int ctas = a.cluster, rpg = (int)min(a.rows_per_gate, (int64_t)16);
+            for (int c = (int)cta * (int)blockDim.x + (int)threadIdx.x; c < D; c += ctas * (int)blockDim.x) {
+                float v[2][8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < ctas) {
+                        v[0][r] = load_remote(sums_of(0) + c, r);
+                        if (a.gate || post) v[1][r] = load_remote(sums_of(1) + c, r);
+                    }
+                float pre = 0.f, A = 0.f, gp = 0.f;
+                const float w2 = post ? a.weight_bias + Cvt<T>::load1(static_cast<const T *>(a.w_post) + c) : 1.f;
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < ctas) {
+                        pre += v[0][r];
+                        if (a.gate || post) A += v[1][r];
+                        const bool last = r == ctas - 1 || (!per_row && (r + 1) % rpg == 0);
+                        if (last) {
+                            float k = 1.f;
+                            if (a.gate && !per_row) {
+                                k = Cvt<T>::load1(static_cast<const T *>(a.gate) + (int64_t)(r / rpg) * a.ld_gate + c);
+                                a.g_gate[(int64_t)(r / rpg) * D + c] = A * w2;
+                            }
+                            gp = fmaf(k, A, gp);
+                            A = 0.f;
+                        }
+                    }
+                a.gw_pre[c] = pre;
+                if (post) a.gw_post[c] = gp;
+            }
+            cluster_sync_all();  // no CTA leaves while another reads its sums
+            return;
+        }
     flush(acc_pre, x_pre, a.part_pre + cta * D, 1.f);
 }
 

@@ -44,6 +44,7 @@ struct BlockArgs {
     int team;                      // rows are dealt out (VJP: a gate row's to CTAs of their own)
     int64_t rows_per_team;         // VJP: rows_per_gate, or all rows where the gate has one for each
     int64_t split_q, split_r;      // team: CTAs / gate rows, else rows / CTAs, and the remainder
+    int cluster;                   // VJP: the CTAs are one cluster, which adds up its own parts
     int run;                       // team: CTAs that share a run of rows (0: all of them)
     int64_t run_q, run_r;          // a team's rows / its runs, and the remainder
     float eps, weight_bias, scale;
@@ -131,12 +132,15 @@ inline int block_slices(int64_t gate_rows) {
 // Bytes of the table w1 in shared memory.
 __host__ __device__ constexpr uint32_t block_table_bytes(int64_t D) { return ((uint32_t)D * 4u + 127u) & ~127u; }
 
+// Bytes of a row of sums in shared memory.
+__host__ __device__ constexpr size_t block_sum_bytes(int64_t D) { return (size_t)(D + 3) / 4 * 16; }
+
 // How a call runs: BLOCK_GENERIC for rows that do not fit on chip, else the
 // tier of block.cuh with units of `ub` bytes.
 enum : int { BLOCK_STAGED = 0, BLOCK_DIRECT = 1, BLOCK_WARP = 2, BLOCK_GENERIC = 3 };
 
 struct BlockPlan {
-    int kind, ub, threads, grid, stages, chunk_shift, team, half, shift, run;
+    int kind, ub, threads, grid, stages, chunk_shift, team, half, shift, run, cluster;
     uint32_t stage_bytes;
     size_t smem;
 };

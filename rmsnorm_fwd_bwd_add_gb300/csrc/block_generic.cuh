@@ -155,12 +155,11 @@ __global__ void __launch_bounds__(BLOCK_GENERIC_NT) block_vjp_generic_kernel(con
     }
 }
 
-// Second stage: a CTA covers 32 columns with BR_WARPS warps.
+// Second stage: a CTA covers 32 columns with W warps.
 //   gw_pre = the CTAs' partial rows, each warp a contiguous run of them, the
 //   warps' sums added in warp order.
-//   A of each gate row: with fewer gate rows than warps, BR_WARPS / G warps
-//   share a gate row's parts; with more, warp k takes the gate rows k, k +
-//   BR_WARPS, ...  A part is a row of part_mid, or the whole sum that one CTA
+//   A of each gate row: with fewer gate rows than warps, W / G warps share a gate
+//   row's parts; with more, warp k takes the gate rows k, k + W, ...  A part is a row of part_mid, or the whole sum that one CTA
 //   left in g_gate, which becomes w2 * A in place.  Gate rows of one row each
 //   come finished from the first stage, which also weighted its sums.
 // With many gate rows the grid has slices in y, each with a run of them, whose
@@ -169,12 +168,11 @@ __global__ void __launch_bounds__(BLOCK_GENERIC_NT) block_vjp_generic_kernel(con
 // warp's first loads of both sums are in flight together, and the row
 // arithmetic is 32-bit (I) where the row count allows (64-bit divisions made
 // the whole stage 14 us at 16384 x 4096 in 8 gate rows).
-constexpr int BR_WARPS = 32;
 constexpr int BR_BATCH = 16;
 
-template <typename T, typename I>
-__global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const BlockArgs a, int grid) {
-    __shared__ float sums[2][BR_WARPS][33];
+template <typename T, typename I, int W>
+__global__ void __launch_bounds__(32 * W) block_reduce_kernel(const BlockArgs a, int grid) {
+    __shared__ float sums[2][W][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int D = a.D;
     const int64_t col = (int64_t)blockIdx.x * 32 + lane;
@@ -184,8 +182,8 @@ __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const Block
     const I rows = (I)a.rows, rpg = (I)a.rows_per_gate, G = rows / rpg;
     const I q = (I)a.split_q, r = (I)a.split_r;
     const bool need_mid = w2 || gate, per_row = gate && rpg == 1;
-    const int team = G >= BR_WARPS ? 1 : BR_WARPS / (int)G;  // warps a gate row
-    const int per = (grid + BR_WARPS - 1) / BR_WARPS;
+    const int team = G >= W ? 1 : W / (int)G;  // warps a gate row
+    const int per = (grid + W - 1) / W;
     const int p0 = min(grid, warp * per), p1 = min(grid, p0 + per);
     // CTAs c0 .. c1 have gate row gr's rows (as vjp_rows deals them out); the warps
     // of a team take equal runs of them
@@ -238,7 +236,7 @@ __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const Block
     } else if (need_mid) {
         const int mate = warp % team;
         const I g0 = (I)((uint64_t)G * blockIdx.y / gridDim.y), g1 = (I)((uint64_t)G * (blockIdx.y + 1) / gridDim.y);
-        for (I gr = g0 + warp / team; gr < g1; gr += BR_WARPS / team) {
+        for (I gr = g0 + warp / team; gr < g1; gr += W / team) {
             I c0, c1;
             ctas_of(gr, c0, c1);
             float A = 0.f;
@@ -275,11 +273,11 @@ __global__ void __launch_bounds__(32 * BR_WARPS) block_reduce_kernel(const Block
     if (warp == 0 && in && pre_here) {
         float t = sums[0][0][lane];
 #pragma unroll
-        for (int k = 1; k < BR_WARPS; ++k) t += sums[0][k][lane];
+        for (int k = 1; k < W; ++k) t += sums[0][k][lane];
         a.gw_pre[col] = t;
     }
     if (!need_mid) return;
-    const int places = per_row || team == 1 ? BR_WARPS : (int)G;  // what gw_post adds up
+    const int places = per_row || team == 1 ? W : (int)G;  // what gw_post adds up
     if (places == (int)G && team > 1) {  // each team's first warp joins its gate row's parts
         float A = 0.f;
         if (warp % team == 0 && warp / team < (int)G) {

@@ -19,6 +19,8 @@ cudaError_t launch_block_inst(const BlockPlan &p, const BlockArgs &a, cudaStream
         const cudaError_t e = allow_max_dynamic_smem((const void *)kern, smem_mask);
         if (e != cudaSuccess) return e;
     }
+    if constexpr (VJP && KIND != BLOCK_STAGED)
+        if (p.cluster) return launch_pdl_cluster(kern, dim3(p.grid), dim3(p.threads), p.smem, s, p.cluster, a);
     return launch_pdl(kern, dim3(p.grid), dim3(p.threads), p.smem, s, a);
 }
 
@@ -77,15 +79,24 @@ cudaError_t launch_block(const BlockPlan &p, const BlockArgs &a, cudaStream_t s)
     return launch_block_unit<VJP, T, 4>(p, a, s);
 }
 
+template <typename T, int W>
+cudaError_t launch_block_reduce(const BlockPlan &p, const BlockArgs &a, int slices, cudaStream_t s) {
+    const dim3 grid((unsigned)((a.D + 31) / 32), slices), block(32 * W);
+    return a.rows <= INT32_MAX ? launch_pdl(block_reduce_kernel<T, uint32_t, W>, grid, block, 0, s, a, p.grid)
+                               : launch_pdl(block_reduce_kernel<T, int64_t, W>, grid, block, 0, s, a, p.grid);
+}
+
 template <typename T>
 cudaError_t launch_block_vjp_both(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
     cudaError_t e = launch_block<true, T>(p, a, s);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || p.cluster) return e;
     const int64_t G = a.rows / a.rows_per_gate;
     const int slices = block_slices(a.team || a.rows_per_gate == 1 ? 1 : G);
-    const dim3 grid((unsigned)((a.D + 31) / 32), slices), block(32 * BR_WARPS);
-    e = a.rows <= INT32_MAX ? launch_pdl(block_reduce_kernel<T, uint32_t>, grid, block, 0, s, a, p.grid)
-                            : launch_pdl(block_reduce_kernel<T, int64_t>, grid, block, 0, s, a, p.grid);
+    // Few parts: 8 warps have them all in flight at once, and an SM holds the CTAs of
+    // several blocks of columns (100 rows of D = 5248: 10.2 us; with 32 warps two
+    // rounds of CTAs, 13).
+    e = p.grid <= 8 * BR_BATCH && slices == 1 ? launch_block_reduce<T, 8>(p, a, slices, s)
+                                              : launch_block_reduce<T, 32>(p, a, slices, s);
     if (e != cudaSuccess || slices == 1 || !a.w_post) return e;
     return launch_gw_reduce(a.part_post, a.gw_post, slices, a.D, s);
 }

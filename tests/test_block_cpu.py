@@ -159,12 +159,12 @@ int64_t lanes_units(const BlockPlan &p) { return (int64_t)p.threads * (p.half ? 
 int main() {
     const int sms[] = {1, 2, 132, 152};
     for (int64_t D = 1; D <= 40000; D += D < 1100 ? 1 : D < 9000 ? 7 : 61)
-        for (int64_t rows : {1, 2, 7, 151, 300, 305, 1217, 5000, 16384, 1000000})
+        for (int64_t rows : {1, 2, 7, 8, 9, 16, 17, 33, 64, 65, 151, 300, 305, 1217, 5000, 16384, 1000000})
             for (int es : {2, 4})
                 for (int vjp = 0; vjp < 2; ++vjp)
                     for (int sm : sms) {
-                        const int asked = std::max(make_block_plan(rows, D, es, 16, 3, true, 1, sm, 0).grid,
-                                                   make_block_plan(rows, D, es, es, 3, true, 1, sm, 1).grid);
+                        const int asked = std::max(make_block_plan(rows, D, es, 16, 3, true, 2, sm, 0).grid,
+                                                   make_block_plan(rows, D, es, es, 3, true, 2, sm, 1).grid);
                         for (int tensors = vjp ? 3 : 2; tensors <= (vjp ? 5 : 3); ++tensors)
                             for (int how = 0; how < 12; ++how)
                                 for (int64_t gates : {(int64_t)1, (int64_t)5, rows}) {
@@ -174,7 +174,7 @@ int main() {
                                         make_block_plan(rows, D, es, unit, tensors, vjp, gates, sm, classes);
                                     const char *why = nullptr;
                                     if (p.grid < 1 || p.grid > rows) why = "grid";
-                                    if (vjp && p.grid > asked) why = "more scratch than the size asked beforehand";
+                                    if (vjp && !p.cluster && p.grid > asked) why = "more scratch than the size asked beforehand";
                                     if (p.kind != BLOCK_GENERIC) {
                                         const int64_t lanes = p.kind == BLOCK_WARP ? 32 : p.threads;
                                         const int per = p.half ? 16 : 32;
@@ -194,7 +194,17 @@ int main() {
                                         if (8 * p.stages > 128) why = "barriers";
                                     }
                                     if (p.kind == BLOCK_WARP && vjp &&
-                                        p.smem != (size_t)p.threads / 32 * ((D + 3) / 4 * 16)) why = "warps' rows";
+                                        p.smem != ((size_t)p.threads / 32 + (p.cluster ? 2 : 0)) * block_sum_bytes(D))
+                                        why = "warps' rows";
+                                    if (p.cluster) {
+                                        if (!vjp || p.cluster > 8 || p.grid != p.cluster || p.team || p.smem > 227 * 1024)
+                                            why = "cluster";
+                                        if (p.kind == BLOCK_DIRECT && p.smem != 2 * block_sum_bytes(D)) why = "cluster's sums";
+                                        if (p.kind != BLOCK_DIRECT && p.kind != BLOCK_WARP) why = "cluster's tier";
+                                        // several gate rows, or rows that stand differently: a row a CTA
+                                        if ((gates > 1 || (p.shift && classes > 1)) && p.grid != rows) why = "cluster's rows";
+                                        if (p.kind == BLOCK_WARP && (rows + p.grid - 1) / p.grid > p.threads / 32) why = "cluster's warps";
+                                    }
                                     if (p.kind != BLOCK_GENERIC && p.kind != BLOCK_WARP && p.shift &&
                                         D - std::min(D * es / 16 - 1, lanes_units(p)) * (16 / es) > p.threads)
                                         why = "threads for the ends";
@@ -207,7 +217,7 @@ int main() {
                                                                        (p.run && p.run != classes)))
                                             why = "shift's teams";
                                     } else if (p.team && vjp && gates * 8 > p.grid) why = "team";
-                                    if (p.kind == BLOCK_DIRECT && p.grid != rows) why = "direct";
+                                    if (p.kind == BLOCK_DIRECT && p.grid != rows && !p.cluster) why = "direct";
                                     if (p.kind == BLOCK_GENERIC && p.team) why = "generic team";
                                     if (p.chunk_shift && ((int64_t)p.grid << p.chunk_shift) > rows) why = "chunk";
                                     if (why) {

@@ -443,6 +443,26 @@ def test_block_rows_off_boundaries_leave_their_neighbours_alone():
         assert (buf.cpu()[keep] == 7.0).all()
 
 
+@pytest.mark.parametrize("rows,D,groups,pad,off", [
+    (1, 64, 0, 0, 0), (8, 100, 1, 0, 1), (9, 512, 0, 0, 0), (16, 37, 16, 0, 0), (17, 200, 1, 8, 0), (33, 256, 33, 0, 0),
+    (61, 511, 1, 0, 0), (64, 512, 0, 0, 0), (64, 128, 2, 0, 0), (65, 512, 1, 0, 0), (2, 5248, 0, 8, 0), (8, 4096, 4, 0, 0),
+    (6, 1000, 2, 0, 0), (7, 4097, 7, 0, 0), (8, 8191, 8, 0, 3), (16, 4096, 1, 0, 0), (13, 2048, 0, 0, 0), (11, 4104, 11, 0, 0),
+    (16, 4097, 1, 7, 0), (15, 1001, 1, 0, 0), (16, 16384, 1, 0, 0), (12, 2000, 3, 0, 0), (4, 10000, 2, 0, 0), (120, 5248, 3, 0, 0)])
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_block_few_rows(rows, D, groups, pad, off, dt):
+    """Up to 64 rows, on both sides of what one cluster sums by itself."""
+    for i, (post, wb) in enumerate([(True, 0.0), (True, 1.0), (False, 0.0)]):
+        p = _problem(rows, D, DT[dt], groups, post, wb, pad, off, seed=61 + i, gate_pad=pad)
+        a = _check_vjp(p, 0.8, g_res=i != 1, saved=i != 1)
+        for _ in range(3):  # the same bits on every run
+            b = rn.rmsnorm_block_vjp(p["y"], p["h"], p["w_post"], p["w_pre"], p["g"], EPS, wb, p["gate"], 0.8,
+                                     p["g_res"] if i != 1 else None,
+                                     rstd=None if i == 1 else torch.stack([1 / torch.sqrt((t.double() ** 2).mean(1) + EPS)
+                                                                          for t in (p["y"], p["h"])]).float())
+            for s, t in zip(a, b):
+                assert (s is None and t is None) or torch.equal(s, t)
+
+
 @pytest.mark.parametrize("D", [384, 4096, 4099, 20000])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("y_std,gate_std,res_std", [(1e12, 1e12, 1e12), (1e-15, 1e-10, 1e-10), (1e-15, 1e-10, 0.0)])
