@@ -53,10 +53,11 @@ inline BlockPlan make_block_plan(int64_t rows, int64_t D, int es, int unit, int 
     auto generic_plan = [&] {
         BlockPlan g{};
         g.kind = BLOCK_GENERIC;
-        // the VJP keeps three fp32 rows of scratch a CTA: two CTAs an SM, fewer
+        g.ub = p.ub;
+        // as many CTAs as fit at once; the VJP keeps three fp32 rows of scratch each: fewer
         // where they would take more than 256 MB
-        const int64_t fit = vjp ? std::max<int64_t>(8, ((int64_t)256 << 20) / (12 * D)) : 4 * sm;
-        g.grid = (int)std::min<int64_t>(rows, std::min<int64_t>((vjp ? 2 : 4) * (int64_t)sm, fit));
+        const int64_t fit = vjp ? std::max<int64_t>(8, ((int64_t)256 << 20) / (12 * D)) : 3 * sm;
+        g.grid = (int)std::min<int64_t>(rows, std::min<int64_t>((vjp ? 2 : 3) * (int64_t)sm, fit));
         return g;
     };
     auto unshifted = [&] { return make_block_plan(rows, D, es, unit, tensors, vjp, gates, sm, 0); };

@@ -11,8 +11,9 @@
 // request they belong to (a warp per request took 41 us to give back 80 requests
 // of 128 blocks each among 4000, and 32 us to hand out 1400 single blocks).  The
 // tokens are written by a second kernel over all SMs, or by the same CTA, from
-// shared memory, when they are few.  Everything is in request order: the
-// results are the same on every run.
+// shared memory, when they are few.  Release and plan of 250 requests with a token
+// each take 10.5 us of GPU time together, of 4000 with up to 64 tokens 25 us.
+// Everything is in request order: the results are the same on every run.
 //
 // Lengths and block ids are device data and are checked there: a negative
 // length, a stack that runs over or an id outside the pool sets
