@@ -8,14 +8,14 @@
 // serves both directions.  Elements past rot_dim are copied.
 //
 // Bound by memory: every element is read and written once.  A warp takes one
-// token (or one of a token's parts, when tokens are fewer than warps): a lane
+// token (or one of a token's parts, where tokens are fewer than warps): a lane
 // owns one rotation unit -- the pairs of one vector (interleaved) or of two
 // vectors half a rotation apart -- of 32 / units heads at a time and computes
 // the cosines and sines of its pairs once for all of the token's heads.
 //
 // On the GB300: 16384 tokens of 32 + 8 heads of 128 (bf16, views of one projection) 54 us,
 // 92 % of the copy bandwidth; 5001 of 16 + 4 (fp32, interleaved, half rotated,
-// inverse) 18.5 us, 83 %; the append of 4096 tokens of 32 + 8 heads of 80 11.5 us, 81 %,
+// inverse) 17.4 us, 88 %; the append of 4096 tokens of 32 + 8 heads of 80 11.5 us, 81 %,
 // of 8 tokens 3.0 us.  The loops carry only loads, rotations and stores: every head's
 // address is one 32 x 32 + 64 multiply-add (64-bit strides cost a tenth of the time).
 //
@@ -145,11 +145,12 @@ template <typename T> __device__ __forceinline__ void put_pair(uint4 &v, int m, 
 // more of them.
 template <int VB> __host__ __device__ constexpr int heads_in_flight() { return VB == 16 ? 4 : 8; }
 
-// wpt: warps a token; cw: units of a head a warp takes at a time.
+// wpt: warps a token, from token `whole` on (before it, one); cw: units of a head a
+// warp takes at a time.
 // APPEND: k and v go to cache rows.
 template <typename T, int VB, bool INTERLEAVED, bool APPEND>
 __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __grid_constant__ RopeExArgs a,
-                                                                       int wpt, int cw) {
+                                                                       int64_t whole, int wpt, int cw) {
     using V = typename RawUnit<VB>::type;
     constexpr int VE = VB / (int)sizeof(T);
     constexpr bool PAIRED = INTERLEAVED && VE > 1;  // both halves of a pair in one vector
@@ -171,20 +172,21 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
     const bool q_moves = a.q_out.p != a.q.p, k_moves = a.k_out.p != a.k.p;  // in place: nothing to copy
     const int hpi = 32 / cw, hs = lane / cw, lu = lane - hs * cw;
     const int n_qk = a.Hq + a.Hkv, n_all = n_qk + (APPEND ? a.Hkv : 0);
-    const int64_t n_items = a.T * wpt, n_warps = (int64_t)gridDim.x * (RX_NT / 32);
+    const int64_t n_items = whole + (a.T - whole) * wpt, n_warps = (int64_t)gridDim.x * (RX_NT / 32);
     const int wshift = 31 - __clz(wpt);  // wpt is a power of two
     int64_t w = ((int64_t)blockIdx.x * RX_NT + threadIdx.x) >> 5;
     int64_t p_next = 0, slot_next = 0;  // of the item ahead, loaded one item early
+    auto token_of = [&](int64_t item) { return item < whole ? item : whole + ((item - whole) >> wshift); };
     auto look_ahead = [&](int64_t item) {
         if (item < n_items) {
-            p_next = a.positions[item >> wshift];
-            if constexpr (APPEND) slot_next = a.slots[item >> wshift];
+            p_next = a.positions[token_of(item)];
+            if constexpr (APPEND) slot_next = a.slots[token_of(item)];
         }
     };
     look_ahead(w);
     for (; w < n_items; w += n_warps) {
-        const int64_t t = w >> wshift, p = p_next, slot = slot_next;
-        const int part = (int)(w & (wpt - 1));
+        const int64_t t = token_of(w), p = p_next, slot = slot_next;
+        const int parts = w < whole ? 1 : wpt, part = w < whole ? 0 : (int)((w - whole) & (wpt - 1));
         look_ahead(w + n_warps);
         const int64_t b = a.S == a.T ? 0 : t / a.S, s = t - b * a.S;
         const bool pos_ok = p >= 0, slot_ok = !APPEND || slot < a.num_slots;
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
                     }
                 }
             }
-            const int step = wpt * hpi;
+            const int step = parts * hpi;
             // HB heads' loads ahead of their stores (heads never share an address, so
             // in place too)
             for (int h0 = part * hpi + hs; h0 < heads; h0 += HB * step) {
@@ -306,20 +308,25 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
 template <typename T, int VB, bool INTERLEAVED>
 cudaError_t launch_layout(const RopeExArgs &a, int sm, cudaStream_t s) {
     // Warps a token (k) and units a step (c).  Each warp computes its units' angles,
-    // about half a trip to memory, and makes a trip for every few heads; all warps go
-    // through equal rounds of tokens' parts.
+    // about half a trip to memory, and makes a trip for every few heads.  All warps go
+    // through equal rounds of whole tokens; what is left, less than a round, is split
+    // into as many parts as there are warps for (5001 tokens on 2432 warps: 19.7 us with
+    // a third round of 137 whole tokens, 17.4 with them in 16 parts each).
     const int64_t resident = (int64_t)sm * RX_CTAS_PER_SM, warps = resident * (RX_NT / 32);
     constexpr int VE = VB / (int)sizeof(T);
     const int lanes = HeadMap<VE, (INTERLEAVED && VE > 1), INTERLEAVED>(a.Dh, a.rot).lanes;
     const int heads = a.Hq + a.Hkv * (a.slots ? 2 : 1);
+    const int64_t whole = a.T / warps * warps, rest = a.T - whole;
     int wpt = 1, cw = 1;
     int64_t best = INT64_MAX;
     for (int steps = (lanes + 31) / 32; steps <= 12; ++steps) {
         const int c = (lanes + steps - 1) / steps;  // a head in `steps` equal steps
-        for (int k = 1; k <= 8; k *= 2) {
-            const int per_trip = (32 / c) * heads_in_flight<VB>() * k;
-            const int64_t rounds = (a.T * k + warps - 1) / warps, trips = (heads + per_trip - 1) / per_trip;
-            const int64_t cost = rounds * (1 + (1 + 2 * trips) * steps);
+        auto cost_of = [&](int64_t rounds, int k) {
+            const int per_trip = (32 / c) * heads_in_flight<VB>() * k, trips = (heads + per_trip - 1) / per_trip;
+            return rounds * (1 + (1 + 2 * trips) * steps);
+        };
+        for (int k = 1; k <= 16; k *= 2) {
+            const int64_t cost = cost_of(whole / warps, 1) + cost_of((rest * k + warps - 1) / warps, k);
             if (cost < best) {
                 best = cost;
                 wpt = k;
@@ -328,9 +335,10 @@ cudaError_t launch_layout(const RopeExArgs &a, int sm, cudaStream_t s) {
         }
         if (c == 1) break;
     }
-    const int grid = (int)std::min<int64_t>((a.T * wpt + RX_NT / 32 - 1) / (RX_NT / 32), resident);
+    const int64_t items = whole + rest * wpt;
+    const int grid = (int)std::min<int64_t>((items + RX_NT / 32 - 1) / (RX_NT / 32), resident);
     return launch_pdl(a.slots ? rope_ex_kernel<T, VB, INTERLEAVED, true> : rope_ex_kernel<T, VB, INTERLEAVED, false>,
-                      dim3(grid), dim3(RX_NT), 0, s, a, wpt, cw);
+                      dim3(grid), dim3(RX_NT), 0, s, a, whole, wpt, cw);
 }
 
 // unit: bytes that divide every address, stride and length.
