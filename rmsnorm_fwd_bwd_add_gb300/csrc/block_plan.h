@@ -36,7 +36,7 @@ inline BlockPlan make_block_plan(int64_t rows, int64_t D, int es, int unit, int 
     // rows of bf16, D = 4097: 49.6 us in 2-byte units, 28.7 so; VJP of 16384: 365 and
     // 159).  A CTA's rows all have to stand the same way: they are dealt out to a
     // multiple of `classes` CTAs.  Up to four units that would take a warp of their own
-    // go the same way (D = 4104: VJP 206 us with it).
+    // go the same way (VJP of 16384, D = 4104: 206 us with that warp, 160 without).
     int64_t units = row / 16;
     const bool few = units % 64 >= 1 && units % 64 <= 4;
     if (few) units -= units % 64;
@@ -44,8 +44,7 @@ inline BlockPlan make_block_plan(int64_t rows, int64_t D, int es, int unit, int 
     const int64_t width = p.shift ? units * (16 / es) : D;  // columns in units
     if (p.shift) threads = ((width + per_thread - 1) / per_thread + 31) / 32 * 32;
     // VJP rows of 257-320 threads leave an SM one CTA of 9 or 10 warps; with half as
-    // much a thread it is 17 to 20 (16384 rows of bf16: D = 5120 232 -> 218 us, 4097
-    // 470 -> 365).
+    // much a thread it is 17 to 20 (16384 rows of bf16, D = 5120: 232 -> 207 us).
     if (vjp && threads > 256 && threads <= 320 && rows > sm) {
         p.half = 1;
         threads = ((width + per_thread / 2 - 1) / (per_thread / 2) + 31) / 32 * 32;

@@ -72,7 +72,7 @@ CASES = [  # B, S, Hq, Hkv, Dh, rot
     (1, 1, 1, 1, 2, 2), (1, 1, 32, 8, 128, 128), (2, 7, 4, 2, 64, 32), (1, 300, 8, 2, 128, 64),
     (3, 50, 6, 3, 80, 32), (1, 129, 5, 1, 96, 96), (2, 33, 2, 2, 22, 10), (1, 40, 3, 1, 30, 2),
     (1, 17, 2, 1, 1024, 1024), (2, 9, 1, 1, 512, 256), (1, 5000, 4, 1, 64, 64), (1, 64, 1, 0, 128, 128),
-    (1, 70, 40, 8, 72, 40),
+    (1, 70, 40, 8, 72, 40), (2, 1240, 16, 4, 64, 32), (1, 2433, 24, 2, 32, 32),
 ]
 
 
@@ -157,7 +157,8 @@ def test_rope_autograd(dt, interleaved):
 
 
 @pytest.mark.parametrize("T,Hq,Hkv,Dh,rot", [(1, 32, 8, 128, 128), (8, 32, 8, 128, 64), (300, 6, 3, 80, 32),
-                                             (2000, 8, 2, 64, 64), (37, 4, 2, 22, 10), (9, 2, 1, 96, 48)])
+                                             (2000, 8, 2, 64, 64), (37, 4, 2, 22, 10), (9, 2, 1, 96, 48),
+                                             (2450, 12, 4, 64, 64), (4870, 20, 4, 40, 16)])
 @pytest.mark.parametrize("interleaved", [False, True], ids=["half", "inter"])
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 def test_append(T, Hq, Hkv, Dh, rot, interleaved, dt):
