@@ -11,7 +11,7 @@
 //   VJP: sum m g_h y = r_h (sum u g w1 - c sum u h) + sum u g_res, u = m y: the
 //     same terms as its own sum has, so no digits are lost.  u g w1 and u h must
 //     stay in fp32's range (a second way through, as in the forward, cost the
-//     instances without FULL 150 to 500 bytes of spills a thread).
+//     instances without a FORM 150 to 500 bytes of spills a thread).
 //
 //   BLOCK_STAGED  one row a CTA at a time out of a shared-memory ring that thread
 //                 0 fills with 1-D bulk copies `stages` rows ahead, so that the
@@ -583,9 +583,10 @@ __global__ void __launch_bounds__(MAXT, MINB) block_fwd_kernel(const __grid_cons
 }
 
 // VJP -----------------------------------------------------------------------
-// FULL: a norm after the block, g_res and saved scales are all there.  HALF: 16 bytes
-// of a row a thread instead of 32.
-template <typename T, int UB, int MAXT, int MINB, int KIND, bool GROW, bool SHIFT, bool FULL, bool HALF>
+// FORM: which of a norm after the block, g_res and saved scales are there, known when
+// compiled (FORM_ bits; 0: asked at run time).  HALF: 16 bytes of a row a thread
+// instead of 32.
+template <typename T, int UB, int MAXT, int MINB, int KIND, bool GROW, bool SHIFT, int FORM, bool HALF>
 __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_constant__ BlockArgs a) {
     using SL = Slot<T, UB>;
     using Raw = typename SL::Raw;
@@ -599,8 +600,9 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
     const int D = a.D, nw = (int)(blockDim.x >> 5);
     const float inv_D = 1.0f / (float)D;
     constexpr bool per_row = GROW;  // a gate row for each row
-    const bool post = FULL || a.w_post != nullptr, more = FULL || a.g_res != nullptr;
-    const bool saved = FULL || a.rstd != nullptr;
+    const bool post = FORM ? (FORM & FORM_POST) != 0 : a.w_post != nullptr;
+    const bool more = FORM ? (FORM & FORM_MORE) != 0 : a.g_res != nullptr;
+    const bool saved = FORM ? (FORM & FORM_SAVED) != 0 : a.rstd != nullptr;
     const int64_t cta = blockIdx.x;
     const RowDeal deal = vjp_rows(a, cta);
     // SHIFT: `hd` columns before a row's first 16-byte boundary, the same for all of
@@ -610,7 +612,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
     const int NU = SHIFT ? min((D - hd) / E, V * NT) : D / E;
     const int cx = !SHIFT || t0 >= D - NU * E ? -1 : t0 < hd ? t0 : NU * E + t0;
 
-    const void *src[5] = {a.y, a.res, a.g, a.g_res, per_row ? a.gate : nullptr};
+    const void *src[5] = {a.y, a.res, a.g, more ? a.g_res : nullptr, per_row ? a.gate : nullptr};
     const int64_t ld[5] = {a.ld_y, a.ld_res, a.ld_g, a.ld_g_res, a.ld_gate};
     BlockRing ring{reinterpret_cast<uint64_t *>(smem), smem + BLOCK_HEADER + block_table_bytes(D), a.stages, a.stage_bytes,
                    3 + more + per_row};

@@ -139,6 +139,9 @@ __host__ __device__ constexpr size_t block_sum_bytes(int64_t D) { return (size_t
 // tier of block.cuh with units of `ub` bytes.
 enum : int { BLOCK_STAGED = 0, BLOCK_DIRECT = 1, BLOCK_WARP = 2, BLOCK_GENERIC = 3 };
 
+// What a VJP call has beside y, h and g.
+enum : int { FORM_POST = 1, FORM_MORE = 2, FORM_SAVED = 4 };
+
 struct BlockPlan {
     int kind, ub, threads, grid, stages, chunk_shift, team, half, shift, run, cluster;
     uint32_t stage_bytes;

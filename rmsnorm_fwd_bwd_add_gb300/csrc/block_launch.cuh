@@ -9,11 +9,11 @@ namespace rmsn {
 
 cudaError_t launch_gw_reduce(const float *partials, float *gw, int P, int D, cudaStream_t stream);
 
-template <bool VJP, typename T, int UB, int MAXT, int MINB, int KIND, bool GROW, bool SHIFT, bool FULL = false, bool HALF = false>
+template <bool VJP, typename T, int UB, int MAXT, int MINB, int KIND, bool GROW, bool SHIFT, int FORM = 0, bool HALF = false>
 cudaError_t launch_block_inst(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> smem_mask{0};
     void (*kern)(BlockArgs);
-    if constexpr (VJP) kern = block_vjp_kernel<T, UB, MAXT, MINB, KIND, GROW, SHIFT, FULL, HALF>;
+    if constexpr (VJP) kern = block_vjp_kernel<T, UB, MAXT, MINB, KIND, GROW, SHIFT, FORM, HALF>;
     else kern = block_fwd_kernel<T, UB, MAXT, MINB, KIND, GROW, SHIFT>;
     if (p.smem > 0) {
         const cudaError_t e = allow_max_dynamic_smem((const void *)kern, smem_mask);
@@ -24,13 +24,35 @@ cudaError_t launch_block_inst(const BlockPlan &p, const BlockArgs &a, cudaStream
     return launch_pdl(kern, dim3(p.grid), dim3(p.threads), p.smem, s, a);
 }
 
+// The VJP's instances of one FORM.  With everything known when compiled: a sixth fewer
+// instructions (16384 rows of bf16: D = 4096 139 -> 129 us, D = 512 33.2 -> 28.1).
+template <typename T, bool SHIFT, int FORM>
+cudaError_t launch_block_form(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
+    if constexpr (!SHIFT)
+        if (p.kind == BLOCK_WARP) return launch_block_inst<true, T, 16, 256, 2, BLOCK_WARP, false, false, FORM>(p, a, s);
+    if (p.half) return launch_block_inst<true, T, 16, 640, 1, BLOCK_STAGED, false, SHIFT, FORM, true>(p, a, s);
+    if (p.threads <= 256) return launch_block_inst<true, T, 16, 256, 2, BLOCK_STAGED, false, SHIFT, FORM>(p, a, s);
+    return launch_block_inst<true, T, 16, 512, 1, BLOCK_STAGED, false, SHIFT, FORM>(p, a, s);
+}
+
 template <bool VJP, typename T, int UB, bool GROW, bool SHIFT>
 cudaError_t launch_block_kind(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
-    // FULL: the training backward with all its operands, without their run-time tests
-    // (16384 rows of bf16: D = 4096 139 -> 129 us, D = 512 33.2 -> 28.1).
-    if constexpr (VJP && UB == 16 && !GROW && !SHIFT)
-        if (p.kind == BLOCK_WARP && a.w_post && a.g_res && a.rstd)
-            return launch_block_inst<VJP, T, UB, 256, 2, BLOCK_WARP, GROW, false, true>(p, a, s);
+    if constexpr (VJP && UB == 16 && !GROW)
+        if (p.kind == BLOCK_WARP || (p.kind == BLOCK_STAGED && (p.half || p.threads <= 512))) {
+            constexpr int ALL = FORM_POST | FORM_MORE | FORM_SAVED;
+            const int form = (a.w_post ? FORM_POST : 0) | (a.g_res ? FORM_MORE : 0) | (a.rstd ? FORM_SAVED : 0);
+            if (form == ALL) return launch_block_form<T, SHIFT, ALL>(p, a, s);
+            if constexpr (!SHIFT)
+                switch (form) {
+                    case FORM_POST | FORM_SAVED: return launch_block_form<T, SHIFT, FORM_POST | FORM_SAVED>(p, a, s);
+                    case FORM_MORE | FORM_SAVED: return launch_block_form<T, SHIFT, FORM_MORE | FORM_SAVED>(p, a, s);
+                    case FORM_SAVED: return launch_block_form<T, SHIFT, FORM_SAVED>(p, a, s);
+                    case FORM_POST | FORM_MORE: return launch_block_form<T, SHIFT, FORM_POST | FORM_MORE>(p, a, s);
+                    case FORM_POST: return launch_block_form<T, SHIFT, FORM_POST>(p, a, s);
+                    case FORM_MORE: return launch_block_form<T, SHIFT, FORM_MORE>(p, a, s);
+                    default: break;
+                }
+        }
     if constexpr (!SHIFT)
         if (p.kind == BLOCK_WARP) return launch_block_inst<VJP, T, UB, 256, 2, BLOCK_WARP, GROW, false>(p, a, s);
     if (p.kind == BLOCK_DIRECT) {
@@ -38,17 +60,8 @@ cudaError_t launch_block_kind(const BlockPlan &p, const BlockArgs &a, cudaStream
         return launch_block_inst<VJP, T, UB, 1024, 1, BLOCK_DIRECT, GROW, SHIFT>(p, a, s);
     }
     if constexpr (VJP)
-        if (p.half) {  // at most 96 registers
-            if constexpr (UB == 16 && !GROW)
-                if (a.w_post && a.g_res && a.rstd)
-                    return launch_block_inst<VJP, T, UB, 640, 1, BLOCK_STAGED, GROW, SHIFT, true, true>(p, a, s);
-            return launch_block_inst<VJP, T, UB, 640, 1, BLOCK_STAGED, GROW, SHIFT, false, true>(p, a, s);
-        }
-    if constexpr (VJP && UB == 16 && !GROW)
-        if (a.w_post && a.g_res && a.rstd) {
-            if (p.threads <= 256) return launch_block_inst<VJP, T, UB, 256, 2, BLOCK_STAGED, GROW, SHIFT, true>(p, a, s);
-            if (p.threads <= 512) return launch_block_inst<VJP, T, UB, 512, 1, BLOCK_STAGED, GROW, SHIFT, true>(p, a, s);
-        }
+        if (p.half)  // at most 96 registers
+            return launch_block_inst<VJP, T, UB, 640, 1, BLOCK_STAGED, GROW, SHIFT, 0, true>(p, a, s);
     // Threads an SM holds (block_resident): 512 with 128 registers each; the
     // forward also fits 96, so its CTAs of 257-320 threads sit two an SM and
     // those of 513-640 one.

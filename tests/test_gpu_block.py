@@ -528,3 +528,16 @@ def test_block_calls_of_two_threads():
     for t in threads:
         t.join()
     assert same == [True, True]
+
+
+@pytest.mark.parametrize("rows,D,groups", [(1000, 4096, 8), (1400, 1024, 2), (400, 5120, 0), (320, 8192, 320), (3000, 512, 1),
+                                           (700, 2041, 7), (330, 12288, 1)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_block_vjp_forms(rows, D, groups, dt):
+    """With and without a norm after the block, the gradient of new_residual and saved
+    scales, on the tiers that are compiled for some of these."""
+    for post in (True, False):
+        p = _problem(rows, D, DT[dt], groups, post, 0.0, seed=81)
+        for g_res in (True, False):
+            for saved in (True, False):
+                _check_vjp(p, 1.1, g_res=g_res, saved=saved)
