@@ -41,7 +41,7 @@
 // On the GB300 (6.7 TB/s copied): forward of 16384 x 8192 bf16 with 8 gate rows 166 us
 // (96 % of that), 5000 x 4097 fp16 29 us (84 %); VJP of 16384 x 4096 bf16 133 us (90 %:
 // 123 registers a thread leave an SM 16 warps, and the last 5 us are the second stage),
-// 4095 x 2048 fp32 with a gate row each 43.5 us (80 %), 16384 x 512 28 us (54 %: no ring,
+// 4095 x 2048 fp32 with a gate row each 41 us (85 %), 16384 x 512 28 us (54 %: no ring,
 // and 16 warps an SM do not hide a row's trip to memory).
 #pragma once
 

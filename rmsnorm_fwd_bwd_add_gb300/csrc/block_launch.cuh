@@ -24,34 +24,40 @@ cudaError_t launch_block_inst(const BlockPlan &p, const BlockArgs &a, cudaStream
     return launch_pdl(kern, dim3(p.grid), dim3(p.threads), p.smem, s, a);
 }
 
-// The VJP's instances of one FORM.  With everything known when compiled: a sixth fewer
-// instructions (16384 rows of bf16: D = 4096 139 -> 129 us, D = 512 33.2 -> 28.1).
-template <typename T, bool SHIFT, int FORM>
+// The VJP's instances of one FORM.  Tests of what is there at run time cost a sixth of the
+// instructions, and spills (16384 rows of bf16, D = 4096: without g_res 135 -> 117 us, without
+// saved scales 151 -> 133, without post-norm 146 -> 132; D = 512 33.2 -> 28.1; 4095 x 2048
+// fp32 with a gate row each 43.3 -> 41.1).  Gates of a row each and rows off boundaries
+// have them for the usual training backward.
+template <typename T, bool GROW, bool SHIFT, int FORM>
 cudaError_t launch_block_form(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
     if constexpr (!SHIFT)
-        if (p.kind == BLOCK_WARP) return launch_block_inst<true, T, 16, 256, 2, BLOCK_WARP, false, false, FORM>(p, a, s);
-    if (p.half) return launch_block_inst<true, T, 16, 640, 1, BLOCK_STAGED, false, SHIFT, FORM, true>(p, a, s);
-    if (p.threads <= 256) return launch_block_inst<true, T, 16, 256, 2, BLOCK_STAGED, false, SHIFT, FORM>(p, a, s);
-    return launch_block_inst<true, T, 16, 512, 1, BLOCK_STAGED, false, SHIFT, FORM>(p, a, s);
+        if (p.kind == BLOCK_WARP) return launch_block_inst<true, T, 16, 256, 2, BLOCK_WARP, GROW, false, FORM>(p, a, s);
+    if (p.half) return launch_block_inst<true, T, 16, 640, 1, BLOCK_STAGED, GROW, SHIFT, FORM, true>(p, a, s);
+    if (p.threads <= 256) return launch_block_inst<true, T, 16, 256, 2, BLOCK_STAGED, GROW, SHIFT, FORM>(p, a, s);
+    return launch_block_inst<true, T, 16, 512, 1, BLOCK_STAGED, GROW, SHIFT, FORM>(p, a, s);
 }
 
 template <bool VJP, typename T, int UB, bool GROW, bool SHIFT>
 cudaError_t launch_block_kind(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
-    if constexpr (VJP && UB == 16 && !GROW)
+    if constexpr (VJP && UB == 16 && !(GROW && SHIFT))
         if (p.kind == BLOCK_WARP || (p.kind == BLOCK_STAGED && (p.half || p.threads <= 512))) {
             constexpr int ALL = FORM_POST | FORM_MORE | FORM_SAVED;
             const int form = (a.w_post ? FORM_POST : 0) | (a.g_res ? FORM_MORE : 0) | (a.rstd ? FORM_SAVED : 0);
-            if (form == ALL) return launch_block_form<T, SHIFT, ALL>(p, a, s);
-            if constexpr (!SHIFT)
+            if (form == ALL) return launch_block_form<T, GROW, SHIFT, ALL>(p, a, s);
+            if constexpr (GROW) {
+                if (form == (FORM_POST | FORM_SAVED)) return launch_block_form<T, GROW, SHIFT, FORM_POST | FORM_SAVED>(p, a, s);
+            } else if constexpr (!SHIFT) {
                 switch (form) {
-                    case FORM_POST | FORM_SAVED: return launch_block_form<T, SHIFT, FORM_POST | FORM_SAVED>(p, a, s);
-                    case FORM_MORE | FORM_SAVED: return launch_block_form<T, SHIFT, FORM_MORE | FORM_SAVED>(p, a, s);
-                    case FORM_SAVED: return launch_block_form<T, SHIFT, FORM_SAVED>(p, a, s);
-                    case FORM_POST | FORM_MORE: return launch_block_form<T, SHIFT, FORM_POST | FORM_MORE>(p, a, s);
-                    case FORM_POST: return launch_block_form<T, SHIFT, FORM_POST>(p, a, s);
-                    case FORM_MORE: return launch_block_form<T, SHIFT, FORM_MORE>(p, a, s);
+                    case FORM_POST | FORM_SAVED: return launch_block_form<T, GROW, SHIFT, FORM_POST | FORM_SAVED>(p, a, s);
+                    case FORM_MORE | FORM_SAVED: return launch_block_form<T, GROW, SHIFT, FORM_MORE | FORM_SAVED>(p, a, s);
+                    case FORM_SAVED: return launch_block_form<T, GROW, SHIFT, FORM_SAVED>(p, a, s);
+                    case FORM_POST | FORM_MORE: return launch_block_form<T, GROW, SHIFT, FORM_POST | FORM_MORE>(p, a, s);
+                    case FORM_POST: return launch_block_form<T, GROW, SHIFT, FORM_POST>(p, a, s);
+                    case FORM_MORE: return launch_block_form<T, GROW, SHIFT, FORM_MORE>(p, a, s);
                     default: break;
                 }
+            }
         }
     if constexpr (!SHIFT)
         if (p.kind == BLOCK_WARP) return launch_block_inst<VJP, T, UB, 256, 2, BLOCK_WARP, GROW, false>(p, a, s);
