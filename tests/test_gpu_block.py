@@ -541,3 +541,31 @@ def test_block_vjp_forms(rows, D, groups, dt):
         for g_res in (True, False):
             for saved in (True, False):
                 _check_vjp(p, 1.1, g_res=g_res, saved=saved)
+
+
+@pytest.mark.parametrize("rows,D,groups", [(5, 4096, 5), (60, 384, 1), (650, 2043, 2), (40, 20000, 4)])
+def test_block_replays_with_new_inputs(rows, D, groups):
+    """A captured call reads what its buffers hold when it is replayed: on the
+    cluster, off-boundary and long-row paths."""
+    p, fresh = (_problem(rows, D, torch.bfloat16, groups, True, 0.0, seed=s) for s in (91, 92))
+
+    def both(q):
+        return rn.rmsnorm_block_fwd(q["y"], q["res"], q["w_post"], q["w_pre"], EPS, 0.0, q["gate"], 0.6, rstd=True) + \
+            rn.rmsnorm_block_vjp(q["y"], q["h"], q["w_post"], q["w_pre"], q["g"], EPS, 0.0, q["gate"], 0.6, q["g_res"])
+
+    want = [both(fresh), both(p)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(p)
+    old = {k: v.clone() for k, v in p.items() if torch.is_tensor(v)}
+    for source, expected in ((fresh, want[0]), (old, want[1])):
+        for k in old:
+            p[k].copy_(source[k])
+        for _ in range(2):
+            for t in got:
+                t.fill_(5.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(got, expected):
+                assert torch.equal(a, b)
