@@ -164,10 +164,8 @@ template <typename T, int UB> struct Slot {
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-constexpr int BLOCK_MAX_STAGES = 8;
-// Shared memory of BLOCK_STAGED: the ring's mbarriers, the table w1, the ring.
-constexpr int BLOCK_HEADER = 128;
-
+// Shared memory of BLOCK_STAGED: the ring's mbarriers (BLOCK_HEADER), the table w1,
+// the ring.
 
 // Sums of four (N <= 4) or eight (N <= 8) values over a warp at once.  The first
 // steps halve the number of values a lane carries instead of summing each over

@@ -129,6 +129,11 @@ inline int block_slices(int64_t gate_rows) {
     return gate_rows < 128 ? 1 : gate_rows >= 64 * BLOCK_MAX_SLICES ? BLOCK_MAX_SLICES : (int)(gate_rows / 64);
 }
 
+// The ring of BLOCK_STAGED: its most stages, and the bytes of their mbarriers ahead
+// of the table w1.
+constexpr int BLOCK_MAX_STAGES = 8;
+constexpr int BLOCK_HEADER = 128;
+
 // Bytes of the table w1 in shared memory.
 __host__ __device__ constexpr uint32_t block_table_bytes(int64_t D) { return ((uint32_t)D * 4u + 127u) & ~127u; }
 

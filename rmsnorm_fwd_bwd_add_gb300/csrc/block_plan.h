@@ -21,6 +21,13 @@ inline int block_resident(int threads, bool vjp) {
     return threads > 512 ? 1024 : 512;
 }
 
+// Static shared memory of the widest instance that CTAs of `threads` take: its sums,
+// two buffers of eight floats a warp.  Those of 641 threads or more (VJP: 513) take the
+// one of 1024, the others one of at most 640.
+inline size_t block_static_bytes(int threads, bool vjp, bool half) {
+    return 64 * (threads > (vjp && !half ? 512 : 640) ? 1024 / 32 : 640 / 32);
+}
+
 // Picks tier, unit and grid.  `unit` divides every address and stride (16 at
 // most); `tensors` row tensors are read.  `classes`: 0, or all row tensors stand
 // alike to 16-byte boundaries, a row `classes` rows on (1, 2, 4 or 8) like this one.
@@ -94,17 +101,19 @@ inline BlockPlan make_block_plan(int64_t rows, int64_t D, int es, int unit, int 
     } else {
         p.kind = BLOCK_STAGED;
         p.stage_bytes = (uint32_t)((row + (unit % 16 == 0 && row % 16 == 0 ? 0 : 15) + 15) / 16 * 16);
-        // an SM's shared memory, less 1 KB a CTA for the system and 2 KB for the
-        // rest; fewer CTAs where it would leave them no second stage
+        // an SM's shared memory, less 1 KB a CTA for the system, its barriers and static
+        // sums (2 KB at least) and its table; fewer CTAs where it would leave them no
+        // second stage
         const size_t set = (size_t)tensors * p.stage_bytes;
+        const size_t fixed = BLOCK_HEADER + block_static_bytes((int)threads, vjp, p.half);
         auto stages_of = [&](int ctas) {
-            const size_t share = (BLOCK_SMEM_PER_SM + 1024) / ctas, used = 3 * 1024 + tables;
-            return share > used ? (int)std::min<size_t>(8, (share - used) / set) : 0;
+            const size_t share = (BLOCK_SMEM_PER_SM + 1024) / ctas, used = 1024 + std::max<size_t>(2 * 1024, fixed) + tables;
+            return share > used ? (int)std::min<size_t>(BLOCK_MAX_STAGES, (share - used) / set) : 0;
         };
         while (per_sm > 1 && stages_of(per_sm) < 2) --per_sm;
         p.stages = stages_of(per_sm);
         p.grid = (int)std::min<int64_t>(rows, (int64_t)sm * per_sm);
-        p.smem = 128 + tables + (size_t)p.stages * set;
+        p.smem = BLOCK_HEADER + tables + (size_t)p.stages * set;
         if (p.stages < 1) return p.shift ? unshifted() : generic_plan();
     }
     if (vjp && p.kind == BLOCK_WARP && !p.cluster)  // scratch traffic small beside the rows'

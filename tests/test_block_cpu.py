@@ -232,6 +232,38 @@ int main() {
 }
 """
 
+LIMITS = r"""
+#include <cstdio>
+#include "block_plan.h"
+using namespace rmsn;
+// The widest CTA of the instance that a plan takes: its sums are two buffers of eight
+// floats a warp in static shared memory, beside the ring and table asked for at launch.
+int widest(const BlockPlan &p, bool vjp) {
+    for (int t : {256, 320, 512, 640})
+        if (p.threads <= t && (t % 320 || (vjp ? t == 640 && p.half : true))) return t;
+    return 1024;
+}
+int main() {
+    for (int es : {2, 4})
+        for (int64_t D = 1; D <= 32768 / es; ++D)
+            for (int64_t rows : {153, 400, 4000})
+                for (int vjp = 0; vjp < 2; ++vjp)
+                    for (int tensors = vjp ? 3 : 2; tensors <= (vjp ? 5 : 3); ++tensors)
+                        for (int classes : {0, 1, 2, 4, 8})
+                            for (int unit : {16, es}) {
+                                const BlockPlan p = make_block_plan(rows, D, es, unit, tensors, vjp, 1, 152, classes);
+                                if (p.kind == BLOCK_GENERIC) continue;
+                                const size_t sums = p.kind == BLOCK_WARP ? 64 : 64 * widest(p, vjp) / 32;
+                                if (p.smem + sums > 227 * 1024) {
+                                    printf("rows %ld D %ld es %d vjp %d tensors %d unit %d classes %d: %zu + %zu bytes\n", (long)rows,
+                                           (long)D, es, vjp, tensors, unit, classes, p.smem, sums);
+                                    return 1;
+                                }
+                            }
+    return 0;
+}
+"""
+
 
 def _run(tmp_path, name, text):
     src, exe = tmp_path / (name + ".cu"), tmp_path / name
@@ -251,3 +283,9 @@ def test_plans_stay_within_the_chip_and_the_workspace(tmp_path):
     """Every plan fits its threads, ring and shared memory, and the VJP's never has
     more CTAs than the workspace query counted on."""
     _run(tmp_path, "plan", PLAN)
+
+
+def test_plans_leave_room_for_the_kernels_static_sums(tmp_path):
+    """What a launch asks for and what its kernel holds anyway fit a CTA's shared
+    memory together, at every row length that has a plan on chip."""
+    _run(tmp_path, "limits", LIMITS)

@@ -569,3 +569,15 @@ def test_block_replays_with_new_inputs(rows, D, groups):
             torch.cuda.synchronize()
             for a, b in zip(got, expected):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dt,widths", [("f32", (4428, 5760, 6400, 6393)), ("bf16", (9600, 11520, 14400, 14377, 10457, 11505))])
+def test_block_rings_that_fill_shared_memory(dt, widths):
+    """Widths whose ring, table and sums come within bytes of what a CTA may have, with
+    more rows than SMs and with every number of row tensors in the ring."""
+    for D in widths:
+        for groups in (1, 400):
+            p = _problem(400, D, DT[dt], groups, True, 0.0, seed=101)
+            _check_fwd(p, 0.9)
+            for g_res in (True, False):
+                _check_vjp(p, 0.9, g_res=g_res, saved=g_res)
