@@ -275,7 +275,7 @@ int rmsnorm_block_fwd(const void *y, int64_t ld_y, const void *residual, int64_t
  * 32 more) comes from the library's pool.  g_y and g_h may each be one of the row
  * inputs.  With w_post, the products of m = scale * gate * (weight_bias + w_post),
  * y and h or g_out are summed in fp32 before the scales are applied, and have to stay
- * in its range.
+ * in its normal range; the scales have to, their squares need not.
  */
 int rmsnorm_block_vjp(const void *y, int64_t ld_y, const void *h, int64_t ld_h, const void *w_post,
                       const void *w_pre, const void *gate, int64_t ld_gate, int64_t gate_rows,

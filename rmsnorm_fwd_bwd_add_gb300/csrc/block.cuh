@@ -889,9 +889,10 @@ __global__ void __launch_bounds__(MAXT, MINB) block_vjp_kernel(const __grid_cons
                 r_h = rsqrtf(sum[4] * inv_D + a.eps);
                 if (post) r_y = rsqrtf(sum[5] * inv_D + a.eps);
             }
-            const float cc = (r_h * r_h) * (sum[0] * inv_D);
+            // scale by scale: without an epsilon a tiny row's r^2 can leave fp32's range
+            const float cc = r_h * (r_h * (sum[0] * inv_D));
             const float dot = fmaf(r_h, sum[1] - cc * sum[2], sum[3]);  // sum of m g_h y
-            const float ee = post ? (r_y * r_y) * (dot * inv_D) : 0.f;
+            const float ee = post ? r_y * (r_y * (dot * inv_D)) : 0.f;
             T *gy = static_cast<T *>(a.out0) + row * a.ld_out0;
             T *gh = static_cast<T *>(a.out1) + row * a.ld_out1;
 #pragma unroll

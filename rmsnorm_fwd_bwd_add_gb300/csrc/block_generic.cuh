@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(BLOCK_GENERIC_NT, 2) block_vjp_generic_kernel(
 #pragma unroll
             for (int e = 0; e < E; ++e) s = fmaf(x[e] * (wb + w[e]), h[e], s);
         }
-        const float cc = (r_h * r_h) * (cta_sum<NT>(s, red) * inv_D);
+        const float cc = r_h * (r_h * (cta_sum<NT>(s, red) * inv_D));  // r_h^2 alone can leave fp32's range
         // g_h, with g and h of the unit
         auto grad_h = [&](int u, float (&v)[E], float (&x)[E], float (&h)[E]) {
             float w[E];
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(BLOCK_GENERIC_NT, 2) block_vjp_generic_kernel(
 #pragma unroll
                 for (int e = 0; e < E; ++e) s = fmaf(m[e] * v[e], yv[e], s);
             }
-            ee = (r_y * r_y) * (cta_sum<NT>(s, red) * inv_D);
+            ee = r_y * (r_y * (cta_sum<NT>(s, red) * inv_D));
         }
         // this gate row's sum: whole here (its own row of g_gate), or a part
         const bool whole = a.g_gate && gr * a.rows_per_gate >= r0 && (gr + 1) * a.rows_per_gate <= r1;

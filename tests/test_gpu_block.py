@@ -581,3 +581,26 @@ def test_block_rings_that_fill_shared_memory(dt, widths):
             _check_fwd(p, 0.9)
             for g_res in (True, False):
                 _check_vjp(p, 0.9, g_res=g_res, saved=g_res)
+
+
+@pytest.mark.parametrize("rows,D,groups", [(8, 512, 1), (330, 384, 330), (330, 4096, 3), (330, 4099, 1), (330, 5120, 0), (6, 4096, 6),
+                                           (24, 20000, 2)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("tiny", ["y", "h"])
+def test_block_vjp_of_rows_whose_scale_squared_leaves_fp32(rows, D, groups, dt, tiny):
+    """Without an epsilon, rows of 3e-20 have a scale near 3e19, whose square is past
+    fp32 while every gradient is in it.  The mean of their squares, 9e-40, is a subnormal:
+    a sum and its mean are off by 2^-150 / 2^-130 = 16 u more each, beside the 64 u of a
+    sum, so k is 256 * 96 / 64."""
+    for post in (True, False):
+        for saved in (True, False):
+            p = _problem(rows, D, DT[dt], groups, post, 0.0, seed=111)
+            p[tiny] = _rand(torch.Generator().manual_seed(5), rows, D, DT[dt], std=3e-20)
+            r = [1 / torch.sqrt((t.double() ** 2).mean(1)) for t in (p["y"], p["h"])]
+            rstd = torch.stack(r).float() if saved else None
+            got = rn.rmsnorm_block_vjp(p["y"], p["h"], p["w_post"], p["w_pre"], p["g"], 0.0, 0.0, p["gate"], 0.7,
+                                       p["g_res"], rstd=rstd)
+            want = ref.vjp(p["y"], p["h"], p["w_post"], p["w_pre"], p["g"], 0.0, 0.0, p["gate"], 0.7, p["g_res"], rstd)
+            for name, t in zip(("g_y", "g_h", "gw_post", "gw_pre", "g_gate"), got):
+                if name in want:
+                    ref.check(name, t, *want[name], k=384.0 if name in ("g_y", "g_h") else 384.0 + 64.0 + rows / 8)
