@@ -239,7 +239,8 @@ int rmsnorm_vjp_ws(const void *x, const void *w, const void *g, float eps,
  *   gate         [gate_rows, D] dtype with row stride ld_gate, or NULL (1).
  *                gate_rows divides rows: gate row j multiplies the rows / gate_rows
  *                consecutive rows from j * rows / gate_rows on (gate_rows = 1: one
- *                learned gate; a row per sequence; gate_rows = rows: one per row).
+ *                learned gate; a row per sequence; gate_rows = rows: one per row,
+ *                none for rows == 0).
  *   scale        finite scalar, the residual scale of the block.
  *   out, new_residual  [rows, D] dtype; new_residual receives round(h), h is
  *                normalised unrounded.

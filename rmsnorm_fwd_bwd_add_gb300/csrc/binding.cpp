@@ -265,7 +265,7 @@ Gate check_gate(const Tensor *gate, const Tensor &x, int64_t rows, int64_t D) {
     if (gate->dim() < 1 || gate->size(-1) != D)
         fail(PyExc_ValueError, "gate must be [..., %lld], got %s", (long long)D, shape_str(gate->sizes()).c_str());
     const Rows r = rows_ld("gate", *gate);
-    if (r.rows < 1 || rows % r.rows)
+    if (r.rows < 1 ? rows != 0 : rows % r.rows != 0)
         fail(PyExc_ValueError, "the gate's %lld rows must divide the %lld rows", (long long)r.rows, (long long)rows);
     return {r.rows, r.ld};
 }

@@ -72,7 +72,7 @@ int check_block(const void *w_post, const void *w_pre, const void *gate, int64_t
     if (!w_pre || !std::isfinite(scale)) return RMSNORM_ERR_INVALID_ARG;
     if (!elem_aligned(w_pre, es) || !elem_aligned(w_post, es) || !elem_aligned(gate, es))
         return RMSNORM_ERR_INVALID_ARG;
-    if (gate) {
+    if (gate && (rows || gate_rows)) {  // a gate row for each of no rows: none
         if (gate_rows <= 0 || rows % gate_rows) return RMSNORM_ERR_INVALID_ARG;
         if (gate_rows > INT64_MAX / (8 * D)) return RMSNORM_ERR_UNSUPPORTED;
         if (gate_rows > 1) return check_ld(ld_gate, gate_rows, D, es);

@@ -58,6 +58,11 @@ def test_block_vjp_refusals(lib):
     assert vjp(lib, rows=0, gate=12 * A, G=1 << 58, g_gate=13 * A) == 2
 
 
+def test_block_fwd_takes_no_gate_rows_for_no_rows(lib):
+    assert fwd(lib, rows=0, gate=11 * A, G=0) == 0 and fwd(lib, rows=0, gate=11 * A, G=3) == 0
+    assert fwd(lib, rows=8, gate=11 * A, G=0) == 1 and fwd(lib, rows=0, gate=11 * A, G=-1) == 1
+
+
 SPLIT = r"""
 #include <cstdio>
 #include <cstdlib>

@@ -604,3 +604,22 @@ def test_block_vjp_of_rows_whose_scale_squared_leaves_fp32(rows, D, groups, dt, 
             for name, t in zip(("g_y", "g_h", "gw_post", "gw_pre", "g_gate"), got):
                 if name in want:
                     ref.check(name, t, *want[name], k=384.0 if name in ("g_y", "g_h") else 384.0 + 64.0 + rows / 8)
+
+
+def test_block_no_rows_and_a_gate_for_each():
+    """An empty batch with a gate row per row: no gate rows."""
+    for shape in ((0, 64), (2, 0, 64)):
+        y = torch.zeros(shape, dtype=torch.bfloat16, device=DEV)
+        w = torch.ones(64, dtype=torch.bfloat16, device=DEV)
+        out, nr, _ = rn.rmsnorm_block_fwd(y, y, w, w, EPS, 0.0, y)
+        assert out.shape == shape and nr.shape == shape
+        got = rn.rmsnorm_block_vjp(y, y, w, w, y, EPS, 0.0, y)
+        assert got[4].shape == shape and got[4].dtype == torch.float32
+        assert (got[2] == 0).all() and (got[3] == 0).all()
+        leaves = [t.clone().requires_grad_() for t in (y, y, w, w, y)]
+        out, nr = rn.block_norm(leaves[0], leaves[1], leaves[2], leaves[3], EPS, 0.0, leaves[4])
+        grads = torch.autograd.grad([out, nr], leaves, [y, y])
+        assert grads[4].shape == shape and (grads[2] == 0).all()
+    full = torch.zeros(3, 64, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError):
+        rn.rmsnorm_block_fwd(full, full.clone(), w, w, EPS, 0.0, full[:0])
