@@ -101,7 +101,7 @@ def _rows_ld(name: str, t: torch.Tensor) -> Tuple[int, int, int]:
         raise ValueError("tensors must be CUDA tensors (there is no CPU path)")
     D = t.shape[-1]
     rows = t.numel() // D if D else 0
-    if D > 1 and t.stride(-1) != 1:
+    if rows and D > 1 and t.stride(-1) != 1:
         raise ValueError("%s: the elements of a row must be contiguous" % name)
     lead = [(n, st) for n, st in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]
     if rows <= 1 or not lead:

@@ -158,7 +158,7 @@ Rows rows_ld(const char *name, const Tensor &t) {
     need_cuda(t);
     const auto sizes = t.sizes(), strides = t.strides();
     const int64_t D = sizes[dim - 1], rows = D ? t.numel() / D : 0;
-    if (D > 1 && strides[dim - 1] != 1)
+    if (rows && D > 1 && strides[dim - 1] != 1)
         fail(PyExc_ValueError, "%s: the elements of a row must be contiguous", name);
     if (rows <= 1) return {rows, D, D};
     int64_t ld = 0, span = 0;  // stride of the innermost long dimension; what the next one must step
@@ -371,7 +371,7 @@ struct Strides {
 };
 
 Strides head_strides(const char *name, const Tensor &t) {
-    if (t.size(-1) > 1 && t.stride(-1) != 1)
+    if (t.numel() && t.size(-1) > 1 && t.stride(-1) != 1)
         fail(PyExc_ValueError, "%s: the elements of a head must be contiguous", name);
     return {{t.dim() == 4 ? t.stride(0) : 0, t.stride(-3), t.stride(-2)}};
 }

@@ -623,3 +623,20 @@ def test_block_no_rows_and_a_gate_for_each():
     full = torch.zeros(3, 64, dtype=torch.bfloat16, device=DEV)
     with pytest.raises(ValueError):
         rn.rmsnorm_block_fwd(full, full.clone(), w, w, EPS, 0.0, full[:0])
+
+
+def test_gradients_of_no_rows_through_a_sum():
+    """The gradient of a sum is an expanded scalar; with no rows torch counts it as
+    contiguous whatever its strides."""
+    y, res, gate = (torch.zeros(2, 0, 64, dtype=torch.bfloat16, device=DEV).requires_grad_() for _ in range(3))
+    w = torch.ones(64, dtype=torch.bfloat16, device=DEV).requires_grad_()
+    for call in (lambda: rn.block_norm(y, res, w, w, EPS, 0.0, gate), lambda: rn.block_norm(y, res, None, w, EPS),
+                 lambda: rn.fused_add_rmsnorm(y, res, w, EPS), lambda: (rn.rms_norm(y, w, EPS),)):
+        w.grad = None
+        sum(t.sum() for t in call()).backward()
+        assert (w.grad == 0).all()
+    q = torch.zeros(0, 4, 16, dtype=torch.bfloat16, device=DEV).requires_grad_()
+    inv, _ = rn.rope_frequencies(8)
+    turned, _ = rn.rope(q, None, torch.zeros(0, dtype=torch.int64, device=DEV), inv)
+    turned.sum().backward()
+    assert q.grad.shape == q.shape
