@@ -8,7 +8,9 @@ runs in the library's CUDA kernels; nothing here computes.
 Tensors: x, residual, g are [..., D] fp16, bf16 or fp32 CUDA tensors,
 contiguous (the *_ex functions also take rows a stride apart: a slice of a
 wider buffer); w is [D] of the same dtype; gw and rstd are fp32.  Leading
-dimensions are flattened into rows.
+dimensions are flattened into rows.  Tensors that the caller gives to be written
+(outputs, caches, tables, in-place inputs) count as changed in place: autograd
+refuses a backward pass through what they held.
 """
 from __future__ import annotations
 
@@ -59,6 +61,18 @@ def _rows_d(x: torch.Tensor) -> Tuple[int, int]:
 # torch entry point present in the supported versions; the public route is the
 # fallback).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+# Counts tensors as changed in place, without the Python around it.
+_increment_version = getattr(torch._C, "_increment_version", None) or torch.autograd.graph.increment_version
+
+
+def _wrote(*tensors: Optional[torch.Tensor]) -> None:
+    """Tells autograd that a call wrote into the caller's tensors (None: not the
+    caller's), so that it refuses a backward pass through what they held."""
+    given = [t for t in tensors if t is not None]
+    if given:
+        _increment_version(given)
 
 
 def _stream(device: torch.device, stream) -> int:
@@ -218,6 +232,7 @@ def rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, eps: float, weight_bias: float
     new_residual=residual to update in place."""
     rows, D, dev, code = _rows_dev(x)
     _weight(w, x, D, dev)
+    given = (out, new_residual)
     if out is None:
         out = torch.empty_like(x)
     else:
@@ -238,6 +253,7 @@ def rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, eps: float, weight_bias: float
                    eps, weight_bias, out.data_ptr() or None, None, rows, D, code)
     if st:
         _native.check("rmsnorm_fwd", st)
+    _wrote(*given)
     return out, new_residual
 
 
@@ -249,6 +265,7 @@ def rmsnorm_vjp(x: torch.Tensor, w: torch.Tensor, g: torch.Tensor, eps: float,
     rows, D, dev, code = _rows_dev(x)
     _weight(w, x, D, dev)
     _like("g", g, x, dev)
+    given = (gx, gw)
     if gx is None:
         gx = torch.empty_like(x)
     else:
@@ -259,6 +276,7 @@ def rmsnorm_vjp(x: torch.Tensor, w: torch.Tensor, g: torch.Tensor, eps: float,
                D, code)
     if st:
         _native.check("rmsnorm_vjp", st)
+    _wrote(*given)
     return gx, gw
 
 
@@ -274,6 +292,7 @@ def rmsnorm_fused_vjp(h: torch.Tensor, w: torch.Tensor, g_out: torch.Tensor, eps
     _like("g_out", g_out, h, dev)
     if g_residual is not None:
         _like("g_residual", g_residual, h, dev)
+    given = (g_h, gw)
     if g_h is None:
         g_h = torch.empty_like(h)
     else:
@@ -285,6 +304,7 @@ def rmsnorm_fused_vjp(h: torch.Tensor, w: torch.Tensor, g_out: torch.Tensor, eps
                g_h.data_ptr() or None, gw.data_ptr(), rows, D, code)
     if st:
         _native.check("rmsnorm_fused_vjp", st)
+    _wrote(*given)
     return g_h, gw
 
 
@@ -296,7 +316,7 @@ class BoundCall:
     norm): it keeps the tensors alive, and they must keep their storage,
     shape and dtype for as long as the bound call is used."""
 
-    __slots__ = ("_fn", "_args", "_dev", "_stream", "_name", "_keep", "outputs")
+    __slots__ = ("_fn", "_args", "_dev", "_stream", "_name", "_keep", "outputs", "_written")
 
     def __init__(self, name, fn, args, dev, stream, keep, outputs):
         self._name = name
@@ -306,11 +326,13 @@ class BoundCall:
         self._stream = stream
         self._keep = keep
         self.outputs = outputs
+        self._written = tuple(t for t in outputs if t is not None)
 
     def __call__(self):
         st = _call(self._dev, self._stream, self._fn, *self._args)
         if st:
             _native.check(self._name, st)
+        _increment_version(self._written)
         return self.outputs
 
 
@@ -376,6 +398,7 @@ def rmsnorm_gated_silu(x: torch.Tensor, *, out: Optional[torch.Tensor] = None, s
     rows, two_d = _rows_d(x)
     d = two_d // 2
     code = _dtype_code(x, (0, 1))
+    given = out
     if out is None:
         out = torch.empty(*x.shape[:-1], d, dtype=x.dtype, device=x.device)
     if (out.dtype != x.dtype or out.device != x.device or out.shape != (*x.shape[:-1], d)
@@ -386,6 +409,7 @@ def rmsnorm_gated_silu(x: torch.Tensor, *, out: Optional[torch.Tensor] = None, s
         st = _native.lib().rmsnorm_gated_silu(_ptr(x), _ptr(out), rows, d, code,
                                               _stream(x.device, stream))
     _native.check("rmsnorm_gated_silu", st)
+    _wrote(given)
     return out
 
 
@@ -421,6 +445,7 @@ def rmsnorm_rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                 or cos_sin.device != q.device or not cos_sin.is_contiguous()):
             raise ValueError("cos_sin must be a contiguous [max_pos, Dh] float32 tensor")
         max_pos = cos_sin.shape[0]
+    given = q_out
     if q_out is None:
         q_out = torch.empty_like(q)
     _check_like("q_out", q_out, q)
@@ -430,6 +455,7 @@ def rmsnorm_rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
             _ptr(v_cache), _ptr(cos_sin), max_pos, rope_base, 1 if interleaved else 0, T, Hq, Hkv,
             Dh, k_cache.shape[0], code, _stream(q.device, stream))
     _native.check("rmsnorm_rope_kv_append", st)
+    _wrote(given, k_cache, v_cache)
     return q_out
 
 
@@ -545,6 +571,7 @@ def rmsnorm_fwd_ex(x: torch.Tensor, w: torch.Tensor, eps: float, weight_bias: fl
     rows, D, ld_x = _rows_ld("x", x)
     code = _dtype_code(x)
     _check_w(w, x, D)
+    given = (out, new_residual, None if rstd is True else rstd)
     ld_r = ld_n = D
     if residual is not None:
         ld_r = _check_rows_like("residual", residual, x)
@@ -565,6 +592,7 @@ def rmsnorm_fwd_ex(x: torch.Tensor, w: torch.Tensor, eps: float, weight_bias: fl
                                           weight_bias, _ptr(out), ld_o, _ptr(new_residual), ld_n,
                                           _ptr(rstd), rows, D, code, _stream(x.device, stream))
     _native.check("rmsnorm_fwd_ex", st)
+    _wrote(*given)
     return out, new_residual, rstd
 
 
@@ -582,6 +610,7 @@ def rmsnorm_vjp_ex(x: torch.Tensor, w: torch.Tensor, g: torch.Tensor, eps: float
     ld_gr = D
     if g_residual is not None:
         ld_gr = _check_rows_like("g_residual", g_residual, x)
+    given = (gx, gw)
     if gx is None:
         gx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     ld_gx = _check_rows_like("gx", gx, x)
@@ -597,6 +626,7 @@ def rmsnorm_vjp_ex(x: torch.Tensor, w: torch.Tensor, g: torch.Tensor, eps: float
                                           ld_gr, _ptr(rstd), eps, weight_bias, _ptr(gx), ld_gx,
                                           _ptr(gw), rows, D, code, _stream(x.device, stream))
     _native.check("rmsnorm_vjp_ex", st)
+    _wrote(*given)
     return gx, gw
 
 
@@ -666,6 +696,7 @@ def rmsnorm_vjp_ws(x: torch.Tensor, w: torch.Tensor, g: torch.Tensor, eps: float
     rows, D = _rows_d(x)
     code = _dtype_code(x)
     _check_w(w, x, D)
+    given = (gx, gw, workspace)
     gx, gw = _vjp_outputs(x, g, gx, gw, D)
     with _OnDevice(x.device):
         if workspace is None:
@@ -678,6 +709,7 @@ def rmsnorm_vjp_ws(x: torch.Tensor, w: torch.Tensor, g: torch.Tensor, eps: float
                                           _ptr(gx), _ptr(gw), rows, D, code, _ptr(workspace),
                                           nbytes, _stream(x.device, stream))
     _native.check("rmsnorm_vjp_ws", st)
+    _wrote(*given)
     return gx, gw
 
 
@@ -691,12 +723,14 @@ def rmsnorm_vjp_noalloc(x: torch.Tensor, w: torch.Tensor, g: torch.Tensor, eps: 
     rows, D = _rows_d(x)
     code = _dtype_code(x)
     _check_w(w, x, D)
+    given = (gx, gw)
     gx, gw = _vjp_outputs(x, g, gx, gw, D)
     with _OnDevice(x.device):
         st = _native.lib().rmsnorm_vjp_noalloc(_ptr(x), _ptr(w), _ptr(g), eps, weight_bias,
                                                _ptr(gx), _ptr(gw), rows, D, code,
                                                _stream(x.device, stream))
     _native.check("rmsnorm_vjp_noalloc", st)
+    _wrote(*given)
     return gx, gw
 
 

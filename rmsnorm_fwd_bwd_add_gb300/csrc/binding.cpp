@@ -128,6 +128,16 @@ struct Args {
 
 void *ptr(const Tensor *t) { return t && t->numel() ? t->data_ptr() : nullptr; }
 
+// A tensor of the caller's that the call wrote: an in-place change to autograd, which
+// then refuses a backward pass through what was there.
+void wrote(const Tensor *t) {
+    if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+template <typename... P> void wrote(const Tensor *t, const P *...more) {
+    wrote(t);
+    wrote(more...);
+}
+
 void need_cuda(const Tensor &t) {
     if (!t.is_cuda()) fail(PyExc_ValueError, "tensors must be CUDA tensors (there is no CPU path)");
 }
@@ -311,6 +321,7 @@ PyObject *block_fwd(PyObject *, PyObject *const *argv, Py_ssize_t n) {
                                  (float)a.number(7), (float)a.number(4), (float)a.number(5), ptr(&out.first),
                                  out.second, ptr(&nr.first), nr.second,
                                  rstd ? static_cast<float *>(ptr(&*rstd)) : nullptr, r.rows, r.D, code, on.stream));
+        wrote(a.optional(8, "out"), a.optional(9, "new_residual"), argv[10] == Py_True ? nullptr : a.optional(10, "rstd"));
         return tuple_of(wrap(out.first), wrap(nr.first), wrap_or_none(rstd));
     });
 }
@@ -350,6 +361,8 @@ PyObject *block_vjp(PyObject *, PyObject *const *argv, Py_ssize_t n) {
                                  ptr(&g_y.first), g_y.second, ptr(&g_h.first), g_h.second, f32(gw_post),
                                  static_cast<float *>(ptr(&gw_pre)), f32(g_gate), r.rows, r.D, code, ptr(&ws), (size_t)bytes,
                                  on.stream));
+        wrote(a.optional(11, "g_y"), a.optional(12, "g_h"), a.optional(13, "gw_post"), a.optional(14, "gw_pre"),
+              a.optional(15, "g_gate"));
         return tuple_of(wrap(g_y.first), wrap(g_h.first), wrap_or_none(gw_post), wrap(gw_pre), wrap_or_none(g_gate));
     });
 }
@@ -429,6 +442,7 @@ PyObject *rope(PyObject *, PyObject *const *argv, Py_ssize_t n) {
                             ko ? ptr(&*ko) : nullptr, sko.s, static_cast<const double *>(inv.data_ptr()),
                             (float)a.number(4), a.truth(5) ? 1 : 0, a.truth(6) ? 1 : 0, dim == 4 ? q.size(0) : 1,
                             q.size(dim - 3), Hq, Hkv, Dh, rot, code, on.stream));
+        wrote(a.optional(7, "q_out"), a.optional(8, "k_out"));
         return tuple_of(wrap(qo), wrap_or_none(ko));
     });
 }
@@ -463,6 +477,7 @@ PyObject *rope_append(PyObject *, PyObject *const *argv, Py_ssize_t n) {
                                    ptr(&qo), sqo.s + 1, ptr(&kc), skc.s + 1, ptr(&vc), svc.s + 1,
                                    static_cast<const double *>(inv.data_ptr()), (float)a.number(8),
                                    a.truth(9) ? 1 : 0, T, Hq, Hkv, Dh, rot, kc.size(0), code, on.stream));
+        wrote(&kc, &vc, a.optional(10, "q_out"));
         return wrap(qo);
     });
 }
@@ -514,6 +529,7 @@ PyObject *kv_release(PyObject *, PyObject *const *argv, Py_ssize_t n) {
                      c_kv_release(i32(&lens), static_cast<const uint8_t *>(ptr(&fin)), i32(&table), p.ld, p.W,
                                   a.integer(3), i32(&free_blocks), i32(&count), p.N, i32(lo), i32(co), p.B,
                                   on.stream));
+        wrote(lo, co, &free_blocks);
         return tuple_of(wrap(*lo), wrap(*co));
     });
 }
@@ -545,6 +561,8 @@ PyObject *kv_plan(PyObject *, PyObject *const *argv, Py_ssize_t n) {
                                i32(count), p.N, i32(lo), i32(co), static_cast<int64_t *>(ptr(&starts)),
                                static_cast<int64_t *>(ptr(&positions)), static_cast<int64_t *>(ptr(&slots)),
                                i32(&requests), static_cast<uint8_t *>(ptr(&granted)), p.B, T, on.stream));
+        wrote(lo, co, count ? &table : nullptr, a.optional(9, "positions"), a.optional(10, "slots"),
+              a.optional(11, "requests"), a.optional(12, "starts"), a.optional(13, "granted"));
         return tuple_of(wrap(positions), wrap(slots), wrap(requests), wrap(starts), wrap(granted), wrap(*lo),
                         co ? wrap(*co) : none());
     });
