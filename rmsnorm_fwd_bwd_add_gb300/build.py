@@ -1,6 +1,7 @@
 """Builds librmsnorm_gb300.so in-tree from csrc/*.cu with nvcc for sm_103a, and
 _binding.*.so, the native argument marshalling of api.py, from csrc/binding.cpp
 with g++ against the installed torch (its version is part of the file's name).
+The library needs nvcc alone; without torch the binding is left out.
 
 Each translation unit compiles in its own nvcc process (in parallel), then
 nvcc links them into one shared library with the CUDA runtime linked
@@ -8,6 +9,7 @@ statically, so the library needs only the driver at run time.  Rebuilds only
 when a source or header is newer than the library.
 
     python -m rmsnorm_fwd_bwd_add_gb300.build [--force] [--verbose]
+    python rmsnorm_fwd_bwd_add_gb300/build.py [--force] [--verbose]   # without torch
 """
 from __future__ import annotations
 
@@ -98,28 +100,38 @@ def _compile_binding(path: str) -> None:
     os.replace(tmp, path)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link the library and the binding if needed; returns the
-    library's path."""
-    binding = binding_path()
-    lib_stale, binding_stale = force or _stale(LIB_PATH), force or _binding_stale(binding)
-    if not lib_stale and not binding_stale:
-        return LIB_PATH
-    os.makedirs(OBJ_DIR, exist_ok=True)
-    srcs = _sources() if lib_stale else []
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        bound = ex.submit(_compile_binding, binding) if binding_stale else None
+def _build_library(verbose: bool) -> None:
+    srcs = _sources()
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        if bound is not None:
-            bound.result()
-    if not lib_stale:
-        return LIB_PATH
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
     cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("nvcc link failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB_PATH)
+
+
+def _have_torch() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return False
+    return True
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile and link the library and, where torch is installed, the binding if
+    needed; returns the library's path.  A binding that does not compile is raised
+    once the library is linked."""
+    binding = binding_path() if _have_torch() else None
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:  # beside the library
+        bound = ex.submit(_compile_binding, binding) if binding and (force or _binding_stale(binding)) else None
+        if force or _stale(LIB_PATH):
+            _build_library(verbose)
+        if bound is not None:
+            bound.result()
     return LIB_PATH
 
 
