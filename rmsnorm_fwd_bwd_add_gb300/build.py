@@ -79,21 +79,24 @@ def _compile(src: str, verbose: bool) -> str:
 
 
 def _binding_stale(path: str) -> bool:
-    src = os.path.join(CSRC, "binding.cpp")
-    return not os.path.exists(path) or os.path.getmtime(src) > os.path.getmtime(path)
+    deps = [os.path.join(CSRC, "binding.cpp"), *glob.glob(os.path.join(INCLUDE, "*.h"))]
+    return not os.path.exists(path) or any(os.path.getmtime(d) > os.path.getmtime(path) for d in deps)
+
+
+def _binding_flags() -> list:
+    import torch
+    inc = [sysconfig.get_paths()["include"], os.path.join(os.path.dirname(torch.__file__), "include"),
+           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")]
+    return ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(), *("-isystem" + i for i in inc)]
 
 
 def _compile_binding(path: str) -> None:
     import torch
-    root = os.path.dirname(torch.__file__)
-    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
-           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")]
     tmp = path + ".tmp%d" % os.getpid()
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(),
-           os.path.join(CSRC, "binding.cpp"), "-o", tmp]
-    cmd += ["-isystem" + i for i in inc]
-    cmd += ["-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    cmd = ["g++", *_binding_flags(), "-I" + INCLUDE, "-shared", os.path.join(CSRC, "binding.cpp"), "-o", tmp]
+    cmd += ["-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed on binding.cpp:\n%s\n%s" % (r.stdout, r.stderr))

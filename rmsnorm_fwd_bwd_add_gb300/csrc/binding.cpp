@@ -24,6 +24,8 @@
 #include <optional>
 #include <string>
 
+#include "rmsnorm.h"
+
 namespace {
 
 using at::Tensor;
@@ -61,33 +63,16 @@ const char *dtype_str(at::ScalarType t) {
 // ---- the library -----------------------------------------------------------
 PyObject *g_check = nullptr;  // check(name, status): raises for a status other than 0
 
-using BlockFwd = int (*)(const void *, int64_t, const void *, int64_t, const void *, const void *, const void *,
-                         int64_t, int64_t, float, float, float, void *, int64_t, void *, int64_t, float *, int64_t,
-                         int64_t, int, void *);
-using BlockVjp = int (*)(const void *, int64_t, const void *, int64_t, const void *, const void *, const void *,
-                         int64_t, int64_t, float, const void *, int64_t, const void *, int64_t, const float *, float,
-                         float, void *, int64_t, void *, int64_t, float *, float *, float *, int64_t, int64_t, int,
-                         void *, size_t, void *);
-using BlockVjpSize = size_t (*)(int64_t, int64_t, int);
-using Rope = int (*)(const void *, const int64_t *, const void *, const int64_t *, const int64_t *, void *,
-                     const int64_t *, void *, const int64_t *, const double *, float, int, int, int64_t, int64_t,
-                     int64_t, int64_t, int64_t, int64_t, int, void *);
-using RopeAppend = int (*)(const void *, const int64_t *, const void *, const int64_t *, const void *,
-                           const int64_t *, const int64_t *, const int64_t *, void *, const int64_t *, void *,
-                           const int64_t *, void *, const int64_t *, const double *, float, int, int64_t, int64_t,
-                           int64_t, int64_t, int64_t, int64_t, int, void *);
-using KvRelease = int (*)(const int32_t *, const uint8_t *, const int32_t *, int64_t, int64_t, int64_t, int32_t *,
-                          const int32_t *, int64_t, int32_t *, int32_t *, int64_t, void *);
-using KvPlan = int (*)(const int32_t *, const int32_t *, int32_t *, int64_t, int64_t, int64_t, const int32_t *,
-                       const int32_t *, int64_t, int32_t *, int32_t *, int64_t *, int64_t *, int64_t *, int32_t *,
-                       uint8_t *, int64_t, int64_t, void *);
-BlockFwd c_block_fwd;
-BlockVjp c_block_vjp_ws;
-BlockVjpSize c_block_vjp_size;
-Rope c_rope;
-RopeAppend c_rope_append;
-KvRelease c_kv_release;
-KvPlan c_kv_plan;
+// The entry points as rmsnorm.h declares them.
+#define ENTRY(name) decltype(&rmsnorm_##name) c_##name
+ENTRY(block_fwd);
+ENTRY(block_vjp_ws);
+ENTRY(block_vjp_workspace_size);
+ENTRY(rope);
+ENTRY(rope_kv_append_ex);
+ENTRY(kv_release);
+ENTRY(kv_plan);
+#undef ENTRY
 
 void check_status(const char *name, int st) {
     if (st == 0) return;
@@ -352,7 +337,7 @@ PyObject *block_vjp(PyObject *, PyObject *const *argv, Py_ssize_t n) {
         if (gate)
             g_gate = given_or_empty("g_gate", a.optional(15, "g_gate"), at::kFloat, gate->sizes(), y.device());
         auto f32 = [](const std::optional<Tensor> &t) { return t ? static_cast<float *>(ptr(&*t)) : nullptr; };
-        const int64_t bytes = (int64_t)c_block_vjp_size(r.rows, r.D, code);
+        const int64_t bytes = (int64_t)c_block_vjp_workspace_size(r.rows, r.D, code);
         const Tensor ws = empty({bytes}, at::kByte);
         check_status("rmsnorm_block_vjp",
                      c_block_vjp_ws(ptr(&y), r.ld, ptr(&h), ld_h, ptr(w_post), ptr(&w_pre), ptr(gate), g.ld, g.G,
@@ -472,11 +457,11 @@ PyObject *rope_append(PyObject *, PyObject *const *argv, Py_ssize_t n) {
         const Strides sq = head_strides("q", q), sk = head_strides("k", k), sv = head_strides("v", v);
         const Strides sqo = head_strides("q_out", qo), skc = head_strides("k_cache", kc), svc = head_strides("v_cache", vc);
         check_status("rmsnorm_rope_kv_append_ex",
-                     c_rope_append(ptr(&q), sq.s + 1, ptr(&k), sk.s + 1, ptr(&v), sv.s + 1,
-                                   static_cast<const int64_t *>(ptr(&pos)), static_cast<const int64_t *>(ptr(&slots)),
-                                   ptr(&qo), sqo.s + 1, ptr(&kc), skc.s + 1, ptr(&vc), svc.s + 1,
-                                   static_cast<const double *>(inv.data_ptr()), (float)a.number(8),
-                                   a.truth(9) ? 1 : 0, T, Hq, Hkv, Dh, rot, kc.size(0), code, on.stream));
+                     c_rope_kv_append_ex(ptr(&q), sq.s + 1, ptr(&k), sk.s + 1, ptr(&v), sv.s + 1,
+                                         static_cast<const int64_t *>(ptr(&pos)), static_cast<const int64_t *>(ptr(&slots)),
+                                         ptr(&qo), sqo.s + 1, ptr(&kc), skc.s + 1, ptr(&vc), svc.s + 1,
+                                         static_cast<const double *>(inv.data_ptr()), (float)a.number(8),
+                                         a.truth(9) ? 1 : 0, T, Hq, Hkv, Dh, rot, kc.size(0), code, on.stream));
         wrote(&kc, &vc, a.optional(10, "q_out"));
         return wrap(qo);
     });
@@ -571,11 +556,11 @@ PyObject *kv_plan(PyObject *, PyObject *const *argv, Py_ssize_t n) {
 // bind(check, {name: address}): the library's entry points.
 PyObject *bind(PyObject *, PyObject *const *argv, Py_ssize_t n) {
     return guarded(n, 2, [&]() -> PyObject * {
+#define SLOT(name) {"rmsnorm_" #name, &c_##name}
         const struct { const char *name; void *slot; } table[] = {
-            {"rmsnorm_block_fwd", &c_block_fwd}, {"rmsnorm_block_vjp_ws", &c_block_vjp_ws},
-            {"rmsnorm_block_vjp_workspace_size", &c_block_vjp_size}, {"rmsnorm_rope", &c_rope},
-            {"rmsnorm_rope_kv_append_ex", &c_rope_append}, {"rmsnorm_kv_release", &c_kv_release},
-            {"rmsnorm_kv_plan", &c_kv_plan}};
+            SLOT(block_fwd), SLOT(block_vjp_ws), SLOT(block_vjp_workspace_size), SLOT(rope), SLOT(rope_kv_append_ex),
+            SLOT(kv_release), SLOT(kv_plan)};
+#undef SLOT
         for (const auto &e : table) {
             PyObject *v = PyDict_GetItemString(argv[1], e.name);  // borrowed
             if (!v) fail(PyExc_KeyError, "%s", e.name);

@@ -1,6 +1,9 @@
 """What building needs: the library only nvcc, the binding torch as well."""
 import os
+import re
+import shutil
 import stat
+import subprocess
 import sys
 
 import pytest
@@ -45,3 +48,28 @@ def test_both_are_built_with_torch(tree, monkeypatch):
     assert made == [b.binding_path()]
     b.build()
     assert len(made) == 1
+
+
+def test_binding_follows_the_header(tmp_path, monkeypatch):
+    """It is compiled against include/rmsnorm.h: another prototype of an entry point that
+    it calls does not compile, and a newer header makes it stale."""
+    if shutil.which("g++") is None or not os.path.exists(b._nvcc()):
+        pytest.skip("needs g++ and the CUDA headers")
+    text = open(os.path.join(b.INCLUDE, "rmsnorm.h")).read()
+    src = os.path.join(b.CSRC, "binding.cpp")
+
+    def compiles(header):
+        (tmp_path / "rmsnorm.h").write_text(header)
+        return subprocess.run(["g++", *b._binding_flags(), "-O0", "-fsyntax-only", "-I" + str(tmp_path), src],
+                              capture_output=True).returncode == 0
+    assert compiles(text)
+    changed = re.sub(r"int rmsnorm_kv_release\(", "int rmsnorm_kv_release(int64_t more, ", text)
+    assert changed != text and not compiles(changed)
+    built = tmp_path / "built.so"
+    built.write_text("")
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(b.INCLUDE, "rmsnorm.h")))
+    os.utime(built, (newest + 1, newest + 1))
+    assert not b._binding_stale(str(built))
+    monkeypatch.setattr(b, "INCLUDE", str(tmp_path))
+    os.utime(tmp_path / "rmsnorm.h", (newest + 2, newest + 2))
+    assert b._binding_stale(str(built))
