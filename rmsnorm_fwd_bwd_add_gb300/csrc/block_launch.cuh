@@ -3,6 +3,7 @@
 
 #include "block.cuh"
 #include "block_generic.cuh"
+#include "block_plan.h"
 #include "launch_util.h"
 
 namespace rmsn {
@@ -94,6 +95,7 @@ cudaError_t launch_block_generic(const BlockPlan &p, const BlockArgs &a, cudaStr
 
 template <bool VJP, typename T>
 cudaError_t launch_block(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
+    if (!block_plan_ok(p)) return cudaErrorInvalidConfiguration;
     if (p.kind == BLOCK_GENERIC)
         return p.ub == 16 ? launch_block_generic<VJP, T, 16>(p, a, s) : launch_block_generic<VJP, T, sizeof(T)>(p, a, s);
     if (p.shift) return launch_block_unit<VJP, T, 16, true>(p, a, s);

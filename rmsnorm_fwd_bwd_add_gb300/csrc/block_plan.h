@@ -147,4 +147,17 @@ inline BlockPlan make_block_plan(int64_t rows, int64_t D, int es, int unit, int 
     return p;
 }
 
+// Whether the kernels can run a plan: a ring with stages to copy into, and rows off
+// 16-byte boundaries on the tiers that take them.  A launch of any other would write
+// outside its shared memory, so the launchers ask.
+inline bool block_plan_ok(const BlockPlan &p) {
+    if (p.grid < 1) return false;
+    if (p.kind == BLOCK_GENERIC) return !p.shift && !p.cluster;
+    if (p.threads < 32 || p.threads > 1024 || p.threads % 32) return false;
+    if (p.kind == BLOCK_STAGED)
+        return p.stages >= 1 && p.stages <= BLOCK_MAX_STAGES && p.stage_bytes > 0 && !p.cluster && (!p.half || p.threads <= 640);
+    if (p.half || p.cluster < 0 || p.cluster > 8) return false;
+    return p.kind == BLOCK_DIRECT || (p.kind == BLOCK_WARP && !p.shift && p.threads <= 256);
+}
+
 }  // namespace rmsn

@@ -269,6 +269,48 @@ int main() {
 }
 """
 
+GUARD = r"""
+#include <cstdio>
+#include "block_plan.h"
+using namespace rmsn;
+int main() {
+    auto refuses = [](BlockPlan p, void (*spoil)(BlockPlan &)) {
+        if (!block_plan_ok(p)) return false;
+        spoil(p);
+        return !block_plan_ok(p);
+    };
+    const BlockPlan staged = make_block_plan(5000, 4096, 2, 16, 4, true, 1, 152, 1);
+    const BlockPlan half = make_block_plan(5000, 5120, 2, 16, 4, true, 1, 152, 1);
+    const BlockPlan shift = make_block_plan(5000, 4097, 2, 2, 4, true, 1, 152, 8);
+    const BlockPlan warp = make_block_plan(5000, 512, 2, 16, 4, true, 1, 152, 1);
+    const BlockPlan cluster = make_block_plan(8, 4096, 2, 16, 4, true, 1, 152, 1);
+    const BlockPlan generic = make_block_plan(5000, 20000, 2, 16, 4, true, 1, 152, 1);
+    if (staged.kind != BLOCK_STAGED || !half.half || !shift.shift || warp.kind != BLOCK_WARP || !cluster.cluster ||
+        generic.kind != BLOCK_GENERIC) return 1;
+    if (!refuses(staged, [](BlockPlan &p) { p.stages = 0; })) return 2;
+    if (!refuses(staged, [](BlockPlan &p) { p.stages = 9; })) return 3;
+    if (!refuses(staged, [](BlockPlan &p) { p.stage_bytes = 0; })) return 4;
+    if (!refuses(staged, [](BlockPlan &p) { p.threads = 1056; })) return 5;
+    if (!refuses(staged, [](BlockPlan &p) { p.grid = 0; })) return 6;
+    if (!refuses(half, [](BlockPlan &p) { p.threads = 672; })) return 7;
+    if (!refuses(shift, [](BlockPlan &p) { p.kind = BLOCK_WARP, p.threads = 32; })) return 8;
+    if (!refuses(shift, [](BlockPlan &p) { p.kind = BLOCK_GENERIC; })) return 9;
+    if (!refuses(warp, [](BlockPlan &p) { p.threads = 512; })) return 10;
+    if (!refuses(cluster, [](BlockPlan &p) { p.cluster = 9; })) return 11;
+    if (!refuses(generic, [](BlockPlan &p) { p.cluster = 2; })) return 12;
+    for (int64_t D = 1; D < 33000; D += D < 300 ? 1 : 13)  // and every plan that is made passes
+        for (int64_t rows : {1, 8, 64, 153, 400, 5000})
+            for (int vjp = 0; vjp < 2; ++vjp)
+                for (int how = 0; how < 8; ++how)
+                    if (!block_plan_ok(make_block_plan(rows, D, how % 2 ? 4 : 2, how / 2 % 2 ? 16 : 4, vjp ? 5 : 2, vjp, 1, 152,
+                                                       how / 4 ? 8 : 0))) {
+                        printf("rows %ld D %ld vjp %d how %d", (long)rows, (long)D, vjp, how);
+                        return 13;
+                    }
+    return 0;
+}
+"""
+
 
 def _run(tmp_path, name, text):
     src, exe = tmp_path / (name + ".cu"), tmp_path / name
@@ -294,3 +336,7 @@ def test_plans_leave_room_for_the_kernels_static_sums(tmp_path):
     """What a launch asks for and what its kernel holds anyway fit a CTA's shared
     memory together, at every row length that has a plan on chip."""
     _run(tmp_path, "limits", LIMITS)
+
+
+def test_plans_that_no_kernel_can_run_are_refused(tmp_path):
+    _run(tmp_path, "guard", GUARD)
