@@ -34,6 +34,7 @@
 #include "checks.h"
 #include "common.cuh"
 #include "launch_util.h"
+#include "rope_plan.h"
 #include "units.cuh"
 
 namespace rmsn {
@@ -307,38 +308,12 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
 
 template <typename T, int VB, bool INTERLEAVED>
 cudaError_t launch_layout(const RopeExArgs &a, int sm, cudaStream_t s) {
-    // Warps a token (k) and units a step (c).  Each warp computes its units' angles,
-    // about half a trip to memory, and makes a trip for every few heads.  All warps go
-    // through equal rounds of whole tokens; what is left, less than a round, is split
-    // into as many parts as there are warps for (5001 tokens on 2432 warps: 19.7 us with
-    // a third round of 137 whole tokens, 17.4 with them in 16 parts each).
-    const int64_t resident = (int64_t)sm * RX_CTAS_PER_SM, warps = resident * (RX_NT / 32);
     constexpr int VE = VB / (int)sizeof(T);
     const int lanes = HeadMap<VE, (INTERLEAVED && VE > 1), INTERLEAVED>(a.Dh, a.rot).lanes;
-    const int heads = a.Hq + a.Hkv * (a.slots ? 2 : 1);
-    const int64_t whole = a.T / warps * warps, rest = a.T - whole;
-    int wpt = 1, cw = 1;
-    int64_t best = INT64_MAX;
-    for (int steps = (lanes + 31) / 32; steps <= 12; ++steps) {
-        const int c = (lanes + steps - 1) / steps;  // a head in `steps` equal steps
-        auto cost_of = [&](int64_t rounds, int k) {
-            const int per_trip = (32 / c) * heads_in_flight<VB>() * k, trips = (heads + per_trip - 1) / per_trip;
-            return rounds * (1 + (1 + 2 * trips) * steps);
-        };
-        for (int k = 1; k <= 16; k *= 2) {
-            const int64_t cost = cost_of(whole / warps, 1) + cost_of((rest * k + warps - 1) / warps, k);
-            if (cost < best) {
-                best = cost;
-                wpt = k;
-                cw = c;
-            }
-        }
-        if (c == 1) break;
-    }
-    const int64_t items = whole + rest * wpt;
-    const int grid = (int)std::min<int64_t>((items + RX_NT / 32 - 1) / (RX_NT / 32), resident);
+    const RopePlan p = make_rope_plan(a.T, lanes, a.Hq + a.Hkv * (a.slots ? 2 : 1), heads_in_flight<VB>(),
+                                      sm * RX_CTAS_PER_SM, RX_NT / 32);
     return launch_pdl(a.slots ? rope_ex_kernel<T, VB, INTERLEAVED, true> : rope_ex_kernel<T, VB, INTERLEAVED, false>,
-                      dim3(grid), dim3(RX_NT), 0, s, a, whole, wpt, cw);
+                      dim3(p.grid), dim3(RX_NT), 0, s, a, p.whole, p.wpt, p.cw);
 }
 
 // unit: bytes that divide every address, stride and length.

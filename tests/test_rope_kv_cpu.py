@@ -4,6 +4,7 @@ import ctypes
 import math
 import os
 import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -167,3 +168,40 @@ def test_python_refuses_cpu_tensors():
     lens = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
         rn.rmsnorm_kv_plan(lens, lens, torch.zeros(2, 2, dtype=torch.int32), 16, 4)
+
+
+PLAN = r"""
+#include <cstdio>
+#include "rope_plan.h"
+using namespace rmsn;
+// Every head length has a plan of its own choosing: a power of two of warps a token, and
+// at most 12 steps a head, or as few as a warp's 32 lanes allow.
+int main() {
+    for (int lanes = 1; lanes <= 520; ++lanes)
+        for (long T : {1, 7, 300, 2432, 2433, 4096, 5001, 100000})
+            for (int heads : {1, 3, 40, 130})
+                for (int in_flight : {4, 8}) {
+                    const RopePlan p = make_rope_plan(T, lanes, heads, in_flight, 304, 8);
+                    const int least = (lanes + 31) / 32, steps = p.cw > 0 ? (lanes + p.cw - 1) / p.cw : 0;
+                    const long rest = T - p.whole;
+                    if (p.cw < 1 || p.cw > 32 || steps > (least > 12 ? least : 12) || p.wpt < 1 || p.wpt > 16 ||
+                        (p.wpt & (p.wpt - 1)) || p.whole < 0 || rest < 0 || rest >= 2432 || p.grid < 1 || p.grid > 304) {
+                        printf("lanes %d T %ld heads %d in flight %d: %d units a step, %d warps a token, grid %d", lanes, T,
+                               heads, in_flight, p.cw, p.wpt, p.grid);
+                        return 1;
+                    }
+                }
+    return 0;
+}
+"""
+
+
+def test_every_head_length_has_a_plan(tmp_path):
+    src, exe = tmp_path / "plan.cu", tmp_path / "plan"
+    src.write_text(PLAN)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    subprocess.run([nvcc, "-std=c++17", "-O2", "-I" + os.path.join(root, "rmsnorm_fwd_bwd_add_gb300", "csrc"), "-o",
+                    str(exe), str(src)], check=True, capture_output=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
