@@ -273,7 +273,7 @@ int rmsnorm_block_fwd(const void *y, int64_t ld_y, const void *residual, int64_t
  *   g_gate       [gate_rows, D] fp32, dense; NULL exactly when gate is.
  * gw_post, gw_pre and g_gate are overwritten (rows == 0: zeros) and bit-identical
  * from run to run, as gw of rmsnorm_vjp; their scratch (three fp32 rows a CTA and
- * 32 more) comes from the library's pool.  g_y and g_h may each be one of the row
+ * up to 32 more) comes from the library's pool.  g_y and g_h may each be one of the row
  * inputs.  With w_post, the products of m = scale * gate * (weight_bias + w_post),
  * y and h or g_out are summed in fp32 before the scales are applied, and have to stay
  * in its normal range; the scales have to, their squares need not.

@@ -160,11 +160,6 @@ extern "C" int rmsnorm_block_fwd(const void *y, int64_t ld_y, const void *residu
 
 namespace {
 
-// Three fp32 rows a CTA, and the second stage's slices.
-size_t scratch_bytes(int grid, int64_t D) {
-    return (((size_t)grid * 3 + BLOCK_MAX_SLICES) * (size_t)D * 4 + 255) & ~(size_t)255;
-}
-
 // The VJP with its scratch in `workspace`, or, with `pooled`, from the library's pool.
 int block_vjp(const void *y, int64_t ld_y, const void *h, int64_t ld_h, const void *w_post,
               const void *w_pre, const void *gate, int64_t ld_gate, int64_t gate_rows, float scale,
@@ -262,7 +257,7 @@ int block_vjp(const void *y, int64_t ld_y, const void *h, int64_t ld_h, const vo
     a.split_q = p.team ? p.grid / gates : rows / p.grid;
     a.split_r = p.team ? p.grid % gates : rows % p.grid;
     set_runs(&a, p, a.rows_per_team, p.grid / gates);
-    const size_t need = scratch_bytes(p.cluster ? 1 : p.grid, D);
+    const size_t need = block_scratch_bytes(p.cluster ? 1 : p.grid, rows, D);
     void *ws = workspace;
     if (pooled && p.cluster) {
         ws = nullptr;  // nothing leaves the cluster
@@ -316,9 +311,5 @@ extern "C" size_t rmsnorm_block_vjp_workspace_size(int64_t rows, int64_t D, int 
     int sm = 0;
     if (check_common(rows, D, dtype, 0.f, 0.f) != RMSNORM_OK || rows == 0 || current_sm_count(&sm) != RMSNORM_OK)
         return 0;
-    // rows on 16-byte boundaries, or off them and alike, with a gate that keeps them out
-    // of one cluster: no other plan has more CTAs
-    const int es = esize_of(dtype);
-    return scratch_bytes(std::max(make_block_plan(rows, D, es, 16, 3, true, 2, sm, 0).grid,
-                                  make_block_plan(rows, D, es, es, 3, true, 2, sm, 1).grid), D);
+    return block_workspace_bytes(rows, D, esize_of(dtype), sm);
 }

@@ -34,7 +34,7 @@ struct BlockArgs {
     float *gw_post, *gw_pre;       // VJP: [D]
     float *part_pre;               // VJP: [grid, D] sums of g h r_h
     float *part_mid;               // VJP: [2 * grid, D] sums A of gate rows split over CTAs
-    float *part_post;              // VJP: [BLOCK_MAX_SLICES, D] sums of gw_post over runs of gate rows
+    float *part_post;              // VJP: [block_slices, D] sums of gw_post over runs of gate rows
     unsigned int *status;
     long long wait_budget;
     int64_t drop_row;              // test hook: this row's copy is never issued
@@ -124,9 +124,12 @@ __host__ __device__ inline int64_t mid_slot(int64_t c, bool first) { return 2 * 
 // The second stage splits many gate rows into so many runs, a CTA each per 32
 // columns: 5461 gate rows of 3 rows on 32 warps took 170 us of dependent trips to
 // memory (D = 1000).
+// Fewer of rows so long that the slices' sums would take more than 64 MB: their columns
+// alone are thousands of CTAs.
 constexpr int BLOCK_MAX_SLICES = 32;
-inline int block_slices(int64_t gate_rows) {
-    return gate_rows < 128 ? 1 : gate_rows >= 64 * BLOCK_MAX_SLICES ? BLOCK_MAX_SLICES : (int)(gate_rows / 64);
+inline int block_slices(int64_t gate_rows, int64_t D) {
+    const int64_t most = ((int64_t)64 << 20) / (4 * D), n = gate_rows / 64 < most ? gate_rows / 64 : most;
+    return gate_rows < 128 || n < 2 ? 1 : n < BLOCK_MAX_SLICES ? (int)n : BLOCK_MAX_SLICES;
 }
 
 // The ring of BLOCK_STAGED: its most stages, and the bytes of their mbarriers ahead

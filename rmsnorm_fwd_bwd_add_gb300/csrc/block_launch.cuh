@@ -117,7 +117,7 @@ cudaError_t launch_block_vjp_both(const BlockPlan &p, const BlockArgs &a, cudaSt
     cudaError_t e = launch_block<true, T>(p, a, s);
     if (e != cudaSuccess || p.cluster) return e;
     const int64_t G = a.rows / a.rows_per_gate;
-    const int slices = block_slices(a.team || a.rows_per_gate == 1 ? 1 : G);
+    const int slices = block_slices(a.team || a.rows_per_gate == 1 ? 1 : G, a.D);
     // Few parts: 8 warps have them all in flight at once, and an SM holds the CTAs of
     // several blocks of columns (100 rows of D = 5248: 10.2 us; with 32 warps two
     // rounds of CTAs, 13).

@@ -60,8 +60,9 @@ inline BlockPlan make_block_plan(int64_t rows, int64_t D, int es, int unit, int 
         BlockPlan g{};
         g.kind = BLOCK_GENERIC;
         g.ub = p.ub;
-        // as many CTAs as fit at once; the VJP keeps three fp32 rows of scratch each: fewer
-        // where they would take more than 256 MB
+        // as many CTAs as fit at once; the VJP keeps three fp32 rows of scratch each: fewer,
+        // but eight, where they would take more than 256 MB (a CTA has a row at least, so it
+        // is never more than the 12 bytes an element of the 16-bit row tensors)
         const int64_t fit = vjp ? std::max<int64_t>(8, ((int64_t)256 << 20) / (12 * D)) : 3 * sm;
         g.grid = (int)std::min<int64_t>(rows, std::min<int64_t>((vjp ? 2 : 3) * (int64_t)sm, fit));
         return g;
@@ -145,6 +146,21 @@ inline BlockPlan make_block_plan(int64_t rows, int64_t D, int es, int unit, int 
            ((int64_t)p.grid << (p.chunk_shift + 1)) * 8 <= rows)
         ++p.chunk_shift;
     return p;
+}
+
+// The VJP's scratch: three fp32 rows a CTA, and one for each slice that the second
+// stage may have, gates of two rows each being the most.
+inline size_t block_scratch_bytes(int grid, int64_t rows, int64_t D) {
+    const int slices = block_slices(rows / 2, D);
+    return (((size_t)grid * 3 + (slices > 1 ? slices : 0)) * (size_t)D * 4 + 255) & ~(size_t)255;
+}
+
+// The most of it that any call of these sizes takes: rows on 16-byte boundaries, or off
+// them and alike, with a gate that keeps them out of one cluster (no other plan has more
+// CTAs).
+inline size_t block_workspace_bytes(int64_t rows, int64_t D, int es, int sm) {
+    return block_scratch_bytes(std::max(make_block_plan(rows, D, es, 16, 3, true, 2, sm, 0).grid,
+                                        make_block_plan(rows, D, es, es, 3, true, 2, sm, 1).grid), rows, D);
 }
 
 // Whether the kernels can run a plan: a ring with stages to copy into, and rows off

@@ -311,6 +311,42 @@ int main() {
 }
 """
 
+SCRATCH = r"""
+#include <cstdio>
+#include "block_plan.h"
+using namespace rmsn;
+// What the size asked beforehand allows: 320 MB of long rows, or the 12 bytes an element
+// of eight CTAs, or of the rows, and never less than a call takes.
+int main() {
+    for (int64_t D = 1; D <= (int64_t)1 << 24; D += D < 100 ? 1 : D / 37 + 1)
+        for (int64_t rows : {1, 2, 9, 127, 128, 256, 300, 1000, 4096, 8192, 100000})
+            for (int es : {2, 4})
+                for (int sm : {2, 152}) {
+                    const size_t asked = block_workspace_bytes(rows, D, es, sm);
+                    const size_t cap = 12 * (size_t)D * (rows < 8 ? rows : 8) + 256;
+                    if (D > 32768 && asked > cap + ((size_t)64 << 20) && asked > ((size_t)320 << 20) + 256) {
+                        printf("rows %ld D %ld: %zu bytes", (long)rows, (long)D, asked);
+                        return 1;
+                    }
+                    if (asked > 12 * (size_t)D * rows + 4 * (size_t)D * (rows / 128) + 256) return 2;
+                    for (int64_t gates : {(int64_t)1, rows / 3, rows / 2})
+                        for (int unit : {16, es})
+                            for (int classes : {0, 1, 2, 4, 8}) {
+                                if (gates < 1 || rows % gates) continue;
+                                const BlockPlan p = make_block_plan(rows, D, es, unit, 3, true, gates, sm, classes);
+                                const size_t need = block_scratch_bytes(p.cluster ? 1 : p.grid, rows, D);
+                                const int slices = block_slices(p.team ? 1 : gates, D);
+                                if (need > asked || need < ((size_t)(p.cluster ? 0 : p.grid) * 3 + (slices > 1 ? slices : 0)) * D * 4) {
+                                    printf("rows %ld D %ld gates %ld unit %d classes %d: %zu of %zu bytes", (long)rows, (long)D,
+                                           (long)gates, unit, classes, need, asked);
+                                    return 3;
+                                }
+                            }
+                }
+    return 0;
+}
+"""
+
 
 def _run(tmp_path, name, text):
     src, exe = tmp_path / (name + ".cu"), tmp_path / name
@@ -340,3 +376,7 @@ def test_plans_leave_room_for_the_kernels_static_sums(tmp_path):
 
 def test_plans_that_no_kernel_can_run_are_refused(tmp_path):
     _run(tmp_path, "guard", GUARD)
+
+
+def test_scratch_of_long_rows_is_bounded(tmp_path):
+    _run(tmp_path, "scratch", SCRATCH)

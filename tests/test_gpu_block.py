@@ -640,3 +640,23 @@ def test_gradients_of_no_rows_through_a_sum():
     turned, _ = rn.rope(q, None, torch.zeros(0, dtype=torch.int64, device=DEV), inv)
     turned.sum().backward()
     assert q.grad.shape == q.shape
+
+
+@pytest.mark.parametrize("rows,D,G", [(256, 515, 128), (600, 512, 300), (4096, 96, 2048), (255, 520, 51)])
+def test_block_vjp_workspace_holds_the_slices_of_many_gate_rows(rows, D, G):
+    """A workspace of just the size asked, with what follows it untouched."""
+    lib = rn._native.lib()
+    p = _problem(rows, D, torch.float16, G, True, 0.0, seed=121)
+    want = rn.rmsnorm_block_vjp(p["y"], p["h"], p["w_post"], p["w_pre"], p["g"], EPS, 0.0, p["gate"], 0.5, p["g_res"])
+    n = lib.rmsnorm_block_vjp_workspace_size(rows, D, 0)
+    ws = torch.full((n + 4096,), 255, dtype=torch.uint8, device=DEV)
+    at = ws.data_ptr() + (-ws.data_ptr()) % 256
+    out = [torch.full_like(t, 5.0) for t in want]
+    st = lib.rmsnorm_block_vjp_ws(
+        p["y"].data_ptr(), D, p["h"].data_ptr(), D, p["w_post"].data_ptr(), p["w_pre"].data_ptr(), p["gate"].data_ptr(), D, G,
+        0.5, p["g"].data_ptr(), D, p["g_res"].data_ptr(), D, None, EPS, 0.0, out[0].data_ptr(), D, out[1].data_ptr(), D,
+        out[2].data_ptr(), out[3].data_ptr(), out[4].data_ptr(), rows, D, 0, at, n, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)
+    assert (ws[at - ws.data_ptr() + n:] == 255).all()
