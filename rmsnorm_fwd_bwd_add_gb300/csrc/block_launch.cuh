@@ -25,11 +25,13 @@ cudaError_t launch_block_inst(const BlockPlan &p, const BlockArgs &a, cudaStream
     return launch_pdl(kern, dim3(p.grid), dim3(p.threads), p.smem, s, a);
 }
 
-// The VJP's instances of one FORM.  Tests of what is there at run time cost a sixth of the
-// instructions, and spills (16384 rows of bf16, D = 4096: without g_res 135 -> 117 us, without
-// saved scales 151 -> 133, without post-norm 146 -> 132; D = 512 33.2 -> 28.1; 4095 x 2048
-// fp32 with a gate row each 43.3 -> 41.1).  Gates of a row each and rows off boundaries
-// have them for the usual training backward.
+// The VJP's instances of one FORM, of rows of up to 512 threads.  Tests of what is there at
+// run time cost a sixth of the instructions, and spills (16384 rows of bf16, D = 4096: without
+// g_res 135 -> 117 us, without saved scales 151 -> 133, without post-norm 146 -> 132; D = 512
+// 33.2 -> 28.1).  With a gate row per row they are compiled for saved scales, which a
+// training backward has (fp32, 4095 x 2048, without g_res: 43.3 -> 41.1; bf16 without
+// post-norm: 8192 x 4096 116.6 -> 107.7, 16384 x 512 40.1 -> 31.4), off 16-byte boundaries
+// for all operands together; every other combination takes the instance that asks.
 template <typename T, bool GROW, bool SHIFT, int FORM>
 cudaError_t launch_block_form(const BlockPlan &p, const BlockArgs &a, cudaStream_t s) {
     if constexpr (!SHIFT)
@@ -47,7 +49,12 @@ cudaError_t launch_block_kind(const BlockPlan &p, const BlockArgs &a, cudaStream
             const int form = (a.w_post ? FORM_POST : 0) | (a.g_res ? FORM_MORE : 0) | (a.rstd ? FORM_SAVED : 0);
             if (form == ALL) return launch_block_form<T, GROW, SHIFT, ALL>(p, a, s);
             if constexpr (GROW) {
-                if (form == (FORM_POST | FORM_SAVED)) return launch_block_form<T, GROW, SHIFT, FORM_POST | FORM_SAVED>(p, a, s);
+                switch (form) {
+                    case FORM_POST | FORM_SAVED: return launch_block_form<T, GROW, SHIFT, FORM_POST | FORM_SAVED>(p, a, s);
+                    case FORM_MORE | FORM_SAVED: return launch_block_form<T, GROW, SHIFT, FORM_MORE | FORM_SAVED>(p, a, s);
+                    case FORM_SAVED: return launch_block_form<T, GROW, SHIFT, FORM_SAVED>(p, a, s);
+                    default: break;
+                }
             } else if constexpr (!SHIFT) {
                 switch (form) {
                     case FORM_POST | FORM_SAVED: return launch_block_form<T, GROW, SHIFT, FORM_POST | FORM_SAVED>(p, a, s);

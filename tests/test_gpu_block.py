@@ -660,3 +660,14 @@ def test_block_vjp_workspace_holds_the_slices_of_many_gate_rows(rows, D, G):
     for a, b in zip(out, want):
         assert torch.equal(a, b)
     assert (ws[at - ws.data_ptr() + n:] == 255).all()
+
+
+@pytest.mark.parametrize("rows,D", [(3000, 512), (1400, 1024), (700, 4096), (400, 5120), (330, 8192)])
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_block_vjp_forms_with_a_gate_row_per_row(rows, D, dt):
+    """Every combination of operands, on each tier that is compiled for some of them."""
+    for post in (True, False):
+        p = _problem(rows, D, DT[dt], rows, post, 0.0, seed=131)
+        for g_res in (True, False):
+            for saved in (True, False):
+                _check_vjp(p, 0.9, g_res=g_res, saved=saved)
