@@ -67,12 +67,18 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _increment_version = getattr(torch._C, "_increment_version", None) or torch.autograd.graph.increment_version
 
 
-def _wrote(*tensors: Optional[torch.Tensor]) -> None:
+def _wrote(a: Optional[torch.Tensor], b: Optional[torch.Tensor] = None,
+           c: Optional[torch.Tensor] = None) -> None:
     """Tells autograd that a call wrote into the caller's tensors (None: not the
     caller's), so that it refuses a backward pass through what they held."""
-    given = [t for t in tensors if t is not None]
-    if given:
-        _increment_version(given)
+    if c is None:
+        if b is None:
+            if a is not None:
+                _increment_version((a,))
+        else:
+            _increment_version((b,) if a is None else (a, b))
+    else:
+        _increment_version([t for t in (a, b, c) if t is not None])
 
 
 def _stream(device: torch.device, stream) -> int:
