@@ -38,11 +38,13 @@
 // for 5000 x 4097.)  Only tensors that stand differently, and rows of a warp, are
 // read in units of 4 or 2 bytes.
 //
-// On the GB300 (6.7 TB/s copied): forward of 16384 x 8192 bf16 with 8 gate rows 166 us
-// (96 % of that), 5000 x 4097 fp16 29 us (84 %); VJP of 16384 x 4096 bf16 133 us (90 %:
-// 123 registers a thread leave an SM 16 warps, and the last 5 us are the second stage),
-// 4095 x 2048 fp32 with a gate row each 41 us (85 %), 16384 x 512 28 us (54 %: no ring,
-// and 16 warps an SM do not hide a row's trip to memory).
+// On the GB300 (6.7 TB/s copied), inputs changing from call to call: forward of 16384 x
+// 8192 bf16 with 8 gate rows 166 us (96 % of that), 5000 x 4097 fp16 31.5 us (78 %); VJP of
+// 16384 x 4096 bf16 135 us (89 %: 123 registers a thread leave an SM 16 warps, and the last
+// 5 us are the second stage), 4095 x 2048 fp32 with a gate row each 42.6 us (82 %), 16384 x
+// 512 31 us (48 %: no ring, and 16 warps an SM do not hide a row's trip to memory), 8192 x
+// 16384 517 us (46 %: rows of 513 threads or more leave the ring one or two stages and a
+// thread 64 registers, which spill).
 #pragma once
 
 #include <cfloat>

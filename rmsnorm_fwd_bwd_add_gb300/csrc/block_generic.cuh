@@ -5,8 +5,8 @@
 // boundaries) per thread and step; a row is read from global memory or L2 once per
 // pass (forward: sum of y^2, sum of h^2, outputs), and the VJP's sums are kept in
 // its scratch.  It takes the rows the tiers that hold a row on chip cannot: 2000 of D =
-// 20000 (bf16) forward in 76 us, 63 % of the copy bandwidth (198 an element at a
-// time), VJP in 250 us, 29 % (465): its sums are read and written for every row.
+// 20000 (bf16) forward in 75 us, 64 % of the copy bandwidth (198 an element at a
+// time), VJP in 253 us, 28 % (465): its sums are read and written for every row.
 #pragma once
 
 #include "block.h"

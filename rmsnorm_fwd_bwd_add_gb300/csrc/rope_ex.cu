@@ -13,11 +13,14 @@
 // vectors half a rotation apart -- of 32 / units heads at a time and computes
 // the cosines and sines of its pairs once for all of the token's heads.
 //
-// On the GB300: 16384 tokens of 32 + 8 heads of 128 (bf16, views of one projection) 54 us,
-// 92 % of the copy bandwidth; 5001 of 16 + 4 (fp32, interleaved, half rotated,
-// inverse) 17.4 us, 88 %; the append of 4096 tokens of 32 + 8 heads of 80 11.5 us, 81 %,
-// of 8 tokens 3.0 us.  The loops carry only loads, rotations and stores: every head's
-// address is one 32 x 32 + 64 multiply-add (64-bit strides cost a tenth of the time).
+// On the GB300, inputs changing from call to call: 16384 tokens of 32 + 8 heads of 128
+// (bf16, views of one projection) 54.6 us, 92 % of the copy bandwidth; 5001 of 16 + 4 (fp32,
+// interleaved, half rotated, inverse) 20.8 us, 73 %; the append of 4096 tokens of 32 + 8
+// heads of 80 15.2 us, 62 % (on one set of buffers, which the L2 holds, 17.4 and 11.7);
+// the append of 8 tokens 2.9 us of GPU time; 4096 tokens of 32 + 8 heads 17.7 us with heads of
+// 128, 34.5 with heads of 126 (units of 4 bytes), 54.4 with heads of 125 (of 2).  The
+// loops carry only loads, rotations and stores: every head's address is one 32 x 32 + 64
+// multiply-add (64-bit strides cost a tenth of the time).
 //
 // Angles are kept in turns (radians / 2 pi): the host splits inv_freq / 2 pi, in
 // double, into a hi + lo pair of floats, the product with p is formed as a
