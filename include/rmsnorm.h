@@ -388,8 +388,8 @@ int rmsnorm_rope(const void *q, const int64_t *q_strides, const void *k, const i
  * [num_slots, Hkv, Dh] with slot and head strides, part of the head rotated.
  * Token t's rotated k and its v go to row slots[t] (negative: not written; the
  * slots of one call are distinct, else that row holds parts of either token).
- * Negative positions and slots >= num_slots are skipped and set
- * RMSNORM_DEVSTATUS_BAD_INDEX, as there.
+ * Negative positions (the whole token) and slots >= num_slots (its cache rows; q is
+ * rotated all the same) are skipped and set RMSNORM_DEVSTATUS_BAD_INDEX.
  */
 int rmsnorm_rope_kv_append_ex(const void *q, const int64_t *q_strides, const void *k,
                               const int64_t *k_strides, const void *v, const int64_t *v_strides,

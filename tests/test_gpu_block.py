@@ -671,3 +671,15 @@ def test_block_vjp_forms_with_a_gate_row_per_row(rows, D, dt):
         for g_res in (True, False):
             for saved in (True, False):
                 _check_vjp(p, 0.9, g_res=g_res, saved=saved)
+
+
+@pytest.mark.parametrize("rows,D,groups,dt", [(8, 16384, 8, "bf16"), (8, 16384, 4, "f16"), (8, 16384, 1, "bf16"), (8, 8192, 2, "f32"),
+                                              (5, 16383, 5, "bf16"), (153, 16384, 0, "bf16"), (153, 8192, 153, "f32"),
+                                              (2560, 4097, 40, "bf16"), (2432, 4097, 38, "bf16"), (640, 8191, 20, "bf16")])
+def test_block_vjp_at_the_ends_of_its_tiers(rows, D, groups, dt):
+    """The widest rows in a cluster and just past the SMs' count, and the most gate rows off
+    16-byte boundaries that keep 16-byte units, with one more."""
+    for post in (True, False):
+        p = _problem(rows, D, DT[dt], groups, post, 0.0, seed=141)
+        for g_res in (True, False):
+            _check_vjp(p, 0.9, g_res=g_res, saved=not g_res)
