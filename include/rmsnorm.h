@@ -304,6 +304,28 @@ int rmsnorm_block_vjp_ws(const void *y, int64_t ld_y, const void *h, int64_t ld_
 size_t rmsnorm_block_vjp_workspace_size(int64_t rows, int64_t D, int dtype);
 
 /*
+ * The fused residual-add forward with its output in 8 bits (e4m3: a sign, four bits of
+ * exponent, three of fraction, largest value 448) and fp32 scales, as the 8-bit matrix
+ * product behind the norm reads it.  Per row, with h and w' as above and for each group
+ * of `group` columns (the last one may be shorter; group = 0: the whole row):
+ *     a = max(max |h_j * w'_j|, 448 * 2^-126),  scale = r * a / 448
+ *     out_j = e4m3(h_j * w'_j * (448 / a))       (nearest, ties to even)
+ * so that out_j * scale stands for h_j * r * w'_j, its largest value 448.
+ *   x, residual, w, eps, weight_bias, new_residual  as for rmsnorm_fwd, fp16, bf16 or
+ *                fp32; new_residual may be x or residual.
+ *   out          [rows, D] e4m3 bytes, row stride ld_out.
+ *   scale        [rows, ceil(D / group)] fp32 contiguous, [rows] for group = 0.
+ *   group        0, 32, 64 or 128.
+ * Row strides in elements (>= D; ignored when rows == 1).  A group that holds a NaN or an
+ * infinity has a scale that is NaN or infinite, and each of its out_j * scale is NaN.
+ * out and scale may not overlap anything else.  Errors as for rmsnorm_fwd.
+ */
+int rmsnorm_fwd_q8(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual,
+                   const void *w, float eps, float weight_bias, void *out, int64_t ld_out,
+                   float *scale, int64_t group, void *new_residual, int64_t ld_new_residual,
+                   int64_t rows, int64_t D, int dtype, void *stream);
+
+/*
  * Gated activation of the decode loop.  Source: "Fused residual-add RMSNorm
  * and fused RoPE + KV-append decode kernels", Background, third bullet (a
  * fused silu(x[:d]) * x[d:2d] gate with 16-byte vectorised loads).
@@ -382,6 +404,25 @@ int rmsnorm_rope(const void *q, const int64_t *q_strides, const void *k, const i
                  int interleaved, int inverse, int64_t B, int64_t S, int64_t Hq, int64_t Hkv,
                  int64_t Dh, int64_t rot_dim, int dtype, void *stream);
 
+/* Most axes of a position. */
+#define RMSNORM_ROPE_MAX_AXES 4
+
+/*
+ * rmsnorm_rope with positions of several axes, as tokens of images and video have them
+ * (time, height, width): pair i turns by t = positions[pair_axis[i]][token] * inv_freq[i].
+ *   positions    [axes, B * S] int64, device memory; 1 <= axes <= RMSNORM_ROPE_MAX_AXES.
+ *   pair_axis    [rot_dim / 2] int32, HOST memory, read during the call: each pair's axis,
+ *                below `axes`; or NULL with one axis.
+ * The rest as for rmsnorm_rope; inverse = 1 is the VJP.  A token with a negative position on
+ * any axis is skipped and sets RMSNORM_DEVSTATUS_BAD_INDEX.
+ */
+int rmsnorm_rope_axes(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                      const int64_t *positions, int axes, const int32_t *pair_axis, void *q_out,
+                      const int64_t *q_out_strides, void *k_out, const int64_t *k_out_strides,
+                      const double *inv_freq, float attn_scale, int interleaved, int inverse, int64_t B,
+                      int64_t S, int64_t Hq, int64_t Hkv, int64_t Dh, int64_t rot_dim, int dtype,
+                      void *stream);
+
 /*
  * rmsnorm_rope_kv_append with the layouts and frequencies of rmsnorm_rope: q, k
  * and v [T, H, Dh] with host arrays of their token and head strides, caches
@@ -400,6 +441,57 @@ int rmsnorm_rope_kv_append_ex(const void *q, const int64_t *q_strides, const voi
                               float attn_scale, int interleaved, int64_t T, int64_t Hq, int64_t Hkv,
                               int64_t Dh, int64_t rot_dim, int64_t num_slots, int dtype,
                               void *stream);
+
+/* What a cache holds. */
+typedef enum {
+    RMSNORM_CACHE_SAME = 0, /* values of the inputs' dtype, no scales */
+    RMSNORM_CACHE_E4M3 = 1, /* e4m3 bytes (largest value 448) */
+    RMSNORM_CACHE_I8 = 2    /* int8, -127 to 127 */
+} rmsnorm_cache_t;
+
+/*
+ * rmsnorm_rope_kv_append_ex into a cache of 8 bits, quantised as it is written, with
+ * positions of one axis or several.  Each head of the rotated k (unrounded) and of v has a
+ * scale of its own; with x the head's values and top = 448 (e4m3) or 127 (int8):
+ *     a = max(max |x_j|, top * 2^-126),  scale = a / top,  code_j = round(x_j * (top / a))
+ * to the nearest code, ties to even.
+ *   q, k, v, positions, slots, q_out, inv_freq, attn_scale, interleaved  as for
+ *                rmsnorm_rope_kv_append_ex; axes, pair_axis and positions [axes, T] as for
+ *                rmsnorm_rope_axes.
+ *   k_cache, v_cache  [num_slots, Hkv, Dh] of cache_format, slot and head strides in elements.
+ *   k_scale, v_scale  [num_slots, Hkv] fp32, slot and head strides in elements; NULL for
+ *                RMSNORM_CACHE_SAME, whose values are rounded to dtype instead.
+ * A head that holds a NaN or an infinity has a scale that is NaN or infinite, and each of
+ * its code_j * scale is NaN.  Caches and scales may not overlap each other, the inputs or
+ * q_out; skipped tokens and errors as for rmsnorm_rope_kv_append_ex.
+ */
+int rmsnorm_kv_append(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                      const void *v, const int64_t *v_strides, const int64_t *positions, int axes,
+                      const int32_t *pair_axis, const int64_t *slots, void *q_out,
+                      const int64_t *q_out_strides, void *k_cache, const int64_t *k_cache_strides,
+                      void *v_cache, const int64_t *v_cache_strides, float *k_scale,
+                      const int64_t *k_scale_strides, float *v_scale, const int64_t *v_scale_strides,
+                      const double *inv_freq, float attn_scale, int interleaved, int64_t T, int64_t Hq,
+                      int64_t Hkv, int64_t Dh, int64_t rot_dim, int64_t num_slots, int cache_format,
+                      int dtype, void *stream);
+
+/*
+ * Reads tokens back from an 8-bit cache: token t's k and v are code * scale of row slots[t],
+ * each rounded once to dtype; zeros where slots[t] is negative (the padding of a captured
+ * step).  A slot >= num_slots gives zeros too and sets RMSNORM_DEVSTATUS_BAD_INDEX.  A slot may
+ * be named any number of times.
+ *   caches, scales, cache_format  as rmsnorm_kv_append writes them (RMSNORM_CACHE_E4M3 or _I8).
+ *   slots        [T] int64, device memory; rmsnorm_kv_plan gives those of whole contexts for
+ *                lens = 0 and new_lens = the contexts' lengths, without a pool.
+ *   k_out, v_out [T, Hkv, Dh] dtype, token and head strides in elements.
+ * Dh at most 1024.  The outputs may not overlap each other or anything that is read.  T == 0 is a
+ * no-op.  Errors as for rmsnorm_rope_kv_append_ex.
+ */
+int rmsnorm_kv_read(const void *k_cache, const int64_t *k_cache_strides, const void *v_cache,
+                    const int64_t *v_cache_strides, const float *k_scale, const int64_t *k_scale_strides,
+                    const float *v_scale, const int64_t *v_scale_strides, const int64_t *slots, void *k_out,
+                    const int64_t *k_out_strides, void *v_out, const int64_t *v_out_strides, int64_t T,
+                    int64_t Hkv, int64_t Dh, int64_t num_slots, int cache_format, int dtype, void *stream);
 
 /* How rmsnorm_rope_frequencies stretches the frequencies f_i = base^(-2i / rot_dim)
  * of a model trained on trained_length positions by `factor`. */

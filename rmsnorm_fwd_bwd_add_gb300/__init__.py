@@ -23,6 +23,10 @@ include/rmsnorm.h (librmsnorm_gb300.so), with these thin Python bindings:
                   positions over part of the head, stretched for long contexts,
                   on strided heads: forward, VJP (rope: torch.autograd) and the
                   append.
+  rope_sections, rmsnorm_rope_axes -- the same with positions of several axes.
+  rmsnorm_fwd_q8 -- the forward with an e4m3 output and its scales.
+  rmsnorm_kv_append, rmsnorm_kv_read -- the append into a cache of 8 bits with a
+                  scale a head, and tokens read back from it.
   rmsnorm_kv_plan, rmsnorm_kv_release -- block tables and slot maps of a paged
                   cache from the requests' lengths.
 
@@ -42,10 +46,14 @@ from .api import (  # noqa: F401
     rmsnorm_fwd,
     rmsnorm_fwd_bind,
     rmsnorm_fwd_ex,
+    rmsnorm_fwd_q8,
     rmsnorm_gated_silu,
+    rmsnorm_kv_append,
     rmsnorm_kv_plan,
+    rmsnorm_kv_read,
     rmsnorm_kv_release,
     rmsnorm_rope,
+    rmsnorm_rope_axes,
     rmsnorm_rope_kv_append,
     rmsnorm_rope_kv_append_ex,
     rmsnorm_status_string,
@@ -56,6 +64,7 @@ from .api import (  # noqa: F401
     rmsnorm_vjp_workspace_size,
     rmsnorm_vjp_ws,
     rope_frequencies,
+    rope_sections,
 )
 from ._native import DEVSTATUS_BAD_INDEX, DEVSTATUS_WAIT_TIMEOUT, MAX_D, RmsnormError  # noqa: F401
 from .autograd import block_norm, fused_add_rmsnorm, rms_norm, rope  # noqa: F401
@@ -75,7 +84,12 @@ __all__ = [
     "rmsnorm_rope_kv_append",
     "rope_frequencies",
     "rmsnorm_rope",
+    "rope_sections",
+    "rmsnorm_rope_axes",
     "rmsnorm_rope_kv_append_ex",
+    "rmsnorm_fwd_q8",
+    "rmsnorm_kv_append",
+    "rmsnorm_kv_read",
     "rmsnorm_kv_plan",
     "rmsnorm_kv_release",
     "KvPlan",

@@ -25,10 +25,14 @@ EXPORTS = (
     "rmsnorm_block_vjp",
     "rmsnorm_block_vjp_ws",
     "rmsnorm_block_vjp_workspace_size",
+    "rmsnorm_fwd_q8",
     "rmsnorm_gated_silu",
     "rmsnorm_rope_kv_append",
     "rmsnorm_rope",
+    "rmsnorm_rope_axes",
     "rmsnorm_rope_kv_append_ex",
+    "rmsnorm_kv_append",
+    "rmsnorm_kv_read",
     "rmsnorm_rope_frequencies",
     "rmsnorm_kv_release",
     "rmsnorm_kv_plan",
@@ -55,6 +59,7 @@ STATUS = {
 DEVSTATUS_WAIT_TIMEOUT = 1
 DEVSTATUS_BAD_INDEX = 2
 ROPE_SCALING = {None: 0, "linear": 1, "ntk": 2, "yarn": 3, "llama3": 4}
+ROPE_MAX_AXES = 4
 MAX_D = 1 << 24
 VJP_NOALLOC_MAX_BYTES = 16 << 20
 
@@ -116,6 +121,18 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
                                               _vp, _vp, _vp, _vp, _f, _i, _i64, _i64, _i64, _i64,
                                               _i64, _i64, _i, _vp]
     lib.rmsnorm_rope_kv_append_ex.restype = _i
+    lib.rmsnorm_rope_axes.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _f, _i,
+                                      _i, _i64, _i64, _i64, _i64, _i64, _i64, _i, _vp]
+    lib.rmsnorm_rope_axes.restype = _i
+    lib.rmsnorm_kv_append.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp,
+                                      _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f, _i, _i64, _i64, _i64, _i64,
+                                      _i64, _i64, _i, _i, _vp]
+    lib.rmsnorm_kv_append.restype = _i
+    lib.rmsnorm_kv_read.argtypes = [_vp] * 13 + [_i64, _i64, _i64, _i64, _i, _i, _vp]
+    lib.rmsnorm_kv_read.restype = _i
+    lib.rmsnorm_fwd_q8.argtypes = [_vp, _i64, _vp, _i64, _vp, _f, _f, _vp, _i64, _vp, _i64, _vp, _i64, _i64,
+                                   _i64, _i, _vp]
+    lib.rmsnorm_fwd_q8.restype = _i
     lib.rmsnorm_rope_frequencies.argtypes = [_i, _i64, _d, _d, _d, _d, _d, _vp,
                                              ctypes.POINTER(ctypes.c_float)]
     lib.rmsnorm_rope_frequencies.restype = _i
@@ -164,7 +181,7 @@ def lib() -> ctypes.CDLL:
 
 
 _BOUND = ("rmsnorm_block_fwd", "rmsnorm_block_vjp_ws", "rmsnorm_block_vjp_workspace_size", "rmsnorm_rope", "rmsnorm_rope_kv_append_ex",
-          "rmsnorm_kv_release", "rmsnorm_kv_plan")
+          "rmsnorm_rope_axes", "rmsnorm_kv_append", "rmsnorm_kv_read", "rmsnorm_fwd_q8", "rmsnorm_kv_release", "rmsnorm_kv_plan")
 _binding = None
 
 

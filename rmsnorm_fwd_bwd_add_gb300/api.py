@@ -15,7 +15,7 @@ refuses a backward pass through what they held.
 from __future__ import annotations
 
 import ctypes
-from typing import NamedTuple, Optional, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
@@ -515,6 +515,62 @@ def rmsnorm_rope_kv_append_ex(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                 interleaved, q_out)
 
 
+def rope_sections(sections: Sequence[int], *, in_turn: bool = False) -> torch.Tensor:
+    """pair_axis of a rotary embedding over several axes: sections[a] pairs turn by
+    axis a, as runs in the axes' order, or (in_turn=True) going round the axes, past
+    those that have all of theirs.  [sum(sections)] int32, host memory."""
+    left = [int(n) for n in sections]
+    if not left or len(left) > _native.ROPE_MAX_AXES or min(left) < 0 or sum(left) == 0:
+        raise ValueError("sections must be one to %d numbers of pairs" % _native.ROPE_MAX_AXES)
+    if in_turn:
+        order = [a for turn in range(max(left)) for a, n in enumerate(left) if turn < n]
+    else:
+        order = [a for a, n in enumerate(left) for _ in range(n)]
+    return torch.tensor(order, dtype=torch.int32)
+
+
+def rmsnorm_rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
+                      inv_freq: torch.Tensor, pair_axis: torch.Tensor, *, attn_scale: float = 1.0,
+                      interleaved: bool = False, inverse: bool = False,
+                      q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                      stream=None):
+    """rmsnorm_rope with positions of several axes (time, height and width of image and
+    video tokens): pair i turns by its token's position on axis pair_axis[i].
+    positions: int64 [axes, ...] with q's leading shape behind the axes (at most 4);
+    pair_axis: [len(inv_freq)] int32 CPU, as rope_sections returns it.  Returns (q_out,
+    k_out)."""
+    return _run("rope_axes", stream, q, k, positions, inv_freq, pair_axis, attn_scale, interleaved, inverse,
+                q_out, k_out)
+
+
+def rmsnorm_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                      slots: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      inv_freq: torch.Tensor, *, k_scale: Optional[torch.Tensor] = None,
+                      v_scale: Optional[torch.Tensor] = None, pair_axis: Optional[torch.Tensor] = None,
+                      attn_scale: float = 1.0, interleaved: bool = False,
+                      q_out: Optional[torch.Tensor] = None, stream=None):
+    """rmsnorm_rope_kv_append_ex into caches that are quantised as they are written, with
+    positions of one axis or several.  Caches [num_slots, Hkv, Dh] of torch.float8_e4m3fn or
+    torch.int8 with k_scale and v_scale [num_slots, Hkv] float32 (a scale for each head of a
+    token; code * scale is the value), any slot and head strides; or of q's type, without
+    scales.  positions: [T], or [axes, T] with pair_axis as for rmsnorm_rope_axes.  Returns
+    q_out."""
+    return _run("kv_append", stream, q, k, v, positions, slots, k_cache, v_cache, inv_freq, k_scale, v_scale,
+                pair_axis, attn_scale, interleaved, q_out)
+
+
+def rmsnorm_kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                    v_scale: torch.Tensor, slots: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16,
+                    k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                    stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Reads the tokens at rows `slots` ([T] int64) of 8-bit caches back: k and v [T, Hkv, Dh]
+    in `dtype`, zeros where a slot is negative.  Caches and scales as rmsnorm_kv_append
+    writes them; k_out and v_out may have any token and head strides.  rmsnorm_kv_plan with
+    lens of zero, new_lens of the contexts' lengths and no pool gives the slots of whole
+    contexts."""
+    return _run("kv_read", stream, k_cache, v_cache, k_scale, v_scale, slots, dtype, k_out, v_out)
+
+
 class KvPlan(NamedTuple):
     """What rmsnorm_kv_plan writes: positions, slots [T] int64 and requests [T]
     int32 of the tokens, starts [B + 1] int64, granted [B] bool, and the state
@@ -651,6 +707,19 @@ def _run(name: str, stream, *args):
         raise ValueError("the stream is on cuda:%d, the tensors on %s" % (stream.device_index, args[0].device))
     with torch.cuda.stream(stream):
         return f(*args)
+
+
+def rmsnorm_fwd_q8(x: torch.Tensor, w: torch.Tensor, eps: float, weight_bias: float = 0.0,
+                   residual: Optional[torch.Tensor] = None, *, group: int = 0,
+                   out: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                   new_residual: Optional[torch.Tensor] = None, stream=None):
+    """The forward with its output in 8 bits: out [..., D] torch.float8_e4m3fn and float32
+    scales, one a row ([...], group=0) or one for each 32, 64 or 128 columns ([...,
+    ceil(D / group)]), so that out * scale is the normalised row and each group's largest
+    value is 448.  Rows may lie a stride apart.  Returns (out, scale, new_residual);
+    new_residual is None without a residual, and may be given as x or residual to update it
+    in place."""
+    return _run("fwd_q8", stream, x, w, eps, weight_bias, residual, group, out, scale, new_residual)
 
 
 def rmsnorm_block_fwd(y: torch.Tensor, residual: torch.Tensor, w_post: Optional[torch.Tensor],

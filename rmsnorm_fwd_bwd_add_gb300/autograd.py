@@ -9,8 +9,9 @@ rms_norm(x, w, eps, weight_bias) -> out
 block_norm(y, residual, w_post, w_pre, eps, weight_bias, gate, scale) -> (out, new_residual)
     forward: rmsnorm_block_fwd with both scales saved; backward:
     rmsnorm_block_vjp on y and the saved new_residual.
-rope(q, k, positions, inv_freq, attn_scale, interleaved) -> (q_out, k_out)
-    forward: rmsnorm_rope; backward: the same rotation inverted.
+rope(q, k, positions, inv_freq, attn_scale, interleaved, pair_axis) -> (q_out, k_out)
+    forward: rmsnorm_rope, or rmsnorm_rope_axes with pair_axis; backward: the same
+    rotation inverted.
 Inputs whose rows sit a stride apart (slices of wider buffers) are used in
 place; fp16, bf16 and fp32.
 
@@ -29,7 +30,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from .api import (rmsnorm_block_fwd, rmsnorm_block_vjp, rmsnorm_fwd_ex, rmsnorm_rope,
-                  rmsnorm_vjp_ex, rows_layout_ok)
+                  rmsnorm_rope_axes, rmsnorm_vjp_ex, rows_layout_ok)
 
 
 def _rows(t):
@@ -89,29 +90,35 @@ def _heads(t):
     return t if t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
 
 
+def _turn(q, k, positions, inv_freq, pair_axis, **how):
+    if pair_axis is None:
+        return rmsnorm_rope(q, k, positions, inv_freq, **how)
+    return rmsnorm_rope_axes(q, k, positions, inv_freq, pair_axis, **how)
+
+
 class RopeFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, positions, inv_freq, attn_scale: float, interleaved: bool):
+    def forward(ctx, q, k, positions, inv_freq, attn_scale: float, interleaved: bool, pair_axis):
         ctx.set_materialize_grads(False)
-        ctx.save_for_backward(positions, inv_freq)
+        ctx.save_for_backward(positions, inv_freq, pair_axis)
         ctx.attn_scale = attn_scale
         ctx.interleaved = interleaved
-        return rmsnorm_rope(_heads(q), None if k is None else _heads(k), positions, inv_freq,
-                            attn_scale=attn_scale, interleaved=interleaved)
+        return _turn(_heads(q), None if k is None else _heads(k), positions, inv_freq, pair_axis,
+                     attn_scale=attn_scale, interleaved=interleaved)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, g_q, g_k):
-        positions, inv_freq = ctx.saved_tensors
+        positions, inv_freq, pair_axis = ctx.saved_tensors
         both = [g for g in (g_q, g_k) if g is not None]
         turned = (None, None)
         if both:  # a gradient that is missing takes no part
-            turned = rmsnorm_rope(_heads(both[0]), _heads(both[1]) if len(both) == 2 else None, positions,
-                                  inv_freq, attn_scale=ctx.attn_scale, interleaved=ctx.interleaved,
-                                  inverse=True)
+            turned = _turn(_heads(both[0]), _heads(both[1]) if len(both) == 2 else None, positions,
+                           inv_freq, pair_axis, attn_scale=ctx.attn_scale, interleaved=ctx.interleaved,
+                           inverse=True)
         got = iter(turned)
         return (next(got) if g_q is not None else None, next(got) if g_k is not None else None,
-                None, None, None, None)
+                None, None, None, None, None)
 
 
 class BlockNormFunction(torch.autograd.Function):
@@ -168,7 +175,8 @@ def block_norm(y, residual, w_post, w_pre, eps: float, weight_bias: float = 0.0,
     return BlockNormFunction.apply(y, residual, w_post, w_pre, eps, weight_bias, gate, scale)
 
 
-def rope(q, k, positions, inv_freq, attn_scale: float = 1.0, interleaved: bool = False):
+def rope(q, k, positions, inv_freq, attn_scale: float = 1.0, interleaved: bool = False, pair_axis=None):
     """(q_out, k_out): q and k (which may be None) rotated to their positions, as
-    rmsnorm_rope; differentiable in q and k."""
-    return RopeFunction.apply(q, k, positions, inv_freq, attn_scale, interleaved)
+    rmsnorm_rope, or with pair_axis to positions [axes, ...] of several axes, as
+    rmsnorm_rope_axes; differentiable in q and k."""
+    return RopeFunction.apply(q, k, positions, inv_freq, attn_scale, interleaved, pair_axis)

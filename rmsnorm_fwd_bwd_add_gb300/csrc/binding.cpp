@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -57,6 +58,8 @@ const char *dtype_str(at::ScalarType t) {
            : t == at::kInt      ? "torch.int32"
            : t == at::kLong     ? "torch.int64"
            : t == at::kBool     ? "torch.bool"
+           : t == at::kChar     ? "torch.int8"
+           : t == at::kFloat8_e4m3fn ? "torch.float8_e4m3fn"
                                 : c10::toString(t);
 }
 
@@ -70,6 +73,10 @@ ENTRY(block_vjp_ws);
 ENTRY(block_vjp_workspace_size);
 ENTRY(rope);
 ENTRY(rope_kv_append_ex);
+ENTRY(rope_axes);
+ENTRY(kv_append);
+ENTRY(kv_read);
+ENTRY(fwd_q8);
 ENTRY(kv_release);
 ENTRY(kv_plan);
 #undef ENTRY
@@ -352,6 +359,49 @@ PyObject *block_vjp(PyObject *, PyObject *const *argv, Py_ssize_t n) {
     });
 }
 
+// ---- the norm with an 8-bit output -------------------------------------------
+PyObject *fwd_q8(PyObject *, PyObject *const *argv, Py_ssize_t n) {
+    return guarded(n, 9, [&]() -> PyObject * {
+        const Args a{argv, n};
+        const Tensor &x = a.tensor(0, "x"), &w = a.tensor(1, "w");
+        const Tensor *res = a.optional(4, "residual");
+        const Rows r = rows_ld("x", x);
+        const int code = dtype_code(x);
+        const int64_t ld_r = res ? rows_like("residual", *res, x) : r.D;
+        weight("w", w, x, r.D);
+        const int64_t group = a.integer(5);
+        if (group != 0 && group != 32 && group != 64 && group != 128)
+            fail(PyExc_ValueError, "group must be 0 (the row), 32, 64 or 128");
+        if (!res && argv[8] != Py_None) fail(PyExc_ValueError, "new_residual given without residual");
+        c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end() - 1);
+        if (group) shape.push_back((r.D + group - 1) / group);
+        const OnDevice on(x.device());
+        const Tensor *given = a.optional(6, "out");
+        int64_t ld_o = r.D;
+        if (given) {
+            if (given->scalar_type() != at::kFloat8_e4m3fn || given->sizes() != x.sizes() || given->device() != x.device())
+                fail(PyExc_ValueError, "out must be a %s torch.float8_e4m3fn tensor on %s", shape_str(x.sizes()).c_str(),
+                     x.device().str().c_str());
+            ld_o = rows_ld("out", *given).ld;
+        }
+        const Tensor out = given ? *given : empty(x.sizes(), at::kFloat8_e4m3fn);
+        const Tensor scale = given_or_empty("scale", a.optional(7, "scale"), at::kFloat, shape, x.device());
+        std::optional<Tensor> nr;
+        int64_t ld_n = r.D;
+        if (res) {
+            const auto made = row_output("new_residual", a.optional(8, "new_residual"), x, r.D);
+            nr = made.first;
+            ld_n = made.second;
+        }
+        check_status("rmsnorm_fwd_q8",
+                     c_fwd_q8(ptr(&x), r.ld, ptr(res), ld_r, ptr(&w), (float)a.number(2), (float)a.number(3), ptr(&out),
+                              ld_o, static_cast<float *>(ptr(&scale)), group, nr ? ptr(&*nr) : nullptr, ld_n, r.rows,
+                              r.D, code, on.stream));
+        wrote(given, a.optional(7, "scale"), a.optional(8, "new_residual"));
+        return tuple_of(wrap(out), wrap(scale), wrap_or_none(nr));
+    });
+}
+
 // ---- rotary positions --------------------------------------------------------
 int64_t rot_dim(const Tensor &inv, int64_t Dh) {
     if (inv.scalar_type() != at::kDouble || inv.dim() != 1 || !inv.device().is_cpu() || !inv.is_contiguous())
@@ -429,6 +479,189 @@ PyObject *rope(PyObject *, PyObject *const *argv, Py_ssize_t n) {
                             q.size(dim - 3), Hq, Hkv, Dh, rot, code, on.stream));
         wrote(a.optional(7, "q_out"), a.optional(8, "k_out"));
         return tuple_of(wrap(qo), wrap_or_none(ko));
+    });
+}
+
+// Positions [axes, ...] of `tokens` leading dimensions, or those dimensions alone (one
+// axis), and the axis of each pair.
+struct Axes {
+    int n;
+    const int32_t *of;
+};
+
+Axes check_axes(const Tensor &pos, const Tensor *pair_axis, c10::IntArrayRef tokens, int64_t rot, const c10::Device &dev) {
+    if (!pair_axis) {
+        exactly("positions", pos, at::kLong, tokens, dev);
+        return {1, nullptr};
+    }
+    if (pair_axis->scalar_type() != at::kInt || pair_axis->dim() != 1 || pair_axis->size(0) != rot / 2 ||
+        !pair_axis->device().is_cpu() || !pair_axis->is_contiguous())
+        fail(PyExc_ValueError, "pair_axis must be a contiguous [%lld] int32 CPU tensor, an axis for each pair",
+             (long long)(rot / 2));
+    const int64_t n = pos.dim() ? pos.size(0) : 0;
+    if (n < 1 || n > RMSNORM_ROPE_MAX_AXES)
+        fail(PyExc_ValueError, "positions must have one to %d axes in their first dimension", RMSNORM_ROPE_MAX_AXES);
+    c10::SmallVector<int64_t, 4> want{n};
+    want.append(tokens.begin(), tokens.end());
+    exactly("positions", pos, at::kLong, want, dev);
+    const int32_t *of = pair_axis->const_data_ptr<int32_t>();
+    for (int64_t i = 0; i < rot / 2; ++i)
+        if (of[i] < 0 || of[i] >= n)
+            fail(PyExc_ValueError, "pair_axis[%lld] is %d, the positions have %lld axes", (long long)i, (int)of[i],
+                 (long long)n);
+    return {(int)n, of};
+}
+
+PyObject *rope_axes(PyObject *, PyObject *const *argv, Py_ssize_t n) {
+    return guarded(n, 10, [&]() -> PyObject * {
+        const Args a{argv, n};
+        const Tensor &q = a.tensor(0, "q"), &pos = a.tensor(2, "positions"), &inv = a.tensor(3, "inv_freq");
+        const Tensor *k = a.optional(1, "k");
+        const int64_t dim = q.dim();
+        if (dim != 3 && dim != 4) fail(PyExc_ValueError, "q must be [S, Hq, Dh] or [B, S, Hq, Dh]");
+        need_cuda(q);
+        const int code = dtype_code(q);
+        const int64_t Hq = q.size(-2), Dh = q.size(-1), rot = rot_dim(inv, Dh);
+        const Axes axes = check_axes(pos, &a.tensor(4, "pair_axis"), q.sizes().slice(0, dim - 2), rot, q.device());
+        int64_t Hkv = 0;
+        if (k) {
+            if (k->dim() != dim) fail(PyExc_ValueError, "k must have q's leading dimensions");
+            Hkv = k->size(-2);
+            heads_like("k", *k, q, Hkv);
+        } else if (argv[9] != Py_None) {
+            fail(PyExc_ValueError, "k_out given without k");
+        }
+        const OnDevice on(q.device());
+        const Tensor qo = heads_output("q_out", a.optional(8, "q_out"), q);
+        std::optional<Tensor> ko;
+        Strides sk{}, sko{};
+        if (k) {
+            ko = heads_output("k_out", a.optional(9, "k_out"), *k);
+            sk = head_strides("k", *k);
+            sko = head_strides("k_out", *ko);
+        }
+        const Strides sq = head_strides("q", q), sqo = head_strides("q_out", qo);
+        check_status("rmsnorm_rope_axes",
+                     c_rope_axes(ptr(&q), sq.s, ptr(k), sk.s, static_cast<const int64_t *>(ptr(&pos)), axes.n, axes.of,
+                                 ptr(&qo), sqo.s, ko ? ptr(&*ko) : nullptr, sko.s,
+                                 static_cast<const double *>(inv.data_ptr()), (float)a.number(5), a.truth(6) ? 1 : 0,
+                                 a.truth(7) ? 1 : 0, dim == 4 ? q.size(0) : 1, q.size(dim - 3), Hq, Hkv, Dh, rot, code,
+                                 on.stream));
+        wrote(a.optional(8, "q_out"), a.optional(9, "k_out"));
+        return tuple_of(wrap(qo), wrap_or_none(ko));
+    });
+}
+
+// What a cache of this type holds: RMSNORM_CACHE_*.
+int cache_format(const Tensor &c) {
+    return c.scalar_type() == at::kFloat8_e4m3fn ? RMSNORM_CACHE_E4M3
+           : c.scalar_type() == at::kChar        ? RMSNORM_CACHE_I8
+                                                 : RMSNORM_CACHE_SAME;
+}
+
+void check_scales(const char *name, const Tensor &t, int64_t slots, int64_t Hkv, const c10::Device &dev) {
+    if (t.scalar_type() != at::kFloat || t.dim() != 2 || t.size(0) != slots || t.size(1) != Hkv || t.device() != dev)
+        fail(PyExc_ValueError, "%s must be a (%lld, %lld) torch.float32 tensor on %s", name, (long long)slots,
+             (long long)Hkv, dev.str().c_str());
+}
+
+// Both caches [num_slots, Hkv, Dh] of one type.
+void check_caches(const Tensor &kc, const Tensor &vc, int64_t Hkv, int64_t Dh, const c10::Device &dev) {
+    for (const Tensor *c : {&kc, &vc})
+        if (c->scalar_type() != kc.scalar_type() || c->device() != dev || c->dim() != 3 || c->size(1) != Hkv ||
+            c->size(2) != Dh || c->size(0) != kc.size(0))
+            fail(PyExc_ValueError, "the caches must be [num_slots, %lld, %lld] of one type on %s", (long long)Hkv,
+                 (long long)Dh, dev.str().c_str());
+}
+
+// Token (or slot) and head strides of scales [num_slots, Hkv].
+Strides scale_strides(const Tensor *t) {
+    return t ? Strides{{0, t->stride(0), t->stride(1)}} : Strides{};
+}
+
+PyObject *kv_append(PyObject *, PyObject *const *argv, Py_ssize_t n) {
+    return guarded(n, 14, [&]() -> PyObject * {
+        const Args a{argv, n};
+        const Tensor &q = a.tensor(0, "q"), &k = a.tensor(1, "k"), &v = a.tensor(2, "v");
+        const Tensor &pos = a.tensor(3, "positions"), &slots = a.tensor(4, "slots");
+        const Tensor &kc = a.tensor(5, "k_cache"), &vc = a.tensor(6, "v_cache"), &inv = a.tensor(7, "inv_freq");
+        const Tensor *ks = a.optional(8, "k_scale"), *vs = a.optional(9, "v_scale");
+        if (q.dim() != 3 || k.dim() != 3 || v.sizes() != k.sizes())
+            fail(PyExc_ValueError, "q must be [T, Hq, Dh] and k, v [T, Hkv, Dh]");
+        need_cuda(q);
+        const int code = dtype_code(q), format = cache_format(kc);
+        const int64_t T = q.size(0), Hq = q.size(1), Dh = q.size(2), Hkv = k.size(1), rot = rot_dim(inv, Dh);
+        heads_like("k", k, q, Hkv);
+        heads_like("v", v, q, Hkv);
+        check_caches(kc, vc, Hkv, Dh, q.device());
+        if (format == RMSNORM_CACHE_SAME) {
+            if (kc.scalar_type() != q.scalar_type())
+                fail(PyExc_ValueError, "the caches must be torch.float8_e4m3fn, torch.int8 or %s", dtype_str(q.scalar_type()));
+            if (ks || vs) fail(PyExc_ValueError, "k_scale and v_scale go with 8-bit caches");
+        } else {
+            if (!ks || !vs) fail(PyExc_ValueError, "8-bit caches need k_scale and v_scale");
+            check_scales("k_scale", *ks, kc.size(0), Hkv, q.device());
+            check_scales("v_scale", *vs, kc.size(0), Hkv, q.device());
+        }
+        const Axes axes = check_axes(pos, a.optional(10, "pair_axis"), {T}, rot, q.device());
+        exactly("slots", slots, at::kLong, {T}, q.device());
+        const OnDevice on(q.device());
+        const Tensor qo = heads_output("q_out", a.optional(13, "q_out"), q);
+        const Strides sq = head_strides("q", q), sk = head_strides("k", k), sv = head_strides("v", v);
+        const Strides sqo = head_strides("q_out", qo), skc = head_strides("k_cache", kc), svc = head_strides("v_cache", vc);
+        const Strides sks = scale_strides(ks), svs = scale_strides(vs);
+        check_status("rmsnorm_kv_append",
+                     c_kv_append(ptr(&q), sq.s + 1, ptr(&k), sk.s + 1, ptr(&v), sv.s + 1,
+                                 static_cast<const int64_t *>(ptr(&pos)), axes.n, axes.of,
+                                 static_cast<const int64_t *>(ptr(&slots)), ptr(&qo), sqo.s + 1, ptr(&kc), skc.s + 1,
+                                 ptr(&vc), svc.s + 1, static_cast<float *>(ptr(ks)), sks.s + 1,
+                                 static_cast<float *>(ptr(vs)), svs.s + 1, static_cast<const double *>(inv.data_ptr()),
+                                 (float)a.number(11), a.truth(12) ? 1 : 0, T, Hq, Hkv, Dh, rot, kc.size(0), format, code,
+                                 on.stream));
+        wrote(&kc, &vc, ks, vs, a.optional(13, "q_out"));
+        return wrap(qo);
+    });
+}
+
+PyObject *kv_read(PyObject *, PyObject *const *argv, Py_ssize_t n) {
+    return guarded(n, 8, [&]() -> PyObject * {
+        const Args a{argv, n};
+        const Tensor &kc = a.tensor(0, "k_cache"), &vc = a.tensor(1, "v_cache");
+        const Tensor &ks = a.tensor(2, "k_scale"), &vs = a.tensor(3, "v_scale"), &slots = a.tensor(4, "slots");
+        need_cuda(kc);
+        const c10::Device dev = kc.device();
+        const int format = cache_format(kc);
+        if (kc.dim() != 3 || format == RMSNORM_CACHE_SAME)
+            fail(PyExc_ValueError, "the caches must be [num_slots, Hkv, Dh], torch.float8_e4m3fn or torch.int8");
+        const int64_t Hkv = kc.size(1), Dh = kc.size(2);
+        check_caches(kc, vc, Hkv, Dh, dev);
+        check_scales("k_scale", ks, kc.size(0), Hkv, dev);
+        check_scales("v_scale", vs, kc.size(0), Hkv, dev);
+        if (slots.dim() != 1) fail(PyExc_ValueError, "slots must be [T]");
+        const int64_t T = slots.size(0);
+        exactly("slots", slots, at::kLong, {T}, dev);
+        if (!THPDtype_Check(argv[5])) fail(PyExc_TypeError, "dtype must be a torch.dtype");
+        const at::ScalarType type = reinterpret_cast<THPDtype *>(argv[5])->scalar_type;
+        const int code = type == at::kHalf ? 0 : type == at::kBFloat16 ? 1 : type == at::kFloat ? 2 : -1;
+        if (code < 0) fail(PyExc_TypeError, "unsupported dtype %s (fp16 or bf16 or fp32)", dtype_str(type));
+        const OnDevice on(dev);
+        auto output = [&](const char *name, const Tensor *t) {
+            if (!t) return empty({T, Hkv, Dh}, type);
+            if (t->scalar_type() != type || t->device() != dev || t->sizes() != c10::IntArrayRef({T, Hkv, Dh}))
+                fail(PyExc_ValueError, "%s must be a (%lld, %lld, %lld) %s tensor on %s", name, (long long)T,
+                     (long long)Hkv, (long long)Dh, dtype_str(type), dev.str().c_str());
+            return *t;
+        };
+        const Tensor ko = output("k_out", a.optional(6, "k_out")), vo = output("v_out", a.optional(7, "v_out"));
+        const Strides skc = head_strides("k_cache", kc), svc = head_strides("v_cache", vc);
+        const Strides sks = scale_strides(&ks), svs = scale_strides(&vs);
+        const Strides sko = head_strides("k_out", ko), svo = head_strides("v_out", vo);
+        check_status("rmsnorm_kv_read",
+                     c_kv_read(ptr(&kc), skc.s + 1, ptr(&vc), svc.s + 1, static_cast<const float *>(ptr(&ks)), sks.s + 1,
+                               static_cast<const float *>(ptr(&vs)), svs.s + 1, static_cast<const int64_t *>(ptr(&slots)),
+                               ptr(&ko), sko.s + 1, ptr(&vo), svo.s + 1, T, Hkv, Dh, kc.size(0), format, code, on.stream));
+        wrote(a.optional(6, "k_out"), a.optional(7, "v_out"));
+        return tuple_of(wrap(ko), wrap(vo));
     });
 }
 
@@ -559,7 +792,7 @@ PyObject *bind(PyObject *, PyObject *const *argv, Py_ssize_t n) {
 #define SLOT(name) {"rmsnorm_" #name, &c_##name}
         const struct { const char *name; void *slot; } table[] = {
             SLOT(block_fwd), SLOT(block_vjp_ws), SLOT(block_vjp_workspace_size), SLOT(rope), SLOT(rope_kv_append_ex),
-            SLOT(kv_release), SLOT(kv_plan)};
+            SLOT(rope_axes), SLOT(kv_append), SLOT(kv_read), SLOT(fwd_q8), SLOT(kv_release), SLOT(kv_plan)};
 #undef SLOT
         for (const auto &e : table) {
             PyObject *v = PyDict_GetItemString(argv[1], e.name);  // borrowed
@@ -577,7 +810,8 @@ PyObject *bind(PyObject *, PyObject *const *argv, Py_ssize_t n) {
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(bind),        METHOD(block_fwd),  METHOD(block_vjp), METHOD(rope),
-                         METHOD(rope_append), METHOD(kv_release), METHOD(kv_plan),   {nullptr, nullptr, 0, nullptr}};
+                         METHOD(rope_append), METHOD(kv_release), METHOD(kv_plan),   METHOD(rope_axes),
+                         METHOD(kv_append),   METHOD(kv_read),    METHOD(fwd_q8),    {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,57 @@
+// quant.cuh -- values in 8 bits: e4m3 and int8 codes of fp32 values, and the largest
+// magnitude of a group.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "rmsnorm.h"
+
+namespace rmsn {
+
+// A cache's or output's format at compile time: its largest code.
+template <int FMT> __host__ __device__ constexpr float top_code() { return FMT == RMSNORM_CACHE_I8 ? 127.f : 448.f; }
+
+// The least magnitude that a group's scale is made from: scale and 1 / scale are then
+// normal numbers whatever the group holds.
+template <int FMT> __host__ __device__ constexpr float least_top() { return top_code<FMT>() * 0x1p-126f; }
+
+// Magnitudes as the bits of their floats, which order as integers do; NaN is above
+// infinity, so a group's maximum keeps it.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Two values, times their scale's inverse already, as the codes' bytes (the first in
+// the low byte), to nearest even.  e4m3: beyond 448 saturates, NaN stays NaN.
+// int8: NaN is 0 (its scale is not a number).
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(b));
+    return r;
+}
+// One value at the nearest int8 code, in the low byte: beyond the range saturates.
+__device__ __forceinline__ uint32_t i8_code(float a) {
+    uint32_t r;
+    asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(r) : "f"(a));
+    return r & 0xffu;
+}
+template <int FMT> __device__ __forceinline__ uint32_t code_pair(float a, float b) {
+    if constexpr (FMT == RMSNORM_CACHE_I8) return i8_code(a) | i8_code(b) << 8;
+    else return e4m3_pair(a, b);
+}
+template <int FMT> __device__ __forceinline__ uint32_t code_quad(float a, float b, float c, float d) {
+    return code_pair<FMT>(a, b) | code_pair<FMT>(c, d) << 16;
+}
+
+// Two codes (low and high byte of the low half) as floats.
+template <int FMT> __device__ __forceinline__ float2 value_pair(uint32_t codes) {
+    if constexpr (FMT == RMSNORM_CACHE_I8) {
+        return make_float2((float)(int8_t)(codes & 0xffu), (float)(int8_t)(codes >> 8 & 0xffu));
+    } else {  // every e4m3 value is an fp16 one
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+        return Cvt<__half>::unpack2(h);
+    }
+}
+
+}  // namespace rmsn

@@ -1,0 +1,161 @@
+"""The axes of pairs, and the refusals of the 8-bit norm, the rotary axes and the 8-bit
+cache that come before any CUDA call."""
+import ctypes
+import os
+import shutil
+
+import pytest
+
+import rmsnorm_fwd_bwd_add_gb300 as rn
+
+pytestmark = pytest.mark.skipif(shutil.which("nvcc") is None and
+                                not os.path.exists("/usr/local/cuda/bin/nvcc"),
+                                reason="nvcc not available")
+A = 1 << 36
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    from rmsnorm_fwd_bwd_add_gb300 import _native, build
+    build.build()
+    return _native.lib()
+
+
+def on_gpu():
+    import torch
+    return torch.cuda.is_available()  # accepted calls would launch on made-up addresses
+
+
+def test_sections():
+    import torch
+    assert rn.rope_sections((2, 3, 1)).tolist() == [0, 0, 1, 1, 1, 2]
+    assert rn.rope_sections([2, 3, 1], in_turn=True).tolist() == [0, 1, 2, 0, 1, 1]
+    assert rn.rope_sections((24, 20, 20), in_turn=True).tolist() == [0, 1, 2] * 20 + [0] * 4
+    assert rn.rope_sections((0, 2)).tolist() == [1, 1] and rn.rope_sections((3,)).dtype == torch.int32
+    for bad in ((), (0, 0), (1, -1), (1, 1, 1, 1, 1)):
+        with pytest.raises(ValueError):
+            rn.rope_sections(bad)
+
+
+def q8(lib, x=A, ld_x=64, res=2 * A, ld_r=64, w=3 * A, eps=1e-6, wb=0.0, out=4 * A, ld_o=64, scale=5 * A, group=0,
+       nr=6 * A, ld_n=64, rows=10, D=64, dtype=1):
+    return lib.rmsnorm_fwd_q8(x, ld_x, res, ld_r, w, eps, wb, out, ld_o, scale, group, nr, ld_n, rows, D, dtype, None)
+
+
+def test_norm_refusals(lib):
+    for kw in (dict(dtype=3), dict(D=0), dict(rows=-1), dict(eps=-1.0), dict(eps=float("nan")), dict(wb=float("inf")),
+               dict(group=1), dict(group=-32), dict(group=256), dict(w=None), dict(x=None), dict(out=None), dict(scale=None),
+               dict(res=None), dict(nr=None), dict(ld_x=63), dict(ld_r=63), dict(ld_o=63), dict(ld_n=0), dict(x=A + 1),
+               dict(w=3 * A + 1), dict(scale=5 * A + 2), dict(nr=6 * A + 1),
+               dict(out=A), dict(out=A + 1279), dict(out=2 * A), dict(out=3 * A), dict(out=6 * A), dict(scale=A),
+               dict(scale=4 * A + 636), dict(scale=6 * A), dict(scale=3 * A), dict(nr=A + 128), dict(nr=2 * A - 128),
+               dict(nr=3 * A), dict(scale=2 * A + 1276), dict(group=32, scale=6 * A - 76)):
+        assert q8(lib, **kw) == 1, kw
+    assert q8(lib, D=(1 << 24) + 1) == 2 and q8(lib, rows=1 << 62) == 2 and q8(lib, ld_o=1 << 62, rows=1 << 40) == 2
+    assert q8(lib, rows=0, x=None, out=None, scale=None) == 0
+    if on_gpu():
+        return
+    for kw in (dict(), dict(nr=A), dict(nr=2 * A), dict(res=None, nr=None), dict(out=4 * A + 1, ld_o=65), dict(group=32),
+               dict(rows=1, ld_x=0, ld_o=0, ld_r=0, ld_n=0), dict(ld_x=100, ld_n=100, nr=A), dict(scale=4 * A + 640),
+               # x and residual side by side in one buffer, updated in place
+               dict(ld_x=128, ld_r=128, res=A + 128, nr=A + 128, ld_n=128)):
+        assert q8(lib, **kw) == 3, kw
+
+
+def strides(*s):
+    return (ctypes.c_int64 * len(s))(*s)
+
+
+def axes_of(of):
+    return None if of is None else (ctypes.c_int32 * len(of))(*of)
+
+
+def rope(lib, q=A, qs=(0, 128, 16), k=2 * A, ks=(0, 64, 16), pos=3 * A, axes=2, of=(0, 1), qo=4 * A, qos=(0, 128, 16),
+         ko=5 * A, kos=(0, 64, 16), inv=(1.0, 0.5), scale=1.0, B=1, S=10, Hq=8, Hkv=4, Dh=16, rot=4, dtype=1):
+    f = (ctypes.c_double * len(inv))(*inv) if inv is not None else None
+    return lib.rmsnorm_rope_axes(q, strides(*qs), k, strides(*ks), pos, axes, axes_of(of), qo, strides(*qos), ko,
+                                 strides(*kos), f, scale, 0, 0, B, S, Hq, Hkv, Dh, rot, dtype, None)
+
+
+def test_rope_axes_refusals(lib):
+    for kw in (dict(axes=0), dict(axes=-1), dict(of=None), dict(of=(0, 2)), dict(of=(-1, 0)), dict(dtype=3), dict(rot=3),
+               dict(inv=None), dict(pos=None), dict(q=None), dict(qo=3 * A + 88), dict(qo=3 * A), dict(ko=A), dict(B=-1),
+               # the second axis' positions in an output
+               dict(ko=3 * A + 120), dict(axes=1, of=(0, 1))):
+        assert rope(lib, **kw) == 1, kw
+    assert rope(lib, axes=5) == 2 and rope(lib, Dh=2048) == 2
+    assert rope(lib, S=0, q=None, qo=None) == 0
+    if on_gpu():
+        return
+    for kw in (dict(), dict(axes=1, of=None), dict(axes=1, of=(0, 0)), dict(axes=4, of=(3, 0)), dict(qo=A, ko=2 * A),
+               dict(Hkv=0, k=None, ko=None), dict(ko=3 * A + 160)):
+        assert rope(lib, **kw) == 3, kw
+
+
+def append(lib, q=A, qs=(128, 16), k=2 * A, ks=(64, 16), v=3 * A, vs=(64, 16), pos=4 * A, axes=1, of=None, slots=5 * A,
+           qo=6 * A, qos=(128, 16), kc=7 * A, kcs=(64, 16), vc=8 * A, vcs=(64, 16), ksc=9 * A, kss=(4, 1), vsc=10 * A,
+           vss=(4, 1), T=10, Hq=8, Hkv=4, N=100, fmt=1, dtype=1):
+    return lib.rmsnorm_kv_append(q, strides(*qs), k, strides(*ks), v, strides(*vs), pos, axes, axes_of(of), slots, qo,
+                                 strides(*qos), kc, strides(*kcs), vc, strides(*vcs), ksc, strides(*kss), vsc,
+                                 strides(*vss), (ctypes.c_double * 2)(1.0, 0.5), 1.0, 0, T, Hq, Hkv, 16, 4, N, fmt, dtype,
+                                 None)
+
+
+PACKED = dict(kcs=(160, 16), vc=7 * A + 64, vcs=(160, 16), ksc=7 * A + 128, kss=(40, 1), vsc=7 * A + 144, vss=(40, 1))
+
+
+def test_append_refusals(lib):
+    for kw in (dict(fmt=3), dict(fmt=-1), dict(dtype=3), dict(N=-1), dict(axes=0), dict(axes=2), dict(pos=None),
+               dict(slots=None), dict(kc=None), dict(vc=None), dict(ksc=None), dict(vsc=None), dict(v=None), dict(qo=None),
+               dict(kcs=(60, 16)), dict(kcs=(64, 8)), dict(kss=(3, 1)), dict(kss=(4, 0)), dict(ksc=9 * A + 2),
+               dict(vc=7 * A), dict(vc=7 * A + 6399), dict(vsc=9 * A), dict(ksc=7 * A), dict(ksc=8 * A + 6396),
+               dict(kc=A), dict(kc=2 * A + 1279), dict(vc=3 * A), dict(kc=6 * A), dict(ksc=A), dict(vsc=6 * A),
+               dict(kc=4 * A), dict(ksc=5 * A - 1596), dict(qo=4 * A), dict(qo=2 * A), dict(qo=A + 32),
+               dict(axes=2, of=(0, 1), ksc=4 * A + 156), dict(**{**PACKED, "ksc": 7 * A + 124}),
+               dict(**{**PACKED, "vsc": 7 * A + 140}), dict(fmt=0), dict(fmt=0, ksc=None)):
+        assert append(lib, **kw) == 1, kw
+    assert append(lib, axes=5, of=(0, 0)) == 2
+    assert append(lib, T=0, q=None) == 0
+    if on_gpu():
+        return
+    for kw in (dict(), dict(fmt=2), dict(fmt=0, ksc=None, vsc=None), PACKED, dict(N=0, kc=None, vc=None, ksc=None, vsc=None),
+               dict(qo=A), dict(axes=2, of=(0, 1), ksc=4 * A + 160), dict(Hkv=0, k=None, v=None),
+               dict(kcs=(16, 1600), kss=(1, 100)), dict(vc=7 * A + 6400), dict(vsc=9 * A + 1600)):
+        assert append(lib, **kw) == 3, kw
+
+
+def read(lib, kc=A, kcs=(64, 16), vc=2 * A, vcs=(64, 16), ksc=3 * A, kss=(4, 1), vsc=4 * A, vss=(4, 1), slots=5 * A,
+         ko=6 * A, kos=(64, 16), vo=7 * A, vos=(64, 16), T=10, Hkv=4, Dh=16, N=100, fmt=1, dtype=1):
+    return lib.rmsnorm_kv_read(kc, strides(*kcs), vc, strides(*vcs), ksc, strides(*kss), vsc, strides(*vss), slots, ko,
+                               strides(*kos), vo, strides(*vos), T, Hkv, Dh, N, fmt, dtype, None)
+
+
+def test_read_refusals(lib):
+    for kw in (dict(fmt=0), dict(fmt=3), dict(dtype=3), dict(T=-1), dict(Hkv=-1), dict(Dh=0), dict(N=-1), dict(kc=None),
+               dict(vsc=None), dict(slots=None), dict(ko=None), dict(vo=None), dict(kos=(63, 16)), dict(kos=(64, 15)),
+               dict(kcs=(-1, 16)), dict(ksc=3 * A + 1), dict(ko=6 * A + 1), dict(vo=6 * A), dict(ko=7 * A + 1278),
+               dict(ko=A + 6398), dict(vo=2 * A), dict(ko=3 * A), dict(vo=4 * A + 1596), dict(ko=5 * A)):
+        assert read(lib, **kw) == 1, kw
+    assert read(lib, Dh=2000) == 2 and read(lib, T=1 << 50) == 2 and read(lib, Hkv=1 << 20) == 2
+    assert read(lib, T=0, kc=None) == 0 and read(lib, Hkv=0, ko=None) == 0
+    if on_gpu():
+        return
+    for kw in (dict(), dict(fmt=2), dict(N=0, kc=None, vc=None, ksc=None, vsc=None), dict(kcs=(0, 0), kss=(0, 0)),
+               dict(vc=A, vsc=3 * A), dict(kos=(128, 16), vos=(128, 16), vo=6 * A + 128)):
+        assert read(lib, **kw) == 3, kw
+
+
+def test_python_refuses_cpu_tensors():
+    import torch
+    q = torch.zeros(2, 2, 8)
+    inv, _ = rn.rope_frequencies(8)
+    i64 = torch.zeros(2, dtype=torch.int64)
+    c, s = torch.zeros(4, 2, 8, dtype=torch.int8), torch.zeros(4, 2)
+    with pytest.raises(ValueError, match="CUDA"):
+        rn.rmsnorm_fwd_q8(torch.zeros(2, 8), torch.ones(8), 1e-6)
+    with pytest.raises(ValueError, match="CUDA"):
+        rn.rmsnorm_rope_axes(q, None, i64.view(2, 1).expand(2, 2), inv, rn.rope_sections((2, 2)))
+    with pytest.raises(ValueError, match="CUDA"):
+        rn.rmsnorm_kv_append(q, q, q, i64, i64, c, c, inv, k_scale=s, v_scale=s)
+    with pytest.raises(ValueError, match="CUDA"):
+        rn.rmsnorm_kv_read(c, c, s, s, i64)
