@@ -1,16 +1,18 @@
 // norm_q8.cu -- rmsnorm_fwd_q8: the fused residual-add norm with an e4m3 output and its
-// scales (argument checks and the choice of kernel; the kernels are in norm_q8.cuh).
+// scales (argument checks and the choice of kernel; the plan is in norm_q8.h, the kernels in norm_q8.cuh).
 #include "rmsnorm.h"
 
 #include <algorithm>
 #include <initializer_list>
 
 #include "checks.h"
-#include "launch_util.h"
-#include "norm_q8.cuh"
+#include "common.cuh"
+#include "norm_q8.h"
 
 namespace rmsn {
 int current_sm_count(int *sm);
+int current_status_word(unsigned int **status);
+void wait_settings(long long *budget, int64_t *drop);
 int record_cuda_error(cudaError_t e);
 }  // namespace rmsn
 
@@ -18,9 +20,16 @@ namespace {
 
 using namespace rmsn;
 
-template <typename T> cudaError_t launch_q8(const Q8Args &a, int sm, cudaStream_t s) {
-    const dim3 grid((unsigned)std::min<int64_t>(a.rows, 4 * (int64_t)sm));
-    return launch_pdl(a.res ? q8_generic_kernel<T, true> : q8_generic_kernel<T, false>, grid, dim3(Q8_GENERIC_NT), 0, s, a);
+// Whether a tensor's rows lie on 16-byte boundaries, or how many rows on they stand to
+// them like the first again.
+int classes_of(const Mat &m, int64_t rows, int es) {
+    const int step = rows > 1 ? (int)((uint64_t)(m.ld * es) & 15u) : 0;
+    int classes = 1;
+    while (step * classes % 16) classes *= 2;
+    return classes;
+}
+bool alike(const Mat &a, const Mat &b, int64_t rows, int es) {
+    return (((uintptr_t)a.p ^ (uintptr_t)b.p) & 15u) == 0 && (rows <= 1 || (((a.ld - b.ld) * es) & 15) == 0);
 }
 
 }  // namespace
@@ -61,11 +70,34 @@ extern "C" int rmsnorm_fwd_q8(const void *x, int64_t ld_x, const void *residual,
     int sm = 0;
     st = current_sm_count(&sm);
     if (st != RMSNORM_OK) return st;
-    const Q8Args a{x,     residual, w,    out,    new_residual, scale, mx.ld, mr.ld,
-                   mo.ld, mn.ld,    rows, (int)D, (int)group,   (int)groups, eps,   weight_bias};
+    const int E = 16 / es;
+    const bool together = !residual || (alike(mx, mr, rows, es) && alike(mx, mn, rows, es));
+    const int classes = together ? classes_of(mx, rows, es) : 0;
+    const bool on = rows_aligned(mx, es);
+    // (weights are read in whole units where the rows' units are the columns')
+    const Q8Plan p = make_q8_plan(rows, D, es, residual != nullptr, classes, on && aligned16(w), sm);
+    Q8Args a{};
+    a.x = x; a.ld_x = mx.ld;
+    a.res = residual; a.ld_res = mr.ld;
+    a.w = w;
+    a.out = out; a.ld_out = mo.ld;
+    a.nres = new_residual; a.ld_nres = mn.ld;
+    a.scale = scale;
+    a.rows = rows; a.D = (int)D;
+    a.group = (int)group; a.groups = (int)groups;
+    while (group && (1 << a.group_shift) < group) ++a.group_shift;
+    a.eps = eps; a.weight_bias = weight_bias;
+    a.stages = p.stages; a.stage_bytes = p.stage_bytes;
+    // codes of a unit of x at a multiple of their number: the first row's, and each row's
+    // step in codes like its step in elements of x
+    const uintptr_t unit0 = (uintptr_t)out + (uintptr_t)(-((uintptr_t)x) & 15u) / es;
+    a.whole_codes = unit0 % E == 0 && (rows <= 1 || (mo.ld - mx.ld) % E == 0);
+    st = current_status_word(&a.status);
+    if (st != RMSNORM_OK) return st;
+    wait_settings(&a.wait_budget, &a.drop_row);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == RMSNORM_F16    ? launch_q8<__half>(a, sm, s)
-                          : dtype == RMSNORM_BF16 ? launch_q8<__nv_bfloat16>(a, sm, s)
-                                                  : launch_q8<float>(a, sm, s);
+    const cudaError_t e = dtype == RMSNORM_F16    ? launch_q8<__half>(p, a, s)
+                          : dtype == RMSNORM_BF16 ? launch_q8<__nv_bfloat16>(p, a, s)
+                                                  : launch_q8<float>(p, a, s);
     return e == cudaSuccess ? RMSNORM_OK : record_cuda_error(e);
 }

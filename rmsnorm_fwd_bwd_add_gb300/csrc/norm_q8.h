@@ -1,6 +1,11 @@
-// norm_q8.h -- arguments of the 8-bit norm's kernels.
+// norm_q8.h -- arguments of the 8-bit norm's kernels and how a call runs (the kernels
+// are in norm_q8.cuh).
 #pragma once
 
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstddef>
 #include <cstdint>
 
 namespace rmsn {
@@ -11,8 +16,99 @@ struct Q8Args {
     float *scale;
     int64_t ld_x, ld_res, ld_out, ld_nres;
     int64_t rows;
-    int D, group, groups;  // group: columns of a scale, 0: the row; groups a row
+    int64_t drop_row;       // test hook: this row's copy is never issued
+    long long wait_budget;
+    unsigned int *status;
+    int D, group, groups;   // group: columns of a scale, 0: the row; groups a row
+    int group_shift;        // log2(group)
+    int whole_codes;        // a unit's codes are stored as one word
+    int stages;
+    uint32_t stage_bytes;   // of one tensor's row in the ring
     float eps, weight_bias;
 };
+
+// Q8_GENERIC: one element a thread.  The others hold a row in registers, 16-byte units:
+// Q8_WARP a row a warp, Q8_DIRECT a row a CTA from global memory, Q8_STAGED from a ring.
+enum : int { Q8_GENERIC = 0, Q8_WARP = 1, Q8_DIRECT = 2, Q8_STAGED = 3 };
+
+constexpr int Q8_GENERIC_NT = 512;
+constexpr int Q8_WARP_NT = 256;
+constexpr int Q8_HEADER = 128;  // the ring's mbarriers
+constexpr int Q8_MAX_STAGES = 8;
+
+struct Q8Plan {
+    int kind, shift;       // shift: the rows' units are those of memory, their ends single elements
+    int threads, units;    // units a thread
+    int grid, stages;
+    uint32_t stage_bytes;
+    size_t smem;
+};
+
+// `classes`: 0: the row tensors stand differently to 16-byte boundaries; else they stand
+// alike, a row `classes` rows on (1, 2, 4 or 8) like this one, 1 with `aligned`: on them.
+inline Q8Plan make_q8_plan(int64_t rows, int64_t D, int es, bool residual, int classes, bool aligned, int sm) {
+    Q8Plan p{};
+    const int E = 16 / es;
+    const int64_t units = D / E, row = D * es;
+    p.shift = !(aligned && row % 16 == 0);
+    auto generic = [&] {
+        Q8Plan g{};
+        g.kind = Q8_GENERIC;
+        g.threads = Q8_GENERIC_NT;
+        g.grid = (int)std::min<int64_t>(rows, 4 * (int64_t)sm);
+        return g;
+    };
+    if (classes == 0 || units < 2 || units > 2048) return generic();
+    if (!p.shift && units <= 128) {
+        p.kind = Q8_WARP;
+        p.units = units <= 32 ? 1 : units <= 64 ? 2 : 4;
+        int warps = Q8_WARP_NT / 32;  // rows side by side; fewer when SMs would idle
+        while (warps > 1 && rows < (int64_t)warps * sm) warps /= 2;
+        p.threads = 32 * warps;
+        p.grid = (int)std::min<int64_t>((rows + warps - 1) / warps, (int64_t)sm * (512 / p.threads));
+        return p;
+    }
+    auto threads_for = [&](int per) { return (int)(((units + per - 1) / per + 31) / 32 * 32); };
+    const int two = threads_for(2), per_sm2 = std::min(16, 1024 / two);
+    if (rows <= (int64_t)sm * per_sm2) {
+        p.kind = Q8_DIRECT;
+        p.units = units <= 512 ? 1 : 2;
+        p.threads = threads_for(p.units);
+        p.grid = (int)rows;
+        return p;
+    }
+    p.kind = Q8_STAGED;
+    p.units = 2;
+    p.threads = two;
+    p.stage_bytes = (uint32_t)((row + (p.shift ? 15 : 0) + 15) / 16 * 16);
+    const size_t set = (size_t)(residual ? 2 : 1) * p.stage_bytes;
+    int per_sm = per_sm2;
+    auto fits = [&](int ctas) {
+        const size_t share = (size_t)228 * 1024 / ctas, used = 1024 + 8 * 1024 + Q8_HEADER;
+        return share > used ? (int)std::min<size_t>(Q8_MAX_STAGES, (share - used) / set) : 0;
+    };
+    while (per_sm > 1 && fits(per_sm) < 2) --per_sm;
+    p.stages = fits(per_sm);
+    if (p.stages < 1) return generic();
+    p.smem = Q8_HEADER + (size_t)p.stages * set;
+    p.grid = (int)std::min<int64_t>(rows, (int64_t)sm * per_sm);
+    if (p.shift && classes > 1) {  // a CTA's rows all stand the same way
+        p.grid = p.grid / classes * classes;
+        if (p.grid == 0) return generic();
+    }
+    return p;
+}
+
+// Whether the kernels can run a plan (a launch of any other would leave its shared memory).
+inline bool q8_plan_ok(const Q8Plan &p) {
+    if (p.grid < 1 || p.threads < 32 || p.threads > 1024 || p.threads % 32) return false;
+    if (p.kind == Q8_STAGED) return p.units == 2 && p.stages >= 1 && p.stages <= Q8_MAX_STAGES && p.stage_bytes > 0;
+    if (p.kind == Q8_WARP) return p.threads <= Q8_WARP_NT && !p.shift && (p.units == 1 || p.units == 2 || p.units == 4);
+    if (p.kind == Q8_DIRECT) return p.units == 2 || (p.units == 1 && p.threads <= 512);
+    return p.kind == Q8_GENERIC && p.threads == Q8_GENERIC_NT;
+}
+
+// Launchers of one element type each (norm_q8_<type>.cu).
+template <typename T> cudaError_t launch_q8(const Q8Plan &p, const Q8Args &a, cudaStream_t s);
 
 }  // namespace rmsn

@@ -1,0 +1,9 @@
+// norm_q8_f32.cu -- instances of the 8-bit norm.
+#include "norm_q8.cuh"
+
+namespace rmsn {
+template <>
+cudaError_t launch_q8<float>(const Q8Plan &p, const Q8Args &a, cudaStream_t s) {
+    return launch_q8_any<float>(p, a, s);
+}
+}  // namespace rmsn
