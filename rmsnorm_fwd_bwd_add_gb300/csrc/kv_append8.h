@@ -1,0 +1,50 @@
+// kv_append8.h -- the 8-bit append's launchers of one input type each
+// (kv_append8_<type>.cu; the kernels are in kv_cache8.cuh).
+#pragma once
+
+#include "kv_cache8.cuh"
+
+namespace rmsn {
+
+// unit: bytes that divide every address, stride and length of q, k, v and q_out, and in
+// elements those of the caches: 16 or 4, or less.
+template <typename T> cudaError_t launch_append8(const AppendArgs &a, int format, bool interleaved, int unit, int sm, cudaStream_t s);
+
+template <typename T, int VB, bool INTERLEAVED, int FMT, int UPL>
+cudaError_t launch_append8_units(const AppendArgs &a, int lanes, int sm, cudaStream_t s) {
+    const RopePlan p = make_append8_plan(a.T, (lanes + UPL - 1) / UPL, a.Hq + 2 * a.Hkv, C8_UNITS_IN_FLIGHT / UPL,
+                                         sm * append8_ctas<VB / (int)sizeof(T), UPL>(), C8_NT / 32);
+    return launch_pdl(append8_kernel<T, VB, INTERLEAVED, FMT, UPL>, dim3(p.grid), dim3(C8_NT), 0, s, a, p.whole, p.wpt, p.cw);
+}
+
+template <typename T, bool INTERLEAVED, int FMT>
+cudaError_t launch_append8_layout(const AppendArgs &a, int unit, int sm, cudaStream_t s) {
+    auto lanes_of = [&](auto ve) { return HeadMap<decltype(ve)::value, INTERLEAVED, INTERLEAVED>(a.Dh, a.rot).lanes; };
+    if (unit == 16) {
+        const int lanes = lanes_of(std::integral_constant<int, 16 / (int)sizeof(T)>{});
+        if (lanes <= 32) return launch_append8_units<T, 16, INTERLEAVED, FMT, 1>(a, lanes, sm, s);
+        if (lanes <= 64) return launch_append8_units<T, 16, INTERLEAVED, FMT, 2>(a, lanes, sm, s);
+        if constexpr (sizeof(T) == 4) return launch_append8_units<T, 16, INTERLEAVED, FMT, 4>(a, lanes, sm, s);
+    }
+    if constexpr (sizeof(T) == 2)
+        if (unit >= 4) {
+            const int lanes = lanes_of(std::integral_constant<int, 2>{});
+            if (lanes <= 32) return launch_append8_units<T, 4, INTERLEAVED, FMT, 1>(a, lanes, sm, s);
+            if (lanes <= 64) return launch_append8_units<T, 4, INTERLEAVED, FMT, 2>(a, lanes, sm, s);
+            if (lanes <= 128) return launch_append8_units<T, 4, INTERLEAVED, FMT, 4>(a, lanes, sm, s);
+        }
+    const int64_t warps = a.T * (a.Hq + 2 * (int64_t)a.Hkv);
+    const dim3 grid((unsigned)std::min<int64_t>((warps + C8_NT / 32 - 1) / (C8_NT / 32), 8 * (int64_t)sm));
+    return launch_pdl(append8_generic_kernel<T, FMT, INTERLEAVED>, grid, dim3(C8_NT), 0, s, a);
+}
+
+template <typename T>
+cudaError_t launch_append8_any(const AppendArgs &a, int format, bool interleaved, int unit, int sm, cudaStream_t s) {
+    if (format == RMSNORM_CACHE_I8)
+        return interleaved ? launch_append8_layout<T, true, RMSNORM_CACHE_I8>(a, unit, sm, s)
+                           : launch_append8_layout<T, false, RMSNORM_CACHE_I8>(a, unit, sm, s);
+    return interleaved ? launch_append8_layout<T, true, RMSNORM_CACHE_E4M3>(a, unit, sm, s)
+                       : launch_append8_layout<T, false, RMSNORM_CACHE_E4M3>(a, unit, sm, s);
+}
+
+}  // namespace rmsn

@@ -9,6 +9,7 @@
 
 #include "checks.h"
 #include "heads.h"
+#include "kv_append8.h"
 #include "kv_cache8.cuh"
 #include "launch_util.h"
 #include "rope_host.h"
@@ -38,17 +39,24 @@ bool hits(const Span &a, const void *p, size_t n) {
     return a.hi > a.lo && overlaps((const void *)a.lo, a.hi - a.lo, p, n);
 }
 
-template <typename T, int FMT> cudaError_t launch_append(const AppendArgs &a, int interleaved, int sm, cudaStream_t s) {
-    const int64_t warps = a.T * (a.Hq + 2 * (int64_t)a.Hkv);
-    const dim3 grid((unsigned)std::min<int64_t>((warps + C8_NT / 32 - 1) / (C8_NT / 32), 8 * (int64_t)sm));
-    return launch_pdl(interleaved ? append8_generic_kernel<T, FMT, true> : append8_generic_kernel<T, FMT, false>, grid,
-                      dim3(C8_NT), 0, s, a);
+template <typename T, int FMT, int C> cudaError_t launch_read_units(const ReadArgs &a, int sm, cudaStream_t s) {
+    // as many parts a token as there are warps for, and units for
+    const int64_t warps = (int64_t)sm * R8_CTAS_PER_SM * (C8_NT / 32), units = (int64_t)2 * a.Hkv * (a.Dh / C);
+    int wpt = 1;
+    while (wpt < 64 && 2 * wpt * a.T <= warps && wpt * 32 < units) wpt *= 2;
+    const int64_t ctas = (a.T * wpt + C8_NT / 32 - 1) / (C8_NT / 32);
+    return launch_pdl(read8_kernel<T, FMT, C>, dim3((unsigned)std::min<int64_t>(ctas, sm * R8_CTAS_PER_SM)), dim3(C8_NT), 0,
+                      s, a, wpt);
 }
 
-template <typename T, int FMT> cudaError_t launch_read(const ReadArgs &a, int sm, cudaStream_t s) {
-    const int64_t warps = a.T * 2 * a.Hkv;
-    const dim3 grid((unsigned)std::min<int64_t>((warps + C8_NT / 32 - 1) / (C8_NT / 32), 8 * (int64_t)sm));
-    return launch_pdl(read8_generic_kernel<T, FMT>, grid, dim3(C8_NT), 0, s, a);
+// unit: codes that divide every address, stride and head of the caches, and in
+// elements those of the outputs.
+template <typename T, int FMT> cudaError_t launch_read(const ReadArgs &a, int unit, int sm, cudaStream_t s) {
+    return unit == 16  ? launch_read_units<T, FMT, 16>(a, sm, s)
+           : unit == 8 ? launch_read_units<T, FMT, 8>(a, sm, s)
+           : unit == 4 ? launch_read_units<T, FMT, 4>(a, sm, s)
+           : unit == 2 ? launch_read_units<T, FMT, 2>(a, sm, s)
+                       : launch_read_units<T, FMT, 1>(a, sm, s);
 }
 
 template <typename T> struct Tag { using type = T; };
@@ -133,9 +141,17 @@ extern "C" int rmsnorm_kv_append(const void *q, const int64_t *q_strides, const 
     fill_rope_axes(&a.axes, pair_axes, rot_dim);
     a.k_scale = ks;
     a.v_scale = vs;
-    const cudaError_t e = by_type(dtype, cache_format, [&](auto t, auto f) {
-        return launch_append<typename decltype(t)::type, decltype(f)::value>(a, interleaved, sm, static_cast<cudaStream_t>(stream));
-    });
+    // the widest vectors that divide the inputs, the rotated part's halves (half layout)
+    // or whole (interleaved) and the head, with their codes at a multiple of their number
+    const uintptr_t bits = byte_bits(hq, 1, T, Hq, es) | byte_bits(hqo, 1, T, Hq, es) | byte_bits(hk, 1, T, Hkv, es) |
+                           byte_bits(hv, 1, T, Hkv, es) | byte_bits(hkc, 1, num_slots, Hkv, 1) * es |
+                           byte_bits(hvc, 1, num_slots, Hkv, 1) * es |
+                           (uintptr_t)((interleaved ? rot_dim : rot_dim / 2) * es) | (uintptr_t)(Dh * es);
+    const int unit = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == RMSNORM_F16    ? launch_append8<__half>(a, cache_format, interleaved, unit, sm, s)
+                          : dtype == RMSNORM_BF16 ? launch_append8<__nv_bfloat16>(a, cache_format, interleaved, unit, sm, s)
+                                                  : launch_append8<float>(a, cache_format, interleaved, unit, sm, s);
     return e == cudaSuccess ? RMSNORM_OK : record_cuda_error(e);
 }
 
@@ -176,8 +192,13 @@ extern "C" int rmsnorm_kv_read(const void *k_cache, const int64_t *k_cache_strid
     if (st == RMSNORM_OK) st = current_status_word(&status);
     if (st != RMSNORM_OK) return st;
     const ReadArgs a{hk, hv, hko, hvo, ks, vs, slots, T, num_slots, (int)Hkv, (int)Dh, status};
+    // whole words of codes, and of elements: at most 16 bytes
+    uintptr_t bits = (uintptr_t)Dh | byte_bits(hk, 1, num_slots, Hkv, 1) | byte_bits(hv, 1, num_slots, Hkv, 1);
+    const uintptr_t out_bits = byte_bits(hko, 1, T, Hkv, es) | byte_bits(hvo, 1, T, Hkv, es);
+    bits |= out_bits % 16 == 0 ? 0 : out_bits / es;
+    const int unit = bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
     const cudaError_t e = by_type(dtype, cache_format, [&](auto t, auto f) {
-        return launch_read<typename decltype(t)::type, decltype(f)::value>(a, sm, static_cast<cudaStream_t>(stream));
+        return launch_read<typename decltype(t)::type, decltype(f)::value>(a, unit, sm, static_cast<cudaStream_t>(stream));
     });
     return e == cudaSuccess ? RMSNORM_OK : record_cuda_error(e);
 }

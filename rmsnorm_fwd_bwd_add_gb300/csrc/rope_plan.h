@@ -49,4 +49,23 @@ inline RopePlan make_rope_plan(int64_t T, int lanes, int heads, int in_flight, i
     return p;
 }
 
+// The same for the 8-bit append, whose steps are whole heads: `cw` lanes each.
+inline RopePlan make_append8_plan(int64_t T, int cw, int heads, int in_flight, int ctas, int cta_warps) {
+    const int64_t warps = (int64_t)ctas * cta_warps;
+    RopePlan p{T / warps * warps, 1, cw, 0};
+    const int64_t rest = T - p.whole;
+    int64_t best = INT64_MAX;
+    for (int k = 1; k <= 16; k *= 2) {
+        const int per_trip = (32 / cw) * in_flight * k, trips = (heads + per_trip - 1) / per_trip;
+        const int64_t cost = (rest * k + warps - 1) / warps * (2 + 2 * trips);
+        if (cost < best) {
+            best = cost;
+            p.wpt = k;
+        }
+    }
+    const int64_t items = p.whole + rest * p.wpt;
+    p.grid = (int)std::min<int64_t>((items + cta_warps - 1) / cta_warps, ctas);
+    return p;
+}
+
 }  // namespace rmsn
