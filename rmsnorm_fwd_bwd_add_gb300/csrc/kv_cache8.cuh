@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(C8_NT, (append8_ctas<VB / (int)sizeof(T), UPL>
                 const bool mine = hs < hpi && h < heads, is_q = h < a.Hq, is_v = h >= n_qk;
                 const uint32_t wanted = !mine ? 0u : is_v ? v_in : is_q && !q_moves ? turns : in, both = is_v ? v_two : two;
                 float fa[UPL][VE], fb[UPL][VE];
-                uint32_t top = 0;
+                float top = 0.f;
 #pragma unroll
                 for (int i = 0; i < UPL; ++i)
                     if (wanted >> i & 1) {
@@ -210,18 +210,18 @@ __global__ void __launch_bounds__(C8_NT, (append8_ctas<VB / (int)sizeof(T), UPL>
                             if (both >> i & 1) *reinterpret_cast<V *>(dst + ib[i]) = pack_raw<T, VB>(fb[i]);
                         } else {
 #pragma unroll
-                            for (int e = 0; e < VE; ++e) top = max(top, max(magnitude(fa[i][e]), magnitude(fb[i][e])));
+                            for (int e = 0; e < VE; ++e) top = max_abs(top, fa[i][e], fb[i][e]);
                         }
                     }
                 if (first + hpi <= a.Hq) continue;  // heads of q alone
                 // the largest of the head's cw lanes (counting some twice does no harm)
                 for (int off = 1; off < cw; off *= 2) {
                     const int at = lu + off;
-                    top = max(top, __shfl_sync(0xffffffffu, top, hs < hpi ? lane - lu + (at < cw ? at : at - cw) : lane));
+                    top = max_abs(top, __shfl_sync(0xffffffffu, top, hs < hpi ? lane - lu + (at < cw ? at : at - cw) : lane));
                 }
                 if (!mine || is_q) continue;
-                const float most = __uint_as_float(max(top, __float_as_uint(least_top<FMT>())));
-                const float by = top_code<FMT>() / most;
+                const float most = scaled_top<FMT>(top);
+                const float by = code_factor<FMT>(most);
                 unsigned char *dst = (is_v ? vo : ko) + (uint64_t)(uint32_t)h * (is_v ? a.v_out.head_bytes : a.k_out.head_bytes);
 #pragma unroll
                 for (int i = 0; i < UPL; ++i)
@@ -287,11 +287,10 @@ __global__ void __launch_bounds__(C8_NT) append8_generic_kernel(const __grid_con
             });
             continue;
         }
-        uint32_t top = 0;
-        each([&](int, float u, int, float w) { top = max(top, max(magnitude(u), magnitude(w))); });
-        top = __reduce_max_sync(0xffffffffu, top);
-        const float most = __uint_as_float(max(top, __float_as_uint(least_top<FMT>())));
-        const float by = top_code<FMT>() / most;
+        float top = 0.f;
+        each([&](int, float u, int, float w) { top = max_abs(top, u, w); });
+        const float most = scaled_top<FMT>(warp_max(top));
+        const float by = code_factor<FMT>(most);
         const Heads &dst = what == 1 ? a.k_out : a.v_out;
         uint8_t *o = static_cast<uint8_t *>(const_cast<void *>(dst.p)) + slot * dst.st + hk * dst.sh;
         each([&](int i, float u, int j, float w) {

@@ -12,6 +12,8 @@
 //              thread has its units in registers, at the row's barrier.
 //   Q8_DIRECT  one row a CTA from global memory: no more rows than CTAs fit at once.
 //   Q8_WARP    short rows, one a warp, the next one's loads ahead of this one's sums.
+//   Q8_LONG, Q8_GENERIC  rows that do not fit, or whose tensors stand differently to
+//              16-byte boundaries, read twice.
 //
 // SHIFT: rows off 16-byte boundaries whose tensors all stand alike.  Units are then those
 // of memory (hd columns in), the columns before and behind them one a thread; a CTA's rows
@@ -28,31 +30,42 @@
 namespace rmsn {
 
 // The scale of a group and the factor of its codes.
-__device__ __forceinline__ float2 q8_scale(uint32_t top, float r) {
-    // (integers: NaN and infinity stay)
-    const float a = __uint_as_float(max(top, __float_as_uint(least_top<RMSNORM_CACHE_E4M3>())));
-    return make_float2(r * a * (1.f / 448.f), 448.f / a);
+__device__ __forceinline__ float2 q8_scale(float top, float r) {
+    const float a = scaled_top<RMSNORM_CACHE_E4M3>(top);
+    return make_float2(r * a * (1.f / 448.f), code_factor<RMSNORM_CACHE_E4M3>(a));
 }
 
-// The 8 (16-bit inputs) or 4 codes of a unit.
-template <int E> __device__ __forceinline__ void store_codes(uint8_t *p, const float (&v)[E], float by, bool whole) {
-    uint32_t c[E / 4];
+// The 8 (16-bit inputs) or 4 codes of a unit, P pairs of values, stored if `in`.
+template <int P> __device__ __forceinline__ void store_codes(uint8_t *p, const float2 (&v)[P], float by, bool whole, bool in) {
+    uint32_t c[P / 2];
 #pragma unroll
-    for (int i = 0; i < E / 4; ++i)
-        c[i] = code_quad<RMSNORM_CACHE_E4M3>(v[4 * i] * by, v[4 * i + 1] * by, v[4 * i + 2] * by, v[4 * i + 3] * by);
+    for (int i = 0; i < P / 2; ++i) {
+        const float2 a = f2mul(v[2 * i], make_float2(by, by)), b = f2mul(v[2 * i + 1], make_float2(by, by));
+        c[i] = code_quad<RMSNORM_CACHE_E4M3>(a.x, a.y, b.x, b.y);
+    }
     if (whole) {
-        if constexpr (E == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(c[0], c[1]);
-        else *reinterpret_cast<uint32_t *>(p) = c[0];
-    } else {
+        if constexpr (P == 4) {
+            if (in) *reinterpret_cast<uint2 *>(p) = make_uint2(c[0], c[1]);
+        } else {
+            if (in) *reinterpret_cast<uint32_t *>(p) = c[0];
+        }
+    } else if (in) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) p[e] = (uint8_t)(c[e / 4] >> (8 * (e % 4)));
+        for (int e = 0; e < 2 * P; ++e) p[e] = (uint8_t)(c[e / 4] >> (8 * (e % 4)));
     }
 }
 
-// Maximum over aligned runs of n lanes (a power of two).
-__device__ __forceinline__ uint32_t run_max(uint32_t v, int n) {
-    for (int off = 1; off < n; off *= 2) v = max(v, __shfl_xor_sync(0xffffffffu, v, off));
-    return v;
+// run_max of V values at once.
+template <int V> __device__ __forceinline__ void run_maxima(float (&top)[V], int n) {
+    if (n == 32) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) top[j] = warp_max(top[j]);
+        return;
+    }
+    for (int off = 1; off < n; off *= 2) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) top[j] = max_abs(top[j], __shfl_xor_sync(0xffffffffu, top[j], off));
+    }
 }
 
 template <typename T>
@@ -73,22 +86,24 @@ __device__ __forceinline__ void q8_issue(const Q8Args &a, uint64_t *full, unsign
 // One row a CTA.  V units a thread.
 template <typename T, bool RES, bool SHIFT, bool STAGED, int V, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) q8_row_kernel(const __grid_constant__ Q8Args a) {
-    constexpr int E = vec_elems<T>(), MAXW = MAXT / 32;
+    constexpr int E = vec_elems<T>(), P = vec_pairs<T>(), MAXW = MAXT / 32;
     constexpr int MAXG = SHIFT ? MAXT * V * E / 32 + 2 : 1;  // groups of 32 columns
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float s_sum[2][MAXW];
-    __shared__ uint32_t s_top[2][MAXW];
+    __shared__ float2 s_row[2][MAXW];  // a warp's sum of squares and largest value
     __shared__ uint32_t s_group[SHIFT ? 3 : 1][MAXG];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, NT = blockDim.x, nw = NT >> 5;
     const int D = a.D;
     const float inv_D = 1.0f / (float)D;
     const bool grouped = a.group != 0;
-    const int run = grouped ? a.group / E : 32;  // units (lanes) of a group
+    const int run = grouped ? a.group / E : 32, run_shift = 31 - __clz(run);  // units (lanes) of a group
     const int64_t r0 = blockIdx.x, step = gridDim.x;
     // hd: columns before a row's first 16-byte boundary
     const int hd = SHIFT ? (int)(-((uintptr_t)(static_cast<const T *>(a.x) + r0 * a.ld_x)) & 15u) / (int)sizeof(T) : 0;
     const int NU = SHIFT ? min((D - hd) / E, V * NT) : D / E;
     const int cx = !SHIFT || t >= D - NU * E ? -1 : t < hd ? t : NU * E + t;  // this thread's single column
+    // SHIFT: whether this thread's units cross a group's border, their first E - hd elements
+    // before it (a CTA's threads are whole groups)
+    const bool crosses = SHIFT && grouped && hd && (t & (run - 1)) == run - 1;
 
     uint64_t *full = reinterpret_cast<uint64_t *>(smem);
     unsigned char *data = smem + Q8_HEADER;
@@ -109,12 +124,16 @@ __global__ void __launch_bounds__(MAXT, MINB) q8_row_kernel(const __grid_constan
         if (t == 0)
             for (int s = 0; s < a.stages && r0 + s * step < a.rows; ++s) q8_issue<T>(a, full, data, r0 + s * step, s, policy);
 
-    uint4 vx[V], vr[RES ? V : 1], vw[V];
+    // A thread's units past the row are zeros, and its loops run over all V of them: with a
+    // branch around each, none of their work overlapped.
+    uint4 vx[V], vr[RES ? V : 1];
     float xx = 0.f, xr = 0.f, xw = 0.f;  // of column cx
     auto fetch = [&](const T *px, const T *pr) {  // at column hd
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int u = t + j * NT;
+            vx[j] = make_uint4(0, 0, 0, 0);
+            if constexpr (RES) vr[j] = make_uint4(0, 0, 0, 0);
             if (u < NU) {
                 vx[j] = STAGED ? reinterpret_cast<const uint4 *>(px)[u] : ld_stream(reinterpret_cast<const uint4 *>(px) + u);
                 if constexpr (RES)
@@ -127,33 +146,34 @@ __global__ void __launch_bounds__(MAXT, MINB) q8_row_kernel(const __grid_constan
                 if constexpr (RES) xr = Cvt<T>::load1(pr + (cx - hd));
             }
     };
-    auto fetch_global = [&](int64_t row) {
-        fetch(static_cast<const T *>(a.x) + row * a.ld_x + hd,
-              RES ? static_cast<const T *>(a.res) + row * a.ld_res + hd : nullptr);
-    };
-    if constexpr (!STAGED) fetch_global(r0);
+    if constexpr (!STAGED)
+        fetch(static_cast<const T *>(a.x) + r0 * a.ld_x + hd, RES ? static_cast<const T *>(a.res) + r0 * a.ld_res + hd : nullptr);
     const T *wg = static_cast<const T *>(a.w);
+    float2 w[V][P];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int u = t + j * NT;
+        uint4 c = make_uint4(0, 0, 0, 0);
         if (u < NU) {
             if constexpr (SHIFT) {
-                T c[E];
+                T e1[E];
 #pragma unroll
-                for (int e = 0; e < E; ++e) c[e] = wg[hd + u * E + e];
-                memcpy(&vw[j], c, 16);
+                for (int e = 0; e < E; ++e) e1[e] = wg[hd + u * E + e];
+                memcpy(&c, e1, 16);
             } else {
-                vw[j] = __ldg(reinterpret_cast<const uint4 *>(wg) + u);
+                c = __ldg(reinterpret_cast<const uint4 *>(wg) + u);
             }
         }
+        unpack_vec<T>(c, w[j]);
+#pragma unroll
+        for (int m = 0; m < P; ++m) w[j][m] = f2add(w[j][m], make_float2(a.weight_bias, a.weight_bias));
     }
     if constexpr (SHIFT)
         if (cx >= 0) xw = a.weight_bias + Cvt<T>::load1(wg + cx);
 
-    int s = 0, buf = 0;
+    int s = 0, buf = 0, side = 0;
     uint32_t ph = 0;
-    int64_t i = 0;
-    for (int64_t row = r0; row < a.rows; row += step, ++i) {
+    for (int64_t row = r0; row < a.rows; row += step) {
         bool ok = true;
         if constexpr (STAGED) {
             const unsigned char *st = data + (size_t)s * (RES ? 2 : 1) * a.stage_bytes;
@@ -163,45 +183,42 @@ __global__ void __launch_bounds__(MAXT, MINB) q8_row_kernel(const __grid_constan
         }
         T *nres = RES ? static_cast<T *>(a.nres) + row * a.ld_nres + hd : nullptr;
         uint8_t *out = static_cast<uint8_t *>(a.out) + row * a.ld_out + hd;
-        float v[V][E], ss = 0.f;
-        uint32_t top = 0, part[V];  // part: a group's maximum so far
+        float2 v[V][P], s2 = make_float2(0.f, 0.f);
+        float part[V];  // a unit's largest value
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int u = t + j * NT;
-            part[j] = 0;
-            if (u < NU) {
-                float w[E];
-                unpack_vec<T>(vx[j], v[j]);
-                if constexpr (RES) {
-                    float r[E];
-                    unpack_vec<T>(vr[j], r);
+            unpack_vec<T>(vx[j], v[j]);
+            if constexpr (RES) {
+                float2 r[P];
+                unpack_vec<T>(vr[j], r);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) v[j][e] += r[e];
-                    if (ok) reinterpret_cast<uint4 *>(nres)[u] = pack_vec<T>(v[j]);
-                }
-                unpack_vec<T>(vw[j], w);
+                for (int m = 0; m < P; ++m) v[j][m] = f2add(v[j][m], r[m]);
+                if (ok && t + j * NT < NU) reinterpret_cast<uint4 *>(nres)[t + j * NT] = pack_vec<T>(v[j]);
+            }
+            part[j] = 0.f;
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    ss = fmaf(v[j][e], v[j][e], ss);
-                    v[j][e] *= a.weight_bias + w[e];
-                }
-                if constexpr (SHIFT) {
-                    // a unit across a border: its first E - hd elements (all where hd = 0)
-                    const int own = grouped && (u & (run - 1)) == run - 1 ? E - hd : E;
-                    uint32_t next = 0;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        if (e < own) part[j] = max(part[j], magnitude(v[j][e]));
-                        else next = max(next, magnitude(v[j][e]));
-                    }
-                    if (own < E) atomicMax(&s_group[buf][u / run + 1], next);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) part[j] = max(part[j], magnitude(v[j][e]));
-                }
+            for (int m = 0; m < P; ++m) {
+                s2 = f2fma(v[j][m], v[j][m], s2);
+                v[j][m] = f2mul(v[j][m], w[j][m]);
+                part[j] = max_abs(part[j], v[j][m].x, v[j][m].y);
             }
         }
-        float xv = 0.f;
+        if constexpr (SHIFT)
+            if (crosses) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float next = 0.f;
+                    part[j] = 0.f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const float x = e & 1 ? v[j][e / 2].y : v[j][e / 2].x;
+                        if (e < E - hd) part[j] = max_abs(part[j], x);
+                        else next = max_abs(next, x);
+                    }
+                    if (t + j * NT < NU) atomicMax(&s_group[buf][((t + j * NT) >> run_shift) + 1], __float_as_uint(next));
+                }
+            }
+        float xv = 0.f, ss = s2.x + s2.y, top = 0.f;
         if constexpr (SHIFT)
             if (cx >= 0) {
                 const float h = xx + xr;
@@ -209,34 +226,35 @@ __global__ void __launch_bounds__(MAXT, MINB) q8_row_kernel(const __grid_constan
                     if (ok) Cvt<T>::store1(nres + (cx - hd), h);
                 ss = fmaf(h, h, ss);
                 xv = h * xw;
-                if (grouped) atomicMax(&s_group[buf][cx >> a.group_shift], magnitude(xv));
-                top = magnitude(xv);
+                if (grouped) atomicMax(&s_group[buf][cx >> a.group_shift], __float_as_uint(max_abs(0.f, xv)));
+                top = max_abs(0.f, xv);
             }
+        if (grouped) {
+            run_maxima(part, run);
+            if constexpr (SHIFT) {
+                if ((t & (run - 1)) == 0) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int u = t + j * NT;
-            if (!grouped) {
-                top = max(top, part[j]);
-            } else {
-                part[j] = run_max(part[j], run);
-                if constexpr (SHIFT) {
-                    if (u < NU && (u & (run - 1)) == 0) atomicMax(&s_group[buf][u / run], part[j]);
-                } else if (ok && u < NU) {  // no need to wait for the row's sum
-                    store_codes<E>(out + u * E, v[j], q8_scale(part[j], 1.f).y, a.whole_codes);
+                    for (int j = 0; j < V; ++j)
+                        if (t + j * NT < NU) atomicMax(&s_group[buf][(t + j * NT) >> run_shift], __float_as_uint(part[j]));
                 }
+            } else if (ok) {  // no need to wait for the row's sum
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    store_codes(out + (t + j * NT) * E, v[j], q8_scale(part[j], 1.f).y, a.whole_codes, t + j * NT < NU);
             }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) top = max_abs(top, part[j]);
+            top = warp_max(top);
         }
         ss = group_sum<32>(ss);
-        if (!grouped) top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) {
-            s_sum[i & 1][warp] = ss;
-            s_top[i & 1][warp] = top;
-        }
+        if (lane == 0) s_row[side][warp] = make_float2(ss, top);
         const bool bad = __syncthreads_or(!ok);
         if constexpr (STAGED) {
             if (bad) {  // leave once this CTA's copies have landed
                 if (t == 0) {
                     atomicOr(a.status, DEVSTATUS_WAIT_TIMEOUT);
+                    const int64_t i = (row - r0) / step;
                     for (int64_t k = i; k < i + a.stages && r0 + k * step < a.rows; ++k)
                         if (r0 + k * step != a.drop_row)
                             mbar_wait_bounded(&full[k % a.stages], (uint32_t)((k / a.stages) & 1), DEFAULT_WAIT_BUDGET);
@@ -245,78 +263,79 @@ __global__ void __launch_bounds__(MAXT, MINB) q8_row_kernel(const __grid_constan
             }
             if (t == 0 && row + a.stages * step < a.rows) q8_issue<T>(a, full, data, row + a.stages * step, s, policy);
         }
-        ss = group_sum<32>(lane < nw ? s_sum[i & 1][lane] : 0.f);
-        const float r = rsqrtf(ss * inv_D + a.eps);
+        // every lane of MAXW has a warp's, the next MAXW lanes the same again
+        const float2 mine = (lane & (MAXW - 1)) < nw ? s_row[side][lane & (MAXW - 1)] : make_float2(0.f, 0.f);
+        side ^= 1;
+        const float r = rsqrtf(group_sum<MAXW>(mine.x) * inv_D + a.eps);
         if (!grouped) {
-            const float2 sc = q8_scale(__reduce_max_sync(0xffffffffu, lane < nw ? s_top[i & 1][lane] : 0u), r);
+            const float2 sc = q8_scale(run_max(mine.y, MAXW), r);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int u = t + j * NT;
-                if (u < NU) store_codes<E>(out + u * E, v[j], sc.y, a.whole_codes);
-            }
+            for (int j = 0; j < V; ++j) store_codes(out + (t + j * NT) * E, v[j], sc.y, a.whole_codes, t + j * NT < NU);
             if constexpr (SHIFT)
                 if (cx >= 0) out[cx - hd] = (uint8_t)e4m3_pair(xv * sc.y, 0.f);
             if (t == 0) a.scale[row] = sc.x;
         } else if constexpr (SHIFT) {
+            auto scale_of = [&](int g) { return q8_scale(__uint_as_float(s_group[buf][g]), r); };
+            float by[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int u = t + j * NT;
-                if (u < NU) {
-                    const float by = q8_scale(s_group[buf][u / run], r).y;
-                    if ((u & (run - 1)) == run - 1 && hd) {
-                        const float next = q8_scale(s_group[buf][u / run + 1], r).y;
+            for (int j = 0; j < V; ++j) by[j] = t + j * NT < NU ? scale_of((t + j * NT) >> run_shift).y : 0.f;
+            if (crosses) {
 #pragma unroll
-                        for (int e = 0; e < E; ++e) v[j][e] *= e < E - hd ? by : next;
-                        store_codes<E>(out + u * E, v[j], 1.f, a.whole_codes);
-                    } else {
-                        store_codes<E>(out + u * E, v[j], by, a.whole_codes);
+                for (int j = 0; j < V; ++j)
+                    if (t + j * NT < NU) {
+                        const float next = scale_of(((t + j * NT) >> run_shift) + 1).y;
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            float &x = e & 1 ? v[j][e / 2].y : v[j][e / 2].x;
+                            x *= e < E - hd ? by[j] : next;
+                        }
+                        by[j] = 1.f;
                     }
-                }
             }
-            if (cx >= 0) out[cx - hd] = (uint8_t)e4m3_pair(xv * q8_scale(s_group[buf][cx >> a.group_shift], r).y, 0.f);
-            for (int g = t; g < a.groups; g += NT) {
-                a.scale[row * a.groups + g] = q8_scale(s_group[buf][g], r).x;
-            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) store_codes(out + (t + j * NT) * E, v[j], by[j], a.whole_codes, t + j * NT < NU);
+            if (cx >= 0) out[cx - hd] = (uint8_t)e4m3_pair(xv * scale_of(cx >> a.group_shift).y, 0.f);
+            for (int g = t; g < a.groups; g += NT) a.scale[row * a.groups + g] = scale_of(g).x;
             // The buffer of two rows on was last read before this row's barrier, and is
             // next added to behind the next row's.
             const int far = buf == 0 ? 2 : buf - 1;
             for (int g = t; g <= a.groups; g += NT) s_group[far][g] = 0;
             buf = buf == 2 ? 0 : buf + 1;
-        } else {
+        } else if ((t & (run - 1)) == 0) {
+            float *scale = a.scale + row * a.groups;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int u = t + j * NT;
-                if (u < NU && (u & (run - 1)) == 0) a.scale[row * a.groups + u / run] = q8_scale(part[j], r).x;
-            }
+            for (int j = 0; j < V; ++j)
+                if (t + j * NT < NU) scale[(t + j * NT) >> run_shift] = q8_scale(part[j], r).x;
         }
         if constexpr (STAGED)
             if (++s == a.stages) {
                 s = 0;
                 ph ^= 1u;
             }
-        if constexpr (!STAGED)
-            if (row + step < a.rows) fetch_global(row + step);
     }
 }
 
 // One row a warp, V units a lane.
 template <typename T, bool RES, int V>
 __global__ void __launch_bounds__(Q8_WARP_NT, 2) q8_warp_kernel(const __grid_constant__ Q8Args a) {
-    constexpr int E = vec_elems<T>();
+    constexpr int E = vec_elems<T>(), P = vec_pairs<T>();
     const int lane = threadIdx.x & 31, NU = a.D / E;
     const float inv_D = 1.0f / (float)a.D;
     const bool grouped = a.group != 0;
-    const int run = grouped ? a.group / E : 32;
+    const int run = grouped ? a.group / E : 32, run_shift = 31 - __clz(run);
     const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
     griddep_wait();
     griddep_launch_dependents();
-    uint4 vx[V], vr[RES ? V : 1], vw[V];
-    auto fetch = [&](int64_t row) {
+    uint4 vx[V], vr[RES ? V : 1];
+    float2 w[V][P];
+    auto fetch = [&](int64_t row) {  // units past the row are zeros
         const uint4 *px = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + row * a.ld_x);
         const uint4 *pr = RES ? reinterpret_cast<const uint4 *>(static_cast<const T *>(a.res) + row * a.ld_res) : nullptr;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int u = lane + 32 * j;
+            vx[j] = make_uint4(0, 0, 0, 0);
+            if constexpr (RES) vr[j] = make_uint4(0, 0, 0, 0);
             if (u < NU) {
                 vx[j] = ld_stream(px + u);
                 if constexpr (RES) vr[j] = ld_stream(pr + u);
@@ -326,57 +345,57 @@ __global__ void __launch_bounds__(Q8_WARP_NT, 2) q8_warp_kernel(const __grid_con
     int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     if (row < a.rows) fetch(row);
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (lane + 32 * j < NU) vw[j] = __ldg(static_cast<const uint4 *>(a.w) + lane + 32 * j);
+    for (int j = 0; j < V; ++j) {
+        const uint4 c = lane + 32 * j < NU ? __ldg(static_cast<const uint4 *>(a.w) + lane + 32 * j) : make_uint4(0, 0, 0, 0);
+        unpack_vec<T>(c, w[j]);
+#pragma unroll
+        for (int m = 0; m < P; ++m) w[j][m] = f2add(w[j][m], make_float2(a.weight_bias, a.weight_bias));
+    }
     for (; row < a.rows; row += step) {
-        float v[V][E], ss = 0.f;
-        uint32_t top = 0, part[V];
+        float2 v[V][P], s2 = make_float2(0.f, 0.f);
+        float part[V], top = 0.f;
         uint4 *nres = RES ? reinterpret_cast<uint4 *>(static_cast<T *>(a.nres) + row * a.ld_nres) : nullptr;
         uint8_t *out = static_cast<uint8_t *>(a.out) + row * a.ld_out;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int u = lane + 32 * j;
-            part[j] = 0;
-            if (u < NU) {
-                unpack_vec<T>(vx[j], v[j]);
-                if constexpr (RES) {
-                    float r[E];
-                    unpack_vec<T>(vr[j], r);
+            unpack_vec<T>(vx[j], v[j]);
+            if constexpr (RES) {
+                float2 r[P];
+                unpack_vec<T>(vr[j], r);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) v[j][e] += r[e];
-                }
+                for (int m = 0; m < P; ++m) v[j][m] = f2add(v[j][m], r[m]);
             }
         }
-        // The next row may be this one's new residual's neighbour, never the same.
-        if (row + step < a.rows) fetch(row + step);
+        if (row + step < a.rows) fetch(row + step);  // (another row: nothing this one writes)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int u = lane + 32 * j;
-            if (u < NU) {
-                float w[E];
-                if constexpr (RES) nres[u] = pack_vec<T>(v[j]);
-                unpack_vec<T>(vw[j], w);
+            if constexpr (RES)
+                if (lane + 32 * j < NU) nres[lane + 32 * j] = pack_vec<T>(v[j]);
+            part[j] = 0.f;
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    ss = fmaf(v[j][e], v[j][e], ss);
-                    v[j][e] *= a.weight_bias + w[e];
-                    part[j] = max(part[j], magnitude(v[j][e]));
-                }
+            for (int m = 0; m < P; ++m) {
+                s2 = f2fma(v[j][m], v[j][m], s2);
+                v[j][m] = f2mul(v[j][m], w[j][m]);
+                part[j] = max_abs(part[j], v[j][m].x, v[j][m].y);
             }
-            top = max(top, part[j]);
+            top = max_abs(top, part[j]);
         }
-        const float r = rsqrtf(group_sum<32>(ss) * inv_D + a.eps);
-        const float2 whole = grouped ? make_float2(0.f, 0.f) : q8_scale(__reduce_max_sync(0xffffffffu, top), r);
+        const float r = rsqrtf(group_sum<32>(s2.x + s2.y) * inv_D + a.eps);
+        if (grouped) {
+            run_maxima(part, run);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int u = lane + 32 * j;
-            const float2 sc = grouped ? q8_scale(run_max(part[j], run), r) : whole;
-            if (u < NU) {
-                store_codes<E>(out + u * E, v[j], sc.y, a.whole_codes);
-                if (grouped && (u & (run - 1)) == 0) a.scale[row * a.groups + u / run] = sc.x;
+            for (int j = 0; j < V; ++j) {
+                const int u = lane + 32 * j;
+                const float2 sc = q8_scale(part[j], r);
+                store_codes(out + u * E, v[j], sc.y, a.whole_codes, u < NU);
+                if (u < NU && (u & (run - 1)) == 0) a.scale[row * a.groups + (u >> run_shift)] = sc.x;
             }
+        } else {
+            const float2 sc = q8_scale(warp_max(top), r);
+#pragma unroll
+            for (int j = 0; j < V; ++j) store_codes(out + (lane + 32 * j) * E, v[j], sc.y, a.whole_codes, lane + 32 * j < NU);
+            if (lane == 0) a.scale[row] = sc.x;
         }
-        if (!grouped && lane == 0) a.scale[row] = whole.x;
     }
 }
 
@@ -386,7 +405,7 @@ template <typename T, bool RES>
 __global__ void __launch_bounds__(Q8_GENERIC_NT) q8_generic_kernel(const Q8Args a) {
     constexpr int NW = Q8_GENERIC_NT / 32;
     __shared__ float s_sum[NW];
-    __shared__ uint32_t s_top[NW];
+    __shared__ float s_top[NW];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const T *w = static_cast<const T *>(a.w);
     griddep_wait();
@@ -398,18 +417,18 @@ __global__ void __launch_bounds__(Q8_GENERIC_NT) q8_generic_kernel(const Q8Args 
         auto weight = [&](int j) { return a.weight_bias + Cvt<T>::load1(w + j); };
         // a sum of sums of 64, so that rounding grows with neither length alone
         float ss = 0.f;
-        uint32_t top = 0;
+        float top = 0.f;
         for (int j0 = threadIdx.x; j0 < a.D; j0 += 64 * Q8_GENERIC_NT) {
             float part = 0.f;
             for (int i = 0, j = j0; i < 64 && j < a.D; ++i, j += Q8_GENERIC_NT) {
                 const float h = h_of(j);
                 part = fmaf(h, h, part);
-                if (!a.group) top = max(top, magnitude(h * weight(j)));
+                if (!a.group) top = max_abs(top, h * weight(j));
             }
             ss += part;
         }
         ss = group_sum<32>(ss);
-        top = __reduce_max_sync(0xffffffffu, top);
+        top = warp_max(top);
         __syncthreads();  // the row before has been read
         if (lane == 0) {
             s_sum[warp] = ss;
@@ -425,28 +444,114 @@ __global__ void __launch_bounds__(Q8_GENERIC_NT) q8_generic_kernel(const Q8Args 
             if (RES) Cvt<T>::store1(nres + j, h);
         };
         if (!a.group) {
-            top = __reduce_max_sync(0xffffffffu, lane < NW ? s_top[lane] : 0u);
+            top = warp_max(lane < NW ? s_top[lane] : 0.f);
             const float2 s = q8_scale(top, r);
             for (int j = threadIdx.x; j < a.D; j += Q8_GENERIC_NT) write(j, h_of(j), s.y);
             if (threadIdx.x == 0) a.scale[row] = s.x;
         } else {
             for (int g = warp; g < a.groups; g += NW) {
                 float h[4];
-                uint32_t t = 0;
+                float t = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = g * a.group + 32 * i + lane;
                     const bool in = 32 * i < a.group && j < a.D;
                     h[i] = in ? h_of(j) : 0.f;
-                    if (in) t = max(t, magnitude(h[i] * weight(j)));
+                    if (in) t = max_abs(t, h[i] * weight(j));
                 }
-                const float2 s = q8_scale(__reduce_max_sync(0xffffffffu, t), r);
+                const float2 s = q8_scale(warp_max(t), r);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = g * a.group + 32 * i + lane;
                     if (32 * i < a.group && j < a.D) write(j, h[i], s.y);
                 }
                 if (lane == 0) a.scale[row * a.groups + g] = s.x;
+            }
+        }
+    }
+}
+
+// Rows too long for registers, on 16-byte boundaries: read twice, the second time from
+// L2, in 16-byte units.
+template <typename T, bool RES>
+__global__ void __launch_bounds__(Q8_GENERIC_NT, 2) q8_long_kernel(const __grid_constant__ Q8Args a) {
+    constexpr int E = vec_elems<T>(), P = vec_pairs<T>(), NT = Q8_GENERIC_NT, NW = NT / 32, V = 4;
+    __shared__ float2 s_row[2][NW];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, NU = a.D / E;
+    const bool grouped = a.group != 0;
+    const int run = grouped ? a.group / E : 32, run_shift = 31 - __clz(run);
+    const uint4 *w = static_cast<const uint4 *>(a.w);
+    griddep_wait();
+    griddep_launch_dependents();
+    int side = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + row * a.ld_x);
+        const uint4 *res = RES ? reinterpret_cast<const uint4 *>(static_cast<const T *>(a.res) + row * a.ld_res) : nullptr;
+        uint4 *nres = RES ? reinterpret_cast<uint4 *>(static_cast<T *>(a.nres) + row * a.ld_nres) : nullptr;
+        uint8_t *out = static_cast<uint8_t *>(a.out) + row * a.ld_out;
+        // h and h w' of unit u, zeros past the row
+        auto load = [&](int u, float2 (&h)[P], float2 (&v)[P]) {
+            uint4 cx = make_uint4(0, 0, 0, 0), cr = cx, cw = cx;
+            if (u < NU) {
+                cx = x[u];
+                if constexpr (RES) cr = res[u];
+                cw = __ldg(w + u);
+            }
+            float2 r[P];
+            unpack_vec<T>(cx, h);
+            unpack_vec<T>(cw, v);
+            if constexpr (RES) unpack_vec<T>(cr, r);
+#pragma unroll
+            for (int m = 0; m < P; ++m) {
+                if constexpr (RES) h[m] = f2add(h[m], r[m]);
+                v[m] = f2mul(h[m], f2add(v[m], make_float2(a.weight_bias, a.weight_bias)));
+            }
+        };
+        float ss = 0.f, top = 0.f;
+        for (int u0 = t; u0 < NU; u0 += V * NT) {
+            float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float2 h[P], v[P];
+                load(u0 + j * NT, h, v);
+#pragma unroll
+                for (int m = 0; m < P; ++m) {
+                    s2 = f2fma(h[m], h[m], s2);
+                    top = max_abs(top, v[m].x, v[m].y);
+                }
+            }
+            ss += s2.x + s2.y;
+        }
+        ss = group_sum<32>(ss);
+        top = warp_max(top);
+        if (lane == 0) s_row[side][warp] = make_float2(ss, top);
+        __syncthreads();
+        const float2 mine = s_row[side][lane & (NW - 1)];
+        side ^= 1;
+        const float r = rsqrtf(group_sum<NW>(mine.x) * (1.0f / (float)a.D) + a.eps);
+        const float2 whole = q8_scale(run_max(mine.y, NW), r);
+        if (!grouped && t == 0) a.scale[row] = whole.x;
+        for (int u0 = t - lane; u0 < NU; u0 += V * NT) {  // the same in a warp's lanes
+            float2 v[V][P];
+            float part[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int u = u0 + lane + j * NT;
+                float2 h[P];
+                load(u, h, v[j]);
+                if constexpr (RES)
+                    if (u < NU) nres[u] = pack_vec<T>(h);
+                part[j] = 0.f;
+#pragma unroll
+                for (int m = 0; m < P; ++m) part[j] = max_abs(part[j], v[j][m].x, v[j][m].y);
+            }
+            if (grouped) run_maxima(part, run);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int u = u0 + lane + j * NT;
+                const float2 sc = grouped ? q8_scale(part[j], r) : whole;
+                store_codes(out + (int64_t)u * E, v[j], sc.y, a.whole_codes, u < NU);
+                if (grouped && u < NU && (u & (run - 1)) == 0) a.scale[row * a.groups + (u >> run_shift)] = sc.x;
             }
         }
     }
@@ -469,13 +574,14 @@ cudaError_t launch_q8_cta(const Q8Plan &p, const Q8Args &a, cudaStream_t s) {
     if (p.kind == Q8_DIRECT)
         return p.units == 1 ? launch_q8_row<T, RES, SHIFT, false, 1, 512, 2>(p, a, s)
                             : launch_q8_row<T, RES, SHIFT, false, 2, 1024, 1>(p, a, s);
-    if (p.threads <= 256) return launch_q8_row<T, RES, SHIFT, true, 2, 256, 4>(p, a, s);
-    if (p.threads <= 512) return launch_q8_row<T, RES, SHIFT, true, 2, 512, 2>(p, a, s);
-    return launch_q8_row<T, RES, SHIFT, true, 2, 1024, 1>(p, a, s);
+    if (p.threads <= 128) return launch_q8_row<T, RES, SHIFT, true, Q8_UNITS, 128, 4>(p, a, s);
+    if (p.threads <= 256) return launch_q8_row<T, RES, SHIFT, true, Q8_UNITS, 256, 2>(p, a, s);
+    return launch_q8_row<T, RES, SHIFT, true, Q8_UNITS, 512, 1>(p, a, s);
 }
 
 template <typename T, bool RES> cudaError_t launch_q8_kind(const Q8Plan &p, const Q8Args &a, cudaStream_t s) {
     if (p.kind == Q8_GENERIC) return launch_pdl(q8_generic_kernel<T, RES>, dim3(p.grid), dim3(p.threads), 0, s, a);
+    if (p.kind == Q8_LONG) return launch_pdl(q8_long_kernel<T, RES>, dim3(p.grid), dim3(p.threads), 0, s, a);
     if (p.kind == Q8_WARP)
         return launch_pdl(p.units == 1   ? q8_warp_kernel<T, RES, 1>
                           : p.units == 2 ? q8_warp_kernel<T, RES, 2>

@@ -17,9 +17,42 @@ template <int FMT> __host__ __device__ constexpr float top_code() { return FMT =
 // normal numbers whatever the group holds.
 template <int FMT> __host__ __device__ constexpr float least_top() { return top_code<FMT>() * 0x1p-126f; }
 
-// Magnitudes as the bits of their floats, which order as integers do; NaN is above
-// infinity, so a group's maximum keeps it.
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// The largest magnitude among a group: NaN if any value is.
+__device__ __forceinline__ float max_abs(float top, float a, float b) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(top), "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_abs(float top, float a) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(top), "f"(fabsf(a)));
+    return r;
+}
+// Over all lanes of a warp, and over aligned runs of n lanes (a power of two).
+__device__ __forceinline__ float warp_max(float top) {
+    float r;
+    asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(top));
+    return r;
+}
+__device__ __forceinline__ float run_max(float top, int n) {
+    for (int off = 1; off < n; off *= 2) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, off));
+    return top;
+}
+
+// The magnitude that a group's scale is made from.
+template <int FMT> __device__ __forceinline__ float scaled_top(float top) { return max_abs(least_top<FMT>(), top); }
+
+// top_code / a for such an a, to 2^-24: an approximate reciprocal and one step of Newton's
+// correction of the quotient, on a brought down by a power of two so that neither a nor
+// its reciprocal leaves the normal numbers.  NaN for a that is not finite.
+template <int FMT> __device__ __forceinline__ float code_factor(float a) {
+    constexpr float down = FMT == RMSNORM_CACHE_I8 ? 1.f / 64.f : 1.f / 256.f, n = top_code<FMT>() * down;
+    const float x = a * down;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    const float q = n * r;
+    return fmaf(fmaf(-q, x, n), r, q);
+}
 
 // Two values, times their scale's inverse already, as the codes' bytes (the first in
 // the low byte), to nearest even.  e4m3: beyond 448 saturates, NaN stays NaN.
