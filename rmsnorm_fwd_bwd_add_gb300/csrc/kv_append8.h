@@ -12,14 +12,15 @@ template <typename T> cudaError_t launch_append8(const AppendArgs &a, int format
 
 template <typename T, int VB, bool INTERLEAVED, int FMT, int UPL>
 cudaError_t launch_append8_units(const AppendArgs &a, int lanes, int sm, cudaStream_t s) {
-    const RopePlan p = make_append8_plan(a.T, (lanes + UPL - 1) / UPL, a.Hq + 2 * a.Hkv, C8_UNITS_IN_FLIGHT / UPL,
+    const RopePlan p = make_append8_plan(a.T, (lanes + UPL - 1) / UPL, a.Hq + 2 * a.Hkv, append8_batch<UPL>(),
                                          sm * append8_ctas<VB / (int)sizeof(T), UPL>(), C8_NT / 32);
-    return launch_pdl(append8_kernel<T, VB, INTERLEAVED, FMT, UPL>, dim3(p.grid), dim3(C8_NT), 0, s, a, p.whole, p.wpt, p.cw);
+    return launch_pdl(append8_kernel<T, VB, INTERLEAVED, FMT, UPL>, dim3(p.grid), dim3(C8_NT),
+                      (size_t)(C8_NT / 32) * 2 * append8_plane(a.rot) * sizeof(float), s, a, p.whole, p.wpt, p.cw);
 }
 
 template <typename T, bool INTERLEAVED, int FMT>
 cudaError_t launch_append8_layout(const AppendArgs &a, int unit, int sm, cudaStream_t s) {
-    auto lanes_of = [&](auto ve) { return HeadMap<decltype(ve)::value, INTERLEAVED, INTERLEAVED>(a.Dh, a.rot).lanes; };
+    auto lanes_of = [&](auto ve) { return HeadMap<decltype(ve)::value, (INTERLEAVED && decltype(ve)::value > 1), INTERLEAVED>(a.Dh, a.rot).lanes; };
     if (unit == 16) {
         const int lanes = lanes_of(std::integral_constant<int, 16 / (int)sizeof(T)>{});
         if (lanes <= 32) return launch_append8_units<T, 16, INTERLEAVED, FMT, 1>(a, lanes, sm, s);
@@ -33,6 +34,11 @@ cudaError_t launch_append8_layout(const AppendArgs &a, int unit, int sm, cudaStr
             if (lanes <= 64) return launch_append8_units<T, 4, INTERLEAVED, FMT, 2>(a, lanes, sm, s);
             if (lanes <= 128) return launch_append8_units<T, 4, INTERLEAVED, FMT, 4>(a, lanes, sm, s);
         }
+    const int lanes = lanes_of(std::integral_constant<int, 1>{});
+    constexpr int VB = (int)sizeof(T);
+    if (lanes <= 32) return launch_append8_units<T, VB, INTERLEAVED, FMT, 1>(a, lanes, sm, s);
+    if (lanes <= 64) return launch_append8_units<T, VB, INTERLEAVED, FMT, 2>(a, lanes, sm, s);
+    if (lanes <= 128) return launch_append8_units<T, VB, INTERLEAVED, FMT, 4>(a, lanes, sm, s);
     const int64_t warps = a.T * (a.Hq + 2 * (int64_t)a.Hkv);
     const dim3 grid((unsigned)std::min<int64_t>((warps + C8_NT / 32 - 1) / (C8_NT / 32), 8 * (int64_t)sm));
     return launch_pdl(append8_generic_kernel<T, FMT, INTERLEAVED>, grid, dim3(C8_NT), 0, s, a);

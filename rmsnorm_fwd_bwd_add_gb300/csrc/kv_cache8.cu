@@ -40,10 +40,11 @@ bool hits(const Span &a, const void *p, size_t n) {
 }
 
 template <typename T, int FMT, int C> cudaError_t launch_read_units(const ReadArgs &a, int sm, cudaStream_t s) {
-    // as many parts a token as there are warps for, and units for
-    const int64_t warps = (int64_t)sm * R8_CTAS_PER_SM * (C8_NT / 32), units = (int64_t)2 * a.Hkv * (a.Dh / C);
+    // as many parts a token as there are warps for, and heads for
+    const int64_t warps = (int64_t)sm * R8_CTAS_PER_SM * (C8_NT / 32);
+    const int hpi = 32 / read8_lanes(a.Dh / C);
     int wpt = 1;
-    while (wpt < 64 && 2 * wpt * a.T <= warps && wpt * 32 < units) wpt *= 2;
+    while (wpt < 64 && 2 * wpt * a.T <= warps && wpt * hpi < a.Hkv) wpt *= 2;
     const int64_t ctas = (a.T * wpt + C8_NT / 32 - 1) / (C8_NT / 32);
     return launch_pdl(read8_kernel<T, FMT, C>, dim3((unsigned)std::min<int64_t>(ctas, sm * R8_CTAS_PER_SM)), dim3(C8_NT), 0,
                       s, a, wpt);
@@ -52,9 +53,9 @@ template <typename T, int FMT, int C> cudaError_t launch_read_units(const ReadAr
 // unit: codes that divide every address, stride and head of the caches, and in
 // elements those of the outputs.
 template <typename T, int FMT> cudaError_t launch_read(const ReadArgs &a, int unit, int sm, cudaStream_t s) {
-    return unit == 16  ? launch_read_units<T, FMT, 16>(a, sm, s)
-           : unit == 8 ? launch_read_units<T, FMT, 8>(a, sm, s)
-           : unit == 4 ? launch_read_units<T, FMT, 4>(a, sm, s)
+    if constexpr (sizeof(T) == 2)
+        if (unit == 8) return launch_read_units<T, FMT, 8>(a, sm, s);
+    return unit >= 4   ? launch_read_units<T, FMT, 4>(a, sm, s)
            : unit == 2 ? launch_read_units<T, FMT, 2>(a, sm, s)
                        : launch_read_units<T, FMT, 1>(a, sm, s);
 }
@@ -196,7 +197,7 @@ extern "C" int rmsnorm_kv_read(const void *k_cache, const int64_t *k_cache_strid
     uintptr_t bits = (uintptr_t)Dh | byte_bits(hk, 1, num_slots, Hkv, 1) | byte_bits(hv, 1, num_slots, Hkv, 1);
     const uintptr_t out_bits = byte_bits(hko, 1, T, Hkv, es) | byte_bits(hvo, 1, T, Hkv, es);
     bits |= out_bits % 16 == 0 ? 0 : out_bits / es;
-    const int unit = bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
+    const int unit = bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
     const cudaError_t e = by_type(dtype, cache_format, [&](auto t, auto f) {
         return launch_read<typename decltype(t)::type, decltype(f)::value>(a, unit, sm, static_cast<cudaStream_t>(stream));
     });

@@ -24,51 +24,92 @@ template <int VE> struct CodeWord;
 template <> struct CodeWord<8> { using type = uint2; };
 template <> struct CodeWord<4> { using type = uint32_t; };
 template <> struct CodeWord<2> { using type = uint16_t; };
+template <> struct CodeWord<1> { using type = uint8_t; };
 
 template <int FMT, int VE> __device__ __forceinline__ typename CodeWord<VE>::type code_word(const float (&f)[VE], float by) {
-    if constexpr (VE == 8) {
-        return make_uint2(code_quad<FMT>(f[0] * by, f[1] * by, f[2] * by, f[3] * by),
-                          code_quad<FMT>(f[4] * by, f[5] * by, f[6] * by, f[7] * by));
-    } else if constexpr (VE == 4) {
-        return code_quad<FMT>(f[0] * by, f[1] * by, f[2] * by, f[3] * by);
+    if constexpr (VE >= 4) {
+        uint32_t c[VE / 4];
+#pragma unroll
+        for (int i = 0; i < VE / 4; ++i) {
+            const float2 x = f2mul(make_float2(f[4 * i], f[4 * i + 1]), make_float2(by, by));
+            const float2 y = f2mul(make_float2(f[4 * i + 2], f[4 * i + 3]), make_float2(by, by));
+            c[i] = code_quad<FMT>(x.x, x.y, y.x, y.y);
+        }
+        if constexpr (VE == 8) return make_uint2(c[0], c[1]);
+        else return c[0];
     } else {
-        return (uint16_t)code_pair<FMT>(f[0] * by, f[1] * by);
+        return (typename CodeWord<VE>::type)code_pair<FMT>(f[0] * by, VE == 2 ? f[VE - 1] * by : 0.f);
     }
 }
 
 template <typename T, int VB, int VE> __device__ __forceinline__ void unpack_raw(const typename RawUnit<VB>::type &v, float (&f)[VE]) {
-    if constexpr (VB == 16) {
-        unpack_vec<T>(v, f);
-    } else {
+    if constexpr (VE == 2) {
         const float2 p = Cvt<T>::unpack2(v);
         f[0] = p.x;
         f[1] = p.y;
+    } else {
+        unpack_unit<T, VB>(v, f);
     }
 }
 template <typename T, int VB, int VE> __device__ __forceinline__ typename RawUnit<VB>::type pack_raw(const float (&f)[VE]) {
-    if constexpr (VB == 16) return pack_vec<T>(f);
-    else return Cvt<T>::pack2(f[0], f[1]);
+    if constexpr (VE == 2) return Cvt<T>::pack2(f[0], f[1]);
+    else return pack_unit<T, VB>(f);
+}
+
+// VE floats from shared memory, at a multiple of their number.
+template <int VE> __device__ __forceinline__ void load_floats(const float *p, float (&f)[VE]) {
+    if constexpr (VE >= 4) {
+#pragma unroll
+        for (int i = 0; i < VE / 4; ++i) {
+            const float4 v = reinterpret_cast<const float4 *>(p)[i];
+            f[4 * i] = v.x;
+            f[4 * i + 1] = v.y;
+            f[4 * i + 2] = v.z;
+            f[4 * i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) f[i] = p[i];
+    }
 }
 
 // Units of a head a lane holds at a time, over all heads in flight.
-constexpr int C8_UNITS_IN_FLIGHT = 4;
+#ifndef XUNITS
+#define XUNITS 4
+#endif
+constexpr int C8_UNITS_IN_FLIGHT = XUNITS;
 
-// CTAs an SM holds: long heads need twice the registers for their cosines and sines.
-template <int VE, int UPL> __host__ __device__ constexpr int append8_ctas() { return VE * UPL > 8 ? 1 : 2; }
+// Steps of heads in one of the two batches that a warp has in flight.
+template <int UPL> __host__ __device__ constexpr int append8_batch() { return UPL < C8_UNITS_IN_FLIGHT / 2 ? C8_UNITS_IN_FLIGHT / 2 / UPL : 1; }
+
+// CTAs an SM holds: long heads need more registers.
+template <int VE, int UPL> __host__ __device__ constexpr int append8_ctas() { return
+#ifdef XCTAS
+ XCTAS;
+#else
+ 2;
+#endif
+ }
+
+// Shared memory of a warp: the cosines, then the sines of a token's pairs.
+__host__ __device__ constexpr int append8_plane(int rot) { return (rot / 2 + 3) / 4 * 4; }
 
 // A warp takes a token (or one of a token's `wpt` parts, from token `whole` on), 32 / cw
 // heads at a time: cw lanes a head, UPL units of two vectors each a lane (rope_ex.cuh's
-// units), so that a head's largest value is a few shuffles away.  The cosines and sines
-// of a lane's pairs are computed once for all of its heads.
+// units), so that a head's largest value is a few shuffles away.  The token's cosines and
+// sines are computed by the warp's lanes together, once for all of its heads, to fp32's
+// precision: the SFU's (2^-21) would move values across the codes' borders.
 template <typename T, int VB, bool INTERLEAVED, int FMT, int UPL>
 __global__ void __launch_bounds__(C8_NT, (append8_ctas<VB / (int)sizeof(T), UPL>())) append8_kernel(const __grid_constant__ AppendArgs a, int64_t whole, int wpt, int cw) {
     using V = typename RawUnit<VB>::type;
-    constexpr int VE = VB / (int)sizeof(T), HB = C8_UNITS_IN_FLIGHT / UPL;
-    constexpr bool PAIRED = INTERLEAVED;  // VE > 1
+    constexpr int VE = VB / (int)sizeof(T), HB = append8_batch<UPL>();
+    constexpr bool PAIRED = INTERLEAVED && VE > 1;
     using Codes = typename CodeWord<VE>::type;
+    extern __shared__ __align__(16) float s_turn[];
+    const int lane = threadIdx.x & 31, half = a.rot / 2, plane = append8_plane(a.rot);
+    float *s_cos = s_turn + (threadIdx.x >> 5) * 2 * plane, *s_sin = s_cos + plane;
     __shared__ float2 s_turns[RX_MAX_DH / 2];
     __shared__ uint8_t s_axis[RX_MAX_DH / 2];
-    const int half = a.rot / 2;
     for (int i = threadIdx.x; i < half; i += C8_NT) {
         s_turns[i] = a.turns[i];
         s_axis[i] = a.axes.of[i];
@@ -77,10 +118,8 @@ __global__ void __launch_bounds__(C8_NT, (append8_ctas<VB / (int)sizeof(T), UPL>
     griddep_wait();
     griddep_launch_dependents();
 
-    const int lane = threadIdx.x & 31, hpi = 32 / cw, hs = lane / cw, lu = lane - hs * cw;
+    const int hpi = 32 / cw, hs = lane / cw, lu = lane - hs * cw;
     const HeadMap<VE, PAIRED, INTERLEAVED> map(a.Dh, a.rot), v_map(a.Dh, 0);
-    const bool q_moves = a.q_out.p != a.q.p;  // in place: nothing to copy
-    const int n_qk = a.Hq + a.Hkv, n_all = n_qk + a.Hkv;
     // unit i of this lane: first elements of its two vectors in a head of q or k, and of v
     int ia[UPL], ib[UPL], va[UPL], vb[UPL];
     uint32_t in = 0, two = 0, turns = 0, v_in = 0, v_two = 0;  // a bit a unit
@@ -89,153 +128,207 @@ __global__ void __launch_bounds__(C8_NT, (append8_ctas<VB / (int)sizeof(T), UPL>
         const int l = lu + i * cw;
         bool w;
         map.at(l, ia[i], ib[i], w);
-        if (l < map.lanes) in |= 1u << i, two |= (uint32_t)w << i;
+        if (hs < hpi && l < map.lanes) in |= 1u << i, two |= (uint32_t)w << i;
         if (l < map.rot_units) turns |= 1u << i;
         v_map.at(l, va[i], vb[i], w);
-        if (l < v_map.lanes) v_in |= 1u << i, v_two |= (uint32_t)w << i;
+        if (hs < hpi && l < v_map.lanes) v_in |= 1u << i, v_two |= (uint32_t)w << i;
     }
+    turns &= in;
+    const uint32_t q_in = a.q_out.p != a.q.p ? in : turns;  // in place: nothing to copy
+    // the largest of a head's cw lanes: butterflies, or turns of 1, 2, 4, ... lanes around
+    // them (counting some twice does no harm)
+    const bool square = (cw & (cw - 1)) == 0;
+    auto head_max = [&](float top) {
+        if (square) return run_max(top, cw);
+        for (int off = 1; off < cw; off *= 2) {
+            const int at = lu + off;
+            top = max_abs(top, __shfl_sync(0xffffffffu, top, hs < hpi ? lane - lu + (at < cw ? at : at - cw) : lane));
+        }
+        return top;
+    };
     const int64_t n_items = whole + (a.T - whole) * wpt, n_warps = (int64_t)gridDim.x * (C8_NT / 32);
     const int wshift = 31 - __clz(wpt);  // wpt is a power of two
     int64_t w = ((int64_t)blockIdx.x * C8_NT + threadIdx.x) >> 5;
-    int64_t p_next[RX_MAX_AXES] = {}, slot_next = 0;  // of the item ahead
-    auto token_of = [&](int64_t item) { return item < whole ? item : whole + ((item - whole) >> wshift); };
-    auto look_ahead = [&](int64_t item) {
-        if (item < n_items) {
-            const int64_t t = token_of(item);
-            slot_next = a.slots[t];
+    // An item: a token, or part `part` of `parts` of one; its steps of 32 / cw heads, those
+    // of q, then of k, then of v.
+    struct Item {
+        int64_t t;
+        int part, parts, nq, nk;
+    };
+    auto item_of = [&](int64_t i) {
+        Item it;
+        it.t = i < whole ? i : whole + ((i - whole) >> wshift);
+        it.parts = i < whole ? 1 : wpt;
+        it.part = i < whole ? 0 : (int)((i - whole) & (wpt - 1));
+        const int step = it.parts * hpi, from = it.part * hpi;
+        it.nq = a.Hq > from ? (a.Hq - from + step - 1) / step : 0;
+        it.nk = a.Hkv > from ? (a.Hkv - from + step - 1) / step : 0;
+        return it;
+    };
+    // Loads steps s0 .. s0 + HB - 1 of an item.
+    auto load = [&](V (&xa)[HB][UPL], V (&xb)[HB][UPL], const Item &it, int s0) {
 #pragma unroll
-            for (int x = 0; x < RX_MAX_AXES; ++x)
-                if (x < a.axes.n) p_next[x] = a.positions[x * a.T + t];
+        for (int j = 0; j < HB; ++j) {
+            const int s = s0 + j;
+            if (s >= it.nq + 2 * it.nk) break;
+            const bool is_q = s < it.nq, is_v = s >= it.nq + it.nk;
+            const int h = ((s - (is_q ? 0 : is_v ? it.nq + it.nk : it.nq)) * it.parts + it.part) * hpi + hs;
+            const Heads &x = is_q ? a.q : is_v ? a.v : a.k;
+            const uint32_t wanted = is_q ? q_in : is_v ? v_in : in, both = is_v ? v_two : two;
+            if (h < (is_q ? a.Hq : a.Hkv)) {
+                const T *src = reinterpret_cast<const T *>((const unsigned char *)x.p + (it.t * x.st * (int64_t)sizeof(T) + (uint64_t)(uint32_t)h * x.head_bytes));
+#pragma unroll
+                for (int i = 0; i < UPL; ++i) {
+                    if (wanted >> i & 1) xa[j][i] = *reinterpret_cast<const V *>(src + (is_v ? va[i] : ia[i]));
+                    if (wanted & both & 1u << i) xb[j][i] = *reinterpret_cast<const V *>(src + (is_v ? vb[i] : ib[i]));
+                }
+            }
         }
     };
-    look_ahead(w);
+    int64_t p_next = 0, slot_next = 0;  // of the item ahead; lane x has its position on axis x
+    auto look_ahead = [&](int64_t t) {
+        slot_next = a.slots[t];
+        if (lane < a.axes.n) p_next = a.positions[lane * a.T + t];
+    };
+    V xa0[HB][UPL], xb0[HB][UPL], xa1[HB][UPL], xb1[HB][UPL];  // two batches of steps
+    Item it{};
+    if (w < n_items) {
+        it = item_of(w);
+        load(xa0, xb0, it, 0);
+        look_ahead(it.t);
+    }
     for (; w < n_items; w += n_warps) {
-        const int64_t t = token_of(w), slot = slot_next;
-        float2 pos[RX_MAX_AXES];
-        bool pos_ok = true;
-#pragma unroll
-        for (int x = 0; x < RX_MAX_AXES; ++x) {
-            pos[x] = split_position(p_next[x]);
-            pos_ok = pos_ok && p_next[x] >= 0;
+        const int64_t t = it.t, slot = slot_next;
+        const float2 mine = split_position(p_next);
+        const bool pos_ok = __all_sync(0xffffffffu, p_next >= 0);
+        const Item now = it;
+        const bool more = w + n_warps < n_items;
+        if (more) {
+            it = item_of(w + n_warps);
+            look_ahead(it.t);
         }
-        const int parts = w < whole ? 1 : wpt, part = w < whole ? 0 : (int)((w - whole) & (wpt - 1));
-        look_ahead(w + n_warps);
-        const bool slot_ok = slot < a.num_slots;
-        if ((!pos_ok || !slot_ok) && lane == 0 && part == 0) atomicOr(a.status, BAD_INDEX);
-        if (!pos_ok) continue;
-        const int heads = slot_ok && slot >= 0 ? n_all : a.Hq;
-        auto place = [&](const Heads &x, int64_t row, int es, int before) {
-            return (unsigned char *)x.p + (row * x.st * es - (int64_t)before * x.head_bytes);
+        const bool slot_ok = slot < a.num_slots, kept = slot_ok && slot >= 0;
+        if ((!pos_ok || !slot_ok) && lane == 0 && now.part == 0) atomicOr(a.status, BAD_INDEX);
+        if (!pos_ok) {
+            if (more) load(xa0, xb0, it, 0);
+            continue;
+        }
+        __syncwarp();  // the token before has been read
+        for (int m0 = 0; m0 < half; m0 += 32) {
+            const int m = min(m0 + lane, half - 1), axis = s_axis[m];
+            const float2 p = make_float2(__shfl_sync(0xffffffffu, mine.x, axis), __shfl_sync(0xffffffffu, mine.y, axis));
+            const float2 c = cos_sin<true>(p, s_turns[m]);
+            s_cos[m] = c.x * a.scale;
+            s_sin[m] = c.y * a.scale;
+        }
+        __syncwarp();
+        // Unit i of a head turned.  (Its cosines and sines come from shared memory each
+        // time: in registers they left an SM 16 warps instead of 24.)
+        auto turn = [&](int i, float (&fa)[VE], float (&fb)[VE]) {
+            if constexpr (PAIRED) {
+                auto pairs = [&](float (&f)[VE], int from) {
+                    float cs[VE / 2], sn[VE / 2];
+                    load_floats(s_cos + from / 2, cs);
+                    load_floats(s_sin + from / 2, sn);
+#pragma unroll
+                    for (int m = 0; m < VE / 2; ++m) {
+                        const float x = f[2 * m], y = f[2 * m + 1];
+                        f[2 * m] = fmaf(-y, sn[m], x * cs[m]);
+                        f[2 * m + 1] = fmaf(x, sn[m], y * cs[m]);
+                    }
+                };
+                pairs(fa, ia[i]);
+                if (two >> i & 1) pairs(fb, ib[i]);
+            } else {
+                float cs[VE], sn[VE];
+                const int first = VE == 1 && INTERLEAVED ? ia[i] / 2 : ia[i];
+                load_floats(s_cos + first, cs);
+                load_floats(s_sin + first, sn);
+                if constexpr (VE > 1) {
+#pragma unroll
+                    for (int m = 0; m < VE; m += 2) {
+                        const float2 x = make_float2(fa[m], fa[m + 1]), y = make_float2(fb[m], fb[m + 1]);
+                        const float2 c = make_float2(cs[m], cs[m + 1]), s = make_float2(sn[m], sn[m + 1]);
+                        const float2 xc = f2mul(x, c), yc = f2fma(x, s, f2mul(y, c));
+                        fa[m] = fmaf(-y.x, s.x, xc.x);
+                        fa[m + 1] = fmaf(-y.y, s.y, xc.y);
+                        fb[m] = yc.x;
+                        fb[m + 1] = yc.y;
+                    }
+                } else {
+                    const float x = fa[0], y = fb[0];
+                    fa[0] = fmaf(-y, sn[0], x * cs[0]);
+                    fb[0] = fmaf(x, sn[0], y * cs[0]);
+                }
+            }
         };
-        const unsigned char *q = place(a.q, t, sizeof(T), 0), *k = place(a.k, t, sizeof(T), a.Hq), *v = place(a.v, t, sizeof(T), n_qk);
-        unsigned char *qo = place(a.q_out, t, sizeof(T), 0), *ko = place(a.k_out, slot, 1, a.Hq), *vo = place(a.v_out, slot, 1, n_qk);
-        // of a head's pairs; quantised values take sines to fp32's precision: the SFU's
-        // (2^-21) would move values across the codes' borders
-        float cs[UPL][VE], sn[UPL][VE];
-#pragma unroll
-        for (int i = 0; i < UPL; ++i)
-            if (turns >> i & 1) {
-#pragma unroll
-                for (int m = 0; m < VE; ++m) {
-                    const int pair = !PAIRED ? ia[i] + m : m < VE / 2 ? ia[i] / 2 + m : min(ib[i] / 2 + m - VE / 2, half - 1);
-                    const int axis = s_axis[pair];
-                    float2 p = pos[0];
-#pragma unroll
-                    for (int x = 1; x < RX_MAX_AXES; ++x) p = axis == x ? pos[x] : p;
-                    const float2 c = cos_sin<true>(p, s_turns[pair]);
-                    cs[i][m] = c.x * a.scale;
-                    sn[i][m] = c.y * a.scale;
-                }
-            }
-        const int step = parts * hpi;
-        for (int hb = part * hpi; hb < heads; hb += HB * step) {
-            V xa[HB][UPL], xb[HB][UPL];
-#pragma unroll
-            for (int j = 0; j < HB; ++j) {
-                const int h = hb + j * step + hs;
-                if (hs >= hpi || h >= heads) continue;
-                const bool is_v = h >= n_qk;
-                const unsigned char *base = h < a.Hq ? q : is_v ? v : k;
-                const uint32_t sh = h < a.Hq ? a.q.head_bytes : is_v ? a.v.head_bytes : a.k.head_bytes;
-                const T *src = reinterpret_cast<const T *>(base + (uint64_t)(uint32_t)h * sh);
-                const uint32_t wanted = is_v ? v_in : h < a.Hq && !q_moves ? turns : in, both = is_v ? v_two : two;
+        // Step s, whose heads are in xa and xb, in a loop that all lanes run.
+        auto finish = [&](V (&xa)[UPL], V (&xb)[UPL], int s) {
+            const bool is_q = s < now.nq, is_v = s >= now.nq + now.nk;
+            const int h = ((s - (is_q ? 0 : is_v ? now.nq + now.nk : now.nq)) * now.parts + now.part) * hpi + hs;
+            if (is_q) {
+                if (h >= a.Hq) return;
+                T *dst = reinterpret_cast<T *>((unsigned char *)a.q_out.p + (t * a.q_out.st * (int64_t)sizeof(T) + (uint64_t)(uint32_t)h * a.q_out.head_bytes));
 #pragma unroll
                 for (int i = 0; i < UPL; ++i)
-                    if (wanted >> i & 1) {
-                        xa[j][i] = *reinterpret_cast<const V *>(src + (is_v ? va[i] : ia[i]));
-                        if (both >> i & 1) xb[j][i] = *reinterpret_cast<const V *>(src + (is_v ? vb[i] : ib[i]));
-                    }
-            }
-#pragma unroll
-            for (int j = 0; j < HB; ++j) {
-                const int first = hb + j * step;  // the same in the whole warp
-                if (first >= heads) break;
-                const int h = first + hs;
-                const bool mine = hs < hpi && h < heads, is_q = h < a.Hq, is_v = h >= n_qk;
-                const uint32_t wanted = !mine ? 0u : is_v ? v_in : is_q && !q_moves ? turns : in, both = is_v ? v_two : two;
-                float fa[UPL][VE], fb[UPL][VE];
-                float top = 0.f;
-#pragma unroll
-                for (int i = 0; i < UPL; ++i)
-                    if (wanted >> i & 1) {
-                        unpack_raw<T, VB>(xa[j][i], fa[i]);
-                        if (both >> i & 1) unpack_raw<T, VB>(xb[j][i], fb[i]);
-                        else
-#pragma unroll
-                            for (int e = 0; e < VE; ++e) fb[i][e] = 0.f;
-                        if (!is_v && (turns >> i & 1)) {
-                            if constexpr (PAIRED) {
-                                auto pairs = [&](float (&f)[VE], int from) {
-#pragma unroll
-                                    for (int m = 0; m < VE / 2; ++m) {
-                                        const float x = f[2 * m], y = f[2 * m + 1], c = cs[i][from + m], s = sn[i][from + m];
-                                        f[2 * m] = fmaf(-y, s, x * c);
-                                        f[2 * m + 1] = fmaf(x, s, y * c);
-                                    }
-                                };
-                                pairs(fa[i], 0);
-                                pairs(fb[i], VE / 2);
-                            } else {
-#pragma unroll
-                                for (int m = 0; m < VE; ++m) {
-                                    const float x = fa[i][m], y = fb[i][m], c = cs[i][m], s = sn[i][m];
-                                    fa[i][m] = fmaf(-y, s, x * c);
-                                    fb[i][m] = fmaf(x, s, y * c);
-                                }
-                            }
+                    if (q_in >> i & 1) {
+                        if (turns >> i & 1) {
+                            float fa[VE], fb[VE] = {};
+                            unpack_raw<T, VB>(xa[i], fa);
+                            if (two >> i & 1) unpack_raw<T, VB>(xb[i], fb);
+                            turn(i, fa, fb);
+                            xa[i] = pack_raw<T, VB>(fa);
+                            xb[i] = pack_raw<T, VB>(fb);
                         }
-                        if (is_q) {
-                            T *dst = reinterpret_cast<T *>(qo + (uint64_t)(uint32_t)h * a.q_out.head_bytes);
-                            *reinterpret_cast<V *>(dst + ia[i]) = pack_raw<T, VB>(fa[i]);
-                            if (both >> i & 1) *reinterpret_cast<V *>(dst + ib[i]) = pack_raw<T, VB>(fb[i]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < VE; ++e) top = max_abs(top, fa[i][e], fb[i][e]);
-                        }
+                        *reinterpret_cast<V *>(dst + ia[i]) = xa[i];
+                        if (two >> i & 1) *reinterpret_cast<V *>(dst + ib[i]) = xb[i];
                     }
-                if (first + hpi <= a.Hq) continue;  // heads of q alone
-                // the largest of the head's cw lanes (counting some twice does no harm)
-                for (int off = 1; off < cw; off *= 2) {
-                    const int at = lu + off;
-                    top = max_abs(top, __shfl_sync(0xffffffffu, top, hs < hpi ? lane - lu + (at < cw ? at : at - cw) : lane));
-                }
-                if (!mine || is_q) continue;
-                const float most = scaled_top<FMT>(top);
-                const float by = code_factor<FMT>(most);
-                unsigned char *dst = (is_v ? vo : ko) + (uint64_t)(uint32_t)h * (is_v ? a.v_out.head_bytes : a.k_out.head_bytes);
-#pragma unroll
-                for (int i = 0; i < UPL; ++i)
-                    if (wanted >> i & 1) {
-                        *reinterpret_cast<Codes *>(dst + (is_v ? va[i] : ia[i])) = code_word<FMT>(fa[i], by);
-                        if (both >> i & 1) *reinterpret_cast<Codes *>(dst + (is_v ? vb[i] : ib[i])) = code_word<FMT>(fb[i], by);
-                    }
-                if (lu == 0) {
-                    const float scale = most * (1.f / top_code<FMT>());
-                    if (is_v) a.v_scale.p[slot * a.v_scale.st + (h - n_qk) * a.v_scale.sh] = scale;
-                    else a.k_scale.p[slot * a.k_scale.st + (h - a.Hq) * a.k_scale.sh] = scale;
-                }
+                return;
             }
+            const uint32_t wanted = h < a.Hkv ? is_v ? v_in : in : 0u, both = is_v ? v_two : two;
+            float fa[UPL][VE], fb[UPL][VE], top = 0.f;
+#pragma unroll
+            for (int i = 0; i < UPL; ++i)
+                if (wanted >> i & 1) {
+                    unpack_raw<T, VB>(xa[i], fa[i]);
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) fb[i][e] = 0.f;
+                    if (both >> i & 1) unpack_raw<T, VB>(xb[i], fb[i]);
+                    if (!is_v && (turns >> i & 1)) turn(i, fa[i], fb[i]);
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) top = max_abs(top, fa[i][e], fb[i][e]);
+                }
+            const float most = scaled_top<FMT>(head_max(top));
+            const float by = code_factor<FMT>(most);
+            if (!wanted) return;
+            const Heads &cache = is_v ? a.v_out : a.k_out;
+            unsigned char *dst = (unsigned char *)cache.p + (slot * cache.st + (uint64_t)(uint32_t)h * cache.head_bytes);
+#pragma unroll
+            for (int i = 0; i < UPL; ++i)
+                if (wanted >> i & 1) {
+                    *reinterpret_cast<Codes *>(dst + (is_v ? va[i] : ia[i])) = code_word<FMT>(fa[i], by);
+                    if (both >> i & 1) *reinterpret_cast<Codes *>(dst + (is_v ? vb[i] : ib[i])) = code_word<FMT>(fb[i], by);
+                }
+            if (lu == 0) {
+                const Scales &scales = is_v ? a.v_scale : a.k_scale;
+                scales.p[slot * scales.st + h * scales.sh] = most * (1.f / top_code<FMT>());
+            }
+        };
+        // One batch's loads are under way while the other's heads are worked on; behind the
+        // last come the first of the next token.
+        const int n = now.nq + (kept ? 2 * now.nk : 0);
+        for (int s = 0; s < n; s += 2 * HB) {
+            if (s + HB < n) load(xa1, xb1, now, s + HB);
+#pragma unroll
+            for (int j = 0; j < HB; ++j)
+                if (s + j < n) finish(xa0[j], xb0[j], s + j);
+            if (s + 2 * HB < n) load(xa0, xb0, now, s + 2 * HB);
+            else if (more) load(xa0, xb0, it, 0);
+#pragma unroll
+            for (int j = 0; j < HB; ++j)
+                if (s + HB + j < n) finish(xa1[j], xb1[j], s + HB + j);
         }
+        if (n == 0 && more) load(xa0, xb0, it, 0);
     }
 }
 
@@ -312,9 +405,8 @@ struct ReadArgs {
     unsigned int *status;
 };
 
-// C codes as one load, and C elements as 16-byte stores or one of less.
+// C codes as one load, and C elements as one store.
 template <int C> struct CodeLoad;
-template <> struct CodeLoad<16> { using type = uint4; };
 template <> struct CodeLoad<8> { using type = uint2; };
 template <> struct CodeLoad<4> { using type = uint32_t; };
 template <> struct CodeLoad<2> { using type = uint16_t; };
@@ -327,19 +419,12 @@ __device__ __forceinline__ void write_values(T *out, const typename CodeLoad<C>:
     float f[C < 2 ? 2 : C];
 #pragma unroll
     for (int i = 0; i < (C + 1) / 2; ++i) {
-        const float2 v = value_pair<FMT>(w[i / 2] >> (16 * (i % 2)) & 0xffffu);
-        f[2 * i] = v.x * by;
-        f[2 * i + 1] = v.y * by;
+        const float2 v = f2mul(value_pair<FMT>(w[i / 2] >> (16 * (i % 2)) & 0xffffu), make_float2(by, by));
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
     }
-    constexpr int E = vec_elems<T>();
-    if constexpr (C >= E) {
-#pragma unroll
-        for (int i = 0; i < C / E; ++i) {
-            float g[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) g[e] = f[i * E + e];
-            reinterpret_cast<uint4 *>(out)[i] = pack_vec<T>(g);
-        }
+    if constexpr (C == vec_elems<T>()) {
+        *reinterpret_cast<uint4 *>(out) = pack_vec<T>(f);
     } else if constexpr (C == 1) {
         Cvt<T>::store1(out, f[0]);
     } else if constexpr (sizeof(T) == 4) {  // C == 2
@@ -352,15 +437,20 @@ __device__ __forceinline__ void write_values(T *out, const typename CodeLoad<C>:
 }
 
 constexpr int R8_CTAS_PER_SM = 4;
-constexpr int R8_IN_FLIGHT = 4;
+constexpr int R8_ROUNDS = 4;
 
-// A warp takes a token's k and v, or one of a token's `wpt` parts: a unit of C codes a
-// lane at a time, R8_IN_FLIGHT of them loaded ahead of their stores.
+// Lanes of a head.
+__host__ __device__ constexpr int read8_lanes(int units) { return units < 32 ? units : 32; }
+
+// A warp takes a token's k and v, or one of a token's `wpt` parts: 32 / cw heads of each
+// at a time, cw lanes a head, R8_ROUNDS of k and as many of v loaded ahead of their stores.
+// A lane's C codes become one store of 16 bytes or less, so that a warp's stores fill their
+// lines (16 codes and two stores a lane: 75 us for 65536 tokens of 8 heads of 128, ... so).
 template <typename T, int FMT, int C>
 __global__ void __launch_bounds__(C8_NT, R8_CTAS_PER_SM) read8_kernel(const __grid_constant__ ReadArgs a, int wpt) {
     using L = typename CodeLoad<C>::type;
-    const int lane = threadIdx.x & 31, U = a.Dh / C, heads = 2 * a.Hkv;
-    const int step = 32 * wpt, step_h = step / U, step_u = step - step_h * U;
+    const int lane = threadIdx.x & 31, U = a.Dh / C, cw = read8_lanes(U), hpi = 32 / cw, hs = lane / cw, lu = lane - hs * cw;
+    const int step = hpi * wpt;  // heads a round
     const int64_t n_items = a.T * wpt, n_warps = (int64_t)gridDim.x * (C8_NT / 32);
     const int shift = 31 - __clz(wpt);  // wpt is a power of two
     griddep_wait();
@@ -372,41 +462,47 @@ __global__ void __launch_bounds__(C8_NT, R8_CTAS_PER_SM) read8_kernel(const __gr
         if (w + n_warps < n_items) next = a.slots[(w + n_warps) >> shift];
         const bool there = slot >= 0 && slot < a.num_slots;
         if (slot >= a.num_slots && lane == 0 && part == 0) atomicOr(a.status, BAD_INDEX);
-        // where heads 0 of k and v would be, counted through the list of both
-        const uint8_t *k = static_cast<const uint8_t *>(a.k.p) + slot * a.k.st;
-        const uint8_t *v = static_cast<const uint8_t *>(a.v.p) + slot * a.v.st;
-        const float *ks = a.k_scale.p + slot * a.k_scale.st, *vs = a.v_scale.p + slot * a.v_scale.st;
-        T *ko = static_cast<T *>(const_cast<void *>(a.k_out.p)) + t * a.k_out.st;
-        T *vo = static_cast<T *>(const_cast<void *>(a.v_out.p)) + t * a.v_out.st;
-        int h = (32 * part + lane) / U, u = 32 * part + lane - h * U;
-        while (h < heads) {
-            L codes[R8_IN_FLIGHT];
-            float by[R8_IN_FLIGHT];
-            T *out[R8_IN_FLIGHT];
+        if (hs >= hpi) continue;
+        const int h0 = part * hpi + hs;
+        const uint8_t *k = static_cast<const uint8_t *>(a.k.p) + (slot * a.k.st + h0 * a.k.sh);
+        const uint8_t *v = static_cast<const uint8_t *>(a.v.p) + (slot * a.v.st + h0 * a.v.sh);
+        const float *ks = a.k_scale.p + (slot * a.k_scale.st + h0 * a.k_scale.sh);
+        const float *vs = a.v_scale.p + (slot * a.v_scale.st + h0 * a.v_scale.sh);
+        T *ko = static_cast<T *>(const_cast<void *>(a.k_out.p)) + (t * a.k_out.st + h0 * a.k_out.sh);
+        T *vo = static_cast<T *>(const_cast<void *>(a.v_out.p)) + (t * a.v_out.st + h0 * a.v_out.sh);
+        for (int h = h0; h < a.Hkv; h += R8_ROUNDS * step) {
+            float kb[R8_ROUNDS], vb[R8_ROUNDS];
 #pragma unroll
-            for (int i = 0; i < R8_IN_FLIGHT; ++i) {
-                codes[i] = L{};
-                by[i] = 0.f;
-                out[i] = nullptr;
-                if (h < heads) {
-                    const bool is_v = h >= a.Hkv;
-                    const int64_t hk = is_v ? h - a.Hkv : h;
-                    out[i] = (is_v ? vo + hk * a.v_out.sh : ko + hk * a.k_out.sh) + u * C;
-                    if (there) {
-                        codes[i] = *reinterpret_cast<const L *>((is_v ? v + hk * a.v.sh : k + hk * a.k.sh) + u * C);
-                        by[i] = is_v ? vs[hk * a.v_scale.sh] : ks[hk * a.k_scale.sh];
+            for (int i = 0; i < R8_ROUNDS; ++i) {
+                const bool in = there && h + i * step < a.Hkv;
+                kb[i] = in ? ks[i * step * a.k_scale.sh] : 0.f;
+                vb[i] = in ? vs[i * step * a.v_scale.sh] : 0.f;
+            }
+            for (int u = lu; u < U; u += cw) {
+                L kc[R8_ROUNDS], vc[R8_ROUNDS];
+#pragma unroll
+                for (int i = 0; i < R8_ROUNDS; ++i) {
+                    const bool in = there && h + i * step < a.Hkv;
+                    kc[i] = L{};
+                    vc[i] = L{};
+                    if (in) {
+                        kc[i] = *reinterpret_cast<const L *>(k + i * step * a.k.sh + u * C);
+                        vc[i] = *reinterpret_cast<const L *>(v + i * step * a.v.sh + u * C);
                     }
                 }
-                h += step_h;
-                u += step_u;
-                if (u >= U) {
-                    u -= U;
-                    ++h;
-                }
-            }
 #pragma unroll
-            for (int i = 0; i < R8_IN_FLIGHT; ++i)
-                if (out[i]) write_values<T, FMT, C>(out[i], codes[i], by[i]);
+                for (int i = 0; i < R8_ROUNDS; ++i)
+                    if (h + i * step < a.Hkv) {
+                        write_values<T, FMT, C>(ko + i * step * a.k_out.sh + u * C, kc[i], kb[i]);
+                        write_values<T, FMT, C>(vo + i * step * a.v_out.sh + u * C, vc[i], vb[i]);
+                    }
+            }
+            k += R8_ROUNDS * step * a.k.sh;
+            v += R8_ROUNDS * step * a.v.sh;
+            ks += R8_ROUNDS * step * a.k_scale.sh;
+            vs += R8_ROUNDS * step * a.v_scale.sh;
+            ko += R8_ROUNDS * step * a.k_out.sh;
+            vo += R8_ROUNDS * step * a.v_out.sh;
         }
     }
 }

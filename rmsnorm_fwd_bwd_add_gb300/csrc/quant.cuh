@@ -79,7 +79,10 @@ template <int FMT> __device__ __forceinline__ uint32_t code_quad(float a, float 
 // Two codes (low and high byte of the low half) as floats.
 template <int FMT> __device__ __forceinline__ float2 value_pair(uint32_t codes) {
     if constexpr (FMT == RMSNORM_CACHE_I8) {
-        return make_float2((float)(int8_t)(codes & 0xffu), (float)(int8_t)(codes >> 8 & 0xffu));
+        // 2^23 + 128 + code, whose last bits are the code's with its sign turned, less 2^23 + 128
+        const uint32_t u = codes ^ 0x8080u;
+        return f2add(make_float2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7550)), __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7551))),
+                     make_float2(-8388736.f, -8388736.f));
     } else {  // every e4m3 value is an fp16 one
         uint32_t h;
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));

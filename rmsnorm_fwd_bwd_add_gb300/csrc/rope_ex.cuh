@@ -169,10 +169,12 @@ __global__ void __launch_bounds__(RX_NT, RX_CTAS_PER_SM) rope_ex_kernel(const __
     look_ahead(w);
     for (; w < n_items; w += n_warps) {
         const int64_t t = token_of(w), slot = slot_next;
-        float2 pos[NP];
+        float2 pos[NP] = {};
         bool pos_ok = true;
 #pragma unroll
         for (int x = 0; x < NP; ++x) {
+            if constexpr (AXES)
+                if (x >= a.axes.n) break;
             pos[x] = split_position(p_next[x]);
             pos_ok = pos_ok && p_next[x] >= 0;
         }
