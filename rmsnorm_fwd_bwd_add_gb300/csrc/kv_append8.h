@@ -12,10 +12,14 @@ template <typename T> cudaError_t launch_append8(const AppendArgs &a, int format
 
 template <typename T, int VB, bool INTERLEAVED, int FMT, int UPL>
 cudaError_t launch_append8_units(const AppendArgs &a, int lanes, int sm, cudaStream_t s) {
-    const RopePlan p = make_append8_plan(a.T, (lanes + UPL - 1) / UPL, a.Hq + 2 * a.Hkv, append8_batch<UPL>(),
-                                         sm * append8_ctas<VB / (int)sizeof(T), UPL>(), C8_NT / 32);
-    return launch_pdl(append8_kernel<T, VB, INTERLEAVED, FMT, UPL>, dim3(p.grid), dim3(C8_NT),
-                      (size_t)(C8_NT / 32) * 2 * append8_plane(a.rot) * sizeof(float), s, a, p.whole, p.wpt, p.cw);
+    static std::atomic<uint64_t> smem_mask{0};
+    auto kern = append8_kernel<T, VB, INTERLEAVED, FMT, UPL>;
+    const cudaError_t e = allow_max_dynamic_smem((const void *)kern, smem_mask);
+    if (e != cudaSuccess) return e;
+    const Append8Plan p = make_append8_plan(a.T, (lanes + UPL - 1) / UPL, a.Hq, a.Hkv, a.rot / 2, UPL,
+                                            sm * C8_CTAS_PER_SM, C8_NT / 32);
+    const size_t smem = (size_t)(C8_NT / 32) * (append8_ring<VB, UPL>() * append8_step_bytes<VB, UPL>() + 2 * append8_plane(a.rot) * sizeof(float));
+    return launch_pdl(kern, dim3(p.grid), dim3(C8_NT), smem, s, a, p.wpt, p.cw);
 }
 
 template <typename T, bool INTERLEAVED, int FMT>

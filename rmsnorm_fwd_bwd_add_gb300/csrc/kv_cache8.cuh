@@ -73,41 +73,49 @@ template <int VE> __device__ __forceinline__ void load_floats(const float *p, fl
     }
 }
 
-// Units of a head a lane holds at a time, over all heads in flight.
-#ifndef XUNITS
-#define XUNITS 4
-#endif
-constexpr int C8_UNITS_IN_FLIGHT = XUNITS;
+constexpr int C8_CTAS_PER_SM = 2;
 
-// Steps of heads in one of the two batches that a warp has in flight.
-template <int UPL> __host__ __device__ constexpr int append8_batch() { return UPL < C8_UNITS_IN_FLIGHT / 2 ? C8_UNITS_IN_FLIGHT / 2 / UPL : 1; }
+// A step's copies in shared memory, and the steps that a warp's ring holds: 6 KB of them
+// (16384 tokens of 32 + 8 heads of 128: 61.5 us, 62.9 with 8 KB, 64.4 with 12; with three
+// CTAs an SM 66 to 71).  2-byte units come as whole heads in 4-byte words, a word more each.
+template <int VB, int UPL> __host__ __device__ constexpr int append8_step_bytes() { return 2 * UPL * 32 * VB + (VB == 2 ? 32 * 4 : 0); }
+template <int VB, int UPL> __host__ __device__ constexpr int append8_ring() {
+    constexpr int n = 6144 / append8_step_bytes<VB, UPL>();
+    return n < 2 ? 2 : n > 16 ? 16 : n;
+}
 
-// CTAs an SM holds: long heads need more registers.
-template <int VE, int UPL> __host__ __device__ constexpr int append8_ctas() { return
-#ifdef XCTAS
- XCTAS;
-#else
- 2;
-#endif
- }
+// Asynchronous copy of 16 or 4 bytes from global to shared memory.
+template <int N> __device__ __forceinline__ void copy_async(unsigned char *dst, const void *src) {
+    if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
 
-// Shared memory of a warp: the cosines, then the sines of a token's pairs.
+// Shared memory of a warp: the cosines, then the sines of a token's pairs; and its ring.
 __host__ __device__ constexpr int append8_plane(int rot) { return (rot / 2 + 3) / 4 * 4; }
 
-// A warp takes a token (or one of a token's `wpt` parts, from token `whole` on), 32 / cw
-// heads at a time: cw lanes a head, UPL units of two vectors each a lane (rope_ex.cuh's
-// units), so that a head's largest value is a few shuffles away.  The token's cosines and
-// sines are computed by the warp's lanes together, once for all of its heads, to fp32's
-// precision: the SFU's (2^-21) would move values across the codes' borders.
+// A warp takes a token (or one of a token's `wpt` parts), 32 / cw heads a step: cw lanes a
+// head, UPL units of two vectors each a lane (rope_ex.cuh's units), so that a head's
+// largest value is a few shuffles away.  The token's cosines and sines are computed by the
+// warp's lanes together, once for all of its heads, to fp32's precision: the SFU's
+// (2^-21) would move values across the codes' borders.
+//
+// A lane copies its vectors of the steps to come, through all of its tokens, into a ring
+// of its own in shared memory: with two batches of steps in registers instead a warp
+// waited for memory five times a token (16384 tokens of 32 + 8 heads of 128: 70 us, 61.5
+// so).  Heads in 2-byte units (an odd size, or half a rotation of an odd number of
+// elements) are copied in the 4-byte words of memory, which the head's lanes share.
 template <typename T, int VB, bool INTERLEAVED, int FMT, int UPL>
-__global__ void __launch_bounds__(C8_NT, (append8_ctas<VB / (int)sizeof(T), UPL>())) append8_kernel(const __grid_constant__ AppendArgs a, int64_t whole, int wpt, int cw) {
+__global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __grid_constant__ AppendArgs a, int wpt, int cw) {
     using V = typename RawUnit<VB>::type;
-    constexpr int VE = VB / (int)sizeof(T), HB = append8_batch<UPL>();
+    constexpr int VE = VB / (int)sizeof(T), RING = append8_ring<VB, UPL>(), STEP = append8_step_bytes<VB, UPL>();
     constexpr bool PAIRED = INTERLEAVED && VE > 1;
     using Codes = typename CodeWord<VE>::type;
-    extern __shared__ __align__(16) float s_turn[];
+    extern __shared__ __align__(16) unsigned char s_dyn[];
     const int lane = threadIdx.x & 31, half = a.rot / 2, plane = append8_plane(a.rot);
-    float *s_cos = s_turn + (threadIdx.x >> 5) * 2 * plane, *s_sin = s_cos + plane;
+    constexpr bool WORDS = VB == 2;
+    unsigned char *s_ring = s_dyn + (threadIdx.x >> 5) * RING * STEP;
+    float *s_cos = reinterpret_cast<float *>(s_dyn + (C8_NT / 32) * RING * STEP) + (threadIdx.x >> 5) * 2 * plane;
+    float *s_sin = s_cos + plane;
     __shared__ float2 s_turns[RX_MAX_DH / 2];
     __shared__ uint8_t s_axis[RX_MAX_DH / 2];
     for (int i = threadIdx.x; i < half; i += C8_NT) {
@@ -134,6 +142,9 @@ __global__ void __launch_bounds__(C8_NT, (append8_ctas<VB / (int)sizeof(T), UPL>
         if (hs < hpi && l < v_map.lanes) v_in |= 1u << i, v_two |= (uint32_t)w << i;
     }
     turns &= in;
+    // this lane's vectors of a step, or its head's words
+    const int words = WORDS ? (a.Dh * 2 + 5) / 4 : 0;  // at most
+    s_ring += WORDS ? (hs < hpi ? hs : 0) * words * 4 : lane * VB;
     const uint32_t q_in = a.q_out.p != a.q.p ? in : turns;  // in place: nothing to copy
     // the largest of a head's cw lanes: butterflies, or turns of 1, 2, 4, ... lanes around
     // them (counting some twice does no harm)
@@ -146,73 +157,66 @@ __global__ void __launch_bounds__(C8_NT, (append8_ctas<VB / (int)sizeof(T), UPL>
         }
         return top;
     };
-    const int64_t n_items = whole + (a.T - whole) * wpt, n_warps = (int64_t)gridDim.x * (C8_NT / 32);
+    const int64_t n_items = a.T * wpt, n_warps = (int64_t)gridDim.x * (C8_NT / 32);
     const int wshift = 31 - __clz(wpt);  // wpt is a power of two
     int64_t w = ((int64_t)blockIdx.x * C8_NT + threadIdx.x) >> 5;
-    // An item: a token, or part `part` of `parts` of one; its steps of 32 / cw heads, those
-    // of q, then of k, then of v.
-    struct Item {
-        int64_t t;
-        int part, parts, nq, nk;
-    };
-    auto item_of = [&](int64_t i) {
-        Item it;
-        it.t = i < whole ? i : whole + ((i - whole) >> wshift);
-        it.parts = i < whole ? 1 : wpt;
-        it.part = i < whole ? 0 : (int)((i - whole) & (wpt - 1));
-        const int step = it.parts * hpi, from = it.part * hpi;
-        it.nq = a.Hq > from ? (a.Hq - from + step - 1) / step : 0;
-        it.nk = a.Hkv > from ? (a.Hkv - from + step - 1) / step : 0;
-        return it;
-    };
-    // Loads steps s0 .. s0 + HB - 1 of an item.
-    auto load = [&](V (&xa)[HB][UPL], V (&xb)[HB][UPL], const Item &it, int s0) {
-#pragma unroll
-        for (int j = 0; j < HB; ++j) {
-            const int s = s0 + j;
-            if (s >= it.nq + 2 * it.nk) break;
-            const bool is_q = s < it.nq, is_v = s >= it.nq + it.nk;
-            const int h = ((s - (is_q ? 0 : is_v ? it.nq + it.nk : it.nq)) * it.parts + it.part) * hpi + hs;
+    // An item's steps: those of q's heads, then of k's, then of v's (the same for all items
+    // of a part).
+    auto steps_of = [&](int n, int part) { return n > part * hpi ? (n - part * hpi + wpt * hpi - 1) / (wpt * hpi) : 0; };
+    int64_t ahead = w;  // of the copies: item and its steps, step, place in the ring
+    int ahead_nq = steps_of(a.Hq, (int)(w & (wpt - 1))), ahead_nk = steps_of(a.Hkv, (int)(w & (wpt - 1)));
+    int ahead_step = 0, ahead_at = 0;
+    auto copy_ahead = [&] {
+        if (ahead < n_items) {
+            const int64_t t = ahead >> wshift;
+            const int part = (int)(ahead & (wpt - 1)), nq = ahead_nq, nk = ahead_nk, s = ahead_step;
+            const bool is_q = s < nq, is_v = s >= nq + nk;
+            const int h = ((s - (is_q ? 0 : is_v ? nq + nk : nq)) * wpt + part) * hpi + hs;
             const Heads &x = is_q ? a.q : is_v ? a.v : a.k;
             const uint32_t wanted = is_q ? q_in : is_v ? v_in : in, both = is_v ? v_two : two;
             if (h < (is_q ? a.Hq : a.Hkv)) {
-                const T *src = reinterpret_cast<const T *>((const unsigned char *)x.p + (it.t * x.st * (int64_t)sizeof(T) + (uint64_t)(uint32_t)h * x.head_bytes));
+                const T *src = reinterpret_cast<const T *>((const unsigned char *)x.p + (t * x.st * (int64_t)sizeof(T) + (uint64_t)(uint32_t)h * x.head_bytes));
+                unsigned char *dst = s_ring + ahead_at * STEP;
+                if constexpr (WORDS) {
+                    const uintptr_t from = (uintptr_t)src & ~(uintptr_t)3, to = (uintptr_t)src + a.Dh * 2;
+                    if (hs < hpi)
+                        for (uintptr_t p = from + lu * 4; p < to; p += cw * 4) copy_async<4>(dst + (p - from), reinterpret_cast<const void *>(p));
+                } else {
 #pragma unroll
-                for (int i = 0; i < UPL; ++i) {
-                    if (wanted >> i & 1) xa[j][i] = *reinterpret_cast<const V *>(src + (is_v ? va[i] : ia[i]));
-                    if (wanted & both & 1u << i) xb[j][i] = *reinterpret_cast<const V *>(src + (is_v ? vb[i] : ib[i]));
+                    for (int i = 0; i < UPL; ++i) {
+                        if (wanted >> i & 1) copy_async<VB>(dst + 2 * i * 32 * VB, src + (is_v ? va[i] : ia[i]));
+                        if (wanted & both & 1u << i) copy_async<VB>(dst + (2 * i + 1) * 32 * VB, src + (is_v ? vb[i] : ib[i]));
+                    }
+                }
+            }
+            if (++ahead_step == nq + 2 * nk) {
+                ahead_step = 0;
+                ahead += n_warps;
+                if (wpt > 1) {
+                    ahead_nq = steps_of(a.Hq, (int)(ahead & (wpt - 1)));
+                    ahead_nk = steps_of(a.Hkv, (int)(ahead & (wpt - 1)));
                 }
             }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ahead_at = ahead_at + 1 == RING ? 0 : ahead_at + 1;
     };
     int64_t p_next = 0, slot_next = 0;  // of the item ahead; lane x has its position on axis x
     auto look_ahead = [&](int64_t t) {
         slot_next = a.slots[t];
         if (lane < a.axes.n) p_next = a.positions[lane * a.T + t];
     };
-    V xa0[HB][UPL], xb0[HB][UPL], xa1[HB][UPL], xb1[HB][UPL];  // two batches of steps
-    Item it{};
-    if (w < n_items) {
-        it = item_of(w);
-        load(xa0, xb0, it, 0);
-        look_ahead(it.t);
-    }
+    if (w < n_items) look_ahead(w >> wshift);
+    for (int i = 0; i < RING; ++i) copy_ahead();
+    int at = 0;  // place of the next step in the ring
     for (; w < n_items; w += n_warps) {
-        const int64_t t = it.t, slot = slot_next;
+        const int64_t t = w >> wshift, slot = slot_next;
+        const int part = (int)(w & (wpt - 1));
         const float2 mine = split_position(p_next);
         const bool pos_ok = __all_sync(0xffffffffu, p_next >= 0);
-        const Item now = it;
-        const bool more = w + n_warps < n_items;
-        if (more) {
-            it = item_of(w + n_warps);
-            look_ahead(it.t);
-        }
+        if (w + n_warps < n_items) look_ahead((w + n_warps) >> wshift);
         const bool slot_ok = slot < a.num_slots, kept = slot_ok && slot >= 0;
-        if ((!pos_ok || !slot_ok) && lane == 0 && now.part == 0) atomicOr(a.status, BAD_INDEX);
-        if (!pos_ok) {
-            if (more) load(xa0, xb0, it, 0);
-            continue;
-        }
+        if ((!pos_ok || !slot_ok) && lane == 0 && part == 0) atomicOr(a.status, BAD_INDEX);
         __syncwarp();  // the token before has been read
         for (int m0 = 0; m0 < half; m0 += 32) {
             const int m = min(m0 + lane, half - 1), axis = s_axis[m];
@@ -262,28 +266,52 @@ __global__ void __launch_bounds__(C8_NT, (append8_ctas<VB / (int)sizeof(T), UPL>
                 }
             }
         };
-        // Step s, whose heads are in xa and xb, in a loop that all lanes run.
-        auto finish = [&](V (&xa)[UPL], V (&xb)[UPL], int s) {
-            const bool is_q = s < now.nq, is_v = s >= now.nq + now.nk;
-            const int h = ((s - (is_q ? 0 : is_v ? now.nq + now.nk : now.nq)) * now.parts + now.part) * hpi + hs;
-            if (is_q) {
-                if (h >= a.Hq) return;
-                T *dst = reinterpret_cast<T *>((unsigned char *)a.q_out.p + (t * a.q_out.st * (int64_t)sizeof(T) + (uint64_t)(uint32_t)h * a.q_out.head_bytes));
+        const int nq = steps_of(a.Hq, part), nk = steps_of(a.Hkv, part);
+        for (int s = 0; s < nq + 2 * nk; ++s) {  // all lanes run every step
+            const bool is_q = s < nq, is_v = s >= nq + nk;
+            const int h = ((s - (is_q ? 0 : is_v ? nq + nk : nq)) * wpt + part) * hpi + hs;
+            V xa[UPL], xb[UPL];
+            asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
+            if constexpr (WORDS) {
+                __syncwarp();  // the other lanes' copies too
+                const Heads &x = is_q ? a.q : is_v ? a.v : a.k;
+                const uintptr_t src = (uintptr_t)x.p + (uintptr_t)(t * x.st * (int64_t)sizeof(T)) + (uint64_t)(uint32_t)h * x.head_bytes;
+                const unsigned char *head = s_ring + at * STEP + (src & 3);
 #pragma unroll
-                for (int i = 0; i < UPL; ++i)
-                    if (q_in >> i & 1) {
-                        if (turns >> i & 1) {
-                            float fa[VE], fb[VE] = {};
-                            unpack_raw<T, VB>(xa[i], fa);
-                            if (two >> i & 1) unpack_raw<T, VB>(xb[i], fb);
-                            turn(i, fa, fb);
-                            xa[i] = pack_raw<T, VB>(fa);
-                            xb[i] = pack_raw<T, VB>(fb);
+                for (int i = 0; i < UPL; ++i) {
+                    if ((is_v ? v_in : in) >> i & 1) xa[i] = reinterpret_cast<const V *>(head)[is_v ? va[i] : ia[i]];
+                    if ((is_v ? v_two : two) >> i & 1) xb[i] = reinterpret_cast<const V *>(head)[is_v ? vb[i] : ib[i]];
+                }
+                __syncwarp();  // before the words are copied over
+            } else {
+#pragma unroll
+                for (int i = 0; i < UPL; ++i) {
+                    xa[i] = *reinterpret_cast<const V *>(s_ring + at * STEP + 2 * i * 32 * VB);
+                    xb[i] = *reinterpret_cast<const V *>(s_ring + at * STEP + (2 * i + 1) * 32 * VB);
+                }
+            }
+            at = at + 1 == RING ? 0 : at + 1;
+            copy_ahead();
+            if (!pos_ok || (!is_q && !kept)) continue;
+            if (is_q) {
+                if (h < a.Hq) {
+                    T *dst = reinterpret_cast<T *>((unsigned char *)a.q_out.p + (t * a.q_out.st * (int64_t)sizeof(T) + (uint64_t)(uint32_t)h * a.q_out.head_bytes));
+#pragma unroll
+                    for (int i = 0; i < UPL; ++i)
+                        if (q_in >> i & 1) {
+                            if (turns >> i & 1) {
+                                float fa[VE], fb[VE] = {};
+                                unpack_raw<T, VB>(xa[i], fa);
+                                if (two >> i & 1) unpack_raw<T, VB>(xb[i], fb);
+                                turn(i, fa, fb);
+                                xa[i] = pack_raw<T, VB>(fa);
+                                xb[i] = pack_raw<T, VB>(fb);
+                            }
+                            *reinterpret_cast<V *>(dst + ia[i]) = xa[i];
+                            if (two >> i & 1) *reinterpret_cast<V *>(dst + ib[i]) = xb[i];
                         }
-                        *reinterpret_cast<V *>(dst + ia[i]) = xa[i];
-                        if (two >> i & 1) *reinterpret_cast<V *>(dst + ib[i]) = xb[i];
-                    }
-                return;
+                }
+                continue;
             }
             const uint32_t wanted = h < a.Hkv ? is_v ? v_in : in : 0u, both = is_v ? v_two : two;
             float fa[UPL][VE], fb[UPL][VE], top = 0.f;
@@ -300,7 +328,7 @@ __global__ void __launch_bounds__(C8_NT, (append8_ctas<VB / (int)sizeof(T), UPL>
                 }
             const float most = scaled_top<FMT>(head_max(top));
             const float by = code_factor<FMT>(most);
-            if (!wanted) return;
+            if (!wanted) continue;
             const Heads &cache = is_v ? a.v_out : a.k_out;
             unsigned char *dst = (unsigned char *)cache.p + (slot * cache.st + (uint64_t)(uint32_t)h * cache.head_bytes);
 #pragma unroll
@@ -313,23 +341,9 @@ __global__ void __launch_bounds__(C8_NT, (append8_ctas<VB / (int)sizeof(T), UPL>
                 const Scales &scales = is_v ? a.v_scale : a.k_scale;
                 scales.p[slot * scales.st + h * scales.sh] = most * (1.f / top_code<FMT>());
             }
-        };
-        // One batch's loads are under way while the other's heads are worked on; behind the
-        // last come the first of the next token.
-        const int n = now.nq + (kept ? 2 * now.nk : 0);
-        for (int s = 0; s < n; s += 2 * HB) {
-            if (s + HB < n) load(xa1, xb1, now, s + HB);
-#pragma unroll
-            for (int j = 0; j < HB; ++j)
-                if (s + j < n) finish(xa0[j], xb0[j], s + j);
-            if (s + 2 * HB < n) load(xa0, xb0, now, s + 2 * HB);
-            else if (more) load(xa0, xb0, it, 0);
-#pragma unroll
-            for (int j = 0; j < HB; ++j)
-                if (s + HB + j < n) finish(xa1[j], xb1[j], s + HB + j);
         }
-        if (n == 0 && more) load(xa0, xb0, it, 0);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Any stride, alignment and head: a warp a head of a token, a lane its elements 32
