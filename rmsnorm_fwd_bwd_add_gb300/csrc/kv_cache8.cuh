@@ -75,19 +75,29 @@ template <int VE> __device__ __forceinline__ void load_floats(const float *p, fl
 
 constexpr int C8_CTAS_PER_SM = 2;
 
-// A step's copies in shared memory, and the steps that a warp's ring holds: 6 KB of them
-// (16384 tokens of 32 + 8 heads of 128: 61.5 us, 62.9 with 8 KB, 64.4 with 12; with three
-// CTAs an SM 66 to 71).  2-byte units come as whole heads in 4-byte words, a word more each.
-template <int VB, int UPL> __host__ __device__ constexpr int append8_step_bytes() { return 2 * UPL * 32 * VB + (VB == 2 ? 32 * 4 : 0); }
+// Hides from the compiler that a register's value is unchanged, so that it is unpacked
+// again instead of being held unpacked.
+__device__ __forceinline__ void same_bits(uint4 &v) { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }
+__device__ __forceinline__ void same_bits(uint32_t &v) { asm volatile("" : "+r"(v)); }
+__device__ __forceinline__ void same_bits(uint16_t &v) { asm volatile("" : "+h"(v)); }
+
+// Smaller units come as whole heads in the 16-byte words of memory: the bytes that a head
+// of `bytes` may touch.
+__host__ __device__ constexpr int append8_head_bytes(int bytes) { return (bytes + 30) / 16 * 16; }
+
+// A step's copies in shared memory, and the steps that a warp's ring holds: 3 KB of them.
+// Reading further ahead holds up the writes (16384 tokens of 32 + 8 heads of 128: 60.0 us,
+// 61.9 with 2 KB, 65.1 with 4, 67.9 with 6; with three CTAs an SM 79).
+template <int VB, int UPL> __host__ __device__ inline int append8_step_bytes(int head_bytes, int cw) {
+    return VB == 16 ? 2 * UPL * 32 * VB : 32 / cw * append8_head_bytes(head_bytes);
+}
 template <int VB, int UPL> __host__ __device__ constexpr int append8_ring() {
-    constexpr int n = 6144 / append8_step_bytes<VB, UPL>();
-    return n < 2 ? 2 : n > 16 ? 16 : n;
+    constexpr int n = VB == 16 ? 3072 / (2 * UPL * 32 * VB) : 4;
+    return n < 2 ? 2 : n;
 }
 
-// Asynchronous copy of 16 or 4 bytes from global to shared memory.
-template <int N> __device__ __forceinline__ void copy_async(unsigned char *dst, const void *src) {
-    if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void copy_async16(unsigned char *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
 
 // Shared memory of a warp: the cosines, then the sines of a token's pairs; and its ring.
@@ -101,18 +111,19 @@ __host__ __device__ constexpr int append8_plane(int rot) { return (rot / 2 + 3) 
 //
 // A lane copies its vectors of the steps to come, through all of its tokens, into a ring
 // of its own in shared memory: with two batches of steps in registers instead a warp
-// waited for memory five times a token (16384 tokens of 32 + 8 heads of 128: 70 us, 61.5
-// so).  Heads in 2-byte units (an odd size, or half a rotation of an odd number of
-// elements) are copied in the 4-byte words of memory, which the head's lanes share.
+// waited for memory five times a token (16384 tokens of 32 + 8 heads of 128: 70 us, 60
+// so).  Heads in smaller units (off 16-byte boundaries, or turned by an odd number of
+// pairs) are copied whole, in the words of memory, which the head's lanes share.
 template <typename T, int VB, bool INTERLEAVED, int FMT, int UPL>
 __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __grid_constant__ AppendArgs a, int wpt, int cw) {
     using V = typename RawUnit<VB>::type;
-    constexpr int VE = VB / (int)sizeof(T), RING = append8_ring<VB, UPL>(), STEP = append8_step_bytes<VB, UPL>();
+    constexpr int VE = VB / (int)sizeof(T), RING = append8_ring<VB, UPL>();
     constexpr bool PAIRED = INTERLEAVED && VE > 1;
     using Codes = typename CodeWord<VE>::type;
     extern __shared__ __align__(16) unsigned char s_dyn[];
     const int lane = threadIdx.x & 31, half = a.rot / 2, plane = append8_plane(a.rot);
-    constexpr bool WORDS = VB == 2;
+    constexpr bool WORDS = VB < 16;
+    const int STEP = append8_step_bytes<VB, UPL>(a.Dh * (int)sizeof(T), cw);
     unsigned char *s_ring = s_dyn + (threadIdx.x >> 5) * RING * STEP;
     float *s_cos = reinterpret_cast<float *>(s_dyn + (C8_NT / 32) * RING * STEP) + (threadIdx.x >> 5) * 2 * plane;
     float *s_sin = s_cos + plane;
@@ -143,8 +154,7 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
     }
     turns &= in;
     // this lane's vectors of a step, or its head's words
-    const int words = WORDS ? (a.Dh * 2 + 5) / 4 : 0;  // at most
-    s_ring += WORDS ? (hs < hpi ? hs : 0) * words * 4 : lane * VB;
+    s_ring += WORDS ? (hs < hpi ? hs : 0) * append8_head_bytes(a.Dh * (int)sizeof(T)) : lane * VB;
     const uint32_t q_in = a.q_out.p != a.q.p ? in : turns;  // in place: nothing to copy
     // the largest of a head's cw lanes: butterflies, or turns of 1, 2, 4, ... lanes around
     // them (counting some twice does no harm)
@@ -160,47 +170,62 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
     const int64_t n_items = a.T * wpt, n_warps = (int64_t)gridDim.x * (C8_NT / 32);
     const int wshift = 31 - __clz(wpt);  // wpt is a power of two
     int64_t w = ((int64_t)blockIdx.x * C8_NT + threadIdx.x) >> 5;
-    // An item's steps: those of q's heads, then of k's, then of v's (the same for all items
-    // of a part).
-    auto steps_of = [&](int n, int part) { return n > part * hpi ? (n - part * hpi + wpt * hpi - 1) / (wpt * hpi) : 0; };
-    int64_t ahead = w;  // of the copies: item and its steps, step, place in the ring
-    int ahead_nq = steps_of(a.Hq, (int)(w & (wpt - 1))), ahead_nk = steps_of(a.Hkv, (int)(w & (wpt - 1)));
-    int ahead_step = 0, ahead_at = 0;
+    const int h_step = wpt * hpi;  // from a lane's head to its next
+    // The copies run ahead through the items, the kinds 0 (q), 1 (k) and 2 (v) of each and
+    // the steps of a kind: this lane's next head and its address.
+    int64_t ahead = w;
+    int ahead_kind = 0, ahead_h = 0, ahead_heads = 0, ahead_at = 0;
+    const unsigned char *ahead_src = nullptr;
+    auto begin_kind = [&] {
+        const Heads &x = ahead_kind == 0 ? a.q : ahead_kind == 1 ? a.k : a.v;
+        ahead_heads = ahead_kind == 0 ? a.Hq : a.Hkv;
+        ahead_h = (int)(ahead & (wpt - 1)) * hpi + hs;
+        ahead_src = (const unsigned char *)x.p + ((ahead >> wshift) * x.st * (int64_t)sizeof(T) + (uint64_t)(uint32_t)ahead_h * x.head_bytes);
+    };
+    auto first_kind = [&] {  // from ahead_kind on, that has heads in this part
+        while (ahead < n_items) {
+            begin_kind();
+            if (ahead_h - hs < ahead_heads) return;
+            if (++ahead_kind == 3) {
+                ahead_kind = 0;
+                ahead += n_warps;
+            }
+        }
+    };
     auto copy_ahead = [&] {
         if (ahead < n_items) {
-            const int64_t t = ahead >> wshift;
-            const int part = (int)(ahead & (wpt - 1)), nq = ahead_nq, nk = ahead_nk, s = ahead_step;
-            const bool is_q = s < nq, is_v = s >= nq + nk;
-            const int h = ((s - (is_q ? 0 : is_v ? nq + nk : nq)) * wpt + part) * hpi + hs;
-            const Heads &x = is_q ? a.q : is_v ? a.v : a.k;
-            const uint32_t wanted = is_q ? q_in : is_v ? v_in : in, both = is_v ? v_two : two;
-            if (h < (is_q ? a.Hq : a.Hkv)) {
-                const T *src = reinterpret_cast<const T *>((const unsigned char *)x.p + (t * x.st * (int64_t)sizeof(T) + (uint64_t)(uint32_t)h * x.head_bytes));
-                unsigned char *dst = s_ring + ahead_at * STEP;
+            const bool is_v = ahead_kind == 2;
+            unsigned char *dst = s_ring + ahead_at * STEP;
+            if (ahead_h < ahead_heads) {
                 if constexpr (WORDS) {
-                    const uintptr_t from = (uintptr_t)src & ~(uintptr_t)3, to = (uintptr_t)src + a.Dh * 2;
+                    const unsigned char *from = (const unsigned char *)((uintptr_t)ahead_src & ~(uintptr_t)15);
+                    const int end = (int)(ahead_src - from) + a.Dh * (int)sizeof(T);
                     if (hs < hpi)
-                        for (uintptr_t p = from + lu * 4; p < to; p += cw * 4) copy_async<4>(dst + (p - from), reinterpret_cast<const void *>(p));
+                        for (int b = lu * 16; b < end; b += cw * 16) copy_async16(dst + b, from + b);
                 } else {
+                    const uint32_t wanted = ahead_kind == 0 ? q_in : is_v ? v_in : in, both = wanted & (is_v ? v_two : two);
+                    const T *src = reinterpret_cast<const T *>(ahead_src);
 #pragma unroll
                     for (int i = 0; i < UPL; ++i) {
-                        if (wanted >> i & 1) copy_async<VB>(dst + 2 * i * 32 * VB, src + (is_v ? va[i] : ia[i]));
-                        if (wanted & both & 1u << i) copy_async<VB>(dst + (2 * i + 1) * 32 * VB, src + (is_v ? vb[i] : ib[i]));
+                        if (wanted >> i & 1) copy_async16(dst + 2 * i * 32 * VB, src + (is_v ? va[i] : ia[i]));
+                        if (both >> i & 1) copy_async16(dst + (2 * i + 1) * 32 * VB, src + (is_v ? vb[i] : ib[i]));
                     }
                 }
             }
-            if (++ahead_step == nq + 2 * nk) {
-                ahead_step = 0;
-                ahead += n_warps;
-                if (wpt > 1) {
-                    ahead_nq = steps_of(a.Hq, (int)(ahead & (wpt - 1)));
-                    ahead_nk = steps_of(a.Hkv, (int)(ahead & (wpt - 1)));
+            ahead_h += h_step;
+            ahead_src += (uint64_t)(uint32_t)h_step * (ahead_kind == 0 ? a.q.head_bytes : is_v ? a.v.head_bytes : a.k.head_bytes);
+            if (ahead_h - hs >= ahead_heads) {
+                if (++ahead_kind == 3) {
+                    ahead_kind = 0;
+                    ahead += n_warps;
                 }
+                first_kind();
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         ahead_at = ahead_at + 1 == RING ? 0 : ahead_at + 1;
     };
+    first_kind();
     int64_t p_next = 0, slot_next = 0;  // of the item ahead; lane x has its position on axis x
     auto look_ahead = [&](int64_t t) {
         slot_next = a.slots[t];
@@ -266,82 +291,94 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
                 }
             }
         };
-        const int nq = steps_of(a.Hq, part), nk = steps_of(a.Hkv, part);
-        for (int s = 0; s < nq + 2 * nk; ++s) {  // all lanes run every step
-            const bool is_q = s < nq, is_v = s >= nq + nk;
-            const int h = ((s - (is_q ? 0 : is_v ? nq + nk : nq)) * wpt + part) * hpi + hs;
-            V xa[UPL], xb[UPL];
-            asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
-            if constexpr (WORDS) {
-                __syncwarp();  // the other lanes' copies too
-                const Heads &x = is_q ? a.q : is_v ? a.v : a.k;
-                const uintptr_t src = (uintptr_t)x.p + (uintptr_t)(t * x.st * (int64_t)sizeof(T)) + (uint64_t)(uint32_t)h * x.head_bytes;
-                const unsigned char *head = s_ring + at * STEP + (src & 3);
+        // The steps of one kind, in a loop that all lanes run: f(xa, xb, h) has a head's units.
+        auto steps = [&](const Heads &x, int n, uint32_t wanted, uint32_t both, const int (&at_a)[UPL], const int (&at_b)[UPL], auto f) {
+            for (int h = part * hpi + hs; h - hs < n; h += h_step) {
+                V xa[UPL], xb[UPL];
+                asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
+                if constexpr (WORDS) {
+                    __syncwarp();  // the other lanes' copies too
+                    const uintptr_t src = (uintptr_t)x.p + (uintptr_t)(t * x.st * (int64_t)sizeof(T)) + (uint64_t)(uint32_t)h * x.head_bytes;
+                    const T *head = reinterpret_cast<const T *>(s_ring + at * STEP + (src & 15));
 #pragma unroll
-                for (int i = 0; i < UPL; ++i) {
-                    if ((is_v ? v_in : in) >> i & 1) xa[i] = reinterpret_cast<const V *>(head)[is_v ? va[i] : ia[i]];
-                    if ((is_v ? v_two : two) >> i & 1) xb[i] = reinterpret_cast<const V *>(head)[is_v ? vb[i] : ib[i]];
-                }
-                __syncwarp();  // before the words are copied over
-            } else {
+                    for (int i = 0; i < UPL; ++i) {
+                        if (wanted >> i & 1) xa[i] = *reinterpret_cast<const V *>(head + at_a[i]);
+                        if (both >> i & 1) xb[i] = *reinterpret_cast<const V *>(head + at_b[i]);
+                    }
+                    __syncwarp();  // before the words are copied over
+                } else {
 #pragma unroll
-                for (int i = 0; i < UPL; ++i) {
-                    xa[i] = *reinterpret_cast<const V *>(s_ring + at * STEP + 2 * i * 32 * VB);
-                    xb[i] = *reinterpret_cast<const V *>(s_ring + at * STEP + (2 * i + 1) * 32 * VB);
+                    for (int i = 0; i < UPL; ++i) {
+                        xa[i] = *reinterpret_cast<const V *>(s_ring + at * STEP + 2 * i * 32 * VB);
+                        xb[i] = *reinterpret_cast<const V *>(s_ring + at * STEP + (2 * i + 1) * 32 * VB);
+                    }
                 }
+                at = at + 1 == RING ? 0 : at + 1;
+                copy_ahead();
+                f(xa, xb, h);
             }
-            at = at + 1 == RING ? 0 : at + 1;
-            copy_ahead();
-            if (!pos_ok || (!is_q && !kept)) continue;
-            if (is_q) {
-                if (h < a.Hq) {
-                    T *dst = reinterpret_cast<T *>((unsigned char *)a.q_out.p + (t * a.q_out.st * (int64_t)sizeof(T) + (uint64_t)(uint32_t)h * a.q_out.head_bytes));
+        };
+        steps(a.q, a.Hq, in, two, ia, ib, [&](V (&xa)[UPL], V (&xb)[UPL], int h) {
+            if (!pos_ok || h >= a.Hq) return;
+            T *dst = reinterpret_cast<T *>((unsigned char *)a.q_out.p + (t * a.q_out.st * (int64_t)sizeof(T) + (uint64_t)(uint32_t)h * a.q_out.head_bytes));
 #pragma unroll
-                    for (int i = 0; i < UPL; ++i)
-                        if (q_in >> i & 1) {
-                            if (turns >> i & 1) {
-                                float fa[VE], fb[VE] = {};
-                                unpack_raw<T, VB>(xa[i], fa);
-                                if (two >> i & 1) unpack_raw<T, VB>(xb[i], fb);
-                                turn(i, fa, fb);
-                                xa[i] = pack_raw<T, VB>(fa);
-                                xb[i] = pack_raw<T, VB>(fb);
-                            }
-                            *reinterpret_cast<V *>(dst + ia[i]) = xa[i];
-                            if (two >> i & 1) *reinterpret_cast<V *>(dst + ib[i]) = xb[i];
+            for (int i = 0; i < UPL; ++i)
+                if (q_in >> i & 1) {
+                    if (turns >> i & 1) {
+                        float fa[VE], fb[VE] = {};
+                        unpack_raw<T, VB>(xa[i], fa);
+                        if (two >> i & 1) unpack_raw<T, VB>(xb[i], fb);
+                        turn(i, fa, fb);
+                        xa[i] = pack_raw<T, VB>(fa);
+                        xb[i] = pack_raw<T, VB>(fb);
+                    }
+                    *reinterpret_cast<V *>(dst + ia[i]) = xa[i];
+                    if (two >> i & 1) *reinterpret_cast<V *>(dst + ib[i]) = xb[i];
+                }
+        });
+        auto quantise = [&](const Heads &x, const Heads &cache, const Scales &scales, uint32_t wanted, uint32_t both, uint32_t turned,
+                            const int (&at_a)[UPL], const int (&at_b)[UPL]) {
+            steps(x, a.Hkv, wanted, both, at_a, at_b, [&](V (&xa)[UPL], V (&xb)[UPL], int h) {
+                if (!pos_ok || !kept) return;
+                const bool mine = h < a.Hkv;
+                // Several units are turned again behind the maximum: their values in
+                // registers would spill.
+                constexpr bool HOLD = UPL == 1;
+                float fa[VE], fb[VE], top = 0.f;
+                auto values = [&](int i) {
+                    unpack_raw<T, VB>(xa[i], fa);
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) fb[e] = 0.f;
+                    if (both >> i & 1) unpack_raw<T, VB>(xb[i], fb);
+                    if (turned >> i & 1) turn(i, fa, fb);
+                };
+#pragma unroll
+                for (int i = 0; i < UPL; ++i)
+                    if (mine && (wanted >> i & 1)) {
+                        values(i);
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) top = max_abs(top, fa[e], fb[e]);
+                    }
+                const float most = scaled_top<FMT>(head_max(top));
+                const float by = code_factor<FMT>(most);
+                if (!mine || hs >= hpi) return;
+                unsigned char *dst = (unsigned char *)cache.p + (slot * cache.st + (uint64_t)(uint32_t)h * cache.head_bytes);
+#pragma unroll
+                for (int i = 0; i < UPL; ++i)
+                    if (wanted >> i & 1) {
+                        if constexpr (!HOLD) {
+                            same_bits(xa[i]);
+                            same_bits(xb[i]);
+                            values(i);
                         }
-                }
-                continue;
-            }
-            const uint32_t wanted = h < a.Hkv ? is_v ? v_in : in : 0u, both = is_v ? v_two : two;
-            float fa[UPL][VE], fb[UPL][VE], top = 0.f;
-#pragma unroll
-            for (int i = 0; i < UPL; ++i)
-                if (wanted >> i & 1) {
-                    unpack_raw<T, VB>(xa[i], fa[i]);
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) fb[i][e] = 0.f;
-                    if (both >> i & 1) unpack_raw<T, VB>(xb[i], fb[i]);
-                    if (!is_v && (turns >> i & 1)) turn(i, fa[i], fb[i]);
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) top = max_abs(top, fa[i][e], fb[i][e]);
-                }
-            const float most = scaled_top<FMT>(head_max(top));
-            const float by = code_factor<FMT>(most);
-            if (!wanted) continue;
-            const Heads &cache = is_v ? a.v_out : a.k_out;
-            unsigned char *dst = (unsigned char *)cache.p + (slot * cache.st + (uint64_t)(uint32_t)h * cache.head_bytes);
-#pragma unroll
-            for (int i = 0; i < UPL; ++i)
-                if (wanted >> i & 1) {
-                    *reinterpret_cast<Codes *>(dst + (is_v ? va[i] : ia[i])) = code_word<FMT>(fa[i], by);
-                    if (both >> i & 1) *reinterpret_cast<Codes *>(dst + (is_v ? vb[i] : ib[i])) = code_word<FMT>(fb[i], by);
-                }
-            if (lu == 0) {
-                const Scales &scales = is_v ? a.v_scale : a.k_scale;
-                scales.p[slot * scales.st + h * scales.sh] = most * (1.f / top_code<FMT>());
-            }
-        }
+                        *reinterpret_cast<Codes *>(dst + at_a[i]) = code_word<FMT>(fa, by);
+                        if (both >> i & 1) *reinterpret_cast<Codes *>(dst + at_b[i]) = code_word<FMT>(fb, by);
+                    }
+                if (lu == 0) scales.p[slot * scales.st + h * scales.sh] = most * (1.f / top_code<FMT>());
+            });
+        };
+        quantise(a.k, a.k_out, a.k_scale, in, two, turns, ia, ib);
+        quantise(a.v, a.v_out, a.v_scale, v_in, v_two, 0u, va, vb);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
