@@ -40,14 +40,9 @@ bool hits(const Span &a, const void *p, size_t n) {
 }
 
 template <typename T, int FMT, int C> cudaError_t launch_read_units(const ReadArgs &a, int sm, cudaStream_t s) {
-    // as many parts a token as there are warps for, and heads for
-    const int64_t warps = (int64_t)sm * R8_CTAS_PER_SM * (C8_NT / 32);
-    const int hpi = 32 / read8_lanes(a.Dh / C);
-    int wpt = 1;
-    while (wpt < 64 && 2 * wpt * a.T <= warps && wpt * hpi < a.Hkv) wpt *= 2;
-    const int64_t ctas = (a.T * wpt + C8_NT / 32 - 1) / (C8_NT / 32);
-    return launch_pdl(read8_kernel<T, FMT, C>, dim3((unsigned)std::min<int64_t>(ctas, sm * R8_CTAS_PER_SM)), dim3(C8_NT), 0,
-                      s, a, wpt);
+    const Read8Plan p = make_read8_plan(a.T, a.Dh / C, a.Hkv, sm, R8_CTAS_PER_SM, R8_SMALL_CTAS_PER_SM, C8_NT / 32);
+    if (p.tokens > 1) return launch_pdl(read8_tokens_kernel<T, FMT, C>, dim3(p.grid), dim3(C8_NT), 0, s, a, p.cw, p.tokens);
+    return launch_pdl(read8_kernel<T, FMT, C>, dim3(p.grid), dim3(C8_NT), 0, s, a, p.cw, p.wpt);
 }
 
 // unit: codes that divide every address, stride and head of the caches, and in

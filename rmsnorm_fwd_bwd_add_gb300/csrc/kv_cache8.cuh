@@ -475,7 +475,7 @@ __device__ __forceinline__ void write_values(T *out, const typename CodeLoad<C>:
         f[2 * i + 1] = v.y;
     }
     if constexpr (C == vec_elems<T>()) {
-        *reinterpret_cast<uint4 *>(out) = pack_vec<T>(f);
+        __stcs(reinterpret_cast<uint4 *>(out), pack_vec<T>(f));  // read once, and far behind in a long context
     } else if constexpr (C == 1) {
         Cvt<T>::store1(out, f[0]);
     } else if constexpr (sizeof(T) == 4) {  // C == 2
@@ -487,20 +487,22 @@ __device__ __forceinline__ void write_values(T *out, const typename CodeLoad<C>:
     }
 }
 
-constexpr int R8_CTAS_PER_SM = 4;
-constexpr int R8_ROUNDS = 4;
+// Rounds of heads (or tokens) of k, and as many of v, that a warp has in flight.  Reading
+// further ahead holds up the writes (65536 tokens of 8 heads of 128, bf16: 65 us with two
+// rounds, 72 with four), but rounds in small units have few bytes each (16384 tokens of 8
+// heads of 90: 31 us with two, 27 with four).
+template <int C> __host__ __device__ constexpr int read8_rounds() { return C >= 4 ? 2 : 4; }
+constexpr int R8_CTAS_PER_SM = 4, R8_SMALL_CTAS_PER_SM = 3;  // with four rounds of tokens: 80 registers
 
-// Lanes of a head.
-__host__ __device__ constexpr int read8_lanes(int units) { return units < 32 ? units : 32; }
-
-// A warp takes a token's k and v, or one of a token's `wpt` parts: 32 / cw heads of each
-// at a time, cw lanes a head, R8_ROUNDS of k and as many of v loaded ahead of their stores.
-// A lane's C codes become one store of 16 bytes or less, so that a warp's stores fill their
-// lines (16 codes and two stores a lane: 75 us for 65536 tokens of 8 heads of 128, ... so).
+// A warp takes a token's k and v, or one of a token's `wpt` parts: 32 / cw heads of each a
+// round, cw lanes a head and C codes a lane.  A lane's C codes become one store of 16 bytes
+// or less, so that a warp's stores fill their lines (with 16 codes and two stores a lane
+// 65536 tokens of 8 heads of 128 took 75 us).
 template <typename T, int FMT, int C>
-__global__ void __launch_bounds__(C8_NT, R8_CTAS_PER_SM) read8_kernel(const __grid_constant__ ReadArgs a, int wpt) {
+__global__ void __launch_bounds__(C8_NT, R8_CTAS_PER_SM) read8_kernel(const __grid_constant__ ReadArgs a, int cw, int wpt) {
     using L = typename CodeLoad<C>::type;
-    const int lane = threadIdx.x & 31, U = a.Dh / C, cw = read8_lanes(U), hpi = 32 / cw, hs = lane / cw, lu = lane - hs * cw;
+    constexpr int R = read8_rounds<C>();
+    const int lane = threadIdx.x & 31, U = a.Dh / C, hpi = 32 / cw, hs = lane / cw, lu = lane - hs * cw;
     const int step = hpi * wpt;  // heads a round
     const int64_t n_items = a.T * wpt, n_warps = (int64_t)gridDim.x * (C8_NT / 32);
     const int shift = 31 - __clz(wpt);  // wpt is a power of two
@@ -521,39 +523,93 @@ __global__ void __launch_bounds__(C8_NT, R8_CTAS_PER_SM) read8_kernel(const __gr
         const float *vs = a.v_scale.p + (slot * a.v_scale.st + h0 * a.v_scale.sh);
         T *ko = static_cast<T *>(const_cast<void *>(a.k_out.p)) + (t * a.k_out.st + h0 * a.k_out.sh);
         T *vo = static_cast<T *>(const_cast<void *>(a.v_out.p)) + (t * a.v_out.st + h0 * a.v_out.sh);
-        for (int h = h0; h < a.Hkv; h += R8_ROUNDS * step) {
-            float kb[R8_ROUNDS], vb[R8_ROUNDS];
+        for (int h = h0; h < a.Hkv; h += R * step) {
+            float kb[R], vb[R];
 #pragma unroll
-            for (int i = 0; i < R8_ROUNDS; ++i) {
+            for (int i = 0; i < R; ++i) {
                 const bool in = there && h + i * step < a.Hkv;
                 kb[i] = in ? ks[i * step * a.k_scale.sh] : 0.f;
                 vb[i] = in ? vs[i * step * a.v_scale.sh] : 0.f;
             }
             for (int u = lu; u < U; u += cw) {
-                L kc[R8_ROUNDS], vc[R8_ROUNDS];
+                L kc[R], vc[R];
 #pragma unroll
-                for (int i = 0; i < R8_ROUNDS; ++i) {
-                    const bool in = there && h + i * step < a.Hkv;
+                for (int i = 0; i < R; ++i) {
                     kc[i] = L{};
                     vc[i] = L{};
-                    if (in) {
-                        kc[i] = *reinterpret_cast<const L *>(k + i * step * a.k.sh + u * C);
-                        vc[i] = *reinterpret_cast<const L *>(v + i * step * a.v.sh + u * C);
+                    if (there && h + i * step < a.Hkv) {
+                        kc[i] = __ldcs(reinterpret_cast<const L *>(k + i * step * a.k.sh + u * C));
+                        vc[i] = __ldcs(reinterpret_cast<const L *>(v + i * step * a.v.sh + u * C));
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < R8_ROUNDS; ++i)
+                for (int i = 0; i < R; ++i)
                     if (h + i * step < a.Hkv) {
                         write_values<T, FMT, C>(ko + i * step * a.k_out.sh + u * C, kc[i], kb[i]);
                         write_values<T, FMT, C>(vo + i * step * a.v_out.sh + u * C, vc[i], vb[i]);
                     }
             }
-            k += R8_ROUNDS * step * a.k.sh;
-            v += R8_ROUNDS * step * a.v.sh;
-            ks += R8_ROUNDS * step * a.k_scale.sh;
-            vs += R8_ROUNDS * step * a.v_scale.sh;
-            ko += R8_ROUNDS * step * a.k_out.sh;
-            vo += R8_ROUNDS * step * a.v_out.sh;
+            k += R * step * a.k.sh;
+            v += R * step * a.v.sh;
+            ks += R * step * a.k_scale.sh;
+            vs += R * step * a.v_scale.sh;
+            ko += R * step * a.k_out.sh;
+            vo += R * step * a.v_out.sh;
+        }
+    }
+}
+
+// Tokens of few heads: a round is all heads of `tokens` tokens, and the rounds are dealt
+// out to the warps in turn (60000 tokens of 2 heads of 64: 24 us with a warp a token, 11 so).
+template <typename T, int FMT, int C>
+__global__ void __launch_bounds__(C8_NT, R8_SMALL_CTAS_PER_SM) read8_tokens_kernel(const __grid_constant__ ReadArgs a, int cw, int tokens) {
+    using L = typename CodeLoad<C>::type;
+    constexpr int R = read8_rounds<C>();
+    const int lane = threadIdx.x & 31, U = a.Dh / C, hs = lane / cw, lu = lane - hs * cw;
+    const int sub = hs / a.Hkv, h = hs - sub * a.Hkv;  // this lane's token within a round, and head
+    const bool in = sub < tokens;
+    const int64_t step = (int64_t)gridDim.x * (C8_NT / 32) * tokens;  // tokens of all warps' rounds
+    int64_t t = (((int64_t)blockIdx.x * C8_NT + threadIdx.x) >> 5) * tokens + sub, slot[R];
+    griddep_wait();
+    griddep_launch_dependents();
+#pragma unroll
+    for (int i = 0; i < R; ++i) slot[i] = in && t + i * step < a.T ? a.slots[t + i * step] : -1;
+    for (; t - sub < a.T; t += R * step) {  // the same in a warp's lanes
+        int64_t at[R];
+        float kb[R], vb[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            at[i] = slot[i];
+            const int64_t next = t + (R + i) * step;  // its slot a trip to memory early
+            slot[i] = in && next < a.T ? a.slots[next] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (at[i] >= a.num_slots) {
+                if (lu == 0) atomicOr(a.status, BAD_INDEX);
+                at[i] = -1;
+            }
+            kb[i] = at[i] >= 0 ? a.k_scale.p[at[i] * a.k_scale.st + h * a.k_scale.sh] : 0.f;
+            vb[i] = at[i] >= 0 ? a.v_scale.p[at[i] * a.v_scale.st + h * a.v_scale.sh] : 0.f;
+        }
+        for (int u = lu; u < U; u += cw) {
+            L kc[R], vc[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                kc[i] = L{};
+                vc[i] = L{};
+                if (at[i] >= 0) {
+                    kc[i] = __ldcs(reinterpret_cast<const L *>(static_cast<const uint8_t *>(a.k.p) + (at[i] * a.k.st + h * a.k.sh)) + u);
+                    vc[i] = __ldcs(reinterpret_cast<const L *>(static_cast<const uint8_t *>(a.v.p) + (at[i] * a.v.st + h * a.v.sh)) + u);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                if (in && t + i * step < a.T) {
+                    const int64_t to = t + i * step;
+                    write_values<T, FMT, C>(static_cast<T *>(const_cast<void *>(a.k_out.p)) + (to * a.k_out.st + h * a.k_out.sh + u * C), kc[i], kb[i]);
+                    write_values<T, FMT, C>(static_cast<T *>(const_cast<void *>(a.v_out.p)) + (to * a.v_out.st + h * a.v_out.sh + u * C), vc[i], vb[i]);
+                }
         }
     }
 }

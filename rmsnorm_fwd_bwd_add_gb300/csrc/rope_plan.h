@@ -74,4 +74,34 @@ inline Append8Plan make_append8_plan(int64_t T, int cw, int Hq, int Hkv, int pai
     return p;
 }
 
+// How a read from the 8-bit cache deals tokens out: lanes a head, warps a token (a power
+// of two) or tokens a warp at a time.
+struct Read8Plan {
+    int cw, wpt, tokens, grid;
+};
+
+// As many lanes a head as it has units, or fewer where a token's heads then take a fifth
+// fewer steps (8 heads of 45 units: 4 x 3 steps of 15 lanes, 8 x 2 of 32; 16384 such
+// tokens 22.7 us, 26.7 so; but 3 heads of 45, 1 x 5 steps of 9 lanes, 3 x 2 of 32: 11.8 and
+// 10.1, for the wider stores).
+inline Read8Plan make_read8_plan(int64_t T, int units, int Hkv, int sm, int per_sm, int per_sm_tokens, int cta_warps) {
+    Read8Plan p{};
+    auto steps = [&](int cw) { return (int64_t)((Hkv + 32 / cw - 1) / (32 / cw)) * ((units + cw - 1) / cw); };
+    p.cw = std::min(units, 32);
+    int64_t most = steps(p.cw) * 4 / 5;
+    for (int cw = p.cw - 1; cw >= 1; --cw)
+        if (steps(cw) <= most) {
+            most = steps(cw) - 1;
+            p.cw = cw;
+        }
+    const int hpi = 32 / p.cw;
+    const int64_t warps = (int64_t)sm * per_sm * cta_warps;
+    p.wpt = 1;
+    while (p.wpt < 64 && 2 * p.wpt * T <= warps && p.wpt * hpi < Hkv) p.wpt *= 2;
+    p.tokens = std::max(1, hpi / Hkv);
+    const int64_t items = p.tokens > 1 ? (T + p.tokens - 1) / p.tokens : T * p.wpt;
+    p.grid = (int)std::min<int64_t>((items + cta_warps - 1) / cta_warps, (int64_t)sm * (p.tokens > 1 ? per_sm_tokens : per_sm));
+    return p;
+}
+
 }  // namespace rmsn
