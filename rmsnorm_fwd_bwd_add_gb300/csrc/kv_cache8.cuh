@@ -463,6 +463,12 @@ template <> struct CodeLoad<4> { using type = uint32_t; };
 template <> struct CodeLoad<2> { using type = uint16_t; };
 template <> struct CodeLoad<1> { using type = uint8_t; };
 
+// Codes are read once; those of less than a sector a warp are met again.
+template <int C> __device__ __forceinline__ typename CodeLoad<C>::type load_codes(const typename CodeLoad<C>::type *p) {
+    if constexpr (C >= 4) return __ldcs(p);
+    else return *p;
+}
+
 template <typename T, int FMT, int C>
 __device__ __forceinline__ void write_values(T *out, const typename CodeLoad<C>::type &codes, float by) {
     uint32_t w[(C + 3) / 4] = {};
@@ -538,8 +544,8 @@ __global__ void __launch_bounds__(C8_NT, R8_CTAS_PER_SM) read8_kernel(const __gr
                     kc[i] = L{};
                     vc[i] = L{};
                     if (there && h + i * step < a.Hkv) {
-                        kc[i] = __ldcs(reinterpret_cast<const L *>(k + i * step * a.k.sh + u * C));
-                        vc[i] = __ldcs(reinterpret_cast<const L *>(v + i * step * a.v.sh + u * C));
+                        kc[i] = load_codes<C>(reinterpret_cast<const L *>(k + i * step * a.k.sh + u * C));
+                        vc[i] = load_codes<C>(reinterpret_cast<const L *>(v + i * step * a.v.sh + u * C));
                     }
                 }
 #pragma unroll
@@ -599,8 +605,8 @@ __global__ void __launch_bounds__(C8_NT, R8_SMALL_CTAS_PER_SM) read8_tokens_kern
                 kc[i] = L{};
                 vc[i] = L{};
                 if (at[i] >= 0) {
-                    kc[i] = __ldcs(reinterpret_cast<const L *>(static_cast<const uint8_t *>(a.k.p) + (at[i] * a.k.st + h * a.k.sh)) + u);
-                    vc[i] = __ldcs(reinterpret_cast<const L *>(static_cast<const uint8_t *>(a.v.p) + (at[i] * a.v.st + h * a.v.sh)) + u);
+                    kc[i] = load_codes<C>(reinterpret_cast<const L *>(static_cast<const uint8_t *>(a.k.p) + (at[i] * a.k.st + h * a.k.sh)) + u);
+                    vc[i] = load_codes<C>(reinterpret_cast<const L *>(static_cast<const uint8_t *>(a.v.p) + (at[i] * a.v.st + h * a.v.sh)) + u);
                 }
             }
 #pragma unroll
