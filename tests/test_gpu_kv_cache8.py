@@ -82,6 +82,9 @@ CASES = [  # T, Hq, Hkv, Dh, sections
     (37, 4, 2, 22, (5,)), (9, 2, 1, 96, (24, 24)), (2450, 12, 4, 64, (32,)), (41, 5, 5, 125, (20, 20, 7)),
     (5, 2, 2, 1024, (512,)), (7, 3, 2, 1022, (100, 30)), (64, 8, 8, 256, (128,)), (1, 1, 1, 2, (1,)), (3, 2, 1, 3, (1,)),
     (700, 3, 3, 192, (96,)), (21, 4, 2, 512, (256,)), (19, 2, 2, 320, (64,)),
+    # long runs of tokens a warp, heads that leave lanes idle, parts of a token without q or k heads
+    (5000, 8, 1, 128, (64,)), (6001, 3, 1, 64, (8, 12, 12)), (4901, 2, 2, 100, (50,)), (3000, 5, 3, 126, (63,)),
+    (2, 64, 1, 64, (32,)), (3, 1, 40, 16, (8,)), (1, 130, 2, 128, (64,)), (33, 2, 70, 24, (12,)), (11, 9, 4, 112, (56,)),
 ]
 
 
@@ -391,3 +394,53 @@ def test_written_tensors_count_as_changed():
     before = [x._version for x in (ko, vo, kc)]
     rn.rmsnorm_kv_read(kc, vc, ks, vs, slots, k_out=ko, v_out=vo)
     assert [x._version for x in (ko, vo, kc)] == [before[0] + 1, before[1] + 1, before[2]]
+
+
+def test_a_slot_read_many_times_and_scales_of_any_size():
+    """The same rows over and over, and scales that take values out of the 16-bit types."""
+    H, Dh, N = 2, 64, 5
+    g = torch.Generator().manual_seed(12)
+    kc, vc, ks, vs = make_cache(g, N, H, Dh, "i8", "dense")
+    ks[1], ks[2], ks[3, 0] = 1e-30, 1e36, float("inf")
+    at = torch.randint(0, N, (3000,), generator=g).to(DEV)
+    for dt in (torch.float16, torch.bfloat16, torch.float32):
+        ko, vo = rn.rmsnorm_kv_read(kc, vc, ks, vs, at, dtype=dt)
+        for got, c, s in ((ko, kc, ks), (vo, vc, vs)):
+            want = (c.float()[at] * s[at][..., None]).to(dt)
+            assert torch.equal(got.isnan(), want.isnan())
+            assert torch.equal(got.nan_to_num(nan=0.0), want.nan_to_num(nan=0.0))
+
+
+def test_calls_of_two_threads():
+    """Two host threads, each with its own stream, caches and tokens, at once."""
+    import threading
+    g = torch.Generator().manual_seed(13)
+    problems = []
+    for T, Hq, H, Dh, fmt in ((3000, 8, 2, 128, "e4m3"), (777, 4, 4, 125, "i8")):
+        q, k, v = (torch.randn(T, h, Dh, generator=g).to(torch.bfloat16).to(DEV) for h in (Hq, H, H))
+        inv, _ = rn.rope_frequencies(Dh // 4 * 2)
+        pos, slots = torch.arange(T, device=DEV), torch.randperm(T + 9, generator=g)[:T].to(DEV)
+        problems.append((q, k, v, pos, slots, inv, make_cache(g, T + 9, H, Dh, fmt, "dense")))
+
+    def step(p):
+        q, k, v, pos, slots, inv, c = p
+        qo = rn.rmsnorm_kv_append(q, k, v, pos, slots, c[0], c[1], inv, k_scale=c[2], v_scale=c[3])
+        return (qo, *rn.rmsnorm_kv_read(*c, slots))
+
+    want = [step(p) for p in problems]
+    torch.cuda.synchronize()
+    same = [False, False]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got = [step(problems[i]) for _ in range(20)]
+        s.synchronize()
+        same[i] = all(torch.equal(a, b) for r in got for a, b in zip(r, want[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(same)

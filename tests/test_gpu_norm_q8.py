@@ -61,7 +61,10 @@ def _rows(g, rows, D, dtype, pad=0, off=0, std=1.0):
 
 SHAPES = [(1, 1), (3, 7), (5, 33), (1, 64), (4, 128), (9, 200), (700, 256), (65, 257), (1000, 512), (3, 1000),
           (33, 1024), (2000, 1024), (4, 4096), (400, 4096), (200, 4104), (300, 4097), (37, 8192), (500, 8192),
-          (6, 12288), (400, 16384), (3, 16392), (170, 20001), (2, 40000), (1, 1 << 20)]
+          (6, 12288), (400, 16384), (3, 16392), (170, 20001), (2, 40000), (1, 1 << 20),
+          # rings, aligned and not, with whole and ragged last units, groups and warps
+          (1300, 2048), (1301, 2200), (900, 2049), (700, 4096), (1500, 4097), (3000, 1001), (5000, 263), (470, 5121),
+          (310, 8200), (320, 16385), (330, 12296)]
 
 
 @pytest.mark.parametrize("rows,D", SHAPES, ids=["%dx%d" % s for s in SHAPES])
@@ -75,7 +78,8 @@ def test_shapes(rows, D, group, dt):
     _check(rn.rmsnorm_fwd_q8(x, w - 1, EPS, 1.0, group=group), x, None, w - 1, 1.0, group)
 
 
-@pytest.mark.parametrize("rows,D", [(50, 96), (40, 1000), (333, 2048), (170, 4096), (300, 4097), (5, 8192), (7, 16384)])
+@pytest.mark.parametrize("rows,D", [(50, 96), (40, 1000), (333, 2048), (170, 4096), (300, 4097), (5, 8192), (7, 16384),
+                                    (1300, 2048), (640, 4104), (2, 20000)])
 @pytest.mark.parametrize("group", [0, 64])
 @pytest.mark.parametrize("pads", [(0, 8, 16, 16), (8, 8, 8, 8), (1, 3, 1, 5), (64, 0, 0, 1)])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
@@ -99,7 +103,8 @@ def test_strides_and_offsets(rows, D, group, pads, dt):
         assert (whole[:, D:] == 7).all()
 
 
-@pytest.mark.parametrize("rows,D", [(3, 64), (6, 4096), (400, 4096), (20, 4097), (300, 1024), (3, 33000)])
+@pytest.mark.parametrize("rows,D", [(3, 64), (6, 4096), (400, 4096), (20, 4097), (300, 1024), (3, 33000), (900, 4096),
+                                    (1700, 4097), (5000, 1024)])
 @pytest.mark.parametrize("group", [0, 128])
 def test_new_residual_in_place(rows, D, group):
     g = torch.Generator().manual_seed(D)
@@ -253,3 +258,74 @@ def test_written_tensors_count_as_changed():
     before = [t._version for t in (o, s, n, x)]
     rn.rmsnorm_fwd_q8(x, w, EPS, 0.0, x, out=o, scale=s, new_residual=n)
     assert [t._version for t in (o, s, n, x)] == [before[0] + 1, before[1] + 1, before[2] + 1, before[3]]
+
+
+@pytest.mark.parametrize("rows,D", [(4, 4096), (900, 4096), (700, 4104), (1000, 1000), (5, 20000)])
+@pytest.mark.parametrize("group", [0, 32, 128])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_all_tensors_at_one_offset(rows, D, group, dt):
+    """Rows one element past a 16-byte boundary, codes one byte past a word; and weights
+    alone off their boundary."""
+    g = torch.Generator().manual_seed(D)
+    x, res, nr = (_rows(g, rows, D, DT[dt], off=1) for _ in range(3))
+    wide = (1 + 0.2 * torch.randn(D + 1, generator=g)).to(DT[dt]).to(DEV)
+    out = torch.empty(rows * D + 1, dtype=torch.uint8, device=DEV)[1:].view(rows, D).view(E4M3)
+    _check(rn.rmsnorm_fwd_q8(x, wide[:D], EPS, 0.0, res, group=group, out=out, new_residual=nr), x, res, wide[:D], 0.0, group)
+    y = x.contiguous().clone()
+    assert y.data_ptr() % 16 == 0
+    _check(rn.rmsnorm_fwd_q8(y, wide[1:], EPS, group=group), y, None, wide[1:], 0.0, group)
+
+
+def test_more_rows_than_a_ring_goes_round():
+    """Many rows a CTA, each unlike its neighbours."""
+    for rows, D, dt, group in ((20000, 1536, torch.bfloat16, 0), (9001, 4097, torch.float16, 64), (6000, 2048, torch.float32, 128),
+                               (40000, 256, torch.bfloat16, 32)):
+        g = torch.Generator().manual_seed(rows)
+        x, res = _rows(g, rows, D, dt), _rows(g, rows, D, dt)
+        w = (1 + 0.2 * torch.randn(D, generator=g)).to(dt).to(DEV)
+        _check(rn.rmsnorm_fwd_q8(x, w, EPS, 0.0, res, group=group), x, res, w, 0.0, group)
+
+
+@pytest.mark.parametrize("D,group", [(4096, 0), (4096, 128), (4097, 64)])
+def test_wait_timeout_is_reported_and_context_survives(D, group):
+    """A row whose copies are never issued: the wait ends, the status says so, and the
+    next call is right."""
+    g = torch.Generator().manual_seed(6)
+    x, res = _rows(g, 3000, D, torch.bfloat16), _rows(g, 3000, D, torch.bfloat16)
+    w = torch.ones(D, dtype=torch.bfloat16, device=DEV)
+    rn.rmsnorm_device_status(clear=True)
+    rn.rmsnorm_debug_inject(drop_tile=1501, budget_cycles=2_000_000)
+    try:
+        rn.rmsnorm_fwd_q8(x, w, EPS, 0.0, res, group=group)
+        bits = rn.rmsnorm_device_status(clear=True)
+    finally:
+        rn.rmsnorm_debug_inject(-1, 0)
+    assert bits & rn.DEVSTATUS_WAIT_TIMEOUT
+    _check(rn.rmsnorm_fwd_q8(x, w, EPS, 0.0, res, group=group), x, res, w, 0.0, group)
+    assert rn.rmsnorm_device_status(clear=True) == 0
+
+
+def test_calls_of_two_threads():
+    """Two host threads, each with its own stream and problem, at once."""
+    import threading
+    g = torch.Generator().manual_seed(7)
+    problems = [(_rows(g, 3000, 4096, torch.bfloat16), torch.ones(4096, dtype=torch.bfloat16, device=DEV), 0),
+                (_rows(g, 2000, 1001, torch.float32), torch.ones(1001, device=DEV), 32)]
+    want = [rn.rmsnorm_fwd_q8(x, w, EPS, 0.0, x, group=gr) for x, w, gr in problems]
+    torch.cuda.synchronize()
+    same = [False, False]
+
+    def work(i):
+        x, w, gr = problems[i]
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got = [rn.rmsnorm_fwd_q8(x, w, EPS, 0.0, x, group=gr) for _ in range(20)]
+        s.synchronize()
+        same[i] = all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for r in got for a, b in zip(r, want[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(same)

@@ -3,6 +3,7 @@ cache that come before any CUDA call."""
 import ctypes
 import os
 import shutil
+import subprocess
 
 import pytest
 
@@ -159,3 +160,118 @@ def test_python_refuses_cpu_tensors():
         rn.rmsnorm_kv_append(q, q, q, i64, i64, c, c, inv, k_scale=s, v_scale=s)
     with pytest.raises(ValueError, match="CUDA"):
         rn.rmsnorm_kv_read(c, c, s, s, i64)
+
+
+def run_host(tmp_path, text):
+    """Compiles and runs a host program against the plans' headers."""
+    src, exe = tmp_path / "plan.cu", tmp_path / "plan"
+    src.write_text(text)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    subprocess.run([nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-std=c++17", "-O1", "-I" + os.path.join(root, "include"),
+                    "-I" + os.path.join(root, "rmsnorm_fwd_bwd_add_gb300", "csrc"), "-o", str(exe), str(src)], check=True,
+                   capture_output=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+
+
+def test_norm_plans(tmp_path):
+    """Every plan is one that the kernels take: a row's units have threads, its single
+    columns too, rings fit an SM's shared memory beside the static sums, a CTA's rows
+    stand alike."""
+    run_host(tmp_path, r"""
+#include <cstdio>
+#include "norm_q8.h"
+using namespace rmsn;
+int main() {
+    const long lengths[] = {1, 7, 8, 15, 16, 17, 63, 64, 255, 256, 257, 1000, 1024, 1032, 2047, 2048, 2056, 4096, 4097, 4104, 5120,
+                            8192, 8193, 8200, 12288, 16384, 16385, 16392, 20000, 1L << 20, 1L << 24};
+    for (long D : lengths)
+        for (long rows : {1, 2, 5, 152, 153, 303, 304, 305, 607, 609, 1216, 1217, 4000, 100000})
+            for (int es : {2, 4})
+                for (int res = 0; res < 2; ++res)
+                    for (int classes : {0, 1, 2, 4, 8})
+                        for (int aligned = 0; aligned < 2; ++aligned) {
+                            if (aligned && classes != 1) continue;
+                            const Q8Plan p = make_q8_plan(rows, D, es, res, classes, aligned, 152);
+                            const long E = 16 / es, units = D / E;
+                            bool ok = q8_plan_ok(p) && p.grid <= rows;
+                            const bool held = p.kind == Q8_DIRECT || p.kind == Q8_STAGED;
+                            if (p.kind == Q8_WARP) ok = ok && !p.shift && D % E == 0 && units <= 32 * p.units && aligned;
+                            if (held) ok = ok && units >= 2 && units <= (long)p.threads * p.units && classes > 0;
+                            // up to E - 1 columns before the units and as many behind
+                            if (held && p.shift) ok = ok && p.threads >= 2 * (E - 1);
+                            if (held && !p.shift) ok = ok && aligned && D % E == 0;
+                            if (p.kind == Q8_DIRECT) ok = ok && p.grid == rows;
+                            if (p.kind == Q8_LONG) ok = ok && aligned && D % E == 0;
+                            if (p.kind == Q8_STAGED) {
+                                const long need = (p.shift ? D * es + 30 : D * es + 15) / 16 * 16;
+                                const int cap = p.threads <= 128 ? 128 : p.threads <= 256 ? 256 : 512;
+                                const long groups = p.shift ? 3 * 4 * (cap * p.units * E / 32 + 2) : 12;
+                                const long fixed = groups + 2 * 8 * (cap / 32);
+                                ok = ok && (long)p.stage_bytes >= need && p.stage_bytes % 16 == 0;
+                                ok = ok && (long)p.smem == Q8_HEADER + (long)p.stages * (res ? 2 : 1) * p.stage_bytes;
+                                ok = ok && (long)p.smem + fixed <= 227 * 1024 && p.stages * 8 <= Q8_HEADER;
+                                const int per_sm = (p.grid + 151) / 152;
+                                ok = ok && per_sm * ((long)p.smem + fixed + 1024) <= 228 * 1024 && per_sm * p.threads <= 512;
+                                if (p.shift) ok = ok && p.grid % classes == 0;
+                            }
+                            if (!ok) {
+                                printf("D %ld rows %ld es %d res %d classes %d aligned %d: kind %d threads %d units %d stages %d grid %d smem %zu",
+                                       D, rows, es, res, classes, aligned, p.kind, p.threads, p.units, p.stages, p.grid, p.smem);
+                                return 1;
+                            }
+                        }
+    return 0;
+}
+""")
+
+
+def test_cache_plans(tmp_path):
+    """Every part of a token has heads, a head's lanes are a warp's, rings fit shared memory
+    and hold what a step copies."""
+    run_host(tmp_path, r"""
+#include <cstdio>
+#include "kv_append8.h"
+using namespace rmsn;
+template <int VB, int UPL> bool append_ok(long T, int Dh, int lanes, int Hq, int Hkv, int pairs, int es) {
+    const int cw = (lanes + UPL - 1) / UPL;
+    const Append8Plan p = make_append8_plan(T, cw, Hq, Hkv, pairs, UPL, 152 * C8_CTAS_PER_SM, C8_NT / 32);
+    const int hpi = 32 / cw, most = Hq > Hkv ? Hq : Hkv;
+    bool ok = p.cw == cw && cw >= 1 && cw <= 32 && p.wpt >= 1 && (p.wpt & (p.wpt - 1)) == 0 && (p.wpt - 1) * hpi < most;
+    ok = ok && p.grid >= 1 && p.grid <= 152 * C8_CTAS_PER_SM;
+    const long step = append8_step_bytes<VB, UPL>(Dh * es, cw);
+    if (VB < 16) ok = ok && step >= (long)hpi * ((Dh * es + 30) / 16 * 16);
+    const long smem = (C8_NT / 32) * (append8_ring<VB, UPL>() * step + 2 * append8_plane(2 * pairs) * 4);
+    return ok && step % 16 == 0 && smem + 4608 <= 227 * 1024;
+}
+int main() {
+    for (int Dh = 2; Dh <= 1024; ++Dh)
+        for (long T : {1, 8, 300, 2432, 2433, 4096, 100000})
+            for (int Hq : {0, 1, 5, 32, 130})
+                for (int Hkv : {0, 1, 3, 8, 70}) {
+                    if (Hq + Hkv == 0) continue;
+                    const int pairs = Dh / 2, odd = (Dh + 1) / 2;
+                    bool ok = true;
+                    if (Dh % 16 == 0 && Dh / 16 <= 32) ok = ok && append_ok<16, 1>(T, Dh, Dh / 16, Hq, Hkv, pairs, 2);
+                    if (Dh % 16 == 0) ok = ok && append_ok<16, 2>(T, Dh, Dh / 16, Hq, Hkv, pairs, 2);
+                    if (Dh % 8 == 0 && Dh / 8 <= 64) ok = ok && append_ok<16, 2>(T, Dh, Dh / 8, Hq, Hkv, pairs, 4);
+                    if (Dh % 8 == 0) ok = ok && append_ok<16, 4>(T, Dh, Dh / 8, Hq, Hkv, pairs, 4);
+                    if ((Dh + 3) / 4 <= 128) ok = ok && append_ok<4, 4>(T, Dh, (Dh + 3) / 4, Hq, Hkv, pairs, 2);
+                    if (odd <= 256) ok = ok && append_ok<2, 8>(T, Dh, odd, Hq, Hkv, pairs, 2) && append_ok<4, 8>(T, Dh, odd, Hq, Hkv, pairs, 4);
+                    if (Hkv)
+                        for (int C : {1, 2, 4, 8}) {
+                            if (Dh % C) continue;
+                            const Read8Plan p = make_read8_plan(T, Dh / C, Hkv, 152, 4, 3, C8_NT / 32);
+                            const int hpi = p.cw > 0 ? 32 / p.cw : 0;
+                            ok = ok && p.cw >= 1 && p.cw <= 32 && p.cw <= Dh / C && p.wpt >= 1 && (p.wpt & (p.wpt - 1)) == 0 && p.grid >= 1;
+                            ok = ok && (p.wpt == 1 || (p.wpt / 2) * hpi < Hkv) && (p.tokens == 1 || p.tokens * Hkv <= hpi);
+                        }
+                    if (!ok) {
+                        printf("Dh %d T %ld heads %d + %d", Dh, T, Hq, Hkv);
+                        return 1;
+                    }
+                }
+    return 0;
+}
+""")
