@@ -16,31 +16,38 @@ cudaError_t launch_append8_units(const AppendArgs &a, int lanes, int sm, cudaStr
     auto kern = append8_kernel<T, VB, INTERLEAVED, FMT, UPL>;
     const cudaError_t e = allow_max_dynamic_smem((const void *)kern, smem_mask);
     if (e != cudaSuccess) return e;
-    const Append8Plan p = make_append8_plan(a.T, (lanes + UPL - 1) / UPL, a.Hq, a.Hkv, a.rot / 2, UPL,
+    const Append8Plan p = make_append8_plan(a.T, (lanes + UPL - 1) / UPL, a.Hq, a.Hkv, a.slots ? 2 : 1, a.rot / 2, UPL,
                                             sm * C8_CTAS_PER_SM, C8_NT / 32);
-    const size_t smem = (size_t)(C8_NT / 32) * (append8_ring<VB, UPL>() * append8_step_bytes<VB, UPL>(a.Dh * (int)sizeof(T), p.cw) +
+    const size_t smem = (size_t)(C8_NT / 32) * (append8_ring<VB, UPL, FMT>() * append8_step_bytes<VB, UPL>(a.Dh * (int)sizeof(T), p.cw) +
                                                 2 * append8_plane(a.rot) * sizeof(float));
-    return launch_pdl(kern, dim3(p.grid), dim3(C8_NT), smem, s, a, p.wpt, p.cw);
+    return launch_pdl(kern, dim3(p.grid), dim3(C8_NT), smem, s, a, p.whole, p.wpt, p.cw);
 }
 
+// Lanes of a head in units of VE elements.
+template <int VE, bool INTERLEAVED> int head_lanes(const AppendArgs &a) {
+    return HeadMap<VE, (INTERLEAVED && VE > 1), INTERLEAVED>(a.Dh, a.rot).lanes;
+}
+
+// Heads in 16-byte units, 16 elements a lane while a head's lanes are a warp's.
+template <typename T, bool INTERLEAVED, int FMT>
+cudaError_t launch_append8_vectors(const AppendArgs &a, int sm, cudaStream_t s) {
+    constexpr int E = 16 / (int)sizeof(T);
+    const int lanes = head_lanes<E, INTERLEAVED>(a);
+    if (lanes <= 32 * (8 / E)) return launch_append8_units<T, 16, INTERLEAVED, FMT, 8 / E>(a, lanes, sm, s);
+    return launch_append8_units<T, 16, INTERLEAVED, FMT, 16 / E>(a, lanes, sm, s);
+}
+
+// Smaller units: fewer lanes a head leave each step less work beside its elements (4096
+// tokens of 32 + 8 heads of 100 in 4-byte units: 66 us with 4 elements a lane, 30 with 16).
 template <typename T, bool INTERLEAVED, int FMT>
 cudaError_t launch_append8_layout(const AppendArgs &a, int unit, int sm, cudaStream_t s) {
-    auto lanes_of = [&](auto ve) { return HeadMap<decltype(ve)::value, (INTERLEAVED && decltype(ve)::value > 1), INTERLEAVED>(a.Dh, a.rot).lanes; };
-    // 16 elements a lane where the head has as many: fewer lanes a head leave each step less
-    // work beside them (4096 tokens of 32 + 8 heads of 100 in 4-byte units: 66 us with 4
-    // elements a lane, ... so).
-    constexpr int E = 16 / (int)sizeof(T);
-    if (unit == 16) {
-        const int lanes = lanes_of(std::integral_constant<int, E>{});
-        if (lanes <= 32 * (8 / E)) return launch_append8_units<T, 16, INTERLEAVED, FMT, 8 / E>(a, lanes, sm, s);
-        return launch_append8_units<T, 16, INTERLEAVED, FMT, 16 / E>(a, lanes, sm, s);
-    }
+    if (unit == 16) return launch_append8_vectors<T, INTERLEAVED, FMT>(a, sm, s);
     if constexpr (sizeof(T) == 2)
         if (unit == 4) {
-            const int lanes = lanes_of(std::integral_constant<int, 2>{});
+            const int lanes = head_lanes<2, INTERLEAVED>(a);
             if (lanes <= 128) return launch_append8_units<T, 4, INTERLEAVED, FMT, 4>(a, lanes, sm, s);
         }
-    const int lanes = lanes_of(std::integral_constant<int, 1>{});
+    const int lanes = head_lanes<1, INTERLEAVED>(a);
     if (lanes <= 256) return launch_append8_units<T, (int)sizeof(T), INTERLEAVED, FMT, 8>(a, lanes, sm, s);
     const int64_t warps = a.T * (a.Hq + 2 * (int64_t)a.Hkv);
     const dim3 grid((unsigned)std::min<int64_t>((warps + C8_NT / 32 - 1) / (C8_NT / 32), 8 * (int64_t)sm));

@@ -85,14 +85,16 @@ __device__ __forceinline__ void same_bits(uint16_t &v) { asm volatile("" : "+h"(
 // of `bytes` may touch.
 __host__ __device__ constexpr int append8_head_bytes(int bytes) { return (bytes + 30) / 16 * 16; }
 
-// A step's copies in shared memory, and the steps that a warp's ring holds: 3 KB of them.
-// Reading further ahead holds up the writes (16384 tokens of 32 + 8 heads of 128: 60.0 us,
-// 61.9 with 2 KB, 65.1 with 4, 67.9 with 6; with three CTAs an SM 79).
+// A step's copies in shared memory, and the steps that a warp's ring holds: 3 KB of them,
+// or 2 where as much is written as read.  Reading further ahead holds up the writes (16384
+// tokens of 32 + 8 heads of 128: the 8-bit append 60.0 us, 61.9 with 2 KB, 65.1 with 4,
+// 67.9 with 6, with three CTAs an SM 79; the rotation alone 53.6 with 2 KB, 58.6 with 3,
+// 59.5 with 4).
 template <int VB, int UPL> __host__ __device__ inline int append8_step_bytes(int head_bytes, int cw) {
     return VB == 16 ? 2 * UPL * 32 * VB : 32 / cw * append8_head_bytes(head_bytes);
 }
-template <int VB, int UPL> __host__ __device__ constexpr int append8_ring() {
-    constexpr int n = VB == 16 ? 3072 / (2 * UPL * 32 * VB) : 4;
+template <int VB, int UPL, int FMT> __host__ __device__ constexpr int append8_ring() {
+    constexpr int n = VB == 16 ? (FMT == RMSNORM_CACHE_SAME ? 2048 : 3072) / (2 * UPL * 32 * VB) : 4;
     return n < 2 ? 2 : n;
 }
 
@@ -103,11 +105,14 @@ __device__ __forceinline__ void copy_async16(unsigned char *dst, const void *src
 // Shared memory of a warp: the cosines, then the sines of a token's pairs; and its ring.
 __host__ __device__ constexpr int append8_plane(int rot) { return (rot / 2 + 3) / 4 * 4; }
 
-// A warp takes a token (or one of a token's `wpt` parts), 32 / cw heads a step: cw lanes a
+// FMT is RMSNORM_CACHE_SAME for caches of the inputs' type and, without slots, for
+// rmsnorm_rope_axes, whose k stays with its token (VB = 16 alone).
+//
+// A warp takes a token (or one of a token's `wpt` parts, from token `whole` on), 32 / cw heads a step: cw lanes a
 // head, UPL units of two vectors each a lane (rope_ex.cuh's units), so that a head's
 // largest value is a few shuffles away.  The token's cosines and sines are computed by the
-// warp's lanes together, once for all of its heads, to fp32's precision: the SFU's
-// (2^-21) would move values across the codes' borders.
+// warp's lanes together, once for all of its heads; for codes to fp32's precision, as the
+// SFU's (2^-21) would move values across their borders.
 //
 // A lane copies its vectors of the steps to come, through all of its tokens, into a ring
 // of its own in shared memory: with two batches of steps in registers instead a warp
@@ -115,11 +120,12 @@ __host__ __device__ constexpr int append8_plane(int rot) { return (rot / 2 + 3) 
 // so).  Heads in smaller units (off 16-byte boundaries, or turned by an odd number of
 // pairs) are copied whole, in the words of memory, which the head's lanes share.
 template <typename T, int VB, bool INTERLEAVED, int FMT, int UPL>
-__global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __grid_constant__ AppendArgs a, int wpt, int cw) {
+__global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __grid_constant__ AppendArgs a, int64_t whole, int wpt, int cw) {
     using V = typename RawUnit<VB>::type;
-    constexpr int VE = VB / (int)sizeof(T), RING = append8_ring<VB, UPL>();
+    constexpr int VE = VB / (int)sizeof(T), RING = append8_ring<VB, UPL, FMT>();
     constexpr bool PAIRED = INTERLEAVED && VE > 1;
     using Codes = typename CodeWord<VE>::type;
+    constexpr bool SAME = FMT == RMSNORM_CACHE_SAME;
     extern __shared__ __align__(16) unsigned char s_dyn[];
     const int lane = threadIdx.x & 31, half = a.rot / 2, plane = append8_plane(a.rot);
     constexpr bool WORDS = VB < 16;
@@ -156,6 +162,14 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
     // this lane's vectors of a step, or its head's words
     s_ring += WORDS ? (hs < hpi ? hs : 0) * append8_head_bytes(a.Dh * (int)sizeof(T)) : lane * VB;
     const uint32_t q_in = a.q_out.p != a.q.p ? in : turns;  // in place: nothing to copy
+    const uint32_t k_in = !SAME || a.k_out.p != a.k.p ? in : turns;
+    const int kinds = a.slots ? 3 : 2;
+    // A token's place in q, k, v or q_out, in elements.
+    auto place = [&](const Heads &x, int64_t t) {
+        if (!SAME || a.S == a.T) return t * x.st;
+        const int64_t b = t / a.S;
+        return b * x.sb + (t - b * a.S) * x.st;
+    };
     // the largest of a head's cw lanes: butterflies, or turns of 1, 2, 4, ... lanes around
     // them (counting some twice does no harm)
     const bool square = (cw & (cw - 1)) == 0;
@@ -167,26 +181,29 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
         }
         return top;
     };
-    const int64_t n_items = a.T * wpt, n_warps = (int64_t)gridDim.x * (C8_NT / 32);
+    const int64_t n_items = whole + (a.T - whole) * wpt, n_warps = (int64_t)gridDim.x * (C8_NT / 32);
     const int wshift = 31 - __clz(wpt);  // wpt is a power of two
     int64_t w = ((int64_t)blockIdx.x * C8_NT + threadIdx.x) >> 5;
-    const int h_step = wpt * hpi;  // from a lane's head to its next
+    auto token_of = [&](int64_t item) { return item < whole ? item : whole + ((item - whole) >> wshift); };
+    auto part_of = [&](int64_t item) { return item < whole ? 0 : (int)((item - whole) & (wpt - 1)); };
+    auto parts_of = [&](int64_t item) { return item < whole ? 1 : wpt; };
     // The copies run ahead through the items, the kinds 0 (q), 1 (k) and 2 (v) of each and
     // the steps of a kind: this lane's next head and its address.
     int64_t ahead = w;
-    int ahead_kind = 0, ahead_h = 0, ahead_heads = 0, ahead_at = 0;
+    int ahead_kind = 0, ahead_h = 0, ahead_heads = 0, ahead_at = 0, ahead_step = 0;
     const unsigned char *ahead_src = nullptr;
     auto begin_kind = [&] {
         const Heads &x = ahead_kind == 0 ? a.q : ahead_kind == 1 ? a.k : a.v;
         ahead_heads = ahead_kind == 0 ? a.Hq : a.Hkv;
-        ahead_h = (int)(ahead & (wpt - 1)) * hpi + hs;
-        ahead_src = (const unsigned char *)x.p + ((ahead >> wshift) * x.st * (int64_t)sizeof(T) + (uint64_t)(uint32_t)ahead_h * x.head_bytes);
+        ahead_h = part_of(ahead) * hpi + hs;
+        ahead_step = parts_of(ahead) * hpi;
+        ahead_src = (const unsigned char *)x.p + (place(x, token_of(ahead)) * (int64_t)sizeof(T) + (uint64_t)(uint32_t)ahead_h * x.head_bytes);
     };
     auto first_kind = [&] {  // from ahead_kind on, that has heads in this part
         while (ahead < n_items) {
             begin_kind();
             if (ahead_h - hs < ahead_heads) return;
-            if (++ahead_kind == 3) {
+            if (++ahead_kind == kinds) {
                 ahead_kind = 0;
                 ahead += n_warps;
             }
@@ -203,7 +220,7 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
                     if (hs < hpi)
                         for (int b = lu * 16; b < end; b += cw * 16) copy_async16(dst + b, from + b);
                 } else {
-                    const uint32_t wanted = ahead_kind == 0 ? q_in : is_v ? v_in : in, both = wanted & (is_v ? v_two : two);
+                    const uint32_t wanted = ahead_kind == 0 ? q_in : is_v ? v_in : k_in, both = wanted & (is_v ? v_two : two);
                     const T *src = reinterpret_cast<const T *>(ahead_src);
 #pragma unroll
                     for (int i = 0; i < UPL; ++i) {
@@ -212,10 +229,10 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
                     }
                 }
             }
-            ahead_h += h_step;
-            ahead_src += (uint64_t)(uint32_t)h_step * (ahead_kind == 0 ? a.q.head_bytes : is_v ? a.v.head_bytes : a.k.head_bytes);
+            ahead_h += ahead_step;
+            ahead_src += (uint64_t)(uint32_t)ahead_step * (ahead_kind == 0 ? a.q.head_bytes : is_v ? a.v.head_bytes : a.k.head_bytes);
             if (ahead_h - hs >= ahead_heads) {
-                if (++ahead_kind == 3) {
+                if (++ahead_kind == kinds) {
                     ahead_kind = 0;
                     ahead += n_warps;
                 }
@@ -228,27 +245,27 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
     first_kind();
     int64_t p_next = 0, slot_next = 0;  // of the item ahead; lane x has its position on axis x
     auto look_ahead = [&](int64_t t) {
-        slot_next = a.slots[t];
+        slot_next = SAME && !a.slots ? 0 : a.slots[t];
         if (lane < a.axes.n) p_next = a.positions[lane * a.T + t];
     };
-    if (w < n_items) look_ahead(w >> wshift);
+    if (w < n_items) look_ahead(token_of(w));
     for (int i = 0; i < RING; ++i) copy_ahead();
     int at = 0;  // place of the next step in the ring
     for (; w < n_items; w += n_warps) {
-        const int64_t t = w >> wshift, slot = slot_next;
-        const int part = (int)(w & (wpt - 1));
+        const int64_t t = token_of(w), slot = slot_next;
+        const int part = part_of(w), h_step = parts_of(w) * hpi;  // from a lane's head to its next
         const float2 mine = split_position(p_next);
         const bool pos_ok = __all_sync(0xffffffffu, p_next >= 0);
-        if (w + n_warps < n_items) look_ahead((w + n_warps) >> wshift);
+        if (w + n_warps < n_items) look_ahead(token_of(w + n_warps));
         const bool slot_ok = slot < a.num_slots, kept = slot_ok && slot >= 0;
         if ((!pos_ok || !slot_ok) && lane == 0 && part == 0) atomicOr(a.status, BAD_INDEX);
         __syncwarp();  // the token before has been read
         for (int m0 = 0; m0 < half; m0 += 32) {
             const int m = min(m0 + lane, half - 1), axis = s_axis[m];
             const float2 p = make_float2(__shfl_sync(0xffffffffu, mine.x, axis), __shfl_sync(0xffffffffu, mine.y, axis));
-            const float2 c = cos_sin<true>(p, s_turns[m]);
+            const float2 c = cos_sin<!SAME || sizeof(T) == 4>(p, s_turns[m]);
             s_cos[m] = c.x * a.scale;
-            s_sin[m] = c.y * a.scale;
+            s_sin[m] = c.y * (a.scale * a.sign);
         }
         __syncwarp();
         // Unit i of a head turned.  (Its cosines and sines come from shared memory each
@@ -298,7 +315,7 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
                 asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
                 if constexpr (WORDS) {
                     __syncwarp();  // the other lanes' copies too
-                    const uintptr_t src = (uintptr_t)x.p + (uintptr_t)(t * x.st * (int64_t)sizeof(T)) + (uint64_t)(uint32_t)h * x.head_bytes;
+                    const uintptr_t src = (uintptr_t)x.p + (uintptr_t)(place(x, t) * (int64_t)sizeof(T)) + (uint64_t)(uint32_t)h * x.head_bytes;
                     const T *head = reinterpret_cast<const T *>(s_ring + at * STEP + (src & 15));
 #pragma unroll
                     for (int i = 0; i < UPL; ++i) {
@@ -318,24 +335,34 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
                 f(xa, xb, h);
             }
         };
-        steps(a.q, a.Hq, in, two, ia, ib, [&](V (&xa)[UPL], V (&xb)[UPL], int h) {
-            if (!pos_ok || h >= a.Hq) return;
-            T *dst = reinterpret_cast<T *>((unsigned char *)a.q_out.p + (t * a.q_out.st * (int64_t)sizeof(T) + (uint64_t)(uint32_t)h * a.q_out.head_bytes));
+        // Heads turned and stored in the inputs' type, from the element `row` of y on.
+        auto move = [&](const Heads &x, const Heads &y, int64_t row, int n, uint32_t wanted, uint32_t both, uint32_t turned,
+                        const int (&at_a)[UPL], const int (&at_b)[UPL]) {
+            steps(x, n, wanted, both, at_a, at_b, [&](V (&xa)[UPL], V (&xb)[UPL], int h) {
+                if (!pos_ok || h >= n || row < 0) return;
+                T *dst = reinterpret_cast<T *>((unsigned char *)y.p + (row * (int64_t)sizeof(T) + (uint64_t)(uint32_t)h * y.head_bytes));
 #pragma unroll
-            for (int i = 0; i < UPL; ++i)
-                if (q_in >> i & 1) {
-                    if (turns >> i & 1) {
-                        float fa[VE], fb[VE] = {};
-                        unpack_raw<T, VB>(xa[i], fa);
-                        if (two >> i & 1) unpack_raw<T, VB>(xb[i], fb);
-                        turn(i, fa, fb);
-                        xa[i] = pack_raw<T, VB>(fa);
-                        xb[i] = pack_raw<T, VB>(fb);
+                for (int i = 0; i < UPL; ++i)
+                    if (wanted >> i & 1) {
+                        if (turned >> i & 1) {
+                            float fa[VE], fb[VE] = {};
+                            unpack_raw<T, VB>(xa[i], fa);
+                            if (both >> i & 1) unpack_raw<T, VB>(xb[i], fb);
+                            turn(i, fa, fb);
+                            xa[i] = pack_raw<T, VB>(fa);
+                            xb[i] = pack_raw<T, VB>(fb);
+                        }
+                        *reinterpret_cast<V *>(dst + at_a[i]) = xa[i];
+                        if (both >> i & 1) *reinterpret_cast<V *>(dst + at_b[i]) = xb[i];
                     }
-                    *reinterpret_cast<V *>(dst + ia[i]) = xa[i];
-                    if (two >> i & 1) *reinterpret_cast<V *>(dst + ib[i]) = xb[i];
-                }
-        });
+            });
+        };
+        move(a.q, a.q_out, place(a.q_out, t), a.Hq, q_in, two, turns, ia, ib);
+        if constexpr (SAME) {
+            move(a.k, a.k_out, !a.slots ? place(a.k_out, t) : kept ? slot * a.k_out.st : -1, a.Hkv, k_in, two, turns, ia, ib);
+            if (a.slots) move(a.v, a.v_out, kept ? slot * a.v_out.st : -1, a.Hkv, v_in, v_two, 0u, va, vb);
+            continue;
+        }
         auto quantise = [&](const Heads &x, const Heads &cache, const Scales &scales, uint32_t wanted, uint32_t both, uint32_t turned,
                             const int (&at_a)[UPL], const int (&at_b)[UPL]) {
             steps(x, a.Hkv, wanted, both, at_a, at_b, [&](V (&xa)[UPL], V (&xb)[UPL], int h) {
@@ -377,8 +404,10 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
                 if (lu == 0) scales.p[slot * scales.st + h * scales.sh] = most * (1.f / top_code<FMT>());
             });
         };
-        quantise(a.k, a.k_out, a.k_scale, in, two, turns, ia, ib);
-        quantise(a.v, a.v_out, a.v_scale, v_in, v_two, 0u, va, vb);
+        if constexpr (!SAME) {
+            quantise(a.k, a.k_out, a.k_scale, in, two, turns, ia, ib);
+            quantise(a.v, a.v_out, a.v_scale, v_in, v_two, 0u, va, vb);
+        }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }

@@ -100,7 +100,9 @@ int rope_run(const Heads &q, const Heads &k, const Heads &v, const int64_t *posi
     } else {
         RopeArgs<false> one;
         static_cast<RopeExArgs &>(one) = a;
-        e = launch_rope<false>(one, interleaved, unit, dtype, sm, s);
+        e = dtype == RMSNORM_F16    ? launch_type<__half>(one, interleaved, unit, sm, s)
+            : dtype == RMSNORM_BF16 ? launch_type<__nv_bfloat16>(one, interleaved, unit, sm, s)
+                                    : launch_type<float>(one, interleaved, unit, sm, s);
     }
     return e == cudaSuccess ? RMSNORM_OK : record_cuda_error(e);
 }

@@ -314,21 +314,14 @@ cudaError_t launch_layout(const RopeArgs<AXES> &a, int sm, cudaStream_t s) {
 }
 
 // unit: bytes that divide every address, stride and length.
-template <typename T, bool AXES>
-cudaError_t launch_type(const RopeArgs<AXES> &a, bool interleaved, int unit, int sm, cudaStream_t s) {
+template <typename T>
+cudaError_t launch_type(const RopeArgs<false> &a, bool interleaved, int unit, int sm, cudaStream_t s) {
     if (unit == 16)
-        return interleaved ? launch_layout<T, 16, true, AXES>(a, sm, s) : launch_layout<T, 16, false, AXES>(a, sm, s);
+        return interleaved ? launch_layout<T, 16, true, false>(a, sm, s) : launch_layout<T, 16, false, false>(a, sm, s);
     if constexpr (sizeof(T) == 2)
         if (unit < 4)
-            return interleaved ? launch_layout<T, 2, true, AXES>(a, sm, s) : launch_layout<T, 2, false, AXES>(a, sm, s);
-    return interleaved ? launch_layout<T, 4, true, AXES>(a, sm, s) : launch_layout<T, 4, false, AXES>(a, sm, s);
-}
-
-template <bool AXES>
-cudaError_t launch_rope(const RopeArgs<AXES> &a, bool interleaved, int unit, int dtype, int sm, cudaStream_t s) {
-    return dtype == RMSNORM_F16    ? launch_type<__half, AXES>(a, interleaved, unit, sm, s)
-           : dtype == RMSNORM_BF16 ? launch_type<__nv_bfloat16, AXES>(a, interleaved, unit, sm, s)
-                                   : launch_type<float, AXES>(a, interleaved, unit, sm, s);
+            return interleaved ? launch_layout<T, 2, true, false>(a, sm, s) : launch_layout<T, 2, false, false>(a, sm, s);
+    return interleaved ? launch_layout<T, 4, true, false>(a, sm, s) : launch_layout<T, 4, false, false>(a, sm, s);
 }
 
 }  // namespace rmsn

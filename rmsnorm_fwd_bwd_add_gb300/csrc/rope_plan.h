@@ -49,28 +49,33 @@ inline RopePlan make_rope_plan(int64_t T, int lanes, int heads, int in_flight, i
     return p;
 }
 
-// How the 8-bit append deals tokens out: warps a token (a power of two), lanes a head.
+// How the 8-bit append deals tokens out: those of one warp each, warps a token of the rest
+// (a power of two), lanes a head.
 struct Append8Plan {
+    int64_t whole;
     int wpt, cw, grid;
 };
 
-// Every warp goes through rounds of items, a token or one of its parts each.  An item
-// costs its positions and cosines (each part its own), and its steps of 32 / cw heads.
-// No part is without heads.
-inline Append8Plan make_append8_plan(int64_t T, int cw, int Hq, int Hkv, int pairs, int units, int ctas, int cta_warps) {
+// All warps go through equal rounds of whole tokens; of what is left, less than a round,
+// each token is split into as many parts as cost least.  A part costs its positions and
+// cosines, and its steps of 32 / cw heads (kv: of k and of v, or of k alone); none is
+// without heads.
+inline Append8Plan make_append8_plan(int64_t T, int cw, int Hq, int Hkv, int kv, int pairs, int units, int ctas, int cta_warps) {
     const int64_t warps = (int64_t)ctas * cta_warps;
     const int hpi = 32 / cw, most = (std::max(Hq, Hkv) + hpi - 1) / hpi;
-    Append8Plan p{1, cw, 0};
-    double best = 1e300;
+    Append8Plan p{T / warps * warps, 1, cw, 0};
+    const int64_t rest = T - p.whole;
+    int64_t best = INT64_MAX;
     for (int k = 1; k <= 16 && k <= most; k *= 2) {
-        const int steps = (Hq + hpi * k - 1) / (hpi * k) + 2 * ((Hkv + hpi * k - 1) / (hpi * k));
-        const double cost = (double)((T * k + warps - 1) / warps) * (200 + 60 * ((pairs + 31) / 32) + 90.0 * units * steps);
+        const int steps = (Hq + hpi * k - 1) / (hpi * k) + kv * ((Hkv + hpi * k - 1) / (hpi * k));
+        const int64_t cost = (rest * k + warps - 1) / warps * (200 + 60 * ((pairs + 31) / 32) + 90 * units * steps);
         if (cost < best) {
             best = cost;
             p.wpt = k;
         }
     }
-    p.grid = (int)std::min<int64_t>((T * p.wpt + cta_warps - 1) / cta_warps, ctas);
+    const int64_t items = p.whole + rest * p.wpt;
+    p.grid = (int)std::min<int64_t>((items + cta_warps - 1) / cta_warps, ctas);
     return p;
 }
 

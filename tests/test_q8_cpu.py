@@ -236,13 +236,13 @@ def test_cache_plans(tmp_path):
 using namespace rmsn;
 template <int VB, int UPL> bool append_ok(long T, int Dh, int lanes, int Hq, int Hkv, int pairs, int es) {
     const int cw = (lanes + UPL - 1) / UPL;
-    const Append8Plan p = make_append8_plan(T, cw, Hq, Hkv, pairs, UPL, 152 * C8_CTAS_PER_SM, C8_NT / 32);
+    const Append8Plan p = make_append8_plan(T, cw, Hq, Hkv, 2, pairs, UPL, 152 * C8_CTAS_PER_SM, C8_NT / 32);
     const int hpi = 32 / cw, most = Hq > Hkv ? Hq : Hkv;
     bool ok = p.cw == cw && cw >= 1 && cw <= 32 && p.wpt >= 1 && (p.wpt & (p.wpt - 1)) == 0 && (p.wpt - 1) * hpi < most;
-    ok = ok && p.grid >= 1 && p.grid <= 152 * C8_CTAS_PER_SM;
+    ok = ok && p.grid >= 1 && p.grid <= 152 * C8_CTAS_PER_SM && p.whole >= 0 && p.whole <= T && T - p.whole < 152 * C8_CTAS_PER_SM * 8;
     const long step = append8_step_bytes<VB, UPL>(Dh * es, cw);
     if (VB < 16) ok = ok && step >= (long)hpi * ((Dh * es + 30) / 16 * 16);
-    const long smem = (C8_NT / 32) * (append8_ring<VB, UPL>() * step + 2 * append8_plane(2 * pairs) * 4);
+    const long smem = (C8_NT / 32) * (append8_ring<VB, UPL, RMSNORM_CACHE_E4M3>() * step + 2 * append8_plane(2 * pairs) * 4);
     return ok && step % 16 == 0 && smem + 4608 <= 227 * 1024;
 }
 int main() {
