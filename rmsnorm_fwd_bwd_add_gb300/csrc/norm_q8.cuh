@@ -55,16 +55,22 @@ template <int P> __device__ __forceinline__ void store_codes(uint8_t *p, const f
     }
 }
 
-// run_max of V values at once.
+// run_max of V values at once.  Runs of 16 lanes (128 columns of 16 bits) are unrolled: 8192
+// rows of fp16, D = 4096 take 22.4 us with the loop, 20.9 so, 21.8 with the others unrolled
+// as well, and 25.6 with reductions of a part of the warp's lanes in one instruction.
 template <int V> __device__ __forceinline__ void run_maxima(float (&top)[V], int n) {
+    auto step = [&](int off) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) top[j] = max_abs(top[j], __shfl_xor_sync(0xffffffffu, top[j], off));
+    };
     if (n == 32) {
 #pragma unroll
         for (int j = 0; j < V; ++j) top[j] = warp_max(top[j]);
-        return;
-    }
-    for (int off = 1; off < n; off *= 2) {
+    } else if (n == 16) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) top[j] = max_abs(top[j], __shfl_xor_sync(0xffffffffu, top[j], off));
+        for (int off = 1; off < 16; off *= 2) step(off);
+    } else {
+        for (int off = 1; off < n; off *= 2) step(off);
     }
 }
 
