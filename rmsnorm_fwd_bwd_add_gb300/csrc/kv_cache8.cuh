@@ -67,9 +67,12 @@ template <int VE> __device__ __forceinline__ void load_floats(const float *p, fl
             f[4 * i + 2] = v.z;
             f[4 * i + 3] = v.w;
         }
+    } else if constexpr (VE == 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        f[0] = v.x;
+        f[1] = v.y;
     } else {
-#pragma unroll
-        for (int i = 0; i < VE; ++i) f[i] = p[i];
+        f[0] = p[0];
     }
 }
 
