@@ -1,5 +1,15 @@
 // kv_cache8.cuh -- kernels of the 8-bit cache: the append that rotates, quantises and
 // writes a step's tokens, and the read that brings them back.
+//
+// A head x (of k, rotated and unrounded, or of v) has a = max(max |x|, top 2^-126), scale =
+// a / top and codes round(x top / a), top = 448 (e4m3) or 127 (int8); it is read back as code *
+// scale.  Both directions are bound by memory: q, k and v are read once, q_out, codes and
+// scales written once.
+//
+// On the GB300 (6.8 TB/s copied), inputs changing from call to call: 16384 tokens of 32 + 8
+// heads of 128 (bf16, three axes, e4m3) appended in 60 us (91 % of that; 61 % of the issue
+// slots used), 8 tokens in 3.7 us (two trips to memory and the cosines); 65536 tokens of 8
+// heads of 128 read in 65 us (92 %), 77 in 2.1 us.
 #pragma once
 
 #include "quant.cuh"
