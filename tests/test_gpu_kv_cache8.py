@@ -444,3 +444,92 @@ def test_calls_of_two_threads():
     for t in threads:
         t.join()
     assert all(same)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(0, 3), (5, 0), (1, 1), (0, 1)])
+@pytest.mark.parametrize("Dh", [64, 30])
+def test_without_heads_of_one_kind(Hq, Hkv, Dh):
+    g = torch.Generator().manual_seed(14)
+    T, N = 70, 80
+    q, k, v = (torch.randn(T, h, Dh, generator=g).to(torch.bfloat16).to(DEV) for h in (Hq, Hkv, Hkv))
+    kc, vc, ks, vs = make_cache(g, N, Hkv, Dh, "i8", "dense")
+    inv, _ = rn.rope_frequencies(Dh)
+    pos, slots = torch.arange(T, device=DEV), torch.randperm(N, generator=g)[:T].to(DEV)
+    zero = torch.zeros(Dh // 2, dtype=torch.int32)
+    qo = rn.rmsnorm_kv_append(q, k, v, pos, slots, kc, vc, inv, k_scale=ks, v_scale=vs)
+    if Hq:
+        check("q", qo, *turned(q, pos[None], zero, inv, 1.0, False), Dh)
+    if Hkv:
+        wk, tk = turned(k, pos[None], zero, inv, 1.0, False)
+        check_written("k", kc, ks, slots, wk, 8e-7 * tk)
+        check_written("v", vc, vs, slots, v.double(), torch.zeros_like(wk))
+    ko, vo = rn.rmsnorm_kv_read(kc, vc, ks, vs, slots)
+    assert ko.shape == (T, Hkv, Dh) and vo.shape == (T, Hkv, Dh)
+    axes = rn.rope_sections((Dh // 4, Dh // 2 - Dh // 4))
+    both = torch.stack([pos, pos // 3])
+    a, b = rn.rmsnorm_rope_axes(q, k, both, inv, axes)
+    for got, x in ((a, q), (b, k)):
+        if x.shape[1]:
+            check("axes", got, *turned(x, both, axes, inv, 1.0, False), Dh)
+
+
+@pytest.mark.parametrize("Dh", [64, 50])
+def test_broadcast_inputs(Dh):
+    """One head shared by all, k and v the same tensor, one token repeated."""
+    g = torch.Generator().manual_seed(15)
+    T, N = 40, 50
+    one = torch.randn(T, 1, Dh, generator=g).to(torch.float16).to(DEV)
+    row = torch.randn(1, 4, Dh, generator=g).to(torch.float16).to(DEV)
+    inv, _ = rn.rope_frequencies(Dh)
+    pos, slots = torch.arange(T, device=DEV), torch.arange(T, device=DEV)
+    for q, k in ((one.expand(T, 4, Dh), one.expand(T, 3, Dh)), (row.expand(T, 4, Dh), row.expand(T, 4, Dh))):
+        got, want = (make_cache(g, N, k.shape[1], Dh, "e4m3", "dense") for _ in range(2))
+        a = rn.rmsnorm_kv_append(q, k, k, pos, slots, got[0], got[1], inv, k_scale=got[2], v_scale=got[3])
+        b = rn.rmsnorm_kv_append(q.contiguous(), k.contiguous(), k.contiguous(), pos, slots, want[0], want[1], inv,
+                                 k_scale=want[2], v_scale=want[3])
+        assert torch.equal(a, b)
+        assert all(torch.equal(bits(x)[:T], bits(y)[:T]) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("Dh,H", [(1, 3), (1, 100), (2, 33), (7, 40), (1024, 1), (1000, 5), (1023, 2), (48, 70)])
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+def test_read_head_sizes(Dh, H, fmt):
+    """From one code a head to the most, from one head to more than a warp has lanes."""
+    g = torch.Generator().manual_seed(Dh + H)
+    for T in (1, 33, 5000):
+        N = 60
+        kc, vc, ks, vs = make_cache(g, N, H, Dh, fmt, "between")
+        at = torch.randint(-1, N, (T,), generator=g).to(DEV)
+        for dt in (torch.float16, torch.float32):
+            ko, vo = rn.rmsnorm_kv_read(kc, vc, ks, vs, at, dtype=dt)
+            for got, c, s in ((ko, kc, ks), (vo, vc, vs)):
+                want = (c.float()[at] * s[at][..., None] * (at >= 0)[:, None, None]).to(dt)
+                assert torch.equal(got, want)
+
+
+def test_more_than_2_31_elements_of_q():
+    """Offsets past 2^31 elements into q and q_out; tokens are independent."""
+    T, Hq, Dh = 525_000, 32, 128
+    q = torch.zeros(T, Hq, Dh, dtype=torch.bfloat16, device=DEV)
+    k = torch.zeros(T, 1, Dh, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator().manual_seed(16)
+    at = torch.tensor([0, 262143, 262144, 524288, 524289, T - 1], device=DEV)
+    q[at] = torch.randn(6, Hq, Dh, generator=g).to(torch.bfloat16).to(DEV)
+    k[at] = torch.randn(6, 1, Dh, generator=g).to(torch.bfloat16).to(DEV)
+    inv, _ = rn.rope_frequencies(Dh)
+    axes = rn.rope_sections((16, 24, 24))
+    pos = torch.stack([torch.arange(T, device=DEV), torch.arange(T, device=DEV) % 1000, torch.arange(T, device=DEV) // 1000])
+    slots = torch.full((T,), -1, dtype=torch.int64, device=DEV)
+    slots[at] = torch.arange(6, device=DEV)
+    kc, vc, ks, vs = make_cache(g, 6, 1, Dh, "e4m3", "dense")
+    qo = rn.rmsnorm_kv_append(q, k, k, pos, slots, kc, vc, inv, k_scale=ks, v_scale=vs, pair_axis=axes)
+    wq, tq = turned(q[at], pos[:, at], axes, inv, 1.0, False)
+    check("q", qo[at], wq, tq, Dh)
+    assert int((qo != 0).any(-1).any(-1).sum()) == 6
+    wk, tk = turned(k[at], pos[:, at], axes, inv, 1.0, False)
+    check_written("k", kc, ks, slots[at], wk, 8e-7 * tk)
+    qo, ko = rn.rmsnorm_rope_axes(q, k, pos, inv, axes, q_out=qo)
+    check("q", qo[at], wq, tq, Dh)
+    check("k", ko[at], wk, tk, Dh)
+    del q, qo
+    torch.cuda.empty_cache()
