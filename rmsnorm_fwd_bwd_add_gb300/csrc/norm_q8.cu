@@ -75,7 +75,7 @@ extern "C" int rmsnorm_fwd_q8(const void *x, int64_t ld_x, const void *residual,
     const int classes = together ? classes_of(mx, rows, es) : 0;
     const bool on = rows_aligned(mx, es);
     // (weights are read in whole units where the rows' units are the columns')
-    const Q8Plan p = make_q8_plan(rows, D, es, residual != nullptr, classes, on && aligned16(w), sm);
+    const Q8Plan p = make_q8_plan(rows, D, es, residual != nullptr, group, classes, on && aligned16(w), sm);
     Q8Args a{};
     a.x = x; a.ld_x = mx.ld;
     a.res = residual; a.ld_res = mr.ld;

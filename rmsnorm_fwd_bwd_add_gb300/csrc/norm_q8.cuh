@@ -23,7 +23,7 @@
 //
 // On the GB300 (6.8 TB/s copied), inputs changing from call to call: 16384 x 8192 bf16 with
 // residual 147 us (94 % of that), 8192 x 12288 in groups of 128 109 us (96 %), 16384 x 4096
-// 77 us (90 %); without a residual 8192 x 4096 fp16 in groups of 128 21 us (72 %: 3 bytes an
+// 73 us (95 %); without a residual 8192 x 4096 fp16 in groups of 128 21 us (72 %: 3 bytes an
 // element for the same instructions, 57 % of the issue slots used by 16 warps an SM); off
 // 16-byte boundaries 16384 x 4097 79 us (88 %), 5000 x 4097 in groups 30 us (71 %: unaligned
 // weights at the start, 8.2 rows a CTA); 4 x 4096 2.2 us.

@@ -49,7 +49,7 @@ struct Q8Plan {
 
 // `classes`: 0: the row tensors stand differently to 16-byte boundaries; else they stand
 // alike, a row `classes` rows on (1, 2, 4 or 8) like this one, 1 with `aligned`: on them.
-inline Q8Plan make_q8_plan(int64_t rows, int64_t D, int es, bool residual, int classes, bool aligned, int sm) {
+inline Q8Plan make_q8_plan(int64_t rows, int64_t D, int es, bool residual, int64_t group, int classes, bool aligned, int sm) {
     Q8Plan p{};
     const int E = 16 / es;
     const int64_t units = D / E, row = D * es;
@@ -97,6 +97,11 @@ inline Q8Plan make_q8_plan(int64_t rows, int64_t D, int es, bool residual, int c
     const size_t room = Q8_SMEM_PER_SM / per_sm;
     if (room < fixed + 2 * set) return two_passes();
     p.stages = (int)std::min<size_t>({std::max<size_t>(2, 115 * 1024 / (set * per_sm)), (room - fixed) / set, (size_t)Q8_MAX_STAGES});
+    // One, where four CTAs or more have 60 KB of rows under way with it, for many rows of
+    // one scale each, which wait for memory alone (16384 x 4096: 73.0 us, 76.5 with two; x
+    // 2048: 38.7 and 40.3; fp32 68.7 and 73.0; but 2560 with 50 KB 50.7 and 49.0, 2000 rows
+    // of 4096 12.7 and 11.2, 8192 in groups of 128 42.3 and 40.4).
+    if (per_sm >= 4 && set * per_sm >= 60 * 1024 && !group && !p.shift && rows >= 8 * (int64_t)sm * per_sm) p.stages = 1;
     p.smem = Q8_HEADER + (size_t)p.stages * set;
     p.grid = (int)std::min<int64_t>(rows, (int64_t)sm * per_sm);
     if (p.shift && classes > 1) {  // a CTA's rows all stand the same way

@@ -278,7 +278,7 @@ def test_all_tensors_at_one_offset(rows, D, group, dt):
 
 def test_more_rows_than_a_ring_goes_round():
     """Many rows a CTA, each unlike its neighbours."""
-    for rows, D, dt, group in ((20000, 1536, torch.bfloat16, 0), (9001, 4097, torch.float16, 64), (6000, 2048, torch.float32, 128),
+    for rows, D, dt, group in ((5001, 4096, torch.bfloat16, 0), (9999, 2048, torch.float16, 0), (20000, 1536, torch.bfloat16, 0), (9001, 4097, torch.float16, 64), (6000, 2048, torch.float32, 128),
                                (40000, 256, torch.bfloat16, 32)):
         g = torch.Generator().manual_seed(rows)
         x, res = _rows(g, rows, D, dt), _rows(g, rows, D, dt)
@@ -286,12 +286,12 @@ def test_more_rows_than_a_ring_goes_round():
         _check(rn.rmsnorm_fwd_q8(x, w, EPS, 0.0, res, group=group), x, res, w, 0.0, group)
 
 
-@pytest.mark.parametrize("D,group", [(4096, 0), (4096, 128), (4097, 64)])
-def test_wait_timeout_is_reported_and_context_survives(D, group):
+@pytest.mark.parametrize("rows,D,group", [(3000, 4096, 0), (6000, 4096, 0), (3000, 4096, 128), (3000, 4097, 64)])
+def test_wait_timeout_is_reported_and_context_survives(rows, D, group):
     """A row whose copies are never issued: the wait ends, the status says so, and the
     next call is right."""
     g = torch.Generator().manual_seed(6)
-    x, res = _rows(g, 3000, D, torch.bfloat16), _rows(g, 3000, D, torch.bfloat16)
+    x, res = _rows(g, rows, D, torch.bfloat16), _rows(g, rows, D, torch.bfloat16)
     w = torch.ones(D, dtype=torch.bfloat16, device=DEV)
     rn.rmsnorm_device_status(clear=True)
     rn.rmsnorm_debug_inject(drop_tile=1501, budget_cycles=2_000_000)

@@ -193,3 +193,36 @@ def test_written_tensors_count_as_changed():
     rn.rmsnorm_rope_axes(q, k, torch.zeros(2, 4, dtype=torch.int64, device=DEV), rn.rope_frequencies(16)[0],
                          rn.rope_sections((4, 4)), q_out=qo, k_out=ko)
     assert [t._version for t in (qo, ko, q)] == [before[0] + 1, before[1] + 1, before[2]]
+
+
+def test_forward_and_backward_captured_together():
+    """Replayed with other inputs, positions and gradients."""
+    g = torch.Generator().manual_seed(12)
+    axis = rn.rope_sections((6, 5, 5))
+    inv, _ = rn.rope_frequencies(32)
+    q = torch.randn(2, 40, 3, 48, generator=g).to(torch.bfloat16).to(DEV).requires_grad_()
+    gq = torch.randn(2, 40, 3, 48, generator=g).to(torch.bfloat16).to(DEV)
+    pos = torch.randint(0, 9000, (3, 2, 40), generator=g).to(DEV)
+
+    def step():
+        out = rn.rope(q, None, pos, inv, 1.0, True, axis)[0]
+        return out, torch.autograd.grad(out, q, gq)[0]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(s)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out, dq = step()
+    for k in range(2):
+        with torch.no_grad():
+            q.mul_(-1.5)
+            gq.add_(0.25)
+            pos.add_(1000)
+        gr.replay()
+        torch.cuda.synchronize()
+        check("out", out, *turned(q.detach(), pos, axis, inv, 1.0, True), 32)
+        check("dq", dq, *turned(gq, pos, axis, inv, 1.0, True, -1.0), 32)

@@ -189,11 +189,11 @@ int main() {
     for (long D : lengths)
         for (long rows : {1, 2, 5, 152, 153, 303, 304, 305, 607, 609, 1216, 1217, 4000, 100000})
             for (int es : {2, 4})
-                for (int res = 0; res < 2; ++res)
+                for (int res = 0; res < 4; ++res)  // bit 1: in groups
                     for (int classes : {0, 1, 2, 4, 8})
                         for (int aligned = 0; aligned < 2; ++aligned) {
                             if (aligned && classes != 1) continue;
-                            const Q8Plan p = make_q8_plan(rows, D, es, res, classes, aligned, 152);
+                            const Q8Plan p = make_q8_plan(rows, D, es, res & 1, res & 2 ? 64 : 0, classes, aligned, 152);
                             const long E = 16 / es, units = D / E;
                             bool ok = q8_plan_ok(p) && p.grid <= rows;
                             const bool held = p.kind == Q8_DIRECT || p.kind == Q8_STAGED;
@@ -210,7 +210,7 @@ int main() {
                                 const long groups = p.shift ? 3 * 4 * (cap * p.units * E / 32 + 2) : 12;
                                 const long fixed = groups + 2 * 8 * (cap / 32);
                                 ok = ok && (long)p.stage_bytes >= need && p.stage_bytes % 16 == 0;
-                                ok = ok && (long)p.smem == Q8_HEADER + (long)p.stages * (res ? 2 : 1) * p.stage_bytes;
+                                ok = ok && (long)p.smem == Q8_HEADER + (long)p.stages * (res & 1 ? 2 : 1) * p.stage_bytes;
                                 ok = ok && (long)p.smem + fixed <= 227 * 1024 && p.stages * 8 <= Q8_HEADER;
                                 const int per_sm = (p.grid + 151) / 152;
                                 ok = ok && per_sm * ((long)p.smem + fixed + 1024) <= 228 * 1024 && per_sm * p.threads <= 512;
