@@ -38,7 +38,9 @@ cudaError_t launch_append8_vectors(const AppendArgs &a, int sm, cudaStream_t s) 
 }
 
 // Smaller units: fewer lanes a head leave each step less work beside its elements (4096
-// tokens of 32 + 8 heads of 100 in 4-byte units: 66 us with 4 elements a lane, 30 with 16).
+// tokens of 32 + 8 heads of 100 in 4-byte units: 53 us with 4 elements a lane, 36 with 8, 31
+// with 16), until they spill (of 126 in single elements 60 us with 4, 46 with 8, 62 with 16,
+// which the longest heads need).
 template <typename T, bool INTERLEAVED, int FMT>
 cudaError_t launch_append8_layout(const AppendArgs &a, int unit, int sm, cudaStream_t s) {
     if (unit == 16) return launch_append8_vectors<T, INTERLEAVED, FMT>(a, sm, s);
@@ -48,6 +50,7 @@ cudaError_t launch_append8_layout(const AppendArgs &a, int unit, int sm, cudaStr
             if (lanes <= 128) return launch_append8_units<T, 4, INTERLEAVED, FMT, 4>(a, lanes, sm, s);
         }
     const int lanes = head_lanes<1, INTERLEAVED>(a);
+    if (lanes <= 128) return launch_append8_units<T, (int)sizeof(T), INTERLEAVED, FMT, 4>(a, lanes, sm, s);
     if (lanes <= 256) return launch_append8_units<T, (int)sizeof(T), INTERLEAVED, FMT, 8>(a, lanes, sm, s);
     const int64_t warps = a.T * (a.Hq + 2 * (int64_t)a.Hkv);
     const dim3 grid((unsigned)std::min<int64_t>((warps + C8_NT / 32 - 1) / (C8_NT / 32), 8 * (int64_t)sm));

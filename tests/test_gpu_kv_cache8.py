@@ -85,6 +85,7 @@ CASES = [  # T, Hq, Hkv, Dh, sections
     # long runs of tokens a warp, heads that leave lanes idle, parts of a token without q or k heads
     (5000, 8, 1, 128, (64,)), (6001, 3, 1, 64, (8, 12, 12)), (4901, 2, 2, 100, (50,)), (3000, 5, 3, 126, (63,)),
     (2, 64, 1, 64, (32,)), (3, 1, 40, 16, (8,)), (1, 130, 2, 128, (64,)), (33, 2, 70, 24, (12,)), (11, 9, 4, 112, (56,)),
+    (300, 4, 2, 127, (63,)), (40, 3, 2, 250, (125,)), (30, 2, 1, 257, (128,)), (9, 2, 2, 511, (10, 245)), (50, 5, 3, 36, (9, 9)),
 ]
 
 

@@ -258,6 +258,7 @@ int main() {
                     if (Dh % 8 == 0 && Dh / 8 <= 64) ok = ok && append_ok<16, 2>(T, Dh, Dh / 8, Hq, Hkv, pairs, 4);
                     if (Dh % 8 == 0) ok = ok && append_ok<16, 4>(T, Dh, Dh / 8, Hq, Hkv, pairs, 4);
                     if ((Dh + 3) / 4 <= 128) ok = ok && append_ok<4, 4>(T, Dh, (Dh + 3) / 4, Hq, Hkv, pairs, 2);
+                    if (odd <= 128) ok = ok && append_ok<2, 4>(T, Dh, odd, Hq, Hkv, pairs, 2) && append_ok<4, 4>(T, Dh, odd, Hq, Hkv, pairs, 4);
                     if (odd <= 256) ok = ok && append_ok<2, 8>(T, Dh, odd, Hq, Hkv, pairs, 2) && append_ok<4, 8>(T, Dh, odd, Hq, Hkv, pairs, 4);
                     if (Hkv)
                         for (int C : {1, 2, 4, 8}) {
