@@ -463,7 +463,9 @@ typedef enum {
  *                RMSNORM_CACHE_SAME, whose values are rounded to dtype instead.
  * A head that holds a NaN or an infinity has a scale that is NaN or infinite, and each of
  * its code_j * scale is NaN.  Caches and scales may not overlap each other, the inputs or
- * q_out; skipped tokens and errors as for rmsnorm_rope_kv_append_ex.
+ * q_out.  The slots of one call are distinct, else that row's codes and scales are of either
+ * token.  Skipped tokens and errors as for rmsnorm_rope_kv_append_ex; a negative position on
+ * any axis skips the token.
  */
 int rmsnorm_kv_append(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
                       const void *v, const int64_t *v_strides, const int64_t *positions, int axes,

@@ -122,7 +122,7 @@ template <int VB, int UPL> __host__ __device__ inline int append8_step_bytes(int
     return VB == 16 ? 2 * UPL * 32 * VB : 32 / cw * append8_head_bytes(head_bytes);
 }
 template <int VB, int UPL, int FMT> __host__ __device__ constexpr int append8_ring() {
-    constexpr int n = VB == 16 ? (FMT == RMSNORM_CACHE_SAME ? 2048 : 3072) / (2 * UPL * 32 * VB) : 4;
+    constexpr int n = VB == 16 ? (FMT == RMSNORM_CACHE_SAME ? 2 : 3) * 1024 / (2 * UPL * 32 * VB) : 4;
     return n < 2 ? 2 : n;
 }
 
@@ -136,10 +136,10 @@ __host__ __device__ constexpr int append8_plane(int rot) { return (rot / 2 + 3) 
 // FMT is RMSNORM_CACHE_SAME for caches of the inputs' type and, without slots, for
 // rmsnorm_rope_axes, whose k stays with its token (VB = 16 alone).
 //
-// A warp takes a token (or one of a token's `wpt` parts, from token `whole` on), 32 / cw heads a step: cw lanes a
-// head, UPL units of two vectors each a lane (rope_ex.cuh's units), so that a head's
-// largest value is a few shuffles away.  The token's cosines and sines are computed by the
-// warp's lanes together, once for all of its heads.
+// A warp takes a token (or one of a token's `wpt` parts, from token `whole` on), 32 / cw
+// heads a step: cw lanes a head, UPL units of two vectors each a lane (rope_ex.cuh's
+// units), so that a head's largest value is a few shuffles away.  The token's cosines and
+// sines are computed by the warp's lanes together, once for all of its heads.
 //
 // A lane copies its vectors of the steps to come, through all of its tokens, into a ring
 // of its own in shared memory: with two batches of steps in registers instead a warp
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
         }
         __syncwarp();
         // Unit i of a head turned.  (Its cosines and sines come from shared memory each
-        // time: in registers they left an SM 16 warps instead of 24.)
+        // time: 16 registers for whole vectors.)
         auto turn = [&](int i, float (&fa)[VE], float (&fb)[VE]) {
             if constexpr (PAIRED) {
                 auto pairs = [&](float (&f)[VE], int from) {
@@ -439,8 +439,8 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Any stride, alignment and head: a warp a head of a token, a lane its elements 32
-// apart, which a head of k or v computes twice: for its largest and for its codes.
+// Heads too long for the ring's single elements (over 512, off 16- and 4-byte units): a
+// warp a head of a token, a lane its elements 32 apart, which a head of k or v computes twice: for its largest and for its codes.
 template <typename T, int FMT, bool INTERLEAVED>
 __global__ void __launch_bounds__(C8_NT) append8_generic_kernel(const __grid_constant__ AppendArgs a) {
     const int lane = threadIdx.x & 31, half = a.rot / 2;
