@@ -12,6 +12,7 @@ template <typename T> cudaError_t launch_append8(const AppendArgs &a, int format
 
 template <typename T, int VB, bool INTERLEAVED, int FMT, int UPL>
 cudaError_t launch_append8_units(const AppendArgs &a, int lanes, int sm, cudaStream_t s) {
+    if (lanes < 1 || lanes > 32 * UPL) return cudaErrorInvalidConfiguration;  // a head's lanes are a warp's
     static std::atomic<uint64_t> smem_mask{0};
     auto kern = append8_kernel<T, VB, INTERLEAVED, FMT, UPL>;
     const cudaError_t e = allow_max_dynamic_smem((const void *)kern, smem_mask);
@@ -24,15 +25,22 @@ cudaError_t launch_append8_units(const AppendArgs &a, int lanes, int sm, cudaStr
 }
 
 // Lanes of a head in units of VE elements.
-template <int VE, bool INTERLEAVED> int head_lanes(const AppendArgs &a) {
-    return HeadMap<VE, (INTERLEAVED && VE > 1), INTERLEAVED>(a.Dh, a.rot).lanes;
+template <int VE, bool INTERLEAVED> int head_lanes(int Dh, int rot) {
+    return HeadMap<VE, (INTERLEAVED && VE > 1), INTERLEAVED>(Dh, rot).lanes;
+}
+
+// Whether a warp's lanes hold a head in 16-byte units.  An odd number of vectors in both
+// its parts takes a lane more than their sum: one of 1024 elements then does not fit.
+template <typename T, bool INTERLEAVED> bool append8_vectors_fit(int Dh, int rot) {
+    constexpr int E = 16 / (int)sizeof(T);
+    return head_lanes<E, INTERLEAVED>(Dh, rot) <= 32 * (16 / E);
 }
 
 // Heads in 16-byte units, 16 elements a lane while a head's lanes are a warp's.
 template <typename T, bool INTERLEAVED, int FMT>
 cudaError_t launch_append8_vectors(const AppendArgs &a, int sm, cudaStream_t s) {
     constexpr int E = 16 / (int)sizeof(T);
-    const int lanes = head_lanes<E, INTERLEAVED>(a);
+    const int lanes = head_lanes<E, INTERLEAVED>(a.Dh, a.rot);
     if (lanes <= 32 * (8 / E)) return launch_append8_units<T, 16, INTERLEAVED, FMT, 8 / E>(a, lanes, sm, s);
     return launch_append8_units<T, 16, INTERLEAVED, FMT, 16 / E>(a, lanes, sm, s);
 }
@@ -43,13 +51,13 @@ cudaError_t launch_append8_vectors(const AppendArgs &a, int sm, cudaStream_t s) 
 // which the longest heads need).
 template <typename T, bool INTERLEAVED, int FMT>
 cudaError_t launch_append8_layout(const AppendArgs &a, int unit, int sm, cudaStream_t s) {
-    if (unit == 16) return launch_append8_vectors<T, INTERLEAVED, FMT>(a, sm, s);
+    if (unit == 16 && append8_vectors_fit<T, INTERLEAVED>(a.Dh, a.rot)) return launch_append8_vectors<T, INTERLEAVED, FMT>(a, sm, s);
     if constexpr (sizeof(T) == 2)
-        if (unit == 4) {
-            const int lanes = head_lanes<2, INTERLEAVED>(a);
+        if (unit >= 4) {
+            const int lanes = head_lanes<2, INTERLEAVED>(a.Dh, a.rot);
             if (lanes <= 128) return launch_append8_units<T, 4, INTERLEAVED, FMT, 4>(a, lanes, sm, s);
         }
-    const int lanes = head_lanes<1, INTERLEAVED>(a);
+    const int lanes = head_lanes<1, INTERLEAVED>(a.Dh, a.rot);
     if (lanes <= 128) return launch_append8_units<T, (int)sizeof(T), INTERLEAVED, FMT, 4>(a, lanes, sm, s);
     if (lanes <= 256) return launch_append8_units<T, (int)sizeof(T), INTERLEAVED, FMT, 8>(a, lanes, sm, s);
     const int64_t warps = a.T * (a.Hq + 2 * (int64_t)a.Hkv);

@@ -21,7 +21,8 @@ template <typename T> cudaError_t launch_small(const RopeArgs<true> &a, bool int
 }
 
 template <typename T> cudaError_t launch_axes(const RopeArgs<true> &a, bool interleaved, int unit, int sm, cudaStream_t s) {
-    if (unit < 16) return launch_small<T>(a, interleaved, unit, sm, s);
+    const bool fits = interleaved ? append8_vectors_fit<T, true>(a.Dh, a.rot) : append8_vectors_fit<T, false>(a.Dh, a.rot);
+    if (unit < 16 || !fits) return launch_small<T>(a, interleaved, unit, sm, s);
     AppendArgs b{};
     static_cast<RopeArgs<true> &>(b) = a;
     return interleaved ? launch_append8_vectors<T, true, RMSNORM_CACHE_SAME>(b, sm, s)

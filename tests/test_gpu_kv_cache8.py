@@ -86,6 +86,7 @@ CASES = [  # T, Hq, Hkv, Dh, sections
     (5000, 8, 1, 128, (64,)), (6001, 3, 1, 64, (8, 12, 12)), (4901, 2, 2, 100, (50,)), (3000, 5, 3, 126, (63,)),
     (2, 64, 1, 64, (32,)), (3, 1, 40, 16, (8,)), (1, 130, 2, 128, (64,)), (33, 2, 70, 24, (12,)), (11, 9, 4, 112, (56,)),
     (300, 4, 2, 127, (63,)), (40, 3, 2, 250, (125,)), (30, 2, 1, 257, (128,)), (9, 2, 2, 511, (10, 245)), (50, 5, 3, 36, (9, 9)),
+    (9, 2, 2, 1024, (300,)), (5, 3, 1, 1024, (52, 50)), (7, 2, 1, 1016, (4, 200)),
 ]
 
 
@@ -144,25 +145,35 @@ def test_append_and_read(T, Hq, Hkv, Dh, sections, interleaved, fmt, dt):
 
 
 @pytest.mark.parametrize("axes", [1, 3])
-def test_append_to_a_cache_of_the_inputs_type(axes):
+@pytest.mark.parametrize("Dh,rot,T", [(96, 64, 100), (30, 20, 70), (64, 64, 3000), (1024, 600, 9), (42, 42, 2500)])
+@pytest.mark.parametrize("interleaved", [False, True], ids=["half", "inter"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_append_to_a_cache_of_the_inputs_type(axes, Dh, rot, T, interleaved, dt):
     """Without scales: rmsnorm_rope_kv_append_ex, with axes the rotation of rmsnorm_rope_axes."""
     g = torch.Generator().manual_seed(3)
-    T, Hq, Hkv, Dh = 100, 8, 2, 96
-    q, k, v = (torch.randn(T, h, Dh, generator=g).to(torch.bfloat16).to(DEV) for h in (Hq, Hkv, Hkv))
-    kc, vc = (torch.randn(T + 5, Hkv, Dh, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
-    inv, _ = rn.rope_frequencies(64)
-    slots = torch.randperm(T + 5, generator=g)[:T].to(DEV)
+    Hq, Hkv = 8, 2
+    q, k, v = (torch.randn(T, h, Dh, generator=g).to(DT[dt]).to(DEV) for h in (Hq, Hkv, Hkv))
+    kc, vc = (torch.randn(T + 5, Hkv, Dh, generator=g).to(DT[dt]).to(DEV) for _ in range(2))
+    inv, _ = rn.rope_frequencies(rot)
+    slots = torch.randperm(T + 5, generator=g)[:T]
+    slots[::7] = -1
+    slots = slots.to(DEV)
     pos = torch.randint(0, 9000, (axes, T), generator=g).to(DEV)
     k2, v2 = kc.clone(), vc.clone()
     if axes == 1:
-        a = rn.rmsnorm_kv_append(q, k, v, pos[0], slots, kc, vc, inv)
-        b = rn.rmsnorm_rope_kv_append_ex(q, k, v, pos[0], slots, k2, v2, inv)
+        a = rn.rmsnorm_kv_append(q, k, v, pos[0], slots, kc, vc, inv, interleaved=interleaved)
+        b = rn.rmsnorm_rope_kv_append_ex(q, k, v, pos[0], slots, k2, v2, inv, interleaved=interleaved)
     else:
-        axis = rn.rope_sections((10, 11, 11), in_turn=True)
-        a = rn.rmsnorm_kv_append(q, k, v, pos, slots, kc, vc, inv, pair_axis=axis)
-        b, kr = rn.rmsnorm_rope_axes(q, k, pos, inv, axis)
-        k2[slots], v2[slots] = kr, v
+        axis = rn.rope_sections((rot // 2 - 2 * (rot // 6), rot // 6, rot // 6), in_turn=True)
+        a = rn.rmsnorm_kv_append(q, k, v, pos, slots, kc, vc, inv, pair_axis=axis, interleaved=interleaved)
+        b, kr = rn.rmsnorm_rope_axes(q, k, pos, inv, axis, interleaved=interleaved)
+        kept = slots >= 0
+        k2[slots[kept]], v2[slots[kept]] = kr[kept], v[kept]
     assert torch.equal(a, b) and torch.equal(kc, k2) and torch.equal(vc, v2)
+    before = a.clone()
+    rn.rmsnorm_kv_append(q, k, v, pos if axes > 1 else pos[0], slots, kc, vc, inv, interleaved=interleaved, q_out=q,
+                         pair_axis=axis if axes > 1 else None)
+    assert torch.equal(q, before) and torch.equal(kc, k2)
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "i8"])

@@ -52,6 +52,7 @@ CASES = [  # B, S, Hq, Hkv, Dh, sections
     (3, 50, 6, 3, 80, (20, 20)), (1, 129, 5, 1, 96, (1, 46, 1)), (2, 33, 2, 2, 22, (2, 1, 1, 1)),
     (1, 17, 2, 1, 1024, (100, 200, 100, 112)), (1, 5000, 4, 1, 64, (8, 12, 12)), (1, 64, 1, 0, 128, (30, 34)),
     (1, 2433, 24, 2, 32, (5, 11)), (1, 40, 3, 1, 30, (1,)),
+    (1, 9, 2, 1, 1024, (100, 100, 100)), (2, 5, 1, 2, 1024, (6, 96)),
 ]
 
 

@@ -276,3 +276,34 @@ int main() {
     return 0;
 }
 """)
+
+
+def test_every_head_has_lanes(tmp_path):
+    """A head that is sent to an instance fits its lanes, whatever part of it turns."""
+    run_host(tmp_path, r"""
+#include <cstdio>
+#include "kv_append8.h"
+using namespace rmsn;
+template <typename T, bool I> bool ok(int Dh, int rot) {
+    constexpr int E = 16 / (int)sizeof(T);
+    const int lanes = head_lanes<E, I>(Dh, rot);
+    // whole vectors, as the dispatch asks for
+    if (Dh % E || (I ? rot : rot / 2) % E) return true;
+    if (!append8_vectors_fit<T, I>(Dh, rot)) return Dh > 1000;  // smaller units
+    const int upl = lanes <= 32 * (8 / E) ? 8 / E : 16 / E, cw = (lanes + upl - 1) / upl;
+    return cw >= 1 && cw <= 32;
+}
+int main() {
+    int left = 0;
+    for (int Dh = 2; Dh <= 1024; ++Dh)
+        for (int rot = 2; rot <= Dh; rot += 2) {
+            if (!(ok<__half, false>(Dh, rot) && ok<__half, true>(Dh, rot) && ok<float, false>(Dh, rot) && ok<float, true>(Dh, rot))) {
+                printf("Dh %d rot %d", Dh, rot);
+                return 1;
+            }
+            left += Dh == 1024 && rot % 8 == 0 && !append8_vectors_fit<__half, true>(Dh, rot);
+        }
+    printf("no head of 1024 with odd parts met");
+    return left > 0 ? 0 : 1;
+}
+""")
