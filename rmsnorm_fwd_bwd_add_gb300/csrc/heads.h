@@ -92,10 +92,14 @@ inline uintptr_t byte_bits(const Heads &h, int64_t B, int64_t S, int64_t H, int 
            (uintptr_t)((H > 1 ? h.sh : 0) * es);
 }
 
-inline Heads heads(const void *p, const int64_t *st, int n, int es) {
+// The stride of a single head counts for nothing, here as in byte_bits: lanes of a warp
+// whose places lie behind the heads form addresses with it, in units that it need not
+// divide, and read shared memory there.
+inline Heads heads(const void *p, const int64_t *st, int n, int es, int64_t H) {
     // n = 3: batch, token, head; n = 2: token, head
-    return p && st ? Heads{p, n == 3 ? st[0] : 0, st[n - 2], st[n - 1], (uint32_t)(st[n - 1] * es)}
-                   : Heads{nullptr, 0, 0, 0, 0};
+    if (!p || !st) return Heads{nullptr, 0, 0, 0, 0};
+    const int64_t sh = H > 1 ? st[n - 1] : 0;
+    return Heads{p, n == 3 ? st[0] : 0, st[n - 2], sh, (uint32_t)(sh * es)};
 }
 
 }  // namespace rmsn

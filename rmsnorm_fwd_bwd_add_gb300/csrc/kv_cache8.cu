@@ -92,10 +92,11 @@ extern "C" int rmsnorm_kv_append(const void *q, const int64_t *q_strides, const 
         return RMSNORM_ERR_INVALID_ARG;
     const Heads none{nullptr, 0, 0, 0, 0};
     const int es = esize_of(dtype), cs = same ? es : 1;
-    const Heads hq = Hq ? heads(q, q_strides, 2, es) : none, hqo = Hq ? heads(q_out, q_out_strides, 2, es) : none;
-    const Heads hk = Hkv ? heads(k, k_strides, 2, es) : none, hv = Hkv ? heads(v, v_strides, 2, es) : none;
-    const Heads hkc = Hkv ? heads(k_cache, k_cache_strides, 2, cs) : none;
-    const Heads hvc = Hkv ? heads(v_cache, v_cache_strides, 2, cs) : none;
+    const Heads hq = Hq ? heads(q, q_strides, 2, es, Hq) : none;
+    const Heads hqo = Hq ? heads(q_out, q_out_strides, 2, es, Hq) : none;
+    const Heads hk = Hkv ? heads(k, k_strides, 2, es, Hkv) : none, hv = Hkv ? heads(v, v_strides, 2, es, Hkv) : none;
+    const Heads hkc = Hkv ? heads(k_cache, k_cache_strides, 2, cs, Hkv) : none;
+    const Heads hvc = Hkv ? heads(v_cache, v_cache_strides, 2, cs, Hkv) : none;
     const PairAxes pair_axes{axes, pair_axis};
     if (same)
         return rope_run(hq, hk, hv, positions, pair_axes, slots, hqo, hkc, hvc, inv_freq, attn_scale, interleaved, 0, 1,
@@ -166,8 +167,8 @@ extern "C" int rmsnorm_kv_read(const void *k_cache, const int64_t *k_cache_strid
                           !k_scale_strides || !v_scale_strides))
         return RMSNORM_ERR_INVALID_ARG;
     const int es = esize_of(dtype);
-    const Heads hk = heads(k_cache, k_cache_strides, 2, 1), hv = heads(v_cache, v_cache_strides, 2, 1);
-    const Heads hko = heads(k_out, k_out_strides, 2, es), hvo = heads(v_out, v_out_strides, 2, es);
+    const Heads hk = heads(k_cache, k_cache_strides, 2, 1, Hkv), hv = heads(v_cache, v_cache_strides, 2, 1, Hkv);
+    const Heads hko = heads(k_out, k_out_strides, 2, es, Hkv), hvo = heads(v_out, v_out_strides, 2, es, Hkv);
     const Scales ks = scales(k_scale, k_scale_strides), vs = scales(v_scale, v_scale_strides);
     Span sk, sv, sks, svs, sko, svo;
     int st = span_of(hk, 1, num_slots, Hkv, Dh, 1, false, &sk);

@@ -124,9 +124,9 @@ extern "C" int rmsnorm_rope(const void *q, const int64_t *q_strides, const void 
         return RMSNORM_ERR_INVALID_ARG;
     const Heads none{nullptr, 0, 0, 0, 0};
     const int es = esize_of(dtype);
-    return rope_run(Hq ? heads(q, q_strides, 3, es) : none, Hkv ? heads(k, k_strides, 3, es) : none, none, positions,
-                    PairAxes{}, nullptr, Hq ? heads(q_out, q_out_strides, 3, es) : none,
-                    Hkv ? heads(k_out, k_out_strides, 3, es) : none, none, inv_freq, attn_scale, interleaved,
+    return rope_run(Hq ? heads(q, q_strides, 3, es, Hq) : none, Hkv ? heads(k, k_strides, 3, es, Hkv) : none, none,
+                    positions, PairAxes{}, nullptr, Hq ? heads(q_out, q_out_strides, 3, es, Hq) : none,
+                    Hkv ? heads(k_out, k_out_strides, 3, es, Hkv) : none, none, inv_freq, attn_scale, interleaved,
                     inverse, B, S, Hq, Hkv, Dh, rot_dim, 0, dtype, stream);
 }
 
@@ -145,9 +145,9 @@ extern "C" int rmsnorm_rope_axes(const void *q, const int64_t *q_strides, const 
         return RMSNORM_ERR_INVALID_ARG;
     const Heads none{nullptr, 0, 0, 0, 0};
     const int es = esize_of(dtype);
-    return rope_run(Hq ? heads(q, q_strides, 3, es) : none, Hkv ? heads(k, k_strides, 3, es) : none, none, positions,
-                    PairAxes{axes, pair_axis}, nullptr, Hq ? heads(q_out, q_out_strides, 3, es) : none,
-                    Hkv ? heads(k_out, k_out_strides, 3, es) : none, none, inv_freq, attn_scale, interleaved,
+    return rope_run(Hq ? heads(q, q_strides, 3, es, Hq) : none, Hkv ? heads(k, k_strides, 3, es, Hkv) : none, none,
+                    positions, PairAxes{axes, pair_axis}, nullptr, Hq ? heads(q_out, q_out_strides, 3, es, Hq) : none,
+                    Hkv ? heads(k_out, k_out_strides, 3, es, Hkv) : none, none, inv_freq, attn_scale, interleaved,
                     inverse, B, S, Hq, Hkv, Dh, rot_dim, 0, dtype, stream);
 }
 
@@ -170,11 +170,12 @@ extern "C" int rmsnorm_rope_kv_append_ex(const void *q, const int64_t *q_strides
         return RMSNORM_ERR_INVALID_ARG;
     const Heads none{nullptr, 0, 0, 0, 0};
     const int es = esize_of(dtype);
-    return rope_run(Hq ? heads(q, q_strides, 2, es) : none, Hkv ? heads(k, k_strides, 2, es) : none,
-                    Hkv ? heads(v, v_strides, 2, es) : none, positions, PairAxes{}, slots,
-                    Hq ? heads(q_out, q_out_strides, 2, es) : none, Hkv ? heads(k_cache, k_cache_strides, 2, es) : none,
-                    Hkv ? heads(v_cache, v_cache_strides, 2, es) : none, inv_freq, attn_scale, interleaved, 0, 1, T,
-                    Hq, Hkv, Dh, rot_dim, num_slots, dtype, stream);
+    return rope_run(Hq ? heads(q, q_strides, 2, es, Hq) : none, Hkv ? heads(k, k_strides, 2, es, Hkv) : none,
+                    Hkv ? heads(v, v_strides, 2, es, Hkv) : none, positions, PairAxes{}, slots,
+                    Hq ? heads(q_out, q_out_strides, 2, es, Hq) : none,
+                    Hkv ? heads(k_cache, k_cache_strides, 2, es, Hkv) : none,
+                    Hkv ? heads(v_cache, v_cache_strides, 2, es, Hkv) : none, inv_freq, attn_scale, interleaved, 0, 1,
+                    T, Hq, Hkv, Dh, rot_dim, num_slots, dtype, stream);
 }
 
 extern "C" int rmsnorm_rope_frequencies(int scaling, int64_t rot_dim, double base, double factor,
