@@ -51,19 +51,19 @@ template <> struct CodeWord<4> { using type = uint32_t; };
 template <> struct CodeWord<2> { using type = uint16_t; };
 template <> struct CodeWord<1> { using type = uint8_t; };
 
-template <int FMT, int VE> __device__ __forceinline__ typename CodeWord<VE>::type code_word(const float (&f)[VE], float by) {
+template <int FMT, int VE> __device__ __forceinline__ typename CodeWord<VE>::type code_word(const float (&f)[VE], float2 by) {
     if constexpr (VE >= 4) {
         uint32_t c[VE / 4];
 #pragma unroll
         for (int i = 0; i < VE / 4; ++i) {
-            const float2 x = f2mul(make_float2(f[4 * i], f[4 * i + 1]), make_float2(by, by));
-            const float2 y = f2mul(make_float2(f[4 * i + 2], f[4 * i + 3]), make_float2(by, by));
+            const float2 x = in_codes(make_float2(f[4 * i], f[4 * i + 1]), by);
+            const float2 y = in_codes(make_float2(f[4 * i + 2], f[4 * i + 3]), by);
             c[i] = code_quad<FMT>(x.x, x.y, y.x, y.y);
         }
         if constexpr (VE == 8) return make_uint2(c[0], c[1]);
         else return c[0];
     } else {
-        return (typename CodeWord<VE>::type)code_pair<FMT>(f[0] * by, VE == 2 ? f[VE - 1] * by : 0.f);
+        return (typename CodeWord<VE>::type)code_pair<FMT>(in_codes(f[0], by), VE == 2 ? in_codes(f[VE - 1], by) : 0.f);
     }
 }
 
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
                         for (int e = 0; e < VE; ++e) top = max_abs(top, fa[e], fb[e]);
                     }
                 const float most = scaled_top<FMT>(head_max(top));
-                const float by = code_factor<FMT>(most);
+                const float2 by = code_factor<FMT>(most);
                 if (!mine || hs >= hpi) return;
                 unsigned char *dst = (unsigned char *)cache.p + (slot * cache.st + (uint64_t)(uint32_t)h * cache.head_bytes);
 #pragma unroll
@@ -490,11 +490,11 @@ __global__ void __launch_bounds__(C8_NT) append8_generic_kernel(const __grid_con
         float top = 0.f;
         each([&](int, float u, int, float w) { top = max_abs(top, u, w); });
         const float most = scaled_top<FMT>(warp_max(top));
-        const float by = code_factor<FMT>(most);
+        const float2 by = code_factor<FMT>(most);
         const Heads &dst = what == 1 ? a.k_out : a.v_out;
         uint8_t *o = static_cast<uint8_t *>(const_cast<void *>(dst.p)) + slot * dst.st + hk * dst.sh;
         each([&](int i, float u, int j, float w) {
-            const uint32_t c = code_pair<FMT>(u * by, w * by);
+            const uint32_t c = code_pair<FMT>(in_codes(u, by), in_codes(w, by));
             o[i] = (uint8_t)c;
             if (j >= 0) o[j] = (uint8_t)(c >> 8);
         });

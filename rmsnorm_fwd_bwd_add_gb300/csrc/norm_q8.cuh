@@ -36,10 +36,14 @@
 
 namespace rmsn {
 
-// The scale of a group and the factor of its codes.
+// The scale of a group and the factor of its codes, its first part alone: v is rounded before
+// it, so that few quotients are borders of codes still (5000 x 4097 with residual in groups
+// of 128: of 41 million codes 245 are not those of 64 bits, 366 in the plain form in fp32,
+// 185 with both parts, which take 33.4 us where this takes 30.0, and 8192 x 4096 without
+// residual 22.0 where this takes 21.0).
 __device__ __forceinline__ float2 q8_scale(float top, float r) {
     const float a = scaled_top<RMSNORM_CACHE_E4M3>(top);
-    return make_float2(r * a * (1.f / 448.f), code_factor<RMSNORM_CACHE_E4M3>(a));
+    return make_float2(r * a * (1.f / 448.f), code_factor<RMSNORM_CACHE_E4M3>(a).x);
 }
 
 // The 8 (16-bit inputs) or 4 codes of a unit, P pairs of values, stored if `in`.
