@@ -25,21 +25,6 @@ struct Scales {
     int64_t st, sh;
 };
 
-// cos_sin for values that become codes: what the reduced angle loses in its last addition
-// (2^-26 turns, three times the error of the sines themselves) is added to first order:
-// of 17 million codes of k 24 to 33 then differ from those of 64-bit values, 45 without it
-// (13 to 32 from torch's cosines of 64-bit angles), and many times that with the SFU's
-// sines (2^-21).
-__device__ __forceinline__ float2 cos_sin_of_codes(float2 p, float2 f) {
-    const float s = p.x * f.x, e = fmaf(p.x, f.x, -s), r = s - rintf(s);  // e, r: exact
-    const float c = fmaf(p.x, f.y, fmaf(p.y, f.x, e));
-    const float a = r + c, bb = a - r, lost = (r - (a - bb)) + (c - bb);  // r + c = a + lost (Knuth's two-sum)
-    float2 cs;
-    sincospif(2.f * a, &cs.y, &cs.x);
-    const float d = 6.2831853071795865f * lost;
-    return make_float2(fmaf(-d, cs.y, cs.x), fmaf(d, cs.x, cs.y));
-}
-
 struct AppendArgs : RopeArgs<true> {
     Scales k_scale, v_scale;
 };
@@ -290,7 +275,7 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
         for (int m0 = 0; m0 < half; m0 += 32) {
             const int m = min(m0 + lane, half - 1), axis = s_axis[m];
             const float2 p = make_float2(__shfl_sync(0xffffffffu, mine.x, axis), __shfl_sync(0xffffffffu, mine.y, axis));
-            const float2 c = SAME ? cos_sin<sizeof(T) == 4>(p, s_turns[m]) : cos_sin_of_codes(p, s_turns[m]);
+            const float2 c = cos_sin<!SAME || sizeof(T) == 4>(p, s_turns[m]);
             s_cos[m] = c.x * a.scale;
             s_sin[m] = c.y * (a.scale * a.sign);
         }
@@ -472,7 +457,7 @@ __global__ void __launch_bounds__(C8_NT) append8_generic_kernel(const __grid_con
                 const int i = INTERLEAVED ? 2 * m : m, j = INTERLEAVED ? i + 1 : m + half;
                 float2 p = pos[0];
                 for (int n = 1; n < RX_MAX_AXES; ++n) p = a.axes.of[m] == n ? pos[n] : p;
-                const float2 cs = cos_sin_of_codes(p, a.turns[m]);
+                const float2 cs = cos_sin<true>(p, a.turns[m]);
                 const float c = cs.x * a.scale, s = cs.y * a.scale;
                 const float u = Cvt<T>::load1(x + i), w = Cvt<T>::load1(x + j);
                 f(i, fmaf(-w, s, u * c), j, fmaf(u, s, w * c));

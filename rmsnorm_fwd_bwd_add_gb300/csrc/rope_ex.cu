@@ -27,7 +27,7 @@
 // double-float, and the whole turns drop out exactly, so a position near 10^7
 // still has its angle to about 1e-8 turns.  16-bit results take the SFU's sine
 // and cosine of the reduced angle (2^-21 absolute, far below their rounding);
-// fp32 results take sincospif.
+// fp32 results take sincospif, with the rounding of the reduced angle added to first order.
 #include "rmsnorm.h"
 
 #include <algorithm>
