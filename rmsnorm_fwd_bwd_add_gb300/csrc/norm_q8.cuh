@@ -525,20 +525,25 @@ __global__ void __launch_bounds__(Q8_GENERIC_NT, 2) q8_long_kernel(const __grid_
                 v[m] = f2mul(h[m], f2add(v[m], make_float2(a.weight_bias, a.weight_bias)));
             }
         };
+        // A sum of sums of 32 rounds, so that rounding grows with neither length alone.
         float ss = 0.f, top = 0.f;
-        for (int u0 = t; u0 < NU; u0 += V * NT) {
-            float2 s2 = make_float2(0.f, 0.f);
+        for (int u1 = t; u1 < NU; u1 += 32 * V * NT) {
+            float some = 0.f;
+            for (int u0 = u1; u0 < min(NU, u1 + 32 * V * NT); u0 += V * NT) {
+                float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float2 h[P], v[P];
-                load(u0 + j * NT, h, v);
+                for (int j = 0; j < V; ++j) {
+                    float2 h[P], v[P];
+                    load(u0 + j * NT, h, v);
 #pragma unroll
-                for (int m = 0; m < P; ++m) {
-                    s2 = f2fma(h[m], h[m], s2);
-                    top = max_abs(top, v[m].x, v[m].y);
+                    for (int m = 0; m < P; ++m) {
+                        s2 = f2fma(h[m], h[m], s2);
+                        top = max_abs(top, v[m].x, v[m].y);
+                    }
                 }
+                some += s2.x + s2.y;
             }
-            ss += s2.x + s2.y;
+            ss += some;
         }
         ss = group_sum<32>(ss);
         top = warp_max(top);
