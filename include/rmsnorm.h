@@ -317,7 +317,9 @@ size_t rmsnorm_block_vjp_workspace_size(int64_t rows, int64_t D, int dtype);
  *   scale        [rows, ceil(D / group)] fp32 contiguous, [rows] for group = 0.
  *   group        0, 32, 64 or 128.
  * Row strides in elements (>= D; ignored when rows == 1).  A group that holds a NaN or an
- * infinity has a scale that is NaN or infinite, and each of its out_j * scale is NaN.
+ * infinity has a scale that is NaN or infinite, and each of its out_j * scale is NaN.  scale
+ * carries r: that of a group far below its row's size may be subnormal or 0, and 1 / scale
+ * infinite.  h_j * w'_j and its product with 448 / a are rounded to fp32.
  * out and scale may not overlap anything else.  Errors as for rmsnorm_fwd.
  */
 int rmsnorm_fwd_q8(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual,
@@ -454,7 +456,8 @@ typedef enum {
  * positions of one axis or several.  Each head of the rotated k (unrounded) and of v has a
  * scale of its own; with x the head's values and top = 448 (e4m3) or 127 (int8):
  *     a = max(max |x_j|, top * 2^-126),  scale = a / top,  code_j = round(x_j * (top / a))
- * to the nearest code, ties to even.
+ * to the nearest code, ties to even: of the exact quotient for 16-bit v, of one rounded once
+ * to fp32 for the rest.
  *   q, k, v, positions, slots, q_out, inv_freq, attn_scale, interleaved  as for
  *                rmsnorm_rope_kv_append_ex; axes, pair_axis and positions [axes, T] as for
  *                rmsnorm_rope_axes.

@@ -48,7 +48,7 @@ cudaError_t launch_append8_vectors(const AppendArgs &a, int sm, cudaStream_t s) 
 // Smaller units: fewer lanes a head leave each step less work beside its elements (4096
 // tokens of 32 + 8 heads of 100 in 4-byte units: 53 us with 4 elements a lane, 36 with 8, 31
 // with 16), until they spill (of 126 in single elements 60 us with 4, 46 with 8, 62 with 16,
-// which the longest heads need).
+// which heads of over 256 take).  Heads of over 512 go to the kernel of a warp a head.
 template <typename T, bool INTERLEAVED, int FMT>
 cudaError_t launch_append8_layout(const AppendArgs &a, int unit, int sm, cudaStream_t s) {
     if (unit == 16 && append8_vectors_fit<T, INTERLEAVED>(a.Dh, a.rot)) return launch_append8_vectors<T, INTERLEAVED, FMT>(a, sm, s);

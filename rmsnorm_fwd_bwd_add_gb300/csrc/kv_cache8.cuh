@@ -7,9 +7,9 @@
 // scales written once.
 //
 // On the GB300 (6.8 TB/s copied), inputs changing from call to call: 16384 tokens of 32 + 8
-// heads of 128 (bf16, three axes, e4m3) appended in 60 us (91 % of that; 61 % of the issue
-// slots used), 8 tokens in 3.7 us (two trips to memory and the cosines); 65536 tokens of 8
-// heads of 128 read in 65 us (92 %), 77 in 2.1 us.
+// heads of 128 (bf16, three axes, e4m3) appended in 60 us (91 % of that), 8 tokens in 3.8 us
+// (two trips to memory and the cosines); 65536 tokens of 8 heads of 128 read in 65 us (92 %),
+// 77 in 2.1 us.
 #pragma once
 
 #include "quant.cuh"
@@ -424,8 +424,12 @@ __global__ void __launch_bounds__(C8_NT, C8_CTAS_PER_SM) append8_kernel(const __
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Heads too long for the ring's single elements (over 512, off 16- and 4-byte units): a
-// warp a head of a token, a lane its elements 32 apart, which a head of k or v computes twice: for its largest and for its codes.
+// Heads of over 512 elements that are not in 16-byte units (in 4-byte units too; and
+// interleaved ones of 1024 with an odd number of vectors in both parts), which have more
+// lanes than the ring's instances for smaller units: a warp a head of a token, a lane its
+// elements 32 apart, which a head of k or v computes twice, for its largest and for its codes.
+// Each head computes its cosines anew: 4096 tokens of 8 + 2 heads of 1022 take 482 us (6 % of
+// the copy bandwidth; heads of 512 in 4-byte units 32, of 1024 in 16-byte units 37).
 template <typename T, int FMT, bool INTERLEAVED>
 __global__ void __launch_bounds__(C8_NT) append8_generic_kernel(const __grid_constant__ AppendArgs a) {
     const int lane = threadIdx.x & 31, half = a.rot / 2;

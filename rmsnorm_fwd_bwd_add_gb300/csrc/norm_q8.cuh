@@ -24,8 +24,9 @@
 // On the GB300 (6.8 TB/s copied), inputs changing from call to call: 16384 x 8192 bf16 with
 // residual 147 us (94 % of that), 8192 x 12288 in groups of 128 109 us (96 %), 16384 x 4096
 // 73 us (95 %); without a residual 8192 x 4096 fp16 in groups of 128 21 us (72 %: 3 bytes an
-// element for the same instructions, 57 % of the issue slots used by 16 warps an SM); off
-// 16-byte boundaries 16384 x 4097 79 us (88 %), 5000 x 4097 in groups 30 us (71 %: unaligned
+// element for the same instructions, whose latency the 16 warps that fit an SM at 106
+// registers, 32 of them the weights, do not cover: 57 % of the issue slots used); off 16-byte
+// boundaries 16384 x 4097 78 us (88 %), 5000 x 4097 in groups 30 us (71 %: the same, unaligned
 // weights at the start, 8.2 rows a CTA); 4 x 4096 2.2 us.
 #pragma once
 
@@ -67,8 +68,11 @@ template <int P> __device__ __forceinline__ void store_codes(uint8_t *p, const f
 }
 
 // run_max of V values at once.  Runs of 16 lanes (128 columns of 16 bits) are unrolled: 8192
-// rows of fp16, D = 4096 take 22.4 us with the loop, 20.9 so, 21.8 with the others unrolled
-// as well, and 25.6 with reductions of a part of the warp's lanes in one instruction.
+// rows of fp16, D = 4096 take 22.4 us with the loop, 20.9 so, and 25.6 with reductions of a
+// part of the warp's lanes in one instruction.  Runs of 8 unrolled as well gain in their own
+// groups and lose in others (these rows in groups of 64 21.3 -> 20.7 us, 128 20.9 -> 21.0; fp32
+// 16384 x 2048 in groups of 32 40.2 -> 38.6, 64 39.7 -> 39.9, 128 37.0 -> 37.3), runs of 4 too
+// lose (fp16 in groups of 32 20.9 -> 21.3, 64 21.6, 128 22.1).
 template <int V> __device__ __forceinline__ void run_maxima(float (&top)[V], int n) {
     auto step = [&](int off) {
 #pragma unroll

@@ -13,8 +13,9 @@ namespace rmsn {
 // A cache's or output's format at compile time: its largest code.
 template <int FMT> __host__ __device__ constexpr float top_code() { return FMT == RMSNORM_CACHE_I8 ? 127.f : 448.f; }
 
-// The least magnitude that a group's scale is made from: scale and 1 / scale are then
-// normal numbers whatever the group holds.
+// The least magnitude a that a group's scale is made from: a / top and top / a are then
+// normal numbers whatever the group holds.  (The norm's scale has its r as a factor beside
+// them, and may be subnormal or 0.)
 template <int FMT> __host__ __device__ constexpr float least_top() { return top_code<FMT>() * 0x1p-126f; }
 
 // The largest magnitude among a group: NaN if any value is.

@@ -4,7 +4,7 @@
 //
 // Heads in 16-byte units go through the 8-bit append's kernel, whose warps compute a
 // token's cosines together and copy heads ahead into shared memory (kv_cache8.cuh; without
-// quantising): 16384 tokens of 32 + 8 heads of 128 57.3 us on rope_ex.cu's kernel, 53.6 so.
+// quantising): 16384 tokens of 32 + 8 heads of 128 57.3 us on rope_ex.cuh's kernel, 53.6 so.
 // Smaller units stay on that one, with a choice of axis beside each pair.
 #include "kv_append8.h"
 #include "rope_ex.cuh"

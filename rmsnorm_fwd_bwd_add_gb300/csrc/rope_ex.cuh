@@ -48,7 +48,7 @@ __device__ __forceinline__ float2 split_position(int64_t p) {
 // that become codes): what the reduced angle loses in its last addition, 2^-26 turns, three
 // times the error of the sines themselves, is added to first order (the fp32 rotation's
 // error against 64 bits 4.9e-8 without it, 4.1e-8 with it and with 64-bit angles; of 17
-// million e4m3 codes of k 45 and 25 differ from 64-bit values', many times that with the
+// million e4m3 codes of k 45 and 24 differ from 64-bit values', many times that with the
 // SFU's sines).  Otherwise the SFU's sines, 2^-21 off, far below the rounding of 16 bits.
 template <bool PRECISE>
 __device__ __forceinline__ float2 cos_sin(float2 p, float2 f) {

@@ -1,5 +1,6 @@
-// rope_plan.h -- how a rotary call's tokens and heads are dealt out to warps (host
-// only; the kernel is in rope_ex.cu).
+// rope_plan.h -- how the tokens and heads of the rotary calls, of the 8-bit append and of
+// the read are dealt out to warps (host only; the kernels are in rope_ex.cuh and
+// kv_cache8.cuh).
 #pragma once
 
 #include <algorithm>
@@ -59,7 +60,12 @@ struct Append8Plan {
 // All warps go through equal rounds of whole tokens; of what is left, less than a round,
 // each token is split into as many parts as cost least.  A part costs its positions and
 // cosines, and its steps of 32 / cw heads (kv: of k and of v, or of k alone); none is
-// without heads.
+// without heads.  The costs' ratios are estimates (a step: two 16-byte vectors a unit), the
+// choices measured: for 8 to 9800 tokens of 32 + 8 and 8 + 1 heads of 128, 16 + 4 of 64 and 32
+// + 8 of 100, and for the rotation of 32 + 8 heads of 128 and 16 + 16 fp32 heads of 80, the
+// time was within 2 % of the best of 1, 2, 4, 8 and 16 parts (300 tokens of 32 + 8 heads of
+// 128 7.4, 5.2, 4.4, 4.5, 4.4 us, 4.4 so; 1000 8.3, 7.0, 9.0, 12.6, 12.6, and 6.9; 3000 17.9,
+// 15.3, 14.6, 16.5, 16.4, and 14.6).
 inline Append8Plan make_append8_plan(int64_t T, int cw, int Hq, int Hkv, int kv, int pairs, int units, int ctas, int cta_warps) {
     const int64_t warps = (int64_t)ctas * cta_warps;
     const int hpi = 32 / cw, most = (std::max(Hq, Hkv) + hpi - 1) / hpi;
